@@ -3,7 +3,9 @@
  * recurrence (sm_103a): the gate activations that turn the layer's raw
  * projections into (g, beta), the short causal depthwise convolution over the
  * q/k/v projections with its per-sequence conv state cache (prefill and
- * decode), and the gated RMSNorm applied to the recurrence's output.
+ * decode, and its gradient), the norm of the queries' and keys' heads with
+ * the position rotation in the same pass (and its gradient), and the gated
+ * RMSNorm applied to the recurrence's output.
  *
  * "Defending Against the Training-Inference Numeric Mismatch in RL
  * (Especially Linear Attention)" keeps these ops identical on the trainer and
@@ -16,6 +18,9 @@
  *     conv y[t, c] = act( bias[c] + sum_{i<W} w[c, i] * xw[t + i, c] ),
  *          xw = (the W-1 rows before the sequence: its conv state) ++ (its rows)
  *     norm y = o / sqrt(mean(o^2) + eps) * weight * silu(z)   (per row of d)
+ *     q/k  n = x * r * weight,  r = 1 / sqrt(sum(x^2) * c + eps),  c = 1/d (RMS) or 1 (L2),
+ *          then the pairs (u, v) of n's first rotary_dim values by the token's angles:
+ *          (u cos - v sin, v cos + u sin)
  *
  * Invariance.  Every output element is computed by one thread with one fixed
  * order of operations that depends on nothing but its own row (conv: its own
@@ -32,7 +37,7 @@
  * size).  Misalignment returns GDN_ERR_INVALID_ARG.  Nothing is allocated;
  * every call is one asynchronous launch on `stream` (a cudaStream_t; NULL =
  * legacy default stream) and returns host-side validation or launch errors
- * only.
+ * only (the two gradients are two launches each and take a workspace).
  */
 #ifndef GDN_LAYER_H_
 #define GDN_LAYER_H_
@@ -107,6 +112,81 @@ gdn_status gdn_causal_conv1d_update(const gdn_conv_shape* shape, const void* x, 
                                     const float* bias, void* conv_state,
                                     const int32_t* state_indices, int num_slots, void* y,
                                     void* stream);
+
+/*
+ * Gradient of gdn_causal_conv1d_fwd for the loss L = sum <d_y, y> +
+ * <d_final_state, final state>.  x, weight, bias (NULL: zero), cu_seqlens as
+ * given to the forward; init_state [N, W-1, C] in dtype is the initial state
+ * of each sequence, in the order of the sequences (NULL: zeros).  d_y
+ * [T_total, C]; d_final_state [N, W-1, C] in dtype (NULL: zero).  Writes dx
+ * [T_total, C] in dtype, dweight [C, W] and dbias [C] fp32 (dbias NULL: not
+ * written) and d_init_state [N, W-1, C] in dtype (NULL: not written).  Rows of
+ * dx that no sequence covers are left as they are.  The outputs must not alias
+ * the inputs.  fp32 sums; each sum's order is fixed by the shape and
+ * cu_seqlens, so results are deterministic; dweight and dbias are not
+ * batch-invariant.  d_y, dx, d_final_state and d_init_state 16-byte aligned,
+ * dweight and dbias 4-byte aligned.
+ */
+size_t gdn_causal_conv1d_bwd_workspace_size(const gdn_conv_shape* shape);
+
+gdn_status gdn_causal_conv1d_bwd(const gdn_conv_shape* shape, const void* x, const float* weight,
+                                 const float* bias, const int32_t* cu_seqlens,
+                                 const void* init_state, const void* d_y,
+                                 const void* d_final_state, void* dx, float* dweight, float* dbias,
+                                 void* d_init_state, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+typedef enum { GDN_NORM_RMS = 0, GDN_NORM_L2 = 1 } gdn_norm;
+
+typedef struct {
+    int64_t T;         /* tokens */
+    int HQ, HK;        /* heads of q and of k (any numbers; HK = 0: no k) */
+    int d;             /* head dim, a multiple of 8 (bf16) or 4 (fp32), at most 256 */
+    int rotary_dim;    /* leading values of a head that are rotated, a multiple of 16 (bf16) or 8 (fp32); 0: none */
+    int interleaved;   /* pairs: 0: (i, i + rotary_dim/2); 1: (2i, 2i + 1) */
+    int norm;          /* gdn_norm */
+    int max_positions; /* rows of cos and sin */
+    float eps;
+    gdn_dtype dtype;   /* q, k, their outputs and gradients */
+    int64_t ldq, ldk;  /* elements from one token's q (k) to the next one's: at least HQ * d (HK * d) */
+} gdn_qk_shape;
+
+/*
+ * Norm of each head of q [T, HQ, d] and k [T, HK, d] and rotation by the
+ * token's position, in one pass.  The heads of a token are dense; tokens are
+ * ldq (ldk) elements apart, so q and k may be columns of one wider row, such
+ * as the conv's output.  q_weight, k_weight [d] fp32 or NULL (ones).  cos, sin
+ * [max_positions, rotary_dim / 2] fp32; token t uses row positions[t] (int32;
+ * positions NULL: row t, and max_positions must be >= T).  A token whose
+ * position is negative or not below max_positions is skipped: its rows of the
+ * outputs are left as they are (with rotary_dim = 0, positions is not read and no token
+ * is skipped).  Outputs q_out [T, HQ, d], k_out [T, HK, d] dense in dtype; they
+ * may alias q and k where those are dense.  Each row is computed by one lane
+ * group in one fixed order: results do not depend on T or the other rows.
+ * Strides are multiples of 8 (bf16) or 4 (fp32) elements.  q, k, the outputs
+ * and the weights are 16-byte aligned, cos, sin and positions 4-byte aligned.
+ */
+gdn_status gdn_qk_norm_rope(const gdn_qk_shape* shape, const void* q, const void* k,
+                            const float* q_weight, const float* k_weight, const float* cos,
+                            const float* sin, const int32_t* positions, void* q_out, void* k_out,
+                            void* stream);
+
+/*
+ * Its gradient: from q, k (the inputs) and d_q_out, d_k_out (dense), dq and dk
+ * with lddq (lddk) elements from token to token, and, where the weight is
+ * given, dq_weight and dk_weight [d] fp32 (NULL: not written).  dq may alias
+ * d_q_out and dk may alias d_k_out where they are dense; a skipped token's rows
+ * are left as they are and add nothing to the weights' gradients.  fp32 sums in
+ * an order fixed by the shape.
+ */
+size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_shape* shape);
+
+gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_shape* shape, const void* q, const void* k,
+                                const float* q_weight, const float* k_weight, const float* cos,
+                                const float* sin, const int32_t* positions, const void* d_q_out,
+                                const void* d_k_out, void* dq, void* dk, int64_t lddq, int64_t lddk,
+                                float* dq_weight, float* dk_weight, void* workspace,
+                                size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,4 @@
-"""Thin ctypes binding over libgdn.so (include/gdn.h).
+"""Thin ctypes binding over libgdn.so (the headers in include/).
 
 Argument marshalling only: tensors are checked for device, dtype, layout and
 alignment, outputs and workspaces are allocated with PyTorch when the caller
@@ -26,7 +26,10 @@ SYMBOLS = ("gdn_workspace_size", "gdn_recurrent_fwd", "gdn_decode_step", "gdn_ch
            "gdn_read_device_error", "gdn_status_string", "gdn_recurrent_fwd_noalloc",
            "gdn_recurrent_fwd_snapshots", "gdn_gates", "gdn_gated_rmsnorm", "gdn_causal_conv1d_fwd",
            "gdn_causal_conv1d_update", "gdn_replay_block_floats", "gdn_replay_workspace_size",
-           "gdn_replay_prefill", "gdn_replay_decode")
+           "gdn_replay_prefill", "gdn_replay_decode", "gdn_causal_conv1d_bwd",
+           "gdn_causal_conv1d_bwd_workspace_size", "gdn_qk_norm_rope", "gdn_qk_norm_rope_bwd",
+           "gdn_qk_norm_rope_bwd_workspace_size", "gdn_selective_scan_fwd", "gdn_selective_scan_update",
+           "gdn_selective_scan_bwd", "gdn_selective_scan_bwd_workspace_size")
 
 
 class GdnShape(ctypes.Structure):
@@ -38,6 +41,20 @@ class GdnShape(ctypes.Structure):
 class ConvShape(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int), ("T_total", ctypes.c_int), ("C", ctypes.c_int), ("W", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("activation", ctypes.c_int)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("HQ", ctypes.c_int), ("HK", ctypes.c_int), ("d", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("norm", ctypes.c_int),
+                ("max_positions", ctypes.c_int), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("ldq", ctypes.c_int64), ("ldk", ctypes.c_int64)]
+
+
+class ScanShape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("T_total", ctypes.c_int), ("C", ctypes.c_int), ("G", ctypes.c_int),
+                ("S", ctypes.c_int), ("dtype", ctypes.c_int), ("dt_softplus", ctypes.c_int),
+                ("ldx", ctypes.c_int64), ("lddt", ctypes.c_int64), ("ldz", ctypes.c_int64),
+                ("ldB", ctypes.c_int64), ("ldC", ctypes.c_int64)]
 
 
 class GdnError(RuntimeError):
@@ -87,6 +104,19 @@ def lib():
         L.gdn_replay_prefill.restype = ctypes.c_int
         L.gdn_replay_decode.argtypes = [ctypes.POINTER(GdnShape)] + [_P] * 8 + [ctypes.c_int, _P, _P]
         L.gdn_replay_decode.restype = ctypes.c_int
+        i, n, z = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+        conv, qk, scan = (ctypes.POINTER(c) for c in (ConvShape, QkShape, ScanShape))
+        for name, args, res in (
+                ("gdn_causal_conv1d_bwd_workspace_size", [conv], z),
+                ("gdn_causal_conv1d_bwd", [conv] + [_P] * 12 + [z, _P], i),
+                ("gdn_qk_norm_rope", [qk] + [_P] * 10, i),
+                ("gdn_qk_norm_rope_bwd_workspace_size", [qk], z),
+                ("gdn_qk_norm_rope_bwd", [qk] + [_P] * 11 + [n, n] + [_P] * 3 + [z, _P], i),
+                ("gdn_selective_scan_fwd", [scan] + [_P] * 11 + [i, _P, _P, _P], i),
+                ("gdn_selective_scan_update", [scan] + [_P] * 10 + [i, _P, _P], i),
+                ("gdn_selective_scan_bwd_workspace_size", [scan], z),
+                ("gdn_selective_scan_bwd", [scan] + [_P] * 22 + [z, _P], i)):
+            getattr(L, name).argtypes, getattr(L, name).restype = args, res
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -446,6 +476,296 @@ def gdn_causal_conv1d_update(x, weight, conv_state, state_indices=None, bias=Non
                                             _ptr(out), _stream(stream))
     _check(rc, "gdn_causal_conv1d_update")
     return out
+
+
+# ---------------------------------------------------------------- gradients, q/k norm with rotation, selective scan
+
+class _On:
+    """The device and, where the caller names one, the stream that a call allocates and launches on.
+    Tensors handed to a named stream are recorded on it, so that memory freed right after the call
+    is not reused while the stream still reads it."""
+
+    def __init__(self, device, stream, tensors):
+        if stream is None:
+            self.ctx = torch.cuda.device(device)
+        else:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.ctx = torch.cuda.stream(stream)
+            if stream != torch.cuda.current_stream(device):
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
+        self.device = device
+
+    def __enter__(self):
+        self.ctx.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _is(t, name, shape, dtype, device):
+    """t is a dense tensor of this shape."""
+    _need(t, name, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _rows(t, name, shape, dtype, device):
+    """t has this shape and its rows t[i] are dense; the elements from one row to the next."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    dense = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and step != dense:
+            raise ValueError(f"each row of {name} must be contiguous")
+        dense *= size
+    if t.shape[0] <= 1:
+        return dense
+    if t.stride(0) < dense:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.stride(0)
+
+
+def _ndim(t, name, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", torch.uint8, device)
+    return workspace
+
+
+def gdn_causal_conv1d_bwd(x, weight, cu_seqlens, d_out, bias=None, init_state=None, d_final_state=None,
+                          activation=True, workspace=None, need_d_init_state=True, stream=None):
+    """Gradient of gdn_causal_conv1d_fwd.  x, d_out [T, C]; weight [C, W], bias [C]
+    fp32; init_state, d_final_state [N, W-1, C] (dtype of x) or None (zero), in
+    the order of the sequences.  Returns dict dx (dtype of x), dweight, dbias
+    (fp32, dbias None without a bias), d_init_state (dtype of x or None).  Rows
+    of dx behind cu_seqlens[N] are not written."""
+    _ndim(x, "x", 2)
+    _ndim(weight, "weight", 2)
+    _ndim(cu_seqlens, "cu_seqlens", 1)
+    dev, dt, (T, C), W = x.device, x.dtype, x.shape, weight.shape[1]
+    N = cu_seqlens.numel() - 1
+    if N < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    _is(x, "x", (T, C), dt, dev)
+    _is(d_out, "d_out", (T, C), dt, dev)
+    _is(weight, "weight", (C, W), torch.float32, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if bias is not None:
+        _is(bias, "bias", (C,), torch.float32, dev)
+    for t, name in ((init_state, "init_state"), (d_final_state, "d_final_state")):
+        if t is not None:
+            _is(t, name, (N, W - 1, C), dt, dev)
+    shape = ConvShape(N, T, C, W, _dtype_code(x), int(bool(activation)))
+    with _On(dev, stream, (x, weight, cu_seqlens, d_out, bias, init_state, d_final_state, workspace)) as s:
+        res = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight),
+                   dbias=None if bias is None else torch.empty_like(bias),
+                   d_init_state=torch.empty(N, W - 1, C, dtype=dt, device=dev) if need_d_init_state else None)
+        ws = _workspace(workspace, lib().gdn_causal_conv1d_bwd_workspace_size(ctypes.byref(shape)), dev)
+        rc = lib().gdn_causal_conv1d_bwd(ctypes.byref(shape), _at(x), _at(weight), _at(bias), _at(cu_seqlens),
+                                         _at(init_state), _at(d_out), _at(d_final_state), _at(res["dx"]),
+                                         _at(res["dweight"]), _at(res["dbias"]), _at(res["d_init_state"]),
+                                         _at(ws), ws.numel(), s)
+    _check(rc, "gdn_causal_conv1d_bwd")
+    return res
+
+
+_NORMS = {"rms": 0, "l2": 1}
+
+
+def _qk_shape(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
+    _ndim(q, "q", 3)
+    _ndim(k, "k", 3)
+    _ndim(cos, "cos", 2)
+    dev, (T, HQ, d), HK = q.device, q.shape, k.shape[1]
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
+    ldq, ldk = _rows(q, "q", (T, HQ, d), q.dtype, dev), _rows(k, "k", (T, HK, d), q.dtype, dev)
+    for t, name in ((cos, "cos"), (sin, "sin")):
+        _is(t, name, cos.shape, torch.float32, dev)
+    if positions is not None:
+        _is(positions, "positions", (T,), torch.int32, dev)
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _is(t, name, (d,), torch.float32, dev)
+    return QkShape(T, HQ, HK, d, 2 * cos.shape[1], int(bool(interleaved)), _NORMS[norm], cos.shape[0], float(eps),
+                   _dtype_code(q), ldq, ldk)
+
+
+def gdn_qk_norm_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
+                     interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norm of each head of q [T, HQ, d] and k [T, HK, d] (norm "rms":
+    x / sqrt(mean(x^2) + eps), "l2": x / sqrt(sum(x^2) + eps), times a weight [d]
+    fp32 or None) and rotation of its first 2 * cos.shape[1] values by row
+    positions[t] (int32, None: row t) of cos, sin [max_positions, rotary_dim / 2]
+    fp32: pairs (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved.  q and k
+    may be column slices of wider rows.  Returns dense (q_out, k_out).  A token
+    whose position is outside the tables is skipped (its rows untouched)."""
+    shape = _qk_shape(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    dev = q.device
+    with _On(dev, stream, (q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out)) as s:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev) if k_out is None else k_out
+        _is(q_out, "q_out", q.shape, q.dtype, dev)
+        _is(k_out, "k_out", k.shape, q.dtype, dev)
+        rc = lib().gdn_qk_norm_rope(ctypes.byref(shape), _at(q), _at(k), _at(q_weight), _at(k_weight), _at(cos),
+                                    _at(sin), _at(positions), _at(q_out), _at(k_out), s)
+    _check(rc, "gdn_qk_norm_rope")
+    return q_out, k_out
+
+
+def gdn_qk_norm_rope_bwd(q, k, cos, sin, d_q_out, d_k_out, positions=None, q_weight=None, k_weight=None, norm="rms",
+                         eps=1e-6, interleaved=False, dq=None, dk=None, workspace=None, stream=None):
+    """Gradient of gdn_qk_norm_rope at its inputs q, k.  dq, dk: written in place
+    when given (they may be column slices of wider rows), else dense.  Returns
+    dict dq, dk, dq_weight, dk_weight (fp32, None without the weight)."""
+    shape = _qk_shape(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    dev = q.device
+    _is(d_q_out, "d_q_out", q.shape, q.dtype, dev)
+    _is(d_k_out, "d_k_out", k.shape, q.dtype, dev)
+    with _On(dev, stream, (q, k, cos, sin, positions, q_weight, k_weight, d_q_out, d_k_out, dq, dk, workspace)) as s:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if dk is None else dk
+        lddq, lddk = _rows(dq, "dq", q.shape, q.dtype, dev), _rows(dk, "dk", k.shape, q.dtype, dev)
+        res = dict(dq=dq, dk=dk, dq_weight=None if q_weight is None else torch.empty_like(q_weight),
+                   dk_weight=None if k_weight is None or shape.HK == 0 else torch.empty_like(k_weight))
+        ws = _workspace(workspace, lib().gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(shape)), dev)
+        rc = lib().gdn_qk_norm_rope_bwd(ctypes.byref(shape), _at(q), _at(k), _at(q_weight), _at(k_weight), _at(cos),
+                                        _at(sin), _at(positions), _at(d_q_out), _at(d_k_out), _at(dq), _at(dk),
+                                        lddq, lddk, _at(res["dq_weight"]), _at(res["dk_weight"]), _at(ws),
+                                        ws.numel(), s)
+    _check(rc, "gdn_qk_norm_rope_bwd")
+    return res
+
+
+def _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus):
+    _ndim(x, "x", 2)
+    _ndim(A_log, "A_log", 2)
+    _ndim(B, "B", 3)
+    dev, ty, (T, ch), S, G = x.device, x.dtype, x.shape, A_log.shape[1], B.shape[1]
+    lds = [_rows(t, name, (T, ch), ty, dev) for t, name in ((x, "x"), (dt, "dt"))]
+    lds.append(0 if z is None else _rows(z, "z", (T, ch), ty, dev))
+    lds += [_rows(t, name, (T, G, S), ty, dev) for t, name in ((B, "B"), (C, "C"))]
+    _is(A_log, "A_log", (ch, S), torch.float32, dev)
+    for t, name in ((D, "D"), (dt_bias, "dt_bias")):
+        if t is not None:
+            _is(t, name, (ch,), torch.float32, dev)
+    return ScanShape(N, T, ch, G, S, _dtype_code(x), int(bool(dt_softplus)), *lds)
+
+
+def gdn_selective_scan_fwd(x, dt, A_log, B, C, cu_seqlens, D=None, z=None, dt_bias=None, state=None,
+                           state_indices=None, has_initial_state=None, dt_softplus=True, out=None, stream=None):
+    """Selective state space scan over a packed varlen batch.
+
+    x, dt, z [T, channels], B, C [T, G, S] (bf16 or fp32, one dtype, rows may be
+    slices of wider ones); A_log [channels, S], D, dt_bias [channels] fp32;
+    cu_seqlens int32 [N+1] on the device.  state [slots, channels, S] fp32 is read
+    as the initial state and overwritten with the final state of each sequence's
+    slot (in place; int32 state_indices, has_initial_state as in
+    gdn_causal_conv1d_fwd).  Returns y [T, channels] (rows behind cu_seqlens[N]
+    not written)."""
+    _ndim(cu_seqlens, "cu_seqlens", 1)
+    N = cu_seqlens.numel() - 1
+    shape = _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
+    dev = x.device
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if N < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    slots = 0
+    if state is not None:
+        _ndim(state, "state", 3)
+        slots = state.shape[0]
+        _is(state, "state", (slots, shape.C, shape.S), torch.float32, dev)
+    for t, name in ((state_indices, "state_indices"), (has_initial_state, "has_initial_state")):
+        if t is not None:
+            _is(t, name, (N,), torch.int32, dev)
+    with _On(dev, stream, (x, dt, A_log, B, C, cu_seqlens, D, z, dt_bias, state, state_indices, has_initial_state,
+                           out)) as s:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        _is(out, "out", x.shape, x.dtype, dev)
+        rc = lib().gdn_selective_scan_fwd(ctypes.byref(shape), _at(x), _at(dt), _at(A_log), _at(B), _at(C), _at(D),
+                                          _at(z), _at(dt_bias), _at(cu_seqlens), _at(state), _at(state_indices),
+                                          slots, _at(has_initial_state), _at(out), s)
+    _check(rc, "gdn_selective_scan_fwd")
+    return out
+
+
+def gdn_selective_scan_update(x, dt, A_log, B, C, state, state_indices=None, D=None, z=None, dt_bias=None,
+                              dt_softplus=True, out=None, stream=None):
+    """One token per sequence: x, dt, z [N, channels], B, C [N, G, S]; state
+    [slots, channels, S] fp32 updated in place.  Returns y [N, channels] (rows of
+    skipped slots untouched)."""
+    _ndim(state, "state", 3)
+    N = x.shape[0]
+    shape = _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
+    dev = x.device
+    _is(state, "state", (state.shape[0], shape.C, shape.S), torch.float32, dev)
+    if state_indices is not None:
+        _is(state_indices, "state_indices", (N,), torch.int32, dev)
+    with _On(dev, stream, (x, dt, A_log, B, C, D, z, dt_bias, state, state_indices, out)) as s:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        _is(out, "out", x.shape, x.dtype, dev)
+        rc = lib().gdn_selective_scan_update(ctypes.byref(shape), _at(x), _at(dt), _at(A_log), _at(B), _at(C), _at(D),
+                                             _at(z), _at(dt_bias), _at(state), _at(state_indices), state.shape[0],
+                                             _at(out), s)
+    _check(rc, "gdn_selective_scan_update")
+    return out
+
+
+def gdn_selective_scan_bwd(x, dt, A_log, B, C, cu_seqlens, d_out, D=None, z=None, dt_bias=None, init_state=None,
+                           d_final_state=None, dt_softplus=True, workspace=None, need_d_init_state=True, stream=None):
+    """Gradient of gdn_selective_scan_fwd.  d_out [T, channels]; init_state,
+    d_final_state [N, channels, S] fp32 or None (zero), in the order of the
+    sequences.  Returns dict dx, ddt, dz, dB, dC (dtype of x), dA_log, dD,
+    ddt_bias, d_init_state (fp32); None where the input is None.  Rows behind
+    cu_seqlens[N] are not written."""
+    _ndim(cu_seqlens, "cu_seqlens", 1)
+    N = cu_seqlens.numel() - 1
+    shape = _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
+    dev, ty = x.device, x.dtype
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if N < 0:
+        raise ValueError("cu_seqlens must have at least one entry")
+    _is(d_out, "d_out", x.shape, ty, dev)
+    for t, name in ((init_state, "init_state"), (d_final_state, "d_final_state")):
+        if t is not None:
+            _is(t, name, (N, shape.C, shape.S), torch.float32, dev)
+    with _On(dev, stream, (x, dt, A_log, B, C, cu_seqlens, d_out, D, z, dt_bias, init_state, d_final_state,
+                           workspace)) as s:
+        like = lambda t, kind=ty: None if t is None else torch.empty(t.shape, dtype=kind, device=dev)  # noqa: E731
+        res = dict(dx=like(x), ddt=like(dt), dA_log=like(A_log, torch.float32), dB=like(B), dC=like(C),
+                   dD=like(D, torch.float32), dz=like(z), ddt_bias=like(dt_bias, torch.float32),
+                   d_init_state=torch.empty(N, shape.C, shape.S, dtype=torch.float32, device=dev)
+                   if need_d_init_state else None)
+        ws = _workspace(workspace, lib().gdn_selective_scan_bwd_workspace_size(ctypes.byref(shape)), dev)
+        rc = lib().gdn_selective_scan_bwd(ctypes.byref(shape), _at(x), _at(dt), _at(A_log), _at(B), _at(C), _at(D),
+                                          _at(z), _at(dt_bias), _at(cu_seqlens), _at(init_state), _at(d_out),
+                                          _at(d_final_state), *(_at(res[k]) for k in
+                                                                ("dx", "ddt", "dA_log", "dB", "dC", "dD", "dz",
+                                                                 "ddt_bias", "d_init_state")),
+                                          _at(ws), ws.numel(), s)
+    _check(rc, "gdn_selective_scan_bwd")
+    return res
 
 
 # ---------------------------------------------------------------- chunk-replay variant (include/gdn_replay.h)

@@ -1,0 +1,141 @@
+// gdn_scan.cuh -- the selective scan's per-element arithmetic, shared by the prompt, single
+// token and gradient kernels so that they agree bit for bit.
+//
+//     d = softplus(dt + bias),  a = exp(d A),  h <- a h + (d x) B,  y = sum_s h C
+//
+// with A = -exp(A_log) held as A log2(e), so that a is one product and one hardware exponential.
+// A channel's states are summed in this fixed tree: per 8 consecutive states one packed
+// (even, odd) chain in ascending order, then even + odd; the 8-state sums as a balanced binary
+// tree over neighbours.  How many of its states a thread holds (4 or 8 and up) is free.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+
+#include "../../include/gdn_scan.h"
+#include "gdn_vec.cuh"
+
+namespace gdn {
+namespace scan {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// A log2(e) of one state from its A_log.
+__device__ __forceinline__ float a_log2(float A_log) { return __fmul_rn(-expf(A_log), kLog2e); }
+
+// softplus(v) = max(v, 0) + log(1 + u), u = e^-|v| in (0, 1], with log(1 + u) = 2 artanh(w),
+// w = u / (2 + u) <= 1/3: relative accuracy is kept for the small steps of strongly negative v,
+// which log of a rounded 1 + u would lose.  artanh(w) / w is a polynomial of degree 4 in w^2
+// (Chebyshev interpolation on [0, 1/9], error 4e-9).  `sig` is the derivative, sigmoid(v).
+__device__ __forceinline__ float log1p_unit(float u) {
+    const float w = __fmul_rn(u, rcp_approx(__fadd_rn(u, 2.f))), q = __fmul_rn(w, w);
+    float p = __fmaf_rn(0.2817465662956238f, q, 0.2796141803264618f);
+    p = __fmaf_rn(p, q, 0.40024852752685547f);
+    p = __fmaf_rn(p, q, 0.6666631698608398f);
+    p = __fmaf_rn(p, q, 2.f);
+    return __fmul_rn(p, w);
+}
+__device__ __forceinline__ float softplus(float v) {
+    const float u = ex2(__fmul_rn(fabsf(v), -kLog2e));
+    return __fadd_rn(fmaxf(v, 0.f), log1p_unit(u));
+}
+__device__ __forceinline__ float softplus(float v, float& sig) {
+    const float u = ex2(__fmul_rn(fabsf(v), -kLog2e));
+    const float r = rcp_approx(__fadd_rn(1.f, u));
+    sig = v >= 0.f ? r : __fmul_rn(u, r);
+    return __fadd_rn(fmaxf(v, 0.f), log1p_unit(u));
+}
+
+// The step d of one (token, channel) from the raw dt and the channel's bias.
+__device__ __forceinline__ float step_of(float raw, float bias, bool use_softplus) {
+    const float v = __fadd_rn(raw, bias);
+    return use_softplus ? softplus(v) : v;
+}
+
+// Two neighbouring states one token on: h <- exp2(d A2) h + dx B.
+__device__ __forceinline__ void advance(float2& h, const float2& A2, const float2& d, const float2& dx,
+                                        const float2& B) {
+    const float2 e = __fmul2_rn(d, A2);
+    h = __ffma2_rn(make_float2(ex2(e.x), ex2(e.y)), h, __fmul2_rn(dx, B));
+}
+
+// y of a token: the tree's sum, the skip term, the gate.
+__device__ __forceinline__ float finish_y(float sum, float D, float x) { return __fmaf_rn(D, x, sum); }
+
+struct Params {
+    int N, T, C, G, CG, bpg;  // CG: channels per group, bpg: channel blocks per group
+    int softplus;
+    const void *x, *dt, *z, *B, *Cm;
+    int64_t ldx, lddt, ldz, ldB, ldC;
+    const float *A_log, *D, *bias;
+    const int32_t* cu;
+    float* state;
+    const int32_t* idx;
+    int num_slots;
+    const int32_t* has_init;
+    void* y;
+};
+
+__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Four consecutive values as two packed pairs.
+__device__ __forceinline__ void load4(const float* p, float2 (&v)[2]) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+    v[0] = make_float2(u.x, u.y), v[1] = make_float2(u.z, u.w);
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float2 (&v)[2]) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+}
+
+// Bounds of sequence n, whatever cu_seqlens holds.
+__device__ __forceinline__ void bounds(const int32_t* cu, int n, int T, int& bos, int& eos) {
+    bos = max(0, min(__ldg(cu + n), T));
+    eos = max(bos, min(__ldg(cu + n + 1), T));
+}
+
+// Sum over a channel's states from the 4 a lane holds (L lanes per channel, lane j the states
+// 4j .. 4j+3): the odd lane of a pair carries on its neighbour's chain.  Valid on odd lanes.
+template <int L>
+__device__ __forceinline__ float sum_states4(const float2 (&h)[2], const float2 (&c)[2], int j) {
+    float2 p = __ffma2_rn(h[1], c[1], __fmul2_rn(h[0], c[0]));
+    float2 q;
+    q.x = __shfl_xor_sync(0xffffffffu, p.x, 1);
+    q.y = __shfl_xor_sync(0xffffffffu, p.y, 1);
+    if (j & 1) p = __ffma2_rn(h[1], c[1], __ffma2_rn(h[0], c[0], q));
+    float s = __fadd_rn(p.x, p.y);
+#pragma unroll
+    for (int off = 2; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+    return s;
+}
+
+}  // namespace scan
+
+// Host side.
+inline gdn_status check_scan(const gdn_scan_shape* s) {
+    if (!s) return GDN_ERR_INVALID_ARG;
+    if (s->N < 0 || s->T_total < 0 || s->C <= 0 || s->G <= 0 || s->C % s->G) return GDN_ERR_INVALID_ARG;
+    if (s->dtype != GDN_F32 && s->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+    if (s->T_total > INT_MAX - 64) return GDN_ERR_UNSUPPORTED;
+    if (s->S != 8 && s->S != 16 && s->S != 32 && s->S != 64) return GDN_ERR_UNSUPPORTED;
+    if ((s->C / s->G) % 8) return GDN_ERR_UNSUPPORTED;
+    if ((long long)s->N * s->C >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
+    const int64_t vn = s->dtype == GDN_BF16 ? 8 : 4;
+    const int64_t bc = (int64_t)s->G * s->S;
+    if (s->ldx < s->C || s->lddt < s->C || s->ldB < bc || s->ldC < bc) return GDN_ERR_INVALID_ARG;
+    if (s->ldx % vn || s->lddt % vn || s->ldB % vn || s->ldC % vn) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+}  // namespace gdn

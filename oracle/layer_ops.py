@@ -103,3 +103,60 @@ def causal_conv1d_update(x, w, conv_state, state_indices=None, bias=None, activa
         y[b] = silu(acc) if activation else acc
         st[s] = xw[1:]
     return y, st
+
+
+def causal_conv1d_bwd(x, w, cu_seqlens, d_y, bias=None, init_state=None, d_final_state=None, activation=True):
+    """Gradients of causal_conv1d for sum <d_y, y> + <d_final_state, final state>: dict dx
+    [T, C] (NaN where no sequence is), dweight [C, W], dbias [C], d_init_state [N, W-1, C]."""
+    x, w, bias, d_y, h0, dhT = map(_f64, (x, w, bias, d_y, init_state, d_final_state))
+    cu = [int(c) for c in cu_seqlens]
+    (T, C), W, N = x.shape, w.shape[1], len(cu) - 1
+    out = dict(dx=np.full((T, C), np.nan), dweight=np.zeros((C, W)), dbias=np.zeros(C), d_init_state=np.zeros((N, W - 1, C)))
+    for n in range(N):
+        a, e = cu[n], cu[n + 1]
+        rows = np.concatenate([np.zeros((W - 1, C)) if h0 is None else h0[n], x[a:e]])
+        d_rows = np.zeros(rows.shape)
+        if dhT is not None:
+            d_rows[len(rows) - (W - 1):] += dhT[n]
+        for t in range(e - a):
+            pre = (w * rows[t:t + W].T).sum(1) + (0.0 if bias is None else bias)
+            s = 1.0 / (1.0 + np.exp(-pre))
+            p = d_y[a + t] * (s * (1.0 + pre * (1.0 - s)) if activation else 1.0)
+            out["dbias"] += p
+            out["dweight"] += p[:, None] * rows[t:t + W].T
+            d_rows[t:t + W] += (p[:, None] * w).T
+        out["d_init_state"][n] = d_rows[:W - 1]
+        out["dx"][a:e] = d_rows[W - 1:]
+    return out
+
+
+def _turn(n, cos, sin, interleaved):
+    """Rotation of n [T, H, d]'s first 2 * cos.shape[1] values by the tokens' angles [T, rd/2]."""
+    half = cos.shape[1]
+    out = n.copy()
+    first, second = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    c, s = cos[:, None], sin[:, None]
+    out[..., first] = n[..., first] * c - n[..., second] * s
+    out[..., second] = n[..., second] * c + n[..., first] * s
+    return out
+
+
+def _scale(x, norm, eps):
+    ss = (x * x).sum(-1, keepdims=True)
+    return 1.0 / np.sqrt((ss / x.shape[-1] if norm == "rms" else ss) + eps)
+
+
+def norm_rope(x, weight, cos, sin, norm="rms", eps=1e-6, interleaved=False):
+    """Normed and rotated heads of x [T, H, d]; cos, sin [T, rotary_dim / 2] of each token."""
+    x, weight, cos, sin = map(_f64, (x, weight, cos, sin))
+    return _turn(x * _scale(x, norm, eps) * (1.0 if weight is None else weight), cos, sin, interleaved)
+
+
+def norm_rope_bwd(x, weight, cos, sin, d_out, norm="rms", eps=1e-6, interleaved=False):
+    """(dx, dweight) of norm_rope for sum <d_out, out>."""
+    x, weight, cos, sin, d_out = map(_f64, (x, weight, cos, sin, d_out))
+    r = _scale(x, norm, eps)
+    dn = _turn(d_out, cos, -sin, interleaved)
+    g = dn * (1.0 if weight is None else weight)
+    share = 1.0 / x.shape[-1] if norm == "rms" else 1.0
+    return r * g - x * r ** 3 * share * (g * x).sum(-1, keepdims=True), (dn * x * r).sum((0, 1))
