@@ -1,5 +1,6 @@
 // gdn_scan.cu -- the selective state space scan: prompts (and the trainer's forward) and
 // single tokens.  The arithmetic is in gdn_scan.cuh.
+#include "gdn_async.cuh"
 #include "gdn_host.h"
 #include "gdn_scan.cuh"
 
@@ -26,187 +27,234 @@ __device__ __forceinline__ float scatter_sum(float (&s)[L], int j) {
     return s[0];
 }
 
-// Prompts.  A CTA walks one sequence over CB channels, a lane 8 states of one channel (L = S / 8
-// lanes a channel).  Per tile of TT tokens the threads first share the work per (token, channel),
-// 16 bytes of x, dt and z each: d = softplus(dt + bias) and d x go to shared memory for the
-// lanes, the next tile's loads are issued, the lanes walk the tile and leave sum_s h C in
-// shared memory, and the threads add D x, apply the gate and store 16 bytes.
+// Prompts.  A CTA walks one sequence over CB channels in tiles of TT tokens, a lane 8 states of Q
+// neighbouring channels (L = S / 8 lanes a channel): every B and C it reads from shared memory
+// serves Q channels.  Per tile:
+//   1. the work per (token, channel), shared out as 16-byte chunks of x and dt: d = softplus(dt +
+//      bias) and d x go to shared memory for the walk, B and C become fp32;
+//   2. the next tile's copies are issued (asynchronous, so they take no registers; a thread reads
+//      back only x, dt and z chunks that it copied itself);
+//   3. the walk: the recurrence over the tile's tokens, sum_s h C left where d was;
+//   4. D x, gate and 16-byte stores of y.
 template <typename T, int S>
 struct FwdTile {
-    static constexpr int L = S / 8, CB = 128 / L, TT = 16, VN = V16<T>::n;
+    static constexpr int L = S / 8, Q = 2, CB = S == 8 ? 128 : S == 64 ? 32 : 64, NT = CB * L / Q, VN = V16<T>::n;
+    static constexpr int TT = S == 8 ? 8 : 16;
     static constexpr int CH = CB / VN;                        // 16-byte chunks of a row
-    static constexpr int NV = (TT * CH + 127) / 128;          // of x (dt, z) per thread and tile
+    static constexpr int NV = (TT * CH + NT - 1) / NT;        // of x (dt, z) per thread and tile
+    static constexpr int RS = NT / CH;                        // tokens between a thread's chunks
     static constexpr int BCH = S / VN;                        // chunks of a row of B (C)
-    static constexpr int NB = (2 * TT * BCH + 127) / 128;     // of B and C per thread and tile
+    static constexpr int NB = (2 * TT * BCH + NT - 1) / NT;   // of B and C per thread and tile
+    static constexpr int MINB = 512 / NT;                     // CTAs an SM shall hold: 16 warps, 128 registers
     // {d, d x} of channel c at c float2s plus one 16-byte gap per 16 channels: the chunk-wise
     // stores and the lanes' loads are both free of bank conflicts.
     static constexpr int ROW = CB + (CB / 16) * 2;            // float2s per token
-    static constexpr int YROW = CB + (L > 1 ? 32 / L : 0);    // the lanes' stores of L tokens miss each other's banks
     alignas(16) float2 d[TT][ROW];
-    alignas(16) float y[TT][YROW];
     alignas(16) float b[2][TT][S];
+    uint4 x[2][TT][CH], z[2][TT][CH], dt[TT][CH];
+    uint4 bc[2 * TT * BCH];
     alignas(16) float D[CB];
     alignas(16) float bias[CB];
+    static_assert(NT % CH == 0, "a thread keeps its columns");
 };
 
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[4]) {
+    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+    v[2] = make_float2(bf_lo(u.z), bf_hi(u.z)), v[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
+}
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
+    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+
 template <typename T, int S>
-__global__ void __launch_bounds__(128) scan_fwd_kernel(const Params p) {
+__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const Params p) {
     using F = FwdTile<T, S>;
-    constexpr int L = F::L, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, BCH = F::BCH, NB = F::NB;
-    __shared__ __align__(16) F sm;
+    constexpr int L = F::L, Q = F::Q, NT = F::NT, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB;
+    __shared__ F sm;
     const int tid = threadIdx.x;
     const int nb = p.bpg * p.G;
     const int n = blockIdx.x / nb, blk = blockIdx.x % nb;
     const int g = blk / p.bpg, cg0 = (blk % p.bpg) * CB, c0 = g * p.CG + cg0;
-    const int j = tid % L, cl = tid / L;
-    const bool ok = cg0 + cl < p.CG;
+    const int j = tid % L, cl = tid / L * Q;
+    const bool ok = cg0 + cl < p.CG;  // all Q or none: p.CG is a multiple of 8
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
     const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
     const bool has_slot = slot >= 0 && slot < p.num_slots;
     const bool use_init = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0);
 
-    for (int c = tid; c < CB; c += 128) {
+    // this thread's chunks: columns col .. col + VN - 1 of tokens row0, row0 + RS, ..
+    const int row0 = tid / CH, ch = tid % CH, col = ch * VN;
+    const bool cok = cg0 + col < p.CG;
+    const bool gate = p.z != nullptr, sp = p.softplus != 0;
+    const T* x = static_cast<const T*>(p.x) + c0 + col + (bos + row0) * p.ldx;
+    const T* dt = static_cast<const T*>(p.dt) + c0 + col + (bos + row0) * p.lddt;
+    const T* z = gate ? static_cast<const T*>(p.z) + c0 + col + (bos + row0) * p.ldz : nullptr;
+    T* y = static_cast<T*>(p.y) + c0 + col + (int64_t)(bos + row0) * p.C;
+    const T* Bg = static_cast<const T*>(p.B) + (int64_t)g * S;
+    const T* Cg = static_cast<const T*>(p.Cm) + (int64_t)g * S;
+    // Chunks behind the sequence or the group's channels are not copied: what the walk makes of
+    // the shared memory's old contents there is never stored.
+    auto copy = [&](int t0, int buf) {
+#pragma unroll
+        for (int r = 0; r < NV; ++r) {
+            const int tt = row0 + r * RS;
+            if (tt < TT && t0 + tt < eos && cok) {
+                copy16_async(&sm.x[buf][tt][ch], x + r * RS * p.ldx);
+                copy16_async(&sm.dt[tt][ch], dt + r * RS * p.lddt);
+                if (gate) copy16_async(&sm.z[buf][tt][ch], z + r * RS * p.ldz);
+            }
+        }
+        x += TT * p.ldx, dt += TT * p.lddt, z += TT * p.ldz;
+#pragma unroll
+        for (int r = 0; r < NB; ++r) {
+            const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
+            const int64_t t = t0 + w / BCH;
+            if (which < 2 && t < eos) copy16_async(&sm.bc[v], which ? Cg + t * p.ldC + (w % BCH) * VN : Bg + t * p.ldB + (w % BCH) * VN);
+        }
+        copy_commit();
+    };
+    copy(bos, 0);
+
+    for (int c = tid; c < CB; c += NT) {
         const bool in = cg0 + c < p.CG;
         sm.D[c] = in && p.D ? __ldg(p.D + c0 + c) : 0.f;
         sm.bias[c] = in && p.bias ? __ldg(p.bias + c0 + c) : 0.f;
     }
-    float2 A2[4], h[4];
+    float2 A2[Q][4], h[Q][4];
     const int64_t own = ok ? (int64_t)(c0 + cl) * S + 8 * j : 0;
     float* st = p.state + (int64_t)slot * p.C * S + own;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float2 t[2];
-        load4(p.A_log + own + 4 * i, t);
-        A2[2 * i] = make_float2(a_log2(t[0].x), a_log2(t[0].y));
-        A2[2 * i + 1] = make_float2(a_log2(t[1].x), a_log2(t[1].y));
-        const float4 u = use_init ? *reinterpret_cast<const float4*>(st + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        h[2 * i] = make_float2(u.x, u.y), h[2 * i + 1] = make_float2(u.z, u.w);
-    }
-    const T* x = static_cast<const T*>(p.x) + c0;
-    const T* dt = static_cast<const T*>(p.dt) + c0;
-    const T* z = static_cast<const T*>(p.z) + c0;
-    const T* Bg = static_cast<const T*>(p.B) + (int64_t)g * S;
-    const T* Cg = static_cast<const T*>(p.Cm) + (int64_t)g * S;
-    T* y = static_cast<T*>(p.y) + c0;
-    const bool gate = p.z != nullptr, sp = p.softplus != 0;
-    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-
-    uint4 rx[NV], rd[NV], rz[NV], rb[NB];
-    auto load = [&](int t0) {
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int r = 0; r < NV; ++r) {
-            const int v = tid + 128 * r, tt = v / CH, c = (v % CH) * VN;
-            const int64_t t = t0 + tt;
-            const bool in = tt < TT && t < eos && cg0 + c < p.CG;
-            rx[r] = in ? ld16_stream(x + t * p.ldx + c) : none;
-            rd[r] = in ? ld16_stream(dt + t * p.lddt + c) : none;
-            rz[r] = in && gate ? ld16_stream(z + t * p.ldz + c) : none;
+        for (int i = 0; i < 2; ++i) {
+            const int64_t at = q * S + 4 * i;
+            float2 t[2];
+            load4(p.A_log + own + at, t);
+            A2[q][2 * i] = make_float2(a_log2(t[0].x), a_log2(t[0].y));
+            A2[q][2 * i + 1] = make_float2(a_log2(t[1].x), a_log2(t[1].y));
+            const float4 u = use_init ? *reinterpret_cast<const float4*>(st + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            h[q][2 * i] = make_float2(u.x, u.y), h[q][2 * i + 1] = make_float2(u.z, u.w);
         }
-#pragma unroll
-        for (int r = 0; r < NB; ++r) {
-            const int v = tid + 128 * r, which = v / (TT * BCH), w = v % (TT * BCH), tt = w / BCH;
-            const int64_t t = t0 + tt;
-            rb[r] = none;
-            if (which < 2 && t < eos)
-                rb[r] = ld16(which ? Cg + t * p.ldC + (w % BCH) * VN : Bg + t * p.ldB + (w % BCH) * VN);
-        }
-    };
-    load(bos);
     __syncthreads();
-    for (int t0 = bos; t0 < eos; t0 += TT) {
-        uint4 cx[NV], cz[NV];
+    for (int t0 = bos, buf = 0; t0 < eos; t0 += TT, buf ^= 1) {
+        copy_wait<0>();
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
-            const int v = tid + 128 * r, tt = v / CH, c = (v % CH) * VN;
-            cx[r] = rx[r], cz[r] = rz[r];
+            const int tt = row0 + r * RS;
             if (tt < TT) {
-                float xv[VN], dv[VN];
-                unpack(rx[r], xv);
-                unpack(rd[r], dv);
-                float4* to = reinterpret_cast<float4*>(&sm.d[tt][c + (c / 16) * 2]);
+                float2 xv[VN / 2], dv[VN / 2];
+                unpack2(sm.x[buf][tt][ch], xv);
+                unpack2(sm.dt[tt][ch], dv);
+                float4* to = reinterpret_cast<float4*>(&sm.d[tt][col + (col / 16) * 2]);
 #pragma unroll
-                for (int e = 0; e < VN; e += 2) {
-                    const float2 b2 = *reinterpret_cast<const float2*>(&sm.bias[c + e]);
-                    const float d0 = step_of(dv[e], b2.x, sp), d1 = step_of(dv[e + 1], b2.y, sp);
-                    to[e / 2] = make_float4(d0, __fmul_rn(d0, xv[e]), d1, __fmul_rn(d1, xv[e + 1]));
+                for (int e = 0; e < VN / 2; ++e) {
+                    const float2 d = step_of(dv[e], *reinterpret_cast<const float2*>(&sm.bias[col + 2 * e]), sp);
+                    const float2 dx = __fmul2_rn(d, xv[e]);
+                    to[e] = make_float4(d.x, dx.x, d.y, dx.y);
                 }
             }
         }
 #pragma unroll
         for (int r = 0; r < NB; ++r) {
-            const int v = tid + 128 * r, which = v / (TT * BCH), w = v % (TT * BCH);
+            const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
             if (which < 2) {
                 float f[VN];
-                unpack(rb[r], f);
+                unpack(sm.bc[v], f);
                 float4* to = reinterpret_cast<float4*>(&sm.b[which][w / BCH][(w % BCH) * VN]);
 #pragma unroll
                 for (int e = 0; e < VN; e += 4) to[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
             }
         }
         __syncthreads();
-        load(t0 + TT);
+        copy(t0 + TT, buf ^ 1);
         const int len = min(TT, eos - t0);
-        const float2* dp = &sm.d[0][cl + (cl / 16) * 2];
-        auto token = [&](int tt) {
-            const float2 d = dp[tt * F::ROW];
+        float2* dp = &sm.d[0][cl + (cl / 16) * 2];
+        auto token = [&](int tt, float (&s)[Q]) {
+            float2 d[Q];
+#pragma unroll
+            for (int q = 0; q < Q; q += 2) {
+                const float4 u = *reinterpret_cast<const float4*>(dp + tt * F::ROW + q);
+                d[q] = make_float2(u.x, u.y), d[q + 1] = make_float2(u.z, u.w);
+            }
             const float4* b4 = reinterpret_cast<const float4*>(&sm.b[0][tt][8 * j]);
             const float4* c4 = reinterpret_cast<const float4*>(&sm.b[1][tt][8 * j]);
-            const float2 d2 = make_float2(d.x, d.x), x2 = make_float2(d.y, d.y);
-            float2 acc;
+            float2 acc[Q];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 b = b4[i], c = c4[i];
-                advance(h[2 * i], A2[2 * i], d2, x2, make_float2(b.x, b.y));
-                advance(h[2 * i + 1], A2[2 * i + 1], d2, x2, make_float2(b.z, b.w));
-                acc = i ? __ffma2_rn(h[2 * i], make_float2(c.x, c.y), acc) : __fmul2_rn(h[0], make_float2(c.x, c.y));
-                acc = __ffma2_rn(h[2 * i + 1], make_float2(c.z, c.w), acc);
+            for (int k = 0; k < 2; ++k) {
+                const float4 b = b4[k], c = c4[k];
+                const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
+                const float2 k0 = make_float2(c.x, c.y), k1 = make_float2(c.z, c.w);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    advance(h[q][2 * k], A2[q][2 * k], both(d[q].x), both(d[q].y), b0);
+                    advance(h[q][2 * k + 1], A2[q][2 * k + 1], both(d[q].x), both(d[q].y), b1);
+                    acc[q] = k ? __ffma2_rn(h[q][2 * k], k0, acc[q]) : __fmul2_rn(h[q][0], k0);
+                    acc[q] = __ffma2_rn(h[q][2 * k + 1], k1, acc[q]);
+                }
             }
-            return __fadd_rn(acc.x, acc.y);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) s[q] = __fadd_rn(acc[q].x, acc[q].y);
+        };
+        auto leave = [&](int tt, const float (&s)[Q]) {  // only this channel's lanes read its d, and they have
+#pragma unroll
+            for (int q = 0; q < Q; ++q) dp[tt * F::ROW + q].x = s[q];
         };
         if (len == TT) {
-#pragma unroll (TT / L > 4 ? 2 : 1)
+#pragma unroll (L == 2 ? 2 : 1)
             for (int tt = 0; tt < TT; tt += L) {
-                float s[L];
+                float s[Q][L], out[Q];
 #pragma unroll
-                for (int i = 0; i < L; ++i) s[i] = token(tt + i);
-                sm.y[tt + j][cl] = scatter_sum<L>(s, j);
+                for (int k = 0; k < L; ++k) {
+                    float one[Q];
+                    token(tt + k, one);
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) s[q][k] = one[q];
+                }
+#pragma unroll
+                for (int q = 0; q < Q; ++q) out[q] = scatter_sum<L>(s[q], j);
+                leave(tt + j, out);
             }
         } else {
             for (int tt = 0; tt < len; ++tt) {
-                float s = token(tt);
+                float s[Q];
+                token(tt, s);
 #pragma unroll
-                for (int off = 1; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-                if (j == 0) sm.y[tt][cl] = s;
+                for (int q = 0; q < Q; ++q)
+#pragma unroll
+                    for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
+                if (j == 0) leave(tt, s);
             }
         }
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
-            const int v = tid + 128 * r, tt = v / CH, c = (v % CH) * VN;
-            if (tt < len && cg0 + c < p.CG) {
-                float xv[VN], zv[VN], out[VN];
-                unpack(cx[r], xv);
-                unpack(cz[r], zv);
+            const int tt = row0 + r * RS;
+            if (tt < len && cok) {
+                float2 xv[VN / 2], zv[VN / 2], sig;
+                float out[VN];
+                unpack2(sm.x[buf][tt][ch], xv);
+                if (gate) unpack2(sm.z[buf][tt][ch], zv);
+                const float4* from = reinterpret_cast<const float4*>(&sm.d[tt][col + (col / 16) * 2]);
 #pragma unroll
-                for (int e = 0; e < VN; e += 4) {
-                    const float4 s4 = *reinterpret_cast<const float4*>(&sm.y[tt][c + e]);
-                    const float4 D4 = *reinterpret_cast<const float4*>(&sm.D[c + e]);
-                    out[e] = finish_y(s4.x, D4.x, xv[e]), out[e + 1] = finish_y(s4.y, D4.y, xv[e + 1]);
-                    out[e + 2] = finish_y(s4.z, D4.z, xv[e + 2]), out[e + 3] = finish_y(s4.w, D4.w, xv[e + 3]);
+                for (int e = 0; e < VN / 2; ++e) {
+                    const float4 s = from[e];
+                    float2 o = __ffma2_rn(*reinterpret_cast<const float2*>(&sm.D[col + 2 * e]), xv[e], make_float2(s.x, s.z));
+                    if (gate) o = __fmul2_rn(o, silu2(zv[e], sig));
+                    out[2 * e] = o.x, out[2 * e + 1] = o.y;
                 }
-                if (gate) {
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) out[e] = __fmul_rn(out[e], silu_fast(zv[e]));
-                }
-                st16_stream(y + (int64_t)(t0 + tt) * p.C + c, pack(out));
+                st16_stream(y + (int64_t)r * RS * p.C, pack(out));
             }
         }
+        y += (int64_t)TT * p.C;
     }
+    copy_wait<0>();
     if (has_slot && ok) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float4*>(st + 4 * i) = make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float4*>(st + q * S + 4 * i) = make_float4(h[q][2 * i].x, h[q][2 * i].y, h[q][2 * i + 1].x, h[q][2 * i + 1].y);
     }
 }
 
@@ -227,15 +275,16 @@ __global__ void __launch_bounds__(128) scan_update_kernel(const Params p) {
     const float4 u = *reinterpret_cast<const float4*>(st);
     h[0] = make_float2(u.x, u.y), h[1] = make_float2(u.z, u.w);
     const float xv = load1(static_cast<const T*>(p.x) + n * p.ldx + c);
-    const float d = step_of(load1(static_cast<const T*>(p.dt) + n * p.lddt + c), p.bias ? __ldg(p.bias + c) : 0.f, p.softplus);
+    const float d = step_of(both(load1(static_cast<const T*>(p.dt) + n * p.lddt + c)), both(p.bias ? __ldg(p.bias + c) : 0.f), p.softplus).x;
     const float dx = __fmul_rn(d, xv);
     load4(static_cast<const T*>(p.B) + n * p.ldB + (int64_t)g * S + 4 * j, b);
     load4(static_cast<const T*>(p.Cm) + n * p.ldC + (int64_t)g * S + 4 * j, cc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         advance(h[i], make_float2(a_log2(A2[i].x), a_log2(A2[i].y)), make_float2(d, d), make_float2(dx, dx), b[i]);
-    float s = finish_y(sum_states4<L>(h, cc, j), p.D ? __ldg(p.D + c) : 0.f, xv);
-    if (p.z) s = __fmul_rn(s, silu_fast(load1(static_cast<const T*>(p.z) + n * p.ldz + c)));
+    float s = __fmaf_rn(p.D ? __ldg(p.D + c) : 0.f, xv, sum_states4<L>(h, cc, j));
+    float2 sig;
+    if (p.z) s = __fmul_rn(s, silu2(both(load1(static_cast<const T*>(p.z) + n * p.ldz + c)), sig).x);
     if (!ok) return;
     if (j == 1) store1(static_cast<T*>(p.y) + (int64_t)n * p.C + c, s);
     *reinterpret_cast<float4*>(st) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
@@ -264,30 +313,34 @@ gdn_status prepare(const gdn_scan_shape* s, const void* x, const void* dt, const
     return GDN_OK;
 }
 
-// K::cb(S): channels of a CTA.
-template <template <typename, int> class K, typename T>
-gdn_status by_states(int S, cudaStream_t s, Params& p) {
-    const int cb = K<T, 8>::cb(S);
+// K<T, S>::go launches; K<T, S>::cb: channels of a CTA.
+template <template <typename, int> class K, typename T, int S>
+gdn_status launch(cudaStream_t s, Params& p) {
+    constexpr int cb = K<T, S>::cb;
     p.bpg = (p.CG + cb - 1) / cb;
     const long long ctas = (long long)p.N * p.G * p.bpg;
     if (ctas >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
-    switch (S) {
-        case 8: K<T, 8>::go((unsigned)ctas, s, p); break;
-        case 16: K<T, 16>::go((unsigned)ctas, s, p); break;
-        case 32: K<T, 32>::go((unsigned)ctas, s, p); break;
-        case 64: K<T, 64>::go((unsigned)ctas, s, p); break;
-        default: return GDN_ERR_UNSUPPORTED;
-    }
+    K<T, S>::go((unsigned)ctas, s, p);
     return launch_status();
+}
+template <template <typename, int> class K, typename T>
+gdn_status by_states(int S, cudaStream_t s, Params& p) {
+    switch (S) {
+        case 8: return launch<K, T, 8>(s, p);
+        case 16: return launch<K, T, 16>(s, p);
+        case 32: return launch<K, T, 32>(s, p);
+        case 64: return launch<K, T, 64>(s, p);
+    }
+    return GDN_ERR_UNSUPPORTED;
 }
 template <typename T, int S>
 struct FwdK {
-    static int cb(int states) { return 128 / (states / 8); }
-    static void go(unsigned grid, cudaStream_t s, const Params& p) { scan_fwd_kernel<T, S><<<grid, 128, 0, s>>>(p); }
+    static constexpr int cb = FwdTile<T, S>::CB;
+    static void go(unsigned grid, cudaStream_t s, const Params& p) { scan_fwd_kernel<T, S><<<grid, FwdTile<T, S>::NT, 0, s>>>(p); }
 };
 template <typename T, int S>
 struct UpdK {
-    static int cb(int states) { return 128 / (states / 4); }
+    static constexpr int cb = 128 / (S / 4);
     static void go(unsigned grid, cudaStream_t s, const Params& p) { scan_update_kernel<T, S><<<grid, 128, 0, s>>>(p); }
 };
 

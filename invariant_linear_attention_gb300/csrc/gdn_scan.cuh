@@ -34,30 +34,40 @@ __device__ __forceinline__ float a_log2(float A_log) { return __fmul_rn(-expf(A_
 // softplus(v) = max(v, 0) + log(1 + u), u = e^-|v| in (0, 1], with log(1 + u) = 2 artanh(w),
 // w = u / (2 + u) <= 1/3: relative accuracy is kept for the small steps of strongly negative v,
 // which log of a rounded 1 + u would lose.  artanh(w) / w is a polynomial of degree 4 in w^2
-// (Chebyshev interpolation on [0, 1/9], error 4e-9).  `sig` is the derivative, sigmoid(v).
-__device__ __forceinline__ float log1p_unit(float u) {
-    const float w = __fmul_rn(u, rcp_approx(__fadd_rn(u, 2.f))), q = __fmul_rn(w, w);
-    float p = __fmaf_rn(0.2817465662956238f, q, 0.2796141803264618f);
-    p = __fmaf_rn(p, q, 0.40024852752685547f);
-    p = __fmaf_rn(p, q, 0.6666631698608398f);
-    p = __fmaf_rn(p, q, 2.f);
-    return __fmul_rn(p, w);
+// (Chebyshev interpolation on [0, 1/9], error 4e-9).  Two values at a time: packed operations
+// take half the issue slots.  `u` is left for the derivative.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 softplus2(const float2& v, float2& u) {
+    const float2 m = make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f));
+    const float2 e = __fmul2_rn(__ffma2_rn(m, both(-2.f), v), both(kLog2e));  // v - 2 max(v, 0) = -|v|, exactly
+    u = make_float2(ex2(e.x), ex2(e.y));
+    const float2 s = __fadd2_rn(u, both(2.f));
+    const float2 w = __fmul2_rn(u, make_float2(rcp_approx(s.x), rcp_approx(s.y))), q = __fmul2_rn(w, w);
+    float2 p = __ffma2_rn(both(0.2817465662956238f), q, both(0.2796141803264618f));
+    p = __ffma2_rn(p, q, both(0.40024852752685547f));
+    p = __ffma2_rn(p, q, both(0.6666631698608398f));
+    p = __ffma2_rn(p, q, both(2.f));
+    return __ffma2_rn(p, w, m);
 }
-__device__ __forceinline__ float softplus(float v) {
-    const float u = ex2(__fmul_rn(fabsf(v), -kLog2e));
-    return __fadd_rn(fmaxf(v, 0.f), log1p_unit(u));
+// Its derivative sigmoid(v), from the u that softplus2 left.
+__device__ __forceinline__ float2 sigmoid2(const float2& v, const float2& u) {
+    const float2 s = __fadd2_rn(u, both(1.f));
+    const float a = rcp_approx(s.x), b = rcp_approx(s.y);
+    return make_float2(v.x >= 0.f ? a : __fmul_rn(u.x, a), v.y >= 0.f ? b : __fmul_rn(u.y, b));
 }
-__device__ __forceinline__ float softplus(float v, float& sig) {
-    const float u = ex2(__fmul_rn(fabsf(v), -kLog2e));
-    const float r = rcp_approx(__fadd_rn(1.f, u));
-    sig = v >= 0.f ? r : __fmul_rn(u, r);
-    return __fadd_rn(fmaxf(v, 0.f), log1p_unit(u));
+// silu(z) = z / (1 + e^-z) and, with it, sigmoid(z).
+__device__ __forceinline__ float2 silu2(const float2& z, float2& sig) {
+    const float2 e = __fmul2_rn(z, both(-kLog2e));
+    const float2 s = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), both(1.f));
+    sig = make_float2(rcp_approx(s.x), rcp_approx(s.y));
+    return __fmul2_rn(z, sig);
 }
 
-// The step d of one (token, channel) from the raw dt and the channel's bias.
-__device__ __forceinline__ float step_of(float raw, float bias, bool use_softplus) {
-    const float v = __fadd_rn(raw, bias);
-    return use_softplus ? softplus(v) : v;
+// The steps d of two (token, channel) pairs from the raw dt and the channels' biases.
+__device__ __forceinline__ float2 step_of(const float2& raw, const float2& bias, bool use_softplus) {
+    const float2 v = __fadd2_rn(raw, bias);
+    float2 u;
+    return use_softplus ? softplus2(v, u) : v;
 }
 
 // Two neighbouring states one token on: h <- exp2(d A2) h + dx B.
@@ -66,9 +76,6 @@ __device__ __forceinline__ void advance(float2& h, const float2& A2, const float
     const float2 e = __fmul2_rn(d, A2);
     h = __ffma2_rn(make_float2(ex2(e.x), ex2(e.y)), h, __fmul2_rn(dx, B));
 }
-
-// y of a token: the tree's sum, the skip term, the gate.
-__device__ __forceinline__ float finish_y(float sum, float D, float x) { return __fmaf_rn(D, x, sum); }
 
 struct Params {
     int N, T, C, G, CG, bpg;  // CG: channels per group, bpg: channel blocks per group

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(128) scan_states_kernel(const BwdParams q) {
             store_state(out, h);
             out += (int64_t)p.C * S;
         }
-        const float d = step_of(load1(dt + t * p.lddt), bias, p.softplus);
+        const float d = step_of(both(load1(dt + t * p.lddt)), both(bias), p.softplus).x;
         const float dx = __fmul_rn(d, load1(x + t * p.ldx));
         float2 b[2];
         load4(B + t * p.ldB, b);
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(const BwdParams q) {
         for (int i = 0; i < kChunk; ++i) {
             if (i >= len) break;
             const int t = t0 + i;
-            const float d = step_of(load1(dt + t * p.lddt), bias, p.softplus);
+            const float d = step_of(both(load1(dt + t * p.lddt)), both(bias), p.softplus).x;
             const float dx = __fmul_rn(d, load1(x + t * p.ldx));
             float2 b[2], cc[2];
             load4(B + t * p.ldB, b);
@@ -158,7 +158,12 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(const BwdParams q) {
             const int t = t0 + i;
             const float xv = load1(x + t * p.ldx);
             float sig = 1.f, d = __fadd_rn(load1(dt + t * p.lddt), bias);
-            if (p.softplus) d = softplus(d, sig);
+            if (p.softplus) {
+                float2 u;
+                const float2 v = both(d);
+                d = softplus2(v, u).x;
+                sig = sigmoid2(v, u).x;
+            }
             const float dx = __fmul_rn(d, xv);
             const float dyv = l.ok ? load1(dy + (int64_t)t * p.C) : 0.f;
             float e = dyv;
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(128) scan_bwd_kernel(const BwdParams q) {
                 e = __fmul_rn(dyv, __fmul_rn(zv, s));
                 const float ds = __fmul_rn(s, __fmaf_rn(zv, __fsub_rn(1.f, s), 1.f));
                 if (l.ok && l.j == 1)
-                    store1(static_cast<T*>(q.dz) + (int64_t)t * p.C + l.c, __fmul_rn(__fmul_rn(dyv, finish_y(ysum[i], D, xv)), ds));
+                    store1(static_cast<T*>(q.dz) + (int64_t)t * p.C + l.c, __fmul_rn(__fmul_rn(dyv, __fmaf_rn(D, xv, ysum[i])), ds));
             }
             float2 b[2], cc[2];
             load4(B + t * p.ldB, b);
