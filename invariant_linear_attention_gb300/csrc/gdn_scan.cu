@@ -58,14 +58,6 @@ struct FwdTile {
     static_assert(NT % CH == 0, "a thread keeps its columns");
 };
 
-__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[4]) {
-    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
-    v[2] = make_float2(bf_lo(u.z), bf_hi(u.z)), v[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
-}
-__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
-    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-}
-
 template <typename T, int S>
 __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const Params p) {
     using F = FwdTile<T, S>;

@@ -106,6 +106,15 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float2 (&v)[2]) {
     v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
 }
 
+// The values of a 16-byte chunk as packed pairs.
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[4]) {
+    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+    v[2] = make_float2(bf_lo(u.z), bf_hi(u.z)), v[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
+}
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
+    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+
 // Bounds of sequence n, whatever cu_seqlens holds.
 __device__ __forceinline__ void bounds(const int32_t* cu, int n, int T, int& bos, int& eos) {
     bos = max(0, min(__ldg(cu + n), T));

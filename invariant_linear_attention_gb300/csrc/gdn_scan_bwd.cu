@@ -1,15 +1,26 @@
-// gdn_scan_bwd.cu -- gradient of the selective scan.  With e = d_y silu(z) and g the gradient
-// with respect to h:
+// gdn_scan_bwd.cu -- gradient of the selective scan.  With e = d_y silu(z), g the gradient with
+// respect to h and G = a g what of it reaches the token before:
 //
-//     g_t = e_t Cm_t + a_{t+1} g_{t+1}      (from d_final_state behind the last token)
-//     dC = sum_c e h,  dB = sum_c g d x,  u = sum_s g B,  w = g a h_{t-1}
-//     dx = d u + D e,  dd = x u + sum_s w A,  ddt = dd sigmoid,  dz = d_y (y / silu) silu'
-//     dA_log = A sum_t w d,  dD = sum_t e x,  ddt_bias = sum_t ddt,  d_init_state = a_0 g_0
+//     g_t = e_t C_t + G_{t+1}               (G = d_final_state behind the last token)
+//     dC = sum_c e h,  dB = sum_c g d x,  u = sum_s g B,  w = G_t h_{t-1}
+//     dx = d u + D e,  dd = x u + sum_s w A,  ddt = dd softplus',  dz = d_y (y / silu) silu'
+//     dA_log = A sum_t w d,  dD = sum_t e x,  ddt_bias = sum_t ddt,  d_init_state = G_0
 //
-// First the states at every kChunk-th token (the forward recurrence without its outputs), then
-// the chunks of a sequence last to first: a chunk's states are recomputed into registers and
-// walked backwards.  The sums over channels leave one partial per channel block, the sums over
-// tokens one per sequence; two small kernels add those up in order.
+// A training batch has few sequences, and a walk is bound by its own latency, so the sequences
+// are cut into segments of m tiles of 8 tokens that are walked side by side:
+//   1. local: every segment's final state from a zero start, its G from a zero end (both in one
+//      forward pass, with the running product of the decays), the states at its tiles' starts
+//      and the sums of d up to there;
+//   2. join: along each sequence, the segments' true start states and end G's;
+//   3. grad: per segment, tiles last to first.  A tile's states are recomputed from its start,
+//      four tokens at a time into registers, and those tokens walked backwards;
+//   4. sums: the channel blocks' partials of dB and dC, the segments' of the parameters' gradients.
+// Every sum's order is fixed by the shapes and cu_seqlens.
+//
+// The fp32 pipe and the instruction issue bound 1 and 3: per state and token 6 packed products or
+// sums and 1 exponential in 1, 14.5 and 2.5 in 3; HBM traffic is 7 (T, C) tensors, 64 bytes
+// per channel and tile for the tiles' states, written and read once, and the segments' states.
+#include "gdn_async.cuh"
 #include "gdn_host.h"
 #include "gdn_scan.cuh"
 
@@ -18,36 +29,168 @@ namespace {
 
 using namespace scan;
 
-constexpr int kChunk = 8;
+constexpr int kTile = 8;
 
 struct BwdParams {
     Params f;
+    int m;  // tiles per segment
     const float *h0, *dhT;
     const void* dy;
     void *dx, *ddt, *dz, *dB, *dC;
     float *dA, *dD, *dbias, *dh0;
-    float *ckpt, *bc, *pA, *pD, *pb;
+    // Workspace.  Segment k of sequence n is number cu[n] / (m kTile) + n + k (never two on one),
+    // its tile i number segment * m + i.
+    float* tiles;  // [tiles, C, S] the state at the tile's start, from a zero start of its segment
+    float* cum;    // [tiles, C] sum of d up to the tile's start
+    float* seg_h;  // [segments, C, S] local final state, then the true start state
+    float* seg_g;  // [segments, C, S] local G, then the true end G, then the segment's part of dA
+    float* seg_d;  // [segments, C] sum of d
+    float* bc;     // [channel blocks, T, 2, S] parts of dB and dC
+    float *pD, *pb;  // [segments, C]
 };
 
-// Chunk k of sequence n is number cu[n] / kChunk + n + k: never two on one number.
-__device__ __forceinline__ int64_t chunk_base(int bos, int n) { return (int64_t)(bos / kChunk) + n; }
-
-struct Lane {
-    int n, g, j, c, blk;
-    bool ok;
+// Channels and threads of a CTA: a lane holds 4 states (L = S / 4 lanes a channel) of 4 channels.
+template <typename T, int S>
+struct Geo {
+    static constexpr int L = S / 4, CB = S == 64 ? 32 : 64, NT = CB * L / 4, VN = V16<T>::n;
+    static constexpr int CH = CB / VN, NV = (kTile * CH + NT - 1) / NT, RS = NT / CH;  // 16-byte chunks, as in the forward
+    static constexpr int BCH = S / VN, NB = (2 * kTile * BCH + NT - 1) / NT;
+    static_assert(NT % 32 == 0 && NT % CH == 0, "whole warps; a thread keeps its columns");
 };
-template <int S>
-__device__ __forceinline__ Lane lane_of(const Params& p) {
-    constexpr int L = S / 4, CB = 128 / L;
-    const int nb = p.bpg * p.G;
-    Lane l;
-    l.n = blockIdx.x / nb, l.blk = blockIdx.x % nb;
-    l.g = l.blk / p.bpg, l.j = threadIdx.x % L;
-    const int cg = (l.blk % p.bpg) * CB + threadIdx.x / L;
-    l.ok = cg < p.CG;
-    l.c = l.g * p.CG + (l.ok ? cg : 0);
-    return l;
+
+// What both walks read per (token, channel): {d, d x, e, softplus'}, and B and C in fp32.  Channel
+// c of a token lies at float4 place(c): threads that write 8 (or 4) neighbours and lanes that
+// read one each all miss each other's banks.  Zeros where there is no token or no channel: such
+// a step has a = 1 and adds nothing.
+__device__ __forceinline__ int place(int c) { return (c & ~7) | ((c ^ (c >> 3)) & 7); }
+
+template <typename T, int S>
+struct Input {
+    using F = Geo<T, S>;
+    alignas(16) float4 d[kTile][F::CB];
+    alignas(16) float b[2][kTile][S];
+    uint4 x[2][kTile][F::CH], dt[2][kTile][F::CH], dy[2][kTile][F::CH], z[2][kTile][F::CH];
+    uint4 bc[2][2 * kTile * F::BCH];
+};
+
+// Where a CTA stands: sequence, segment, its tokens [lo, hi), group, channels.
+struct Where {
+    int n, seg, lo, hi, eos, g, blk, cg0, c0;
+};
+template <typename T, int S>
+__device__ __forceinline__ bool where(const BwdParams& q, Where& w) {
+    const Params& p = q.f;
+    const int nb = p.bpg * p.G, len = q.m * kTile;
+    const int at = blockIdx.x / nb;
+    w.blk = blockIdx.x % nb, w.g = w.blk / p.bpg, w.cg0 = (w.blk % p.bpg) * Geo<T, S>::CB, w.c0 = w.g * p.CG + w.cg0;
+    // the last sequence whose first segment is at or before `at`
+    int lo = 0, hi = p.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (max(0, min(__ldg(p.cu + mid), p.T)) / len + mid <= at) lo = mid;
+        else hi = mid - 1;
+    }
+    int bos;
+    bounds(p.cu, lo, p.T, bos, w.eos);
+    const int k = at - (bos / len + lo);
+    w.n = lo, w.seg = at;
+    if (k < 0 || k > (w.eos - bos) / len) return false;
+    w.lo = bos + k * len;
+    w.hi = min(w.eos, w.lo + len);
+    return w.lo < w.hi;
 }
+
+// A thread's share of a CTA's inputs: columns col .. col + VN - 1 of tokens row0, row0 + RS, .. of a tile.
+template <typename T, int S, int NB_ = Geo<T, S>::NB>
+struct Feed {
+    using F = Geo<T, S>;
+    static constexpr int VN = F::VN;
+    int row0, ch, col, hi;
+    bool cok, gate, sp;
+    const T *x, *dt, *dy, *z, *B, *C;
+    int64_t ldx, lddt, lddy, ldz, ldB, ldC;
+    float2 bias[VN / 2];
+
+    __device__ __forceinline__ Feed(const BwdParams& q, const Where& w) {
+        const Params& p = q.f;
+        row0 = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, col = ch * VN, hi = w.hi;
+        cok = w.cg0 + col < p.CG, gate = p.z != nullptr, sp = p.softplus != 0;
+        const int c = w.c0 + col;
+        x = static_cast<const T*>(p.x) + c, dt = static_cast<const T*>(p.dt) + c, dy = static_cast<const T*>(q.dy) + c;
+        z = gate ? static_cast<const T*>(p.z) + c : nullptr;
+        B = static_cast<const T*>(p.B) + (int64_t)w.g * S, C = static_cast<const T*>(p.Cm) + (int64_t)w.g * S;
+        ldx = p.ldx, lddt = p.lddt, lddy = p.C, ldz = p.ldz, ldB = p.ldB, ldC = p.ldC;
+#pragma unroll
+        for (int e = 0; e < VN / 2; ++e)
+            bias[e] = cok && p.bias ? make_float2(__ldg(p.bias + c + 2 * e), __ldg(p.bias + c + 2 * e + 1)) : both(0.f);
+    }
+    __device__ __forceinline__ bool has(int t0, int r) const {
+        const int tt = row0 + r * F::RS;
+        return tt < kTile && t0 + tt < hi && cok;
+    }
+    __device__ __forceinline__ void copy(Input<T, S>& in, int t0, int buf) const {
+#pragma unroll
+        for (int r = 0; r < F::NV; ++r) {
+            const int tt = row0 + r * F::RS;
+            const int64_t t = t0 + tt;
+            if (has(t0, r)) {
+                copy16_async(&in.x[buf][tt][ch], x + t * ldx);
+                copy16_async(&in.dt[buf][tt][ch], dt + t * lddt);
+                copy16_async(&in.dy[buf][tt][ch], dy + t * lddy);
+                if (gate) copy16_async(&in.z[buf][tt][ch], z + t * ldz);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NB_; ++r) {
+            const int v = threadIdx.x + F::NT * r, which = v / (kTile * F::BCH), k = v % (kTile * F::BCH);
+            const int64_t t = t0 + k / F::BCH;
+            if (which < 2 && t < hi) copy16_async(&in.bc[buf][v], which ? C + t * ldC + (k % F::BCH) * VN : B + t * ldB + (k % F::BCH) * VN);
+        }
+    }
+    // {d, d x, e, softplus'} and the fp32 B and C of the tile whose copies have arrived.
+    __device__ __forceinline__ void prepare(Input<T, S>& in, int t0, int buf) const {
+#pragma unroll
+        for (int r = 0; r < F::NV; ++r) {
+            const int tt = row0 + r * F::RS;
+            if (tt >= kTile) continue;
+            if (!has(t0, r)) {
+#pragma unroll
+                for (int e = 0; e < VN; ++e) in.d[tt][place(col + e)] = make_float4(0.f, 0.f, 0.f, 0.f);
+                continue;
+            }
+            float2 xv[VN / 2], dv[VN / 2], ev[VN / 2], zv[VN / 2];
+            unpack2(in.x[buf][tt][ch], xv);
+            unpack2(in.dt[buf][tt][ch], dv);
+            unpack2(in.dy[buf][tt][ch], ev);
+            if (gate) unpack2(in.z[buf][tt][ch], zv);
+#pragma unroll
+            for (int e = 0; e < VN / 2; ++e) {
+                float2 d = __fadd2_rn(dv[e], bias[e]), sig = both(1.f), u, s;
+                if (sp) {
+                    const float2 v = d;
+                    d = softplus2(v, u);
+                    sig = sigmoid2(v, u);
+                }
+                const float2 dx = __fmul2_rn(d, xv[e]);
+                const float2 g = gate ? __fmul2_rn(ev[e], silu2(zv[e], s)) : ev[e];
+                in.d[tt][place(col + 2 * e)] = make_float4(d.x, dx.x, g.x, sig.x);
+                in.d[tt][place(col + 2 * e + 1)] = make_float4(d.y, dx.y, g.y, sig.y);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < NB_; ++r) {
+            const int v = threadIdx.x + F::NT * r, which = v / (kTile * F::BCH), k = v % (kTile * F::BCH);
+            if (which < 2) {
+                const bool ok = t0 + k / F::BCH < hi;
+                float f[VN];
+                unpack(in.bc[buf][v], f);
+                float4* to = reinterpret_cast<float4*>(&in.b[which][k / F::BCH][(k % F::BCH) * VN]);
+#pragma unroll
+                for (int e = 0; e < VN; e += 4) to[e / 4] = ok ? make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+    }
+};
 
 __device__ __forceinline__ void load_state(const float* p, float2 (&h)[2]) {
     const float4 u = *reinterpret_cast<const float4*>(p);
@@ -56,244 +199,495 @@ __device__ __forceinline__ void load_state(const float* p, float2 (&h)[2]) {
 __device__ __forceinline__ void store_state(float* p, const float2 (&h)[2]) {
     *reinterpret_cast<float4*>(p) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
 }
+__device__ __forceinline__ float2 ex2_2(const float2& v) { return make_float2(ex2(v.x), ex2(v.y)); }
 
+// ---------------------------------------------------------------- 1. local
 template <typename T, int S>
-__global__ void __launch_bounds__(128) scan_states_kernel(const BwdParams q) {
+__global__ void __launch_bounds__(Geo<T, S>::NT, 512 / Geo<T, S>::NT) scan_local_kernel(const BwdParams q) {
+    using F = Geo<T, S>;
+    constexpr int L = F::L;
+    __shared__ Input<T, S> in;
+    Where w;
+    if (!where<T, S>(q, w)) return;
     const Params& p = q.f;
-    const Lane l = lane_of<S>(p);
-    int bos, eos;
-    bounds(p.cu, l.n, p.T, bos, eos);
-    if (!l.ok) return;
-    float2 A2[2], h[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    load4(p.A_log + (int64_t)l.c * S + 4 * l.j, A2);
+    const Feed<T, S> feed(q, w);
+    feed.copy(in, w.lo, 0);
+    copy_commit();
+    const int j = threadIdx.x % L, cl = threadIdx.x / L * 4;
+    const bool ok = w.cg0 + cl < p.CG;  // all 4 or none: p.CG is a multiple of 8
+    const int64_t C = p.C, own = ok ? (int64_t)(w.c0 + cl) * S + 4 * j : 0;
+    float2 A2[4][2], h[4][2], G[4][2], P[4][2];
+    float cum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) A2[i] = make_float2(a_log2(A2[i].x), a_log2(A2[i].y));
-    if (q.h0) load_state(q.h0 + ((int64_t)l.n * p.C + l.c) * S + 4 * l.j, h);
-    const float bias = p.bias ? __ldg(p.bias + l.c) : 0.f;
-    const T* x = static_cast<const T*>(p.x) + l.c;
-    const T* dt = static_cast<const T*>(p.dt) + l.c;
-    const T* B = static_cast<const T*>(p.B) + (int64_t)l.g * S + 4 * l.j;
-    float* out = q.ckpt + (chunk_base(bos, l.n) * p.C + l.c) * S + 4 * l.j;
-    for (int t = bos; t < eos; ++t) {
-        if ((t - bos) % kChunk == 0) {
-            store_state(out, h);
-            out += (int64_t)p.C * S;
+    for (int c = 0; c < 4; ++c) {
+        load4(p.A_log + own + (int64_t)(ok ? c : 0) * S, A2[c]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            A2[c][i] = make_float2(a_log2(A2[c][i].x), a_log2(A2[c][i].y));
+            h[c][i] = G[c][i] = both(0.f), P[c][i] = both(1.f);
         }
-        const float d = step_of(both(load1(dt + t * p.lddt)), both(bias), p.softplus).x;
-        const float dx = __fmul_rn(d, load1(x + t * p.ldx));
-        float2 b[2];
-        load4(B + t * p.ldB, b);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) advance(h[i], A2[i], make_float2(d, d), make_float2(dx, dx), b[i]);
     }
-}
-
-template <int L>
-__device__ __forceinline__ float sum_lanes(float s) {
+    int at[4];  // this lane's channels in a row of in.d
 #pragma unroll
-    for (int off = 1; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    return s;
-}
-template <int L>
-__device__ __forceinline__ float sum_channels(float s) {
+    for (int c = 0; c < 4; ++c) at[c] = place(cl + c);
+    int64_t tile = (int64_t)w.seg * q.m;
+    for (int t0 = w.lo, buf = 0; t0 < w.hi; t0 += kTile, buf ^= 1, ++tile) {
+        copy_wait<0>();
+        feed.prepare(in, t0, buf);
+        __syncthreads();
+        feed.copy(in, t0 + kTile, buf ^ 1);
+        copy_commit();
+        if (ok && t0 > w.lo) {
 #pragma unroll
-    for (int off = L; off < 32; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    return s;
-}
-
-template <typename T, int S>
-__global__ void __launch_bounds__(128) scan_bwd_kernel(const BwdParams q) {
-    constexpr int L = S / 4;
-    __shared__ float sums[4][kChunk][2][S];  // per warp: dB and dC of the chunk's tokens
-    const Params& p = q.f;
-    const Lane l = lane_of<S>(p);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int bos, eos;
-    bounds(p.cu, l.n, p.T, bos, eos);
-    float2 A2[2], A[2], G[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    load4(p.A_log + (int64_t)l.c * S + 4 * l.j, A2);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        A[i] = make_float2(-expf(A2[i].x), -expf(A2[i].y));
-        A2[i] = make_float2(a_log2(A2[i].x), a_log2(A2[i].y));
-    }
-    const int64_t so = ((int64_t)l.n * p.C + l.c) * S + 4 * l.j;
-    if (q.dhT) load_state(q.dhT + so, G);
-    float2 dA[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    float dD = 0.f, db = 0.f;
-    const float bias = p.bias ? __ldg(p.bias + l.c) : 0.f, D = p.D ? __ldg(p.D + l.c) : 0.f;
-    const T* x = static_cast<const T*>(p.x) + l.c;
-    const T* dt = static_cast<const T*>(p.dt) + l.c;
-    const T* z = p.z ? static_cast<const T*>(p.z) + l.c : nullptr;
-    const T* dy = static_cast<const T*>(q.dy) + l.c;
-    const T* B = static_cast<const T*>(p.B) + (int64_t)l.g * S + 4 * l.j;
-    const T* Cm = static_cast<const T*>(p.Cm) + (int64_t)l.g * S + 4 * l.j;
-    const int chunks = (eos - bos + kChunk - 1) / kChunk;
-    for (int k = chunks - 1; k >= 0; --k) {
-        const int t0 = bos + k * kChunk, len = min(kChunk, eos - t0);
-        float2 h[2], ah[kChunk][2], a[kChunk][2];
-        load_state(q.ckpt + ((chunk_base(bos, l.n) + k) * p.C + l.c) * S + 4 * l.j, h);
-        float ysum[kChunk];
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-            if (i >= len) break;
-            const int t = t0 + i;
-            const float d = step_of(both(load1(dt + t * p.lddt)), both(bias), p.softplus).x;
-            const float dx = __fmul_rn(d, load1(x + t * p.ldx));
-            float2 b[2], cc[2];
-            load4(B + t * p.ldB, b);
-            load4(Cm + t * p.ldC, cc);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float2 e = __fmul2_rn(make_float2(d, d), A2[m]);
-                a[i][m] = make_float2(ex2(e.x), ex2(e.y));
-                ah[i][m] = __fmul2_rn(a[i][m], h[m]);
-                h[m] = __ffma2_rn(make_float2(dx, dx), b[m], ah[i][m]);
-            }
-            ysum[i] = z ? sum_states4<L>(h, cc, l.j) : 0.f;
+            for (int c = 0; c < 4; ++c) store_state(q.tiles + tile * C * S + own + c * S, h[c]);
+            if (j == 0) *reinterpret_cast<float4*>(q.cum + tile * C + w.c0 + cl) = make_float4(cum[0], cum[1], cum[2], cum[3]);
         }
+#pragma unroll 2
+        for (int t = 0; t < kTile; ++t) {
+            float2 b[2], k[2];
+            load_state(&in.b[0][t][4 * j], b);
+            load_state(&in.b[1][t][4 * j], k);
 #pragma unroll
-        for (int i = kChunk - 1; i >= 0; --i) {
-            if (i >= len) continue;
-            const int t = t0 + i;
-            const float xv = load1(x + t * p.ldx);
-            float sig = 1.f, d = __fadd_rn(load1(dt + t * p.lddt), bias);
-            if (p.softplus) {
-                float2 u;
-                const float2 v = both(d);
-                d = softplus2(v, u).x;
-                sig = sigmoid2(v, u).x;
-            }
-            const float dx = __fmul_rn(d, xv);
-            const float dyv = l.ok ? load1(dy + (int64_t)t * p.C) : 0.f;
-            float e = dyv;
-            if (z) {
-                const float zv = load1(z + t * p.ldz), s = rcp_approx(__fadd_rn(1.f, __expf(-zv)));
-                e = __fmul_rn(dyv, __fmul_rn(zv, s));
-                const float ds = __fmul_rn(s, __fmaf_rn(zv, __fsub_rn(1.f, s), 1.f));
-                if (l.ok && l.j == 1)
-                    store1(static_cast<T*>(q.dz) + (int64_t)t * p.C + l.c, __fmul_rn(__fmul_rn(dyv, __fmaf_rn(D, xv, ysum[i])), ds));
-            }
-            float2 b[2], cc[2];
-            load4(B + t * p.ldB, b);
-            load4(Cm + t * p.ldC, cc);
-            float2 u = make_float2(0.f, 0.f), v = u;
-            const float2 e2 = make_float2(e, e), d2 = make_float2(d, d), dx2 = make_float2(dx, dx);
-            float2 sb[2], sc[2];
+            for (int c = 0; c < 4; ++c) {
+                const float4 v = in.d[t][at[c]];
+                cum[c] = __fadd_rn(cum[c], v.x);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float2 ht = __ffma2_rn(dx2, b[m], ah[i][m]);
-                const float2 gt = __ffma2_rn(e2, cc[m], G[m]);
-                u = __ffma2_rn(gt, b[m], u);
-                const float2 w = __fmul2_rn(gt, ah[i][m]);
-                v = __ffma2_rn(w, A[m], v);
-                dA[m] = __ffma2_rn(w, d2, dA[m]);
-                G[m] = __fmul2_rn(a[i][m], gt);
-                sb[m] = l.ok ? __fmul2_rn(gt, dx2) : make_float2(0.f, 0.f);
-                sc[m] = l.ok ? __fmul2_rn(ht, e2) : make_float2(0.f, 0.f);
-            }
-            const float us = sum_lanes<L>(__fadd_rn(u.x, u.y)), vs = sum_lanes<L>(__fadd_rn(v.x, v.y));
-            const float ddt = __fmul_rn(__fmaf_rn(xv, us, vs), sig);
-            dD = __fmaf_rn(e, xv, dD);
-            db = __fadd_rn(db, ddt);
-            if (l.ok && l.j == 0) {
-                store1(static_cast<T*>(q.dx) + (int64_t)t * p.C + l.c, __fmaf_rn(d, us, __fmul_rn(D, e)));
-                store1(static_cast<T*>(q.ddt) + (int64_t)t * p.C + l.c, ddt);
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float v0 = sum_channels<L>(sb[m].x), v1 = sum_channels<L>(sb[m].y);
-                const float v2 = sum_channels<L>(sc[m].x), v3 = sum_channels<L>(sc[m].y);
-                if (lane < L) {
-                    sums[warp][i][0][4 * l.j + 2 * m] = v0, sums[warp][i][0][4 * l.j + 2 * m + 1] = v1;
-                    sums[warp][i][1][4 * l.j + 2 * m] = v2, sums[warp][i][1][4 * l.j + 2 * m + 1] = v3;
+                for (int i = 0; i < 2; ++i) {
+                    const float2 a = ex2_2(__fmul2_rn(both(v.x), A2[c][i]));
+                    h[c][i] = __ffma2_rn(a, h[c][i], __fmul2_rn(both(v.y), b[i]));
+                    P[c][i] = __fmul2_rn(P[c][i], a);
+                    G[c][i] = __ffma2_rn(P[c][i], __fmul2_rn(both(v.z), k[i]), G[c][i]);
                 }
             }
         }
         __syncthreads();
-        for (int f = threadIdx.x; f < len * 2 * S; f += 128) {
-            const float* r = &sums[0][0][0][0] + f;
-            constexpr int W = kChunk * 2 * S;
-            q.bc[((int64_t)l.blk * p.T + t0) * 2 * S + f] = __fadd_rn(__fadd_rn(r[0], r[W]), __fadd_rn(r[2 * W], r[3 * W]));
+    }
+    copy_wait<0>();
+    if (!ok) return;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        store_state(q.seg_h + (int64_t)w.seg * C * S + own + c * S, h[c]);
+        store_state(q.seg_g + (int64_t)w.seg * C * S + own + c * S, G[c]);
+    }
+    if (j == 0) *reinterpret_cast<float4*>(q.seg_d + (int64_t)w.seg * C + w.c0 + cl) = make_float4(cum[0], cum[1], cum[2], cum[3]);
+}
+
+// ---------------------------------------------------------------- 2. join
+// A thread joins 4 states of one channel along one sequence: forwards (blockIdx.z 0) the start
+// states, backwards (1) the end G's.  The loads do not depend on the chain and run ahead of it.
+__global__ void __launch_bounds__(128) scan_join_kernel(const BwdParams q, int S) {
+    const Params& p = q.f;
+    const int64_t CS = (int64_t)p.C * S, i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+    if (i >= CS) return;
+    const int n = blockIdx.y, c = (int)(i / S), len = q.m * kTile;
+    const bool back = blockIdx.z;
+    int bos, eos;
+    bounds(p.cu, n, p.T, bos, eos);
+    const int segs = (eos - bos + len - 1) / len;
+    const int64_t first = bos / len + n;
+    float2 A2[2], h[2] = {both(0.f), both(0.f)};
+    load4(p.A_log + i, A2);
+    A2[0] = make_float2(a_log2(A2[0].x), a_log2(A2[0].y)), A2[1] = make_float2(a_log2(A2[1].x), a_log2(A2[1].y));
+    const float* from = back ? q.dhT : q.h0;
+    if (from) load_state(from + n * CS + i, h);
+    float* seg = back ? q.seg_g : q.seg_h;
+    constexpr int U = 8;
+    for (int k0 = 0; k0 < segs; k0 += U) {
+        float2 s[U][2];
+        float d[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k0 + u < segs) {
+                const int64_t at = first + (back ? segs - 1 - k0 - u : k0 + u);
+                load_state(seg + at * CS + i, s[u]);
+                d[u] = q.seg_d[at * p.C + c];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k0 + u < segs) {
+                const int64_t at = first + (back ? segs - 1 - k0 - u : k0 + u);
+                store_state(seg + at * CS + i, h);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) h[m] = __ffma2_rn(ex2_2(__fmul2_rn(both(d[u]), A2[m])), h[m], s[u][m]);
+            }
+    }
+    if (back && q.dh0) store_state(q.dh0 + n * CS + i, h);
+}
+
+// ---------------------------------------------------------------- 3. grad
+// Sum over the lanes of a channel.  Slot c of lane j holds channel c ^ (j & 3) (j & 1 for L = 2)
+// of the lane's four, so a lane keeps its first slots and sends the others to the lane whose
+// first slots they are, without selecting; lanes beyond four add by a butterfly.  Lane j ends
+// with channel j & 3 (j and j ^ 2 for L = 2).
+template <int L>
+__device__ __forceinline__ void sum_states(float (&v)[4]) {
+    constexpr uint32_t all = 0xffffffffu;
+    if constexpr (L >= 4) {
+        v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[2], 2));
+        v[1] = __fadd_rn(v[1], __shfl_xor_sync(all, v[3], 2));
+        v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[1], 1));
+#pragma unroll
+        for (int off = 4; off < L; off <<= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[0], off));
+    } else {
+        v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[1], 1));
+        v[2] = __fadd_rn(v[2], __shfl_xor_sync(all, v[3], 1));
+    }
+}
+// Sum of a lane's four states over the 32 / L lane groups.  Pair slot m of group k holds pair
+// m ^ (k & 1): the first slot stays, the second goes to the neighbour group; then (four groups
+// or more) a lane keeps x or y by the group's second bit, and further groups add by a butterfly.
+template <int L>
+__device__ __forceinline__ float2 sum_channels(float2 (&v)[2]) {
+    constexpr uint32_t all = 0xffffffffu;
+    v[0].x = __fadd_rn(v[0].x, __shfl_xor_sync(all, v[1].x, L));
+    v[0].y = __fadd_rn(v[0].y, __shfl_xor_sync(all, v[1].y, L));
+    if constexpr (32 / L >= 4) {
+        const bool up = (threadIdx.x & 31) / L & 2;
+        float s = up ? v[0].y : v[0].x;
+        s = __fadd_rn(s, __shfl_xor_sync(all, up ? v[0].x : v[0].y, 2 * L));
+#pragma unroll
+        for (int off = 4 * L; off < 32; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(all, s, off));
+        v[0].x = s;
+    }
+    return v[0];
+}
+
+template <typename T, int S>
+struct GradMem {
+    using F = Geo<T, S>;
+    Input<T, S> in;
+    float uvy[3][kTile][F::CB + 4];
+    float bc[F::NT / 32][kTile][2 * S];  // each warp's dB and dC
+    alignas(16) float4 h[4][F::NT];      // each thread's states at the tile's start
+};
+
+template <typename T, int S>
+__global__ void __launch_bounds__(Geo<T, S>::NT, 384 / Geo<T, S>::NT) scan_grad_kernel(const BwdParams q) {
+    using F = Geo<T, S>;
+    constexpr int L = F::L, NT = F::NT, VN = F::VN;
+    extern __shared__ __align__(16) unsigned char raw[];
+    GradMem<T, S>& sm = *reinterpret_cast<GradMem<T, S>*>(raw);
+    Input<T, S>& in = sm.in;
+    Where w;
+    if (!where<T, S>(q, w)) return;
+    const Params& p = q.f;
+    const Feed<T, S> feed(q, w);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tiles = (w.hi - w.lo + kTile - 1) / kTile;
+    feed.copy(in, w.lo + (tiles - 1) * kTile, 0);
+    copy_commit();
+    const int j = tid % L, jq = j & 3, cl = tid / L * 4, pm = tid / L & 1;
+    const bool ok = w.cg0 + cl < p.CG;
+    const int64_t C = p.C, own = ok ? (int64_t)(w.c0 + cl) * S + 4 * j : 0;
+    // slot c: channel cl + (c ^ jq); pair slot i: states 4 j + 2 (i ^ pm) and the next one
+    int at[4];
+    int64_t so[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) at[c] = place(cl + (c ^ jq)), so[c] = own + (int64_t)(ok ? c ^ jq : 0) * S;
+    auto load_pairs = [&](const float* from, float2 (&v)[2]) {
+        float2 t[2];
+        load_state(from, t);
+        v[0] = pm ? t[1] : t[0], v[1] = pm ? t[0] : t[1];
+    };
+    auto store_pairs = [&](float* to, const float2 (&v)[2]) {
+        const float2 t[2] = {pm ? v[1] : v[0], pm ? v[0] : v[1]};
+        store_state(to, t);
+    };
+    float2 A2[4][2], G[4][2], dA[4][2];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        load_pairs(p.A_log + so[c], A2[c]);
+        load_pairs(q.seg_g + (int64_t)w.seg * C * S + so[c], G[c]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            A2[c][i] = make_float2(a_log2(A2[c][i].x), a_log2(A2[c][i].y));
+            if (!ok) G[c][i] = both(0.f);
+            dA[c][i] = both(0.f);
+        }
+    }
+    float2 sD[VN / 2], sb[VN / 2];  // this thread's sums for dD and ddt_bias
+#pragma unroll
+    for (int e = 0; e < VN / 2; ++e) sD[e] = sb[e] = both(0.f);
+
+    for (int k = tiles - 1, buf = 0; k >= 0; --k, buf ^= 1) {
+        const int t0 = w.lo + k * kTile;
+        const int64_t tile = (int64_t)w.seg * q.m + k;
+        float2 h[4][2];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {  // the tile's start: its segment's start state, decayed, plus the local state
+            load_pairs(q.seg_h + (int64_t)w.seg * C * S + so[c], h[c]);
+            if (k) {
+                float2 s[2];
+                load_pairs(q.tiles + tile * C * S + so[c], s);
+                const float cum = ok ? q.cum[tile * C + w.c0 + cl + (c ^ jq)] : 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) h[c][i] = __ffma2_rn(ex2_2(__fmul2_rn(both(cum), A2[c][i])), h[c][i], s[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (!ok) h[c][i] = both(0.f);
+            sm.h[c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+        }
+        copy_wait<0>();
+        feed.prepare(in, t0, buf);
+        __syncthreads();
+        if (k) feed.copy(in, t0 - kTile, buf ^ 1);
+        copy_commit();
+
+        auto pairs = [&](int which, int t, float2 (&v)[2]) {
+            const float2* from = reinterpret_cast<const float2*>(&in.b[which][t][4 * j]);
+            v[0] = from[pm], v[1] = from[pm ^ 1];
+        };
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {  // to the states before token 4
+            float2 b[2];
+            pairs(0, t, b);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float2 v = *reinterpret_cast<const float2*>(&in.d[t][at[c]]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) advance(h[c][i], A2[c][i], both(v.x), both(v.y), b[i]);
+            }
+        }
+#pragma unroll 1
+        for (int half = 4; half >= 0; half -= 4) {
+            float2 old[4][4][2];  // the states before tokens half .. half + 3
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float2 b[2], kc[2], sc[2];
+                float ys[4];
+                pairs(0, half + t, b);
+                pairs(1, half + t, kc);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 v = in.d[half + t][at[c]];
+                    float2 acc;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        old[t][c][i] = h[c][i];
+                        advance(h[c][i], A2[c][i], both(v.x), both(v.y), b[i]);
+                        acc = i ? __ffma2_rn(h[c][i], kc[i], acc) : __fmul2_rn(h[c][i], kc[i]);
+                        sc[i] = c ? __ffma2_rn(h[c][i], both(v.z), sc[i]) : __fmul2_rn(h[c][i], both(v.z));
+                    }
+                    ys[c] = __fadd_rn(acc.x, acc.y);
+                }
+                if (feed.gate) {
+                    sum_states<L>(ys);
+                    if (j < 4) {
+                        sm.uvy[2][half + t][cl + jq] = ys[0];
+                        if (L == 2) sm.uvy[2][half + t][cl + (jq ^ 2)] = ys[2];
+                    }
+                }
+                const float2 s = sum_channels<L>(sc);
+                if constexpr (32 / L >= 4) {
+                    if (lane / L < 4) sm.bc[warp][half + t][S + 4 * j + 2 * pm + (lane / L >> 1)] = s.x;
+                } else {
+                    *reinterpret_cast<float2*>(&sm.bc[warp][half + t][S + 4 * j + 2 * pm]) = s;
+                }
+            }
+#pragma unroll
+            for (int t = 3; t >= 0; --t) {
+                float2 b[2], kc[2], sbv[2];
+                float us[4], vs[4];
+                pairs(0, half + t, b);
+                pairs(1, half + t, kc);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 v = in.d[half + t][at[c]];
+                    float2 u, x;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 a = ex2_2(__fmul2_rn(both(v.x), A2[c][i]));
+                        const float2 g = __ffma2_rn(both(v.z), kc[i], G[c][i]);
+                        u = i ? __ffma2_rn(g, b[i], u) : __fmul2_rn(g, b[i]);
+                        sbv[i] = c ? __ffma2_rn(g, both(v.y), sbv[i]) : __fmul2_rn(g, both(v.y));
+                        G[c][i] = __fmul2_rn(a, g);
+                        const float2 wv = __fmul2_rn(G[c][i], old[t][c][i]);
+                        x = i ? __ffma2_rn(wv, A2[c][i], x) : __fmul2_rn(wv, A2[c][i]);
+                        dA[c][i] = __ffma2_rn(wv, both(v.x), dA[c][i]);
+                    }
+                    us[c] = __fadd_rn(u.x, u.y), vs[c] = __fadd_rn(x.x, x.y);
+                }
+                sum_states<L>(us);
+                sum_states<L>(vs);
+                if (j < 4) {
+                    sm.uvy[0][half + t][cl + jq] = us[0], sm.uvy[1][half + t][cl + jq] = vs[0];
+                    if (L == 2) sm.uvy[0][half + t][cl + (jq ^ 2)] = us[2], sm.uvy[1][half + t][cl + (jq ^ 2)] = vs[2];
+                }
+                const float2 s = sum_channels<L>(sbv);
+                if constexpr (32 / L >= 4) {
+                    if (lane / L < 4) sm.bc[warp][half + t][4 * j + 2 * pm + (lane / L >> 1)] = s.x;
+                } else {
+                    *reinterpret_cast<float2*>(&sm.bc[warp][half + t][4 * j + 2 * pm]) = s;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float4 u = sm.h[c][tid];
+                h[c][0] = make_float2(u.x, u.y), h[c][1] = make_float2(u.z, u.w);
+            }
         }
         __syncthreads();
-    }
-    if (!l.ok) return;
-    if (q.dh0) store_state(q.dh0 + so, G);
+        // per (token, channel): this thread's chunks
 #pragma unroll
-    for (int m = 0; m < 2; ++m) dA[m] = __fmul2_rn(dA[m], A[m]);
-    store_state(q.pA + so, dA);
-    if (l.j == 0) {
-        q.pD[(int64_t)l.n * p.C + l.c] = dD;
-        q.pb[(int64_t)l.n * p.C + l.c] = db;
+        for (int r = 0; r < F::NV; ++r) {
+            if (!feed.has(t0, r)) continue;
+            const int tt = feed.row0 + r * F::RS, col = feed.col;
+            const int64_t to = (int64_t)(t0 + tt) * C + w.c0 + col;
+            float2 xv[VN / 2], ev[VN / 2], zv[VN / 2];
+            float odx[VN], odt[VN], odz[VN];
+            unpack2(in.x[buf][tt][feed.ch], xv);
+            if (feed.gate) unpack2(in.dy[buf][tt][feed.ch], ev), unpack2(in.z[buf][tt][feed.ch], zv);
+#pragma unroll
+            for (int e = 0; e < VN / 2; ++e) {
+                const float4 v0 = in.d[tt][place(col + 2 * e)], v1 = in.d[tt][place(col + 2 * e + 1)];
+                const float2 d = make_float2(v0.x, v1.x), g = make_float2(v0.z, v1.z), sig = make_float2(v0.w, v1.w);
+                const float2 u = *reinterpret_cast<const float2*>(&sm.uvy[0][tt][col + 2 * e]);
+                const float2 v = __fmul2_rn(*reinterpret_cast<const float2*>(&sm.uvy[1][tt][col + 2 * e]), both(0.6931471805599453f));
+                const float2 D = p.D ? make_float2(__ldg(p.D + w.c0 + col + 2 * e), __ldg(p.D + w.c0 + col + 2 * e + 1)) : both(0.f);
+                const float2 dx = __ffma2_rn(d, u, __fmul2_rn(D, g));
+                const float2 dt = __fmul2_rn(__ffma2_rn(xv[e], u, v), sig);
+                odx[2 * e] = dx.x, odx[2 * e + 1] = dx.y, odt[2 * e] = dt.x, odt[2 * e + 1] = dt.y;
+                sD[e] = __ffma2_rn(g, xv[e], sD[e]);
+                sb[e] = __fadd2_rn(sb[e], dt);
+                if (feed.gate) {
+                    float2 s;
+                    const float2 y = __ffma2_rn(D, xv[e], *reinterpret_cast<const float2*>(&sm.uvy[2][tt][col + 2 * e]));
+                    silu2(zv[e], s);
+                    const float2 slope = __fmul2_rn(s, __ffma2_rn(zv[e], __ffma2_rn(s, both(-1.f), both(1.f)), both(1.f)));
+                    const float2 dz = __fmul2_rn(__fmul2_rn(ev[e], y), slope);
+                    odz[2 * e] = dz.x, odz[2 * e + 1] = dz.y;
+                }
+            }
+            st16_stream(static_cast<T*>(q.dx) + to, pack(odx));
+            st16_stream(static_cast<T*>(q.ddt) + to, pack(odt));
+            if (feed.gate) st16_stream(static_cast<T*>(q.dz) + to, pack(odz));
+        }
+        for (int f = tid; f < min(kTile, w.hi - t0) * 2 * S; f += NT) {
+            float s = (&sm.bc[0][0][0])[f];
+#pragma unroll
+            for (int i = 1; i < NT / 32; ++i) s = __fadd_rn(s, (&sm.bc[i][0][0])[f]);
+            q.bc[((int64_t)w.blk * p.T + t0) * 2 * S + f] = s;
+        }
+    }
+    copy_wait<0>();
+    if (ok) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) dA[c][i] = __fmul2_rn(__fmul2_rn(dA[c][i], A2[c][i]), both(0.6931471805599453f));
+            store_pairs(q.seg_g + (int64_t)w.seg * C * S + so[c], dA[c]);
+        }
+    }
+    // the columns' sums over this CTA's threads, in the order of their rows
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(raw);  // [RS][2][CB]
+#pragma unroll
+    for (int e = 0; e < VN / 2; ++e) {
+        float* to = red + feed.row0 * 2 * F::CB + feed.col + 2 * e;
+        to[0] = sD[e].x, to[1] = sD[e].y, to[F::CB] = sb[e].x, to[F::CB + 1] = sb[e].y;
+    }
+    __syncthreads();
+    for (int f = tid; f < 2 * F::CB; f += NT) {
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < F::RS; ++r) s = __fadd_rn(s, red[r * 2 * F::CB + f]);
+        const int c = f % F::CB;
+        if (w.cg0 + c < p.CG) (f < F::CB ? q.pD : q.pb)[(int64_t)w.seg * C + w.c0 + c] = s;
     }
 }
 
-// dB and dC of every covered token: the channel blocks' partials of its group in order.
+// ---------------------------------------------------------------- 4. sums
+// The first `nbc` CTAs: dB and dC of every covered token, the channel blocks' parts of its group
+// in order.  The others: dA_log [C, S], dD, ddt_bias [C], the segments' parts in order.
 template <typename T, int S>
-__global__ void __launch_bounds__(256) scan_bc_kernel(const BwdParams q) {
+__global__ void __launch_bounds__(256) scan_sums_kernel(const BwdParams q, unsigned nbc) {
     const Params& p = q.f;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, per = (int64_t)p.G * 2 * S;
-    const int end = max(0, min(__ldg(p.cu + p.N), p.T));
-    const int64_t t = i / per;
-    if (t >= end) return;
-    const int g = (int)(i % per) / (2 * S), s = (int)(i % (2 * S));
-    float sum = 0.f;
-    for (int b = 0; b < p.bpg; ++b) sum = __fadd_rn(sum, q.bc[(((int64_t)g * p.bpg + b) * p.T + t) * 2 * S + s]);
-    T* out = static_cast<T*>(s < S ? q.dB : q.dC);
-    store1(out + (t * p.G + g) * S + (s < S ? s : s - S), sum);
-}
-
-// dA_log [C, S], dD, ddt_bias [C]: the sequences' partials in order.
-__global__ void __launch_bounds__(256) scan_params_kernel(int N, int C, int S, const float* __restrict__ pA, const float* __restrict__ pD,
-                                                          const float* __restrict__ pb, float* __restrict__ dA, float* __restrict__ dD,
-                                                          float* __restrict__ db) {
-    const int64_t nA = (int64_t)C * S, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= nA + 2 * C) return;
-    const float* src = i < nA ? pA + i : i < nA + C ? pD + (i - nA) : pb + (i - nA - C);
-    float* dst = i < nA ? dA + i : i < nA + C ? (dD ? dD + (i - nA) : nullptr) : (db ? db + (i - nA - C) : nullptr);
+    if (blockIdx.x < nbc) {
+        const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, per = (int64_t)p.G * 2 * S;
+        const int end = max(0, min(__ldg(p.cu + p.N), p.T));
+        const int64_t t = i / per;
+        if (t >= end) return;
+        const int g = (int)(i % per) / (2 * S), s = (int)(i % (2 * S));
+        float sum = 0.f;
+#pragma unroll 8
+        for (int b = 0; b < p.bpg; ++b) sum = __fadd_rn(sum, q.bc[(((int64_t)g * p.bpg + b) * p.T + t) * 2 * S + s]);
+        T* out = static_cast<T*>(s < S ? q.dB : q.dC);
+        store1(out + (t * p.G + g) * S + (s < S ? s : s - S), sum);
+        return;
+    }
+    const int64_t nA = (int64_t)p.C * S, i = (int64_t)(blockIdx.x - nbc) * blockDim.x + threadIdx.x;
+    if (i >= nA + 2 * p.C) return;
+    const bool isA = i < nA, isD = i < nA + p.C;
+    const float* src = isA ? q.seg_g + i : isD ? q.pD + (i - nA) : q.pb + (i - nA - p.C);
+    float* dst = isA ? q.dA + i : isD ? (q.dD ? q.dD + (i - nA) : nullptr) : (q.dbias ? q.dbias + (i - nA - p.C) : nullptr);
     if (!dst) return;
-    float s = 0.f;
-    for (int n = 0; n < N; ++n) s = __fadd_rn(s, src[n * (i < nA ? nA : C)]);
-    *dst = s;
+    const int64_t step = isA ? nA : p.C;
+    const int len = q.m * kTile;
+    float sum = 0.f;
+    for (int n = 0; n < p.N; ++n) {
+        int bos, eos;
+        bounds(p.cu, n, p.T, bos, eos);
+        const int segs = (eos - bos + len - 1) / len;
+        const float* at = src + (int64_t)(bos / len + n) * step;
+#pragma unroll 8
+        for (int k = 0; k < segs; ++k) sum = __fadd_rn(sum, at[k * step]);
+    }
+    *dst = sum;
 }
 
 struct Layout {
-    size_t ckpt, bc, pA, pD, pb, total;  // offsets in floats
-    int bpg;
+    size_t tiles, cum, seg_h, seg_g, seg_d, bc, pD, pb, total;  // offsets in floats
+    int bpg, m;
+    long long segs;
 };
 Layout layout(const gdn_scan_shape* s) {
-    const int cb = 128 / (s->S / 4), cg = s->C / s->G;
+    const int cb = s->S == 64 ? 32 : 64, cg = s->C / s->G;
     Layout l;
     l.bpg = (cg + cb - 1) / cb;
-    const size_t cs = (size_t)s->C * s->S;
-    l.ckpt = 0;
-    l.bc = l.ckpt + ((size_t)s->T_total / kChunk + s->N) * cs;
-    l.pA = l.bc + (size_t)s->G * l.bpg * s->T_total * 2 * s->S;
-    l.pD = l.pA + s->N * cs;
-    l.pb = l.pD + (size_t)s->N * s->C;
-    l.total = l.pb + (size_t)s->N * s->C;
+    // Long segments save traffic and joins; short ones give a small batch CTAs to run side by side.
+    l.m = ((long long)s->T_total / 64 + s->N) * s->G * l.bpg >= 4LL * kSMs ? 8 : 2;
+    l.segs = (long long)s->T_total / (l.m * kTile) + s->N;
+    const size_t c = s->C, cs = c * s->S, n = (size_t)l.segs;
+    l.tiles = 0;
+    l.cum = l.tiles + n * l.m * cs;
+    l.seg_h = l.cum + n * l.m * c;
+    l.seg_g = l.seg_h + n * cs;
+    l.seg_d = l.seg_g + n * cs;
+    l.bc = l.seg_d + n * c;
+    l.pD = l.bc + (size_t)s->G * l.bpg * s->T_total * 2 * s->S;
+    l.pb = l.pD + n * c;
+    l.total = l.pb + n * c;
     return l;
 }
 
 template <typename T, int S>
-gdn_status launch(cudaStream_t s, const BwdParams& q) {
+gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
+    using F = Geo<T, S>;
     const Params& p = q.f;
-    const long long ctas = (long long)p.N * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S + 255) / 256;
-    if (ctas >= (1LL << 31) || bc >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
-    scan_states_kernel<T, S><<<(unsigned)ctas, 128, 0, s>>>(q);
-    scan_bwd_kernel<T, S><<<(unsigned)ctas, 128, 0, s>>>(q);
-    if (bc) scan_bc_kernel<T, S><<<(unsigned)bc, 256, 0, s>>>(q);
-    scan_params_kernel<<<(unsigned)(((int64_t)p.C * (S + 2) + 255) / 256), 256, 0, s>>>(p.N, p.C, S, q.pA, q.pD, q.pb, q.dA, q.dD, q.dbias);
+    const long long ctas = segs * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S + 255) / 256;
+    const long long par = ((long long)p.C * (S + 2) + 255) / 256;
+    if (ctas >= (1LL << 31) || bc + par >= (1LL << 31) || p.N > 65535) return GDN_ERR_UNSUPPORTED;
+    constexpr size_t smem = sizeof(GradMem<T, S>);
+    if constexpr (smem > 48 * 1024) {
+        if (cudaFuncSetAttribute(scan_grad_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+            return GDN_ERR_CUDA;
+    }
+    if (p.N > 0) {
+        if (p.T > 0) scan_local_kernel<T, S><<<(unsigned)ctas, F::NT, 0, s>>>(q);
+        scan_join_kernel<<<dim3((unsigned)(((int64_t)p.C * S / 4 + 127) / 128), (unsigned)p.N, 2), 128, 0, s>>>(q, S);
+        if (p.T > 0) scan_grad_kernel<T, S><<<(unsigned)ctas, F::NT, smem, s>>>(q);
+    }
+    scan_sums_kernel<T, S><<<(unsigned)(bc + par), 256, 0, s>>>(q, (unsigned)bc);
     return launch_status();
 }
 template <typename T>
-gdn_status by_states(int S, cudaStream_t s, const BwdParams& q) {
+gdn_status by_states(int S, cudaStream_t s, const BwdParams& q, long long segs) {
     switch (S) {
-        case 8: return launch<T, 8>(s, q);
-        case 16: return launch<T, 16>(s, q);
-        case 32: return launch<T, 32>(s, q);
-        case 64: return launch<T, 64>(s, q);
+        case 8: return launch<T, 8>(s, q, segs);
+        case 16: return launch<T, 16>(s, q, segs);
+        case 32: return launch<T, 32>(s, q, segs);
+        case 64: return launch<T, 64>(s, q, segs);
     }
     return GDN_ERR_UNSUPPORTED;
 }
@@ -332,9 +726,8 @@ extern "C" gdn_status gdn_selective_scan_bwd(const gdn_scan_shape* shape, const 
         for (const void* v : {x, dt, B, Cm, z, d_y})
             if (o && o == v) return GDN_ERR_INVALID_ARG;
     if (d_init_state && (d_init_state == init_state || d_init_state == d_final_state)) return GDN_ERR_INVALID_ARG;
-    if (!workspace || !aligned16(workspace) || workspace_bytes < gdn_selective_scan_bwd_workspace_size(shape))
-        return GDN_ERR_WORKSPACE;
     const Layout l = layout(shape);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < l.total * sizeof(float)) return GDN_ERR_WORKSPACE;
     float* w = static_cast<float*>(workspace);
     BwdParams q{};
     scan::Params& p = q.f;
@@ -343,14 +736,11 @@ extern "C" gdn_status gdn_selective_scan_bwd(const gdn_scan_shape* shape, const 
     p.x = x, p.dt = dt, p.z = z, p.B = B, p.Cm = Cm;
     p.ldx = shape->ldx, p.lddt = shape->lddt, p.ldz = shape->ldz, p.ldB = shape->ldB, p.ldC = shape->ldC;
     p.A_log = A_log, p.D = D, p.bias = dt_bias, p.cu = cu_seqlens;
-    q.h0 = init_state, q.dhT = d_final_state, q.dy = d_y;
+    q.m = l.m, q.h0 = init_state, q.dhT = d_final_state, q.dy = d_y;
     q.dx = dx, q.ddt = ddt, q.dz = dz, q.dB = dB, q.dC = dC;
     q.dA = dA_log, q.dD = dD, q.dbias = ddt_bias, q.dh0 = d_init_state;
-    q.ckpt = w + l.ckpt, q.bc = w + l.bc, q.pA = w + l.pA, q.pD = w + l.pD, q.pb = w + l.pb;
+    q.tiles = w + l.tiles, q.cum = w + l.cum, q.seg_h = w + l.seg_h, q.seg_g = w + l.seg_g, q.seg_d = w + l.seg_d;
+    q.bc = w + l.bc, q.pD = w + l.pD, q.pb = w + l.pb;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (shape->N == 0) {  // no tokens, no sequences: the sums are empty
-        scan_params_kernel<<<(unsigned)(((int64_t)p.C * (shape->S + 2) + 255) / 256), 256, 0, s>>>(0, p.C, shape->S, q.pA, q.pD, q.pb, q.dA, q.dD, q.dbias);
-        return launch_status();
-    }
-    return shape->dtype == GDN_BF16 ? by_states<__nv_bfloat16>(shape->S, s, q) : by_states<float>(shape->S, s, q);
+    return shape->dtype == GDN_BF16 ? by_states<__nv_bfloat16>(shape->S, s, q, l.segs) : by_states<float>(shape->S, s, q, l.segs);
 }

@@ -230,6 +230,20 @@ def test_backward_vs_oracle(dtype, S, G, C, gate, states):
     assert (g["dz"] is None) == (not gate) and (g["dD"] is None) == (c.D is None) and (g["d_init_state"] is None) == (not states)
 
 
+@pytest.mark.parametrize("dtype,S,G,C", [(torch.float32, 8, 64, 512), (torch.bfloat16, 16, 56, 448)])
+def test_backward_of_a_batch_with_many_ctas(dtype, S, G, C):
+    # enough channel blocks and tokens for the longer segments, sequences of several of them
+    lens = [390, 0, 150, 64, 1]
+    c = Case(lens, C, G, S, dtype, 23, slow=True)
+    g = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args())
+    want = ref.selective_scan_bwd(cu=c.cu_list, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args())
+    mag = ref.selective_scan_bwd(cu=c.cu_list, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, magnitude=True, **c.args())
+    units = 3 * c.error_units() + C + sum(lens) + 3 * (6 + 2.4 * np.abs(to_np(c.z)).max())
+    for k in want:
+        kind = torch.float32 if g[k].dtype == torch.float32 else dtype
+        check(g[k], want[k], mag[k], units + (40 if k == "dz" else 0), kind, 60 if k == "dz" else 0)
+
+
 def test_backward_repeats_its_bits_and_takes_a_callers_workspace():
     c = Case([300, 41, 0, 7], 200, 1, 16, torch.bfloat16, 18)
     a = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, init_state=c.h0, **c.args())
