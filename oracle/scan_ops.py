@@ -114,7 +114,9 @@ def selective_scan_bwd(x, dt, A_log, B, C, cu, d_out, D=None, z=None, dt_bias=No
         out["dC"][s] = r["dC"].reshape(-1, G, ch // G, S).sum(2)
         if z is not None:
             slope = p[s] * (1.0 + z[s] * (1.0 - p[s]))
-            out["dz"][s] = dy[s] * ((h * C[s]).sum(-1) + D * x[s]) * (np.abs(slope) if magnitude else slope)
+            if magnitude:  # the slope is a sum of two terms that cancel near z = -1.28
+                slope = p[s] * (1.0 + np.abs(z[s]))
+            out["dz"][s] = dy[s] * ((h * C[s]).sum(-1) + D * x[s]) * slope
         out["dA_log"] += r["dA"] * A_sum
         out["dD"] += (e[s] * x[s]).sum(0)
         out["ddt_bias"] += ddt.sum(0)

@@ -12,6 +12,11 @@ itself).  With the products and sums of a token (2 u each, L of them) and those 
     E = 64 + 6 L + 52 min(40, max over channels of sum d |A|) + S / 4.
 The gate adds (6 + 2.4 |z|) u of the result.  A gradient multiplies two such recurrences (2 E)
 and three more products; sums over channels or tokens add one rounding each (C or T): 3 E + C + T.
+The gate's slope p (1 + z (1 - p)), p = sigmoid(z), is a sum that cancels near z = -1.28: with p's
+relative error E_p = (7 + 2.4 |z|) u its absolute error is at most
+p (E_p |1 + z (1 - p)| + |z| p E_p + 2 u (1 + |z|)) <= (E_p + 2 u) p (1 + |z|): the oracle's
+magnitude of dz takes p (1 + |z|) for the slope, and E_p + 2 u is within the 3 (6 + 2.4 |z|) u that
+the gate adds to a gradient.
 A bf16 output adds its own rounding, 2^-8 of the value.
 """
 import numpy as np
@@ -224,9 +229,7 @@ def test_backward_vs_oracle(dtype, S, G, C, gate, states):
             (("dD", "ddt_bias") if c.D is not None else ()):
         wide = k in ("dA_log", "dD", "ddt_bias", "d_init_state")
         assert g[k].dtype == (torch.float32 if wide else dtype)
-        # dz: y passes through the forward's error only, its slope through a cancellation of s (1 + z (1 - s))
-        check(g[k], want[k], mag[k], units + (40 if k == "dz" else 0), torch.float32 if wide else dtype,
-              60 if k == "dz" else 0)
+        check(g[k], want[k], mag[k], units, torch.float32 if wide else dtype)
     assert (g["dz"] is None) == (not gate) and (g["dD"] is None) == (c.D is None) and (g["d_init_state"] is None) == (not states)
 
 
@@ -241,7 +244,7 @@ def test_backward_of_a_batch_with_many_ctas(dtype, S, G, C):
     units = 3 * c.error_units() + C + sum(lens) + 3 * (6 + 2.4 * np.abs(to_np(c.z)).max())
     for k in want:
         kind = torch.float32 if g[k].dtype == torch.float32 else dtype
-        check(g[k], want[k], mag[k], units + (40 if k == "dz" else 0), kind, 60 if k == "dz" else 0)
+        check(g[k], want[k], mag[k], units, kind)
 
 
 def test_backward_repeats_its_bits_and_takes_a_callers_workspace():
