@@ -12,13 +12,13 @@
 //      forward pass, with the running product of the decays), the states at its tiles' starts
 //      and the sums of d up to there;
 //   2. join: along each sequence, the segments' true start states and end G's;
-//   3. grad: per segment, tiles last to first.  A tile's states are recomputed from its start,
-//      four tokens at a time into registers, and those tokens walked backwards;
+//   3. grad: per segment, tiles last to first.  A tile's states are recomputed from its start into
+//      registers, and its tokens walked backwards;
 //   4. sums: the channel blocks' partials of dB and dC, the segments' of the parameters' gradients.
 // Every sum's order is fixed by the shapes and cu_seqlens.
 //
-// The fp32 pipe and the instruction issue bound 1 and 3: per state and token 6 packed products or
-// sums and 1 exponential in 1, 14.5 and 2.5 in 3; HBM traffic is 7 (T, C) tensors, 64 bytes
+// The fp32 pipe and the instruction issue bound 1 and 3: per state and token 6 products or sums
+// (packed by twos) and 1 exponential in 1, 13 and 2 in 3; HBM traffic is 7 (T, C) tensors, 64 bytes
 // per channel and tile for the tiles' states, written and read once, and the segments' states.
 #include "gdn_async.cuh"
 #include "gdn_host.h"
@@ -30,6 +30,7 @@ namespace {
 using namespace scan;
 
 constexpr int kTile = 8;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct BwdParams {
     Params f;
@@ -49,10 +50,11 @@ struct BwdParams {
     float *pD, *pb;  // [segments, C]
 };
 
-// Channels and threads of a CTA: a lane holds 4 states (L = S / 4 lanes a channel) of 4 channels.
-template <typename T, int S>
+// Channels and threads of a CTA: a lane holds 4 states (L = S / 4 lanes a channel) of Q channels.
+__host__ __device__ constexpr int channels_of(int S) { return S <= 16 ? 64 : 32; }
+template <typename T, int S, int Q>
 struct Geo {
-    static constexpr int L = S / 4, CB = S == 64 ? 32 : 64, NT = CB * L / 4, VN = V16<T>::n;
+    static constexpr int L = S / 4, CB = channels_of(S), NT = CB * L / Q, VN = V16<T>::n;
     static constexpr int CH = CB / VN, NV = (kTile * CH + NT - 1) / NT, RS = NT / CH;  // 16-byte chunks, as in the forward
     static constexpr int BCH = S / VN, NB = (2 * kTile * BCH + NT - 1) / NT;
     static_assert(NT % 32 == 0 && NT % CH == 0, "whole warps; a thread keeps its columns");
@@ -66,7 +68,7 @@ __device__ __forceinline__ int place(int c) { return (c & ~7) | ((c ^ (c >> 3)) 
 
 template <typename T, int S>
 struct Input {
-    using F = Geo<T, S>;
+    using F = Geo<T, S, 2>;
     alignas(16) float4 d[kTile][F::CB];
     alignas(16) float b[2][kTile][S];
     uint4 x[2][kTile][F::CH], dt[2][kTile][F::CH], dy[2][kTile][F::CH], z[2][kTile][F::CH];
@@ -82,7 +84,7 @@ __device__ __forceinline__ bool where(const BwdParams& q, Where& w) {
     const Params& p = q.f;
     const int nb = p.bpg * p.G, len = q.m * kTile;
     const int at = blockIdx.x / nb;
-    w.blk = blockIdx.x % nb, w.g = w.blk / p.bpg, w.cg0 = (w.blk % p.bpg) * Geo<T, S>::CB, w.c0 = w.g * p.CG + w.cg0;
+    w.blk = blockIdx.x % nb, w.g = w.blk / p.bpg, w.cg0 = (w.blk % p.bpg) * channels_of(S), w.c0 = w.g * p.CG + w.cg0;
     // the last sequence whose first segment is at or before `at`
     int lo = 0, hi = p.N - 1;
     while (lo < hi) {
@@ -100,55 +102,50 @@ __device__ __forceinline__ bool where(const BwdParams& q, Where& w) {
     return w.lo < w.hi;
 }
 
-// A thread's share of a CTA's inputs: columns col .. col + VN - 1 of tokens row0, row0 + RS, .. of a tile.
-template <typename T, int S, int NB_ = Geo<T, S>::NB>
+// A thread's share of a CTA's inputs: columns col .. col + VN - 1 of tokens row0, row0 + RS, .. of a
+// tile.  Pointers and strides stay in the kernel's parameters: the walks need the registers.
+template <typename T, int S, int Q>
 struct Feed {
-    using F = Geo<T, S>;
+    using F = Geo<T, S, Q>;
     static constexpr int VN = F::VN;
-    int row0, ch, col, hi;
-    bool cok, gate, sp;
-    const T *x, *dt, *dy, *z, *B, *C;
-    int64_t ldx, lddt, lddy, ldz, ldB, ldC;
-    float2 bias[VN / 2];
+    const BwdParams& q;
+    int row0, ch, col, hi, c, g;
+    bool cok;
 
-    __device__ __forceinline__ Feed(const BwdParams& q, const Where& w) {
-        const Params& p = q.f;
-        row0 = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, col = ch * VN, hi = w.hi;
-        cok = w.cg0 + col < p.CG, gate = p.z != nullptr, sp = p.softplus != 0;
-        const int c = w.c0 + col;
-        x = static_cast<const T*>(p.x) + c, dt = static_cast<const T*>(p.dt) + c, dy = static_cast<const T*>(q.dy) + c;
-        z = gate ? static_cast<const T*>(p.z) + c : nullptr;
-        B = static_cast<const T*>(p.B) + (int64_t)w.g * S, C = static_cast<const T*>(p.Cm) + (int64_t)w.g * S;
-        ldx = p.ldx, lddt = p.lddt, lddy = p.C, ldz = p.ldz, ldB = p.ldB, ldC = p.ldC;
-#pragma unroll
-        for (int e = 0; e < VN / 2; ++e)
-            bias[e] = cok && p.bias ? make_float2(__ldg(p.bias + c + 2 * e), __ldg(p.bias + c + 2 * e + 1)) : both(0.f);
+    __device__ __forceinline__ Feed(const BwdParams& q_, const Where& w) : q(q_) {
+        row0 = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, col = ch * VN, hi = w.hi, c = w.c0 + col, g = w.g;
+        cok = w.cg0 + col < q.f.CG;
     }
+    __device__ __forceinline__ bool gate() const { return q.f.z != nullptr; }
     __device__ __forceinline__ bool has(int t0, int r) const {
         const int tt = row0 + r * F::RS;
         return tt < kTile && t0 + tt < hi && cok;
     }
     __device__ __forceinline__ void copy(Input<T, S>& in, int t0, int buf) const {
+        const Params& p = q.f;
 #pragma unroll
         for (int r = 0; r < F::NV; ++r) {
             const int tt = row0 + r * F::RS;
             const int64_t t = t0 + tt;
             if (has(t0, r)) {
-                copy16_async(&in.x[buf][tt][ch], x + t * ldx);
-                copy16_async(&in.dt[buf][tt][ch], dt + t * lddt);
-                copy16_async(&in.dy[buf][tt][ch], dy + t * lddy);
-                if (gate) copy16_async(&in.z[buf][tt][ch], z + t * ldz);
+                copy16_async(&in.x[buf][tt][ch], static_cast<const T*>(p.x) + t * p.ldx + c);
+                copy16_async(&in.dt[buf][tt][ch], static_cast<const T*>(p.dt) + t * p.lddt + c);
+                copy16_async(&in.dy[buf][tt][ch], static_cast<const T*>(q.dy) + t * p.C + c);
+                if (gate()) copy16_async(&in.z[buf][tt][ch], static_cast<const T*>(p.z) + t * p.ldz + c);
             }
         }
 #pragma unroll
-        for (int r = 0; r < NB_; ++r) {
+        for (int r = 0; r < F::NB; ++r) {
             const int v = threadIdx.x + F::NT * r, which = v / (kTile * F::BCH), k = v % (kTile * F::BCH);
             const int64_t t = t0 + k / F::BCH;
-            if (which < 2 && t < hi) copy16_async(&in.bc[buf][v], which ? C + t * ldC + (k % F::BCH) * VN : B + t * ldB + (k % F::BCH) * VN);
+            const int e = g * S + (k % F::BCH) * VN;
+            if (which < 2 && t < hi)
+                copy16_async(&in.bc[buf][v], which ? static_cast<const T*>(p.Cm) + t * p.ldC + e : static_cast<const T*>(p.B) + t * p.ldB + e);
         }
     }
     // {d, d x, e, softplus'} and the fp32 B and C of the tile whose copies have arrived.
     __device__ __forceinline__ void prepare(Input<T, S>& in, int t0, int buf) const {
+        const Params& p = q.f;
 #pragma unroll
         for (int r = 0; r < F::NV; ++r) {
             const int tt = row0 + r * F::RS;
@@ -162,23 +159,24 @@ struct Feed {
             unpack2(in.x[buf][tt][ch], xv);
             unpack2(in.dt[buf][tt][ch], dv);
             unpack2(in.dy[buf][tt][ch], ev);
-            if (gate) unpack2(in.z[buf][tt][ch], zv);
+            if (gate()) unpack2(in.z[buf][tt][ch], zv);
 #pragma unroll
             for (int e = 0; e < VN / 2; ++e) {
-                float2 d = __fadd2_rn(dv[e], bias[e]), sig = both(1.f), u, s;
-                if (sp) {
+                const float2 bias = p.bias ? make_float2(__ldg(p.bias + c + 2 * e), __ldg(p.bias + c + 2 * e + 1)) : both(0.f);
+                float2 d = __fadd2_rn(dv[e], bias), sig = both(1.f), u, s;
+                if (p.softplus) {
                     const float2 v = d;
                     d = softplus2(v, u);
                     sig = sigmoid2(v, u);
                 }
                 const float2 dx = __fmul2_rn(d, xv[e]);
-                const float2 g = gate ? __fmul2_rn(ev[e], silu2(zv[e], s)) : ev[e];
+                const float2 g = gate() ? __fmul2_rn(ev[e], silu2(zv[e], s)) : ev[e];
                 in.d[tt][place(col + 2 * e)] = make_float4(d.x, dx.x, g.x, sig.x);
                 in.d[tt][place(col + 2 * e + 1)] = make_float4(d.y, dx.y, g.y, sig.y);
             }
         }
 #pragma unroll
-        for (int r = 0; r < NB_; ++r) {
+        for (int r = 0; r < F::NB; ++r) {
             const int v = threadIdx.x + F::NT * r, which = v / (kTile * F::BCH), k = v % (kTile * F::BCH);
             if (which < 2) {
                 const bool ok = t0 + k / F::BCH < hi;
@@ -203,14 +201,14 @@ __device__ __forceinline__ float2 ex2_2(const float2& v) { return make_float2(ex
 
 // ---------------------------------------------------------------- 1. local
 template <typename T, int S>
-__global__ void __launch_bounds__(Geo<T, S>::NT, 512 / Geo<T, S>::NT) scan_local_kernel(const BwdParams q) {
-    using F = Geo<T, S>;
+__global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan_local_kernel(const __grid_constant__ BwdParams q) {
+    using F = Geo<T, S, 4>;
     constexpr int L = F::L;
     __shared__ Input<T, S> in;
     Where w;
     if (!where<T, S>(q, w)) return;
     const Params& p = q.f;
-    const Feed<T, S> feed(q, w);
+    const Feed<T, S, 4> feed(q, w);
     feed.copy(in, w.lo, 0);
     copy_commit();
     const int j = threadIdx.x % L, cl = threadIdx.x / L * 4;
@@ -315,55 +313,51 @@ __global__ void __launch_bounds__(128) scan_join_kernel(const BwdParams q, int S
 }
 
 // ---------------------------------------------------------------- 3. grad
-// Sum over the lanes of a channel.  Slot c of lane j holds channel c ^ (j & 3) (j & 1 for L = 2)
-// of the lane's four, so a lane keeps its first slots and sends the others to the lane whose
-// first slots they are, without selecting; lanes beyond four add by a butterfly.  Lane j ends
-// with channel j & 3 (j and j ^ 2 for L = 2).
+// Sum over the lanes of a channel.  Slot c of lane j holds channel c ^ (j & 1) of the lane's two:
+// the first slot stays, the second goes to the neighbour, whose first it is, without selecting;
+// further lanes add by a butterfly.  Lane j ends with channel j & 1.
 template <int L>
-__device__ __forceinline__ void sum_states(float (&v)[4]) {
-    constexpr uint32_t all = 0xffffffffu;
-    if constexpr (L >= 4) {
-        v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[2], 2));
-        v[1] = __fadd_rn(v[1], __shfl_xor_sync(all, v[3], 2));
-        v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[1], 1));
+__device__ __forceinline__ float sum_states(const float (&v)[2]) {
+    float s = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[1], 1));
 #pragma unroll
-        for (int off = 4; off < L; off <<= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[0], off));
-    } else {
-        v[0] = __fadd_rn(v[0], __shfl_xor_sync(all, v[1], 1));
-        v[2] = __fadd_rn(v[2], __shfl_xor_sync(all, v[3], 1));
-    }
+    for (int off = 2; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+    return s;
 }
 // Sum of a lane's four states over the 32 / L lane groups.  Pair slot m of group k holds pair
 // m ^ (k & 1): the first slot stays, the second goes to the neighbour group; then (four groups
 // or more) a lane keeps x or y by the group's second bit, and further groups add by a butterfly.
 template <int L>
-__device__ __forceinline__ float2 sum_channels(float2 (&v)[2]) {
+__device__ __forceinline__ float2 sum_channels(const float2 (&v)[2]) {
     constexpr uint32_t all = 0xffffffffu;
-    v[0].x = __fadd_rn(v[0].x, __shfl_xor_sync(all, v[1].x, L));
-    v[0].y = __fadd_rn(v[0].y, __shfl_xor_sync(all, v[1].y, L));
+    float2 r;
+    r.x = __fadd_rn(v[0].x, __shfl_xor_sync(all, v[1].x, L));
+    r.y = __fadd_rn(v[0].y, __shfl_xor_sync(all, v[1].y, L));
     if constexpr (32 / L >= 4) {
         const bool up = (threadIdx.x & 31) / L & 2;
-        float s = up ? v[0].y : v[0].x;
-        s = __fadd_rn(s, __shfl_xor_sync(all, up ? v[0].x : v[0].y, 2 * L));
+        float s = up ? r.y : r.x;
+        s = __fadd_rn(s, __shfl_xor_sync(all, up ? r.x : r.y, 2 * L));
 #pragma unroll
         for (int off = 4 * L; off < 32; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(all, s, off));
-        v[0].x = s;
+        r.x = s;
     }
-    return v[0];
+    return r;
 }
+
+// Keeps the compiler from loading later tokens' values early: the states of a tile fill the registers.
+__device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
 
 template <typename T, int S>
 struct GradMem {
-    using F = Geo<T, S>;
+    using F = Geo<T, S, 2>;
     Input<T, S> in;
     float uvy[3][kTile][F::CB + 4];
     float bc[F::NT / 32][kTile][2 * S];  // each warp's dB and dC
-    alignas(16) float4 h[4][F::NT];      // each thread's states at the tile's start
+    float2 sums[F::VN][F::NT];           // each thread's sums for dD and ddt_bias (the walk needs the registers)
 };
 
 template <typename T, int S>
-__global__ void __launch_bounds__(Geo<T, S>::NT, 384 / Geo<T, S>::NT) scan_grad_kernel(const BwdParams q) {
-    using F = Geo<T, S>;
+__global__ void __launch_bounds__(Geo<T, S, 2>::NT, 512 / Geo<T, S, 2>::NT) scan_grad_kernel(const __grid_constant__ BwdParams q) {
+    using F = Geo<T, S, 2>;
     constexpr int L = F::L, NT = F::NT, VN = F::VN;
     extern __shared__ __align__(16) unsigned char raw[];
     GradMem<T, S>& sm = *reinterpret_cast<GradMem<T, S>*>(raw);
@@ -371,33 +365,27 @@ __global__ void __launch_bounds__(Geo<T, S>::NT, 384 / Geo<T, S>::NT) scan_grad_
     Where w;
     if (!where<T, S>(q, w)) return;
     const Params& p = q.f;
-    const Feed<T, S> feed(q, w);
+    const Feed<T, S, 2> feed(q, w);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles = (w.hi - w.lo + kTile - 1) / kTile;
     feed.copy(in, w.lo + (tiles - 1) * kTile, 0);
     copy_commit();
-    const int j = tid % L, jq = j & 3, cl = tid / L * 4, pm = tid / L & 1;
+    const int j = tid % L, jq = j & 1, cl = tid / L * 2, pm = tid / L & 1;
     const bool ok = w.cg0 + cl < p.CG;
     const int64_t C = p.C, own = ok ? (int64_t)(w.c0 + cl) * S + 4 * j : 0;
     // slot c: channel cl + (c ^ jq); pair slot i: states 4 j + 2 (i ^ pm) and the next one
-    int at[4];
-    int64_t so[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) at[c] = place(cl + (c ^ jq)), so[c] = own + (int64_t)(ok ? c ^ jq : 0) * S;
+    const int at0 = place(cl + jq), at1 = place(cl + (jq ^ 1));
+    const int64_t so0 = own + (ok ? jq : 0) * S, so1 = own + (ok ? jq ^ 1 : 0) * S;
     auto load_pairs = [&](const float* from, float2 (&v)[2]) {
         float2 t[2];
         load_state(from, t);
         v[0] = pm ? t[1] : t[0], v[1] = pm ? t[0] : t[1];
     };
-    auto store_pairs = [&](float* to, const float2 (&v)[2]) {
-        const float2 t[2] = {pm ? v[1] : v[0], pm ? v[0] : v[1]};
-        store_state(to, t);
-    };
-    float2 A2[4][2], G[4][2], dA[4][2];
+    float2 A2[2][2], G[2][2], dA[2][2];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        load_pairs(p.A_log + so[c], A2[c]);
-        load_pairs(q.seg_g + (int64_t)w.seg * C * S + so[c], G[c]);
+    for (int c = 0; c < 2; ++c) {
+        load_pairs(p.A_log + (c ? so1 : so0), A2[c]);
+        load_pairs(q.seg_g + (int64_t)w.seg * C * S + (c ? so1 : so0), G[c]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             A2[c][i] = make_float2(a_log2(A2[c][i].x), a_log2(A2[c][i].y));
@@ -405,28 +393,26 @@ __global__ void __launch_bounds__(Geo<T, S>::NT, 384 / Geo<T, S>::NT) scan_grad_
             dA[c][i] = both(0.f);
         }
     }
-    float2 sD[VN / 2], sb[VN / 2];  // this thread's sums for dD and ddt_bias
 #pragma unroll
-    for (int e = 0; e < VN / 2; ++e) sD[e] = sb[e] = both(0.f);
+    for (int e = 0; e < VN; ++e) sm.sums[e][tid] = both(0.f);
 
     for (int k = tiles - 1, buf = 0; k >= 0; --k, buf ^= 1) {
         const int t0 = w.lo + k * kTile;
         const int64_t tile = (int64_t)w.seg * q.m + k;
-        float2 h[4][2];
+        float2 h[kTile + 1][2][2];  // the states before each token, and behind the last
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // the tile's start: its segment's start state, decayed, plus the local state
-            load_pairs(q.seg_h + (int64_t)w.seg * C * S + so[c], h[c]);
+        for (int c = 0; c < 2; ++c) {  // the tile's start: its segment's start state, decayed, plus the local state
+            load_pairs(q.seg_h + (int64_t)w.seg * C * S + (c ? so1 : so0), h[0][c]);
             if (k) {
                 float2 s[2];
-                load_pairs(q.tiles + tile * C * S + so[c], s);
+                load_pairs(q.tiles + tile * C * S + (c ? so1 : so0), s);
                 const float cum = ok ? q.cum[tile * C + w.c0 + cl + (c ^ jq)] : 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) h[c][i] = __ffma2_rn(ex2_2(__fmul2_rn(both(cum), A2[c][i])), h[c][i], s[i]);
+                for (int i = 0; i < 2; ++i) h[0][c][i] = __ffma2_rn(ex2_2(__fmul2_rn(both(cum), A2[c][i])), h[0][c][i], s[i]);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (!ok) h[c][i] = both(0.f);
-            sm.h[c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+                if (!ok) h[0][c][i] = both(0.f);
         }
         copy_wait<0>();
         feed.prepare(in, t0, buf);
@@ -439,118 +425,87 @@ __global__ void __launch_bounds__(Geo<T, S>::NT, 384 / Geo<T, S>::NT) scan_grad_
             v[0] = from[pm], v[1] = from[pm ^ 1];
         };
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {  // to the states before token 4
+        for (int t = 0; t < kTile; ++t) {
+            fence();
             float2 b[2];
             pairs(0, t, b);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float2 v = *reinterpret_cast<const float2*>(&in.d[t][at[c]]);
+            for (int c = 0; c < 2; ++c) {
+                const float2 v = *reinterpret_cast<const float2*>(&in.d[t][c ? at1 : at0]);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) advance(h[c][i], A2[c][i], both(v.x), both(v.y), b[i]);
+                for (int i = 0; i < 2; ++i) {
+                    h[t + 1][c][i] = h[t][c][i];
+                    advance(h[t + 1][c][i], A2[c][i], both(v.x), both(v.y), b[i]);
+                }
             }
         }
-#pragma unroll 1
-        for (int half = 4; half >= 0; half -= 4) {
-            float2 old[4][4][2];  // the states before tokens half .. half + 3
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float2 b[2], kc[2], sc[2];
-                float ys[4];
-                pairs(0, half + t, b);
-                pairs(1, half + t, kc);
+        for (int t = kTile - 1; t >= 0; --t) {
+            float2 b[2], kc[2], sB[2], sC[2];
+            float us[2], vs[2], ys[2];
+            fence();
+            pairs(0, t, b);
+            pairs(1, t, kc);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 v = in.d[half + t][at[c]];
-                    float2 acc;
+            for (int c = 0; c < 2; ++c) {
+                const float4 v = in.d[t][c ? at1 : at0];
+                float2 u, x, y;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        old[t][c][i] = h[c][i];
-                        advance(h[c][i], A2[c][i], both(v.x), both(v.y), b[i]);
-                        acc = i ? __ffma2_rn(h[c][i], kc[i], acc) : __fmul2_rn(h[c][i], kc[i]);
-                        sc[i] = c ? __ffma2_rn(h[c][i], both(v.z), sc[i]) : __fmul2_rn(h[c][i], both(v.z));
-                    }
-                    ys[c] = __fadd_rn(acc.x, acc.y);
+                for (int i = 0; i < 2; ++i) {
+                    const float2 a = ex2_2(__fmul2_rn(both(v.x), A2[c][i]));
+                    const float2 g = __ffma2_rn(both(v.z), kc[i], G[c][i]), ht = h[t + 1][c][i];
+                    y = i ? __ffma2_rn(ht, kc[i], y) : __fmul2_rn(ht, kc[i]);
+                    sC[i] = c ? __ffma2_rn(ht, both(v.z), sC[i]) : __fmul2_rn(ht, both(v.z));
+                    u = i ? __ffma2_rn(g, b[i], u) : __fmul2_rn(g, b[i]);
+                    sB[i] = c ? __ffma2_rn(g, both(v.y), sB[i]) : __fmul2_rn(g, both(v.y));
+                    G[c][i] = __fmul2_rn(a, g);
+                    const float2 wv = __fmul2_rn(G[c][i], h[t][c][i]);
+                    x = i ? __ffma2_rn(wv, A2[c][i], x) : __fmul2_rn(wv, A2[c][i]);
+                    dA[c][i] = __ffma2_rn(wv, both(v.x), dA[c][i]);
                 }
-                if (feed.gate) {
-                    sum_states<L>(ys);
-                    if (j < 4) {
-                        sm.uvy[2][half + t][cl + jq] = ys[0];
-                        if (L == 2) sm.uvy[2][half + t][cl + (jq ^ 2)] = ys[2];
-                    }
-                }
-                const float2 s = sum_channels<L>(sc);
-                if constexpr (32 / L >= 4) {
-                    if (lane / L < 4) sm.bc[warp][half + t][S + 4 * j + 2 * pm + (lane / L >> 1)] = s.x;
-                } else {
-                    *reinterpret_cast<float2*>(&sm.bc[warp][half + t][S + 4 * j + 2 * pm]) = s;
-                }
+                us[c] = __fadd_rn(u.x, u.y), vs[c] = __fadd_rn(x.x, x.y), ys[c] = __fadd_rn(y.x, y.y);
             }
-#pragma unroll
-            for (int t = 3; t >= 0; --t) {
-                float2 b[2], kc[2], sbv[2];
-                float us[4], vs[4];
-                pairs(0, half + t, b);
-                pairs(1, half + t, kc);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 v = in.d[half + t][at[c]];
-                    float2 u, x;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 a = ex2_2(__fmul2_rn(both(v.x), A2[c][i]));
-                        const float2 g = __ffma2_rn(both(v.z), kc[i], G[c][i]);
-                        u = i ? __ffma2_rn(g, b[i], u) : __fmul2_rn(g, b[i]);
-                        sbv[i] = c ? __ffma2_rn(g, both(v.y), sbv[i]) : __fmul2_rn(g, both(v.y));
-                        G[c][i] = __fmul2_rn(a, g);
-                        const float2 wv = __fmul2_rn(G[c][i], old[t][c][i]);
-                        x = i ? __ffma2_rn(wv, A2[c][i], x) : __fmul2_rn(wv, A2[c][i]);
-                        dA[c][i] = __ffma2_rn(wv, both(v.x), dA[c][i]);
-                    }
-                    us[c] = __fadd_rn(u.x, u.y), vs[c] = __fadd_rn(x.x, x.y);
-                }
-                sum_states<L>(us);
-                sum_states<L>(vs);
-                if (j < 4) {
-                    sm.uvy[0][half + t][cl + jq] = us[0], sm.uvy[1][half + t][cl + jq] = vs[0];
-                    if (L == 2) sm.uvy[0][half + t][cl + (jq ^ 2)] = us[2], sm.uvy[1][half + t][cl + (jq ^ 2)] = vs[2];
-                }
-                const float2 s = sum_channels<L>(sbv);
-                if constexpr (32 / L >= 4) {
-                    if (lane / L < 4) sm.bc[warp][half + t][4 * j + 2 * pm + (lane / L >> 1)] = s.x;
-                } else {
-                    *reinterpret_cast<float2*>(&sm.bc[warp][half + t][4 * j + 2 * pm]) = s;
-                }
+            const float u = sum_states<L>(us), v = sum_states<L>(vs);
+            if (j < 2) sm.uvy[0][t][cl + jq] = u, sm.uvy[1][t][cl + jq] = v;
+            if (feed.gate()) {
+                const float y = sum_states<L>(ys);
+                if (j < 2) sm.uvy[2][t][cl + jq] = y;
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float4 u = sm.h[c][tid];
-                h[c][0] = make_float2(u.x, u.y), h[c][1] = make_float2(u.z, u.w);
+            const float2 db = sum_channels<L>(sB), dc = sum_channels<L>(sC);
+            if constexpr (32 / L >= 4) {
+                if (lane / L < 4) {
+                    float* to = &sm.bc[warp][t][4 * j + 2 * pm + (lane / L >> 1)];
+                    to[0] = db.x, to[S] = dc.x;
+                }
+            } else {
+                float2* to = reinterpret_cast<float2*>(&sm.bc[warp][t][4 * j + 2 * pm]);
+                to[0] = db, to[S / 2] = dc;
             }
         }
         __syncthreads();
         // per (token, channel): this thread's chunks
 #pragma unroll
         for (int r = 0; r < F::NV; ++r) {
-            if (!feed.has(t0, r)) continue;
+            if (!feed.has(t0, r)) break;
             const int tt = feed.row0 + r * F::RS, col = feed.col;
             const int64_t to = (int64_t)(t0 + tt) * C + w.c0 + col;
             float2 xv[VN / 2], ev[VN / 2], zv[VN / 2];
             float odx[VN], odt[VN], odz[VN];
             unpack2(in.x[buf][tt][feed.ch], xv);
-            if (feed.gate) unpack2(in.dy[buf][tt][feed.ch], ev), unpack2(in.z[buf][tt][feed.ch], zv);
+            if (feed.gate()) unpack2(in.dy[buf][tt][feed.ch], ev), unpack2(in.z[buf][tt][feed.ch], zv);
 #pragma unroll
             for (int e = 0; e < VN / 2; ++e) {
                 const float4 v0 = in.d[tt][place(col + 2 * e)], v1 = in.d[tt][place(col + 2 * e + 1)];
                 const float2 d = make_float2(v0.x, v1.x), g = make_float2(v0.z, v1.z), sig = make_float2(v0.w, v1.w);
                 const float2 u = *reinterpret_cast<const float2*>(&sm.uvy[0][tt][col + 2 * e]);
-                const float2 v = __fmul2_rn(*reinterpret_cast<const float2*>(&sm.uvy[1][tt][col + 2 * e]), both(0.6931471805599453f));
+                const float2 v = __fmul2_rn(*reinterpret_cast<const float2*>(&sm.uvy[1][tt][col + 2 * e]), both(kLn2));
                 const float2 D = p.D ? make_float2(__ldg(p.D + w.c0 + col + 2 * e), __ldg(p.D + w.c0 + col + 2 * e + 1)) : both(0.f);
                 const float2 dx = __ffma2_rn(d, u, __fmul2_rn(D, g));
                 const float2 dt = __fmul2_rn(__ffma2_rn(xv[e], u, v), sig);
                 odx[2 * e] = dx.x, odx[2 * e + 1] = dx.y, odt[2 * e] = dt.x, odt[2 * e + 1] = dt.y;
-                sD[e] = __ffma2_rn(g, xv[e], sD[e]);
-                sb[e] = __fadd2_rn(sb[e], dt);
-                if (feed.gate) {
+                sm.sums[2 * e][tid] = __ffma2_rn(g, xv[e], sm.sums[2 * e][tid]);
+                sm.sums[2 * e + 1][tid] = __fadd2_rn(sm.sums[2 * e + 1][tid], dt);
+                if (feed.gate()) {
                     float2 s;
                     const float2 y = __ffma2_rn(D, xv[e], *reinterpret_cast<const float2*>(&sm.uvy[2][tt][col + 2 * e]));
                     silu2(zv[e], s);
@@ -561,7 +516,7 @@ __global__ void __launch_bounds__(Geo<T, S>::NT, 384 / Geo<T, S>::NT) scan_grad_
             }
             st16_stream(static_cast<T*>(q.dx) + to, pack(odx));
             st16_stream(static_cast<T*>(q.ddt) + to, pack(odt));
-            if (feed.gate) st16_stream(static_cast<T*>(q.dz) + to, pack(odz));
+            if (feed.gate()) st16_stream(static_cast<T*>(q.dz) + to, pack(odz));
         }
         for (int f = tid; f < min(kTile, w.hi - t0) * 2 * S; f += NT) {
             float s = (&sm.bc[0][0][0])[f];
@@ -573,26 +528,23 @@ __global__ void __launch_bounds__(Geo<T, S>::NT, 384 / Geo<T, S>::NT) scan_grad_
     copy_wait<0>();
     if (ok) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) dA[c][i] = __fmul2_rn(__fmul2_rn(dA[c][i], A2[c][i]), both(0.6931471805599453f));
-            store_pairs(q.seg_g + (int64_t)w.seg * C * S + so[c], dA[c]);
+            for (int i = 0; i < 2; ++i) dA[c][i] = __fmul2_rn(__fmul2_rn(dA[c][i], A2[c][i]), both(kLn2));
+            const float2 v[2] = {pm ? dA[c][1] : dA[c][0], pm ? dA[c][0] : dA[c][1]};
+            store_state(q.seg_g + (int64_t)w.seg * C * S + (c ? so1 : so0), v);
         }
     }
     // the columns' sums over this CTA's threads, in the order of their rows
     __syncthreads();
-    float* red = reinterpret_cast<float*>(raw);  // [RS][2][CB]
-#pragma unroll
-    for (int e = 0; e < VN / 2; ++e) {
-        float* to = red + feed.row0 * 2 * F::CB + feed.col + 2 * e;
-        to[0] = sD[e].x, to[1] = sD[e].y, to[F::CB] = sb[e].x, to[F::CB + 1] = sb[e].y;
-    }
-    __syncthreads();
     for (int f = tid; f < 2 * F::CB; f += NT) {
+        const int c = f % F::CB, e = c % VN / 2 * 2 + (f >= F::CB);
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < F::RS; ++r) s = __fadd_rn(s, red[r * 2 * F::CB + f]);
-        const int c = f % F::CB;
+        for (int r = 0; r < F::RS; ++r) {
+            const float2 v = sm.sums[e][r * F::CH + c / VN];
+            s = __fadd_rn(s, c & 1 ? v.y : v.x);
+        }
         if (w.cg0 + c < p.CG) (f < F::CB ? q.pD : q.pb)[(int64_t)w.seg * C + w.c0 + c] = s;
     }
 }
@@ -642,7 +594,7 @@ struct Layout {
     long long segs;
 };
 Layout layout(const gdn_scan_shape* s) {
-    const int cb = s->S == 64 ? 32 : 64, cg = s->C / s->G;
+    const int cb = channels_of(s->S), cg = s->C / s->G;
     Layout l;
     l.bpg = (cg + cb - 1) / cb;
     // Long segments save traffic and joins; short ones give a small batch CTAs to run side by side.
@@ -663,7 +615,6 @@ Layout layout(const gdn_scan_shape* s) {
 
 template <typename T, int S>
 gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
-    using F = Geo<T, S>;
     const Params& p = q.f;
     const long long ctas = segs * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S + 255) / 256;
     const long long par = ((long long)p.C * (S + 2) + 255) / 256;
@@ -674,9 +625,9 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
             return GDN_ERR_CUDA;
     }
     if (p.N > 0) {
-        if (p.T > 0) scan_local_kernel<T, S><<<(unsigned)ctas, F::NT, 0, s>>>(q);
+        if (p.T > 0) scan_local_kernel<T, S><<<(unsigned)ctas, Geo<T, S, 4>::NT, 0, s>>>(q);
         scan_join_kernel<<<dim3((unsigned)(((int64_t)p.C * S / 4 + 127) / 128), (unsigned)p.N, 2), 128, 0, s>>>(q, S);
-        if (p.T > 0) scan_grad_kernel<T, S><<<(unsigned)ctas, F::NT, smem, s>>>(q);
+        if (p.T > 0) scan_grad_kernel<T, S><<<(unsigned)ctas, Geo<T, S, 2>::NT, smem, s>>>(q);
     }
     scan_sums_kernel<T, S><<<(unsigned)(bc + par), 256, 0, s>>>(q, (unsigned)bc);
     return launch_status();
