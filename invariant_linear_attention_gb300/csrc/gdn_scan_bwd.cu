@@ -73,6 +73,8 @@ struct Input {
     alignas(16) float b[2][kTile][S];
     uint4 x[2][kTile][F::CH], dt[2][kTile][F::CH], dy[2][kTile][F::CH], z[2][kTile][F::CH];
     uint4 bc[2][2 * kTile * F::BCH];
+    alignas(16) float D[F::CB];
+    alignas(16) float bias[F::CB];
 };
 
 // Where a CTA stands: sequence, segment, its tokens [lo, hi), group, channels.
@@ -115,6 +117,15 @@ struct Feed {
     __device__ __forceinline__ Feed(const BwdParams& q_, const Where& w) : q(q_) {
         row0 = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, col = ch * VN, hi = w.hi, c = w.c0 + col, g = w.g;
         cok = w.cg0 + col < q.f.CG;
+    }
+    // D and dt_bias of the CTA's channels; in place after the next barrier.
+    __device__ __forceinline__ void columns(Input<T, S>& in, const Where& w) const {
+        const Params& p = q.f;
+        for (int i = threadIdx.x; i < F::CB; i += F::NT) {
+            const bool ok = w.cg0 + i < p.CG;
+            in.D[i] = ok && p.D ? __ldg(p.D + w.c0 + i) : 0.f;
+            in.bias[i] = ok && p.bias ? __ldg(p.bias + w.c0 + i) : 0.f;
+        }
     }
     __device__ __forceinline__ bool gate() const { return q.f.z != nullptr; }
     __device__ __forceinline__ bool has(int t0, int r) const {
@@ -162,8 +173,7 @@ struct Feed {
             if (gate()) unpack2(in.z[buf][tt][ch], zv);
 #pragma unroll
             for (int e = 0; e < VN / 2; ++e) {
-                const float2 bias = p.bias ? make_float2(__ldg(p.bias + c + 2 * e), __ldg(p.bias + c + 2 * e + 1)) : both(0.f);
-                float2 d = __fadd2_rn(dv[e], bias), sig = both(1.f), u, s;
+                float2 d = __fadd2_rn(dv[e], *reinterpret_cast<const float2*>(&in.bias[col + 2 * e])), sig = both(1.f), u, s;
                 if (p.softplus) {
                     const float2 v = d;
                     d = softplus2(v, u);
@@ -211,6 +221,7 @@ __global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan
     const Feed<T, S, 4> feed(q, w);
     feed.copy(in, w.lo, 0);
     copy_commit();
+    feed.columns(in, w);
     const int j = threadIdx.x % L, cl = threadIdx.x / L * 4;
     const bool ok = w.cg0 + cl < p.CG;  // all 4 or none: p.CG is a multiple of 8
     const int64_t C = p.C, own = ok ? (int64_t)(w.c0 + cl) * S + 4 * j : 0;
@@ -229,6 +240,7 @@ __global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan
 #pragma unroll
     for (int c = 0; c < 4; ++c) at[c] = place(cl + c);
     int64_t tile = (int64_t)w.seg * q.m;
+    __syncthreads();
     for (int t0 = w.lo, buf = 0; t0 < w.hi; t0 += kTile, buf ^= 1, ++tile) {
         copy_wait<0>();
         feed.prepare(in, t0, buf);
@@ -273,7 +285,7 @@ __global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan
 // ---------------------------------------------------------------- 2. join
 // A thread joins 4 states of one channel along one sequence: forwards (blockIdx.z 0) the start
 // states, backwards (1) the end G's.  The loads do not depend on the chain and run ahead of it.
-__global__ void __launch_bounds__(128) scan_join_kernel(const BwdParams q, int S) {
+__global__ void __launch_bounds__(128) scan_join_kernel(const __grid_constant__ BwdParams q, int S) {
     const Params& p = q.f;
     const int64_t CS = (int64_t)p.C * S, i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
     if (i >= CS) return;
@@ -352,30 +364,52 @@ struct GradMem {
     Input<T, S> in;
     float uvy[3][kTile][F::CB + 4];
     float bc[F::NT / 32][kTile][2 * S];  // each warp's dB and dC
-    float2 sums[F::VN][F::NT];           // each thread's sums for dD and ddt_bias (the walk needs the registers)
+    // each thread's own: its sums for dD and ddt_bias, its segment's start states, the next tile's local ones
+    float2 sums[F::VN][F::NT];
+    // and its states at the tile's start
+    alignas(16) float4 seg[2][F::NT];
+    alignas(16) float4 tile[2][F::NT];
+    alignas(16) float4 h[2][F::NT];
 };
 
 template <typename T, int S>
-__global__ void __launch_bounds__(Geo<T, S, 2>::NT, 512 / Geo<T, S, 2>::NT) scan_grad_kernel(const __grid_constant__ BwdParams q) {
+__global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 512 : 384) / Geo<T, S, 2>::NT) scan_grad_kernel(const __grid_constant__ BwdParams q) {
     using F = Geo<T, S, 2>;
     constexpr int L = F::L, NT = F::NT, VN = F::VN;
     extern __shared__ __align__(16) unsigned char raw[];
     GradMem<T, S>& sm = *reinterpret_cast<GradMem<T, S>*>(raw);
     Input<T, S>& in = sm.in;
     Where w;
-    if (!where<T, S>(q, w)) return;
+    const bool some = where<T, S>(q, w);
     const Params& p = q.f;
+    const int64_t C = p.C;
+    if (!some) {  // no segment of this number: its parts of the sums are zero
+        const int64_t at = (int64_t)w.seg * C + w.c0, n = min(F::CB, p.CG - w.cg0);
+        for (int i = threadIdx.x; i < n * S; i += NT) q.seg_g[at * S + i] = 0.f;
+        for (int i = threadIdx.x; i < n; i += NT) q.pD[at + i] = q.pb[at + i] = 0.f;
+        return;
+    }
     const Feed<T, S, 2> feed(q, w);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles = (w.hi - w.lo + kTile - 1) / kTile;
     feed.copy(in, w.lo + (tiles - 1) * kTile, 0);
-    copy_commit();
+    feed.columns(in, w);
     const int j = tid % L, jq = j & 1, cl = tid / L * 2, pm = tid / L & 1;
     const bool ok = w.cg0 + cl < p.CG;
-    const int64_t C = p.C, own = ok ? (int64_t)(w.c0 + cl) * S + 4 * j : 0;
+    const int64_t own = ok ? (int64_t)(w.c0 + cl) * S + 4 * j : 0;
     // slot c: channel cl + (c ^ jq); pair slot i: states 4 j + 2 (i ^ pm) and the next one
     const int at0 = place(cl + jq), at1 = place(cl + (jq ^ 1));
     const int64_t so0 = own + (ok ? jq : 0) * S, so1 = own + (ok ? jq ^ 1 : 0) * S;
+    auto copy_tile = [&](int k) {  // the local states at tile k's start
+        const float* from = q.tiles + ((int64_t)w.seg * q.m + k) * C * S;
+        if (k > 0) copy16_async(&sm.tile[0][tid], from + so0), copy16_async(&sm.tile[1][tid], from + so1);
+        copy_commit();
+    };
+    copy_tile(tiles - 1);
+    sm.seg[0][tid] = *reinterpret_cast<const float4*>(q.seg_h + (int64_t)w.seg * C * S + so0);
+    sm.seg[1][tid] = *reinterpret_cast<const float4*>(q.seg_h + (int64_t)w.seg * C * S + so1);
+    auto cum_of = [&](int k, int c) { return ok && k > 0 ? q.cum[((int64_t)w.seg * q.m + k) * C + w.c0 + cl + (c ^ jq)] : 0.f; };
+    float cum[2] = {cum_of(tiles - 1, 0), cum_of(tiles - 1, 1)};
     auto load_pairs = [&](const float* from, float2 (&v)[2]) {
         float2 t[2];
         load_state(from, t);
@@ -396,90 +430,106 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, 512 / Geo<T, S, 2>::NT) scan
 #pragma unroll
     for (int e = 0; e < VN; ++e) sm.sums[e][tid] = both(0.f);
 
+    __syncthreads();
     for (int k = tiles - 1, buf = 0; k >= 0; --k, buf ^= 1) {
         const int t0 = w.lo + k * kTile;
-        const int64_t tile = (int64_t)w.seg * q.m + k;
-        float2 h[kTile + 1][2][2];  // the states before each token, and behind the last
+        copy_wait<0>();
+        float2 h[2][2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // the tile's start: its segment's start state, decayed, plus the local state
-            load_pairs(q.seg_h + (int64_t)w.seg * C * S + (c ? so1 : so0), h[0][c]);
-            if (k) {
-                float2 s[2];
-                load_pairs(q.tiles + tile * C * S + (c ? so1 : so0), s);
-                const float cum = ok ? q.cum[tile * C + w.c0 + cl + (c ^ jq)] : 0.f;
+            const float4 v = sm.seg[c][tid], u = sm.tile[c][tid];
+            h[c][0] = pm ? make_float2(v.z, v.w) : make_float2(v.x, v.y), h[c][1] = pm ? make_float2(v.x, v.y) : make_float2(v.z, v.w);
+            const float2 s[2] = {pm ? make_float2(u.z, u.w) : make_float2(u.x, u.y), pm ? make_float2(u.x, u.y) : make_float2(u.z, u.w)};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) h[0][c][i] = __ffma2_rn(ex2_2(__fmul2_rn(both(cum), A2[c][i])), h[0][c][i], s[i]);
+            for (int i = 0; i < 2; ++i) {
+                if (k) h[c][i] = __ffma2_rn(ex2_2(__fmul2_rn(both(cum[c]), A2[c][i])), h[c][i], s[i]);
+                if (!ok) h[c][i] = both(0.f);
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (!ok) h[0][c][i] = both(0.f);
+            sm.h[c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
         }
-        copy_wait<0>();
+        cum[0] = cum_of(k - 1, 0), cum[1] = cum_of(k - 1, 1);
         feed.prepare(in, t0, buf);
         __syncthreads();
         if (k) feed.copy(in, t0 - kTile, buf ^ 1);
-        copy_commit();
+        copy_tile(k - 1);
 
         auto pairs = [&](int which, int t, float2 (&v)[2]) {
             const float2* from = reinterpret_cast<const float2*>(&in.b[which][t][4 * j]);
             v[0] = from[pm], v[1] = from[pm ^ 1];
         };
-#pragma unroll
-        for (int t = 0; t < kTile; ++t) {
-            fence();
+        auto step = [&](int t, const float2 (&from)[2][2], float2 (&to)[2][2]) {
             float2 b[2];
+            fence();
             pairs(0, t, b);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float2 v = *reinterpret_cast<const float2*>(&in.d[t][c ? at1 : at0]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    h[t + 1][c][i] = h[t][c][i];
-                    advance(h[t + 1][c][i], A2[c][i], both(v.x), both(v.y), b[i]);
+                    to[c][i] = from[c][i];
+                    advance(to[c][i], A2[c][i], both(v.x), both(v.y), b[i]);
                 }
             }
-        }
+        };
 #pragma unroll
-        for (int t = kTile - 1; t >= 0; --t) {
-            float2 b[2], kc[2], sB[2], sC[2];
-            float us[2], vs[2], ys[2];
-            fence();
-            pairs(0, t, b);
-            pairs(1, t, kc);
+        for (int t = 0; t < kTile / 2; ++t) step(t, h, h);
+        // the second half of the tile, then, from its start again, the first
+#pragma unroll 1
+        for (int half = kTile / 2; half >= 0; half -= kTile / 2) {
+            float2 old[kTile / 2 + 1][2][2];  // the states before each token of the half, and behind the last
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) old[0][c][i] = h[c][i];
+#pragma unroll
+            for (int t = 0; t < kTile / 2; ++t) step(half + t, old[t], old[t + 1]);
+#pragma unroll
+            for (int t = kTile / 2 - 1; t >= 0; --t) {
+                float2 b[2], kc[2], sB[2], sC[2];
+                float us[2], vs[2], ys[2];
+                fence();
+                pairs(0, half + t, b);
+                pairs(1, half + t, kc);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float4 v = in.d[half + t][c ? at1 : at0];
+                    float2 u, x, y;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 a = ex2_2(__fmul2_rn(both(v.x), A2[c][i]));
+                        const float2 g = __ffma2_rn(both(v.z), kc[i], G[c][i]), ht = old[t + 1][c][i];
+                        y = i ? __ffma2_rn(ht, kc[i], y) : __fmul2_rn(ht, kc[i]);
+                        sC[i] = c ? __ffma2_rn(ht, both(v.z), sC[i]) : __fmul2_rn(ht, both(v.z));
+                        u = i ? __ffma2_rn(g, b[i], u) : __fmul2_rn(g, b[i]);
+                        sB[i] = c ? __ffma2_rn(g, both(v.y), sB[i]) : __fmul2_rn(g, both(v.y));
+                        G[c][i] = __fmul2_rn(a, g);
+                        const float2 wv = __fmul2_rn(G[c][i], old[t][c][i]);
+                        x = i ? __ffma2_rn(wv, A2[c][i], x) : __fmul2_rn(wv, A2[c][i]);
+                        dA[c][i] = __ffma2_rn(wv, both(v.x), dA[c][i]);
+                    }
+                    us[c] = __fadd_rn(u.x, u.y), vs[c] = __fadd_rn(x.x, x.y), ys[c] = __fadd_rn(y.x, y.y);
+                }
+                const float u = sum_states<L>(us), v = sum_states<L>(vs);
+                if (j < 2) sm.uvy[0][half + t][cl + jq] = u, sm.uvy[1][half + t][cl + jq] = v;
+                if (feed.gate()) {
+                    const float y = sum_states<L>(ys);
+                    if (j < 2) sm.uvy[2][half + t][cl + jq] = y;
+                }
+                const float2 db = sum_channels<L>(sB), dc = sum_channels<L>(sC);
+                if constexpr (32 / L >= 4) {
+                    if (lane / L < 4) {
+                        float* to = &sm.bc[warp][half + t][4 * j + 2 * pm + (lane / L >> 1)];
+                        to[0] = db.x, to[S] = dc.x;
+                    }
+                } else {
+                    float2* to = reinterpret_cast<float2*>(&sm.bc[warp][half + t][4 * j + 2 * pm]);
+                    to[0] = db, to[S / 2] = dc;
+                }
+            }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float4 v = in.d[t][c ? at1 : at0];
-                float2 u, x, y;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 a = ex2_2(__fmul2_rn(both(v.x), A2[c][i]));
-                    const float2 g = __ffma2_rn(both(v.z), kc[i], G[c][i]), ht = h[t + 1][c][i];
-                    y = i ? __ffma2_rn(ht, kc[i], y) : __fmul2_rn(ht, kc[i]);
-                    sC[i] = c ? __ffma2_rn(ht, both(v.z), sC[i]) : __fmul2_rn(ht, both(v.z));
-                    u = i ? __ffma2_rn(g, b[i], u) : __fmul2_rn(g, b[i]);
-                    sB[i] = c ? __ffma2_rn(g, both(v.y), sB[i]) : __fmul2_rn(g, both(v.y));
-                    G[c][i] = __fmul2_rn(a, g);
-                    const float2 wv = __fmul2_rn(G[c][i], h[t][c][i]);
-                    x = i ? __ffma2_rn(wv, A2[c][i], x) : __fmul2_rn(wv, A2[c][i]);
-                    dA[c][i] = __ffma2_rn(wv, both(v.x), dA[c][i]);
-                }
-                us[c] = __fadd_rn(u.x, u.y), vs[c] = __fadd_rn(x.x, x.y), ys[c] = __fadd_rn(y.x, y.y);
-            }
-            const float u = sum_states<L>(us), v = sum_states<L>(vs);
-            if (j < 2) sm.uvy[0][t][cl + jq] = u, sm.uvy[1][t][cl + jq] = v;
-            if (feed.gate()) {
-                const float y = sum_states<L>(ys);
-                if (j < 2) sm.uvy[2][t][cl + jq] = y;
-            }
-            const float2 db = sum_channels<L>(sB), dc = sum_channels<L>(sC);
-            if constexpr (32 / L >= 4) {
-                if (lane / L < 4) {
-                    float* to = &sm.bc[warp][t][4 * j + 2 * pm + (lane / L >> 1)];
-                    to[0] = db.x, to[S] = dc.x;
-                }
-            } else {
-                float2* to = reinterpret_cast<float2*>(&sm.bc[warp][t][4 * j + 2 * pm]);
-                to[0] = db, to[S / 2] = dc;
+                const float4 u = sm.h[c][tid];
+                h[c][0] = make_float2(u.x, u.y), h[c][1] = make_float2(u.z, u.w);
             }
         }
         __syncthreads();
@@ -499,7 +549,7 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, 512 / Geo<T, S, 2>::NT) scan
                 const float2 d = make_float2(v0.x, v1.x), g = make_float2(v0.z, v1.z), sig = make_float2(v0.w, v1.w);
                 const float2 u = *reinterpret_cast<const float2*>(&sm.uvy[0][tt][col + 2 * e]);
                 const float2 v = __fmul2_rn(*reinterpret_cast<const float2*>(&sm.uvy[1][tt][col + 2 * e]), both(kLn2));
-                const float2 D = p.D ? make_float2(__ldg(p.D + w.c0 + col + 2 * e), __ldg(p.D + w.c0 + col + 2 * e + 1)) : both(0.f);
+                const float2 D = *reinterpret_cast<const float2*>(&in.D[col + 2 * e]);
                 const float2 dx = __ffma2_rn(d, u, __fmul2_rn(D, g));
                 const float2 dt = __fmul2_rn(__ffma2_rn(xv[e], u, v), sig);
                 odx[2 * e] = dx.x, odx[2 * e + 1] = dx.y, odt[2 * e] = dt.x, odt[2 * e + 1] = dt.y;
@@ -550,42 +600,50 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, 512 / Geo<T, S, 2>::NT) scan
 }
 
 // ---------------------------------------------------------------- 4. sums
-// The first `nbc` CTAs: dB and dC of every covered token, the channel blocks' parts of its group
-// in order.  The others: dA_log [C, S], dD, ddt_bias [C], the segments' parts in order.
+// Sums of rows: dB and dC of every covered token over the channel blocks of its group (the first
+// `nbc` CTAs), dA_log [C, S], dD and ddt_bias [C] over the segments.  A CTA takes 16 neighbouring
+// float4 columns; thread (slice, column) adds rows slice, slice + 16, .., then a thread per column
+// adds the slices in order: 16 times the loads in flight of one thread a column.
 template <typename T, int S>
-__global__ void __launch_bounds__(256) scan_sums_kernel(const BwdParams q, unsigned nbc) {
+__global__ void __launch_bounds__(256) scan_sums_kernel(const __grid_constant__ BwdParams q, unsigned nbc, int segs) {
+    __shared__ float4 part[16][16];
     const Params& p = q.f;
-    if (blockIdx.x < nbc) {
-        const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, per = (int64_t)p.G * 2 * S;
-        const int end = max(0, min(__ldg(p.cu + p.N), p.T));
-        const int64_t t = i / per;
-        if (t >= end) return;
-        const int g = (int)(i % per) / (2 * S), s = (int)(i % (2 * S));
-        float sum = 0.f;
-#pragma unroll 8
-        for (int b = 0; b < p.bpg; ++b) sum = __fadd_rn(sum, q.bc[(((int64_t)g * p.bpg + b) * p.T + t) * 2 * S + s]);
-        T* out = static_cast<T*>(s < S ? q.dB : q.dC);
-        store1(out + (t * p.G + g) * S + (s < S ? s : s - S), sum);
-        return;
+    const int x = threadIdx.x & 15, slice = threadIdx.x >> 4;
+    const bool isbc = blockIdx.x < nbc;
+    const int64_t col = (isbc ? blockIdx.x : blockIdx.x - nbc) * (int64_t)16 + x;
+    const int64_t per = (int64_t)p.T * 2 * S / 4, nA = (int64_t)p.C * S / 4;  // float4 columns of a group, of dA
+    const float4* src = nullptr;
+    int64_t step = 0, t = 0;
+    int rows = 0, g = 0;
+    if (isbc) {
+        g = (int)(col / per), t = col % per * 4 / (2 * S);
+        if (g < p.G && t < max(0, min(__ldg(p.cu + p.N), p.T)))
+            src = reinterpret_cast<const float4*>(q.bc) + (int64_t)g * p.bpg * per + col % per, step = per, rows = p.bpg;
+    } else if (col < nA) {
+        src = reinterpret_cast<const float4*>(q.seg_g) + col, step = nA, rows = segs;
+    } else if (col < nA + p.C / 2) {
+        const int64_t c = col - nA, half = p.C / 4;
+        if (c < half ? q.dD != nullptr : q.dbias != nullptr)
+            src = reinterpret_cast<const float4*>(c < half ? q.pD : q.pb) + c % half, step = half, rows = segs;
     }
-    const int64_t nA = (int64_t)p.C * S, i = (int64_t)(blockIdx.x - nbc) * blockDim.x + threadIdx.x;
-    if (i >= nA + 2 * p.C) return;
-    const bool isA = i < nA, isD = i < nA + p.C;
-    const float* src = isA ? q.seg_g + i : isD ? q.pD + (i - nA) : q.pb + (i - nA - p.C);
-    float* dst = isA ? q.dA + i : isD ? (q.dD ? q.dD + (i - nA) : nullptr) : (q.dbias ? q.dbias + (i - nA - p.C) : nullptr);
-    if (!dst) return;
-    const int64_t step = isA ? nA : p.C;
-    const int len = q.m * kTile;
-    float sum = 0.f;
-    for (int n = 0; n < p.N; ++n) {
-        int bos, eos;
-        bounds(p.cu, n, p.T, bos, eos);
-        const int segs = (eos - bos + len - 1) / len;
-        const float* at = src + (int64_t)(bos / len + n) * step;
-#pragma unroll 8
-        for (int k = 0; k < segs; ++k) sum = __fadd_rn(sum, at[k * step]);
+    const bool any = src != nullptr;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& v) { s.x = __fadd_rn(s.x, v.x), s.y = __fadd_rn(s.y, v.y), s.z = __fadd_rn(s.z, v.z), s.w = __fadd_rn(s.w, v.w); };
+#pragma unroll 4
+    for (int r = slice; r < rows; r += 16) add(src[r * step]);
+    part[slice][x] = s;
+    __syncthreads();
+    if (slice || !any) return;
+#pragma unroll
+    for (int i = 1; i < 16; ++i) add(part[i][x]);
+    if (isbc) {
+        const int e = (int)(col % per * 4 % (2 * S));
+        T* out = static_cast<T*>(e < S ? q.dB : q.dC) + (t * p.G + g) * S + (e < S ? e : e - S);
+        store1(out, s.x), store1(out + 1, s.y), store1(out + 2, s.z), store1(out + 3, s.w);
+    } else {
+        float* out = col < nA ? q.dA + col * 4 : col - nA < p.C / 4 ? q.dD + (col - nA) * 4 : q.dbias + (col - nA - p.C / 4) * 4;
+        out[0] = s.x, out[1] = s.y, out[2] = s.z, out[3] = s.w;
     }
-    *dst = sum;
 }
 
 struct Layout {
@@ -616,8 +674,8 @@ Layout layout(const gdn_scan_shape* s) {
 template <typename T, int S>
 gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     const Params& p = q.f;
-    const long long ctas = segs * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S + 255) / 256;
-    const long long par = ((long long)p.C * (S + 2) + 255) / 256;
+    const long long ctas = segs * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S / 4 + 15) / 16;
+    const long long par = ((long long)p.C * (S + 2) / 4 + 15) / 16;
     if (ctas >= (1LL << 31) || bc + par >= (1LL << 31) || p.N > 65535) return GDN_ERR_UNSUPPORTED;
     constexpr size_t smem = sizeof(GradMem<T, S>);
     if constexpr (smem > 48 * 1024) {
@@ -629,7 +687,7 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
         scan_join_kernel<<<dim3((unsigned)(((int64_t)p.C * S / 4 + 127) / 128), (unsigned)p.N, 2), 128, 0, s>>>(q, S);
         if (p.T > 0) scan_grad_kernel<T, S><<<(unsigned)ctas, Geo<T, S, 2>::NT, smem, s>>>(q);
     }
-    scan_sums_kernel<T, S><<<(unsigned)(bc + par), 256, 0, s>>>(q, (unsigned)bc);
+    scan_sums_kernel<T, S><<<(unsigned)(bc + par), 256, 0, s>>>(q, (unsigned)bc, p.T > 0 ? (int)segs : 0);
     return launch_status();
 }
 template <typename T>
