@@ -59,7 +59,7 @@ struct FwdTile {
 };
 
 template <typename T, int S>
-__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const Params p) {
+__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
     using F = FwdTile<T, S>;
     constexpr int L = F::L, Q = F::Q, NT = F::NT, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB;
     __shared__ F sm;
@@ -250,36 +250,83 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
     }
 }
 
+// Single tokens: HBM bound by the states, read and written once.  A lane holds 4 states (16 bytes)
+// of a channel, L = S / 4 lanes a channel, a CTA 128 / L channels of `rows` batch rows, whose A and
+// D it reads once and whose B and C it keeps in shared memory in fp32.  RW rows go together: lane
+// j does the work per (row, channel) of row j, softplus before and skip, gate and store after, so
+// that no lane repeats it, and the rows' states are in flight at once.
+constexpr int kUpdRows = 16;
+
 template <typename T, int S>
-__global__ void __launch_bounds__(128) scan_update_kernel(const Params p) {
-    constexpr int L = S / 4, CB = 128 / L;
-    const int nb = p.bpg * p.G;
-    const int n = blockIdx.x / nb, blk = blockIdx.x % nb;
-    const int g = blk / p.bpg, j = threadIdx.x % L;
+__global__ void __launch_bounds__(128) scan_update_kernel(const __grid_constant__ Params p, int rows) {
+    constexpr int L = S / 4, CB = 128 / L, RW = L < 4 ? L : 4;
+    constexpr uint32_t all = 0xffffffffu;
+    __shared__ float4 bc[kUpdRows][2][S / 4];
+    __shared__ int slots[kUpdRows];
+    const int nb = p.bpg * p.G, blk = blockIdx.x % nb, b0 = blockIdx.x / nb * rows, nr = min(rows, p.N - b0);
+    const int g = blk / p.bpg, j = threadIdx.x % L, jr = j % RW;
     const int cg = (blk % p.bpg) * CB + threadIdx.x / L;
     const bool ok = cg < p.CG;
     const int c = g * p.CG + (ok ? cg : 0);
-    const int slot = p.idx ? __ldg(p.idx + n) : n;
-    if (slot < 0 || slot >= p.num_slots) return;
-    float2 A2[2], h[2], b[2], cc[2];
+    for (int i = threadIdx.x; i < nr * (S / 2); i += 128) {
+        const int r = i / (S / 2), which = i % (S / 2) / (S / 4), q = i % (S / 4);
+        const int64_t row = b0 + r;
+        float2 v[2];
+        load4((which ? static_cast<const T*>(p.Cm) + row * p.ldC : static_cast<const T*>(p.B) + row * p.ldB) + (int64_t)g * S + 4 * q, v);
+        bc[r][which][q] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+    for (int i = threadIdx.x; i < nr; i += 128) {
+        const int slot = p.idx ? __ldg(p.idx + b0 + i) : b0 + i;
+        slots[i] = slot < p.num_slots ? slot : -1;
+    }
+    float2 A2[2];
     load4(p.A_log + (int64_t)c * S + 4 * j, A2);
-    float* st = p.state + ((int64_t)slot * p.C + c) * S + 4 * j;
-    const float4 u = *reinterpret_cast<const float4*>(st);
-    h[0] = make_float2(u.x, u.y), h[1] = make_float2(u.z, u.w);
-    const float xv = load1(static_cast<const T*>(p.x) + n * p.ldx + c);
-    const float d = step_of(both(load1(static_cast<const T*>(p.dt) + n * p.lddt + c)), both(p.bias ? __ldg(p.bias + c) : 0.f), p.softplus).x;
-    const float dx = __fmul_rn(d, xv);
-    load4(static_cast<const T*>(p.B) + n * p.ldB + (int64_t)g * S + 4 * j, b);
-    load4(static_cast<const T*>(p.Cm) + n * p.ldC + (int64_t)g * S + 4 * j, cc);
+    A2[0] = make_float2(a_log2(A2[0].x), a_log2(A2[0].y)), A2[1] = make_float2(a_log2(A2[1].x), a_log2(A2[1].y));
+    const float bias = p.bias ? __ldg(p.bias + c) : 0.f, D = p.D ? __ldg(p.D + c) : 0.f;
+    float* st = p.state + (int64_t)c * S + 4 * j;
+    const int64_t CS = (int64_t)p.C * S;
+    __syncthreads();
+
+    float4 s[RW];
+    float x, dt, z;
+    auto load = [&](int r0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        advance(h[i], make_float2(a_log2(A2[i].x), a_log2(A2[i].y)), make_float2(d, d), make_float2(dx, dx), b[i]);
-    float s = __fmaf_rn(p.D ? __ldg(p.D + c) : 0.f, xv, sum_states4<L>(h, cc, j));
-    float2 sig;
-    if (p.z) s = __fmul_rn(s, silu2(both(load1(static_cast<const T*>(p.z) + n * p.ldz + c)), sig).x);
-    if (!ok) return;
-    if (j == 1) store1(static_cast<T*>(p.y) + (int64_t)n * p.C + c, s);
-    *reinterpret_cast<float4*>(st) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+        for (int r = 0; r < RW; ++r) {
+            const int slot = r0 + r < nr ? slots[r0 + r] : -1;
+            s[r] = slot >= 0 ? *reinterpret_cast<const float4*>(st + slot * CS) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const int64_t row = b0 + min(r0 + jr, nr - 1);
+        x = load1(static_cast<const T*>(p.x) + row * p.ldx + c);
+        dt = load1(static_cast<const T*>(p.dt) + row * p.lddt + c);
+        z = p.z ? load1(static_cast<const T*>(p.z) + row * p.ldz + c) : 0.f;
+    };
+    load(0);
+    for (int r0 = 0; r0 < nr; r0 += RW) {
+        float2 h[RW][2];
+#pragma unroll
+        for (int r = 0; r < RW; ++r) h[r][0] = make_float2(s[r].x, s[r].y), h[r][1] = make_float2(s[r].z, s[r].w);
+        const float xv = x, zv = z;
+        const float d = step_of(both(dt), both(bias), p.softplus).x, dx = __fmul_rn(d, xv);
+        if (r0 + RW < nr) load(r0 + RW);
+        float mine = 0.f;
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const int at = min(r0 + r, nr - 1), from = (threadIdx.x & 31 & ~(L - 1)) + r;
+            const float dr = __shfl_sync(all, d, from), dxr = __shfl_sync(all, dx, from);
+            const float4 b = bc[at][0][j], k = bc[at][1][j];
+            const float2 cc[2] = {make_float2(k.x, k.y), make_float2(k.z, k.w)};
+            advance(h[r][0], A2[0], both(dr), both(dxr), make_float2(b.x, b.y));
+            advance(h[r][1], A2[1], both(dr), both(dxr), make_float2(b.z, b.w));
+            const float t = __shfl_sync(all, sum_states4<L>(h[r], cc, j), (threadIdx.x & 31 & ~(L - 1)) + 1);
+            if (jr == r) mine = t;
+            if (ok && r0 + r < nr && slots[at] >= 0)
+                *reinterpret_cast<float4*>(st + slots[at] * CS) = make_float4(h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y);
+        }
+        float y = __fmaf_rn(D, xv, mine);
+        float2 sig;
+        if (p.z) y = __fmul_rn(y, silu2(both(zv), sig).x);
+        if (ok && j < RW && r0 + j < nr && slots[r0 + j] >= 0) store1(static_cast<T*>(p.y) + (int64_t)(b0 + r0 + j) * p.C + c, y);
+    }
 }
 
 // Validation common to the two entry points; fills the parameters.
@@ -305,14 +352,13 @@ gdn_status prepare(const gdn_scan_shape* s, const void* x, const void* dt, const
     return GDN_OK;
 }
 
-// K<T, S>::go launches; K<T, S>::cb: channels of a CTA.
+// K<T, S>::go launches over p.N sequences (rows) and the channel blocks; K<T, S>::cb: channels of a CTA.
 template <template <typename, int> class K, typename T, int S>
 gdn_status launch(cudaStream_t s, Params& p) {
     constexpr int cb = K<T, S>::cb;
     p.bpg = (p.CG + cb - 1) / cb;
-    const long long ctas = (long long)p.N * p.G * p.bpg;
-    if (ctas >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
-    K<T, S>::go((unsigned)ctas, s, p);
+    if ((long long)p.N * p.G * p.bpg >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
+    K<T, S>::go((unsigned)(p.G * p.bpg), s, p);
     return launch_status();
 }
 template <template <typename, int> class K, typename T>
@@ -328,12 +374,17 @@ gdn_status by_states(int S, cudaStream_t s, Params& p) {
 template <typename T, int S>
 struct FwdK {
     static constexpr int cb = FwdTile<T, S>::CB;
-    static void go(unsigned grid, cudaStream_t s, const Params& p) { scan_fwd_kernel<T, S><<<grid, FwdTile<T, S>::NT, 0, s>>>(p); }
+    static void go(unsigned blocks, cudaStream_t s, const Params& p) { scan_fwd_kernel<T, S><<<blocks * p.N, FwdTile<T, S>::NT, 0, s>>>(p); }
 };
 template <typename T, int S>
 struct UpdK {
     static constexpr int cb = 128 / (S / 4);
-    static void go(unsigned grid, cudaStream_t s, const Params& p) { scan_update_kernel<T, S><<<grid, 128, 0, s>>>(p); }
+    // Many rows a CTA where that leaves every SM several CTAs; else as few as go together.
+    static void go(unsigned blocks, cudaStream_t s, const Params& p) {
+        const int most = (int)((long long)blocks * p.N / (kSMs * 16));
+        const int rows = most >= kUpdRows ? kUpdRows : most >= 8 ? 8 : 4;
+        scan_update_kernel<T, S><<<blocks * ((p.N + rows - 1) / rows), 128, 0, s>>>(p, rows);
+    }
 };
 
 }  // namespace
