@@ -10,11 +10,14 @@
 // A thread owns 4 channels (two packed pairs) and walks a range of tokens forwards with the last
 // W-1 rows of x and of p in registers: row t - (W-1) of dx is complete when p_t is known.  A
 // range is T / K tokens whatever sequences it crosses, so ragged batches balance; it re-reads
-// W-1 rows on either side.  Its dw and dbias sums stay in registers until the end: one row of
-// partials per range, which the second kernel adds up in order.
+// W-1 rows on either side.  x and d_y pass through a ring of asynchronous copies in shared memory,
+// thread-private (no barriers), two blocks of 8 (fp32: 4) tokens: taps, window and sums leave no registers
+// to hold loads in flight.  The dw and dbias sums stay in registers until the end: one row of partials
+// per range, which the second kernel adds up in order.
 #include <limits.h>
 
 #include "../../include/gdn_layer.h"
+#include "gdn_async.cuh"
 #include "gdn_host.h"
 #include "gdn_vec.cuh"
 
@@ -57,6 +60,8 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const Quad& q) {
 __device__ __forceinline__ void store(float* p, const Quad& q) {
     __stcs(reinterpret_cast<float4*>(p), make_float4(q.a.x, q.a.y, q.b.x, q.b.y));
 }
+__device__ __forceinline__ void copy_async(uint2* to, const void* from) { copy8_async(to, from); }
+__device__ __forceinline__ void copy_async(uint4* to, const void* from) { copy16_async(to, from); }
 __device__ __forceinline__ Quad zero() { return {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}; }
 __device__ __forceinline__ Quad fma(const Quad& u, const Quad& v, const Quad& w) {
     return {__ffma2_rn(u.a, v.a, w.a), __ffma2_rn(u.b, v.b, w.b)};
@@ -65,15 +70,18 @@ __device__ __forceinline__ Quad mul(const Quad& u, const Quad& v) { return {__fm
 __device__ __forceinline__ Quad add(const Quad& u, const Quad& v) { return {__fadd2_rn(u.a, v.a), __fadd2_rn(u.b, v.b)}; }
 
 // silu'(x) = s (1 + x (1 - s)), s = sigmoid(x)
-__device__ __forceinline__ float dsilu(float x) {
-    const float s = rcp_approx(__fadd_rn(1.f, __expf(-x)));
-    return __fmul_rn(s, __fmaf_rn(x, __fsub_rn(1.f, s), 1.f));
+__device__ __forceinline__ float2 dsilu(const float2& x) {
+    const float2 one = make_float2(1.f, 1.f), e = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), one);
+    const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    return __fmul2_rn(s, __ffma2_rn(x, __ffma2_rn(s, make_float2(-1.f, -1.f), one), one));
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvBwdParams p) {
+__global__ void __launch_bounds__(128, W <= 4 ? 4 : 2) conv_bwd_kernel(const __grid_constant__ ConvBwdParams p) {
     using R = typename Raw<T>::type;
-    constexpr int WM = W - 1, U = 4;
+    constexpr int WM = W - 1, U = sizeof(R) == 8 ? 8 : 4, NS = 2;  // ring: NS blocks of U tokens, 32 KB
+    __shared__ R ring[NS][U][2][128];
     const int c0 = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
     if (c0 >= p.C) return;
     const int k = blockIdx.y;
@@ -135,8 +143,7 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvBwdParams p) {
 #pragma unroll
                 for (int i = 0; i < WM; ++i) pre = fma(w[i], win[i], pre);
                 pre = fma(w[WM], xc, pre);
-                const Quad g = {make_float2(dsilu(pre.a.x), dsilu(pre.a.y)), make_float2(dsilu(pre.b.x), dsilu(pre.b.y))};
-                pt = mul(dyc, g);
+                pt = mul(dyc, {dsilu(pre.a), dsilu(pre.b)});
             }
             if (own) {
 #pragma unroll
@@ -160,11 +167,33 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvBwdParams p) {
             for (int i = WM - 1; i > 0; --i) pw[i] = pw[i - 1];
             pw[0] = pt;
         };
-        auto any = [&](int t) {  // a token near the segment's ends
+        // the ring's tokens: the segment's own and, for the last rows of dx, the W - 1 behind it
+        const int loaded = min(e + WM, eos) - s, steps = e + WM - s;
+        auto copy = [&](int i) {
+            const T* xs = x + (int64_t)(s + i * U) * p.C;
+            const T* ys = dy + (int64_t)(s + i * U) * p.C;
+            const int64_t C = p.C;
+            if ((i + 1) * U <= loaded) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    copy_async(&ring[i % NS][u][0][threadIdx.x], xs + u * C);
+                    copy_async(&ring[i % NS][u][1][threadIdx.x], ys + u * C);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i * U + u < loaded) {
+                        copy_async(&ring[i % NS][u][0][threadIdx.x], xs + u * C);
+                        copy_async(&ring[i % NS][u][1][threadIdx.x], ys + u * C);
+                    }
+            }
+            copy_commit();
+        };
+        auto any = [&](int t, const R& xr, const R& yr) {  // a token near the segment's ends
             Quad xc = zero(), pt = zero();
             if (t < eos) {
-                xc = quad(rd(x, t));
-                pt = point(xc, quad(rd(dy, t)), t < e);
+                xc = quad(xr);
+                pt = point(xc, quad(yr), t < e);
             }
             const int r = t - WM;
             if (r >= s || s == bos) {
@@ -176,32 +205,26 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvBwdParams p) {
             }
             slide(xc, pt);
         };
-        int t = s;
-        for (; t < min(s + WM, e + WM); ++t) any(t);
-        // whole blocks of the segment's own tokens (d_final_state only meets rows that are
-        // complete at t >= eos)
-        R xa[U], ya[U], xb[U], yb[U];
-        auto load = [&](R(&xr)[U], R(&yr)[U], int b) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (b + u < e) xr[u] = rd(x, b + u), yr[u] = rd(dy, b + u);
-        };
-        auto block = [&](const R(&xr)[U], const R(&yr)[U], int b) {
+        for (int i = 0; i < NS - 1; ++i) copy(i);
+        for (int i = 0; i * U < steps; ++i) {
+            copy(i + NS - 1);
+            copy_wait<NS - 1>();
+            const int t = s + i * U;
+            if (t >= s + WM && t + U <= e) {  // all the segment's own, all with a row of dx (d_final_state meets rows complete at t >= eos)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const Quad xc = quad(xr[u]), pt = point(xc, quad(yr[u]), true);
-                store(dx + (int64_t)(b + u - WM) * p.C, row(pt));
-                slide(xc, pt);
+                for (int u = 0; u < U; ++u) {
+                    const Quad xc = quad(ring[i % NS][u][0][threadIdx.x]), pt = point(xc, quad(ring[i % NS][u][1][threadIdx.x]), true);
+                    store(dx + (int64_t)(t + u - WM) * p.C, row(pt));
+                    slide(xc, pt);
+                }
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < U; ++u)
+                    if (t + u < e + WM) any(t + u, ring[i % NS][u][0][threadIdx.x], ring[i % NS][u][1][threadIdx.x]);
             }
-        };
-        load(xa, ya, t);
-        for (; t + 2 * U <= e; t += 2 * U) {
-            load(xb, yb, t + U);
-            block(xa, ya, t);
-            load(xa, ya, t + 2 * U);
-            block(xb, yb, t + U);
         }
-        for (; t < e + WM; ++t) any(t);
+        copy_wait<0>();
     }
     float* out = p.part + (int64_t)k * (W + 1) * p.C + c0;
 #pragma unroll
@@ -209,23 +232,37 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvBwdParams p) {
     store(out + (int64_t)W * p.C, db);
 }
 
-// dweight [C, W] and dbias [C]: the ranges' partials in ascending order.
+// dweight [C, W] and dbias [C]: the ranges' partials.  A CTA takes 16 float4 columns of one tap;
+// thread (slice, column) adds ranges slice, slice + 16, .., then a thread per column the slices in order.
 __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(int W, int C, int K, const float* __restrict__ part,
                                                            float* __restrict__ dw, float* __restrict__ db) {
-    const int c = blockIdx.x * blockDim.x + threadIdx.x, i = blockIdx.y;
-    if (c >= C) return;
-    float s = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < K; ++k) s = __fadd_rn(s, part[((int64_t)k * (W + 1) + i) * C + c]);
-    if (i < W) dw[(int64_t)c * W + i] = s;
-    else if (db) db[c] = s;
+    __shared__ float4 sums[16][16];
+    const int x = threadIdx.x & 15, slice = threadIdx.x >> 4, i = blockIdx.y;
+    const int c = (blockIdx.x * 16 + x) * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& v) { s.x = __fadd_rn(s.x, v.x), s.y = __fadd_rn(s.y, v.y), s.z = __fadd_rn(s.z, v.z), s.w = __fadd_rn(s.w, v.w); };
+    if (c < C) {
+#pragma unroll 4
+        for (int k = slice; k < K; k += 16) add(*reinterpret_cast<const float4*>(part + ((int64_t)k * (W + 1) + i) * C + c));
+    }
+    sums[slice][x] = s;
+    __syncthreads();
+    if (slice || c >= C) return;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) add(sums[k][x]);
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (i < W) dw[(int64_t)(c + e) * W + i] = v[e];
+        else if (db) db[c + e] = v[e];
+    }
 }
 
-// Token ranges: enough CTAs of 128 x 4 channels for every SM to hold several, none under 16 tokens.
+// Token ranges: one wave of CTAs of 128 x 4 channels, four an SM, but no range under 16 tokens.
 int conv_ranges(int T, int C) {
     const int cols = (C + 511) / 512;
     const int most = (T + 15) / 16;
-    const int want = (kSMs * 4 + cols - 1) / cols;
+    const int want = kSMs * 4 / cols > 1 ? kSMs * 4 / cols : 1;
     return want < most ? want : (most > 1 ? most : 1);
 }
 
@@ -290,6 +327,6 @@ extern "C" gdn_status gdn_causal_conv1d_bwd(const gdn_conv_shape* shape, const v
     const dim3 grid((unsigned)((C + 511) / 512), (unsigned)p.K);
     st = shape->dtype == GDN_BF16 ? conv_bwd_launch<__nv_bfloat16>(W, grid, s, p) : conv_bwd_launch<float>(W, grid, s, p);
     if (st != GDN_OK) return st;
-    conv_bwd_sum_kernel<<<dim3((unsigned)((C + 255) / 256), (unsigned)(W + 1)), 256, 0, s>>>(W, C, p.K, p.part, dweight, dbias);
+    conv_bwd_sum_kernel<<<dim3((unsigned)((C + 63) / 64), (unsigned)(W + 1)), 256, 0, s>>>(W, C, p.K, p.part, dweight, dbias);
     return launch_status();
 }

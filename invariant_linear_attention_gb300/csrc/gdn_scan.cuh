@@ -20,14 +20,6 @@
 namespace gdn {
 namespace scan {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // A log2(e) of one state from its A_log.
 __device__ __forceinline__ float a_log2(float A_log) { return __fmul_rn(-expf(A_log), kLog2e); }
 

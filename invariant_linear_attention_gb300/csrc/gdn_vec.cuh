@@ -67,4 +67,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 __device__ __forceinline__ float silu_fast(float x) { return __fmul_rn(x, rcp_approx(__fadd_rn(1.f, __expf(-x)))); }
 
+// 2^x by the bare hardware exponential: __expf also rescales around subnormal results, four more
+// instructions that 1 + e^x does not need.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 }  // namespace gdn
