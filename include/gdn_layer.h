@@ -163,8 +163,8 @@ typedef struct {
  * is skipped).  Outputs q_out [T, HQ, d], k_out [T, HK, d] dense in dtype; they
  * may alias q and k where those are dense.  Each row is computed by one lane
  * group in one fixed order: results do not depend on T or the other rows.
- * Strides are multiples of 8 (bf16) or 4 (fp32) elements.  q, k, the outputs
- * and the weights are 16-byte aligned, cos, sin and positions 4-byte aligned.
+ * Strides are multiples of 8 (bf16) or 4 (fp32) elements.  q, k, the outputs, the
+ * weights, cos and sin are 16-byte aligned, positions 4-byte aligned.
  */
 gdn_status gdn_qk_norm_rope(const gdn_qk_shape* shape, const void* q, const void* k,
                             const float* q_weight, const float* k_weight, const float* cos,

@@ -9,7 +9,8 @@
 // chunks (u, u + rotary_dim/2) of the halves form, two neighbouring chunks otherwise.  A lane
 // takes one unit, a power-of-two group of lanes one row, so a rotation needs no other lane and
 // the sum of squares a fixed butterfly.  A warp takes as many heads of one token as it has
-// groups and goes on to the token's other heads with the same cos and sin in registers.
+// groups per pass, several passes' loads at once, and goes on to the token's other heads with the same
+// angles in registers.  Packed pairs of values: issue slots bound the first version (17 a value).
 #include "../../include/gdn_layer.h"
 #include "gdn_host.h"
 #include "gdn_vec.cuh"
@@ -50,46 +51,76 @@ __device__ __forceinline__ Unit unit_of(int u, int d, int rd, int inter) {
     return r;
 }
 
-// The pairs of a unit by its angles (back: by their negatives).  Halves: (a[e], b[e]); neighbours: (a[2e], a[2e+1]), then b's.
+// A unit's values as packed pairs: its first chunk in [0, VN / 2), its second behind it.
 template <int VN>
-__device__ __forceinline__ void rotate(float (&a)[VN], float (&b)[VN], const float (&cs)[VN], const float (&sn)[VN],
-                                       bool inter, bool back) {
+__device__ __forceinline__ void unpack_unit(const uint4& a, const uint4& b, float2 (&v)[VN]) {
+    float f[VN], g[VN];
+    unpack(a, f);
+    unpack(b, g);
 #pragma unroll
-    for (int e = 0; e < VN; ++e) {
-        const float s = back ? -sn[e] : sn[e];
-        if (!inter) {
-            const float u = a[e], v = b[e];
-            a[e] = __fmaf_rn(u, cs[e], -__fmul_rn(v, s));
-            b[e] = __fmaf_rn(v, cs[e], __fmul_rn(u, s));
-        }
-    }
-    if (inter) {
-#pragma unroll
-        for (int e = 0; e < VN; ++e) {
-            const float s = back ? -sn[e] : sn[e];
-            float& u0 = e < VN / 2 ? a[(2 * e) % VN] : b[(2 * e) % VN];
-            float& v0 = e < VN / 2 ? a[(2 * e + 1) % VN] : b[(2 * e + 1) % VN];
-            const float u = u0, v = v0;
-            u0 = __fmaf_rn(u, cs[e], -__fmul_rn(v, s));
-            v0 = __fmaf_rn(v, cs[e], __fmul_rn(u, s));
-        }
-    }
+    for (int e = 0; e < VN / 2; ++e) v[e] = make_float2(f[2 * e], f[2 * e + 1]), v[VN / 2 + e] = make_float2(g[2 * e], g[2 * e + 1]);
 }
+template <int VN>
+__device__ __forceinline__ uint4 pack_half(const float2* v) {
+    float f[VN];
+#pragma unroll
+    for (int e = 0; e < VN / 2; ++e) f[2 * e] = v[e].x, f[2 * e + 1] = v[e].y;
+    return pack(f);
+}
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
+// The angles of a unit's VN pairs (1 and 0 where it is not rotated); back: the negative ones.
 template <int VN>
-__device__ __forceinline__ void load_f(const float* p, bool ok, float other, float (&v)[VN]) {
+struct Angles {
+    float2 c[VN / 2], s[VN / 2], ns[VN / 2];
+    __device__ __forceinline__ void load(const QkParams& p, int64_t row, int u, bool rot, bool back) {
+        const float* pc = p.cos + row * (p.rd / 2) + u * VN;
+        const float* ps = p.sin + row * (p.rd / 2) + u * VN;
 #pragma unroll
-    for (int e = 0; e < VN; e += 4) {
-        const float4 u = ok ? __ldg(reinterpret_cast<const float4*>(p + e)) : make_float4(other, other, other, other);
-        v[e] = u.x, v[e + 1] = u.y, v[e + 2] = u.z, v[e + 3] = u.w;
+        for (int e = 0; e < VN / 2; e += 2) {
+            const float4 c4 = rot ? __ldg(reinterpret_cast<const float4*>(pc + 2 * e)) : make_float4(1.f, 1.f, 1.f, 1.f);
+            const float4 s4 = rot ? __ldg(reinterpret_cast<const float4*>(ps + 2 * e)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            c[e] = make_float2(c4.x, c4.y), c[e + 1] = make_float2(c4.z, c4.w);
+            s[e] = make_float2(s4.x, s4.y), s[e + 1] = make_float2(s4.z, s4.w);
+        }
+#pragma unroll
+        for (int e = 0; e < VN / 2; ++e) {
+            ns[e] = make_float2(-s[e].x, -s[e].y);
+            if (back) {
+                const float2 t = s[e];
+                s[e] = ns[e], ns[e] = t;
+            }
+        }
     }
-}
-template <int VN>
-__device__ __forceinline__ void load_angles(const QkParams& p, int64_t pos, int u, bool rot, float (&cs)[VN], float (&sn)[VN]) {
+    // (u, v) -> (u c - v s, v c + u s).  Halves: u in the first chunk, v in the second; neighbours: a pair is (u, v).
+    template <bool INTER>
+    __device__ __forceinline__ void turn(float2 (&v)[VN]) const {
+        if constexpr (!INTER) {
 #pragma unroll
-    for (int e = 0; e < VN; ++e) {
-        cs[e] = rot ? __ldg(p.cos + pos * (p.rd / 2) + u * VN + e) : 1.f;
-        sn[e] = rot ? __ldg(p.sin + pos * (p.rd / 2) + u * VN + e) : 0.f;
+            for (int e = 0; e < VN / 2; ++e) {
+                const float2 a = v[e], b = v[VN / 2 + e];
+                v[e] = __ffma2_rn(b, ns[e], __fmul2_rn(a, c[e]));
+                v[VN / 2 + e] = __ffma2_rn(a, s[e], __fmul2_rn(b, c[e]));
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                const float2 a = v[e];
+                const float ce = e & 1 ? c[e / 2].y : c[e / 2].x, se = e & 1 ? s[e / 2].y : s[e / 2].x, me = e & 1 ? ns[e / 2].y : ns[e / 2].x;
+                v[e] = make_float2(__fmaf_rn(a.y, me, __fmul_rn(a.x, ce)), __fmaf_rn(a.x, se, __fmul_rn(a.y, ce)));
+            }
+        }
+    }
+};
+
+// A unit's weights (ones where there is no weight).
+template <int VN>
+__device__ __forceinline__ void load_weight(const float* w, const Unit& un, float2 (&v)[VN]) {
+#pragma unroll
+    for (int e = 0; e < VN; e += 2) {
+        const bool has = w && (e < VN / 2 ? un.has0 : un.has1);
+        const float4 t = has ? __ldg(reinterpret_cast<const float4*>(w + (e < VN / 2 ? un.e0 + 2 * e : un.e1 + 2 * e - VN))) : make_float4(1.f, 1.f, 1.f, 1.f);
+        v[e] = make_float2(t.x, t.y), v[e + 1] = make_float2(t.z, t.w);
     }
 }
 
@@ -97,15 +128,12 @@ __device__ __forceinline__ float group_sum(float s, int lpr) {
     for (int off = 1; off < lpr; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
     return s;
 }
-
 template <int VN>
-__device__ __forceinline__ float squares(const float (&a)[VN], const float (&b)[VN]) {
-    float s = 0.f;
+__device__ __forceinline__ float dot(const float2 (&a)[VN], const float2 (&b)[VN]) {
+    float2 s = __fmul2_rn(a[0], b[0]);
 #pragma unroll
-    for (int e = 0; e < VN; ++e) s = __fmaf_rn(a[e], a[e], s);
-#pragma unroll
-    for (int e = 0; e < VN; ++e) s = __fmaf_rn(b[e], b[e], s);
-    return s;
+    for (int e = 1; e < VN; ++e) s = __ffma2_rn(a[e], b[e], s);
+    return __fadd_rn(s.x, s.y);
 }
 
 // The token's angle row, or -1 where it is skipped.
@@ -115,8 +143,9 @@ __device__ __forceinline__ int64_t angle_row(const QkParams& p, int64_t t) {
     return pos >= 0 && pos < p.max_pos ? pos : -1;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) qk_kernel(const QkParams p) {
+// UR: passes whose loads are in flight together.
+template <typename T, bool INTER, bool HASW, int UR>
+__global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParams p) {
     constexpr int VN = V16<T>::n;
     const int lane = threadIdx.x & 31, u = lane & (p.lpr - 1), sub = lane / p.lpr, hpw = 32 / p.lpr;
     const Unit un = unit_of<VN>(u, p.d, p.rd, p.inter);
@@ -127,37 +156,50 @@ __global__ void __launch_bounds__(256) qk_kernel(const QkParams p) {
         const int64_t t = it / per;
         const int64_t row = angle_row(p, t);
         if (row < 0) continue;
-        float cs[VN], sn[VN];
-        load_angles<VN>(p, row, u, un.rot, cs, sn);
+        Angles<VN> an;
+        an.load(p, row, u, un.rot, false);
         const int first = (int)(it % per) * p.passes, last = min(first + p.passes, all);
-        for (int ps = first; ps < last; ++ps) {
-            const bool isq = ps < p.pq;
-            const int h = (isq ? ps : ps - p.pq) * hpw + sub;
-            const bool ok = h < (isq ? p.HQ : p.HK);
-            const T* src = (isq ? static_cast<const T*>(p.q) + t * p.ldq : static_cast<const T*>(p.k) + t * p.ldk) + (int64_t)h * p.d;
-            T* dst = (isq ? static_cast<T*>(p.qo) + t * p.HQ * p.d : static_cast<T*>(p.ko) + t * p.HK * p.d) + (int64_t)h * p.d;
-            const float* w = isq ? p.qw : p.kw;
-            float a[VN], b[VN], wa[VN], wb[VN];
-            unpack(ok && un.has0 ? ld16_stream(src + un.e0) : none, a);
-            unpack(ok && un.has1 ? ld16_stream(src + un.e1) : none, b);
-            load_f<VN>(w + un.e0, w && un.has0, 1.f, wa);
-            load_f<VN>(w + un.e1, w && un.has1, 1.f, wb);
-            const float r = __frsqrt_rn(__fmaf_rn(group_sum(squares<VN>(a, b), p.lpr), p.c, p.eps));
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {  // q, then k
+            const int H = side ? p.HK : p.HQ, lo = side ? max(first - p.pq, 0) : first, hi = side ? last - p.pq : min(last, p.pq);
+            if (lo >= hi) continue;
+            const T* src = (side ? static_cast<const T*>(p.k) + t * p.ldk : static_cast<const T*>(p.q) + t * p.ldq);
+            T* dst = (side ? static_cast<T*>(p.ko) : static_cast<T*>(p.qo)) + t * H * p.d;
+            float2 w[VN];
+            if constexpr (HASW) load_weight<VN>(side ? p.kw : p.qw, un, w);
+            for (int ps = lo; ps < hi; ps += UR) {
+                uint4 ra[UR], rb[UR];
 #pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                a[e] = __fmul_rn(__fmul_rn(a[e], r), wa[e]);
-                b[e] = __fmul_rn(__fmul_rn(b[e], r), wb[e]);
+                for (int i = 0; i < UR; ++i) {
+                    const int h = (ps + i) * hpw + sub;
+                    const bool ok = ps + i < hi && h < H;
+                    ra[i] = ok && un.has0 ? ld16_stream(src + h * p.d + un.e0) : none;
+                    rb[i] = ok && un.has1 ? ld16_stream(src + h * p.d + un.e1) : none;
+                }
+#pragma unroll
+                for (int i = 0; i < UR; ++i) {
+                    if (ps + i >= hi) break;
+                    const int h = (ps + i) * hpw + sub;
+                    float2 v[VN];
+                    unpack_unit<VN>(ra[i], rb[i], v);
+                    const float2 r = twice(rsqrtf(__fmaf_rn(group_sum(dot<VN>(v, v), p.lpr), p.c, p.eps)));
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) {
+                        v[e] = __fmul2_rn(v[e], r);
+                        if constexpr (HASW) v[e] = __fmul2_rn(v[e], w[e]);
+                    }
+                    an.template turn<INTER>(v);
+                    if (h < H && un.has0) st16_stream(dst + h * p.d + un.e0, pack_half<VN>(v));
+                    if (h < H && un.has1) st16_stream(dst + h * p.d + un.e1, pack_half<VN>(v + VN / 2));
+                }
             }
-            if (un.rot) rotate<VN>(a, b, cs, sn, p.inter, false);
-            if (ok && un.has0) st16_stream(dst + un.e0, pack(a));
-            if (ok && un.has1) st16_stream(dst + un.e1, pack(b));
         }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) qk_bwd_kernel(const QkParams p) {
-    constexpr int VN = V16<T>::n;
+template <typename T, bool INTER, bool HASW>
+__global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ QkParams p) {
+    constexpr int VN = V16<T>::n, UR = 2;
     extern __shared__ float acc[];  // [256 / lpr groups][d]
     const int lane = threadIdx.x & 31, u = lane & (p.lpr - 1), sub = lane / p.lpr, hpw = 32 / p.lpr;
     const Unit un = unit_of<VN>(u, p.d, p.rd, p.inter);
@@ -166,61 +208,69 @@ __global__ void __launch_bounds__(256) qk_bwd_kernel(const QkParams p) {
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {  // q, then k
         const int H = side ? p.HK : p.HQ, np = side ? p.pk : p.pq;
-        const float* w = side ? p.kw : p.qw;
         const int64_t ld = side ? p.ldk : p.ldq, ldd = side ? p.lddk : p.lddq;
         const T* x = static_cast<const T*>(side ? p.k : p.q);
         const T* dout = static_cast<const T*>(side ? p.dko : p.dqo);
         T* dx = static_cast<T*>(side ? p.ko : p.qo);
-        float wa[VN], wb[VN], sa[VN], sb[VN];
-        load_f<VN>(w + un.e0, w && un.has0, 1.f, wa);
-        load_f<VN>(w + un.e1, w && un.has1, 1.f, wb);
+        const float* wp = side ? p.kw : p.qw;
+        float2 w[VN], sum[VN];
+        if constexpr (HASW) {
+            load_weight<VN>(wp, un, w);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) sa[e] = sb[e] = 0.f;
+            for (int e = 0; e < VN; ++e) sum[e] = twice(0.f);
+        }
         for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < p.T; t += nwarps) {
             const int64_t row = angle_row(p, t);
             if (row < 0) continue;
-            float cs[VN], sn[VN];
-            load_angles<VN>(p, row, u, un.rot, cs, sn);
-            for (int ps = 0; ps < np; ++ps) {
-                const int h = ps * hpw + sub;
-                const bool ok = h < H;
-                const T* src = x + t * ld + (int64_t)h * p.d;
-                const T* dsrc = dout + (t * H + h) * p.d;
-                T* dst = dx + t * ldd + (int64_t)h * p.d;
-                float a[VN], b[VN], ga[VN], gb[VN];
-                unpack(ok && un.has0 ? ld16_stream(src + un.e0) : none, a);
-                unpack(ok && un.has1 ? ld16_stream(src + un.e1) : none, b);
-                unpack(ok && un.has0 ? ld16_stream(dsrc + un.e0) : none, ga);
-                unpack(ok && un.has1 ? ld16_stream(dsrc + un.e1) : none, gb);
-                const float r = __frsqrt_rn(__fmaf_rn(group_sum(squares<VN>(a, b), p.lpr), p.c, p.eps));
-                if (un.rot) rotate<VN>(ga, gb, cs, sn, p.inter, true);
-                float dot = 0.f;
+            Angles<VN> an;
+            an.load(p, row, u, un.rot, true);
+            const T* src = x + t * ld;
+            const T* dsrc = dout + t * H * p.d;
+            T* dst = dx + t * ldd;
+            for (int ps = 0; ps < np; ps += UR) {
+                uint4 ra[UR], rb[UR], ga[UR], gb[UR];
 #pragma unroll
-                for (int e = 0; e < VN; ++e) {
-                    sa[e] = __fmaf_rn(__fmul_rn(a[e], r), ga[e], sa[e]);
-                    sb[e] = __fmaf_rn(__fmul_rn(b[e], r), gb[e], sb[e]);
-                    ga[e] = __fmul_rn(ga[e], wa[e]), gb[e] = __fmul_rn(gb[e], wb[e]);
-                    dot = __fmaf_rn(ga[e], a[e], dot);
-                    dot = __fmaf_rn(gb[e], b[e], dot);
+                for (int i = 0; i < UR; ++i) {
+                    const int h = (ps + i) * hpw + sub;
+                    const bool ok = ps + i < np && h < H;
+                    ra[i] = ok && un.has0 ? ld16_stream(src + h * p.d + un.e0) : none;
+                    rb[i] = ok && un.has1 ? ld16_stream(src + h * p.d + un.e1) : none;
+                    ga[i] = ok && un.has0 ? ld16_stream(dsrc + h * p.d + un.e0) : none;
+                    gb[i] = ok && un.has1 ? ld16_stream(dsrc + h * p.d + un.e1) : none;
                 }
-                dot = group_sum(dot, p.lpr);
-                const float f = -__fmul_rn(__fmul_rn(__fmul_rn(r, r), __fmul_rn(r, p.c)), dot);
 #pragma unroll
-                for (int e = 0; e < VN; ++e) {
-                    a[e] = __fmaf_rn(a[e], f, __fmul_rn(r, ga[e]));
-                    b[e] = __fmaf_rn(b[e], f, __fmul_rn(r, gb[e]));
+                for (int i = 0; i < UR; ++i) {
+                    if (ps + i >= np) break;
+                    const int h = (ps + i) * hpw + sub;
+                    float2 v[VN], g[VN];
+                    unpack_unit<VN>(ra[i], rb[i], v);
+                    unpack_unit<VN>(ga[i], gb[i], g);
+                    const float r = rsqrtf(__fmaf_rn(group_sum(dot<VN>(v, v), p.lpr), p.c, p.eps));
+                    an.template turn<INTER>(g);
+                    if constexpr (HASW) {
+#pragma unroll
+                        for (int e = 0; e < VN; ++e) {
+                            sum[e] = __ffma2_rn(__fmul2_rn(v[e], twice(h < H ? r : 0.f)), g[e], sum[e]);
+                            g[e] = __fmul2_rn(g[e], w[e]);
+                        }
+                    }
+                    const float gx = group_sum(dot<VN>(g, v), p.lpr);
+                    const float f = -__fmul_rn(__fmul_rn(__fmul_rn(r, r), __fmul_rn(r, p.c)), gx);
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) v[e] = __ffma2_rn(v[e], twice(f), __fmul2_rn(twice(r), g[e]));
+                    if (h < H && un.has0) st16_stream(dst + h * p.d + un.e0, pack_half<VN>(v));
+                    if (h < H && un.has1) st16_stream(dst + h * p.d + un.e1, pack_half<VN>(v + VN / 2));
                 }
-                if (ok && un.has0) st16_stream(dst + un.e0, pack(a));
-                if (ok && un.has1) st16_stream(dst + un.e1, pack(b));
             }
         }
         // the CTA's sum for the weight: its lane groups in ascending order
-        if (w && p.part) {
+        if constexpr (HASW) {
+            if (!p.part) continue;
             float* mine = acc + (int64_t)(threadIdx.x / p.lpr) * p.d;
 #pragma unroll
             for (int e = 0; e < VN; ++e) {
-                if (un.has0) mine[un.e0 + e] = sa[e];
-                if (un.has1) mine[un.e1 + e] = sb[e];
+                float* to = mine + (e < VN / 2 ? un.e0 + 2 * e : un.e1 + 2 * e - VN);
+                if (e < VN / 2 ? un.has0 : un.has1) to[0] = sum[e].x, to[1] = sum[e].y;
             }
             __syncthreads();
             for (int e = threadIdx.x; e < p.d; e += blockDim.x) {
@@ -233,17 +283,25 @@ __global__ void __launch_bounds__(256) qk_bwd_kernel(const QkParams p) {
     }
 }
 
-// dweight [d] of q (blockIdx.y 0) and k (1): a warp adds the CTAs' partials of one value, lane l
-// those of CTAs l, l + 32, .. in order, then a butterfly.
+// dweight [d] of q (blockIdx.y 0) and k (1): the CTAs' partials.  A CTA takes 4 float4 columns;
+// thread (slice, column) adds partials slice, slice + 64, .., then a thread per column the slices in order.
 __global__ void __launch_bounds__(256) qk_bwd_sum_kernel(int d, int ctas, const float* __restrict__ part,
                                                          float* __restrict__ dqw, float* __restrict__ dkw) {
-    const int e = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, side = blockIdx.y;
+    __shared__ float4 sums[64][4];
+    const int x = threadIdx.x & 3, slice = threadIdx.x >> 2, side = blockIdx.y, e = (blockIdx.x * 4 + x) * 4;
     float* out = side ? dkw : dqw;
-    if (e >= d || !out) return;
-    float s = 0.f;
-    for (int i = threadIdx.x & 31; i < ctas; i += 32) s = __fadd_rn(s, part[((int64_t)i * 2 + side) * d + e]);
-    s = group_sum(s, 32);
-    if ((threadIdx.x & 31) == 0) out[e] = s;
+    if (!out) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& v) { s.x = __fadd_rn(s.x, v.x), s.y = __fadd_rn(s.y, v.y), s.z = __fadd_rn(s.z, v.z), s.w = __fadd_rn(s.w, v.w); };
+    if (e < d) {
+#pragma unroll 4
+        for (int i = slice; i < ctas; i += 64) add(*reinterpret_cast<const float4*>(part + ((int64_t)i * 2 + side) * d + e));
+    }
+    sums[slice][x] = s;
+    __syncthreads();
+    if (slice || e >= d) return;
+    for (int i = 1; i < 64; ++i) add(sums[i][x]);
+    out[e] = s.x, out[e + 1] = s.y, out[e + 2] = s.z, out[e + 3] = s.w;
 }
 
 gdn_status check_qk(const gdn_qk_shape* s) {
@@ -275,15 +333,31 @@ QkParams qk_params(const gdn_qk_shape* s) {
 
 gdn_status check_angles(const gdn_qk_shape* s, const float* cos, const float* sin, const int32_t* pos) {
     if (s->rotary_dim == 0) return GDN_OK;
-    if (!cos || !sin || !aligned4(cos) || !aligned4(sin) || !aligned4(pos)) return GDN_ERR_INVALID_ARG;
+    if (!cos || !sin || !aligned16(cos) || !aligned16(sin) || !aligned4(pos)) return GDN_ERR_INVALID_ARG;
     if (!pos && s->max_positions < s->T) return GDN_ERR_INVALID_ARG;
     return GDN_OK;
 }
 
-// CTAs of the gradient: every SM several, a token per warp at least.
+template <typename T, bool INTER, bool HASW>
+void qk_launch2(int grid, cudaStream_t s, const QkParams& p) {
+    if (p.passes >= 2) qk_kernel<T, INTER, HASW, 2><<<grid, 256, 0, s>>>(p);
+    else qk_kernel<T, INTER, HASW, 1><<<grid, 256, 0, s>>>(p);
+}
+template <typename T>
+void qk_launch(int grid, cudaStream_t s, const QkParams& p, bool w) {
+    if (p.inter) w ? qk_launch2<T, true, true>(grid, s, p) : qk_launch2<T, true, false>(grid, s, p);
+    else w ? qk_launch2<T, false, true>(grid, s, p) : qk_launch2<T, false, false>(grid, s, p);
+}
+template <typename T>
+void qk_bwd_launch(int grid, size_t smem, cudaStream_t s, const QkParams& p, bool w) {
+    if (p.inter) w ? qk_bwd_kernel<T, true, true><<<grid, 256, smem, s>>>(p) : qk_bwd_kernel<T, true, false><<<grid, 256, smem, s>>>(p);
+    else w ? qk_bwd_kernel<T, false, true><<<grid, 256, smem, s>>>(p) : qk_bwd_kernel<T, false, false><<<grid, 256, smem, s>>>(p);
+}
+
+// CTAs of the gradient: one wave of two an SM (128 registers a thread), a token per warp at least.
 int qk_bwd_ctas(const gdn_qk_shape* s) {
     const int64_t want = (s->T + 7) / 8;
-    return (int)(want < kSMs * 4 ? (want > 1 ? want : 1) : kSMs * 4);
+    return (int)(want < kSMs * 2 ? (want > 1 ? want : 1) : kSMs * 2);
 }
 
 }  // namespace
@@ -315,8 +389,9 @@ extern "C" gdn_status gdn_qk_norm_rope(const gdn_qk_shape* shape, const void* q,
     const int64_t want = (p.items + 7) / 8;
     const int grid = (int)(want < kSMs * 16 ? want : kSMs * 16);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (shape->dtype == GDN_BF16) qk_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(p);
-    else qk_kernel<float><<<grid, 256, 0, s>>>(p);
+    const bool w = q_weight || k_weight;
+    if (shape->dtype == GDN_BF16) qk_launch<__nv_bfloat16>(grid, s, p, w);
+    else qk_launch<float>(grid, s, p, w);
     return launch_status();
 }
 
@@ -358,10 +433,11 @@ extern "C" gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_shape* shape, const void
     const int ctas = qk_bwd_ctas(shape);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t smem = sums ? (size_t)(256 / p.lpr) * p.d * sizeof(float) : 0;
-    if (shape->dtype == GDN_BF16) qk_bwd_kernel<__nv_bfloat16><<<ctas, 256, smem, s>>>(p);
-    else qk_bwd_kernel<float><<<ctas, 256, smem, s>>>(p);
+    const bool w = q_weight || k_weight;
+    if (shape->dtype == GDN_BF16) qk_bwd_launch<__nv_bfloat16>(ctas, smem, s, p, w);
+    else qk_bwd_launch<float>(ctas, smem, s, p, w);
     st = launch_status();
     if (st != GDN_OK || !sums) return st;
-    qk_bwd_sum_kernel<<<dim3((unsigned)((p.d + 7) / 8), 2), 256, 0, s>>>(p.d, ctas, p.part, dq_weight, dk_weight);
+    qk_bwd_sum_kernel<<<dim3((unsigned)((p.d + 15) / 16), 2), 256, 0, s>>>(p.d, ctas, p.part, dq_weight, dk_weight);
     return launch_status();
 }

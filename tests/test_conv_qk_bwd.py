@@ -184,6 +184,22 @@ def test_qk_rows_do_not_depend_on_the_batch_and_skipped_tokens_stay():
     assert np.abs(to_np(g["dq_weight"]) - want).max() <= 1e-4 * np.abs(want).max()
 
 
+def test_qk_with_one_weight():
+    c = QkCase(torch.bfloat16, 40, 3, 2, 64, 32, "rms")
+    cs, sn = c.cos[c.pos.long()], c.sin[c.pos.long()]
+    for kw in (dict(q_weight=c.qw), dict(k_weight=c.kw)):
+        qo, ko = gdn.gdn_qk_norm_rope(c.q, c.k, c.cos, c.sin, positions=c.pos, **kw)
+        g = gdn.gdn_qk_norm_rope_bwd(c.q, c.k, c.cos, c.sin, c.dq, c.dk, positions=c.pos, **kw)
+        for x, w, out, do, dx, dw in ((c.q, kw.get("q_weight"), qo, c.dq, g["dq"], g["dq_weight"]),
+                                      (c.k, kw.get("k_weight"), ko, c.dk, g["dk"], g["dk_weight"])):
+            want, want_w = ref.norm_rope_bwd(x, w, cs, sn, do)
+            assert np.abs(to_np(out) - ref.norm_rope(x, w, cs, sn)).max() <= 2 * BF16_ROUND * np.abs(to_np(out)).max()
+            assert np.abs(to_np(dx) - want).max() <= 2 * BF16_ROUND * np.abs(want).max()
+            assert (dw is None) == (w is None)
+            if w is not None:
+                assert np.abs(to_np(dw) - want_w).max() <= 1e-4 * np.abs(want_w).max()
+
+
 def test_qk_positions_default_to_rows_and_outputs_in_place():
     c = QkCase(torch.float32, 50, 2, 2, 32, 32, "l2")
     q, k = c.q.contiguous(), c.k.contiguous()
