@@ -8,6 +8,7 @@ library's own kernels.  There is no fallback: if the library is missing or a
 call fails, a RuntimeError is raised.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -479,78 +480,138 @@ def gdn_causal_conv1d_update(x, weight, conv_state, state_indices=None, bias=Non
 
 
 # ---------------------------------------------------------------- gradients, q/k norm with rotation, selective scan
+#
+# A decode step calls these once per layer with little to compute: the checks read each attribute
+# once, in one expression that holds for a good argument, and look for what is wrong only after it
+# does not; shape structs and workspace sizes are kept by their values.
 
-class _On:
-    """The device and, where the caller names one, the stream that a call allocates and launches on.
-    Tensors handed to a named stream are recorded on it, so that memory freed right after the call
-    is not reused while the stream still reads it."""
-
-    def __init__(self, device, stream, tensors):
-        if stream is None:
-            self.ctx = torch.cuda.device(device)
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            self.ctx = torch.cuda.stream(stream)
-            if stream != torch.cuda.current_stream(device):
-                for t in tensors:
-                    if t is not None:
-                        t.record_stream(stream)
-        self.device = device
-
-    def __enter__(self):
-        self.ctx.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
-def _is(t, name, shape, dtype, device):
-    """t is a dense tensor of this shape."""
-    _need(t, name, dtype, device)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+def _on(call, args):
+    """call(**args) on the stream that args name: its outputs and workspace belong to that stream, and
+    the tensors it is given are recorded on it, so that memory freed right after the call is not
+    reused while the stream still reads it."""
+    stream = args.pop("stream")
+    tensors = [t for t in args.values() if isinstance(t, torch.Tensor) and t.is_cuda]
+    for t in tensors:
+        if t.device != stream.device:
+            raise ValueError(f"stream is on {stream.device}, a tensor on {t.device}")
+    if stream != torch.cuda.current_stream(stream.device):
+        for t in tensors:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return call(**args)
 
 
-def _rows(t, name, shape, dtype, device):
-    """t has this shape and its rows t[i] are dense; the elements from one row to the next."""
+def _invoke(name, index, *args):
+    """The C entry point on the current stream of device `index`."""
+    entry = getattr(lib(), name)
+    if torch.cuda.current_device() == index:
+        rc = entry(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = entry(*args, _raw_stream(index))
+    if rc != GDN_OK:
+        raise GdnError(rc, name)
+
+
+def _wrong(t, name, shape, dtype, index):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    dense = 1
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and step != dense:
-            raise ValueError(f"each row of {name} must be contiguous")
-        dense *= size
-    if t.shape[0] <= 1:
-        return dense
-    if t.stride(0) < dense:
-        raise ValueError(f"the rows of {name} must not overlap")
-    return t.stride(0)
 
 
-def _ndim(t, name, n):
+def _is(t, name, shape, dtype, index):
+    """Address of t, a dense tensor of this shape (None: null)."""
+    if t is None:
+        return None
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _wrong(t, name, shape, dtype, index)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name, shape, dtype, index):
+    """Address of t, a tensor of this shape with dense rows t[i], and the elements from one row to the next."""
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape:
+            dense = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+            if t.is_contiguous():
+                return t.data_ptr(), dense
+            step = t.stride()
+            inner = step[-1] == 1 or shape[-1] == 1
+            if len(step) == 3:
+                inner = inner and (step[1] == shape[2] or shape[1] == 1)
+            if inner and (step[0] >= dense or shape[0] == 1):
+                return t.data_ptr(), dense if shape[0] == 1 else step[0]
+    except AttributeError:
+        pass
+    _wrong(t, name, shape, dtype, index)
+    raise ValueError(f"the rows of {name} must be contiguous and must not overlap")
+
+
+def _first(t, name, dims):
+    """Shape, dtype and device index of the tensor that the others are checked against."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    return t.shape, t.dtype, t.get_device()
+
+
+def _dims(t, name, n):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != n:
         raise ValueError(f"{name} must have {n} dimensions, got {t.dim()}")
+    return t.shape
 
 
-def _workspace(workspace, need, device):
+def _sequences(cu_seqlens, index):
+    """Number of sequences and address of cu_seqlens."""
+    n = _dims(cu_seqlens, "cu_seqlens", 1)[0]
+    if n < 1:
+        raise ValueError("cu_seqlens must have at least one entry")
+    return n - 1, _is(cu_seqlens, "cu_seqlens", (n,), torch.int32, index)
+
+
+def _like(t):
+    """A dense tensor like t to write to (t's rows may be slices); t None: None."""
+    return None if t is None else torch.empty_like(t)
+
+
+def _space(workspace, need, device):
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=device)
     _need(workspace, "workspace", torch.uint8, device)
     return workspace
+
+
+@functools.lru_cache(4096)
+def _struct(kind, *values):
+    return ctypes.byref(kind(*values))
+
+
+@functools.lru_cache(4096)
+def _space_of(entry, kind, *values):
+    return max(int(getattr(lib(), entry)(ctypes.byref(kind(*values)))), 16)
 
 
 def gdn_causal_conv1d_bwd(x, weight, cu_seqlens, d_out, bias=None, init_state=None, d_final_state=None,
@@ -560,56 +621,44 @@ def gdn_causal_conv1d_bwd(x, weight, cu_seqlens, d_out, bias=None, init_state=No
     the order of the sequences.  Returns dict dx (dtype of x), dweight, dbias
     (fp32, dbias None without a bias), d_init_state (dtype of x or None).  Rows
     of dx behind cu_seqlens[N] are not written."""
-    _ndim(x, "x", 2)
-    _ndim(weight, "weight", 2)
-    _ndim(cu_seqlens, "cu_seqlens", 1)
-    dev, dt, (T, C), W = x.device, x.dtype, x.shape, weight.shape[1]
-    N = cu_seqlens.numel() - 1
-    if N < 0:
-        raise ValueError("cu_seqlens must have at least one entry")
-    _is(x, "x", (T, C), dt, dev)
-    _is(d_out, "d_out", (T, C), dt, dev)
-    _is(weight, "weight", (C, W), torch.float32, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    if bias is not None:
-        _is(bias, "bias", (C,), torch.float32, dev)
-    for t, name in ((init_state, "init_state"), (d_final_state, "d_final_state")):
-        if t is not None:
-            _is(t, name, (N, W - 1, C), dt, dev)
-    shape = ConvShape(N, T, C, W, _dtype_code(x), int(bool(activation)))
-    with _On(dev, stream, (x, weight, cu_seqlens, d_out, bias, init_state, d_final_state, workspace)) as s:
-        res = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight),
-                   dbias=None if bias is None else torch.empty_like(bias),
-                   d_init_state=torch.empty(N, W - 1, C, dtype=dt, device=dev) if need_d_init_state else None)
-        ws = _workspace(workspace, lib().gdn_causal_conv1d_bwd_workspace_size(ctypes.byref(shape)), dev)
-        rc = lib().gdn_causal_conv1d_bwd(ctypes.byref(shape), _at(x), _at(weight), _at(bias), _at(cu_seqlens),
-                                         _at(init_state), _at(d_out), _at(d_final_state), _at(res["dx"]),
-                                         _at(res["dweight"]), _at(res["dbias"]), _at(res["d_init_state"]),
-                                         _at(ws), ws.numel(), s)
-    _check(rc, "gdn_causal_conv1d_bwd")
-    return res
+    if stream is not None:
+        return _on(gdn_causal_conv1d_bwd, locals())
+    shape, ty, index = _first(x, "x", 2)
+    (T, C), W, f32 = shape, _dims(weight, "weight", 2)[1], torch.float32
+    N, cu = _sequences(cu_seqlens, index)
+    state = (N, W - 1, C)
+    ptrs = (_is(x, "x", shape, ty, index), _is(weight, "weight", (C, W), f32, index), _is(bias, "bias", (C,), f32, index),
+            cu, _is(init_state, "init_state", state, ty, index), _is(d_out, "d_out", shape, ty, index),
+            _is(d_final_state, "d_final_state", state, ty, index))
+    sizes = (ConvShape, N, T, C, W, _dtype_code(x), int(bool(activation)))
+    dx, dw, db = _like(x), _like(weight), _like(bias)
+    dh = torch.empty(state, dtype=ty, device=x.device) if need_d_init_state else None
+    ws = _space(workspace, _space_of("gdn_causal_conv1d_bwd_workspace_size", *sizes), x.device)
+    _invoke("gdn_causal_conv1d_bwd", index, _struct(*sizes), *ptrs, dx.data_ptr(), dw.data_ptr(), _at(db), _at(dh),
+            ws.data_ptr(), ws.numel())
+    return dict(dx=dx, dweight=dw, dbias=db, d_init_state=dh)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 _NORMS = {"rms": 0, "l2": 1}
 
 
-def _qk_shape(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
-    _ndim(q, "q", 3)
-    _ndim(k, "k", 3)
-    _ndim(cos, "cos", 2)
-    dev, (T, HQ, d), HK = q.device, q.shape, k.shape[1]
+def _qk(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved):
+    """Sizes for the struct, the inputs' addresses, the device index."""
+    qs, ty, index = _first(q, "q", 3)
+    ks, angles = _dims(k, "k", 3), _dims(cos, "cos", 2)
+    (T, HQ, d), HK, f32 = qs, ks[1], torch.float32
     if norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
-    ldq, ldk = _rows(q, "q", (T, HQ, d), q.dtype, dev), _rows(k, "k", (T, HK, d), q.dtype, dev)
-    for t, name in ((cos, "cos"), (sin, "sin")):
-        _is(t, name, cos.shape, torch.float32, dev)
-    if positions is not None:
-        _is(positions, "positions", (T,), torch.int32, dev)
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _is(t, name, (d,), torch.float32, dev)
-    return QkShape(T, HQ, HK, d, 2 * cos.shape[1], int(bool(interleaved)), _NORMS[norm], cos.shape[0], float(eps),
-                   _dtype_code(q), ldq, ldk)
+    (qp, ldq), (kp, ldk) = _rows(q, "q", qs, ty, index), _rows(k, "k", (T, HK, d), ty, index)
+    ptrs = (qp, kp, _is(q_weight, "q_weight", (d,), f32, index), _is(k_weight, "k_weight", (d,), f32, index),
+            _is(cos, "cos", angles, f32, index), _is(sin, "sin", angles, f32, index),
+            _is(positions, "positions", (T,), torch.int32, index))
+    return (QkShape, T, HQ, HK, d, 2 * angles[1], int(bool(interleaved)), _NORMS[norm], angles[0], float(eps),
+            _dtype_code(q), ldq, ldk), ptrs, index
 
 
 def gdn_qk_norm_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, norm="rms", eps=1e-6,
@@ -621,16 +670,13 @@ def gdn_qk_norm_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=Non
     fp32: pairs (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved.  q and k
     may be column slices of wider rows.  Returns dense (q_out, k_out).  A token
     whose position is outside the tables is skipped (its rows untouched)."""
-    shape = _qk_shape(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
-    dev = q.device
-    with _On(dev, stream, (q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out)) as s:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev) if k_out is None else k_out
-        _is(q_out, "q_out", q.shape, q.dtype, dev)
-        _is(k_out, "k_out", k.shape, q.dtype, dev)
-        rc = lib().gdn_qk_norm_rope(ctypes.byref(shape), _at(q), _at(k), _at(q_weight), _at(k_weight), _at(cos),
-                                    _at(sin), _at(positions), _at(q_out), _at(k_out), s)
-    _check(rc, "gdn_qk_norm_rope")
+    if stream is not None:
+        return _on(gdn_qk_norm_rope, locals())
+    sizes, ptrs, index = _qk(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    q_out = _like(q) if q_out is None else q_out
+    k_out = _like(k) if k_out is None else k_out
+    _invoke("gdn_qk_norm_rope", index, _struct(*sizes), *ptrs, _is(q_out, "q_out", q.shape, q.dtype, index),
+            _is(k_out, "k_out", k.shape, q.dtype, index))
     return q_out, k_out
 
 
@@ -639,38 +685,33 @@ def gdn_qk_norm_rope_bwd(q, k, cos, sin, d_q_out, d_k_out, positions=None, q_wei
     """Gradient of gdn_qk_norm_rope at its inputs q, k.  dq, dk: written in place
     when given (they may be column slices of wider rows), else dense.  Returns
     dict dq, dk, dq_weight, dk_weight (fp32, None without the weight)."""
-    shape = _qk_shape(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
-    dev = q.device
-    _is(d_q_out, "d_q_out", q.shape, q.dtype, dev)
-    _is(d_k_out, "d_k_out", k.shape, q.dtype, dev)
-    with _On(dev, stream, (q, k, cos, sin, positions, q_weight, k_weight, d_q_out, d_k_out, dq, dk, workspace)) as s:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=q.dtype, device=dev) if dk is None else dk
-        lddq, lddk = _rows(dq, "dq", q.shape, q.dtype, dev), _rows(dk, "dk", k.shape, q.dtype, dev)
-        res = dict(dq=dq, dk=dk, dq_weight=None if q_weight is None else torch.empty_like(q_weight),
-                   dk_weight=None if k_weight is None or shape.HK == 0 else torch.empty_like(k_weight))
-        ws = _workspace(workspace, lib().gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(shape)), dev)
-        rc = lib().gdn_qk_norm_rope_bwd(ctypes.byref(shape), _at(q), _at(k), _at(q_weight), _at(k_weight), _at(cos),
-                                        _at(sin), _at(positions), _at(d_q_out), _at(d_k_out), _at(dq), _at(dk),
-                                        lddq, lddk, _at(res["dq_weight"]), _at(res["dk_weight"]), _at(ws),
-                                        ws.numel(), s)
-    _check(rc, "gdn_qk_norm_rope_bwd")
-    return res
+    if stream is not None:
+        return _on(gdn_qk_norm_rope_bwd, locals())
+    sizes, ptrs, index = _qk(q, k, cos, sin, positions, q_weight, k_weight, norm, eps, interleaved)
+    qs, ks, ty = q.shape, k.shape, q.dtype
+    grads = (_is(d_q_out, "d_q_out", qs, ty, index), _is(d_k_out, "d_k_out", ks, ty, index))
+    dq = _like(q) if dq is None else dq
+    dk = _like(k) if dk is None else dk
+    (dqp, lddq), (dkp, lddk) = _rows(dq, "dq", qs, ty, index), _rows(dk, "dk", ks, ty, index)
+    dqw, dkw = _like(q_weight), _like(k_weight) if ks[1] else None
+    ws = None
+    if dqw is not None or dkw is not None:
+        ws = _space(workspace, _space_of("gdn_qk_norm_rope_bwd_workspace_size", *sizes), q.device)
+    _invoke("gdn_qk_norm_rope_bwd", index, _struct(*sizes), *ptrs, *grads, dqp, dkp, lddq, lddk, _at(dqw), _at(dkw),
+            _at(ws), 0 if ws is None else ws.numel())
+    return dict(dq=dq, dk=dk, dq_weight=dqw, dk_weight=dkw)
 
 
-def _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus):
-    _ndim(x, "x", 2)
-    _ndim(A_log, "A_log", 2)
-    _ndim(B, "B", 3)
-    dev, ty, (T, ch), S, G = x.device, x.dtype, x.shape, A_log.shape[1], B.shape[1]
-    lds = [_rows(t, name, (T, ch), ty, dev) for t, name in ((x, "x"), (dt, "dt"))]
-    lds.append(0 if z is None else _rows(z, "z", (T, ch), ty, dev))
-    lds += [_rows(t, name, (T, G, S), ty, dev) for t, name in ((B, "B"), (C, "C"))]
-    _is(A_log, "A_log", (ch, S), torch.float32, dev)
-    for t, name in ((D, "D"), (dt_bias, "dt_bias")):
-        if t is not None:
-            _is(t, name, (ch,), torch.float32, dev)
-    return ScanShape(N, T, ch, G, S, _dtype_code(x), int(bool(dt_softplus)), *lds)
+def _scan(shape, ty, index, x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus):
+    """Sizes for the struct and the inputs' addresses, x to dt_bias."""
+    (T, ch), S, G = shape, _dims(A_log, "A_log", 2)[1], _dims(B, "B", 3)[1]
+    f32, bc = torch.float32, (T, G, S)
+    (xp, ldx), (dtp, lddt) = _rows(x, "x", shape, ty, index), _rows(dt, "dt", shape, ty, index)
+    zp, ldz = (None, 0) if z is None else _rows(z, "z", shape, ty, index)
+    (Bp, ldB), (Cp, ldC) = _rows(B, "B", bc, ty, index), _rows(C, "C", bc, ty, index)
+    ptrs = (xp, dtp, _is(A_log, "A_log", (ch, S), f32, index), Bp, Cp, _is(D, "D", (ch,), f32, index), zp,
+            _is(dt_bias, "dt_bias", (ch,), f32, index))
+    return (ScanShape, N, T, ch, G, S, _dtype_code(x), int(bool(dt_softplus)), ldx, lddt, ldz, ldB, ldC), ptrs
 
 
 def gdn_selective_scan_fwd(x, dt, A_log, B, C, cu_seqlens, D=None, z=None, dt_bias=None, state=None,
@@ -684,29 +725,17 @@ def gdn_selective_scan_fwd(x, dt, A_log, B, C, cu_seqlens, D=None, z=None, dt_bi
     slot (in place; int32 state_indices, has_initial_state as in
     gdn_causal_conv1d_fwd).  Returns y [T, channels] (rows behind cu_seqlens[N]
     not written)."""
-    _ndim(cu_seqlens, "cu_seqlens", 1)
-    N = cu_seqlens.numel() - 1
-    shape = _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
-    dev = x.device
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    if N < 0:
-        raise ValueError("cu_seqlens must have at least one entry")
-    slots = 0
-    if state is not None:
-        _ndim(state, "state", 3)
-        slots = state.shape[0]
-        _is(state, "state", (slots, shape.C, shape.S), torch.float32, dev)
-    for t, name in ((state_indices, "state_indices"), (has_initial_state, "has_initial_state")):
-        if t is not None:
-            _is(t, name, (N,), torch.int32, dev)
-    with _On(dev, stream, (x, dt, A_log, B, C, cu_seqlens, D, z, dt_bias, state, state_indices, has_initial_state,
-                           out)) as s:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-        _is(out, "out", x.shape, x.dtype, dev)
-        rc = lib().gdn_selective_scan_fwd(ctypes.byref(shape), _at(x), _at(dt), _at(A_log), _at(B), _at(C), _at(D),
-                                          _at(z), _at(dt_bias), _at(cu_seqlens), _at(state), _at(state_indices),
-                                          slots, _at(has_initial_state), _at(out), s)
-    _check(rc, "gdn_selective_scan_fwd")
+    if stream is not None:
+        return _on(gdn_selective_scan_fwd, locals())
+    shape, ty, index = _first(x, "x", 2)
+    N, cu = _sequences(cu_seqlens, index)
+    sizes, ptrs = _scan(shape, ty, index, x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
+    slots = 0 if state is None else _dims(state, "state", 3)[0]
+    state_ptrs = (_is(state, "state", (slots, sizes[3], sizes[5]), torch.float32, index),
+                  _is(state_indices, "state_indices", (N,), torch.int32, index), slots,
+                  _is(has_initial_state, "has_initial_state", (N,), torch.int32, index))
+    out = _like(x) if out is None else out
+    _invoke("gdn_selective_scan_fwd", index, _struct(*sizes), *ptrs, cu, *state_ptrs, _is(out, "out", shape, ty, index))
     return out
 
 
@@ -715,20 +744,15 @@ def gdn_selective_scan_update(x, dt, A_log, B, C, state, state_indices=None, D=N
     """One token per sequence: x, dt, z [N, channels], B, C [N, G, S]; state
     [slots, channels, S] fp32 updated in place.  Returns y [N, channels] (rows of
     skipped slots untouched)."""
-    _ndim(state, "state", 3)
-    N = x.shape[0]
-    shape = _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
-    dev = x.device
-    _is(state, "state", (state.shape[0], shape.C, shape.S), torch.float32, dev)
-    if state_indices is not None:
-        _is(state_indices, "state_indices", (N,), torch.int32, dev)
-    with _On(dev, stream, (x, dt, A_log, B, C, D, z, dt_bias, state, state_indices, out)) as s:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-        _is(out, "out", x.shape, x.dtype, dev)
-        rc = lib().gdn_selective_scan_update(ctypes.byref(shape), _at(x), _at(dt), _at(A_log), _at(B), _at(C), _at(D),
-                                             _at(z), _at(dt_bias), _at(state), _at(state_indices), state.shape[0],
-                                             _at(out), s)
-    _check(rc, "gdn_selective_scan_update")
+    if stream is not None:
+        return _on(gdn_selective_scan_update, locals())
+    shape, ty, index = _first(x, "x", 2)
+    sizes, ptrs = _scan(shape, ty, index, x, dt, A_log, B, C, shape[0], D, z, dt_bias, dt_softplus)
+    slots = _dims(state, "state", 3)[0]
+    state_ptrs = (_is(state, "state", (slots, sizes[3], sizes[5]), torch.float32, index),
+                  _is(state_indices, "state_indices", (shape[0],), torch.int32, index), slots)
+    out = _like(x) if out is None else out
+    _invoke("gdn_selective_scan_update", index, _struct(*sizes), *ptrs, *state_ptrs, _is(out, "out", shape, ty, index))
     return out
 
 
@@ -739,32 +763,20 @@ def gdn_selective_scan_bwd(x, dt, A_log, B, C, cu_seqlens, d_out, D=None, z=None
     sequences.  Returns dict dx, ddt, dz, dB, dC (dtype of x), dA_log, dD,
     ddt_bias, d_init_state (fp32); None where the input is None.  Rows behind
     cu_seqlens[N] are not written."""
-    _ndim(cu_seqlens, "cu_seqlens", 1)
-    N = cu_seqlens.numel() - 1
-    shape = _scan_shape(x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
-    dev, ty = x.device, x.dtype
-    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
-    if N < 0:
-        raise ValueError("cu_seqlens must have at least one entry")
-    _is(d_out, "d_out", x.shape, ty, dev)
-    for t, name in ((init_state, "init_state"), (d_final_state, "d_final_state")):
-        if t is not None:
-            _is(t, name, (N, shape.C, shape.S), torch.float32, dev)
-    with _On(dev, stream, (x, dt, A_log, B, C, cu_seqlens, d_out, D, z, dt_bias, init_state, d_final_state,
-                           workspace)) as s:
-        like = lambda t, kind=ty: None if t is None else torch.empty(t.shape, dtype=kind, device=dev)  # noqa: E731
-        res = dict(dx=like(x), ddt=like(dt), dA_log=like(A_log, torch.float32), dB=like(B), dC=like(C),
-                   dD=like(D, torch.float32), dz=like(z), ddt_bias=like(dt_bias, torch.float32),
-                   d_init_state=torch.empty(N, shape.C, shape.S, dtype=torch.float32, device=dev)
-                   if need_d_init_state else None)
-        ws = _workspace(workspace, lib().gdn_selective_scan_bwd_workspace_size(ctypes.byref(shape)), dev)
-        rc = lib().gdn_selective_scan_bwd(ctypes.byref(shape), _at(x), _at(dt), _at(A_log), _at(B), _at(C), _at(D),
-                                          _at(z), _at(dt_bias), _at(cu_seqlens), _at(init_state), _at(d_out),
-                                          _at(d_final_state), *(_at(res[k]) for k in
-                                                                ("dx", "ddt", "dA_log", "dB", "dC", "dD", "dz",
-                                                                 "ddt_bias", "d_init_state")),
-                                          _at(ws), ws.numel(), s)
-    _check(rc, "gdn_selective_scan_bwd")
+    if stream is not None:
+        return _on(gdn_selective_scan_bwd, locals())
+    shape, ty, index = _first(x, "x", 2)
+    N, cu = _sequences(cu_seqlens, index)
+    sizes, ptrs = _scan(shape, ty, index, x, dt, A_log, B, C, N, D, z, dt_bias, dt_softplus)
+    state = (N, sizes[3], sizes[5])
+    more = (cu, _is(init_state, "init_state", state, torch.float32, index), _is(d_out, "d_out", shape, ty, index),
+            _is(d_final_state, "d_final_state", state, torch.float32, index))
+    res = dict(dx=_like(x), ddt=_like(dt), dA_log=_like(A_log), dB=_like(B), dC=_like(C), dD=_like(D), dz=_like(z),
+               ddt_bias=_like(dt_bias),
+               d_init_state=torch.empty(state, dtype=torch.float32, device=x.device) if need_d_init_state else None)
+    ws = _space(workspace, _space_of("gdn_selective_scan_bwd_workspace_size", *sizes), x.device)
+    _invoke("gdn_selective_scan_bwd", index, _struct(*sizes), *ptrs, *more, *map(_at, res.values()), ws.data_ptr(),
+            ws.numel())
     return res
 
 

@@ -309,3 +309,21 @@ def test_captured_calls_replay_on_new_inputs_and_other_streams():
     assert torch.equal(bits(y2), bits(want[c][0]))
     for n in g2:
         assert torch.equal(bits(g2[n]), bits(want[c][2][n])), n
+
+
+def test_refused_tensors():
+    """What the binding refuses before it launches anything (the good call runs last)."""
+    x, bc, A = torch.zeros(4, 16, device=DEV), torch.zeros(4, 1, 8, device=DEV), torch.zeros(16, 8, device=DEV)
+    cu, st = torch.tensor([0, 4], dtype=torch.int32, device=DEV), torch.zeros(2, 16, 8, device=DEV)
+    good = dict(x=x, dt=x, A_log=A, B=bc, C=bc, cu_seqlens=cu, state=st)
+    wide = torch.zeros(4, 32, device=DEV)
+    for error, change in ((ValueError, dict(x=x[:, :8])), (ValueError, dict(dt=x.cpu())), (TypeError, dict(B=bc.bfloat16())),
+                          (ValueError, dict(z=wide[:, ::2])), (ValueError, dict(x=x[:1].expand(4, 16))), (TypeError, dict(cu_seqlens=cu.long())),
+                          (ValueError, dict(A_log=A.t().contiguous().t())), (ValueError, dict(state=st[:, :8])),
+                          (ValueError, dict(state_indices=cu)), (TypeError, dict(x=x.half(), dt=x.half(), B=bc.half(), C=bc.half())),
+                          (gdn.GdnError, dict(z=torch.zeros(4, 17, device=DEV)[:, :16])), (gdn.GdnError, dict(out=x)),
+                          (ValueError, dict(out=wide[:, :16])), (ValueError, dict(D=A[:, 0])), (TypeError, dict(C=None)),
+                          (ValueError, dict(cu_seqlens=cu[:0]))):
+        with pytest.raises(error):
+            gdn.gdn_selective_scan_fwd(**dict(good, **change))
+    assert gdn.gdn_selective_scan_fwd(**good).shape == (4, 16)

@@ -158,7 +158,7 @@ def test_binding_refuses_before_the_library():
     with pytest.raises(ValueError):
         gdn.gdn_selective_scan_fwd(x[0], x, A, bc, bc, cu)
     with pytest.raises(TypeError):
-        gdn.gdn_selective_scan_update(x, x, A, bc, bc, None)
+        gdn.gdn_selective_scan_update(None, x, A, bc, bc, A)
     with pytest.raises(ValueError):
         gdn.gdn_selective_scan_bwd(x, x, A, bc, bc, cu, x)
     with pytest.raises(ValueError):
