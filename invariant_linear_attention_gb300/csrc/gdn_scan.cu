@@ -32,14 +32,27 @@ __device__ __forceinline__ float scatter_sum(float (&s)[L], int j) {
 // serves Q channels.  Per tile:
 //   1. the work per (token, channel), shared out as 16-byte chunks of x and dt: d = softplus(dt +
 //      bias) and d x go to shared memory for the walk, B and C become fp32;
-//   2. the next tile's copies are issued (asynchronous, so they take no registers; a thread reads
+//   2. a later tile's copies are issued (asynchronous, so they take no registers; a thread reads
 //      back only x, dt and z chunks that it copied itself);
 //   3. the walk: the recurrence over the tile's tokens, sum_s h C left where d was;
 //   4. D x, gate and 16-byte stores of y.
-template <typename T, int S>
+// A lane of the narrow form holds 4 states of one channel: four times the threads for a batch that
+// leaves most of the GPU idle otherwise, the same additions.  CTAs of 64 channels and 16 states, bf16,
+// us per 1000 tokens at 1 / 2 / 3 / 8 an SM: wide 160 / 166 / 207 / 339, narrow 98 / 157 / 240 / 615.
+//
+// What bounds the wide form: the step alone (per two states 4 packed products or fmas and 2
+// exponentials, in registers) runs at 6.8 T states/s on this GPU, of 10 T that the
+// exponentials and 9.6 T that the fma pipe would allow; with its loads, sums and the work per (token, channel)
+// it reaches 3.7 T.  Shared memory is the next limit: a load delivers 128 bytes a cycle into
+// registers whether lanes share an address or not, and B and C take 64 bytes a lane and token.
+// Four channels a lane halve that and lose more in the registers they take (2.9 T); one channel a lane: 3.2 T.
+template <typename T, int S, bool WIDE>
 struct FwdTile {
-    static constexpr int L = S / 8, Q = 2, CB = S == 8 ? 128 : S == 64 ? 32 : 64, NT = CB * L / Q, VN = V16<T>::n;
-    static constexpr int TT = S == 8 ? 8 : 16;
+    static constexpr int P = WIDE ? 8 : 4, Q = WIDE ? 2 : 1, L = S / P;  // states and channels of a lane, lanes of a channel
+    static constexpr int CB = WIDE ? (S == 8 ? 128 : S == 64 ? 32 : 64) : (S <= 16 ? 64 : 1024 / S);
+    static constexpr int NT = CB * L / Q, VN = V16<T>::n;
+    // A narrow walk is bound by the latency of a tile's phases: longer tiles where shared memory allows.
+    static constexpr int TT = WIDE ? (S == 8 ? 8 : 16) : (VN == 8 ? 32 : 16);
     static constexpr int CH = CB / VN;                        // 16-byte chunks of a row
     static constexpr int NV = (TT * CH + NT - 1) / NT;        // of x (dt, z) per thread and tile
     static constexpr int RS = NT / CH;                        // tokens between a thread's chunks
@@ -51,21 +64,45 @@ struct FwdTile {
     static constexpr int ROW = CB + (CB / 16) * 2;            // float2s per token
     alignas(16) float2 d[TT][ROW];
     alignas(16) float b[2][TT][S];
-    uint4 x[2][TT][CH], z[2][TT][CH], dt[TT][CH];
-    uint4 bc[2 * TT * BCH];
+    static constexpr int ST = 2;                              // tiles of x and z in flight or in use
+    uint4 x[ST][TT][CH], z[ST][TT][CH], dt[ST - 1][TT][CH];
+    uint4 bc[ST - 1][2 * TT * BCH];
     alignas(16) float D[CB];
     alignas(16) float bias[CB];
     static_assert(NT % CH == 0, "a thread keeps its columns");
 };
 
-template <typename T, int S>
-__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
-    using F = FwdTile<T, S>;
-    constexpr int L = F::L, Q = F::Q, NT = F::NT, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB;
+// The sequence of rank `rank` by length, the longest first (ties by number): with more CTAs than
+// the GPU holds, the longest walks must not be the last to start (16 ragged prompts, 16384 x 8192
+// x 16: 676 us in order of number, 610 in order of length).
+constexpr int kRanked = 256;
+__device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
+    __shared__ int len[kRanked], found;
+    for (int i = threadIdx.x; i < p.N; i += threads) {
+        int bos, eos;
+        bounds(p.cu, i, p.T, bos, eos);
+        len[i] = eos - bos;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.N; i += threads) {
+        const int mine = len[i];
+        int before = 0;
+        for (int k = 0; k < p.N; ++k) before += len[k] > mine || (len[k] == mine && k < i);
+        if (before == rank) found = i;
+    }
+    __syncthreads();
+    return found;
+}
+
+template <typename T, int S, bool WIDE>
+__global__ void __launch_bounds__(FwdTile<T, S, WIDE>::NT, FwdTile<T, S, WIDE>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
+    using F = FwdTile<T, S, WIDE>;
+    constexpr int P = F::P, L = F::L, Q = F::Q, NT = F::NT, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB, ST = F::ST;
     __shared__ F sm;
     const int tid = threadIdx.x;
     const int nb = p.bpg * p.G;
-    const int n = blockIdx.x / nb, blk = blockIdx.x % nb;
+    const int at = blockIdx.x / nb, blk = blockIdx.x % nb;
+    const int n = p.ranked ? ranked(p, at, NT) : at;
     const int g = blk / p.bpg, cg0 = (blk % p.bpg) * CB, c0 = g * p.CG + cg0;
     const int j = tid % L, cl = tid / L * Q;
     const bool ok = cg0 + cl < p.CG;  // all Q or none: p.CG is a multiple of 8
@@ -87,14 +124,15 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
     const T* Cg = static_cast<const T*>(p.Cm) + (int64_t)g * S;
     // Chunks behind the sequence or the group's channels are not copied: what the walk makes of
     // the shared memory's old contents there is never stored.
-    auto copy = [&](int t0, int buf) {
+    auto copy = [&](int i) {  // tile i
+        const int t0 = bos + i * TT, full = i % ST, half = i % (ST - 1);
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
             const int tt = row0 + r * RS;
             if (tt < TT && t0 + tt < eos && cok) {
-                copy16_async(&sm.x[buf][tt][ch], x + r * RS * p.ldx);
-                copy16_async(&sm.dt[tt][ch], dt + r * RS * p.lddt);
-                if (gate) copy16_async(&sm.z[buf][tt][ch], z + r * RS * p.ldz);
+                copy16_async(&sm.x[full][tt][ch], x + r * RS * p.ldx);
+                copy16_async(&sm.dt[half][tt][ch], dt + r * RS * p.lddt);
+                if (gate) copy16_async(&sm.z[full][tt][ch], z + r * RS * p.ldz);
             }
         }
         x += TT * p.ldx, dt += TT * p.lddt, z += TT * p.ldz;
@@ -102,24 +140,24 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
         for (int r = 0; r < NB; ++r) {
             const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
             const int64_t t = t0 + w / BCH;
-            if (which < 2 && t < eos) copy16_async(&sm.bc[v], which ? Cg + t * p.ldC + (w % BCH) * VN : Bg + t * p.ldB + (w % BCH) * VN);
+            if (which < 2 && t < eos) copy16_async(&sm.bc[half][v], which ? Cg + t * p.ldC + (w % BCH) * VN : Bg + t * p.ldB + (w % BCH) * VN);
         }
         copy_commit();
     };
-    copy(bos, 0);
+    for (int i = 0; i < ST - 1; ++i) copy(i);
 
     for (int c = tid; c < CB; c += NT) {
         const bool in = cg0 + c < p.CG;
         sm.D[c] = in && p.D ? __ldg(p.D + c0 + c) : 0.f;
         sm.bias[c] = in && p.bias ? __ldg(p.bias + c0 + c) : 0.f;
     }
-    float2 A2[Q][4], h[Q][4];
-    const int64_t own = ok ? (int64_t)(c0 + cl) * S + 8 * j : 0;
+    float2 A2[Q][P / 2], h[Q][P / 2];
+    const int64_t own = ok ? (int64_t)(c0 + cl) * S + P * j : 0;
     float* st = p.state + (int64_t)slot * p.C * S + own;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < P / 4; ++i) {
             const int64_t at = q * S + 4 * i;
             float2 t[2];
             load4(p.A_log + own + at, t);
@@ -129,15 +167,16 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
             h[q][2 * i] = make_float2(u.x, u.y), h[q][2 * i + 1] = make_float2(u.z, u.w);
         }
     __syncthreads();
-    for (int t0 = bos, buf = 0; t0 < eos; t0 += TT, buf ^= 1) {
-        copy_wait<0>();
+    for (int i = 0, t0 = bos; t0 < eos; ++i, t0 += TT) {
+        const int buf = i % ST, half = i % (ST - 1);
+        copy_wait<ST - 2>();
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
             const int tt = row0 + r * RS;
             if (tt < TT) {
                 float2 xv[VN / 2], dv[VN / 2];
                 unpack2(sm.x[buf][tt][ch], xv);
-                unpack2(sm.dt[tt][ch], dv);
+                unpack2(sm.dt[half][tt][ch], dv);
                 float4* to = reinterpret_cast<float4*>(&sm.d[tt][col + (col / 16) * 2]);
 #pragma unroll
                 for (int e = 0; e < VN / 2; ++e) {
@@ -152,70 +191,99 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
             const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
             if (which < 2) {
                 float f[VN];
-                unpack(sm.bc[v], f);
+                unpack(sm.bc[half][v], f);
                 float4* to = reinterpret_cast<float4*>(&sm.b[which][w / BCH][(w % BCH) * VN]);
 #pragma unroll
                 for (int e = 0; e < VN; e += 4) to[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
             }
         }
         __syncthreads();
-        copy(t0 + TT, buf ^ 1);
+        copy(i + ST - 1);
         const int len = min(TT, eos - t0);
         float2* dp = &sm.d[0][cl + (cl / 16) * 2];
-        auto token = [&](int tt, float (&s)[Q]) {
-            float2 d[Q];
+        if constexpr (WIDE) {
+            auto token = [&](int tt, float (&s)[Q]) {
+                float2 d[Q];
 #pragma unroll
-            for (int q = 0; q < Q; q += 2) {
-                const float4 u = *reinterpret_cast<const float4*>(dp + tt * F::ROW + q);
-                d[q] = make_float2(u.x, u.y), d[q + 1] = make_float2(u.z, u.w);
-            }
-            const float4* b4 = reinterpret_cast<const float4*>(&sm.b[0][tt][8 * j]);
-            const float4* c4 = reinterpret_cast<const float4*>(&sm.b[1][tt][8 * j]);
-            float2 acc[Q];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 b = b4[k], c = c4[k];
-                const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
-                const float2 k0 = make_float2(c.x, c.y), k1 = make_float2(c.z, c.w);
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    advance(h[q][2 * k], A2[q][2 * k], both(d[q].x), both(d[q].y), b0);
-                    advance(h[q][2 * k + 1], A2[q][2 * k + 1], both(d[q].x), both(d[q].y), b1);
-                    acc[q] = k ? __ffma2_rn(h[q][2 * k], k0, acc[q]) : __fmul2_rn(h[q][0], k0);
-                    acc[q] = __ffma2_rn(h[q][2 * k + 1], k1, acc[q]);
+                for (int q = 0; q < Q; q += 2) {
+                    const float4 u = *reinterpret_cast<const float4*>(dp + tt * F::ROW + q);
+                    d[q] = make_float2(u.x, u.y), d[q + 1] = make_float2(u.z, u.w);
                 }
-            }
+                const float4* b4 = reinterpret_cast<const float4*>(&sm.b[0][tt][8 * j]);
+                const float4* c4 = reinterpret_cast<const float4*>(&sm.b[1][tt][8 * j]);
+                float2 acc[Q];
 #pragma unroll
-            for (int q = 0; q < Q; ++q) s[q] = __fadd_rn(acc[q].x, acc[q].y);
-        };
-        auto leave = [&](int tt, const float (&s)[Q]) {  // only this channel's lanes read its d, and they have
+                for (int k = 0; k < 2; ++k) {
+                    const float4 b = b4[k], c = c4[k];
+                    const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
+                    const float2 k0 = make_float2(c.x, c.y), k1 = make_float2(c.z, c.w);
 #pragma unroll
-            for (int q = 0; q < Q; ++q) dp[tt * F::ROW + q].x = s[q];
-        };
-        if (len == TT) {
+                    for (int q = 0; q < Q; ++q) {
+                        advance(h[q][2 * k], A2[q][2 * k], both(d[q].x), both(d[q].y), b0);
+                        advance(h[q][2 * k + 1], A2[q][2 * k + 1], both(d[q].x), both(d[q].y), b1);
+                        acc[q] = k ? __ffma2_rn(h[q][2 * k], k0, acc[q]) : __fmul2_rn(h[q][0], k0);
+                        acc[q] = __ffma2_rn(h[q][2 * k + 1], k1, acc[q]);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < Q; ++q) s[q] = __fadd_rn(acc[q].x, acc[q].y);
+            };
+            auto leave = [&](int tt, const float (&s)[Q]) {  // only this channel's lanes read its d, and they have
+#pragma unroll
+                for (int q = 0; q < Q; ++q) dp[tt * F::ROW + q].x = s[q];
+            };
+            if (len == TT) {
 #pragma unroll (L == 2 ? 2 : 1)
-            for (int tt = 0; tt < TT; tt += L) {
-                float s[Q][L], out[Q];
+                for (int tt = 0; tt < TT; tt += L) {
+                    float s[Q][L], out[Q];
 #pragma unroll
-                for (int k = 0; k < L; ++k) {
-                    float one[Q];
-                    token(tt + k, one);
+                    for (int k = 0; k < L; ++k) {
+                        float one[Q];
+                        token(tt + k, one);
 #pragma unroll
-                    for (int q = 0; q < Q; ++q) s[q][k] = one[q];
+                        for (int q = 0; q < Q; ++q) s[q][k] = one[q];
+                    }
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) out[q] = scatter_sum<L>(s[q], j);
+                    leave(tt + j, out);
                 }
+            } else {
+                for (int tt = 0; tt < len; ++tt) {
+                    float s[Q];
+                    token(tt, s);
 #pragma unroll
-                for (int q = 0; q < Q; ++q) out[q] = scatter_sum<L>(s[q], j);
-                leave(tt + j, out);
+                    for (int q = 0; q < Q; ++q)
+#pragma unroll
+                        for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
+                    if (j == 0) leave(tt, s);
+                }
             }
         } else {
-            for (int tt = 0; tt < len; ++tt) {
-                float s[Q];
-                token(tt, s);
+            auto token = [&](int tt) {
+                const float2 d = dp[tt * F::ROW];
+                const float4 b = *reinterpret_cast<const float4*>(&sm.b[0][tt][4 * j]), c = *reinterpret_cast<const float4*>(&sm.b[1][tt][4 * j]);
+                const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+                advance(h[0][0], A2[0][0], both(d.x), both(d.y), make_float2(b.x, b.y));
+                advance(h[0][1], A2[0][1], both(d.x), both(d.y), make_float2(b.z, b.w));
+                return sum_states4<L>(h[0], cc, j);
+            };
+            constexpr int U = 8;  // tokens whose loads and exponentials run ahead of the recurrence
+            if (len == TT) {
+#pragma unroll 1
+                for (int tt = 0; tt < TT; tt += U) {
+                    float s[U];
 #pragma unroll
-                for (int q = 0; q < Q; ++q)
+                    for (int k = 0; k < U; ++k) s[k] = token(tt + k);
+                    if (j == 1) {
 #pragma unroll
-                    for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
-                if (j == 0) leave(tt, s);
+                        for (int k = 0; k < U; ++k) dp[(tt + k) * F::ROW].x = s[k];
+                    }
+                }
+            } else {
+                for (int tt = 0; tt < len; ++tt) {
+                    const float s = token(tt);
+                    if (j == 1) dp[tt * F::ROW].x = s;
+                }
             }
         }
         __syncthreads();
@@ -245,7 +313,7 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < P / 4; ++i)
                 *reinterpret_cast<float4*>(st + q * S + 4 * i) = make_float4(h[q][2 * i].x, h[q][2 * i].y, h[q][2 * i + 1].x, h[q][2 * i + 1].y);
     }
 }
@@ -371,11 +439,20 @@ gdn_status by_states(int S, cudaStream_t s, Params& p) {
     }
     return GDN_ERR_UNSUPPORTED;
 }
-template <typename T, int S>
-struct FwdK {
-    static constexpr int cb = FwdTile<T, S>::CB;
-    static void go(unsigned blocks, cudaStream_t s, const Params& p) { scan_fwd_kernel<T, S><<<blocks * p.N, FwdTile<T, S>::NT, 0, s>>>(p); }
+template <typename T, int S, bool WIDE>
+struct FwdOf {
+    using F = FwdTile<T, S, WIDE>;
+    static constexpr int cb = F::CB;
+    static void go(unsigned blocks, cudaStream_t s, const Params& p) {
+        Params q = p;
+        q.ranked = p.N > 1 && p.N <= kRanked && (long long)blocks * p.N > (long long)kSMs * F::MINB;
+        scan_fwd_kernel<T, S, WIDE><<<blocks * p.N, F::NT, 0, s>>>(q);
+    }
 };
+template <typename T, int S>
+using FwdK = FwdOf<T, S, true>;
+template <typename T, int S>
+using FwdNarrowK = FwdOf<T, S, false>;
 template <typename T, int S>
 struct UpdK {
     static constexpr int cb = 128 / (S / 4);
@@ -405,8 +482,11 @@ extern "C" gdn_status gdn_selective_scan_fwd(const gdn_scan_shape* shape, const 
     if (st != GDN_OK) return st;
     p.cu = cu_seqlens, p.has_init = has_initial_state;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return shape->dtype == GDN_BF16 ? by_states<FwdK, __nv_bfloat16>(shape->S, s, p)
-                                    : by_states<FwdK, float>(shape->S, s, p);
+    // Narrow below two wide CTAs an SM: see FwdTile.
+    const bool narrow = (int64_t)p.N * p.C * shape->S < (int64_t)kSMs * 2 * 1024;
+    if (shape->dtype == GDN_BF16)
+        return narrow ? by_states<FwdNarrowK, __nv_bfloat16>(shape->S, s, p) : by_states<FwdK, __nv_bfloat16>(shape->S, s, p);
+    return narrow ? by_states<FwdNarrowK, float>(shape->S, s, p) : by_states<FwdK, float>(shape->S, s, p);
 }
 
 extern "C" gdn_status gdn_selective_scan_update(const gdn_scan_shape* shape, const void* x, const void* dt,

@@ -81,6 +81,7 @@ struct Params {
     int num_slots;
     const int32_t* has_init;
     void* y;
+    int ranked;  // prompts: take the sequences in order of length
 };
 
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
