@@ -148,17 +148,30 @@ def test_bits_do_not_depend_on_the_batch_or_on_how_tokens_arrive(dtype, S, C):
     assert torch.equal(bits(st[2]), bits(pool[2]))
 
 
-def test_many_sequences_and_wide_channels_agree_with_a_sequence_alone():
-    # large enough for every way the kernels split their work
-    lens = [257] * 40
-    c = Case(lens, 2056, 1, 16, torch.bfloat16, 13)
+@pytest.mark.parametrize("dtype,S,G,C,gate", [(torch.bfloat16, 16, 1, 2056, True), (torch.float32, 16, 2, 592, False), (torch.bfloat16, 8, 3, 1056, False),
+                                              (torch.float32, 8, 1, 1032, True), (torch.bfloat16, 32, 1, 264, True),
+                                              (torch.float32, 32, 2, 272, False), (torch.bfloat16, 64, 1, 136, False), (torch.float32, 64, 2, 144, True)])
+def test_large_batches_agree_with_a_sequence_alone(dtype, S, G, C, gate):
+    # batches that take the form with more states a lane (the first also the order by length)
+    lens = [(37 * i) % 90 for i in range(40)]
+    c = Case(lens, C, G, S, dtype, 13, gate=gate, D=gate, bias=not gate)
     pool = c.h0.clone()
     y = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, state=pool, **c.args())
-    for n in (0, 39):
-        t = slice(n * 257, n * 257 + 257)
+    for n in range(40):
+        t = slice(c.cu_list[n], c.cu_list[n + 1])
         st = c.h0[n:n + 1].clone()
-        alone = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu[:2].contiguous(), state=st, **c.args(t))
-        assert torch.equal(bits(alone), bits(y[t])) and torch.equal(bits(st[0]), bits(pool[n]))
+        cu = torch.tensor([0, lens[n]], dtype=torch.int32, device=DEV)
+        alone = gdn.gdn_selective_scan_fwd(cu_seqlens=cu, state=st, **c.args(t))
+        assert torch.equal(bits(alone), bits(y[t])) and torch.equal(bits(st[0]), bits(pool[n])), n
+
+
+@pytest.mark.parametrize("dtype,S,B,C", [(torch.bfloat16, 16, 300, 4160), (torch.float32, 8, 150, 4160), (torch.float32, 64, 37, 1000)])
+def test_large_updates_agree_with_prompts_of_one_token(dtype, S, B, C):
+    c = Case([1] * B, C, 1, S, dtype, 24)
+    a, b = c.h0.clone(), c.h0.clone()
+    y = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, state=a, **c.args())
+    z = gdn.gdn_selective_scan_update(state=b, **c.args())
+    assert torch.equal(bits(y), bits(z)) and torch.equal(bits(a), bits(b))
 
 
 @pytest.mark.parametrize("dtype,S,G,C,gate", GRID)
