@@ -246,10 +246,10 @@ def test_backward_vs_oracle(dtype, S, G, C, gate, states):
     assert (g["dz"] is None) == (not gate) and (g["dD"] is None) == (c.D is None) and (g["d_init_state"] is None) == (not states)
 
 
-@pytest.mark.parametrize("dtype,S,G,C", [(torch.float32, 8, 64, 512), (torch.bfloat16, 16, 56, 448)])
-def test_backward_of_a_batch_with_many_ctas(dtype, S, G, C):
+@pytest.mark.parametrize("dtype,S,G,C,lens", [(torch.float32, 8, 64, 512, [390, 0, 150, 64, 1]), (torch.bfloat16, 16, 56, 448, [390, 0, 150, 64, 1]),
+                                              (torch.float32, 8, 500, 4000, [270, 0, 130])])
+def test_backward_of_a_batch_with_many_ctas(dtype, S, G, C, lens):
     # enough channel blocks and tokens for the longer segments, sequences of several of them
-    lens = [390, 0, 150, 64, 1]
     c = Case(lens, C, G, S, dtype, 23, slow=True)
     g = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args())
     want = ref.selective_scan_bwd(cu=c.cu_list, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args())
