@@ -330,12 +330,32 @@ __global__ void __launch_bounds__(128) scan_update_kernel(const __grid_constant_
     constexpr int L = S / 4, CB = 128 / L, RW = L < 4 ? L : 4;
     constexpr uint32_t all = 0xffffffffu;
     __shared__ float4 bc[kUpdRows][2][S / 4];
-    __shared__ int slots[kUpdRows];
     const int nb = p.bpg * p.G, blk = blockIdx.x % nb, b0 = blockIdx.x / nb * rows, nr = min(rows, p.N - b0);
     const int g = blk / p.bpg, j = threadIdx.x % L, jr = j % RW;
     const int cg = (blk % p.bpg) * CB + threadIdx.x / L;
     const bool ok = cg < p.CG;
     const int c = g * p.CG + (ok ? cg : 0);
+    float* st = p.state + (int64_t)c * S + 4 * j;
+    const int64_t CS = (int64_t)p.C * S;
+    float4 s[RW];
+    int slot[RW];
+    float x, dt, z;
+    auto load = [&](int r0) {
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+            const int row = b0 + r0 + r;
+            slot[r] = r0 + r < nr ? (p.idx ? __ldg(p.idx + row) : row) : -1;
+            if (slot[r] >= p.num_slots) slot[r] = -1;
+        }
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+            s[r] = slot[r] >= 0 ? *reinterpret_cast<const float4*>(st + slot[r] * CS) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const int64_t row = b0 + min(r0 + jr, nr - 1);
+        x = load1(static_cast<const T*>(p.x) + row * p.ldx + c);
+        dt = load1(static_cast<const T*>(p.dt) + row * p.lddt + c);
+        z = p.z ? load1(static_cast<const T*>(p.z) + row * p.ldz + c) : 0.f;
+    };
+    load(0);
     for (int i = threadIdx.x; i < nr * (S / 2); i += 128) {
         const int r = i / (S / 2), which = i % (S / 2) / (S / 4), q = i % (S / 4);
         const int64_t row = b0 + r;
@@ -343,40 +363,21 @@ __global__ void __launch_bounds__(128) scan_update_kernel(const __grid_constant_
         load4((which ? static_cast<const T*>(p.Cm) + row * p.ldC : static_cast<const T*>(p.B) + row * p.ldB) + (int64_t)g * S + 4 * q, v);
         bc[r][which][q] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     }
-    for (int i = threadIdx.x; i < nr; i += 128) {
-        const int slot = p.idx ? __ldg(p.idx + b0 + i) : b0 + i;
-        slots[i] = slot < p.num_slots ? slot : -1;
-    }
     float2 A2[2];
     load4(p.A_log + (int64_t)c * S + 4 * j, A2);
     A2[0] = make_float2(a_log2(A2[0].x), a_log2(A2[0].y)), A2[1] = make_float2(a_log2(A2[1].x), a_log2(A2[1].y));
     const float bias = p.bias ? __ldg(p.bias + c) : 0.f, D = p.D ? __ldg(p.D + c) : 0.f;
-    float* st = p.state + (int64_t)c * S + 4 * j;
-    const int64_t CS = (int64_t)p.C * S;
     __syncthreads();
-
-    float4 s[RW];
-    float x, dt, z;
-    auto load = [&](int r0) {
-#pragma unroll
-        for (int r = 0; r < RW; ++r) {
-            const int slot = r0 + r < nr ? slots[r0 + r] : -1;
-            s[r] = slot >= 0 ? *reinterpret_cast<const float4*>(st + slot * CS) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        const int64_t row = b0 + min(r0 + jr, nr - 1);
-        x = load1(static_cast<const T*>(p.x) + row * p.ldx + c);
-        dt = load1(static_cast<const T*>(p.dt) + row * p.lddt + c);
-        z = p.z ? load1(static_cast<const T*>(p.z) + row * p.ldz + c) : 0.f;
-    };
-    load(0);
     for (int r0 = 0; r0 < nr; r0 += RW) {
         float2 h[RW][2];
+        int own[RW];
 #pragma unroll
-        for (int r = 0; r < RW; ++r) h[r][0] = make_float2(s[r].x, s[r].y), h[r][1] = make_float2(s[r].z, s[r].w);
+        for (int r = 0; r < RW; ++r) h[r][0] = make_float2(s[r].x, s[r].y), h[r][1] = make_float2(s[r].z, s[r].w), own[r] = slot[r];
         const float xv = x, zv = z;
         const float d = step_of(both(dt), both(bias), p.softplus).x, dx = __fmul_rn(d, xv);
         if (r0 + RW < nr) load(r0 + RW);
         float mine = 0.f;
+        int mine_slot = -1;
 #pragma unroll
         for (int r = 0; r < RW; ++r) {
             const int at = min(r0 + r, nr - 1), from = (threadIdx.x & 31 & ~(L - 1)) + r;
@@ -386,14 +387,13 @@ __global__ void __launch_bounds__(128) scan_update_kernel(const __grid_constant_
             advance(h[r][0], A2[0], both(dr), both(dxr), make_float2(b.x, b.y));
             advance(h[r][1], A2[1], both(dr), both(dxr), make_float2(b.z, b.w));
             const float t = __shfl_sync(all, sum_states4<L>(h[r], cc, j), (threadIdx.x & 31 & ~(L - 1)) + 1);
-            if (jr == r) mine = t;
-            if (ok && r0 + r < nr && slots[at] >= 0)
-                *reinterpret_cast<float4*>(st + slots[at] * CS) = make_float4(h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y);
+            if (jr == r) mine = t, mine_slot = own[r];
+            if (ok && own[r] >= 0) *reinterpret_cast<float4*>(st + own[r] * CS) = make_float4(h[r][0].x, h[r][0].y, h[r][1].x, h[r][1].y);
         }
         float y = __fmaf_rn(D, xv, mine);
         float2 sig;
         if (p.z) y = __fmul_rn(y, silu2(both(zv), sig).x);
-        if (ok && j < RW && r0 + j < nr && slots[r0 + j] >= 0) store1(static_cast<T*>(p.y) + (int64_t)(b0 + r0 + j) * p.C + c, y);
+        if (ok && j < RW && mine_slot >= 0) store1(static_cast<T*>(p.y) + (int64_t)(b0 + r0 + j) * p.C + c, y);
     }
 }
 
