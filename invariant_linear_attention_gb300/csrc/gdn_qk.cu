@@ -69,7 +69,8 @@ __device__ __forceinline__ uint4 pack_half(const float2* v) {
 }
 __device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
-// The angles of a unit's VN pairs (1 and 0 where it is not rotated); back: the negative ones.
+// The angles of a unit's VN pairs; back: the negative ones.  A unit that is not rotated is not turned
+// by 1 and 0 either: that would spread an infinity to its neighbour.
 template <int VN>
 struct Angles {
     float2 c[VN / 2], s[VN / 2], ns[VN / 2];
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
                         v[e] = __fmul2_rn(v[e], r);
                         if constexpr (HASW) v[e] = __fmul2_rn(v[e], w[e]);
                     }
-                    an.template turn<INTER>(v);
+                    if (un.rot) an.template turn<INTER>(v);
                     if (h < H && un.has0) st16_stream(dst + h * p.d + un.e0, pack_half<VN>(v));
                     if (h < H && un.has1) st16_stream(dst + h * p.d + un.e1, pack_half<VN>(v + VN / 2));
                 }
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
                     unpack_unit<VN>(ra[i], rb[i], v);
                     unpack_unit<VN>(ga[i], gb[i], g);
                     const float r = rsqrtf(__fmaf_rn(group_sum(dot<VN>(v, v), p.lpr), p.c, p.eps));
-                    an.template turn<INTER>(g);
+                    if (un.rot) an.template turn<INTER>(g);
                     if constexpr (HASW) {
 #pragma unroll
                         for (int e = 0; e < VN; ++e) {

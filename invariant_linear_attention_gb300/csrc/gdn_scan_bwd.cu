@@ -283,14 +283,16 @@ __global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan
 }
 
 // ---------------------------------------------------------------- 2. join
-// A thread joins 4 states of one channel along one sequence: forwards (blockIdx.z 0) the start
+// A thread joins 4 states of one channel along one sequence: forwards (blockIdx.y 0) the start
 // states, backwards (1) the end G's.  The loads do not depend on the chain and run ahead of it.
 __global__ void __launch_bounds__(128) scan_join_kernel(const __grid_constant__ BwdParams q, int S) {
     const Params& p = q.f;
-    const int64_t CS = (int64_t)p.C * S, i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+    const int64_t CS = (int64_t)p.C * S;
+    const int blocks = (int)((CS / 4 + blockDim.x - 1) / blockDim.x), n = blockIdx.x / blocks;
+    const int64_t i = ((int64_t)(blockIdx.x % blocks) * blockDim.x + threadIdx.x) * 4;
     if (i >= CS) return;
-    const int n = blockIdx.y, c = (int)(i / S), len = q.m * kTile;
-    const bool back = blockIdx.z;
+    const int c = (int)(i / S), len = q.m * kTile;
+    const bool back = blockIdx.y;
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
     const int segs = (eos - bos + len - 1) / len;
@@ -678,7 +680,8 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     const Params& p = q.f;
     const long long ctas = segs * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S / 4 + 15) / 16;
     const long long par = ((long long)p.C * (S + 2) / 4 + 15) / 16;
-    if (ctas >= (1LL << 31) || bc + par >= (1LL << 31) || p.N > 65535) return GDN_ERR_UNSUPPORTED;
+    const long long joins = ((long long)p.C * S / 4 + 127) / 128 * p.N;
+    if (ctas >= (1LL << 31) || bc + par >= (1LL << 31) || joins >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
     constexpr size_t smem = sizeof(GradMem<T, S>);
     if constexpr (smem > 48 * 1024) {
         if (cudaFuncSetAttribute(scan_grad_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -686,7 +689,7 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     }
     if (p.N > 0) {
         if (p.T > 0) scan_local_kernel<T, S><<<(unsigned)ctas, Geo<T, S, 4>::NT, 0, s>>>(q);
-        scan_join_kernel<<<dim3((unsigned)(((int64_t)p.C * S / 4 + 127) / 128), (unsigned)p.N, 2), 128, 0, s>>>(q, S);
+        scan_join_kernel<<<dim3((unsigned)joins, 2), 128, 0, s>>>(q, S);
         if (p.T > 0) scan_grad_kernel<T, S><<<(unsigned)ctas, Geo<T, S, 2>::NT, smem, s>>>(q);
     }
     scan_sums_kernel<T, S><<<(unsigned)(bc + par), 256, 0, s>>>(q, (unsigned)bc, p.T > 0 ? (int)segs : 0);

@@ -200,6 +200,19 @@ def test_qk_with_one_weight():
                 assert np.abs(to_np(dw) - want_w).max() <= 1e-4 * np.abs(want_w).max()
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_qk_infinity_stays_in_its_pair(inter):
+    # r = 0 in a row with an infinity: its finite values become 0, the infinity (and, rotated, its pair) NaN
+    x = torch.randn(2, 1, 32, generator=torch.Generator().manual_seed(1)).to(DEV)
+    x[0, 0, 20] = float("inf")  # not rotated
+    x[1, 0, 3] = float("inf")   # rotated: pairs (3, 11) or (2, 3)
+    th = torch.randn(2, 8, generator=torch.Generator().manual_seed(2)).to(DEV)
+    out, _ = gdn.gdn_qk_norm_rope(x, x, th.cos(), th.sin(), interleaved=inter)
+    assert torch.isnan(out[0, 0]).nonzero().flatten().tolist() == [20]
+    assert torch.isnan(out[1, 0]).nonzero().flatten().tolist() == ([2, 3] if inter else [3, 11])
+    assert torch.all(out[~torch.isnan(out)] == 0)
+
+
 def test_qk_positions_default_to_rows_and_outputs_in_place():
     c = QkCase(torch.float32, 50, 2, 2, 32, 32, "l2")
     q, k = c.q.contiguous(), c.k.contiguous()
@@ -219,6 +232,59 @@ def test_qk_positions_default_to_rows_and_outputs_in_place():
     w = torch.ones(32, device=DEV)
     g = gdn.gdn_qk_norm_rope_bwd(none, none, c.cos, c.sin, none, none, q_weight=w, k_weight=w)
     assert qo.shape == (0, 2, 32) and torch.all(g["dq_weight"] == 0) and torch.all(g["dk_weight"] == 0)
+
+
+# ---------------------------------------------------------------- offsets past 2^31 values
+
+def test_offsets_past_32_bits():
+    """A batch whose last sequence lies behind 2^31 values: its bits alone and in place, for the
+    conv's gradient, the q/k norm and its gradient, and the scan with its gradient."""
+    C, L, tail = 8192, 262300, 70
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(5)
+    rn = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    T = L + tail
+    assert L * C > 2 ** 31
+
+    def big(width):
+        t = torch.zeros(T, width, dtype=torch.bfloat16, device=DEV)
+        t[L:] = rn(tail, width).to(torch.bfloat16)
+        return t
+
+    cu = torch.tensor([0, L, T], dtype=torch.int32, device=DEV)
+    one = torch.tensor([0, tail], dtype=torch.int32, device=DEV)
+    x, dy = big(C), big(C)
+    w = rn(C, 4)
+    g, a = gdn.gdn_causal_conv1d_bwd(x, w, cu, dy), gdn.gdn_causal_conv1d_bwd(x[L:], w, one, dy[L:])
+    assert torch.equal(bits(g["dx"][L:]), bits(a["dx"])) and torch.all(g["dx"][:L - 3] == 0)
+    del g, a
+    q = x.unflatten(1, (64, 128))
+    th = rn(97, 64)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) % 97
+    kw = dict(cos=th.cos(), sin=th.sin())
+    big_q, _ = gdn.gdn_qk_norm_rope(q, q[:, :1], positions=pos, **kw)
+    sub_q, _ = gdn.gdn_qk_norm_rope(q[L:], q[L:, :1], positions=pos[L:], **kw)
+    assert torch.equal(bits(big_q[L:]), bits(sub_q)) and torch.all(big_q[:L] == 0)
+    del big_q, sub_q
+    d = dy.unflatten(1, (64, 128))
+    big_g = gdn.gdn_qk_norm_rope_bwd(q, q[:, :1], d_q_out=d, d_k_out=d[:, :1].contiguous(), positions=pos, **kw)
+    sub_g = gdn.gdn_qk_norm_rope_bwd(q[L:], q[L:, :1], d_q_out=d[L:], d_k_out=d[L:, :1].contiguous(), positions=pos[L:], **kw)
+    assert torch.equal(bits(big_g["dq"][L:]), bits(sub_g["dq"])) and torch.equal(bits(big_g["dk"][L:]), bits(sub_g["dk"]))
+    del big_g, sub_g
+    B = big(8).unflatten(1, (1, 8))
+    args = lambda s: dict(x=x[s], dt=dy[s], A_log=A_log, B=B[s], C=B[s], dt_bias=bias)  # noqa: E731
+    A_log, bias = rn(C, 8) * 0.2, rn(C) - 3
+    whole, last = slice(None), slice(L, T)
+    y, ya = gdn.gdn_selective_scan_fwd(cu_seqlens=cu, **args(whole)), gdn.gdn_selective_scan_fwd(cu_seqlens=one, **args(last))
+    assert torch.equal(bits(y[L:]), bits(ya))
+    del y, ya
+    g = gdn.gdn_selective_scan_bwd(cu_seqlens=cu, d_out=dy, need_d_init_state=False, **args(whole))
+    a = gdn.gdn_selective_scan_bwd(cu_seqlens=one, d_out=dy[L:], need_d_init_state=False, **args(last))
+    # the segments differ between the two batches: the last sequence's rows agree up to their rounding
+    # and the difference of the segments' decays (a product of at most 128 steps: 128 * 4 u), in the row's largest value
+    for k in ("dx", "ddt", "dB", "dC"):
+        p, q_ = to_np(g[k][L:]).reshape(tail, -1), to_np(a[k]).reshape(tail, -1)
+        assert np.all(np.abs(p - q_) <= 2 * BF16_ROUND * np.abs(q_) + 2e-4 * np.abs(q_).max(1, keepdims=True)), k
 
 
 # ---------------------------------------------------------------- together
