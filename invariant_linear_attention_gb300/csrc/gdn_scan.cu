@@ -36,23 +36,16 @@ __device__ __forceinline__ float scatter_sum(float (&s)[L], int j) {
 //      back only x, dt and z chunks that it copied itself);
 //   3. the walk: the recurrence over the tile's tokens, sum_s h C left where d was;
 //   4. D x, gate and 16-byte stores of y.
-// A lane of the narrow form holds 4 states of one channel: four times the threads for a batch that
-// leaves most of the GPU idle otherwise, the same additions.  CTAs of 64 channels and 16 states, bf16,
-// us per 1000 tokens at 1 / 2 / 3 / 8 an SM: wide 160 / 166 / 207 / 339, narrow 98 / 157 / 240 / 615.
-//
-// What bounds the wide form: the step alone (per two states 4 packed products or fmas and 2
+// What bounds it: the step alone (per two states 4 packed products or fmas and 2
 // exponentials, in registers) runs at 6.8 T states/s on this GPU, of 10 T that the
 // exponentials and 9.6 T that the fma pipe would allow; with its loads, sums and the work per (token, channel)
 // it reaches 3.7 T.  Shared memory is the next limit: a load delivers 128 bytes a cycle into
 // registers whether lanes share an address or not, and B and C take 64 bytes a lane and token.
 // Four channels a lane halve that and lose more in the registers they take (2.9 T); one channel a lane: 3.2 T.
-template <typename T, int S, bool WIDE>
+template <typename T, int S>
 struct FwdTile {
-    static constexpr int P = WIDE ? 8 : 4, Q = WIDE ? 2 : 1, L = S / P;  // states and channels of a lane, lanes of a channel
-    static constexpr int CB = WIDE ? (S == 8 ? 128 : S == 64 ? 32 : 64) : (S <= 16 ? 64 : 1024 / S);
-    static constexpr int NT = CB * L / Q, VN = V16<T>::n;
-    // A narrow walk is bound by the latency of a tile's phases: longer tiles where shared memory allows.
-    static constexpr int TT = WIDE ? (S == 8 ? 8 : 16) : (VN == 8 ? 32 : 16);
+    static constexpr int L = S / 8, Q = 2, CB = S == 8 ? 128 : S == 64 ? 32 : 64, NT = CB * L / Q, VN = V16<T>::n;
+    static constexpr int TT = S == 8 ? 8 : 16;
     static constexpr int CH = CB / VN;                        // 16-byte chunks of a row
     static constexpr int NV = (TT * CH + NT - 1) / NT;        // of x (dt, z) per thread and tile
     static constexpr int RS = NT / CH;                        // tokens between a thread's chunks
@@ -64,9 +57,8 @@ struct FwdTile {
     static constexpr int ROW = CB + (CB / 16) * 2;            // float2s per token
     alignas(16) float2 d[TT][ROW];
     alignas(16) float b[2][TT][S];
-    static constexpr int ST = 2;                              // tiles of x and z in flight or in use
-    uint4 x[ST][TT][CH], z[ST][TT][CH], dt[ST - 1][TT][CH];
-    uint4 bc[ST - 1][2 * TT * BCH];
+    uint4 x[2][TT][CH], z[2][TT][CH], dt[TT][CH];
+    uint4 bc[2 * TT * BCH];
     alignas(16) float D[CB];
     alignas(16) float bias[CB];
     static_assert(NT % CH == 0, "a thread keeps its columns");
@@ -94,10 +86,10 @@ __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
     return found;
 }
 
-template <typename T, int S, bool WIDE>
-__global__ void __launch_bounds__(FwdTile<T, S, WIDE>::NT, FwdTile<T, S, WIDE>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
-    using F = FwdTile<T, S, WIDE>;
-    constexpr int P = F::P, L = F::L, Q = F::Q, NT = F::NT, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB, ST = F::ST;
+template <typename T, int S>
+__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
+    using F = FwdTile<T, S>;
+    constexpr int L = F::L, Q = F::Q, NT = F::NT, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB;
     __shared__ F sm;
     const int tid = threadIdx.x;
     const int nb = p.bpg * p.G;
@@ -125,14 +117,14 @@ __global__ void __launch_bounds__(FwdTile<T, S, WIDE>::NT, FwdTile<T, S, WIDE>::
     // Chunks behind the sequence or the group's channels are not copied: what the walk makes of
     // the shared memory's old contents there is never stored.
     auto copy = [&](int i) {  // tile i
-        const int t0 = bos + i * TT, full = i % ST, half = i % (ST - 1);
+        const int t0 = bos + i * TT, buf = i & 1;
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
             const int tt = row0 + r * RS;
             if (tt < TT && t0 + tt < eos && cok) {
-                copy16_async(&sm.x[full][tt][ch], x + r * RS * p.ldx);
-                copy16_async(&sm.dt[half][tt][ch], dt + r * RS * p.lddt);
-                if (gate) copy16_async(&sm.z[full][tt][ch], z + r * RS * p.ldz);
+                copy16_async(&sm.x[buf][tt][ch], x + r * RS * p.ldx);
+                copy16_async(&sm.dt[tt][ch], dt + r * RS * p.lddt);
+                if (gate) copy16_async(&sm.z[buf][tt][ch], z + r * RS * p.ldz);
             }
         }
         x += TT * p.ldx, dt += TT * p.lddt, z += TT * p.ldz;
@@ -140,24 +132,24 @@ __global__ void __launch_bounds__(FwdTile<T, S, WIDE>::NT, FwdTile<T, S, WIDE>::
         for (int r = 0; r < NB; ++r) {
             const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
             const int64_t t = t0 + w / BCH;
-            if (which < 2 && t < eos) copy16_async(&sm.bc[half][v], which ? Cg + t * p.ldC + (w % BCH) * VN : Bg + t * p.ldB + (w % BCH) * VN);
+            if (which < 2 && t < eos) copy16_async(&sm.bc[v], which ? Cg + t * p.ldC + (w % BCH) * VN : Bg + t * p.ldB + (w % BCH) * VN);
         }
         copy_commit();
     };
-    for (int i = 0; i < ST - 1; ++i) copy(i);
+    copy(0);
 
     for (int c = tid; c < CB; c += NT) {
         const bool in = cg0 + c < p.CG;
         sm.D[c] = in && p.D ? __ldg(p.D + c0 + c) : 0.f;
         sm.bias[c] = in && p.bias ? __ldg(p.bias + c0 + c) : 0.f;
     }
-    float2 A2[Q][P / 2], h[Q][P / 2];
-    const int64_t own = ok ? (int64_t)(c0 + cl) * S + P * j : 0;
+    float2 A2[Q][4], h[Q][4];
+    const int64_t own = ok ? (int64_t)(c0 + cl) * S + 8 * j : 0;
     float* st = p.state + (int64_t)slot * p.C * S + own;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int i = 0; i < P / 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const int64_t at = q * S + 4 * i;
             float2 t[2];
             load4(p.A_log + own + at, t);
@@ -168,15 +160,15 @@ __global__ void __launch_bounds__(FwdTile<T, S, WIDE>::NT, FwdTile<T, S, WIDE>::
         }
     __syncthreads();
     for (int i = 0, t0 = bos; t0 < eos; ++i, t0 += TT) {
-        const int buf = i % ST, half = i % (ST - 1);
-        copy_wait<ST - 2>();
+        const int buf = i & 1;
+        copy_wait<0>();
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
             const int tt = row0 + r * RS;
             if (tt < TT) {
                 float2 xv[VN / 2], dv[VN / 2];
                 unpack2(sm.x[buf][tt][ch], xv);
-                unpack2(sm.dt[half][tt][ch], dv);
+                unpack2(sm.dt[tt][ch], dv);
                 float4* to = reinterpret_cast<float4*>(&sm.d[tt][col + (col / 16) * 2]);
 #pragma unroll
                 for (int e = 0; e < VN / 2; ++e) {
@@ -191,99 +183,70 @@ __global__ void __launch_bounds__(FwdTile<T, S, WIDE>::NT, FwdTile<T, S, WIDE>::
             const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
             if (which < 2) {
                 float f[VN];
-                unpack(sm.bc[half][v], f);
+                unpack(sm.bc[v], f);
                 float4* to = reinterpret_cast<float4*>(&sm.b[which][w / BCH][(w % BCH) * VN]);
 #pragma unroll
                 for (int e = 0; e < VN; e += 4) to[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
             }
         }
         __syncthreads();
-        copy(i + ST - 1);
+        copy(i + 1);
         const int len = min(TT, eos - t0);
         float2* dp = &sm.d[0][cl + (cl / 16) * 2];
-        if constexpr (WIDE) {
-            auto token = [&](int tt, float (&s)[Q]) {
-                float2 d[Q];
+        auto token = [&](int tt, float (&s)[Q]) {
+            float2 d[Q];
 #pragma unroll
-                for (int q = 0; q < Q; q += 2) {
-                    const float4 u = *reinterpret_cast<const float4*>(dp + tt * F::ROW + q);
-                    d[q] = make_float2(u.x, u.y), d[q + 1] = make_float2(u.z, u.w);
-                }
-                const float4* b4 = reinterpret_cast<const float4*>(&sm.b[0][tt][8 * j]);
-                const float4* c4 = reinterpret_cast<const float4*>(&sm.b[1][tt][8 * j]);
-                float2 acc[Q];
+            for (int q = 0; q < Q; q += 2) {
+                const float4 u = *reinterpret_cast<const float4*>(dp + tt * F::ROW + q);
+                d[q] = make_float2(u.x, u.y), d[q + 1] = make_float2(u.z, u.w);
+            }
+            const float4* b4 = reinterpret_cast<const float4*>(&sm.b[0][tt][8 * j]);
+            const float4* c4 = reinterpret_cast<const float4*>(&sm.b[1][tt][8 * j]);
+            float2 acc[Q];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float4 b = b4[k], c = c4[k];
-                    const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
-                    const float2 k0 = make_float2(c.x, c.y), k1 = make_float2(c.z, c.w);
+            for (int k = 0; k < 2; ++k) {
+                const float4 b = b4[k], c = c4[k];
+                const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
+                const float2 k0 = make_float2(c.x, c.y), k1 = make_float2(c.z, c.w);
 #pragma unroll
-                    for (int q = 0; q < Q; ++q) {
-                        advance(h[q][2 * k], A2[q][2 * k], both(d[q].x), both(d[q].y), b0);
-                        advance(h[q][2 * k + 1], A2[q][2 * k + 1], both(d[q].x), both(d[q].y), b1);
-                        acc[q] = k ? __ffma2_rn(h[q][2 * k], k0, acc[q]) : __fmul2_rn(h[q][0], k0);
-                        acc[q] = __ffma2_rn(h[q][2 * k + 1], k1, acc[q]);
-                    }
-                }
-#pragma unroll
-                for (int q = 0; q < Q; ++q) s[q] = __fadd_rn(acc[q].x, acc[q].y);
-            };
-            auto leave = [&](int tt, const float (&s)[Q]) {  // only this channel's lanes read its d, and they have
-#pragma unroll
-                for (int q = 0; q < Q; ++q) dp[tt * F::ROW + q].x = s[q];
-            };
-            if (len == TT) {
-#pragma unroll (L == 2 ? 2 : 1)
-                for (int tt = 0; tt < TT; tt += L) {
-                    float s[Q][L], out[Q];
-#pragma unroll
-                    for (int k = 0; k < L; ++k) {
-                        float one[Q];
-                        token(tt + k, one);
-#pragma unroll
-                        for (int q = 0; q < Q; ++q) s[q][k] = one[q];
-                    }
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) out[q] = scatter_sum<L>(s[q], j);
-                    leave(tt + j, out);
-                }
-            } else {
-                for (int tt = 0; tt < len; ++tt) {
-                    float s[Q];
-                    token(tt, s);
-#pragma unroll
-                    for (int q = 0; q < Q; ++q)
-#pragma unroll
-                        for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
-                    if (j == 0) leave(tt, s);
+                for (int q = 0; q < Q; ++q) {
+                    advance(h[q][2 * k], A2[q][2 * k], both(d[q].x), both(d[q].y), b0);
+                    advance(h[q][2 * k + 1], A2[q][2 * k + 1], both(d[q].x), both(d[q].y), b1);
+                    acc[q] = k ? __ffma2_rn(h[q][2 * k], k0, acc[q]) : __fmul2_rn(h[q][0], k0);
+                    acc[q] = __ffma2_rn(h[q][2 * k + 1], k1, acc[q]);
                 }
             }
+#pragma unroll
+            for (int q = 0; q < Q; ++q) s[q] = __fadd_rn(acc[q].x, acc[q].y);
+        };
+        auto leave = [&](int tt, const float (&s)[Q]) {  // only this channel's lanes read its d, and they have
+#pragma unroll
+            for (int q = 0; q < Q; ++q) dp[tt * F::ROW + q].x = s[q];
+        };
+        if (len == TT) {
+#pragma unroll (L == 2 ? 2 : 1)
+            for (int tt = 0; tt < TT; tt += L) {
+                float s[Q][L], out[Q];
+#pragma unroll
+                for (int k = 0; k < L; ++k) {
+                    float one[Q];
+                    token(tt + k, one);
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) s[q][k] = one[q];
+                }
+#pragma unroll
+                for (int q = 0; q < Q; ++q) out[q] = scatter_sum<L>(s[q], j);
+                leave(tt + j, out);
+            }
         } else {
-            auto token = [&](int tt) {
-                const float2 d = dp[tt * F::ROW];
-                const float4 b = *reinterpret_cast<const float4*>(&sm.b[0][tt][4 * j]), c = *reinterpret_cast<const float4*>(&sm.b[1][tt][4 * j]);
-                const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
-                advance(h[0][0], A2[0][0], both(d.x), both(d.y), make_float2(b.x, b.y));
-                advance(h[0][1], A2[0][1], both(d.x), both(d.y), make_float2(b.z, b.w));
-                return sum_states4<L>(h[0], cc, j);
-            };
-            constexpr int U = 8;  // tokens whose loads and exponentials run ahead of the recurrence
-            if (len == TT) {
-#pragma unroll 1
-                for (int tt = 0; tt < TT; tt += U) {
-                    float s[U];
+            for (int tt = 0; tt < len; ++tt) {
+                float s[Q];
+                token(tt, s);
 #pragma unroll
-                    for (int k = 0; k < U; ++k) s[k] = token(tt + k);
-                    if (j == 1) {
+                for (int q = 0; q < Q; ++q)
 #pragma unroll
-                        for (int k = 0; k < U; ++k) dp[(tt + k) * F::ROW].x = s[k];
-                    }
-                }
-            } else {
-                for (int tt = 0; tt < len; ++tt) {
-                    const float s = token(tt);
-                    if (j == 1) dp[tt * F::ROW].x = s;
-                }
+                    for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
+                if (j == 0) leave(tt, s);
             }
         }
         __syncthreads();
@@ -313,9 +276,209 @@ __global__ void __launch_bounds__(FwdTile<T, S, WIDE>::NT, FwdTile<T, S, WIDE>::
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
-            for (int i = 0; i < P / 4; ++i)
+            for (int i = 0; i < 2; ++i)
                 *reinterpret_cast<float4*>(st + q * S + 4 * i) = make_float4(h[q][2 * i].x, h[q][2 * i].y, h[q][2 * i + 1].x, h[q][2 * i + 1].y);
     }
+}
+
+// Prompts of a small batch, which leaves an SM one CTA at most: what counts is the latency of a
+// token, not the throughput (64 channels, 16 states, bf16: 80 ns a token, the wide form 160; with two
+// CTAs an SM 150 to 167 against 166, hence the rule at the launch).  A walker holds 4 states of one channel (a quarter of the wide form's
+// work, the same additions), and the phases before and after the walk run beside it, on other
+// warps, a tile ahead and a tile behind:
+//   * preparers: d, d x, B and C of tile i + 1 to shared memory;
+//   * walkers: tile i;
+//   * finishers: skip term, gate and stores of tile i - 1.
+// They meet at named barriers: full (tile prepared), free (its d, B, C read), done (its sums
+// written), left (its sums read), one of each per buffer; every side passes each barrier the
+// same number of times.  Preparers and finishers copy their own inputs, asynchronously, two tiles
+// ahead, and read back only chunks that they copied themselves.
+template <typename T, int S>
+struct NarrowTile {
+    static constexpr int L = S / 4, CB = S <= 16 ? 64 : 1024 / S, VN = V16<T>::n, TT = 16;
+    static constexpr int WALK = CB * L, SIDE = 128, NT = WALK + 2 * SIDE;
+    static constexpr int CH = CB / VN, NV = (TT * CH + SIDE - 1) / SIDE, RS = SIDE / CH;
+    static constexpr int BCH = S / VN, NB = (2 * TT * BCH + SIDE - 1) / SIDE;
+    static constexpr int ROW = CB + (CB / 16) * 2;  // as in FwdTile
+    static constexpr int ST = 3;                    // tiles of inputs in flight or in use
+    alignas(16) float2 d[2][TT][ROW];
+    alignas(16) float b[2][2][TT][S];
+    alignas(16) float y[2][TT][CB];
+    uint4 x[ST][TT][CH], dt[ST][TT][CH], bc[ST][2 * TT * BCH];  // preparers'
+    uint4 x2[ST][TT][CH], z[ST][TT][CH];                        // finishers'
+    static_assert(SIDE % CH == 0, "a thread keeps its columns");
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+template <typename T, int S>
+__global__ void __launch_bounds__(NarrowTile<T, S>::NT, 1) scan_fwd_narrow_kernel(const __grid_constant__ Params p) {
+    using F = NarrowTile<T, S>;
+    constexpr int L = F::L, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB, ST = F::ST;
+    constexpr int kFull = 1, kFree = 3, kDone = 5, kLeft = 7, kPair = F::WALK + F::SIDE;
+    extern __shared__ __align__(16) unsigned char raw[];
+    F& sm = *reinterpret_cast<F*>(raw);
+    const int nb = p.bpg * p.G;
+    const int n = blockIdx.x / nb, blk = blockIdx.x % nb;
+    const int g = blk / p.bpg, cg0 = (blk % p.bpg) * CB, c0 = g * p.CG + cg0;
+    int bos, eos;
+    bounds(p.cu, n, p.T, bos, eos);
+    const int tiles = (eos - bos + TT - 1) / TT;
+
+    if (threadIdx.x >= F::WALK) {
+        const bool first = threadIdx.x < F::WALK + F::SIDE;
+        const int tid = (threadIdx.x - F::WALK) % F::SIDE;
+        const int row0 = tid / CH, ch = tid % CH, col = ch * VN;
+        const bool cok = cg0 + col < p.CG, gate = p.z != nullptr;
+        auto has = [&](int t0, int r) { return row0 + r * RS < TT && t0 + row0 + r * RS < eos && cok; };
+        auto copy_rows = [&](uint4(&to)[ST][TT][CH], const void* from, int64_t ld, int i) {
+            const int t0 = bos + i * TT;
+#pragma unroll
+            for (int r = 0; r < NV; ++r) {
+                const int64_t t = t0 + row0 + r * RS;
+                if (has(t0, r)) copy16_async(&to[i % ST][row0 + r * RS][ch], static_cast<const T*>(from) + t * ld + c0 + col);
+            }
+        };
+        if (first) {
+            float2 bias[VN / 2];
+#pragma unroll
+            for (int e = 0; e < VN / 2; ++e)
+                bias[e] = cok && p.bias ? make_float2(__ldg(p.bias + c0 + col + 2 * e), __ldg(p.bias + c0 + col + 2 * e + 1)) : both(0.f);
+            auto copy = [&](int i) {
+                copy_rows(sm.x, p.x, p.ldx, i);
+                copy_rows(sm.dt, p.dt, p.lddt, i);
+#pragma unroll
+                for (int r = 0; r < NB; ++r) {
+                    const int v = tid + F::SIDE * r, which = v / (TT * BCH), w = v % (TT * BCH);
+                    const int64_t t = bos + i * TT + w / BCH;
+                    const int e = g * S + (w % BCH) * VN;
+                    if (which < 2 && t < eos)
+                        copy16_async(&sm.bc[i % ST][v], which ? static_cast<const T*>(p.Cm) + t * p.ldC + e : static_cast<const T*>(p.B) + t * p.ldB + e);
+                }
+                copy_commit();
+            };
+            for (int i = 0; i < ST - 1; ++i) copy(i);
+            for (int i = 0; i < tiles; ++i) {
+                const int b2 = i & 1, b3 = i % ST;
+                copy(i + ST - 1);
+                copy_wait<ST - 1>();
+                if (i >= 2) bar_sync(kFree + b2, kPair);
+#pragma unroll
+                for (int r = 0; r < NV; ++r) {
+                    const int tt = row0 + r * RS;
+                    if (tt < TT) {
+                        float2 xv[VN / 2], dv[VN / 2];
+                        unpack2(sm.x[b3][tt][ch], xv);
+                        unpack2(sm.dt[b3][tt][ch], dv);
+                        float4* to = reinterpret_cast<float4*>(&sm.d[b2][tt][col + (col / 16) * 2]);
+#pragma unroll
+                        for (int e = 0; e < VN / 2; ++e) {
+                            const float2 d = step_of(dv[e], bias[e], p.softplus);
+                            const float2 dx = __fmul2_rn(d, xv[e]);
+                            to[e] = make_float4(d.x, dx.x, d.y, dx.y);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < NB; ++r) {
+                    const int v = tid + F::SIDE * r, which = v / (TT * BCH), w = v % (TT * BCH);
+                    if (which < 2) {
+                        float f[VN];
+                        unpack(sm.bc[b3][v], f);
+                        float4* to = reinterpret_cast<float4*>(&sm.b[b2][which][w / BCH][(w % BCH) * VN]);
+#pragma unroll
+                        for (int e = 0; e < VN; e += 4) to[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                    }
+                }
+                bar_arrive(kFull + b2, kPair);
+            }
+        } else {
+            float2 D[VN / 2];
+#pragma unroll
+            for (int e = 0; e < VN / 2; ++e)
+                D[e] = cok && p.D ? make_float2(__ldg(p.D + c0 + col + 2 * e), __ldg(p.D + c0 + col + 2 * e + 1)) : both(0.f);
+            auto copy = [&](int i) {
+                copy_rows(sm.x2, p.x, p.ldx, i);
+                if (gate) copy_rows(sm.z, p.z, p.ldz, i);
+                copy_commit();
+            };
+            for (int i = 0; i < ST - 1; ++i) copy(i);
+            for (int i = 0; i < tiles; ++i) {
+                const int b2 = i & 1, b3 = i % ST, t0 = bos + i * TT;
+                copy(i + ST - 1);
+                copy_wait<ST - 1>();
+                bar_sync(kDone + b2, kPair);
+#pragma unroll
+                for (int r = 0; r < NV; ++r) {
+                    const int tt = row0 + r * RS;
+                    if (has(t0, r)) {
+                        float2 xv[VN / 2], zv[VN / 2], sig;
+                        float out[VN];
+                        unpack2(sm.x2[b3][tt][ch], xv);
+                        if (gate) unpack2(sm.z[b3][tt][ch], zv);
+#pragma unroll
+                        for (int e = 0; e < VN / 2; ++e) {
+                            float2 o = __ffma2_rn(D[e], xv[e], *reinterpret_cast<const float2*>(&sm.y[b2][tt][col + 2 * e]));
+                            if (gate) o = __fmul2_rn(o, silu2(zv[e], sig));
+                            out[2 * e] = o.x, out[2 * e + 1] = o.y;
+                        }
+                        st16_stream(static_cast<T*>(p.y) + (int64_t)(t0 + tt) * p.C + c0 + col, pack(out));
+                    }
+                }
+                if (i + 2 < tiles) bar_arrive(kLeft + b2, kPair);
+            }
+        }
+        copy_wait<0>();
+        return;
+    }
+
+    const int j = threadIdx.x % L, cl = threadIdx.x / L;
+    const bool ok = cg0 + cl < p.CG;
+    const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
+    const bool has_slot = slot >= 0 && slot < p.num_slots;
+    const bool use_init = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0);
+    const int64_t own = ok ? (int64_t)(c0 + cl) * S + 4 * j : 0;
+    float* st = p.state + (int64_t)slot * p.C * S + own;
+    float2 A2[2], h[2];
+    load4(p.A_log + own, A2);
+    A2[0] = make_float2(a_log2(A2[0].x), a_log2(A2[0].y)), A2[1] = make_float2(a_log2(A2[1].x), a_log2(A2[1].y));
+    const float4 u = use_init ? *reinterpret_cast<const float4*>(st) : make_float4(0.f, 0.f, 0.f, 0.f);
+    h[0] = make_float2(u.x, u.y), h[1] = make_float2(u.z, u.w);
+    for (int i = 0; i < tiles; ++i) {
+        const int b2 = i & 1, len = min(TT, eos - bos - i * TT);
+        bar_sync(kFull + b2, kPair);
+        if (i >= 2) bar_sync(kLeft + b2, kPair);
+        auto token = [&](int tt) {
+            const float2 d = sm.d[b2][tt][cl + (cl / 16) * 2];
+            const float4 b = *reinterpret_cast<const float4*>(&sm.b[b2][0][tt][4 * j]), c = *reinterpret_cast<const float4*>(&sm.b[b2][1][tt][4 * j]);
+            const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+            advance(h[0], A2[0], both(d.x), both(d.y), make_float2(b.x, b.y));
+            advance(h[1], A2[1], both(d.x), both(d.y), make_float2(b.z, b.w));
+            return sum_states4<L>(h, cc, j);
+        };
+        constexpr int U = 16;  // tokens whose loads and exponentials run ahead of the recurrence
+        if (len == TT) {
+#pragma unroll 1
+            for (int tt = 0; tt < TT; tt += U) {
+                float s[U];
+#pragma unroll
+                for (int k = 0; k < U; ++k) s[k] = token(tt + k);
+                if (j == 1) {
+#pragma unroll
+                    for (int k = 0; k < U; ++k) sm.y[b2][tt + k][cl] = s[k];
+                }
+            }
+        } else {
+            for (int tt = 0; tt < len; ++tt) {
+                const float s = token(tt);
+                if (j == 1) sm.y[b2][tt][cl] = s;
+            }
+        }
+        if (i + 2 < tiles) bar_arrive(kFree + b2, kPair);
+        bar_arrive(kDone + b2, kPair);
+    }
+    if (has_slot && ok) *reinterpret_cast<float4*>(st) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
 }
 
 // Single tokens: HBM bound by the states, read and written once.  A lane holds 4 states (16 bytes)
@@ -426,8 +589,7 @@ gdn_status launch(cudaStream_t s, Params& p) {
     constexpr int cb = K<T, S>::cb;
     p.bpg = (p.CG + cb - 1) / cb;
     if ((long long)p.N * p.G * p.bpg >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
-    K<T, S>::go((unsigned)(p.G * p.bpg), s, p);
-    return launch_status();
+    return K<T, S>::go((unsigned)(p.G * p.bpg), s, p);
 }
 template <template <typename, int> class K, typename T>
 gdn_status by_states(int S, cudaStream_t s, Params& p) {
@@ -439,28 +601,37 @@ gdn_status by_states(int S, cudaStream_t s, Params& p) {
     }
     return GDN_ERR_UNSUPPORTED;
 }
-template <typename T, int S, bool WIDE>
-struct FwdOf {
-    using F = FwdTile<T, S, WIDE>;
+template <typename T, int S>
+struct FwdK {
+    using F = FwdTile<T, S>;
     static constexpr int cb = F::CB;
-    static void go(unsigned blocks, cudaStream_t s, const Params& p) {
+    static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
         Params q = p;
         q.ranked = p.N > 1 && p.N <= kRanked && (long long)blocks * p.N > (long long)kSMs * F::MINB;
-        scan_fwd_kernel<T, S, WIDE><<<blocks * p.N, F::NT, 0, s>>>(q);
+        scan_fwd_kernel<T, S><<<blocks * p.N, F::NT, 0, s>>>(q);
+        return launch_status();
     }
 };
 template <typename T, int S>
-using FwdK = FwdOf<T, S, true>;
-template <typename T, int S>
-using FwdNarrowK = FwdOf<T, S, false>;
+struct FwdNarrowK {
+    using F = NarrowTile<T, S>;
+    static constexpr int cb = F::CB;
+    static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
+        if (cudaFuncSetAttribute(scan_fwd_narrow_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
+            return GDN_ERR_CUDA;
+        scan_fwd_narrow_kernel<T, S><<<blocks * p.N, F::NT, sizeof(F), s>>>(p);
+        return launch_status();
+    }
+};
 template <typename T, int S>
 struct UpdK {
     static constexpr int cb = 128 / (S / 4);
     // Many rows a CTA where that leaves every SM several CTAs; else as few as go together.
-    static void go(unsigned blocks, cudaStream_t s, const Params& p) {
+    static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
         const int most = (int)((long long)blocks * p.N / (kSMs * 16));
         const int rows = most >= kUpdRows ? kUpdRows : most >= 8 ? 8 : 4;
         scan_update_kernel<T, S><<<blocks * ((p.N + rows - 1) / rows), 128, 0, s>>>(p, rows);
+        return launch_status();
     }
 };
 
@@ -482,8 +653,9 @@ extern "C" gdn_status gdn_selective_scan_fwd(const gdn_scan_shape* shape, const 
     if (st != GDN_OK) return st;
     p.cu = cu_seqlens, p.has_init = has_initial_state;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Narrow below two wide CTAs an SM: see FwdTile.
-    const bool narrow = (int64_t)p.N * p.C * shape->S < (int64_t)kSMs * 2 * 1024;
+    // Narrow where all its CTAs run at once, one an SM: see NarrowTile.
+    const int cb = shape->S <= 16 ? 64 : 1024 / shape->S;
+    const bool narrow = (int64_t)p.N * p.G * ((p.CG + cb - 1) / cb) <= kSMs;
     if (shape->dtype == GDN_BF16)
         return narrow ? by_states<FwdNarrowK, __nv_bfloat16>(shape->S, s, p) : by_states<FwdK, __nv_bfloat16>(shape->S, s, p);
     return narrow ? by_states<FwdNarrowK, float>(shape->S, s, p) : by_states<FwdK, float>(shape->S, s, p);
