@@ -144,10 +144,11 @@ __device__ __forceinline__ int64_t angle_row(const QkParams& p, int64_t t) {
     return pos >= 0 && pos < p.max_pos ? pos : -1;
 }
 
-// UR: passes whose loads are in flight together.
-template <typename T, bool INTER, bool HASW, int UR>
+// PART: some units are not rotated (whole heads skip the test: 90 us instead of 106 for 32768 x 32 x
+// 128).  UR: passes whose loads are in flight together.
+template <typename T, bool INTER, bool PART, bool HASW>
 __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParams p) {
-    constexpr int VN = V16<T>::n;
+    constexpr int VN = V16<T>::n, UR = 2;
     const int lane = threadIdx.x & 31, u = lane & (p.lpr - 1), sub = lane / p.lpr, hpw = 32 / p.lpr;
     const Unit un = unit_of<VN>(u, p.d, p.rd, p.inter);
     const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
                         v[e] = __fmul2_rn(v[e], r);
                         if constexpr (HASW) v[e] = __fmul2_rn(v[e], w[e]);
                     }
-                    if (un.rot) an.template turn<INTER>(v);
+                    if (!PART || un.rot) an.template turn<INTER>(v);
                     if (h < H && un.has0) st16_stream(dst + h * p.d + un.e0, pack_half<VN>(v));
                     if (h < H && un.has1) st16_stream(dst + h * p.d + un.e1, pack_half<VN>(v + VN / 2));
                 }
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
     }
 }
 
-template <typename T, bool INTER, bool HASW>
+template <typename T, bool INTER, bool PART, bool HASW>
 __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ QkParams p) {
     constexpr int VN = V16<T>::n, UR = 2;
     extern __shared__ float acc[];  // [256 / lpr groups][d]
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
                     unpack_unit<VN>(ra[i], rb[i], v);
                     unpack_unit<VN>(ga[i], gb[i], g);
                     const float r = rsqrtf(__fmaf_rn(group_sum(dot<VN>(v, v), p.lpr), p.c, p.eps));
-                    if (un.rot) an.template turn<INTER>(g);
+                    if (!PART || un.rot) an.template turn<INTER>(g);
                     if constexpr (HASW) {
 #pragma unroll
                         for (int e = 0; e < VN; ++e) {
@@ -339,20 +340,27 @@ gdn_status check_angles(const gdn_qk_shape* s, const float* cos, const float* si
     return GDN_OK;
 }
 
-template <typename T, bool INTER, bool HASW>
-void qk_launch2(int grid, cudaStream_t s, const QkParams& p) {
-    if (p.passes >= 2) qk_kernel<T, INTER, HASW, 2><<<grid, 256, 0, s>>>(p);
-    else qk_kernel<T, INTER, HASW, 1><<<grid, 256, 0, s>>>(p);
+template <typename T, bool INTER, bool PART>
+void qk_launch2(int grid, cudaStream_t s, const QkParams& p, bool w) {
+    if (w) qk_kernel<T, INTER, PART, true><<<grid, 256, 0, s>>>(p);
+    else qk_kernel<T, INTER, PART, false><<<grid, 256, 0, s>>>(p);
 }
 template <typename T>
 void qk_launch(int grid, cudaStream_t s, const QkParams& p, bool w) {
-    if (p.inter) w ? qk_launch2<T, true, true>(grid, s, p) : qk_launch2<T, true, false>(grid, s, p);
-    else w ? qk_launch2<T, false, true>(grid, s, p) : qk_launch2<T, false, false>(grid, s, p);
+    const bool part = p.rd < p.d;
+    if (p.inter) part ? qk_launch2<T, true, true>(grid, s, p, w) : qk_launch2<T, true, false>(grid, s, p, w);
+    else part ? qk_launch2<T, false, true>(grid, s, p, w) : qk_launch2<T, false, false>(grid, s, p, w);
+}
+template <typename T, bool INTER, bool PART>
+void qk_bwd_launch2(int grid, size_t smem, cudaStream_t s, const QkParams& p, bool w) {
+    if (w) qk_bwd_kernel<T, INTER, PART, true><<<grid, 256, smem, s>>>(p);
+    else qk_bwd_kernel<T, INTER, PART, false><<<grid, 256, smem, s>>>(p);
 }
 template <typename T>
 void qk_bwd_launch(int grid, size_t smem, cudaStream_t s, const QkParams& p, bool w) {
-    if (p.inter) w ? qk_bwd_kernel<T, true, true><<<grid, 256, smem, s>>>(p) : qk_bwd_kernel<T, true, false><<<grid, 256, smem, s>>>(p);
-    else w ? qk_bwd_kernel<T, false, true><<<grid, 256, smem, s>>>(p) : qk_bwd_kernel<T, false, false><<<grid, 256, smem, s>>>(p);
+    const bool part = p.rd < p.d;
+    if (p.inter) part ? qk_bwd_launch2<T, true, true>(grid, smem, s, p, w) : qk_bwd_launch2<T, true, false>(grid, smem, s, p, w);
+    else part ? qk_bwd_launch2<T, false, true>(grid, smem, s, p, w) : qk_bwd_launch2<T, false, false>(grid, smem, s, p, w);
 }
 
 // CTAs of the gradient: one wave of two an SM (128 registers a thread), a token per warp at least.
