@@ -26,8 +26,8 @@ __device__ __forceinline__ float a_log2(float A_log) { return __fmul_rn(-expf(A_
 // softplus(v) = max(v, 0) + log(1 + u), u = e^-|v| in (0, 1], with log(1 + u) = 2 artanh(w),
 // w = u / (2 + u) <= 1/3: relative accuracy is kept for the small steps of strongly negative v,
 // which log of a rounded 1 + u would lose.  artanh(w) / w is a polynomial of degree 4 in w^2
-// (Chebyshev interpolation on [0, 1/9], error 4e-9).  Two values at a time: packed operations
-// take half the issue slots.  `u` is left for the derivative.
+// (Chebyshev interpolation on [0, 1/9], error 4e-9).  Two values at a time, in packed operations.
+// `u` is left for the derivative.
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 softplus2(const float2& v, float2& u) {
     const float2 m = make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f));

@@ -105,6 +105,9 @@ def test_conv_backward_without_tokens():
     dT = torch.randn(3, 3, 16, device=DEV)
     g = gdn.gdn_causal_conv1d_bwd(x, w, torch.zeros(4, dtype=torch.int32, device=DEV), x, bias=w[:, 0].contiguous(), d_final_state=dT)
     assert torch.equal(g["d_init_state"], dT) and torch.all(g["dweight"] == 0) and torch.all(g["dbias"] == 0)
+    x = torch.full((7, 16), float("nan"), device=DEV)  # padding only
+    g = gdn.gdn_causal_conv1d_bwd(x, w, torch.zeros(4, dtype=torch.int32, device=DEV), x, bias=w[:, 0].contiguous(), d_final_state=dT)
+    assert torch.equal(g["d_init_state"], dT) and torch.all(g["dweight"] == 0) and torch.all(g["dbias"] == 0)
 
 
 # ---------------------------------------------------------------- q/k norm with rotation

@@ -288,6 +288,27 @@ def test_no_tokens():
     assert gdn.gdn_selective_scan_update(x, x, A, bc, bc, st).shape == (0, 16)
 
 
+def test_padding_only_and_slots_outside_the_pool():
+    """Tokens of which no sequence has any; slots that are not in the pool."""
+    c = Case([0, 0], 16, 1, 8, torch.float32, 25, behind=5)
+    for t in (c.x, c.dt, c.z, c.B, c.Cm, c.dy):
+        t[:] = float("nan")
+    st = c.h0.clone()
+    out = torch.full((5, 16), 3.0, device=DEV)
+    gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, state=st, out=out, **c.args())
+    assert torch.all(out == 3) and torch.equal(st, c.h0)
+    g = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args())
+    assert torch.equal(g["d_init_state"], c.gT)
+    for k in ("dA_log", "dD", "ddt_bias"):
+        assert torch.all(g[k] == 0), k
+    c = Case([9, 4, 6], 16, 1, 8, torch.float32, 26)
+    pool = torch.randn(3, 16, 8, device=DEV)
+    p0 = pool.clone()
+    y = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, state=pool, state_indices=torch.tensor([-1, 3, 1 << 30], dtype=torch.int32, device=DEV),
+                                   **c.args())
+    assert torch.equal(y, gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, **c.args())) and torch.equal(pool, p0)
+
+
 def test_captured_calls_replay_on_new_inputs_and_other_streams():
     c = Case([50, 14], 64, 1, 16, torch.bfloat16, 19)
     d = Case([30, 34], 64, 1, 16, torch.bfloat16, 20)
