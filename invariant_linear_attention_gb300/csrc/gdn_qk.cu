@@ -221,7 +221,10 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < VN; ++e) sum[e] = twice(0.f);
         }
-        for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < p.T; t += nwarps) {
+        const int per = (np + p.passes - 1) / p.passes;  // items of a token
+        for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < p.T * per; it += nwarps) {
+            const int64_t t = per == 1 ? it : it / per;
+            const int first = per == 1 ? 0 : (int)(it % per) * p.passes, last = min(first + p.passes, np);
             const int64_t row = angle_row(p, t);
             if (row < 0) continue;
             Angles<VN> an;
@@ -229,12 +232,12 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
             const T* src = x + t * ld;
             const T* dsrc = dout + t * H * p.d;
             T* dst = dx + t * ldd;
-            for (int ps = 0; ps < np; ps += UR) {
+            for (int ps = first; ps < last; ps += UR) {
                 uint4 ra[UR], rb[UR], ga[UR], gb[UR];
 #pragma unroll
                 for (int i = 0; i < UR; ++i) {
                     const int h = (ps + i) * hpw + sub;
-                    const bool ok = ps + i < np && h < H;
+                    const bool ok = ps + i < last && h < H;
                     ra[i] = ok && un.has0 ? ld16_stream(src + h * p.d + un.e0) : none;
                     rb[i] = ok && un.has1 ? ld16_stream(src + h * p.d + un.e1) : none;
                     ga[i] = ok && un.has0 ? ld16_stream(dsrc + h * p.d + un.e0) : none;
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
                 }
 #pragma unroll
                 for (int i = 0; i < UR; ++i) {
-                    if (ps + i >= np) break;
+                    if (ps + i >= last) break;
                     const int h = (ps + i) * hpw + sub;
                     float2 v[VN], g[VN];
                     unpack_unit<VN>(ra[i], rb[i], v);
@@ -363,9 +366,17 @@ void qk_bwd_launch(int grid, size_t smem, cudaStream_t s, const QkParams& p, boo
     else part ? qk_bwd_launch2<T, false, true>(grid, smem, s, p, w) : qk_bwd_launch2<T, false, false>(grid, smem, s, p, w);
 }
 
-// CTAs of the gradient: one wave of two an SM (128 registers a thread), a token per warp at least.
+// The gradient's items: a token with all its head passes where the tokens give every warp one, else
+// as many passes as go together.
+int qk_bwd_passes(const gdn_qk_shape* s, const QkParams& p) {
+    const int most = p.pq > p.pk ? p.pq : p.pk;
+    return s->T >= kSMs * 2 * 8 || most < 2 ? most : 2;
+}
+// CTAs of the gradient: one wave of two an SM (128 registers a thread), an item per warp at least.
 int qk_bwd_ctas(const gdn_qk_shape* s) {
-    const int64_t want = (s->T + 7) / 8;
+    const QkParams p = qk_params(s);
+    const int passes = qk_bwd_passes(s, p), most = p.pq > p.pk ? p.pq : p.pk;
+    const int64_t want = (s->T * ((most + passes - 1) / passes) + 7) / 8;
     return (int)(want < kSMs * 2 ? (want > 1 ? want : 1) : kSMs * 2);
 }
 
@@ -439,6 +450,7 @@ extern "C" gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_shape* shape, const void
     p.q = q, p.k = k, p.qw = q_weight, p.kw = k_weight, p.cos = cos, p.sin = sin, p.pos = positions;
     p.dqo = d_q_out, p.dko = d_k_out, p.qo = dq, p.ko = dk, p.lddq = lddq, p.lddk = lddk;
     p.part = sums ? static_cast<float*>(workspace) : nullptr;
+    p.passes = qk_bwd_passes(shape, p);
     const int ctas = qk_bwd_ctas(shape);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t smem = sums ? (size_t)(256 / p.lpr) * p.d * sizeof(float) : 0;
