@@ -27,46 +27,10 @@ __device__ __forceinline__ float scatter_sum(float (&s)[L], int j) {
     return s[0];
 }
 
-// Prompts.  A CTA walks one sequence over CB channels in tiles of TT tokens, a lane 8 states of Q
-// neighbouring channels (L = S / 8 lanes a channel): every B and C it reads from shared memory
-// serves Q channels.  Per tile:
-//   1. the work per (token, channel), shared out as 16-byte chunks of x and dt: d = softplus(dt +
-//      bias) and d x go to shared memory for the walk, B and C become fp32;
-//   2. a later tile's copies are issued (asynchronous, so they take no registers; a thread reads
-//      back only x, dt and z chunks that it copied itself);
-//   3. the walk: the recurrence over the tile's tokens, sum_s h C left where d was;
-//   4. D x, gate and 16-byte stores of y.
-// What bounds it: the step alone (per two states 4 packed products or fmas and 2
-// exponentials, in registers) runs at 6.8 T states/s on this GPU, of 10 T that the
-// exponentials and 9.6 T that the fma pipe would allow; with its loads, sums and the work per (token, channel)
-// it reaches 3.7 T.  Shared memory is the next limit: a load delivers 128 bytes a cycle into
-// registers whether lanes share an address or not, and B and C take 64 bytes a lane and token.
-// Four channels a lane halve that and lose more in the registers they take (2.9 T); one channel a lane: 3.2 T.
-template <typename T, int S>
-struct FwdTile {
-    static constexpr int L = S / 8, Q = 2, CB = S == 8 ? 128 : S == 64 ? 32 : 64, NT = CB * L / Q, VN = V16<T>::n;
-    static constexpr int TT = S == 8 ? 8 : 16;
-    static constexpr int CH = CB / VN;                        // 16-byte chunks of a row
-    static constexpr int NV = (TT * CH + NT - 1) / NT;        // of x (dt, z) per thread and tile
-    static constexpr int RS = NT / CH;                        // tokens between a thread's chunks
-    static constexpr int BCH = S / VN;                        // chunks of a row of B (C)
-    static constexpr int NB = (2 * TT * BCH + NT - 1) / NT;   // of B and C per thread and tile
-    static constexpr int MINB = 512 / NT;                     // CTAs an SM shall hold: 16 warps, 128 registers
-    // {d, d x} of channel c at c float2s plus one 16-byte gap per 16 channels: the chunk-wise
-    // stores and the lanes' loads are both free of bank conflicts.
-    static constexpr int ROW = CB + (CB / 16) * 2;            // float2s per token
-    alignas(16) float2 d[TT][ROW];
-    alignas(16) float b[2][TT][S];
-    uint4 x[2][TT][CH], z[2][TT][CH], dt[TT][CH];
-    uint4 bc[2 * TT * BCH];
-    alignas(16) float D[CB];
-    alignas(16) float bias[CB];
-    static_assert(NT % CH == 0, "a thread keeps its columns");
-};
-
-// The sequence of rank `rank` by length, the longest first (ties by number): with more CTAs than
-// the GPU holds, the longest walks must not be the last to start (16 ragged prompts, 16384 x 8192
-// x 16: 676 us in order of number, 610 in order of length).
+// The sequence of rank `rank` by length, the longest first (ties by number).  As soon as an SM gets
+// more than one CTA, the longest walks must neither start last nor share an SM: 16 ragged prompts,
+// 16384 x 8192 x 16, take 603 us in order of number and 567 in order of length; two CTAs an SM,
+// all resident from the start (8192 x 2048 x 16), 188 and 149.
 constexpr int kRanked = 256;
 __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
     __shared__ int len[kRanked], found;
@@ -86,224 +50,45 @@ __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
     return found;
 }
 
-template <typename T, int S>
-__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
-    using F = FwdTile<T, S>;
-    constexpr int L = F::L, Q = F::Q, NT = F::NT, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB;
-    __shared__ F sm;
-    const int tid = threadIdx.x;
-    const int nb = p.bpg * p.G;
-    const int at = blockIdx.x / nb, blk = blockIdx.x % nb;
-    const int n = p.ranked ? ranked(p, at, NT) : at;
-    const int g = blk / p.bpg, cg0 = (blk % p.bpg) * CB, c0 = g * p.CG + cg0;
-    const int j = tid % L, cl = tid / L * Q;
-    const bool ok = cg0 + cl < p.CG;  // all Q or none: p.CG is a multiple of 8
-    int bos, eos;
-    bounds(p.cu, n, p.T, bos, eos);
-    const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
-    const bool has_slot = slot >= 0 && slot < p.num_slots;
-    const bool use_init = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0);
-
-    // this thread's chunks: columns col .. col + VN - 1 of tokens row0, row0 + RS, ..
-    const int row0 = tid / CH, ch = tid % CH, col = ch * VN;
-    const bool cok = cg0 + col < p.CG;
-    const bool gate = p.z != nullptr, sp = p.softplus != 0;
-    const T* x = static_cast<const T*>(p.x) + c0 + col + (bos + row0) * p.ldx;
-    const T* dt = static_cast<const T*>(p.dt) + c0 + col + (bos + row0) * p.lddt;
-    const T* z = gate ? static_cast<const T*>(p.z) + c0 + col + (bos + row0) * p.ldz : nullptr;
-    T* y = static_cast<T*>(p.y) + c0 + col + (int64_t)(bos + row0) * p.C;
-    const T* Bg = static_cast<const T*>(p.B) + (int64_t)g * S;
-    const T* Cg = static_cast<const T*>(p.Cm) + (int64_t)g * S;
-    // Chunks behind the sequence or the group's channels are not copied: what the walk makes of
-    // the shared memory's old contents there is never stored.
-    auto copy = [&](int i) {  // tile i
-        const int t0 = bos + i * TT, buf = i & 1;
-#pragma unroll
-        for (int r = 0; r < NV; ++r) {
-            const int tt = row0 + r * RS;
-            if (tt < TT && t0 + tt < eos && cok) {
-                copy16_async(&sm.x[buf][tt][ch], x + r * RS * p.ldx);
-                copy16_async(&sm.dt[tt][ch], dt + r * RS * p.lddt);
-                if (gate) copy16_async(&sm.z[buf][tt][ch], z + r * RS * p.ldz);
-            }
-        }
-        x += TT * p.ldx, dt += TT * p.lddt, z += TT * p.ldz;
-#pragma unroll
-        for (int r = 0; r < NB; ++r) {
-            const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
-            const int64_t t = t0 + w / BCH;
-            if (which < 2 && t < eos) copy16_async(&sm.bc[v], which ? Cg + t * p.ldC + (w % BCH) * VN : Bg + t * p.ldB + (w % BCH) * VN);
-        }
-        copy_commit();
-    };
-    copy(0);
-
-    for (int c = tid; c < CB; c += NT) {
-        const bool in = cg0 + c < p.CG;
-        sm.D[c] = in && p.D ? __ldg(p.D + c0 + c) : 0.f;
-        sm.bias[c] = in && p.bias ? __ldg(p.bias + c0 + c) : 0.f;
-    }
-    float2 A2[Q][4], h[Q][4];
-    const int64_t own = ok ? (int64_t)(c0 + cl) * S + 8 * j : 0;
-    float* st = p.state + (int64_t)slot * p.C * S + own;
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t at = q * S + 4 * i;
-            float2 t[2];
-            load4(p.A_log + own + at, t);
-            A2[q][2 * i] = make_float2(a_log2(t[0].x), a_log2(t[0].y));
-            A2[q][2 * i + 1] = make_float2(a_log2(t[1].x), a_log2(t[1].y));
-            const float4 u = use_init ? *reinterpret_cast<const float4*>(st + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-            h[q][2 * i] = make_float2(u.x, u.y), h[q][2 * i + 1] = make_float2(u.z, u.w);
-        }
-    __syncthreads();
-    for (int i = 0, t0 = bos; t0 < eos; ++i, t0 += TT) {
-        const int buf = i & 1;
-        copy_wait<0>();
-#pragma unroll
-        for (int r = 0; r < NV; ++r) {
-            const int tt = row0 + r * RS;
-            if (tt < TT) {
-                float2 xv[VN / 2], dv[VN / 2];
-                unpack2(sm.x[buf][tt][ch], xv);
-                unpack2(sm.dt[tt][ch], dv);
-                float4* to = reinterpret_cast<float4*>(&sm.d[tt][col + (col / 16) * 2]);
-#pragma unroll
-                for (int e = 0; e < VN / 2; ++e) {
-                    const float2 d = step_of(dv[e], *reinterpret_cast<const float2*>(&sm.bias[col + 2 * e]), sp);
-                    const float2 dx = __fmul2_rn(d, xv[e]);
-                    to[e] = make_float4(d.x, dx.x, d.y, dx.y);
-                }
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < NB; ++r) {
-            const int v = tid + NT * r, which = v / (TT * BCH), w = v % (TT * BCH);
-            if (which < 2) {
-                float f[VN];
-                unpack(sm.bc[v], f);
-                float4* to = reinterpret_cast<float4*>(&sm.b[which][w / BCH][(w % BCH) * VN]);
-#pragma unroll
-                for (int e = 0; e < VN; e += 4) to[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-            }
-        }
-        __syncthreads();
-        copy(i + 1);
-        const int len = min(TT, eos - t0);
-        float2* dp = &sm.d[0][cl + (cl / 16) * 2];
-        auto token = [&](int tt, float (&s)[Q]) {
-            float2 d[Q];
-#pragma unroll
-            for (int q = 0; q < Q; q += 2) {
-                const float4 u = *reinterpret_cast<const float4*>(dp + tt * F::ROW + q);
-                d[q] = make_float2(u.x, u.y), d[q + 1] = make_float2(u.z, u.w);
-            }
-            const float4* b4 = reinterpret_cast<const float4*>(&sm.b[0][tt][8 * j]);
-            const float4* c4 = reinterpret_cast<const float4*>(&sm.b[1][tt][8 * j]);
-            float2 acc[Q];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 b = b4[k], c = c4[k];
-                const float2 b0 = make_float2(b.x, b.y), b1 = make_float2(b.z, b.w);
-                const float2 k0 = make_float2(c.x, c.y), k1 = make_float2(c.z, c.w);
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    advance(h[q][2 * k], A2[q][2 * k], both(d[q].x), both(d[q].y), b0);
-                    advance(h[q][2 * k + 1], A2[q][2 * k + 1], both(d[q].x), both(d[q].y), b1);
-                    acc[q] = k ? __ffma2_rn(h[q][2 * k], k0, acc[q]) : __fmul2_rn(h[q][0], k0);
-                    acc[q] = __ffma2_rn(h[q][2 * k + 1], k1, acc[q]);
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < Q; ++q) s[q] = __fadd_rn(acc[q].x, acc[q].y);
-        };
-        auto leave = [&](int tt, const float (&s)[Q]) {  // only this channel's lanes read its d, and they have
-#pragma unroll
-            for (int q = 0; q < Q; ++q) dp[tt * F::ROW + q].x = s[q];
-        };
-        if (len == TT) {
-#pragma unroll (L == 2 ? 2 : 1)
-            for (int tt = 0; tt < TT; tt += L) {
-                float s[Q][L], out[Q];
-#pragma unroll
-                for (int k = 0; k < L; ++k) {
-                    float one[Q];
-                    token(tt + k, one);
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) s[q][k] = one[q];
-                }
-#pragma unroll
-                for (int q = 0; q < Q; ++q) out[q] = scatter_sum<L>(s[q], j);
-                leave(tt + j, out);
-            }
-        } else {
-            for (int tt = 0; tt < len; ++tt) {
-                float s[Q];
-                token(tt, s);
-#pragma unroll
-                for (int q = 0; q < Q; ++q)
-#pragma unroll
-                    for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
-                if (j == 0) leave(tt, s);
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < NV; ++r) {
-            const int tt = row0 + r * RS;
-            if (tt < len && cok) {
-                float2 xv[VN / 2], zv[VN / 2], sig;
-                float out[VN];
-                unpack2(sm.x[buf][tt][ch], xv);
-                if (gate) unpack2(sm.z[buf][tt][ch], zv);
-                const float4* from = reinterpret_cast<const float4*>(&sm.d[tt][col + (col / 16) * 2]);
-#pragma unroll
-                for (int e = 0; e < VN / 2; ++e) {
-                    const float4 s = from[e];
-                    float2 o = __ffma2_rn(*reinterpret_cast<const float2*>(&sm.D[col + 2 * e]), xv[e], make_float2(s.x, s.z));
-                    if (gate) o = __fmul2_rn(o, silu2(zv[e], sig));
-                    out[2 * e] = o.x, out[2 * e + 1] = o.y;
-                }
-                st16_stream(y + (int64_t)r * RS * p.C, pack(out));
-            }
-        }
-        y += (int64_t)TT * p.C;
-    }
-    copy_wait<0>();
-    if (has_slot && ok) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                *reinterpret_cast<float4*>(st + q * S + 4 * i) = make_float4(h[q][2 * i].x, h[q][2 * i].y, h[q][2 * i + 1].x, h[q][2 * i + 1].y);
-    }
-}
-
-// Prompts of a small batch, which leaves an SM one CTA at most: what counts is the latency of a
-// token, not the throughput (64 channels, 16 states, bf16: 80 ns a token, the wide form 160; with two
-// CTAs an SM 150 to 167 against 166, hence the rule at the launch).  A walker holds 4 states of one channel (a quarter of the wide form's
-// work, the same additions), and the phases before and after the walk run beside it, on other
-// warps, a tile ahead and a tile behind:
-//   * preparers: d, d x, B and C of tile i + 1 to shared memory;
-//   * walkers: tile i;
-//   * finishers: skip term, gate and stores of tile i - 1.
+// Prompts.  A CTA walks one sequence over CB channels in tiles of TT tokens.  The phases before
+// and after the walk run beside it, on other warps, a tile ahead and a tile behind:
+//   * preparers, the work per (token, channel), 16-byte chunks of x and dt: d = softplus(dt + bias)
+//     and d x, and B and C in fp32, of tile i + 1 to shared memory;
+//   * walkers, the recurrence over tile i, a lane 8 states of one channel (L = S / 8 lanes a
+//     channel), sum_s h C to shared memory;
+//   * finishers: skip term, gate and 16-byte stores of tile i - 1.
 // They meet at named barriers: full (tile prepared), free (its d, B, C read), done (its sums
 // written), left (its sums read), one of each per buffer; every side passes each barrier the
-// same number of times.  Preparers and finishers copy their own inputs, asynchronously, two tiles
+// same number of times.  Preparers and finishers copy their own inputs, asynchronously, a tile
 // ahead, and read back only chunks that they copied themselves.
+//
+// What bounds it: with few CTAs the walkers' latency, with many the issue slots and the path from
+// shared memory into registers (128 bytes a cycle, whether lanes share an address or not; B and C
+// take 64 bytes a lane and token).  The step alone (per two states 4 packed products or fmas and 2
+// exponentials, in registers) runs at 6.8 T states/s on this GPU, of 10 T that the exponentials
+// and 9.6 T that the fma pipe would allow; with its operands, sums and the phases around it, it
+// reaches 3.7 T.  ns a token of all CTAs at 1 / 2 / 4 / 8 CTAs of 64 channels, 16 states, bf16, an
+// SM: 65 / 98 / 178 / 333; with the phases one after the other in every warp and two channels a
+// lane: 160 / 166 / 211 / 338; with 4 states a lane: 80 / 150.
 template <typename T, int S>
-struct NarrowTile {
-    static constexpr int L = S / 4, CB = S <= 16 ? 64 : 1024 / S, VN = V16<T>::n, TT = 16;
-    static constexpr int WALK = CB * L, SIDE = 128, NT = WALK + 2 * SIDE;
+struct FwdTile {
+    static constexpr int L = S / 8, CB = S <= 16 ? 64 : 1024 / S, VN = V16<T>::n, TT = 16;
+    static constexpr int WALK = CB * L, SIDE = 64, NT = WALK + 2 * SIDE;
+    // CTAs an SM shall hold.  With 2 and the registers that this leaves, one CTA an SM gains 10 %,
+    // full SMs lose 5 % (the 16 prompts above: 567 and 592 us).
+    static constexpr int MINB = 3;
     static constexpr int CH = CB / VN, NV = (TT * CH + SIDE - 1) / SIDE, RS = SIDE / CH;
     static constexpr int BCH = S / VN, NB = (2 * TT * BCH + SIDE - 1) / SIDE;
-    static constexpr int ROW = CB + (CB / 16) * 2;  // as in FwdTile
-    static constexpr int ST = 3;                    // tiles of inputs in flight or in use
+    // {d, d x} of channel c at c float2s plus one 16-byte gap per 16 channels: the chunk-wise
+    // stores and the lanes' loads are both free of bank conflicts.
+    static constexpr int ROW = CB + (CB / 16) * 2;
+    static constexpr int YROW = CB + (L > 1 ? 32 / L : 0);  // the lanes' stores of L tokens miss each other's banks
+    static constexpr int ST = 2;                    // tiles of inputs in flight or in use
     alignas(16) float2 d[2][TT][ROW];
-    alignas(16) float b[2][2][TT][S];
-    alignas(16) float y[2][TT][CB];
+    // States 8 j + 4 k .. of B (C) at float4 k L + j: the L lanes' loads touch consecutive chunks
+    // (in order of states, 8 lanes would meet in the same banks: 64 states 6 % slower).
+    float4 b[2][2][TT][2 * L];
+    alignas(16) float y[2][TT][YROW];
     uint4 x[ST][TT][CH], dt[ST][TT][CH], bc[ST][2 * TT * BCH];  // preparers'
     uint4 x2[ST][TT][CH], z[ST][TT][CH];                        // finishers'
     static_assert(SIDE % CH == 0, "a thread keeps its columns");
@@ -313,14 +98,15 @@ __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("ba
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 template <typename T, int S>
-__global__ void __launch_bounds__(NarrowTile<T, S>::NT, 1) scan_fwd_narrow_kernel(const __grid_constant__ Params p) {
-    using F = NarrowTile<T, S>;
+__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
+    using F = FwdTile<T, S>;
     constexpr int L = F::L, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB, ST = F::ST;
     constexpr int kFull = 1, kFree = 3, kDone = 5, kLeft = 7, kPair = F::WALK + F::SIDE;
     extern __shared__ __align__(16) unsigned char raw[];
     F& sm = *reinterpret_cast<F*>(raw);
     const int nb = p.bpg * p.G;
-    const int n = blockIdx.x / nb, blk = blockIdx.x % nb;
+    const int at = blockIdx.x / nb, blk = blockIdx.x % nb;
+    const int n = p.ranked ? ranked(p, at, F::NT) : at;
     const int g = blk / p.bpg, cg0 = (blk % p.bpg) * CB, c0 = g * p.CG + cg0;
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
@@ -386,9 +172,11 @@ __global__ void __launch_bounds__(NarrowTile<T, S>::NT, 1) scan_fwd_narrow_kerne
                     if (which < 2) {
                         float f[VN];
                         unpack(sm.bc[b3][v], f);
-                        float4* to = reinterpret_cast<float4*>(&sm.b[b2][which][w / BCH][(w % BCH) * VN]);
 #pragma unroll
-                        for (int e = 0; e < VN; e += 4) to[e / 4] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                        for (int e = 0; e < VN; e += 4) {
+                            const int q = ((w % BCH) * VN + e) / 4;
+                            sm.b[b2][which][w / BCH][(q & 1) * L + q / 2] = make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                        }
                     }
                 }
                 bar_arrive(kFull + b2, kPair);
@@ -438,47 +226,65 @@ __global__ void __launch_bounds__(NarrowTile<T, S>::NT, 1) scan_fwd_narrow_kerne
     const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
     const bool has_slot = slot >= 0 && slot < p.num_slots;
     const bool use_init = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0);
-    const int64_t own = ok ? (int64_t)(c0 + cl) * S + 4 * j : 0;
+    const int64_t own = ok ? (int64_t)(c0 + cl) * S + 8 * j : 0;
     float* st = p.state + (int64_t)slot * p.C * S + own;
-    float2 A2[2], h[2];
-    load4(p.A_log + own, A2);
-    A2[0] = make_float2(a_log2(A2[0].x), a_log2(A2[0].y)), A2[1] = make_float2(a_log2(A2[1].x), a_log2(A2[1].y));
-    const float4 u = use_init ? *reinterpret_cast<const float4*>(st) : make_float4(0.f, 0.f, 0.f, 0.f);
-    h[0] = make_float2(u.x, u.y), h[1] = make_float2(u.z, u.w);
+    float2 A2[4], h[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float2 t[2];
+        load4(p.A_log + own + 4 * i, t);
+        A2[2 * i] = make_float2(a_log2(t[0].x), a_log2(t[0].y)), A2[2 * i + 1] = make_float2(a_log2(t[1].x), a_log2(t[1].y));
+        const float4 u = use_init ? *reinterpret_cast<const float4*>(st + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        h[2 * i] = make_float2(u.x, u.y), h[2 * i + 1] = make_float2(u.z, u.w);
+    }
     for (int i = 0; i < tiles; ++i) {
         const int b2 = i & 1, len = min(TT, eos - bos - i * TT);
         bar_sync(kFull + b2, kPair);
         if (i >= 2) bar_sync(kLeft + b2, kPair);
-        auto token = [&](int tt) {
+        auto token = [&](int tt) {  // one token on; this lane's 8 states' sum
             const float2 d = sm.d[b2][tt][cl + (cl / 16) * 2];
-            const float4 b = *reinterpret_cast<const float4*>(&sm.b[b2][0][tt][4 * j]), c = *reinterpret_cast<const float4*>(&sm.b[b2][1][tt][4 * j]);
-            const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
-            advance(h[0], A2[0], both(d.x), both(d.y), make_float2(b.x, b.y));
-            advance(h[1], A2[1], both(d.x), both(d.y), make_float2(b.z, b.w));
-            return sum_states4<L>(h, cc, j);
+            float2 acc;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float4 b = sm.b[b2][0][tt][k * L + j], c = sm.b[b2][1][tt][k * L + j];
+                advance(h[2 * k], A2[2 * k], both(d.x), both(d.y), make_float2(b.x, b.y));
+                advance(h[2 * k + 1], A2[2 * k + 1], both(d.x), both(d.y), make_float2(b.z, b.w));
+                acc = k ? __ffma2_rn(h[2 * k], make_float2(c.x, c.y), acc) : __fmul2_rn(h[0], make_float2(c.x, c.y));
+                acc = __ffma2_rn(h[2 * k + 1], make_float2(c.z, c.w), acc);
+            }
+            return __fadd_rn(acc.x, acc.y);
         };
-        constexpr int U = 16;  // tokens whose loads and exponentials run ahead of the recurrence
+        constexpr int U = 16;  // tokens whose loads and exponentials run ahead of the recurrence (8: 583 us)
         if (len == TT) {
 #pragma unroll 1
             for (int tt = 0; tt < TT; tt += U) {
                 float s[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k) s[k] = token(tt + k);
-                if (j == 1) {
 #pragma unroll
-                    for (int k = 0; k < U; ++k) sm.y[b2][tt + k][cl] = s[k];
+                for (int k = 0; k < U; k += L) {
+                    float g[L];
+#pragma unroll
+                    for (int e = 0; e < L; ++e) g[e] = s[k + e];
+                    sm.y[b2][tt + k + j][cl] = scatter_sum<L>(g, j);
                 }
             }
         } else {
             for (int tt = 0; tt < len; ++tt) {
-                const float s = token(tt);
-                if (j == 1) sm.y[b2][tt][cl] = s;
+                float s = token(tt);
+#pragma unroll
+                for (int off = 1; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+                if (j == 0) sm.y[b2][tt][cl] = s;
             }
         }
         if (i + 2 < tiles) bar_arrive(kFree + b2, kPair);
         bar_arrive(kDone + b2, kPair);
     }
-    if (has_slot && ok) *reinterpret_cast<float4*>(st) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+    if (has_slot && ok) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float4*>(st + 4 * i) = make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+    }
 }
 
 // Single tokens: HBM bound by the states, read and written once.  A lane holds 4 states (16 bytes)
@@ -605,20 +411,11 @@ struct FwdK {
     using F = FwdTile<T, S>;
     static constexpr int cb = F::CB;
     static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
-        Params q = p;
-        q.ranked = p.N > 1 && p.N <= kRanked && (long long)blocks * p.N > (long long)kSMs * F::MINB;
-        scan_fwd_kernel<T, S><<<blocks * p.N, F::NT, 0, s>>>(q);
-        return launch_status();
-    }
-};
-template <typename T, int S>
-struct FwdNarrowK {
-    using F = NarrowTile<T, S>;
-    static constexpr int cb = F::CB;
-    static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
-        if (cudaFuncSetAttribute(scan_fwd_narrow_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
+        if (cudaFuncSetAttribute(scan_fwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
             return GDN_ERR_CUDA;
-        scan_fwd_narrow_kernel<T, S><<<blocks * p.N, F::NT, sizeof(F), s>>>(p);
+        Params q = p;
+        q.ranked = p.N > 1 && p.N <= kRanked && (long long)blocks * p.N > kSMs;
+        scan_fwd_kernel<T, S><<<blocks * p.N, F::NT, sizeof(F), s>>>(q);
         return launch_status();
     }
 };
@@ -652,12 +449,8 @@ extern "C" gdn_status gdn_selective_scan_fwd(const gdn_scan_shape* shape, const 
     if (st != GDN_OK) return st;
     p.cu = cu_seqlens, p.has_init = has_initial_state;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Narrow where all its CTAs run at once, one an SM: see NarrowTile.
-    const int cb = shape->S <= 16 ? 64 : 1024 / shape->S;
-    const bool narrow = (int64_t)p.N * p.G * ((p.CG + cb - 1) / cb) <= kSMs;
-    if (shape->dtype == GDN_BF16)
-        return narrow ? by_states<FwdNarrowK, __nv_bfloat16>(shape->S, s, p) : by_states<FwdK, __nv_bfloat16>(shape->S, s, p);
-    return narrow ? by_states<FwdNarrowK, float>(shape->S, s, p) : by_states<FwdK, float>(shape->S, s, p);
+    return shape->dtype == GDN_BF16 ? by_states<FwdK, __nv_bfloat16>(shape->S, s, p)
+                                    : by_states<FwdK, float>(shape->S, s, p);
 }
 
 extern "C" gdn_status gdn_selective_scan_update(const gdn_scan_shape* shape, const void* x, const void* dt,

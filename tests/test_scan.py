@@ -152,7 +152,7 @@ def test_bits_do_not_depend_on_the_batch_or_on_how_tokens_arrive(dtype, S, C):
                                               (torch.float32, 8, 1, 1032, True), (torch.bfloat16, 32, 1, 264, True),
                                               (torch.float32, 32, 2, 272, False), (torch.bfloat16, 64, 1, 136, False), (torch.float32, 64, 2, 144, True)])
 def test_large_batches_agree_with_a_sequence_alone(dtype, S, G, C, gate):
-    # batches that take the form with more states a lane (the first also the order by length)
+    # several CTAs an SM, sequences in order of length
     lens = [(37 * i) % 90 for i in range(40)]
     c = Case(lens, C, G, S, dtype, 13, gate=gate, D=gate, bias=not gate)
     pool = c.h0.clone()
@@ -163,6 +163,22 @@ def test_large_batches_agree_with_a_sequence_alone(dtype, S, G, C, gate):
         cu = torch.tensor([0, lens[n]], dtype=torch.int32, device=DEV)
         alone = gdn.gdn_selective_scan_fwd(cu_seqlens=cu, state=st, **c.args(t))
         assert torch.equal(bits(alone), bits(y[t])) and torch.equal(bits(st[0]), bits(pool[n])), n
+
+
+@pytest.mark.parametrize("N", [255, 256, 257, 300])
+def test_many_sequences_of_equal_and_no_length(N):
+    # around the largest batch that is taken in order of length; equal lengths, empty sequences, slots in reverse
+    lens = [(0, 19, 19, 33)[i % 4] for i in range(N)]
+    c = Case(lens, 72, 1, 16, torch.bfloat16, 17)
+    pool = c.h0.clone()
+    idx = torch.arange(N - 1, -1, -1, dtype=torch.int32, device=DEV)
+    y = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, state=pool, state_indices=idx, **c.args())
+    for n in (0, 1, 2, 3, 4, N // 2, N - 3, N - 2, N - 1):
+        t = slice(c.cu_list[n], c.cu_list[n + 1])
+        st = c.h0[N - 1 - n:N - n].clone()
+        cu = torch.tensor([0, lens[n]], dtype=torch.int32, device=DEV)
+        alone = gdn.gdn_selective_scan_fwd(cu_seqlens=cu, state=st, **c.args(t))
+        assert torch.equal(bits(alone), bits(y[t])) and torch.equal(bits(st[0]), bits(pool[N - 1 - n])), n
 
 
 @pytest.mark.parametrize("dtype,S,B,C", [(torch.bfloat16, 16, 300, 4160), (torch.float32, 8, 150, 4160), (torch.float32, 64, 37, 1000)])
