@@ -29,8 +29,8 @@ __device__ __forceinline__ float scatter_sum(float (&s)[L], int j) {
 
 // The sequence of rank `rank` by length, the longest first (ties by number).  As soon as an SM gets
 // more than one CTA, the longest walks must neither start last nor share an SM: 16 ragged prompts,
-// 16384 x 8192 x 16, take 603 us in order of number and 567 in order of length; two CTAs an SM,
-// all resident from the start (8192 x 2048 x 16), 188 and 149.
+// 16384 x 8192 x 16, one channel a lane, take 603 us in order of number and 567 in order of length;
+// two CTAs an SM, all resident from the start (8192 x 2048 x 16), 188 and 149.
 constexpr int kRanked = 256;
 __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
     __shared__ int len[kRanked], found;
@@ -54,7 +54,7 @@ __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
 // and after the walk run beside it, on other warps, a tile ahead and a tile behind:
 //   * preparers, the work per (token, channel), 16-byte chunks of x and dt: d = softplus(dt + bias)
 //     and d x, and B and C in fp32, of tile i + 1 to shared memory;
-//   * walkers, the recurrence over tile i, a lane 8 states of one channel (L = S / 8 lanes a
+//   * walkers, the recurrence over tile i, a lane 8 states of Q channels (L = S / 8 lanes a
 //     channel), sum_s h C to shared memory;
 //   * finishers: skip term, gate and 16-byte stores of tile i - 1.
 // They meet at named barriers: full (tile prepared), free (its d, B, C read), done (its sums
@@ -62,20 +62,22 @@ __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
 // same number of times.  Preparers and finishers copy their own inputs, asynchronously, a tile
 // ahead, and read back only chunks that they copied themselves.
 //
-// What bounds it: with few CTAs the walkers' latency, with many the issue slots and the path from
-// shared memory into registers (128 bytes a cycle, whether lanes share an address or not; B and C
-// take 64 bytes a lane and token).  The step alone (per two states 4 packed products or fmas and 2
-// exponentials, in registers) runs at 6.8 T states/s on this GPU, of 10 T that the exponentials
-// and 9.6 T that the fma pipe would allow; with its operands, sums and the phases around it, it
-// reaches 3.7 T.  ns a token of all CTAs at 1 / 2 / 4 / 8 CTAs of 64 channels, 16 states, bf16, an
-// SM: 65 / 98 / 178 / 333; with the phases one after the other in every warp and two channels a
-// lane: 160 / 166 / 211 / 338; with 4 states a lane: 80 / 150.
-template <typename T, int S>
+// What bounds it: with few CTAs the walkers' latency; with many and Q = 1 the path from shared
+// memory into registers (128 bytes a cycle, whether lanes share an address or not; B and C take 64
+// bytes a lane and token), with Q = 2 the issue slots.  The step alone (per two states 4 packed
+// products or fmas and 2 exponentials, in registers) runs at 6.8 T states/s on this GPU, of 10 T
+// that the exponentials and 9.6 T that the fma pipe would allow; with its operands, sums and the
+// phases around it, it reaches 4.0 T at 16 states, 4.4 T at 64.  ns a token of all CTAs, 16 states,
+// bf16, at 1 / 2 / 3 / 4 / 8 / 16 blocks of 64 channels an SM: Q = 1 65 / 98 / 136 / 178 / 333 / 646,
+// Q = 2 (4 and up) 174 / 324 / 619; 64 states, 8 blocks of 16 channels: 362 and 283.  With the phases
+// one after the other in every warp and two channels a lane: 160 / 166 / - / 211 / 338; with 4 states
+// a lane: 80 / 150.
+template <typename T, int S, int Q>
 struct FwdTile {
-    static constexpr int L = S / 8, CB = S <= 16 ? 64 : 1024 / S, VN = V16<T>::n, TT = 16;
-    static constexpr int WALK = CB * L, SIDE = 64, NT = WALK + 2 * SIDE;
-    // CTAs an SM shall hold.  With 2 and the registers that this leaves, one CTA an SM gains 10 %,
-    // full SMs lose 5 % (the 16 prompts above: 567 and 592 us).
+    static constexpr int L = S / 8, CB = Q * (S <= 16 ? 64 : 1024 / S), VN = V16<T>::n, TT = 16 / Q;
+    static constexpr int WALK = CB / Q * L, SIDE = 64, NT = WALK + 2 * SIDE;
+    // CTAs an SM shall hold.  With 2 and the registers that this leaves, full SMs lose 4 % for
+    // either Q (the 16 prompts above, Q = 1: 567 and 592 us; Q = 2: 543 and 564), with 4 as much.
     static constexpr int MINB = 3;
     static constexpr int CH = CB / VN, NV = (TT * CH + SIDE - 1) / SIDE, RS = SIDE / CH;
     static constexpr int BCH = S / VN, NB = (2 * TT * BCH + SIDE - 1) / SIDE;
@@ -92,14 +94,23 @@ struct FwdTile {
     uint4 x[ST][TT][CH], dt[ST][TT][CH], bc[ST][2 * TT * BCH];  // preparers'
     uint4 x2[ST][TT][CH], z[ST][TT][CH];                        // finishers'
     static_assert(SIDE % CH == 0, "a thread keeps its columns");
+    static_assert(Q == 1 || (WALK == 128 && 2 * SIDE == 128), "registers move between warpgroups");
 };
 
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-template <typename T, int S>
-__global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
-    using F = FwdTile<T, S>;
+// With two channels a lane the walkers need more registers than the others.  A thread is launched
+// with 80 (at three CTAs of 256 threads); 128 threads go down to 64, 128 up to 96, no more than the
+// CTA holds (checked on the host).  Without: 577 us for the 16 prompts instead of 543; 56 and 104:
+// the same; 48 and 112: 573.
+constexpr int kRegsSide = 64, kRegsWalk = 96;
+template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <typename T, int S, int Q>
+__global__ void __launch_bounds__(FwdTile<T, S, Q>::NT, FwdTile<T, S, Q>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {
+    using F = FwdTile<T, S, Q>;
     constexpr int L = F::L, CB = F::CB, TT = F::TT, VN = F::VN, CH = F::CH, NV = F::NV, RS = F::RS, BCH = F::BCH, NB = F::NB, ST = F::ST;
     constexpr int kFull = 1, kFree = 3, kDone = 5, kLeft = 7, kPair = F::WALK + F::SIDE;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -113,6 +124,7 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
     const int tiles = (eos - bos + TT - 1) / TT;
 
     if (threadIdx.x >= F::WALK) {
+        if constexpr (Q > 1) regs_less<kRegsSide>();
         const bool first = threadIdx.x < F::WALK + F::SIDE;
         const int tid = (threadIdx.x - F::WALK) % F::SIDE;
         const int row0 = tid / CH, ch = tid % CH, col = ch * VN;
@@ -221,60 +233,85 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
         return;
     }
 
-    const int j = threadIdx.x % L, cl = threadIdx.x / L;
-    const bool ok = cg0 + cl < p.CG;
+    if constexpr (Q > 1) regs_more<kRegsWalk>();
+    const int j = threadIdx.x % L, cl = threadIdx.x / L * Q;
+    const bool ok = cg0 + cl < p.CG;  // all Q or none: p.CG is a multiple of 8
     const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
     const bool has_slot = slot >= 0 && slot < p.num_slots;
     const bool use_init = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0);
     const int64_t own = ok ? (int64_t)(c0 + cl) * S + 8 * j : 0;
     float* st = p.state + (int64_t)slot * p.C * S + own;
-    float2 A2[4], h[4];
+    float2 A2[Q][4], h[Q][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float2 t[2];
-        load4(p.A_log + own + 4 * i, t);
-        A2[2 * i] = make_float2(a_log2(t[0].x), a_log2(t[0].y)), A2[2 * i + 1] = make_float2(a_log2(t[1].x), a_log2(t[1].y));
-        const float4 u = use_init ? *reinterpret_cast<const float4*>(st + 4 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
-        h[2 * i] = make_float2(u.x, u.y), h[2 * i + 1] = make_float2(u.z, u.w);
-    }
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = (ok ? q * S : 0) + 4 * i;
+            float2 t[2];
+            load4(p.A_log + own + at, t);
+            A2[q][2 * i] = make_float2(a_log2(t[0].x), a_log2(t[0].y)), A2[q][2 * i + 1] = make_float2(a_log2(t[1].x), a_log2(t[1].y));
+            const float4 u = use_init ? *reinterpret_cast<const float4*>(st + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            h[q][2 * i] = make_float2(u.x, u.y), h[q][2 * i + 1] = make_float2(u.z, u.w);
+        }
     for (int i = 0; i < tiles; ++i) {
         const int b2 = i & 1, len = min(TT, eos - bos - i * TT);
         bar_sync(kFull + b2, kPair);
         if (i >= 2) bar_sync(kLeft + b2, kPair);
-        auto token = [&](int tt) {  // one token on; this lane's 8 states' sum
-            const float2 d = sm.d[b2][tt][cl + (cl / 16) * 2];
-            float2 acc;
+        auto token = [&](int tt, float (&sum)[Q]) {  // one token on; this lane's 8 states' sums
+            float2 d[Q], acc[Q];
+            if constexpr (Q == 2) {
+                const float4 v = *reinterpret_cast<const float4*>(&sm.d[b2][tt][cl + (cl / 16) * 2]);
+                d[0] = make_float2(v.x, v.y), d[1] = make_float2(v.z, v.w);
+            } else {
+                d[0] = sm.d[b2][tt][cl + (cl / 16) * 2];
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const float4 b = sm.b[b2][0][tt][k * L + j], c = sm.b[b2][1][tt][k * L + j];
-                advance(h[2 * k], A2[2 * k], both(d.x), both(d.y), make_float2(b.x, b.y));
-                advance(h[2 * k + 1], A2[2 * k + 1], both(d.x), both(d.y), make_float2(b.z, b.w));
-                acc = k ? __ffma2_rn(h[2 * k], make_float2(c.x, c.y), acc) : __fmul2_rn(h[0], make_float2(c.x, c.y));
-                acc = __ffma2_rn(h[2 * k + 1], make_float2(c.z, c.w), acc);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    advance(h[q][2 * k], A2[q][2 * k], both(d[q].x), both(d[q].y), make_float2(b.x, b.y));
+                    advance(h[q][2 * k + 1], A2[q][2 * k + 1], both(d[q].x), both(d[q].y), make_float2(b.z, b.w));
+                    acc[q] = k ? __ffma2_rn(h[q][2 * k], make_float2(c.x, c.y), acc[q]) : __fmul2_rn(h[q][0], make_float2(c.x, c.y));
+                    acc[q] = __ffma2_rn(h[q][2 * k + 1], make_float2(c.z, c.w), acc[q]);
+                }
             }
-            return __fadd_rn(acc.x, acc.y);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) sum[q] = __fadd_rn(acc[q].x, acc[q].y);
         };
-        constexpr int U = 16;  // tokens whose loads and exponentials run ahead of the recurrence (8: 583 us)
+        auto put = [&](int tt, const float (&v)[Q]) {
+            if constexpr (Q == 2) *reinterpret_cast<float2*>(&sm.y[b2][tt][cl]) = make_float2(v[0], v[1]);
+            else sm.y[b2][tt][cl] = v[0];
+        };
+        constexpr int U = TT;  // tokens whose loads and exponentials run ahead of the recurrence (Q = 1, 8 of them: 583 us)
         if (len == TT) {
 #pragma unroll 1
             for (int tt = 0; tt < TT; tt += U) {
-                float s[U];
+                float s[U][Q];
 #pragma unroll
-                for (int k = 0; k < U; ++k) s[k] = token(tt + k);
+                for (int k = 0; k < U; ++k) token(tt + k, s[k]);
 #pragma unroll
                 for (int k = 0; k < U; k += L) {
-                    float g[L];
+                    float v[Q];
 #pragma unroll
-                    for (int e = 0; e < L; ++e) g[e] = s[k + e];
-                    sm.y[b2][tt + k + j][cl] = scatter_sum<L>(g, j);
+                    for (int q = 0; q < Q; ++q) {
+                        float g[L];
+#pragma unroll
+                        for (int e = 0; e < L; ++e) g[e] = s[k + e][q];
+                        v[q] = scatter_sum<L>(g, j);
+                    }
+                    put(tt + k + j, v);
                 }
             }
         } else {
             for (int tt = 0; tt < len; ++tt) {
-                float s = token(tt);
+                float s[Q];
+                token(tt, s);
 #pragma unroll
-                for (int off = 1; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-                if (j == 0) sm.y[b2][tt][cl] = s;
+                for (int q = 0; q < Q; ++q)
+#pragma unroll
+                    for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
+                if (j == 0) put(tt, s);
             }
         }
         if (i + 2 < tiles) bar_arrive(kFree + b2, kPair);
@@ -282,8 +319,10 @@ __global__ void __launch_bounds__(FwdTile<T, S>::NT, FwdTile<T, S>::MINB) scan_f
     }
     if (has_slot && ok) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float4*>(st + 4 * i) = make_float4(h[2 * i].x, h[2 * i].y, h[2 * i + 1].x, h[2 * i + 1].y);
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<float4*>(st + q * S + 4 * i) = make_float4(h[q][2 * i].x, h[q][2 * i].y, h[q][2 * i + 1].x, h[q][2 * i + 1].y);
     }
 }
 
@@ -408,15 +447,35 @@ gdn_status by_states(int S, cudaStream_t s, Params& p) {
 }
 template <typename T, int S>
 struct FwdK {
-    using F = FwdTile<T, S>;
-    static constexpr int cb = F::CB;
-    static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
-        if (cudaFuncSetAttribute(scan_fwd_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
+    static constexpr int cb = FwdTile<T, S, 1>::CB;
+    template <int Q>
+    static gdn_status run(cudaStream_t s, const Params& p) {
+        using F = FwdTile<T, S, Q>;
+        if (cudaFuncSetAttribute(scan_fwd_kernel<T, S, Q>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
             return GDN_ERR_CUDA;
         Params q = p;
+        q.bpg = (p.CG + F::CB - 1) / F::CB;
+        const unsigned blocks = (unsigned)(q.bpg * q.G);
         q.ranked = p.N > 1 && p.N <= kRanked && (long long)blocks * p.N > kSMs;
-        scan_fwd_kernel<T, S><<<blocks * p.N, F::NT, sizeof(F), s>>>(q);
+        scan_fwd_kernel<T, S, Q><<<blocks * p.N, F::NT, sizeof(F), s>>>(q);
         return launch_status();
+    }
+    // Whether the walkers of the compiled kernel get their registers: else they would wait for ever.
+    static bool two_fit() {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, scan_fwd_kernel<T, S, 2>) == cudaSuccess && 2 * a.numRegs >= kRegsSide + kRegsWalk;
+    }
+    static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
+        // Two channels a lane from four blocks of an equally long sequence an SM on (figures above); with
+        // fewer they leave SMs idle.  The longest of N sequences is taken for up to min(N, 3) mean
+        // lengths: once it walks alone, a token takes twice as long with two channels a lane
+        // (16 ragged prompts, 12265 x 2760 x 16, 4.6 blocks an SM: 192 and 368 us; 16384 x 8192 x 16,
+        // 13 blocks: 567 and 543).  Not for 8 states: their walkers would be half a warpgroup.
+        if constexpr (S >= 16) {
+            static const bool fit = two_fit();
+            if (fit && (long long)blocks * p.N >= 4LL * kSMs * (p.N < 3 ? p.N : 3)) return run<2>(s, p);
+        }
+        return run<1>(s, p);
     }
 };
 template <typename T, int S>

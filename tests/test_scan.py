@@ -150,14 +150,16 @@ def test_bits_do_not_depend_on_the_batch_or_on_how_tokens_arrive(dtype, S, C):
 
 @pytest.mark.parametrize("dtype,S,G,C,gate", [(torch.bfloat16, 16, 1, 2056, True), (torch.float32, 16, 2, 592, False), (torch.bfloat16, 8, 3, 1056, False),
                                               (torch.float32, 8, 1, 1032, True), (torch.bfloat16, 32, 1, 264, True),
-                                              (torch.float32, 32, 2, 272, False), (torch.bfloat16, 64, 1, 136, False), (torch.float32, 64, 2, 144, True)])
+                                              (torch.float32, 32, 2, 272, False), (torch.bfloat16, 64, 1, 136, False), (torch.float32, 64, 2, 144, True),
+                                              (torch.float32, 16, 2, 1040, False), (torch.bfloat16, 32, 1, 520, True), (torch.float32, 32, 2, 528, False),
+                                              (torch.bfloat16, 64, 1, 264, False), (torch.float32, 64, 2, 272, True)])
 def test_large_batches_agree_with_a_sequence_alone(dtype, S, G, C, gate):
-    # several CTAs an SM, sequences in order of length
-    lens = [(37 * i) % 90 for i in range(40)]
+    # several CTAs an SM, sequences in order of length; then also two channels a lane
+    lens = [(37 * i) % 90 for i in range(110)]
     c = Case(lens, C, G, S, dtype, 13, gate=gate, D=gate, bias=not gate)
     pool = c.h0.clone()
     y = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, state=pool, **c.args())
-    for n in range(40):
+    for n in range(110):
         t = slice(c.cu_list[n], c.cu_list[n + 1])
         st = c.h0[n:n + 1].clone()
         cu = torch.tensor([0, lens[n]], dtype=torch.int32, device=DEV)
