@@ -97,16 +97,12 @@ struct FwdTile {
     static_assert(Q == 1 || (WALK == 128 && 2 * SIDE == 128), "registers move between warpgroups");
 };
 
-__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
-__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
 // With two channels a lane the walkers need more registers than the others.  A thread is launched
 // with 80 (at three CTAs of 256 threads); 128 threads go down to 64, 128 up to 96, no more than the
 // CTA holds (checked on the host).  Without: 577 us for the 16 prompts instead of 543; 56 and 104:
 // the same; 48 and 112: 573.
 constexpr int kRegsSide = 64, kRegsWalk = 96;
-template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <typename T, int S, int Q>
 __global__ void __launch_bounds__(FwdTile<T, S, Q>::NT, FwdTile<T, S, Q>::MINB) scan_fwd_kernel(const __grid_constant__ Params p) {

@@ -108,6 +108,12 @@ __device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
     v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
 
+// Named barriers between a CTA's warps, and registers moved between its warpgroups.
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+template <int N> __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Bounds of sequence n, whatever cu_seqlens holds.
 __device__ __forceinline__ void bounds(const int32_t* cu, int n, int T, int& bos, int& eos) {
     bos = max(0, min(__ldg(cu + n), T));

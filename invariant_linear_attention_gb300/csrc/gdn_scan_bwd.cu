@@ -13,7 +13,8 @@
 //      and the sums of d up to there;
 //   2. join: along each sequence, the segments' true start states and end G's;
 //   3. grad: per segment, tiles last to first.  A tile's states are recomputed from its start into
-//      registers, and its tokens walked backwards;
+//      registers, and its tokens walked backwards, on four warps; softplus and the gates before
+//      and dx, ddt, dz and the sums of dB and dC after are other warps' work;
 //   4. sums: the channel blocks' partials of dB and dC, the segments' of the parameters' gradients.
 // Every sum's order is fixed by the shapes and cu_seqlens.
 //
@@ -54,10 +55,8 @@ struct BwdParams {
 __host__ __device__ constexpr int channels_of(int S) { return S <= 16 ? 64 : 32; }
 template <typename T, int S, int Q>
 struct Geo {
-    static constexpr int L = S / 4, CB = channels_of(S), NT = CB * L / Q, VN = V16<T>::n;
-    static constexpr int CH = CB / VN, NV = (kTile * CH + NT - 1) / NT, RS = NT / CH;  // 16-byte chunks, as in the forward
-    static constexpr int BCH = S / VN, NB = (2 * kTile * BCH + NT - 1) / NT;
-    static_assert(NT % 32 == 0 && NT % CH == 0, "whole warps; a thread keeps its columns");
+    static constexpr int L = S / 4, CB = channels_of(S), NT = CB * L / Q;
+    static_assert(NT % 32 == 0, "whole warps");
 };
 
 // What both walks read per (token, channel): {d, d x, e, softplus'}, and B and C in fp32.  Channel
@@ -68,13 +67,12 @@ __device__ __forceinline__ int place(int c) { return (c & ~7) | ((c ^ (c >> 3)) 
 
 template <typename T, int S>
 struct Input {
-    using F = Geo<T, S, 2>;
-    alignas(16) float4 d[kTile][F::CB];
+    static constexpr int CB = channels_of(S), VN = V16<T>::n, CH = CB / VN, BCH = S / VN;  // 16-byte chunks
+    alignas(16) float4 d[kTile][CB];
     alignas(16) float b[2][kTile][S];
-    uint4 x[2][kTile][F::CH], dt[2][kTile][F::CH], dy[2][kTile][F::CH], z[2][kTile][F::CH];
-    uint4 bc[2][2 * kTile * F::BCH];
-    alignas(16) float D[F::CB];
-    alignas(16) float bias[F::CB];
+    uint4 x[2][kTile][CH], dt[2][kTile][CH], dy[2][kTile][CH], z[2][kTile][CH];
+    uint4 bc[2][2 * kTile * BCH];
+    alignas(16) float bias[CB];
 };
 
 // Where a CTA stands: sequence, segment, its tokens [lo, hi), group, channels.
@@ -106,37 +104,38 @@ __device__ __forceinline__ bool where(const BwdParams& q, Where& w) {
 
 // A thread's share of a CTA's inputs: columns col .. col + VN - 1 of tokens row0, row0 + RS, .. of a
 // tile.  Pointers and strides stay in the kernel's parameters: the walks need the registers.
-template <typename T, int S, int Q>
+template <typename T, int S, int NT>
 struct Feed {
-    using F = Geo<T, S, Q>;
-    static constexpr int VN = F::VN;
+    using In = Input<T, S>;
+    static constexpr int VN = In::VN, CH = In::CH, BCH = In::BCH, RS = NT / CH;
+    static constexpr int NV = (kTile * CH + NT - 1) / NT, NB = (2 * kTile * BCH + NT - 1) / NT;
+    static_assert(NT % CH == 0, "a thread keeps its columns");
     const BwdParams& q;
     int row0, ch, col, hi, c, g;
     bool cok;
 
     __device__ __forceinline__ Feed(const BwdParams& q_, const Where& w) : q(q_) {
-        row0 = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, col = ch * VN, hi = w.hi, c = w.c0 + col, g = w.g;
+        row0 = threadIdx.x / CH, ch = threadIdx.x % CH, col = ch * VN, hi = w.hi, c = w.c0 + col, g = w.g;
         cok = w.cg0 + col < q.f.CG;
     }
-    // D and dt_bias of the CTA's channels; in place after the next barrier.
-    __device__ __forceinline__ void columns(Input<T, S>& in, const Where& w) const {
+    // dt_bias of the CTA's channels; in place after the next barrier.
+    __device__ __forceinline__ void columns(In& in, const Where& w) const {
         const Params& p = q.f;
-        for (int i = threadIdx.x; i < F::CB; i += F::NT) {
+        for (int i = threadIdx.x; i < In::CB; i += NT) {
             const bool ok = w.cg0 + i < p.CG;
-            in.D[i] = ok && p.D ? __ldg(p.D + w.c0 + i) : 0.f;
             in.bias[i] = ok && p.bias ? __ldg(p.bias + w.c0 + i) : 0.f;
         }
     }
     __device__ __forceinline__ bool gate() const { return q.f.z != nullptr; }
     __device__ __forceinline__ bool has(int t0, int r) const {
-        const int tt = row0 + r * F::RS;
+        const int tt = row0 + r * RS;
         return tt < kTile && t0 + tt < hi && cok;
     }
-    __device__ __forceinline__ void copy(Input<T, S>& in, int t0, int buf) const {
+    __device__ __forceinline__ void copy(In& in, int t0, int buf) const {
         const Params& p = q.f;
 #pragma unroll
-        for (int r = 0; r < F::NV; ++r) {
-            const int tt = row0 + r * F::RS;
+        for (int r = 0; r < NV; ++r) {
+            const int tt = row0 + r * RS;
             const int64_t t = t0 + tt;
             if (has(t0, r)) {
                 copy16_async(&in.x[buf][tt][ch], static_cast<const T*>(p.x) + t * p.ldx + c);
@@ -146,20 +145,20 @@ struct Feed {
             }
         }
 #pragma unroll
-        for (int r = 0; r < F::NB; ++r) {
-            const int v = threadIdx.x + F::NT * r, which = v / (kTile * F::BCH), k = v % (kTile * F::BCH);
-            const int64_t t = t0 + k / F::BCH;
-            const int e = g * S + (k % F::BCH) * VN;
+        for (int r = 0; r < NB; ++r) {
+            const int v = threadIdx.x + NT * r, which = v / (kTile * BCH), k = v % (kTile * BCH);
+            const int64_t t = t0 + k / BCH;
+            const int e = g * S + (k % BCH) * VN;
             if (which < 2 && t < hi)
                 copy16_async(&in.bc[buf][v], which ? static_cast<const T*>(p.Cm) + t * p.ldC + e : static_cast<const T*>(p.B) + t * p.ldB + e);
         }
     }
     // {d, d x, e, softplus'} and the fp32 B and C of the tile whose copies have arrived.
-    __device__ __forceinline__ void prepare(Input<T, S>& in, int t0, int buf) const {
+    __device__ __forceinline__ void prepare(In& in, int t0, int buf) const {
         const Params& p = q.f;
 #pragma unroll
-        for (int r = 0; r < F::NV; ++r) {
-            const int tt = row0 + r * F::RS;
+        for (int r = 0; r < NV; ++r) {
+            const int tt = row0 + r * RS;
             if (tt >= kTile) continue;
             if (!has(t0, r)) {
 #pragma unroll
@@ -186,13 +185,13 @@ struct Feed {
             }
         }
 #pragma unroll
-        for (int r = 0; r < F::NB; ++r) {
-            const int v = threadIdx.x + F::NT * r, which = v / (kTile * F::BCH), k = v % (kTile * F::BCH);
+        for (int r = 0; r < NB; ++r) {
+            const int v = threadIdx.x + NT * r, which = v / (kTile * BCH), k = v % (kTile * BCH);
             if (which < 2) {
-                const bool ok = t0 + k / F::BCH < hi;
+                const bool ok = t0 + k / BCH < hi;
                 float f[VN];
                 unpack(in.bc[buf][v], f);
-                float4* to = reinterpret_cast<float4*>(&in.b[which][k / F::BCH][(k % F::BCH) * VN]);
+                float4* to = reinterpret_cast<float4*>(&in.b[which][k / BCH][(k % BCH) * VN]);
 #pragma unroll
                 for (int e = 0; e < VN; e += 4) to[e / 4] = ok ? make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan
     Where w;
     if (!where<T, S>(q, w)) return;
     const Params& p = q.f;
-    const Feed<T, S, 4> feed(q, w);
+    const Feed<T, S, F::NT> feed(q, w);
     feed.copy(in, w.lo, 0);
     copy_commit();
     feed.columns(in, w);
@@ -360,42 +359,231 @@ __device__ __forceinline__ float2 sum_channels(const float2 (&v)[2]) {
 // Keeps the compiler from loading later tokens' values early: the states of a tile fill the registers.
 __device__ __forceinline__ void fence() { asm volatile("" ::: "memory"); }
 
+// The work per (token, channel) before and after a tile's walk is done beside it, on SIDE threads
+// of their own: a thread takes 4 channels of tokens row0, row0 + RS, .. of every tile, prepares
+// them for tile i + 1 while the walkers are at tile i, then waits for their sums and finishes it.
+template <typename T> struct V4;
+template <> struct V4<float> { using type = uint4; };
+template <> struct V4<__nv_bfloat16> { using type = uint2; };
+__device__ __forceinline__ void unpack4(const uint4& u, float2 (&v)[2]) { unpack2(u, v); }
+__device__ __forceinline__ void unpack4(const uint2& u, float2 (&v)[2]) {
+    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+}
+__device__ __forceinline__ void copy4_async(uint4* to, const float* from) { copy16_async(to, from); }
+__device__ __forceinline__ void copy4_async(uint2* to, const __nv_bfloat16* from) { copy8_async(to, from); }
+__device__ __forceinline__ void store4_stream(float* to, const float2 (&v)[2]) {
+    __stcs(reinterpret_cast<float4*>(to), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+}
+__device__ __forceinline__ void store4_stream(__nv_bfloat16* to, const float2 (&v)[2]) {
+    __nv_bfloat162 a = __float22bfloat162_rn(v[0]), b = __float22bfloat162_rn(v[1]);
+    __stcs(reinterpret_cast<uint2*>(to), make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b)));
+}
+
 template <typename T, int S>
 struct GradMem {
     using F = Geo<T, S, 2>;
-    Input<T, S> in;
-    float uvy[3][kTile][F::CB + 4];
-    float bc[F::NT / 32][kTile][2 * S];  // each warp's dB and dC
-    // each thread's own: its sums for dD and ddt_bias, its segment's start states, the next tile's local ones
-    float2 sums[F::VN][F::NT];
-    // and its states at the tile's start
-    alignas(16) float4 seg[2][F::NT];
-    alignas(16) float4 tile[2][F::NT];
-    alignas(16) float4 h[2][F::NT];
+    using V = typename V4<T>::type;
+    static constexpr int CB = F::CB, WALK = F::NT, SIDE = WALK < 128 ? 64 : 128, NT = WALK + SIDE;
+    static constexpr int MINB = NT <= 128 ? 4 : 2;  // CTAs an SM shall hold
+    static constexpr int CH = CB / 4, RS = SIDE / CH, NV = (kTile + RS - 1) / RS;
+    static constexpr int NBC = 2 * kTile * S / 4;
+    static constexpr int H = WALK == 128 ? kTile : kTile / 2;  // tokens whose states are in registers at a time
+    static constexpr int PB = S < 64 ? 2 : 1;  // buffers of the warps' dB and dC: with two, 64 states would leave room for one CTA
+    // {d, d x, e, softplus'} of channel c at place(c); then B and C in fp32
+    alignas(16) float4 d[2][kTile][CB];
+    alignas(16) float b[2][2][kTile][S];
+    alignas(16) float uvy[2][3][kTile][CB + 4];
+    alignas(16) float bc[PB][WALK / 32][kTile][2 * S];  // each warp's dB and dC
+    alignas(16) V x[2][kTile][CH], dt[2][kTile][CH], dy[2][kTile][CH], z[2][kTile][CH], in[2][NBC];
+    // each walker's own: its segment's start states, the next tile's local ones, its states at the tile's start
+    alignas(16) float4 seg[2][WALK];
+    alignas(16) float4 tile[2][WALK];
+    alignas(16) float4 h[2][H < kTile ? WALK : 1];
+    static_assert(SIDE % CH == 0, "a thread keeps its columns");
 };
 
+// Two channels' states, their gradients and a tile's history need more registers than the work
+// before and after: as in the forward, registers move to the walkers, no more than the CTA was
+// launched with (128 a thread at two CTAs of 256 threads, 80 at two of 384; checked on the host).
+// 8192 tokens x 4096 channels x 16 states, all kernels: 882 us; three CTAs an SM with 112 registers and half
+// a tile's history a walker 941; two with half a tile 915; every warp doing all phases in turn 965.
+__host__ __device__ constexpr int regs_side(int walkers) { return walkers == 128 ? 64 : 48; }
+__host__ __device__ constexpr int regs_walk(int walkers) { return walkers == 128 ? 192 : 96; }
+
 template <typename T, int S>
-__global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 512 : 384) / Geo<T, S, 2>::NT) scan_grad_kernel(const __grid_constant__ BwdParams q) {
+__global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_grad_kernel(const __grid_constant__ BwdParams q) {
+    using M = GradMem<T, S>;
     using F = Geo<T, S, 2>;
-    constexpr int L = F::L, NT = F::NT, VN = F::VN;
+    constexpr int L = F::L, CB = F::CB, WALK = M::WALK, SIDE = M::SIDE, NT = M::NT;
+    constexpr int kFull = 1, kDone = 3, kLeft = 5, kSums = 6;  // named barriers, the first two one per buffer
     extern __shared__ __align__(16) unsigned char raw[];
-    GradMem<T, S>& sm = *reinterpret_cast<GradMem<T, S>*>(raw);
-    Input<T, S>& in = sm.in;
+    M& sm = *reinterpret_cast<M*>(raw);
     Where w;
     const bool some = where<T, S>(q, w);
     const Params& p = q.f;
     const int64_t C = p.C;
     if (!some) {  // no segment of this number: its parts of the sums are zero
-        const int64_t at = (int64_t)w.seg * C + w.c0, n = min(F::CB, p.CG - w.cg0);
+        const int64_t at = (int64_t)w.seg * C + w.c0, n = min(CB, p.CG - w.cg0);
         for (int i = threadIdx.x; i < n * S; i += NT) q.seg_g[at * S + i] = 0.f;
         for (int i = threadIdx.x; i < n; i += NT) q.pD[at + i] = q.pb[at + i] = 0.f;
         return;
     }
-    const Feed<T, S, 2> feed(q, w);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tiles = (w.hi - w.lo + kTile - 1) / kTile;
-    feed.copy(in, w.lo + (tiles - 1) * kTile, 0);
-    feed.columns(in, w);
+
+    if (threadIdx.x >= WALK) {
+        if constexpr (M::SIDE == 128) regs_less<regs_side(WALK)>();
+        const int tid = threadIdx.x - WALK, row0 = tid / M::CH, ch = tid % M::CH, col = 4 * ch;
+        const bool cok = w.cg0 + col < p.CG, gate = p.z != nullptr;
+        const int c = w.c0 + col;
+        auto has = [&](int t0, int r) { return row0 + r * M::RS < kTile && t0 + row0 + r * M::RS < w.hi && cok; };
+        auto copy = [&](int t0, int buf) {
+#pragma unroll
+            for (int r = 0; r < M::NV; ++r) {
+                const int tt = row0 + r * M::RS;
+                const int64_t t = t0 + tt;
+                if (has(t0, r)) {
+                    copy4_async(&sm.x[buf][tt][ch], static_cast<const T*>(p.x) + t * p.ldx + c);
+                    copy4_async(&sm.dt[buf][tt][ch], static_cast<const T*>(p.dt) + t * p.lddt + c);
+                    copy4_async(&sm.dy[buf][tt][ch], static_cast<const T*>(q.dy) + t * p.C + c);
+                    if (gate) copy4_async(&sm.z[buf][tt][ch], static_cast<const T*>(p.z) + t * p.ldz + c);
+                }
+            }
+            for (int v = tid; v < M::NBC; v += SIDE) {
+                const int which = v / (kTile * S / 4), k = v % (kTile * S / 4);
+                const int64_t t = t0 + k / (S / 4);
+                const int e = w.g * S + k % (S / 4) * 4;
+                if (t < w.hi)
+                    copy4_async(&sm.in[buf][v], which ? static_cast<const T*>(p.Cm) + t * p.ldC + e : static_cast<const T*>(p.B) + t * p.ldB + e);
+            }
+            copy_commit();
+        };
+        float2 D[2], sD[2], sb[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            D[e] = cok && p.D ? make_float2(__ldg(p.D + c + 2 * e), __ldg(p.D + c + 2 * e + 1)) : both(0.f);
+            sD[e] = sb[e] = both(0.f);
+        }
+        auto prepare = [&](int t0, int buf) {
+#pragma unroll
+            for (int r = 0; r < M::NV; ++r) {
+                const int tt = row0 + r * M::RS;
+                if (tt >= kTile) continue;
+                if (!has(t0, r)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sm.d[buf][tt][place(col + e)] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    continue;
+                }
+                float2 xv[2], dv[2], ev[2], zv[2];
+                unpack4(sm.x[buf][tt][ch], xv);
+                unpack4(sm.dt[buf][tt][ch], dv);
+                unpack4(sm.dy[buf][tt][ch], ev);
+                if (gate) unpack4(sm.z[buf][tt][ch], zv);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 bias = p.bias ? make_float2(__ldg(p.bias + c + 2 * e), __ldg(p.bias + c + 2 * e + 1)) : both(0.f);
+                    float2 d = __fadd2_rn(dv[e], bias), sig = both(1.f), u, s;
+                    if (p.softplus) {
+                        const float2 v = d;
+                        d = softplus2(v, u);
+                        sig = sigmoid2(v, u);
+                    }
+                    const float2 dx = __fmul2_rn(d, xv[e]);
+                    const float2 g = gate ? __fmul2_rn(ev[e], silu2(zv[e], s)) : ev[e];
+                    sm.d[buf][tt][place(col + 2 * e)] = make_float4(d.x, dx.x, g.x, sig.x);
+                    sm.d[buf][tt][place(col + 2 * e + 1)] = make_float4(d.y, dx.y, g.y, sig.y);
+                }
+            }
+            for (int v = tid; v < M::NBC; v += SIDE) {
+                const int k = v % (kTile * S / 4);
+                float2 f[2];
+                unpack4(sm.in[buf][v], f);
+                reinterpret_cast<float4*>(&sm.b[buf][0][0][0])[v] =
+                    t0 + k / (S / 4) < w.hi ? make_float4(f[0].x, f[0].y, f[1].x, f[1].y) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            bar_arrive(kFull + buf, NT);
+        };
+        auto finish = [&](int t0, int buf) {
+            const auto& bc = sm.bc[M::PB > 1 ? buf : 0];
+            for (int f = tid; f < min(kTile, w.hi - t0) * 2 * S; f += SIDE) {
+                float s = (&bc[0][0][0])[f];
+#pragma unroll
+                for (int i = 1; i < WALK / 32; ++i) s = __fadd_rn(s, (&bc[i][0][0])[f]);
+                q.bc[((int64_t)w.blk * p.T + t0) * 2 * S + f] = s;
+            }
+            if (M::PB == 1 && t0 > w.lo) bar_arrive(kLeft, NT);
+#pragma unroll
+            for (int r = 0; r < M::NV; ++r) {
+                if (!has(t0, r)) break;
+                const int tt = row0 + r * M::RS;
+                const int64_t to = (int64_t)(t0 + tt) * C + c;
+                float2 xv[2], odx[2], odt[2], odz[2];
+                unpack4(sm.x[buf][tt][ch], xv);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float4 v0 = sm.d[buf][tt][place(col + 2 * e)], v1 = sm.d[buf][tt][place(col + 2 * e + 1)];
+                    const float2 d = make_float2(v0.x, v1.x), g = make_float2(v0.z, v1.z), sig = make_float2(v0.w, v1.w);
+                    const float2 u = *reinterpret_cast<const float2*>(&sm.uvy[buf][0][tt][col + 2 * e]);
+                    const float2 v = __fmul2_rn(*reinterpret_cast<const float2*>(&sm.uvy[buf][1][tt][col + 2 * e]), both(kLn2));
+                    odx[e] = __ffma2_rn(d, u, __fmul2_rn(D[e], g));
+                    odt[e] = __fmul2_rn(__ffma2_rn(xv[e], u, v), sig);
+                    sD[e] = __ffma2_rn(g, xv[e], sD[e]);
+                    sb[e] = __fadd2_rn(sb[e], odt[e]);
+                }
+                store4_stream(static_cast<T*>(q.dx) + to, odx);
+                store4_stream(static_cast<T*>(q.ddt) + to, odt);
+                if (gate) {
+                    float2 ev[2], zv[2];
+                    unpack4(sm.dy[buf][tt][ch], ev), unpack4(sm.z[buf][tt][ch], zv);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float2 s;
+                        const float2 y = __ffma2_rn(D[e], xv[e], *reinterpret_cast<const float2*>(&sm.uvy[buf][2][tt][col + 2 * e]));
+                        silu2(zv[e], s);
+                        const float2 slope = __fmul2_rn(s, __ffma2_rn(zv[e], __ffma2_rn(s, both(-1.f), both(1.f)), both(1.f)));
+                        odz[e] = __fmul2_rn(__fmul2_rn(ev[e], y), slope);
+                    }
+                    store4_stream(static_cast<T*>(q.dz) + to, odz);
+                }
+            }
+        };
+        auto at = [&](int i) { return w.lo + (tiles - 1 - i) * kTile; };  // the i-th tile walked
+        copy(at(0), 0);
+        copy_wait<0>();
+        prepare(at(0), 0);
+        if (tiles > 1) copy(at(1), 1);
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i) {
+            const int buf = i & 1;
+            if (i + 1 < tiles) {
+                copy_wait<0>();
+                prepare(at(i + 1), buf ^ 1);
+            }
+            bar_sync(kDone + buf, NT);
+            finish(at(i), buf);
+            if (i + 2 < tiles) copy(at(i + 2), buf);
+        }
+        // the columns' sums over these threads, in the order of their rows
+        float2* sums = reinterpret_cast<float2*>(&sm.uvy[0][0][0][0]);
+        bar_sync(kSums, SIDE);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sums[(2 * tid + e) * 2] = sD[e], sums[(2 * tid + e) * 2 + 1] = sb[e];
+        bar_sync(kSums, SIDE);
+        for (int f = tid; f < 2 * CB; f += SIDE) {
+            const int k = f % CB, e = k % 4 / 2;
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < (M::RS < kTile ? M::RS : kTile); ++r) {
+                const float2 v = sums[(2 * (r * M::CH + k / 4) + e) * 2 + (f >= CB)];
+                s = __fadd_rn(s, k & 1 ? v.y : v.x);
+            }
+            if (w.cg0 + k < p.CG) (f < CB ? q.pD : q.pb)[(int64_t)w.seg * C + w.c0 + k] = s;
+        }
+        return;
+    }
+
+    if constexpr (M::SIDE == 128) regs_more<regs_walk(WALK)>();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const bool gate = p.z != nullptr;
     const int j = tid % L, jq = j & 1, cl = tid / L * 2, pm = tid / L & 1;
     const bool ok = w.cg0 + cl < p.CG;
     const int64_t own = ok ? (int64_t)(w.c0 + cl) * S + 4 * j : 0;
@@ -429,12 +617,7 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 51
             dA[c][i] = both(0.f);
         }
     }
-#pragma unroll
-    for (int e = 0; e < VN; ++e) sm.sums[e][tid] = both(0.f);
-
-    __syncthreads();
     for (int k = tiles - 1, buf = 0; k >= 0; --k, buf ^= 1) {
-        const int t0 = w.lo + k * kTile;
         copy_wait<0>();
         float2 h[2][2];
 #pragma unroll
@@ -447,16 +630,16 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 51
                 if (k) h[c][i] = __ffma2_rn(ex2_2(__fmul2_rn(both(cum[c]), A2[c][i])), h[c][i], s[i]);
                 if (!ok) h[c][i] = both(0.f);
             }
-            sm.h[c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
         }
         cum[0] = cum_of(k - 1, 0), cum[1] = cum_of(k - 1, 1);
-        feed.prepare(in, t0, buf);
-        __syncthreads();
-        if (k) feed.copy(in, t0 - kTile, buf ^ 1);
         copy_tile(k - 1);
+        bar_sync(kFull + buf, NT);
+        if (M::PB == 1 && k < tiles - 1) bar_sync(kLeft, NT);
+        auto& bc = sm.bc[M::PB > 1 ? buf : 0];
+        auto& uvy = sm.uvy[buf];
 
         auto pairs = [&](int which, int t, float2 (&v)[2]) {
-            const float2* from = reinterpret_cast<const float2*>(&in.b[which][t][4 * j]);
+            const float2* from = reinterpret_cast<const float2*>(&sm.b[buf][which][t][4 * j]);
             v[0] = from[pm], v[1] = from[pm ^ 1];
         };
         auto step = [&](int t, const float2 (&from)[2][2], float2 (&to)[2][2]) {
@@ -465,7 +648,7 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 51
             pairs(0, t, b);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float2 v = *reinterpret_cast<const float2*>(&in.d[t][c ? at1 : at0]);
+                const float2 v = *reinterpret_cast<const float2*>(&sm.d[buf][t][c ? at1 : at0]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     to[c][i] = from[c][i];
@@ -473,20 +656,25 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 51
                 }
             }
         };
+        // H tokens at a time: with H = kTile / 2 the second half of the tile, then, from its start again, the first
+        constexpr int H = M::H;
+        if constexpr (H < kTile) {
 #pragma unroll
-        for (int t = 0; t < kTile / 2; ++t) step(t, h, h);
-        // the second half of the tile, then, from its start again, the first
+            for (int c = 0; c < 2; ++c) sm.h[c][tid] = make_float4(h[c][0].x, h[c][0].y, h[c][1].x, h[c][1].y);
+#pragma unroll
+            for (int t = 0; t < H; ++t) step(t, h, h);
+        }
 #pragma unroll 1
-        for (int half = kTile / 2; half >= 0; half -= kTile / 2) {
-            float2 old[kTile / 2 + 1][2][2];  // the states before each token of the half, and behind the last
+        for (int half = kTile - H; half >= 0; half -= H) {
+            float2 old[H + 1][2][2];  // the states before each of these tokens, and behind the last
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) old[0][c][i] = h[c][i];
 #pragma unroll
-            for (int t = 0; t < kTile / 2; ++t) step(half + t, old[t], old[t + 1]);
+            for (int t = 0; t < H; ++t) step(half + t, old[t], old[t + 1]);
 #pragma unroll
-            for (int t = kTile / 2 - 1; t >= 0; --t) {
+            for (int t = H - 1; t >= 0; --t) {
                 float2 b[2], kc[2], sB[2], sC[2];
                 float us[2], vs[2], ys[2];
                 fence();
@@ -494,7 +682,7 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 51
                 pairs(1, half + t, kc);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float4 v = in.d[half + t][c ? at1 : at0];
+                    const float4 v = sm.d[buf][half + t][c ? at1 : at0];
                     float2 u, x, y;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -512,70 +700,30 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 51
                     us[c] = __fadd_rn(u.x, u.y), vs[c] = __fadd_rn(x.x, x.y), ys[c] = __fadd_rn(y.x, y.y);
                 }
                 const float u = sum_states<L>(us), v = sum_states<L>(vs);
-                if (j < 2) sm.uvy[0][half + t][cl + jq] = u, sm.uvy[1][half + t][cl + jq] = v;
-                if (feed.gate()) {
+                if (j < 2) uvy[0][half + t][cl + jq] = u, uvy[1][half + t][cl + jq] = v;
+                if (gate) {
                     const float y = sum_states<L>(ys);
-                    if (j < 2) sm.uvy[2][half + t][cl + jq] = y;
+                    if (j < 2) uvy[2][half + t][cl + jq] = y;
                 }
                 const float2 db = sum_channels<L>(sB), dc = sum_channels<L>(sC);
                 if constexpr (32 / L >= 4) {
                     if (lane / L < 4) {
-                        float* to = &sm.bc[warp][half + t][4 * j + 2 * pm + (lane / L >> 1)];
+                        float* to = &bc[warp][half + t][4 * j + 2 * pm + (lane / L >> 1)];
                         to[0] = db.x, to[S] = dc.x;
                     }
                 } else {
-                    float2* to = reinterpret_cast<float2*>(&sm.bc[warp][half + t][4 * j + 2 * pm]);
+                    float2* to = reinterpret_cast<float2*>(&bc[warp][half + t][4 * j + 2 * pm]);
                     to[0] = db, to[S / 2] = dc;
                 }
             }
+            if constexpr (H < kTile)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float4 u = sm.h[c][tid];
-                h[c][0] = make_float2(u.x, u.y), h[c][1] = make_float2(u.z, u.w);
-            }
-        }
-        __syncthreads();
-        // per (token, channel): this thread's chunks
-#pragma unroll
-        for (int r = 0; r < F::NV; ++r) {
-            if (!feed.has(t0, r)) break;
-            const int tt = feed.row0 + r * F::RS, col = feed.col;
-            const int64_t to = (int64_t)(t0 + tt) * C + w.c0 + col;
-            float2 xv[VN / 2], ev[VN / 2], zv[VN / 2];
-            float odx[VN], odt[VN], odz[VN];
-            unpack2(in.x[buf][tt][feed.ch], xv);
-            if (feed.gate()) unpack2(in.dy[buf][tt][feed.ch], ev), unpack2(in.z[buf][tt][feed.ch], zv);
-#pragma unroll
-            for (int e = 0; e < VN / 2; ++e) {
-                const float4 v0 = in.d[tt][place(col + 2 * e)], v1 = in.d[tt][place(col + 2 * e + 1)];
-                const float2 d = make_float2(v0.x, v1.x), g = make_float2(v0.z, v1.z), sig = make_float2(v0.w, v1.w);
-                const float2 u = *reinterpret_cast<const float2*>(&sm.uvy[0][tt][col + 2 * e]);
-                const float2 v = __fmul2_rn(*reinterpret_cast<const float2*>(&sm.uvy[1][tt][col + 2 * e]), both(kLn2));
-                const float2 D = *reinterpret_cast<const float2*>(&in.D[col + 2 * e]);
-                const float2 dx = __ffma2_rn(d, u, __fmul2_rn(D, g));
-                const float2 dt = __fmul2_rn(__ffma2_rn(xv[e], u, v), sig);
-                odx[2 * e] = dx.x, odx[2 * e + 1] = dx.y, odt[2 * e] = dt.x, odt[2 * e + 1] = dt.y;
-                sm.sums[2 * e][tid] = __ffma2_rn(g, xv[e], sm.sums[2 * e][tid]);
-                sm.sums[2 * e + 1][tid] = __fadd2_rn(sm.sums[2 * e + 1][tid], dt);
-                if (feed.gate()) {
-                    float2 s;
-                    const float2 y = __ffma2_rn(D, xv[e], *reinterpret_cast<const float2*>(&sm.uvy[2][tt][col + 2 * e]));
-                    silu2(zv[e], s);
-                    const float2 slope = __fmul2_rn(s, __ffma2_rn(zv[e], __ffma2_rn(s, both(-1.f), both(1.f)), both(1.f)));
-                    const float2 dz = __fmul2_rn(__fmul2_rn(ev[e], y), slope);
-                    odz[2 * e] = dz.x, odz[2 * e + 1] = dz.y;
+                for (int c = 0; c < 2; ++c) {
+                    const float4 u = sm.h[c][tid];
+                    h[c][0] = make_float2(u.x, u.y), h[c][1] = make_float2(u.z, u.w);
                 }
-            }
-            st16_stream(static_cast<T*>(q.dx) + to, pack(odx));
-            st16_stream(static_cast<T*>(q.ddt) + to, pack(odt));
-            if (feed.gate()) st16_stream(static_cast<T*>(q.dz) + to, pack(odz));
         }
-        for (int f = tid; f < min(kTile, w.hi - t0) * 2 * S; f += NT) {
-            float s = (&sm.bc[0][0][0])[f];
-#pragma unroll
-            for (int i = 1; i < NT / 32; ++i) s = __fadd_rn(s, (&sm.bc[i][0][0])[f]);
-            q.bc[((int64_t)w.blk * p.T + t0) * 2 * S + f] = s;
-        }
+        bar_arrive(kDone + buf, NT);
     }
     copy_wait<0>();
     if (ok) {
@@ -586,18 +734,6 @@ __global__ void __launch_bounds__(Geo<T, S, 2>::NT, (Geo<T, S, 2>::NT > 128 ? 51
             const float2 v[2] = {pm ? dA[c][1] : dA[c][0], pm ? dA[c][0] : dA[c][1]};
             store_state(q.seg_g + (int64_t)w.seg * C * S + (c ? so1 : so0), v);
         }
-    }
-    // the columns' sums over this CTA's threads, in the order of their rows
-    __syncthreads();
-    for (int f = tid; f < 2 * F::CB; f += NT) {
-        const int c = f % F::CB, e = c % VN / 2 * 2 + (f >= F::CB);
-        float s = 0.f;
-#pragma unroll
-        for (int r = 0; r < F::RS; ++r) {
-            const float2 v = sm.sums[e][r * F::CH + c / VN];
-            s = __fadd_rn(s, c & 1 ? v.y : v.x);
-        }
-        if (w.cg0 + c < p.CG) (f < F::CB ? q.pD : q.pb)[(int64_t)w.seg * C + w.c0 + c] = s;
     }
 }
 
@@ -676,6 +812,13 @@ Layout layout(const gdn_scan_shape* s) {
 }
 
 template <typename T, int S>
+bool registers_fit() {
+    using M = GradMem<T, S>;
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, scan_grad_kernel<T, S>) == cudaSuccess &&
+           a.numRegs * M::NT >= regs_side(M::WALK) * M::SIDE + regs_walk(M::WALK) * M::WALK;
+}
+template <typename T, int S>
 gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     const Params& p = q.f;
     const long long ctas = segs * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S / 4 + 15) / 16;
@@ -683,6 +826,10 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     const long long joins = ((long long)p.C * S / 4 + 127) / 128 * p.N;
     if (ctas >= (1LL << 31) || bc + par >= (1LL << 31) || joins >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
     constexpr size_t smem = sizeof(GradMem<T, S>);
+    if constexpr (GradMem<T, S>::SIDE == 128) {  // the walkers' registers, for which they would wait for ever
+        static const bool fit = registers_fit<T, S>();
+        if (!fit) return GDN_ERR_UNSUPPORTED;
+    }
     if constexpr (smem > 48 * 1024) {
         if (cudaFuncSetAttribute(scan_grad_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return GDN_ERR_CUDA;
@@ -690,7 +837,7 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     if (p.N > 0) {
         if (p.T > 0) scan_local_kernel<T, S><<<(unsigned)ctas, Geo<T, S, 4>::NT, 0, s>>>(q);
         scan_join_kernel<<<dim3((unsigned)joins, 2), 128, 0, s>>>(q, S);
-        if (p.T > 0) scan_grad_kernel<T, S><<<(unsigned)ctas, Geo<T, S, 2>::NT, smem, s>>>(q);
+        if (p.T > 0) scan_grad_kernel<T, S><<<(unsigned)ctas, GradMem<T, S>::NT, smem, s>>>(q);
     }
     scan_sums_kernel<T, S><<<(unsigned)(bc + par), 256, 0, s>>>(q, (unsigned)bc, p.T > 0 ? (int)segs : 0);
     return launch_status();
