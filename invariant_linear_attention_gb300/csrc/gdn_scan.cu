@@ -31,6 +31,9 @@ __device__ __forceinline__ float scatter_sum(float (&s)[L], int j) {
 // more than one CTA, the longest walks must neither start last nor share an SM: 16 ragged prompts,
 // 16384 x 8192 x 16, one channel a lane, take 603 us in order of number and 567 in order of length;
 // two CTAs an SM, all resident from the start (8192 x 2048 x 16), 188 and 149.
+// A CTA's N^2 comparisons have to be few against its walk of T / N tokens: ranked and not, 256
+// sequences take 470 and 218 us at 4096 x 8192 x 16, 300 and 306 at 65536 x 1024, 554 and 652 at
+// 131072 x 1024; hence N^3 <= 256 T.
 constexpr int kRanked = 256;
 __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
     __shared__ int len[kRanked], found;
@@ -452,7 +455,8 @@ struct FwdK {
         Params q = p;
         q.bpg = (p.CG + F::CB - 1) / F::CB;
         const unsigned blocks = (unsigned)(q.bpg * q.G);
-        q.ranked = p.N > 1 && p.N <= kRanked && (long long)blocks * p.N > kSMs;
+        const long long n = p.N;
+        q.ranked = n > 1 && n <= kRanked && blocks * n > kSMs && n * n * n <= 256LL * p.T;
         scan_fwd_kernel<T, S, Q><<<blocks * p.N, F::NT, sizeof(F), s>>>(q);
         return launch_status();
     }
