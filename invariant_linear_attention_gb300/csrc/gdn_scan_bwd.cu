@@ -793,10 +793,11 @@ Layout layout(const gdn_scan_shape* s) {
     const int cb = channels_of(s->S), cg = s->C / s->G;
     Layout l;
     l.bpg = (cg + cb - 1) / cb;
-    // Tiles per segment: long segments save traffic and joins (8192 tokens x 4096 channels: 1089 us
-    // at 4, 1012 at 8, 990 at 16), short ones give a small batch CTAs to run side by side.
+    // Tiles per segment: long segments save traffic and joins, short ones give a small batch CTAs
+    // to run side by side.  us at 2 / 4 / 8 / 16, bf16, 16 states: 512 tokens x 512 channels 30 / 34 / 46 / 77,
+    // 2048 x 1024 93 / 83 / 85 / 93, 2048 x 2048 167 / 144 / 138 / 150, 16384 x 1024 665 / 538 / 482 / 468.
     auto ctas = [&](int m) { return ((long long)s->T_total / (m * kTile) + s->N) * s->G * l.bpg; };
-    l.m = ctas(16) >= 16LL * kSMs ? 16 : ctas(8) >= 4LL * kSMs ? 8 : 2;
+    l.m = ctas(16) >= 8LL * kSMs ? 16 : ctas(8) >= 4LL * kSMs ? 8 : ctas(4) >= 2LL * kSMs ? 4 : 2;
     l.segs = (long long)s->T_total / (l.m * kTile) + s->N;
     const size_t c = s->C, cs = c * s->S, n = (size_t)l.segs;
     l.tiles = 0;
