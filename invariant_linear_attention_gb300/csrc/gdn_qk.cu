@@ -12,7 +12,6 @@
 // groups per pass, several passes' loads at once, and goes on to the token's other heads with the same
 // angles in registers.  Packed pairs of values: issue slots bound the first version (17 a value).
 #include "../../include/gdn_layer.h"
-#include "gdn_async.cuh"
 #include "gdn_host.h"
 #include "gdn_vec.cuh"
 
@@ -93,18 +92,6 @@ struct Angles {
                 s[e] = ns[e], ns[e] = t;
             }
         }
-    }
-    // The negative angles from a lane's chunks in shared memory, `step` chunks apart.
-    __device__ __forceinline__ void take(const uint4* from, int step, bool rot) {
-#pragma unroll
-        for (int e = 0; e < VN / 2; e += 2) {
-            const float4 c4 = rot ? *reinterpret_cast<const float4*>(from + e / 2 * step) : make_float4(1.f, 1.f, 1.f, 1.f);
-            const float4 s4 = rot ? *reinterpret_cast<const float4*>(from + (VN / 4 + e / 2) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
-            c[e] = make_float2(c4.x, c4.y), c[e + 1] = make_float2(c4.z, c4.w);
-            ns[e] = make_float2(s4.x, s4.y), ns[e + 1] = make_float2(s4.z, s4.w);
-        }
-#pragma unroll
-        for (int e = 0; e < VN / 2; ++e) s[e] = make_float2(-ns[e].x, -ns[e].y);
     }
     // (u, v) -> (u c - v s, v c + u s).  Halves: u in the first chunk, v in the second; neighbours: a pair is (u, v).
     template <bool INTER>
@@ -212,31 +199,14 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
     }
 }
 
-// The gradient's shared memory: each lane's own chunks of the passes at hand and the next ones, each
-// warp's angles of the token at hand and the next one; behind the last token the groups' sums.
-template <int VN>
-struct QkStage {
-    static constexpr int UR = 2, AC = VN / 4;  // passes together; 16-byte chunks of a lane's cosines (sines)
-    uint4 rows[2][UR][4][256];
-    uint4 angles[1];  // [2][8 warps][2 AC][lpr]
-    static __host__ __device__ size_t size(int lpr) { return sizeof(uint4) * (2 * UR * 4 * 256 + 2 * 8 * 2 * AC * lpr); }
-};
-
-// The next passes' rows, and the next token's angles, travel to shared memory without registers while
-// the present ones are at work (32768 x 32 x 128, weights: 149 us with loads into registers before
-// each pass, 143 so).
 template <typename T, bool INTER, bool PART, bool HASW>
 __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ QkParams p) {
-    constexpr int VN = V16<T>::n;
-    using Stage = QkStage<VN>;
-    constexpr int UR = Stage::UR, AC = Stage::AC;
-    extern __shared__ __align__(16) unsigned char raw[];
-    Stage& sm = *reinterpret_cast<Stage*>(raw);
-    float* acc = reinterpret_cast<float*>(raw);  // [256 / lpr groups][d]
+    constexpr int VN = V16<T>::n, UR = 2;
+    extern __shared__ float acc[];  // [256 / lpr groups][d]
     const int lane = threadIdx.x & 31, u = lane & (p.lpr - 1), sub = lane / p.lpr, hpw = 32 / p.lpr;
     const Unit un = unit_of<VN>(u, p.d, p.rd, p.inter);
     const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    uint4* angles = sm.angles + (threadIdx.x >> 5) * 2 * AC * p.lpr + u;  // buffer b, chunk c: [(b * 8 * 2 AC + c) * lpr]
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
     for (int side = 0; side < 2; ++side) {  // q, then k
         const int H = side ? p.HK : p.HQ, np = side ? p.pk : p.pq;
@@ -252,63 +222,34 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
             for (int e = 0; e < VN; ++e) sum[e] = twice(0.f);
         }
         const int per = (np + p.passes - 1) / p.passes;  // items of a token
-        const int64_t items = p.T * per;
-        auto token = [&](int64_t it) { return per == 1 ? it : it / per; };
-        auto first_of = [&](int64_t it) { return per == 1 ? 0 : (int)(it % per) * p.passes; };
-        auto row_of = [&](int64_t it) { return it < items ? angle_row(p, token(it)) : -1; };
-        auto copy_rows = [&](int64_t t, int ps, int last, int buf) {
+        for (int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; it < p.T * per; it += nwarps) {
+            const int64_t t = per == 1 ? it : it / per;
+            const int first = per == 1 ? 0 : (int)(it % per) * p.passes, last = min(first + p.passes, np);
+            const int64_t row = angle_row(p, t);
+            if (row < 0) continue;
+            Angles<VN> an;
+            an.load(p, row, u, un.rot, true);
             const T* src = x + t * ld;
             const T* dsrc = dout + t * H * p.d;
-#pragma unroll
-            for (int i = 0; i < UR; ++i) {
-                const int h = (ps + i) * hpw + sub;
-                const bool ok = ps + i < last && h < H, a = ok && un.has0, b = ok && un.has1;
-                const int oa = a ? h * p.d + un.e0 : 0, ob = b ? h * p.d + un.e1 : 0;
-                copy16_async(&sm.rows[buf][i][0][threadIdx.x], src + oa, a);
-                copy16_async(&sm.rows[buf][i][1][threadIdx.x], src + ob, b);
-                copy16_async(&sm.rows[buf][i][2][threadIdx.x], dsrc + oa, a);
-                copy16_async(&sm.rows[buf][i][3][threadIdx.x], dsrc + ob, b);
-            }
-        };
-        auto copy_angles = [&](int64_t row, int buf) {
-            if (row < 0 || sub || !un.rot) return;
-#pragma unroll
-            for (int c = 0; c < 2 * AC; ++c)
-                copy16_async(&angles[(buf * 8 * 2 * AC + c) * p.lpr],
-                             (c < AC ? p.cos : p.sin) + row * (p.rd / 2) + u * VN + c % AC * 4);
-        };
-        int64_t it = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-        int64_t row = row_of(it), next_row = row_of(it + nwarps);
-        if (it < items) {
-            copy_rows(token(it), first_of(it), min(first_of(it) + p.passes, np), 0);
-            copy_angles(row, 0);
-        }
-        copy_commit();
-        int buf = 0, abuf = 0;
-        for (; it < items; it += nwarps, abuf ^= 1) {
-            const int64_t t = token(it), nxt = it + nwarps;
-            const int first = first_of(it), last = min(first + p.passes, np);
             T* dst = dx + t * ldd;
-            Angles<VN> an;
-            for (int ps = first; ps < last; ps += UR, buf ^= 1) {
-                if (ps + UR < last) {
-                    copy_rows(t, ps + UR, last, buf ^ 1);
-                } else if (nxt < items) {
-                    copy_rows(token(nxt), first_of(nxt), min(first_of(nxt) + p.passes, np), buf ^ 1);
-                    copy_angles(next_row, abuf ^ 1);
+            for (int ps = first; ps < last; ps += UR) {
+                uint4 ra[UR], rb[UR], ga[UR], gb[UR];
+#pragma unroll
+                for (int i = 0; i < UR; ++i) {
+                    const int h = (ps + i) * hpw + sub;
+                    const bool ok = ps + i < last && h < H;
+                    ra[i] = ok && un.has0 ? ld16_stream(src + h * p.d + un.e0) : none;
+                    rb[i] = ok && un.has1 ? ld16_stream(src + h * p.d + un.e1) : none;
+                    ga[i] = ok && un.has0 ? ld16_stream(dsrc + h * p.d + un.e0) : none;
+                    gb[i] = ok && un.has1 ? ld16_stream(dsrc + h * p.d + un.e1) : none;
                 }
-                copy_commit();
-                copy_wait<1>();
-                __syncwarp();
-                if (row < 0) continue;
-                if (ps == first) an.take(angles + abuf * 8 * 2 * AC * p.lpr, p.lpr, un.rot);
 #pragma unroll
                 for (int i = 0; i < UR; ++i) {
                     if (ps + i >= last) break;
                     const int h = (ps + i) * hpw + sub;
                     float2 v[VN], g[VN];
-                    unpack_unit<VN>(sm.rows[buf][i][0][threadIdx.x], sm.rows[buf][i][1][threadIdx.x], v);
-                    unpack_unit<VN>(sm.rows[buf][i][2][threadIdx.x], sm.rows[buf][i][3][threadIdx.x], g);
+                    unpack_unit<VN>(ra[i], rb[i], v);
+                    unpack_unit<VN>(ga[i], gb[i], g);
                     const float r = rsqrtf(__fmaf_rn(group_sum(dot<VN>(v, v), p.lpr), p.c, p.eps));
                     if (!PART || un.rot) an.template turn<INTER>(g);
                     if constexpr (HASW) {
@@ -326,14 +267,10 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
                     if (h < H && un.has1) st16_stream(dst + h * p.d + un.e1, pack_half<VN>(v + VN / 2));
                 }
             }
-            __syncwarp();  // the angles are read: their buffer takes the token after next's
-            row = next_row, next_row = row_of(nxt + nwarps);
         }
-        copy_wait<0>();
         // the CTA's sum for the weight: its lane groups in ascending order
         if constexpr (HASW) {
             if (!p.part) continue;
-            __syncthreads();
             float* mine = acc + (int64_t)(threadIdx.x / p.lpr) * p.d;
 #pragma unroll
             for (int e = 0; e < VN; ++e) {
@@ -417,24 +354,16 @@ void qk_launch(int grid, cudaStream_t s, const QkParams& p, bool w) {
     if (p.inter) part ? qk_launch2<T, true, true>(grid, s, p, w) : qk_launch2<T, true, false>(grid, s, p, w);
     else part ? qk_launch2<T, false, true>(grid, s, p, w) : qk_launch2<T, false, false>(grid, s, p, w);
 }
-template <typename T, bool INTER, bool PART, bool HASW>
-gdn_status qk_bwd_launch3(int grid, cudaStream_t s, const QkParams& p) {
-    // covers the groups' sums too: 256 / lpr rows of d <= 2 lpr VN floats, 2 KB VN
-    const size_t smem = QkStage<V16<T>::n>::size(p.lpr);
-    if (cudaFuncSetAttribute(qk_bwd_kernel<T, INTER, PART, HASW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return GDN_ERR_CUDA;
-    qk_bwd_kernel<T, INTER, PART, HASW><<<grid, 256, smem, s>>>(p);
-    return launch_status();
-}
 template <typename T, bool INTER, bool PART>
-gdn_status qk_bwd_launch2(int grid, cudaStream_t s, const QkParams& p, bool w) {
-    return w ? qk_bwd_launch3<T, INTER, PART, true>(grid, s, p) : qk_bwd_launch3<T, INTER, PART, false>(grid, s, p);
+void qk_bwd_launch2(int grid, size_t smem, cudaStream_t s, const QkParams& p, bool w) {
+    if (w) qk_bwd_kernel<T, INTER, PART, true><<<grid, 256, smem, s>>>(p);
+    else qk_bwd_kernel<T, INTER, PART, false><<<grid, 256, smem, s>>>(p);
 }
 template <typename T>
-gdn_status qk_bwd_launch(int grid, cudaStream_t s, const QkParams& p, bool w) {
+void qk_bwd_launch(int grid, size_t smem, cudaStream_t s, const QkParams& p, bool w) {
     const bool part = p.rd < p.d;
-    if (p.inter) return part ? qk_bwd_launch2<T, true, true>(grid, s, p, w) : qk_bwd_launch2<T, true, false>(grid, s, p, w);
-    return part ? qk_bwd_launch2<T, false, true>(grid, s, p, w) : qk_bwd_launch2<T, false, false>(grid, s, p, w);
+    if (p.inter) part ? qk_bwd_launch2<T, true, true>(grid, smem, s, p, w) : qk_bwd_launch2<T, true, false>(grid, smem, s, p, w);
+    else part ? qk_bwd_launch2<T, false, true>(grid, smem, s, p, w) : qk_bwd_launch2<T, false, false>(grid, smem, s, p, w);
 }
 
 // The gradient's items: a token with all its head passes where the tokens give every warp one, else
@@ -524,8 +453,11 @@ extern "C" gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_shape* shape, const void
     p.passes = qk_bwd_passes(shape, p);
     const int ctas = qk_bwd_ctas(shape);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t smem = sums ? (size_t)(256 / p.lpr) * p.d * sizeof(float) : 0;
     const bool w = q_weight || k_weight;
-    st = shape->dtype == GDN_BF16 ? qk_bwd_launch<__nv_bfloat16>(ctas, s, p, w) : qk_bwd_launch<float>(ctas, s, p, w);
+    if (shape->dtype == GDN_BF16) qk_bwd_launch<__nv_bfloat16>(ctas, smem, s, p, w);
+    else qk_bwd_launch<float>(ctas, smem, s, p, w);
+    st = launch_status();
     if (st != GDN_OK || !sums) return st;
     qk_bwd_sum_kernel<<<dim3((unsigned)((p.d + 15) / 16), 2), 256, 0, s>>>(p.d, ctas, p.part, dq_weight, dk_weight);
     return launch_status();
