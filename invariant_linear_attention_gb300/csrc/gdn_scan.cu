@@ -466,14 +466,15 @@ struct FwdK {
         return cudaFuncGetAttributes(&a, scan_fwd_kernel<T, S, 2>) == cudaSuccess && 2 * a.numRegs >= kRegsSide + kRegsWalk;
     }
     static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
-        // Two channels a lane from four blocks of an equally long sequence an SM on (figures above); with
-        // fewer they leave SMs idle.  The longest of N sequences is taken for up to min(N, 3) mean
-        // lengths: once it walks alone, a token takes twice as long with two channels a lane
-        // (16 ragged prompts, 12265 x 2760 x 16, 4.6 blocks an SM: 192 and 368 us; 16384 x 8192 x 16,
-        // 13 blocks: 567 and 543).  Not for 8 states: their walkers would be half a warpgroup.
+        // Two channels a lane from more than the three blocks on that an SM holds at once (4096 tokens x
+        // 8192 x 64, 3.4 blocks an SM: 915 and 583 us; with fewer, figures above, they leave SMs idle).  The
+        // longest of N sequences is taken for up to min(N, 3) mean lengths: once it walks alone, a token
+        // takes twice as long with two channels a lane (16 ragged prompts, 12265 x 2760 x 16, 4.6 blocks an
+        // SM: 192 and 368 us; 16384 x 8192 x 16, 13 blocks: 567 and 543).  Not for 8 states: their walkers
+        // would be half a warpgroup.
         if constexpr (S >= 16) {
             static const bool fit = two_fit();
-            if (fit && (long long)blocks * p.N >= 4LL * kSMs * (p.N < 3 ? p.N : 3)) return run<2>(s, p);
+            if (fit && (long long)blocks * p.N > 3LL * kSMs * (p.N < 3 ? p.N : 3)) return run<2>(s, p);
         }
         return run<1>(s, p);
     }
