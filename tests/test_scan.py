@@ -266,7 +266,7 @@ def test_backward_vs_oracle(dtype, S, G, C, gate, states):
 
 @pytest.mark.parametrize("dtype,S,G,C,lens", [(torch.float32, 8, 64, 512, [390, 0, 150, 64, 1]), (torch.bfloat16, 16, 56, 448, [390, 0, 150, 64, 1]),
                                               (torch.float32, 8, 500, 4000, [270, 0, 130]), (torch.bfloat16, 16, 16, 128, [390, 0, 150, 64, 1]),
-                                              (torch.float32, 64, 28, 224, [390, 0, 150, 64, 1]), (torch.bfloat16, 64, 44, 352, [390, 0, 150, 64, 1])])
+                                              (torch.bfloat16, 16, 320, 2560, [270, 0, 130]), (torch.float32, 64, 28, 224, [390, 0, 150, 64, 1]), (torch.bfloat16, 64, 44, 352, [390, 0, 150, 64, 1])])
 def test_backward_of_a_batch_with_many_ctas(dtype, S, G, C, lens):
     # enough channel blocks and tokens for the longer segments, sequences of several of them
     c = Case(lens, C, G, S, dtype, 23, slow=True)
