@@ -460,11 +460,6 @@ struct FwdK {
         scan_fwd_kernel<T, S, Q><<<blocks * p.N, F::NT, sizeof(F), s>>>(q);
         return launch_status();
     }
-    // Whether the walkers of the compiled kernel get their registers: else they would wait for ever.
-    static bool two_fit() {
-        cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, scan_fwd_kernel<T, S, 2>) == cudaSuccess && 2 * a.numRegs >= kRegsSide + kRegsWalk;
-    }
     static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
         // Two channels a lane from more than the three blocks on that an SM holds at once (4096 tokens x
         // 8192 x 64, 3.4 blocks an SM: 915 and 583 us; with fewer, figures above, they leave SMs idle).  The
@@ -473,8 +468,11 @@ struct FwdK {
         // SM: 192 and 368 us; 16384 x 8192 x 16, 13 blocks: 567 and 543).  Not for 8 states: their walkers
         // would be half a warpgroup.
         if constexpr (S >= 16) {
-            static const bool fit = two_fit();
-            if (fit && (long long)blocks * p.N > 3LL * kSMs * (p.N < 3 ? p.N : 3)) return run<2>(s, p);
+            static std::atomic<bool> known{false};
+            if ((long long)blocks * p.N > 3LL * kSMs * (p.N < 3 ? p.N : 3)) {
+                const gdn_status st = check_registers(scan_fwd_kernel<T, S, 2>, FwdTile<T, S, 2>::NT, 128 * (kRegsSide + kRegsWalk), known);
+                return st == GDN_OK ? run<2>(s, p) : st;
+            }
         }
         return run<1>(s, p);
     }

@@ -14,6 +14,8 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gdn_scan.h"
 #include "gdn_vec.cuh"
 
@@ -138,6 +140,18 @@ __device__ __forceinline__ float sum_states4(const float2 (&h)[2], const float2 
 }  // namespace scan
 
 // Host side.
+
+// Whether a kernel whose warpgroups move registers is launched with the `need` registers a CTA that
+// they then hold: they would wait for ever for more.  A good answer holds for the process.
+template <typename K>
+gdn_status check_registers(K* kernel, int threads, int need, std::atomic<bool>& known) {
+    if (known.load(std::memory_order_relaxed)) return GDN_OK;
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return GDN_ERR_CUDA;
+    if (a.numRegs * threads < need) return GDN_ERR_UNSUPPORTED;
+    known.store(true, std::memory_order_relaxed);
+    return GDN_OK;
+}
 inline gdn_status check_scan(const gdn_scan_shape* s) {
     if (!s) return GDN_ERR_INVALID_ARG;
     if (s->N < 0 || s->T_total < 0 || s->C <= 0 || s->G <= 0 || s->C % s->G) return GDN_ERR_INVALID_ARG;

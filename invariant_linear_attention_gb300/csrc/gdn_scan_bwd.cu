@@ -819,13 +819,6 @@ Layout layout(const gdn_scan_shape* s) {
 }
 
 template <typename T, int S>
-bool registers_fit() {
-    using M = GradMem<T, S>;
-    cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, scan_grad_kernel<T, S>) == cudaSuccess &&
-           a.numRegs * M::NT >= regs_side(M::WALK) * M::SIDE + regs_walk(M::WALK) * M::WALK;
-}
-template <typename T, int S>
 gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     const Params& p = q.f;
     const long long ctas = segs * p.G * p.bpg, bc = ((long long)p.T * p.G * 2 * S / 4 + 15) / 16;
@@ -833,9 +826,11 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     const long long joins = ((long long)p.C * S / 4 + 127) / 128 * p.N;
     if (ctas >= (1LL << 31) || bc + par >= (1LL << 31) || joins >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
     constexpr size_t smem = sizeof(GradMem<T, S>);
-    if constexpr (GradMem<T, S>::SIDE == 128) {  // the walkers' registers, for which they would wait for ever
-        static const bool fit = registers_fit<T, S>();
-        if (!fit) return GDN_ERR_UNSUPPORTED;
+    if constexpr (GradMem<T, S>::SIDE == 128) {
+        using M = GradMem<T, S>;
+        static std::atomic<bool> known{false};
+        const gdn_status st = check_registers(scan_grad_kernel<T, S>, M::NT, regs_side(M::WALK) * M::SIDE + regs_walk(M::WALK) * M::WALK, known);
+        if (st != GDN_OK) return st;
     }
     if constexpr (smem > 48 * 1024) {
         if (cudaFuncSetAttribute(scan_grad_kernel<T, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
