@@ -339,24 +339,14 @@ __device__ __forceinline__ float sum_states(const float (&v)[2]) {
     for (int off = 2; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
     return s;
 }
-// Sum of a lane's four states over the 32 / L lane groups.  Pair slot m of group k holds pair
-// m ^ (k & 1): the first slot stays, the second goes to the neighbour group; then (four groups
-// or more) a lane keeps x or y by the group's second bit, and further groups add by a butterfly.
+// Sum of a lane's four states over its lane group and its neighbour.  Pair slot m of group k holds pair
+// m ^ (k & 1): the first slot stays, the second goes to the neighbour group.  The groups' sums are
+// added up by the other warps, whose issue slots are fewer for it than the walkers' shuffles would be
+// (8192 x 4096 x 16: 885 us with the whole sum here, 818 so).
 template <int L>
-__device__ __forceinline__ float2 sum_channels(const float2 (&v)[2]) {
+__device__ __forceinline__ float2 sum_neighbours(const float2 (&v)[2]) {
     constexpr uint32_t all = 0xffffffffu;
-    float2 r;
-    r.x = __fadd_rn(v[0].x, __shfl_xor_sync(all, v[1].x, L));
-    r.y = __fadd_rn(v[0].y, __shfl_xor_sync(all, v[1].y, L));
-    if constexpr (32 / L >= 4) {
-        const bool up = (threadIdx.x & 31) / L & 2;
-        float s = up ? r.y : r.x;
-        s = __fadd_rn(s, __shfl_xor_sync(all, up ? r.x : r.y, 2 * L));
-#pragma unroll
-        for (int off = 4 * L; off < 32; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(all, s, off));
-        r.x = s;
-    }
-    return r;
+    return make_float2(__fadd_rn(v[0].x, __shfl_xor_sync(all, v[1].x, L)), __fadd_rn(v[0].y, __shfl_xor_sync(all, v[1].y, L)));
 }
 
 // Keeps the compiler from loading later tokens' values early: the states of a tile fill the registers.
@@ -391,12 +381,12 @@ struct GradMem {
     static constexpr int CH = CB / 4, RS = SIDE / CH, NV = (kTile + RS - 1) / RS;
     static constexpr int NBC = 2 * kTile * S / 4;
     static constexpr int H = WALK == 128 ? kTile : kTile / 2;  // tokens whose states are in registers at a time
-    static constexpr int PB = S < 64 ? 2 : 1;  // buffers of the warps' dB and dC: with two, 64 states would leave room for one CTA
+    static constexpr int PB = S == 16 || S == 32 ? 2 : 1;  // buffers of the lanes' dB and dC: with two, fewer than MINB CTAs find room
     // {d, d x, e, softplus'} of channel c at place(c); then B and C in fp32
     alignas(16) float4 d[2][kTile][CB];
     alignas(16) float b[2][2][kTile][S];
     alignas(16) float uvy[2][3][kTile][CB + 4];
-    alignas(16) float bc[PB][WALK / 32][kTile][2 * S];  // each warp's dB and dC
+    alignas(16) float4 bc[PB][kTile][WALK / 32][32];  // each lane's pair of dB and of dC, two groups of lanes added
     alignas(16) V x[2][kTile][CH], dt[2][kTile][CH], dy[2][kTile][CH], z[2][kTile][CH], in[2][NBC];
     // each walker's own: its segment's start states, the next tile's local ones, its states at the tile's start
     alignas(16) float4 seg[2][WALK];
@@ -408,7 +398,7 @@ struct GradMem {
 // Two channels' states, their gradients and a tile's history need more registers than the work
 // before and after: as in the forward, registers move to the walkers, no more than the CTA was
 // launched with (128 a thread at two CTAs of 256 threads, 80 at two of 384; checked on the host).
-// 8192 tokens x 4096 channels x 16 states, all kernels: 882 us; three CTAs an SM with 112 registers and half
+// 8192 tokens x 4096 channels x 16 states, all kernels, when this was chosen: 882 us; three CTAs an SM with 112 registers and half
 // a tile's history a walker 941; two with half a tile 915; every warp doing all phases in turn 965.
 __host__ __device__ constexpr int regs_side(int walkers) { return walkers == 128 ? 64 : 48; }
 __host__ __device__ constexpr int regs_walk(int walkers) { return walkers == 128 ? 192 : 96; }
@@ -506,12 +496,30 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
             bar_arrive(kFull + buf, NT);
         };
         auto finish = [&](int t0, int buf) {
+            // dB and dC: PT threads add up the warps' groups of one token and pair of states
             const auto& bc = sm.bc[M::PB > 1 ? buf : 0];
-            for (int f = tid; f < min(kTile, w.hi - t0) * 2 * S; f += SIDE) {
-                float s = (&bc[0][0][0])[f];
+            constexpr int OUT = kTile * 2 * L, PT = SIDE > OUT ? SIDE / OUT : 1, NW = WALK / 32 / PT;
+#pragma unroll 1
+            for (int f = tid; f < OUT * PT; f += SIDE) {
+                const int pm = f % (2 * L) / L, j = f % L, part = f / (2 * L) % PT, tt = f / (2 * L * PT);
+                float2 b2 = both(0.f), c2 = both(0.f);
 #pragma unroll
-                for (int i = 1; i < WALK / 32; ++i) s = __fadd_rn(s, (&bc[i][0][0])[f]);
-                q.bc[((int64_t)w.blk * p.T + t0) * 2 * S + f] = s;
+                for (int i = 0; i < NW; ++i)
+#pragma unroll
+                    for (int k = 0; k < 32 / L; k += 2) {
+                        const float4 v = bc[tt][part * NW + i][(k + pm) * L + j];
+                        b2 = __fadd2_rn(b2, make_float2(v.x, v.y)), c2 = __fadd2_rn(c2, make_float2(v.z, v.w));
+                    }
+#pragma unroll
+                for (int off = 1; off < PT; off <<= 1) {
+                    const float2 u = make_float2(__shfl_xor_sync(0xffffffffu, b2.x, 2 * L * off), __shfl_xor_sync(0xffffffffu, b2.y, 2 * L * off));
+                    const float2 v = make_float2(__shfl_xor_sync(0xffffffffu, c2.x, 2 * L * off), __shfl_xor_sync(0xffffffffu, c2.y, 2 * L * off));
+                    b2 = __fadd2_rn(b2, u), c2 = __fadd2_rn(c2, v);
+                }
+                if (part == 0 && t0 + tt < w.hi) {
+                    float* to = q.bc + ((int64_t)w.blk * p.T + t0 + tt) * 2 * S + 4 * j + 2 * pm;
+                    *reinterpret_cast<float2*>(to) = b2, *reinterpret_cast<float2*>(to + S) = c2;
+                }
             }
             if (M::PB == 1 && t0 > w.lo) bar_arrive(kLeft, NT);
 #pragma unroll
@@ -708,16 +716,8 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
                     const float y = sum_states<L>(ys);
                     if (j < 2) uvy[2][half + t][cl + jq] = y;
                 }
-                const float2 db = sum_channels<L>(sB), dc = sum_channels<L>(sC);
-                if constexpr (32 / L >= 4) {
-                    if (lane / L < 4) {
-                        float* to = &bc[warp][half + t][4 * j + 2 * pm + (lane / L >> 1)];
-                        to[0] = db.x, to[S] = dc.x;
-                    }
-                } else {
-                    float2* to = reinterpret_cast<float2*>(&bc[warp][half + t][4 * j + 2 * pm]);
-                    to[0] = db, to[S / 2] = dc;
-                }
+                const float2 db = sum_neighbours<L>(sB), dc = sum_neighbours<L>(sC);
+                bc[half + t][warp][lane] = make_float4(db.x, db.y, dc.x, dc.y);
             }
             if constexpr (H < kTile)
 #pragma unroll
