@@ -329,14 +329,17 @@ __global__ void __launch_bounds__(128) scan_join_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- 3. grad
-// Sum over the lanes of a channel.  Slot c of lane j holds channel c ^ (j & 1) of the lane's two:
-// the first slot stays, the second goes to the neighbour, whose first it is, without selecting;
-// further lanes add by a butterfly.  Lane j ends with channel j & 1.
-template <int L>
+// Sum over the lanes of a channel in UP parts: with eight lanes or more the last addition is left to
+// the other warps (2048 tokens x 2048 channels x 32 states, fp32: 428 and 416 us; with four lanes, 16
+// states, the walkers' code gets slower instead, 818 and 899 us for 8192 x 4096).
+// Slot c of lane j holds channel c ^ (j & 1) of the lane's two: the first slot stays, the second
+// goes to the neighbour, whose first it is, without selecting; further lanes add by a butterfly.
+// Lane j ends with channel j & 1 of part j / (L / UP).
+template <int L, int UP>
 __device__ __forceinline__ float sum_states(const float (&v)[2]) {
     float s = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[1], 1));
 #pragma unroll
-    for (int off = 2; off < L; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+    for (int off = 2; off < L / UP; off <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
     return s;
 }
 // Sum of a lane's four states over its lane group and its neighbour.  Pair slot m of group k holds pair
@@ -385,7 +388,8 @@ struct GradMem {
     // {d, d x, e, softplus'} of channel c at place(c); then B and C in fp32
     alignas(16) float4 d[2][kTile][CB];
     alignas(16) float b[2][2][kTile][S];
-    alignas(16) float uvy[2][3][kTile][CB + 4];
+    static constexpr int UP = F::L < 8 ? 1 : 2;
+    alignas(16) float uvy[2][3][kTile][UP][CB + (UP > 1 ? 16 : 4)];  // u, sum w A2, y in parts
     alignas(16) float4 bc[PB][kTile][WALK / 32][32];  // each lane's pair of dB and of dC, two groups of lanes added
     alignas(16) V x[2][kTile][CH], dt[2][kTile][CH], dy[2][kTile][CH], z[2][kTile][CH], in[2][NBC];
     // each walker's own: its segment's start states, the next tile's local ones, its states at the tile's start
@@ -529,12 +533,16 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
                 const int64_t to = (int64_t)(t0 + tt) * C + c;
                 float2 xv[2], odx[2], odt[2], odz[2];
                 unpack4(sm.x[buf][tt][ch], xv);
+                auto sum_of = [&](int which, int e) {
+                    float2 v = *reinterpret_cast<const float2*>(&sm.uvy[buf][which][tt][0][col + 2 * e]);
+                    if constexpr (M::UP > 1) v = __fadd2_rn(v, *reinterpret_cast<const float2*>(&sm.uvy[buf][which][tt][1][col + 2 * e]));
+                    return v;
+                };
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float4 v0 = sm.d[buf][tt][place(col + 2 * e)], v1 = sm.d[buf][tt][place(col + 2 * e + 1)];
                     const float2 d = make_float2(v0.x, v1.x), g = make_float2(v0.z, v1.z), sig = make_float2(v0.w, v1.w);
-                    const float2 u = *reinterpret_cast<const float2*>(&sm.uvy[buf][0][tt][col + 2 * e]);
-                    const float2 v = __fmul2_rn(*reinterpret_cast<const float2*>(&sm.uvy[buf][1][tt][col + 2 * e]), both(kLn2));
+                    const float2 u = sum_of(0, e), v = __fmul2_rn(sum_of(1, e), both(kLn2));
                     odx[e] = __ffma2_rn(d, u, __fmul2_rn(D[e], g));
                     odt[e] = __fmul2_rn(__ffma2_rn(xv[e], u, v), sig);
                     sD[e] = __ffma2_rn(g, xv[e], sD[e]);
@@ -548,7 +556,7 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float2 s;
-                        const float2 y = __ffma2_rn(D[e], xv[e], *reinterpret_cast<const float2*>(&sm.uvy[buf][2][tt][col + 2 * e]));
+                        const float2 y = __ffma2_rn(D[e], xv[e], sum_of(2, e));
                         silu2(zv[e], s);
                         const float2 slope = __fmul2_rn(s, __ffma2_rn(zv[e], __ffma2_rn(s, both(-1.f), both(1.f)), both(1.f)));
                         odz[e] = __fmul2_rn(__fmul2_rn(ev[e], y), slope);
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
             if (i + 2 < tiles) copy(at(i + 2), buf);
         }
         // the columns' sums over these threads, in the order of their rows
-        float2* sums = reinterpret_cast<float2*>(&sm.uvy[0][0][0][0]);
+        float2* sums = reinterpret_cast<float2*>(&sm.uvy[0][0][0][0][0]);
         bar_sync(kSums, SIDE);
 #pragma unroll
         for (int e = 0; e < 2; ++e) sums[(2 * tid + e) * 2] = sD[e], sums[(2 * tid + e) * 2 + 1] = sb[e];
@@ -710,11 +718,12 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
                     }
                     us[c] = __fadd_rn(u.x, u.y), vs[c] = __fadd_rn(x.x, x.y), ys[c] = __fadd_rn(y.x, y.y);
                 }
-                const float u = sum_states<L>(us), v = sum_states<L>(vs);
-                if (j < 2) uvy[0][half + t][cl + jq] = u, uvy[1][half + t][cl + jq] = v;
+                constexpr int LP = L / M::UP;  // lanes of a part; the first two of them keep it
+                const float u = sum_states<L, M::UP>(us), v = sum_states<L, M::UP>(vs);
+                if (j % LP < 2) uvy[0][half + t][j / LP][cl + jq] = u, uvy[1][half + t][j / LP][cl + jq] = v;
                 if (gate) {
-                    const float y = sum_states<L>(ys);
-                    if (j < 2) uvy[2][half + t][cl + jq] = y;
+                    const float y = sum_states<L, M::UP>(ys);
+                    if (j % LP < 2) uvy[2][half + t][j / LP][cl + jq] = y;
                 }
                 const float2 db = sum_neighbours<L>(sB), dc = sum_neighbours<L>(sC);
                 bc[half + t][warp][lane] = make_float4(db.x, db.y, dc.x, dc.y);
