@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(128) scan_join_kernel(const __grid_constant__ 
 }
 
 // ---------------------------------------------------------------- 3. grad
-// Sum over the lanes of a channel in UP parts: with eight lanes or more the last addition is left to
-// the other warps (2048 tokens x 2048 channels x 32 states, fp32: 428 and 416 us; with four lanes, 16
-// states, the walkers' code gets slower instead, 818 and 899 us for 8192 x 4096).
+// Sum over the lanes of a channel in UP parts: with four lanes or more the last addition is left to
+// the other warps (8192 tokens x 4096 channels x 16 states: 806 and 798 us; 4096 x 2048 x 32, fp32: 428
+// and 416).
 // Slot c of lane j holds channel c ^ (j & 1) of the lane's two: the first slot stays, the second
 // goes to the neighbour, whose first it is, without selecting; further lanes add by a butterfly.
 // Lane j ends with channel j & 1 of part j / (L / UP).
@@ -388,7 +388,7 @@ struct GradMem {
     // {d, d x, e, softplus'} of channel c at place(c); then B and C in fp32
     alignas(16) float4 d[2][kTile][CB];
     alignas(16) float b[2][2][kTile][S];
-    static constexpr int UP = F::L < 8 ? 1 : 2;
+    static constexpr int UP = F::L < 4 ? 1 : 2;
     alignas(16) float uvy[2][3][kTile][UP][CB + (UP > 1 ? 16 : 4)];  // u, sum w A2, y in parts
     alignas(16) float4 bc[PB][kTile][WALK / 32][32];  // each lane's pair of dB and of dC, two groups of lanes added
     alignas(16) V x[2][kTile][CH], dt[2][kTile][CH], dy[2][kTile][CH], z[2][kTile][CH], in[2][NBC];
@@ -402,10 +402,12 @@ struct GradMem {
 // Two channels' states, their gradients and a tile's history need more registers than the work
 // before and after: as in the forward, registers move to the walkers, no more than the CTA was
 // launched with (128 a thread at two CTAs of 256 threads, 80 at two of 384; checked on the host).
-// 8192 tokens x 4096 channels x 16 states, all kernels, when this was chosen: 882 us; three CTAs an SM with 112 registers and half
-// a tile's history a walker 941; two with half a tile 915; every warp doing all phases in turn 965.
-__host__ __device__ constexpr int regs_side(int walkers) { return walkers == 128 ? 64 : 48; }
-__host__ __device__ constexpr int regs_walk(int walkers) { return walkers == 128 ? 192 : 96; }
+// 8192 tokens x 4096 channels x 16 states, all kernels: 798 us at 80 and 176 registers, 816 at 64 and
+// 192, 828 at 88 and 168, 855 at 56 and 200.  Before the sums went to the other warps: two CTAs an SM
+// with a tile's history 882, with half a tile's 915, three with 112 registers and half a tile's 941;
+// every warp doing all phases in turn 965.
+__host__ __device__ constexpr int regs_side(int walkers) { return walkers == 128 ? 80 : 48; }
+__host__ __device__ constexpr int regs_walk(int walkers) { return walkers == 128 ? 176 : 96; }
 
 template <typename T, int S>
 __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_grad_kernel(const __grid_constant__ BwdParams q) {
