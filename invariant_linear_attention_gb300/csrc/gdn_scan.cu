@@ -58,8 +58,8 @@ __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
 //   * preparers, the work per (token, channel), 16-byte chunks of x and dt: d = softplus(dt + bias)
 //     and d x, and B and C in fp32, of tile i + 1 to shared memory;
 //   * walkers, the recurrence over tile i, a lane 8 states of Q channels (L = S / 8 lanes a
-//     channel), sum_s h C to shared memory;
-//   * finishers: skip term, gate and 16-byte stores of tile i - 1.
+//     channel), sum_s h C in UP parts to shared memory;
+//   * finishers: the parts' sum, skip term, gate and 16-byte stores of tile i - 1.
 // They meet at named barriers: full (tile prepared), free (its d, B, C read), done (its sums
 // written), left (its sums read), one of each per buffer; every side passes each barrier the
 // same number of times.  Preparers and finishers copy their own inputs, asynchronously, a tile
@@ -93,7 +93,10 @@ struct FwdTile {
     // States 8 j + 4 k .. of B (C) at float4 k L + j: the L lanes' loads touch consecutive chunks
     // (in order of states, 8 lanes would meet in the same banks: 64 states 6 % slower).
     float4 b[2][2][TT][2 * L];
-    alignas(16) float y[2][TT][YROW];
+    // Parts of a sum, whose last addition is the finishers' (full batches: 544 us with it in the walk, 538
+    // so; with one channel a lane the room for two parts would cost fp32 a CTA an SM).
+    static constexpr int UP = Q > 1 ? 2 : 1;
+    alignas(16) float y[2][TT][UP][YROW];
     uint4 x[ST][TT][CH], dt[ST][TT][CH], bc[ST][2 * TT * BCH];  // preparers'
     uint4 x2[ST][TT][CH], z[ST][TT][CH];                        // finishers'
     static_assert(SIDE % CH == 0, "a thread keeps its columns");
@@ -218,7 +221,9 @@ __global__ void __launch_bounds__(FwdTile<T, S, Q>::NT, FwdTile<T, S, Q>::MINB) 
                         if (gate) unpack2(sm.z[b3][tt][ch], zv);
 #pragma unroll
                         for (int e = 0; e < VN / 2; ++e) {
-                            float2 o = __ffma2_rn(D[e], xv[e], *reinterpret_cast<const float2*>(&sm.y[b2][tt][col + 2 * e]));
+                            float2 o = *reinterpret_cast<const float2*>(&sm.y[b2][tt][0][col + 2 * e]);
+                            if constexpr (F::UP > 1) o = __fadd2_rn(o, *reinterpret_cast<const float2*>(&sm.y[b2][tt][1][col + 2 * e]));
+                            o = __ffma2_rn(D[e], xv[e], o);
                             if (gate) o = __fmul2_rn(o, silu2(zv[e], sig));
                             out[2 * e] = o.x, out[2 * e + 1] = o.y;
                         }
@@ -278,9 +283,10 @@ __global__ void __launch_bounds__(FwdTile<T, S, Q>::NT, FwdTile<T, S, Q>::MINB) 
 #pragma unroll
             for (int q = 0; q < Q; ++q) sum[q] = __fadd_rn(acc[q].x, acc[q].y);
         };
+        constexpr int LP = L / F::UP;  // lanes of a part
         auto put = [&](int tt, const float (&v)[Q]) {
-            if constexpr (Q == 2) *reinterpret_cast<float2*>(&sm.y[b2][tt][cl]) = make_float2(v[0], v[1]);
-            else sm.y[b2][tt][cl] = v[0];
+            if constexpr (Q == 2) *reinterpret_cast<float2*>(&sm.y[b2][tt][j / LP][cl]) = make_float2(v[0], v[1]);
+            else sm.y[b2][tt][0][cl] = v[0];
         };
         constexpr int U = TT;  // tokens whose loads and exponentials run ahead of the recurrence (Q = 1, 8 of them: 583 us)
         if (len == TT) {
@@ -290,16 +296,16 @@ __global__ void __launch_bounds__(FwdTile<T, S, Q>::NT, FwdTile<T, S, Q>::MINB) 
 #pragma unroll
                 for (int k = 0; k < U; ++k) token(tt + k, s[k]);
 #pragma unroll
-                for (int k = 0; k < U; k += L) {
+                for (int k = 0; k < U; k += LP) {
                     float v[Q];
 #pragma unroll
                     for (int q = 0; q < Q; ++q) {
-                        float g[L];
+                        float g[LP];
 #pragma unroll
-                        for (int e = 0; e < L; ++e) g[e] = s[k + e][q];
-                        v[q] = scatter_sum<L>(g, j);
+                        for (int e = 0; e < LP; ++e) g[e] = s[k + e][q];
+                        v[q] = scatter_sum<LP>(g, j % LP);
                     }
-                    put(tt + k + j, v);
+                    put(tt + k + j % LP, v);
                 }
             }
         } else {
@@ -309,8 +315,8 @@ __global__ void __launch_bounds__(FwdTile<T, S, Q>::NT, FwdTile<T, S, Q>::MINB) 
 #pragma unroll
                 for (int q = 0; q < Q; ++q)
 #pragma unroll
-                    for (int off = 1; off < L; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
-                if (j == 0) put(tt, s);
+                    for (int off = 1; off < LP; off <<= 1) s[q] = __fadd_rn(s[q], __shfl_xor_sync(0xffffffffu, s[q], off));
+                if (j % LP == 0) put(tt, s);
             }
         }
         if (i + 2 < tiles) bar_arrive(kFree + b2, kPair);
