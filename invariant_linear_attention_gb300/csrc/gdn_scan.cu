@@ -472,12 +472,13 @@ struct FwdK {
         // longest of N sequences is taken for up to min(N, 3) mean lengths: once it walks alone, a token
         // takes twice as long with two channels a lane (16 ragged prompts, 12265 x 2760 x 16, 4.6 blocks an
         // SM: 192 and 368 us; 16384 x 8192 x 16, 13 blocks: 567 and 543).  Not for 8 states: their walkers
-        // would be half a warpgroup.
+        // would be half a warpgroup.  The bits are the same either way, so a compiler that leaves too few
+        // registers to move costs time only.
         if constexpr (S >= 16) {
-            static std::atomic<bool> known{false};
+            static std::atomic<int> known{0};
             if ((long long)blocks * p.N > 3LL * kSMs * (p.N < 3 ? p.N : 3)) {
                 const gdn_status st = check_registers(scan_fwd_kernel<T, S, 2>, FwdTile<T, S, 2>::NT, 128 * (kRegsSide + kRegsWalk), known);
-                return st == GDN_OK ? run<2>(s, p) : st;
+                if (st != GDN_ERR_UNSUPPORTED) return st == GDN_OK ? run<2>(s, p) : st;
             }
         }
         return run<1>(s, p);

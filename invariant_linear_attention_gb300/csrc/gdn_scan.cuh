@@ -142,15 +142,18 @@ __device__ __forceinline__ float sum_states4(const float2 (&h)[2], const float2 
 // Host side.
 
 // Whether a kernel whose warpgroups move registers is launched with the `need` registers a CTA that
-// they then hold: they would wait for ever for more.  A good answer holds for the process.
+// they then hold: they would wait for ever for more.  GDN_ERR_UNSUPPORTED where it is not.  What the
+// runtime answers holds for the process, an error of the runtime does not.
 template <typename K>
-gdn_status check_registers(K* kernel, int threads, int need, std::atomic<bool>& known) {
-    if (known.load(std::memory_order_relaxed)) return GDN_OK;
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return GDN_ERR_CUDA;
-    if (a.numRegs * threads < need) return GDN_ERR_UNSUPPORTED;
-    known.store(true, std::memory_order_relaxed);
-    return GDN_OK;
+gdn_status check_registers(K* kernel, int threads, int need, std::atomic<int>& known) {
+    int ok = known.load(std::memory_order_relaxed);  // 0: not asked yet, 1: enough, -1: too few
+    if (!ok) {
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return GDN_ERR_CUDA;
+        ok = a.numRegs * threads < need ? -1 : 1;
+        known.store(ok, std::memory_order_relaxed);
+    }
+    return ok > 0 ? GDN_OK : GDN_ERR_UNSUPPORTED;
 }
 inline gdn_status check_scan(const gdn_scan_shape* s) {
     if (!s) return GDN_ERR_INVALID_ARG;

@@ -839,7 +839,7 @@ gdn_status launch(cudaStream_t s, const BwdParams& q, long long segs) {
     constexpr size_t smem = sizeof(GradMem<T, S>);
     if constexpr (GradMem<T, S>::SIDE == 128) {
         using M = GradMem<T, S>;
-        static std::atomic<bool> known{false};
+        static std::atomic<int> known{0};
         const gdn_status st = check_registers(scan_grad_kernel<T, S>, M::NT, regs_side(M::WALK) * M::SIDE + regs_walk(M::WALK) * M::WALK, known);
         if (st != GDN_OK) return st;
     }

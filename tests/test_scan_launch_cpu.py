@@ -1,0 +1,103 @@
+"""CPU checks of the selective scan's host side: which form a batch takes for what the runtime
+reports of its kernels (a fake runtime, nothing is launched), and how much memory a call asks for."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import invariant_linear_attention_gb300 as gdn
+from invariant_linear_attention_gb300 import binding, build_lib
+
+FAKE = 0x10000  # never dereferenced: the fake runtime launches nothing
+OK, CUDA_ERROR = 0, -4
+
+RUNTIME = r"""
+#include <cuda_runtime_api.h>
+#include <string.h>
+#include <map>
+#include <string>
+static std::map<const void*, std::string>& names() { static std::map<const void*, std::string> m; return m; }
+static std::string last;
+extern "C" {
+int fake_regs = 0, fake_error = 0, fake_asked = 0;
+const char* fake_last() { return last.c_str(); }
+void** __cudaRegisterFatBinary(void*) { static void* h; return &h; }
+void __cudaRegisterFatBinaryEnd(void**) {}
+void __cudaUnregisterFatBinary(void**) {}
+void __cudaRegisterFunction(void**, const char* host, char*, const char* name, int, void*, void*, void*, void*, int*) { names()[host] = name; }
+unsigned __cudaPushCallConfiguration(dim3, dim3, size_t, void*) { return 0; }
+cudaError_t __cudaPopCallConfiguration(dim3* g, dim3* b, size_t* s, void* st) { return *g = *b = dim3{1, 1, 1}, *s = 0, *static_cast<void**>(st) = 0, cudaSuccess; }
+cudaError_t __cudaGetKernel(void** k, const void* host) { return *k = const_cast<void*>(host), cudaSuccess; }
+cudaError_t __cudaLaunchKernel(void* k, dim3, dim3, void**, size_t, void*) { return last = names()[k], cudaSuccess; }
+cudaError_t CUDARTAPI cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return cudaSuccess; }
+cudaError_t CUDARTAPI cudaGetLastError() { return cudaSuccess; }
+cudaError_t CUDARTAPI cudaFuncGetAttributes(cudaFuncAttributes* a, const void*) {
+    memset(a, 0, sizeof *a);
+    ++fake_asked;
+    return a->numRegs = fake_regs, static_cast<cudaError_t>(fake_error);
+}
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def faked(tmp_path_factory):
+    """A function that loads the scan's forward on a fresh copy of the fake runtime."""
+    build_lib.build()
+    obj = os.path.join(build_lib.BUILD, "gdn_scan.o")
+    nvcc = build_lib._nvcc()
+    if not os.path.exists(obj):
+        os.makedirs(build_lib.BUILD, exist_ok=True)
+        build_lib._compile(nvcc, os.path.join(build_lib.CSRC, "gdn_scan.cu"))
+    at = tmp_path_factory.mktemp("fake")
+    (at / "runtime.cpp").write_text(RUNTIME)
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-Wl,-Bsymbolic", "-I" + include, str(at / "runtime.cpp"), obj, "-o", str(at / "scan.so")], check=True)
+    count = [0]
+
+    def load():
+        count[0] += 1
+        shutil.copy(at / "scan.so", at / f"scan{count[0]}.so")
+        L = ctypes.CDLL(str(at / f"scan{count[0]}.so"))
+        L.gdn_selective_scan_fwd.argtypes = [ctypes.POINTER(gdn.ScanShape)] + [ctypes.c_void_p] * 11 + [ctypes.c_int] + [ctypes.c_void_p] * 3
+        L.fake_last.restype = ctypes.c_char_p
+        return L
+
+    return load
+
+
+def forward(L, S, blocks):
+    """Status of a prompt of `blocks` CTAs of one channel a lane, and the channels a lane of the form it took."""
+    C = blocks * (64 if S <= 16 else 1024 // S)
+    s = gdn.ScanShape(N=1, T_total=100, C=C, G=1, S=S, dtype=binding.GDN_BF16, dt_softplus=1, ldx=C, lddt=C, ldz=C, ldB=S, ldC=S)
+    p = [FAKE + 0x1000 * i for i in range(12)]
+    st = L.gdn_selective_scan_fwd(ctypes.byref(s), *p[:9], None, None, 0, None, p[10], None)
+    name = L.fake_last().decode()
+    assert st != OK or f"scan_fwd_kernelI13__nv_bfloat16Li{S}ELi" in name
+    return st, name.split(f"Li{S}ELi")[1][0] if st == OK else None
+
+
+def regs(L, n, error=0):
+    ctypes.c_int.in_dll(L, "fake_regs").value = n
+    ctypes.c_int.in_dll(L, "fake_error").value = error
+
+
+@pytest.mark.parametrize("S", [16, 32, 64])
+def test_full_batches_do_without_registers_to_move(faked, S):
+    L = faked()
+    regs(L, 80)
+    assert forward(L, S, 100) == (OK, "1") and forward(L, S, 1000) == (OK, "2")
+    # a kernel compiled to fewer registers than its warpgroups would own: the other form, which has the same bits
+    L = faked()
+    regs(L, 79)
+    for _ in range(3):
+        assert forward(L, S, 1000) == (OK, "1")
+    assert ctypes.c_int.in_dll(L, "fake_asked").value == 1
+    # an error of the runtime is an error, and is not remembered
+    L = faked()
+    regs(L, 80, error=2)
+    assert forward(L, S, 1000)[0] == CUDA_ERROR
+    regs(L, 80)
+    assert forward(L, S, 1000) == (OK, "2")
