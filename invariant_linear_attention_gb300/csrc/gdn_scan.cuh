@@ -33,8 +33,7 @@ __device__ __forceinline__ float a_log2(float A_log) { return __fmul_rn(-expf(A_
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 softplus2(const float2& v, float2& u) {
     const float2 m = make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f));
-    const float2 e = __fmul2_rn(__ffma2_rn(m, both(-2.f), v), both(kLog2e));  // v - 2 max(v, 0) = -|v|, exactly
-    u = make_float2(ex2(e.x), ex2(e.y));
+    u = make_float2(ex2(__fmul_rn(fabsf(v.x), -kLog2e)), ex2(__fmul_rn(fabsf(v.y), -kLog2e)));
     const float2 s = __fadd2_rn(u, both(2.f));
     const float2 w = __fmul2_rn(u, make_float2(rcp_approx(s.x), rcp_approx(s.y))), q = __fmul2_rn(w, w);
     float2 p = __ffma2_rn(both(0.2817465662956238f), q, both(0.2796141803264618f));

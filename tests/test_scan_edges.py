@@ -1,0 +1,71 @@
+"""GPU checks of the selective scan where single values leave the usual range, against the fp64 oracle.  Bounds as in
+test_scan.py."""
+import numpy as np
+import pytest
+import torch
+
+import invariant_linear_attention_gb300 as gdn
+from oracle import scan_ops as ref
+from helpers import to_np
+from test_scan import DEV, Case, bits, check
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def check_forward(c, **kw):
+    pool = c.h0.clone()
+    y = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, state=pool, **kw, **c.args())
+    want, fin = ref.selective_scan(cu=c.cu_list, init_state=c.h0, **kw, **c.args())
+    absargs = {k: None if v is None else v.abs() if k in ("x", "B", "C", "D") else v for k, v in c.args().items()}
+    mag, fmag = ref.selective_scan(cu=c.cu_list, init_state=c.h0.abs(), **kw, **dict(absargs, z=None))
+    extra = 0.0
+    if c.z is not None:
+        mag, extra = mag * np.abs(ref.silu(to_np(c.z))), 6 + 2.4 * np.abs(to_np(c.z)).max()
+    check(y, want, mag, c.units, c.dtype, extra)
+    check(pool, fin, fmag, c.units, torch.float32)
+    return y
+
+
+def check_backward(c, **kw):
+    """Every gradient against the oracle's, under test_scan.py's bound."""
+    st = dict(init_state=c.h0, d_final_state=c.gT)
+    g = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, **st, **kw, **c.args())
+    want = ref.selective_scan_bwd(cu=c.cu_list, d_out=c.dy, **st, **kw, **c.args())
+    mag = ref.selective_scan_bwd(cu=c.cu_list, d_out=c.dy, magnitude=True, **st, **kw, **c.args())
+    units = 3 * c.units + c.C + sum(c.lens) + (0 if c.z is None else 3 * (6 + 2.4 * np.abs(to_np(c.z)).max()))
+    for k in want:
+        if g[k] is not None:
+            check(g[k], want[k], mag[k], units, torch.float32 if g[k].dtype == torch.float32 else c.dtype)
+    return g
+
+
+# ---------------------------------------------------------------- steps and decays out of range
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_infinite_steps(dtype):
+    """dt = +inf: softplus is +inf, the state is forgotten and takes +inf B; dt = -inf: the token changes nothing."""
+    dt = torch.zeros(3, 8, device=DEV, dtype=dtype)
+    dt[1], dt[2] = INF, -INF
+    one, bc = torch.ones(3, 8, device=DEV, dtype=dtype), torch.ones(3, 1, 8, device=DEV, dtype=dtype)
+    s0 = torch.rand(3, 8, 8, device=DEV) + 1
+    A = torch.zeros(8, 8, device=DEV)
+    for call in ("update", "prompt"):
+        st = s0.clone()
+        if call == "update":
+            y = gdn.gdn_selective_scan_update(one, dt, A, bc, bc, st)
+        else:
+            y = gdn.gdn_selective_scan_fwd(one, dt, A, bc, bc, torch.arange(4, dtype=torch.int32, device=DEV), state=st)
+        assert torch.all(st[1] == INF) and torch.all(y[1] == INF), call
+        assert torch.equal(st[2], s0[2]) and torch.isfinite(y[[0, 2]]).all() and torch.isfinite(st[0]).all(), call
+
+
+@pytest.mark.parametrize("dtype,S,C", [(torch.float32, 16, 40), (torch.bfloat16, 32, 24), (torch.float32, 8, 72)])
+def test_tokens_masked_by_their_step(dtype, S, C):
+    """dt = -inf masks a token: d and its slope are 0, as in the formula."""
+    c = Case([33, 5, 0, 18], C, 1, S, dtype, 31)
+    c.units = c.error_units()
+    c.dt[::3] = -INF
+    check_forward(c)
+    g = check_backward(c)
+    assert torch.all(g["ddt"][:56:3] == 0)
