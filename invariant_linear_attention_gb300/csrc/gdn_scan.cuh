@@ -11,6 +11,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <limits.h>
 #include <stdint.h>
 
@@ -22,8 +23,13 @@
 namespace gdn {
 namespace scan {
 
-// A log2(e) of one state from its A_log.
-__device__ __forceinline__ float a_log2(float A_log) { return __fmul_rn(-expf(A_log), kLog2e); }
+// A log2(e) of one state from its A_log.  Past fp32's range (A_log > 88.3) the largest finite value stands
+// for it: any step that is not 0 still forgets such a state, but 0 times it (a step of 0, a tile's
+// padding, the gradient of what was forgotten) is 0 and not NaN.
+__device__ __forceinline__ float a_log2(float A_log) {
+    const float a = __fmul_rn(-expf(A_log), kLog2e);
+    return a < -FLT_MAX ? -FLT_MAX : a;
+}
 
 // softplus(v) = max(v, 0) + log(1 + u), u = e^-|v| in (0, 1], with log(1 + u) = 2 artanh(w),
 // w = u / (2 + u) <= 1/3: relative accuracy is kept for the small steps of strongly negative v,

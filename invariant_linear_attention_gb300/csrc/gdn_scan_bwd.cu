@@ -546,7 +546,9 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
                     const float2 d = make_float2(v0.x, v1.x), g = make_float2(v0.z, v1.z), sig = make_float2(v0.w, v1.w);
                     const float2 u = sum_of(0, e), v = __fmul2_rn(sum_of(1, e), both(kLn2));
                     odx[e] = __ffma2_rn(d, u, __fmul2_rn(D[e], g));
-                    odt[e] = __fmul2_rn(__ffma2_rn(xv[e], u, v), sig);
+                    // a masked token (dt = -inf, slope 0) gets 0, though a decay past fp32 may have made its dd infinite
+                    const float2 dd = __ffma2_rn(xv[e], u, v);
+                    odt[e] = make_float2(sig.x != 0.f ? __fmul_rn(dd.x, sig.x) : 0.f, sig.y != 0.f ? __fmul_rn(dd.y, sig.y) : 0.f);
                     sD[e] = __ffma2_rn(g, xv[e], sD[e]);
                     sb[e] = __fadd2_rn(sb[e], odt[e]);
                 }

@@ -69,3 +69,19 @@ def test_tokens_masked_by_their_step(dtype, S, C):
     check_forward(c)
     g = check_backward(c)
     assert torch.all(g["ddt"][:56:3] == 0)
+
+
+@pytest.mark.parametrize("dtype,S,G,C", [(torch.float32, 16, 1, 40), (torch.bfloat16, 16, 2, 144), (torch.float32, 8, 1, 24), (torch.float32, 32, 1, 40), (torch.bfloat16, 64, 1, 24)])
+def test_decays_beyond_fp32(dtype, S, G, C):
+    """exp(A_log) past the largest fp32 value: such a state forgets at once; its gradients are 0 where the formula's
+    are, also where sequences end inside a tile and where a step is 0."""
+    c = Case([33, 0, 1, 70, 6], C, G, S, dtype, 32)
+    c.units = c.error_units()
+    c.A_log[::3, 1::4] = 88.6  # times log2(e) past it
+    c.A_log[1::3, ::4] = 100.0
+    c.A_log[2::3, 3::4] = 700.0
+    check_forward(c)
+    check_backward(c)
+    c.dt[::4] = -INF
+    check_forward(c)
+    check_backward(c)
