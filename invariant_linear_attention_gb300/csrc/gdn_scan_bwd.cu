@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             A2[c][i] = make_float2(a_log2(A2[c][i].x), a_log2(A2[c][i].y));
-            if (!ok) G[c][i] = both(0.f);
+            if (!ok) A2[c][i] = G[c][i] = both(0.f);  // the values of another group's channel stay out of this one's dB and dC
             dA[c][i] = both(0.f);
         }
     }

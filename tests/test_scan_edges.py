@@ -85,3 +85,20 @@ def test_decays_beyond_fp32(dtype, S, G, C):
     c.dt[::4] = -INF
     check_forward(c)
     check_backward(c)
+
+
+@pytest.mark.parametrize("dtype,S,G,CG", [(torch.float32, 16, 2, 24), (torch.bfloat16, 8, 2, 40), (torch.float32, 32, 3, 8), (torch.bfloat16, 64, 2, 16)])
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_a_channels_parameters_stay_in_its_group(dtype, S, G, CG, bad):
+    """A_log of channel 0 not a number: other channels' outputs and other groups' dB and dC have the bits they have without."""
+    c = Case([21, 8, 3], G * CG, G, S, dtype, 33)
+    st = dict(init_state=c.h0, d_final_state=c.gT)
+    good = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, **st, **c.args())
+    y = gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, **c.args())
+    c.A_log[0] = bad
+    g = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, **st, **c.args())
+    assert torch.equal(bits(gdn.gdn_selective_scan_fwd(cu_seqlens=c.cu, **c.args())[:, 1:]), bits(y[:, 1:]))
+    for k in ("dx", "ddt", "dz", "dB", "dC", "d_init_state"):
+        assert torch.equal(bits(g[k][:, 1:]), bits(good[k][:, 1:])), k
+    for k in ("dA_log", "dD", "ddt_bias"):
+        assert torch.equal(bits(g[k][1:]), bits(good[k][1:])), k
