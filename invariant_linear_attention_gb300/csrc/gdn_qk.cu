@@ -260,9 +260,10 @@ __global__ void __launch_bounds__(256, 2) qk_bwd_kernel(const __grid_constant__ 
                         }
                     }
                     const float gx = group_sum(dot<VN>(g, v), p.lpr);
-                    const float f = -__fmul_rn(__fmul_rn(__fmul_rn(r, r), __fmul_rn(r, p.c)), gx);
+                    // r (g - x (r sum(g x)) (r c)): with eps = 0 and small rows r^3 is past fp32, these products are not
+                    const float f = -__fmul_rn(__fmul_rn(r, gx), __fmul_rn(r, p.c));
 #pragma unroll
-                    for (int e = 0; e < VN; ++e) v[e] = __ffma2_rn(v[e], twice(f), __fmul2_rn(twice(r), g[e]));
+                    for (int e = 0; e < VN; ++e) v[e] = __fmul2_rn(twice(r), __ffma2_rn(v[e], twice(f), g[e]));
                     if (h < H && un.has0) st16_stream(dst + h * p.d + un.e0, pack_half<VN>(v));
                     if (h < H && un.has1) st16_stream(dst + h * p.d + un.e1, pack_half<VN>(v + VN / 2));
                 }

@@ -1,12 +1,14 @@
-"""GPU checks of the selective scan where single values leave the usual range, against the fp64 oracle.  Bounds as in
-test_scan.py."""
+"""GPU checks of the selective scan and the q/k norm where single values leave the usual range, against the fp64 oracles.  Bounds as in
+test_scan.py and test_conv_qk_bwd.py."""
 import numpy as np
 import pytest
 import torch
 
 import invariant_linear_attention_gb300 as gdn
+from oracle import layer_ops
 from oracle import scan_ops as ref
 from helpers import to_np
+from test_conv_qk_bwd import turned, within
 from test_scan import DEV, Case, bits, check
 
 pytestmark = pytest.mark.gpu
@@ -102,3 +104,32 @@ def test_a_channels_parameters_stay_in_its_group(dtype, S, G, CG, bad):
         assert torch.equal(bits(g[k][:, 1:]), bits(good[k][:, 1:])), k
     for k in ("dA_log", "dD", "ddt_bias"):
         assert torch.equal(bits(g[k][1:]), bits(good[k][1:])), k
+
+
+# ---------------------------------------------------------------- q/k norm
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("scale", [1.0, 1e-13, 1e-16, 1e-18])
+def test_qk_gradient_of_small_rows_without_eps(norm, scale):
+    """eps = 0 takes rows of any size: r^3 is past fp32 from rows of about 1e-13 down, the gradient is not."""
+    gen = torch.Generator().manual_seed(41)
+    rn = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    T, HQ, HK, d, rd = 7, 3, 2, 64, 32
+    q, k, dq, dk = (rn(T, H, d).to(DEV) for H in (HQ, HK, HQ, HK))
+    q, k = q * scale, k * scale
+    w = (1 + 0.1 * rn(d)).to(DEV) if norm == "rms" else None
+    th = rn(T, rd // 2)
+    cos, sin = th.cos().to(DEV), th.sin().to(DEV)
+    kw = dict(norm=norm, eps=0.0)
+    out = gdn.gdn_qk_norm_rope(q, k, cos, sin, q_weight=w, k_weight=w, **kw)
+    g = gdn.gdn_qk_norm_rope_bwd(q, k, cos, sin, dq, dk, q_weight=w, k_weight=w, **kw)
+    aw, share = (1.0 if w is None else np.abs(to_np(w))), (1.0 / d if norm == "rms" else 1.0)
+    for x, y, do, dx, dw in ((q, out[0], dq, g["dq"], g["dq_weight"]), (k, out[1], dk, g["dk"], g["dk_weight"])):
+        r, ax = layer_ops._scale(to_np(x), norm, 0.0), np.abs(to_np(x))
+        within(y, layer_ops.norm_rope(x, w, cos, sin, **kw), turned(ax * r * aw, cos, sin, False), d + 16, torch.float32)
+        want, want_w = layer_ops.norm_rope_bwd(x, w, cos, sin, do, **kw)
+        back = turned(np.abs(to_np(do)), cos, sin, False)
+        ag = back * aw
+        within(dx, want, r * ag + ax * r ** 3 * share * (ag * ax).sum(-1, keepdims=True), 3 * d + 32, torch.float32)
+        if w is not None:
+            within(dw, want_w, (back * ax * r).sum((0, 1)), 3 * d + 32 + T * x.shape[1], torch.float32)
