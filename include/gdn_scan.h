@@ -92,6 +92,13 @@ gdn_status gdn_selective_scan_update(const gdn_scan_shape* shape, const void* x,
  * recomputed; nothing of the forward call is needed.  fp32 sums, each in an order fixed
  * by the shape and cu_seqlens: deterministic, but the sums over tokens and
  * channels are not batch-invariant.
+ *
+ * The workspace is large: per channel and state it holds an fp32 value every 8 tokens and two per
+ * segment, that is 16 to 128 tokens of a sequence (at most T_total / 16 + N segments), and
+ * 8 S bytes per token and block of 64 (S 32 and 64: 32) channels of a group.  For few
+ * sequences that is 6 bytes for every byte of a bf16 x at 16 states (12 for small batches, whose
+ * segments are shorter), 27 at 64; every further sequence, empty ones too, adds 8 C S bytes, as much
+ * as its init_state and d_init_state together.
  */
 size_t gdn_selective_scan_bwd_workspace_size(const gdn_scan_shape* shape);
 

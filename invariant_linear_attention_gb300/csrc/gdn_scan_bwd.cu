@@ -40,10 +40,12 @@ struct BwdParams {
     const void* dy;
     void *dx, *ddt, *dz, *dB, *dC;
     float *dA, *dD, *dbias, *dh0;
-    // Workspace.  Segment k of sequence n is number cu[n] / (m kTile) + n + k (never two on one),
-    // its tile i number segment * m + i.
-    float* tiles;  // [tiles, C, S] the state at the tile's start, from a zero start of its segment
-    float* cum;    // [tiles, C] sum of d up to the tile's start
+    // Workspace.  Segment k of sequence n is number cu[n] / (m kTile) + n + k (never two on one): as many
+    // as the sequences have segments, but no fewer than one each.  A tile that is not its sequence's first
+    // has the number t0 / kTile - 1 of its first token t0: T / kTile numbers, never two on one, for the last such
+    // tile of a sequence starts before its end and the first of the next one kTile behind it.
+    float* tiles;  // [T / kTile, C, S] the state at the tile's start, from a zero start of its segment (not of a segment's first)
+    float* cum;    // [T / kTile, C] sum of d up to the tile's start
     float* seg_h;  // [segments, C, S] local final state, then the true start state
     float* seg_g;  // [segments, C, S] local G, then the true end G, then the segment's part of dA
     float* seg_d;  // [segments, C] sum of d
@@ -75,6 +77,9 @@ struct Input {
     uint4 bc[2][2 * kTile * BCH];
     alignas(16) float bias[CB];
 };
+
+// The number of the tile of first token t0 among the stored ones (-1: none is stored that starts before kTile).
+__device__ __forceinline__ int place_of(int t0) { return (int)((unsigned)t0 / kTile) - 1; }
 
 // Where a CTA stands: sequence, segment, its tokens [lo, hi), group, channels.
 struct Where {
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan
     int at[4];  // this lane's channels in a row of in.d
 #pragma unroll
     for (int c = 0; c < 4; ++c) at[c] = place(cl + c);
-    int64_t tile = (int64_t)w.seg * q.m;
+    int64_t tile = place_of(w.lo);
     __syncthreads();
     for (int t0 = w.lo, buf = 0; t0 < w.hi; t0 += kTile, buf ^= 1, ++tile) {
         copy_wait<0>();
@@ -613,15 +618,16 @@ __global__ void __launch_bounds__(GradMem<T, S>::NT, GradMem<T, S>::MINB) scan_g
     // slot c: channel cl + (c ^ jq); pair slot i: states 4 j + 2 (i ^ pm) and the next one
     const int at0 = place(cl + jq), at1 = place(cl + (jq ^ 1));
     const int64_t so0 = own + (ok ? jq : 0) * S, so1 = own + (ok ? jq ^ 1 : 0) * S;
+    const int first = place_of(w.lo);
     auto copy_tile = [&](int k) {  // the local states at tile k's start
-        const float* from = q.tiles + ((int64_t)w.seg * q.m + k) * C * S;
+        const float* from = q.tiles + (int64_t)(first + k) * C * S;
         if (k > 0) copy16_async(&sm.tile[0][tid], from + so0), copy16_async(&sm.tile[1][tid], from + so1);
         copy_commit();
     };
     copy_tile(tiles - 1);
     sm.seg[0][tid] = *reinterpret_cast<const float4*>(q.seg_h + (int64_t)w.seg * C * S + so0);
     sm.seg[1][tid] = *reinterpret_cast<const float4*>(q.seg_h + (int64_t)w.seg * C * S + so1);
-    auto cum_of = [&](int k, int c) { return ok && k > 0 ? q.cum[((int64_t)w.seg * q.m + k) * C + w.c0 + cl + (c ^ jq)] : 0.f; };
+    auto cum_of = [&](int k, int c) { return ok && k > 0 ? q.cum[(int64_t)(first + k) * C + w.c0 + cl + (c ^ jq)] : 0.f; };
     float cum[2] = {cum_of(tiles - 1, 0), cum_of(tiles - 1, 1)};
     auto load_pairs = [&](const float* from, float2 (&v)[2]) {
         float2 t[2];
@@ -812,16 +818,21 @@ Layout layout(const gdn_scan_shape* s) {
     // Tiles per segment: long segments save traffic and joins, short ones give a small batch CTAs
     // to run side by side.  us at 2 / 4 / 8 / 16, bf16, 16 states: 512 tokens x 512 channels 30 / 34 / 46 / 77,
     // 2048 x 1024 93 / 83 / 85 / 93, 2048 x 2048 167 / 144 / 138 / 150, 16384 x 1024 665 / 538 / 482 / 468.
-    auto ctas = [&](int m) { return ((long long)s->T_total / (m * kTile) + s->N) * s->G * l.bpg; };
+    // Counted: the segments that the tokens make, and at most as many for the sequences' ragged ends; more
+    // sequences are empty or one segment each whatever m is.
+    auto ctas = [&](int m) {
+        const long long full = s->T_total / (m * kTile);
+        return (full + (s->N < full ? s->N : full)) * s->G * l.bpg;
+    };
     // In waves of the CTAs that the GPU holds (fewer, and 16 lose to the last wave: 4096 x 4096 x 8, 3.6
     // waves at 16, 347 us, 315 at 8).
     const long long wave = kSMs * (s->S == 8 ? 4 : 2);
     l.m = ctas(16) >= 6 * wave ? 16 : ctas(8) >= 2 * wave ? 8 : ctas(4) >= wave ? 4 : 2;
     l.segs = (long long)s->T_total / (l.m * kTile) + s->N;
-    const size_t c = s->C, cs = c * s->S, n = (size_t)l.segs;
+    const size_t c = s->C, cs = c * s->S, n = (size_t)l.segs, tiles = s->T_total / kTile;
     l.tiles = 0;
-    l.cum = l.tiles + n * l.m * cs;
-    l.seg_h = l.cum + n * l.m * c;
+    l.cum = l.tiles + tiles * cs;
+    l.seg_h = l.cum + tiles * c;
     l.seg_g = l.seg_h + n * cs;
     l.seg_d = l.seg_g + n * cs;
     l.bc = l.seg_d + n * c;

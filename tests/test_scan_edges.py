@@ -1,4 +1,5 @@
-"""GPU checks of the selective scan and the q/k norm where single values leave the usual range, against the fp64 oracles.  Bounds as in
+"""GPU checks of the selective scan and the q/k norm where single values leave the usual range,
+and of the gradient on batches of many short sequences, against the fp64 oracles.  Bounds as in
 test_scan.py and test_conv_qk_bwd.py."""
 import numpy as np
 import pytest
@@ -104,6 +105,28 @@ def test_a_channels_parameters_stay_in_its_group(dtype, S, G, CG, bad):
         assert torch.equal(bits(g[k][:, 1:]), bits(good[k][:, 1:])), k
     for k in ("dA_log", "dD", "ddt_bias"):
         assert torch.equal(bits(g[k][1:]), bits(good[k][1:])), k
+
+
+# ---------------------------------------------------------------- many short sequences
+
+@pytest.mark.parametrize("dtype,S,G,lens", [
+    (torch.float32, 8, 2, [(0, 1, 7, 8, 9, 16, 17, 3)[i % 8] for i in range(300)]),
+    (torch.bfloat16, 16, 1, [(13, 0, 24, 1, 40)[i % 5] for i in range(200)]),
+    (torch.float32, 8, 365, [130, 1, 0, 250, 8, 7, 128, 129, 16, 611]),    # 16 tiles a segment
+    (torch.bfloat16, 16, 183, [130, 1, 0, 250, 8, 7, 128, 129, 16, 611]),
+    (torch.bfloat16, 16, 40, [130, 1, 0, 250, 8, 7, 128, 129, 16, 611]),   # 8
+    (torch.float32, 32, 12, [130, 1, 0, 250, 8, 7, 128, 129, 16, 611]),    # 4
+    (torch.bfloat16, 64, 2, [130, 1, 0, 250, 8, 7, 128, 129, 16, 611])])   # 2
+def test_backward_of_sequences_of_every_length(dtype, S, G, lens):
+    """Every sequence's states in a place of their own: the workspace filled with NaN changes nothing."""
+    c = Case(lens, 8 * G, G, S, dtype, 38, slow=True)
+    c.units = c.error_units()
+    g = check_backward(c)
+    shape = gdn.ScanShape(len(lens), sum(lens), 8 * G, G, S, int(dtype == torch.bfloat16), 1, 8 * G, 8 * G, 8 * G, G * S, G * S)
+    ws = torch.full((gdn.lib().gdn_selective_scan_bwd_workspace_size(shape),), 255, dtype=torch.uint8, device=DEV)
+    again = gdn.gdn_selective_scan_bwd(cu_seqlens=c.cu, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, workspace=ws, **c.args())
+    for k in g:
+        assert torch.equal(bits(g[k]), bits(again[k])), k
 
 
 # ---------------------------------------------------------------- q/k norm

@@ -101,3 +101,25 @@ def test_full_batches_do_without_registers_to_move(faked, S):
     assert forward(L, S, 1000)[0] == CUDA_ERROR
     regs(L, 80)
     assert forward(L, S, 1000) == (OK, "2")
+
+
+def workspace(N, T, C, S, G=1, dtype=binding.GDN_BF16):
+    build_lib.build()
+    s = gdn.ScanShape(N=N, T_total=T, C=C, G=G, S=S, dtype=dtype, dt_softplus=1, ldx=C, lddt=C, ldz=C, ldB=G * S, ldC=G * S)
+    return gdn.lib().gdn_selective_scan_bwd_workspace_size(ctypes.byref(s))
+
+
+@pytest.mark.parametrize("T,C,S,G", [(8192, 4096, 16, 1), (32768, 8192, 16, 1), (8192, 1024, 64, 2), (300, 64, 8, 1), (5, 64, 8, 1)])
+@pytest.mark.parametrize("N", [1, 8, 256, 1024, 4096])
+def test_scan_backward_workspace_follows_the_tokens_and_the_sequences(T, C, S, G, N):
+    """A state every 8 tokens, two per segment (never more than T / 16 + N), dB and dC per block of channels."""
+    segs, blocks = T // 16 + N, G * -(-(C // G) // (64 if S <= 16 else 32))
+    bound = 4 * (C * S + C) * (T // 8) + 4 * (2 * C * S + 3 * C) * segs + 8 * S * T * blocks
+    assert 0 < workspace(N, T, C, S, G) <= bound
+    assert workspace(N + 1000, T, C, S, G) - workspace(N, T, C, S, G) <= 1000 * 4 * (2 * C * S + 3 * C) + 4 * (2 * C * S + 3 * C) * (T // 16)
+
+
+def test_scan_backward_workspace_of_many_short_documents():
+    # 64 MB of bf16 x: states of 4096 sequences are 1 GB, twice in the workspace
+    assert workspace(4096, 8192, 4096, 16) < 2.8e9
+    assert workspace(8, 8192, 4096, 16) < 0.45e9
