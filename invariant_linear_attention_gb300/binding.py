@@ -606,12 +606,16 @@ def _space(workspace, need, device):
 
 @functools.lru_cache(4096)
 def _struct(kind, *values):
-    return ctypes.byref(kind(*values))
+    shape = kind(*values)
+    for (name, ty), value in zip(kind._fields_, values):  # ctypes would cut a larger number to its low bits
+        if ty is not ctypes.c_float and getattr(shape, name) != value:
+            raise ValueError(f"{name} is too large: {value}")
+    return ctypes.byref(shape)
 
 
 @functools.lru_cache(4096)
 def _space_of(entry, kind, *values):
-    return max(int(getattr(lib(), entry)(ctypes.byref(kind(*values)))), 16)
+    return max(int(getattr(lib(), entry)(_struct(kind, *values))), 16)
 
 
 def gdn_causal_conv1d_bwd(x, weight, cu_seqlens, d_out, bias=None, init_state=None, d_final_state=None,

@@ -123,3 +123,19 @@ def test_scan_backward_workspace_of_many_short_documents():
     # 64 MB of bf16 x: states of 4096 sequences are 1 GB, twice in the workspace
     assert workspace(4096, 8192, 4096, 16) < 2.8e9
     assert workspace(8, 8192, 4096, 16) < 0.45e9
+
+
+@pytest.mark.parametrize("kind,values", [
+    (gdn.ConvShape, (1, 2 ** 32 + 5, 8, 4, binding.GDN_BF16, 1)), (gdn.ConvShape, (1, 2 ** 31, 8, 4, binding.GDN_BF16, 1)),
+    (gdn.ScanShape, (1, 2 ** 32 + 5, 8, 1, 8, binding.GDN_BF16, 1, 8, 8, 8, 8, 8)), (gdn.ScanShape, (2 ** 32, 0, 8, 1, 8, binding.GDN_BF16, 1, 8, 8, 8, 8, 8)),
+    (gdn.QkShape, (5, 2 ** 32 + 2, 2, 64, 32, 0, 0, 100, 1e-6, binding.GDN_BF16, 2 ** 40, 128)),
+    (gdn.QkShape, (5, 2, 2, 64, 32, 0, 0, 2 ** 32 + 100, 1e-6, binding.GDN_BF16, 128, 128))])
+def test_sizes_past_the_structs_integers_are_refused(kind, values):
+    """A tensor of 2^32 + 5 rows is not one of 5."""
+    with pytest.raises(ValueError):
+        binding._struct(kind, *values)
+
+
+def test_large_sizes_within_the_structs_integers_are_not():
+    binding._struct(gdn.QkShape, 2 ** 40, 2, 2, 64, 32, 0, 0, 2 ** 31 - 1, 1e-6, binding.GDN_BF16, 2 ** 40, 128)
+    binding._struct(gdn.ScanShape, 1, 2 ** 31 - 1, 8, 1, 8, binding.GDN_BF16, 1, 2 ** 33, 8, 8, 8, 8)
