@@ -107,6 +107,31 @@ def test_a_channels_parameters_stay_in_its_group(dtype, S, G, CG, bad):
         assert torch.equal(bits(g[k][1:]), bits(good[k][1:])), k
 
 
+# ---------------------------------------------------------------- steps without softplus
+
+@pytest.mark.parametrize("dtype,S,G,C,gate,bias", [(torch.float32, 16, 1, 72, True, True), (torch.bfloat16, 16, 2, 48, False, False),
+                                                  (torch.bfloat16, 8, 1, 24, True, False), (torch.float32, 32, 1, 40, False, True),
+                                                  (torch.float32, 64, 2, 32, True, False)])
+def test_steps_without_softplus(dtype, S, G, C, gate, bias):
+    """dt (+ dt_bias) taken as it is, prompts, single tokens and the gradient.  Here d is dt, exact, or one rounded sum:
+    error_units counts more for it."""
+    c = Case([33, 0, 1, 70, 16, 2], C, G, S, dtype, 34, gate=gate, bias=bias)
+    c.dt = torch.rand(c.dt.shape, generator=torch.Generator().manual_seed(35)).to(dtype).to(DEV)
+    if bias:
+        c.bias = torch.rand(C, generator=torch.Generator().manual_seed(36)).to(DEV)
+    d, A = to_np(c.dt) + (0 if not bias else to_np(c.bias)), np.exp(to_np(c.A_log))
+    s = max((d[a:b].sum(0)[:, None] * A).max() for a, b in zip(c.cu_list, c.cu_list[1:]))
+    c.units = 64 + 6 * max(c.lens) + 52 * min(40.0, s) + S / 4
+    check_forward(c, dt_softplus=False)
+    check_backward(c, dt_softplus=False)
+    one = Case([1] * 9, C, G, S, dtype, 37, gate=gate, bias=bias)
+    one.dt = c.dt[:9]
+    a, b = one.h0.clone(), one.h0.clone()
+    y = gdn.gdn_selective_scan_fwd(cu_seqlens=one.cu, state=a, dt_softplus=False, **one.args())
+    z = gdn.gdn_selective_scan_update(state=b, dt_softplus=False, **one.args())
+    assert torch.equal(bits(y), bits(z)) and torch.equal(bits(a), bits(b))
+
+
 # ---------------------------------------------------------------- many short sequences
 
 @pytest.mark.parametrize("dtype,S,G,lens", [
