@@ -29,10 +29,10 @@ __device__ __forceinline__ float scatter_sum(float (&s)[L], int j) {
 
 // The sequence of rank `rank` by length, the longest first (ties by number).  As soon as an SM gets
 // more than one CTA, the longest walks must neither start last nor share an SM: 16 ragged prompts,
-// 16384 x 8192 x 16, one channel a lane, take 603 us in order of number and 567 in order of length;
-// two CTAs an SM, all resident from the start (8192 x 2048 x 16), 188 and 149.
+// 16384 x 8192 x 16, take 640 us in order of number and 536 in order of length (one channel a lane
+// 601 and 564); two CTAs an SM, all resident from the start (8000 x 2048 x 16), 188 and 149.
 // A CTA's N^2 comparisons have to be few against its walk of T / N tokens: ranked and not, 256
-// sequences take 470 and 218 us at 4096 x 8192 x 16, 300 and 306 at 65536 x 1024, 554 and 652 at
+// sequences take 473 and 220 us at 4096 x 8192 x 16, 298 and 317 at 65536 x 1024, 546 and 665 at
 // 131072 x 1024; hence N^3 <= 256 T.
 constexpr int kRanked = 256;
 __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
@@ -65,22 +65,21 @@ __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
 // same number of times.  Preparers and finishers copy their own inputs, asynchronously, a tile
 // ahead, and read back only chunks that they copied themselves.
 //
-// What bounds it: with few CTAs the walkers' latency; with many and Q = 1 the path from shared
-// memory into registers (128 bytes a cycle, whether lanes share an address or not; B and C take 64
-// bytes a lane and token), with Q = 2 the issue slots.  The step alone (per two states 4 packed
-// products or fmas and 2 exponentials, in registers) runs at 6.8 T states/s on this GPU, of 10 T
-// that the exponentials and 9.6 T that the fma pipe would allow; with its operands, sums and the
-// phases around it, it reaches 4.0 T at 16 states, 4.4 T at 64.  ns a token of all CTAs, 16 states,
-// bf16, at 1 / 2 / 3 / 4 / 8 / 16 blocks of 64 channels an SM: Q = 1 65 / 98 / 136 / 178 / 333 / 646,
-// Q = 2 (4 and up) 174 / 324 / 619; 64 states, 8 blocks of 16 channels: 362 and 283.  With the phases
-// one after the other in every warp and two channels a lane: 160 / 166 / - / 211 / 338; with 4 states
-// a lane: 80 / 150.
+// What bounds it: with few CTAs the walkers' latency; with many the issue slots (63 % busy) and the
+// path from shared memory into registers (128 bytes a cycle, whether lanes share an address or not; B and
+// C take 64 bytes a lane and token), 70 % busy with Q = 1 and 61 % with Q = 2: neither is full.  The step
+// alone (per two states 4 packed products or fmas and 2 exponentials, in registers) was measured at 6.8 T
+// states/s on this GPU, the exponentials alone at 10 T and the fmas at 9.6 T; the kernel reaches 4.1 T at 16
+// states, 4.5 T at 64.  The difference is loading the operands and the phases around the walk, and for ragged
+// prompts the last ones to end.  ns a token of all CTAs, 2048 tokens, 16 states, bf16, at 1 / 2 / 3 / 4 / 8 /
+// 16 blocks of 64 channels an SM: Q = 1 60 / 93 / 130 / 173 / 327 / 638, Q = 2 102 / 103 / 167 / 168 / 314 /
+// 601; 64 states, 8 blocks of 16 channels: 357 and 277.
 template <typename T, int S, int Q>
 struct FwdTile {
     static constexpr int L = S / 8, CB = Q * (S <= 16 ? 64 : 1024 / S), VN = V16<T>::n, TT = 16 / Q;
     static constexpr int WALK = CB / Q * L, SIDE = 64, NT = WALK + 2 * SIDE;
-    // CTAs an SM shall hold.  With 2 and the registers that this leaves, full SMs lose 4 % for
-    // either Q (the 16 prompts above, Q = 1: 567 and 592 us; Q = 2: 543 and 564), with 4 as much.
+    // CTAs an SM shall hold.  With 2 and the registers that this leaves, full SMs lose 4 to 6 % (the 16
+    // prompts above, Q = 1: 564 and 588 us; Q = 2: 536 and 570), with 4 1 to 5 % (571; 560).
     static constexpr int MINB = 3;
     static constexpr int CH = CB / VN, NV = (TT * CH + SIDE - 1) / SIDE, RS = SIDE / CH;
     static constexpr int BCH = S / VN, NB = (2 * TT * BCH + SIDE - 1) / SIDE;
@@ -93,7 +92,7 @@ struct FwdTile {
     // States 8 j + 4 k .. of B (C) at float4 k L + j: the L lanes' loads touch consecutive chunks
     // (in order of states, 8 lanes would meet in the same banks: 64 states 6 % slower).
     float4 b[2][2][TT][2 * L];
-    // Parts of a sum, whose last addition is the finishers' (full batches: 544 us with it in the walk, 538
+    // Parts of a sum, whose last addition is the finishers' (the 16 prompts: 542 us with it in the walk, 536
     // so; with one channel a lane the room for two parts would cost fp32 a CTA an SM).
     static constexpr int UP = Q > 1 ? 2 : 1;
     alignas(16) float y[2][TT][UP][YROW];
@@ -106,8 +105,8 @@ struct FwdTile {
 
 // With two channels a lane the walkers need more registers than the others.  A thread is launched
 // with 80 (at three CTAs of 256 threads); 128 threads go down to 64, 128 up to 96, no more than the
-// CTA holds (checked on the host).  Without: 577 us for the 16 prompts instead of 543; 56 and 104:
-// the same; 48 and 112: 573.
+// CTA holds (checked on the host).  Without: 576 us for the 16 prompts instead of 536; 48 and 112: 558;
+// 56 and 104: 526.
 constexpr int kRegsSide = 64, kRegsWalk = 96;
 
 template <typename T, int S, int Q>
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(FwdTile<T, S, Q>::NT, FwdTile<T, S, Q>::MINB) 
             if constexpr (Q == 2) *reinterpret_cast<float2*>(&sm.y[b2][tt][j / LP][cl]) = make_float2(v[0], v[1]);
             else sm.y[b2][tt][0][cl] = v[0];
         };
-        constexpr int U = TT;  // tokens whose loads and exponentials run ahead of the recurrence (Q = 1, 8 of them: 583 us)
+        constexpr int U = TT;  // tokens whose loads and exponentials run ahead of the recurrence (Q = 1: 564 us for the 16 prompts, 8 of them 578)
         if (len == TT) {
 #pragma unroll 1
             for (int tt = 0; tt < TT; tt += U) {
@@ -468,10 +467,10 @@ struct FwdK {
     }
     static gdn_status go(unsigned blocks, cudaStream_t s, const Params& p) {
         // Two channels a lane from more than the three blocks on that an SM holds at once (4096 tokens x
-        // 8192 x 64, 3.4 blocks an SM: 915 and 583 us; with fewer, figures above, they leave SMs idle).  The
+        // 8192 x 64, 3.4 blocks an SM: 913 and 581 us; with fewer, figures above, they leave SMs idle).  The
         // longest of N sequences is taken for up to min(N, 3) mean lengths: once it walks alone, a token
         // takes twice as long with two channels a lane (16 ragged prompts, 12265 x 2760 x 16, 4.6 blocks an
-        // SM: 192 and 368 us; 16384 x 8192 x 16, 13 blocks: 567 and 543).  Not for 8 states: their walkers
+        // SM: 192 and 343 us; 16384 x 8192 x 16, 13 blocks: 564 and 536).  Not for 8 states: their walkers
         // would be half a warpgroup.  The bits are the same either way, so a compiler that leaves too few
         // registers to move costs time only.
         if constexpr (S >= 16) {

@@ -34,7 +34,7 @@ __device__ __forceinline__ float a_log2(float A_log) {
 // softplus(v) = max(v, 0) + log(1 + u), u = e^-|v| in (0, 1], with log(1 + u) = 2 artanh(w),
 // w = u / (2 + u) <= 1/3: relative accuracy is kept for the small steps of strongly negative v,
 // which log of a rounded 1 + u would lose.  artanh(w) / w is a polynomial of degree 4 in w^2
-// (Chebyshev interpolation on [0, 1/9], error 4e-9).  Two values at a time, in packed operations.
+// (Chebyshev interpolation on [0, 1/9], its constant term put to 1; error 8e-9).  Two values at a time, in packed operations.
 // `u` is left for the derivative.
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 softplus2(const float2& v, float2& u) {

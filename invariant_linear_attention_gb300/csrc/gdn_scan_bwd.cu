@@ -19,8 +19,9 @@
 // Every sum's order is fixed by the shapes and cu_seqlens.
 //
 // The fp32 pipe and the instruction issue bound 1 and 3: per state and token 6 products or sums
-// (packed by twos) and 1 exponential in 1, 13 and 2 in 3; HBM traffic is 7 (T, C) tensors, 64 bytes
-// per channel and tile for the tiles' states, written and read once, and the segments' states.
+// (packed by twos) and 1 exponential in 1, 13 and 2 in 3; HBM traffic is 11 (T, C) tensors (x, dt, d_y and z
+// read by both, dx, ddt and dz written; 8 without a gate), 4 S bytes per channel and tile for the tiles'
+// states, written and read once, and the segments' states.
 #include "gdn_async.cuh"
 #include "gdn_host.h"
 #include "gdn_scan.cuh"
@@ -215,8 +216,8 @@ __device__ __forceinline__ void store_state(float* p, const float2 (&h)[2]) {
 __device__ __forceinline__ float2 ex2_2(const float2& v) { return make_float2(ex2(v.x), ex2(v.y)); }
 
 // ---------------------------------------------------------------- 1. local
-// Every warp prepares and walks in turn: preparing on other warps, as 3 does, takes as long (884 us for
-// all of 8192 x 4096 x 16 either way, 8 states 3 % longer), for the walk itself keeps the issue slots.
+// Every warp prepares and walks in turn: preparing on other warps, as 3 does, took as long (all
+// of 8192 x 4096 x 16 within 0.3 %, 8 states 3 % longer), for the walk itself keeps the issue slots.
 template <typename T, int S>
 __global__ void __launch_bounds__(Geo<T, S, 4>::NT, 512 / Geo<T, S, 4>::NT) scan_local_kernel(const __grid_constant__ BwdParams q) {
     using F = Geo<T, S, 4>;
@@ -335,8 +336,8 @@ __global__ void __launch_bounds__(128) scan_join_kernel(const __grid_constant__ 
 
 // ---------------------------------------------------------------- 3. grad
 // Sum over the lanes of a channel in UP parts: with four lanes or more the last addition is left to
-// the other warps (8192 tokens x 4096 channels x 16 states: 806 and 798 us; 4096 x 2048 x 32, fp32: 428
-// and 416).
+// the other warps (1 % of the whole gradient of 8192 tokens x 4096 channels x 16 states, 3 % of 4096 x
+// 2048 x 32, fp32).
 // Slot c of lane j holds channel c ^ (j & 1) of the lane's two: the first slot stays, the second
 // goes to the neighbour, whose first it is, without selecting; further lanes add by a butterfly.
 // Lane j ends with channel j & 1 of part j / (L / UP).
@@ -350,7 +351,7 @@ __device__ __forceinline__ float sum_states(const float (&v)[2]) {
 // Sum of a lane's four states over its lane group and its neighbour.  Pair slot m of group k holds pair
 // m ^ (k & 1): the first slot stays, the second goes to the neighbour group.  The groups' sums are
 // added up by the other warps, whose issue slots are fewer for it than the walkers' shuffles would be
-// (8192 x 4096 x 16: 885 us with the whole sum here, 818 so).
+// (with the whole sum here 8192 x 4096 x 16 took 8 % longer).
 template <int L>
 __device__ __forceinline__ float2 sum_neighbours(const float2 (&v)[2]) {
     constexpr uint32_t all = 0xffffffffu;
@@ -407,10 +408,10 @@ struct GradMem {
 // Two channels' states, their gradients and a tile's history need more registers than the work
 // before and after: as in the forward, registers move to the walkers, no more than the CTA was
 // launched with (128 a thread at two CTAs of 256 threads, 80 at two of 384; checked on the host).
-// 8192 tokens x 4096 channels x 16 states, all kernels: 798 us at 80 and 176 registers, 816 at 64 and
-// 192, 828 at 88 and 168, 855 at 56 and 200.  Before the sums went to the other warps: two CTAs an SM
-// with a tile's history 882, with half a tile's 915, three with 112 registers and half a tile's 941;
-// every warp doing all phases in turn 965.
+// 8192 tokens x 4096 channels x 16 states, all kernels: 790 us at 80 and 176 registers, 790 at 88 and
+// 168, 833 at 64 and 192, 902 at 56 and 200.  Before the sums went to the other warps, two CTAs an SM with
+// a tile's history took 4 % less than with half a tile's, 6 % less than three with 112 registers and half a
+// tile's, and 9 % less than every warp doing all phases in turn.
 __host__ __device__ constexpr int regs_side(int walkers) { return walkers == 128 ? 80 : 48; }
 __host__ __device__ constexpr int regs_walk(int walkers) { return walkers == 128 ? 176 : 96; }
 
@@ -816,8 +817,8 @@ Layout layout(const gdn_scan_shape* s) {
     Layout l;
     l.bpg = (cg + cb - 1) / cb;
     // Tiles per segment: long segments save traffic and joins, short ones give a small batch CTAs
-    // to run side by side.  us at 2 / 4 / 8 / 16, bf16, 16 states: 512 tokens x 512 channels 30 / 34 / 46 / 77,
-    // 2048 x 1024 93 / 83 / 85 / 93, 2048 x 2048 167 / 144 / 138 / 150, 16384 x 1024 665 / 538 / 482 / 468.
+    // to run side by side.  us at 2 / 4 / 8 / 16, bf16, 16 states: 512 tokens x 512 channels 29 / 30 / 42 / 67,
+    // 2048 x 1024 87 / 77 / 77 / 85, 2048 x 2048 151 / 130 / 124 / 134, 16384 x 1024 601 / 487 / 435 / 419.
     // Counted: the segments that the tokens make, and at most as many for the sequences' ragged ends; more
     // sequences are empty or one segment each whatever m is.
     auto ctas = [&](int m) {
@@ -825,7 +826,7 @@ Layout layout(const gdn_scan_shape* s) {
         return (full + (s->N < full ? s->N : full)) * s->G * l.bpg;
     };
     // In waves of the CTAs that the GPU holds (fewer, and 16 lose to the last wave: 4096 x 4096 x 8, 3.6
-    // waves at 16, 347 us, 315 at 8).
+    // waves at 16, 325 us, 317 at 8).
     const long long wave = kSMs * (s->S == 8 ? 4 : 2);
     l.m = ctas(16) >= 6 * wave ? 16 : ctas(8) >= 2 * wave ? 8 : ctas(4) >= wave ? 4 : 2;
     l.segs = (long long)s->T_total / (l.m * kTile) + s->N;
