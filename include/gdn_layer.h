@@ -4,8 +4,10 @@
  * projections into (g, beta), the short causal depthwise convolution over the
  * q/k/v projections with its per-sequence conv state cache (prefill and
  * decode, and its gradient), the norm of the queries' and keys' heads with
- * the position rotation in the same pass (and its gradient), and the gated
- * RMSNorm applied to the recurrence's output.
+ * the position rotation in the same pass (and its gradient), the gated
+ * RMSNorm applied to the recurrence's output, and the RMSNorm at the layer's
+ * start with the residual's addition (in the same type or in 8 bits with
+ * scales, and its gradient).
  *
  * "Defending Against the Training-Inference Numeric Mismatch in RL
  * (Especially Linear Attention)" keeps these ops identical on the trainer and
@@ -21,6 +23,7 @@
  *     q/k  n = x * r * weight,  r = 1 / sqrt(sum(x^2) * c + eps),  c = 1/d (RMS) or 1 (L2),
  *          then the pairs (u, v) of n's first rotary_dim values by the token's angles:
  *          (u cos - v sin, v cos + u sin)
+ *     add  s = x + residual, rounded to the type;  y = s * weight / sqrt(mean(s^2) + eps)
  *
  * Invariance.  Every output element is computed by one thread with one fixed
  * order of operations that depends on nothing but its own row (conv: its own
@@ -37,7 +40,7 @@
  * size).  Misalignment returns GDN_ERR_INVALID_ARG.  Nothing is allocated;
  * every call is one asynchronous launch on `stream` (a cudaStream_t; NULL =
  * legacy default stream) and returns host-side validation or launch errors
- * only (the two gradients are two launches each and take a workspace).
+ * only (the gradients are two launches each and take a workspace).
  */
 #ifndef GDN_LAYER_H_
 #define GDN_LAYER_H_
@@ -187,6 +190,56 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_shape* shape, const void* q, const 
                                 const void* d_k_out, void* dq, void* dk, int64_t lddq, int64_t lddk,
                                 float* dq_weight, float* dk_weight, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+typedef struct {
+    int64_t rows;      /* tokens */
+    int d;             /* model width, a multiple of 8 (bf16) or 4 (fp32), at most 16384 */
+    gdn_dtype dtype;   /* x, residual, their sum, y and the gradients */
+    float eps;
+    int group;         /* 8 bits: consecutive values that share a scale: 32, 64 or 128; 0: all of a row */
+    int64_t ldx, ldr;  /* elements from one row of x (residual) to the next one's: at least d */
+} gdn_add_norm_shape;
+
+/*
+ * RMSNorm of x + residual.  residual_out [rows, d] dense: the sum s rounded to
+ * dtype, from which the norm is taken (so the gradient, which gets s, sees the
+ * same values); residual NULL: s = x, and residual_out is not written.  weight
+ * [d] fp32.  y [rows, d] dense in dtype.  residual_out and y may alias x or
+ * residual where those are dense, but not each other.  A row is summed by one
+ * group of lanes in one fixed order that depends on d and dtype alone: results
+ * do not depend on the number of rows or on the other rows.  Strides are
+ * multiples of 8 (bf16) or 4 (fp32) elements; all pointers 16-byte aligned.
+ */
+gdn_status gdn_add_rmsnorm(const gdn_add_norm_shape* shape, const void* x, const void* residual,
+                           const float* weight, void* residual_out, void* y, void* stream);
+
+/*
+ * The same with y in 8 bits (e4m3, [rows, d] dense, 8-byte aligned) and
+ * scales [rows, ceil(d / group)] fp32 (group 0: [rows, 1]; 4-byte aligned):
+ * the value scale * y stands for the norm's.  scale = max |norm's values of
+ * the group| / 448, at least 2^-126 (a group of zeros); y is rounded to
+ * nearest even from the fp32 value.  The last group of a row may be shorter.
+ * NaN stays NaN in y and is left out of the group's maximum.  residual_out may
+ * alias x or residual as above; y aliases nothing.
+ */
+gdn_status gdn_add_rmsnorm_fp8(const gdn_add_norm_shape* shape, const void* x, const void* residual,
+                               const float* weight, void* residual_out, void* y, float* scales,
+                               void* stream);
+
+/*
+ * Its gradient for the loss L = <d_y, y> + <d_residual_out, residual_out>: from
+ * s (residual_out of the forward, or its x; ldx), d_y and d_residual_out (NULL:
+ * zero) [rows, d] dense, dx [rows, d] dense in dtype, which is the gradient of x and of
+ * residual alike, and dweight [d] fp32 (NULL: not written, and no workspace is needed).  dx may alias d_y,
+ * d_residual_out or (dense) s.  fp32 sums in an order fixed by the shape.
+ * shape->group and ldr are not read.
+ */
+size_t gdn_add_rmsnorm_bwd_workspace_size(const gdn_add_norm_shape* shape);
+
+gdn_status gdn_add_rmsnorm_bwd(const gdn_add_norm_shape* shape, const void* s, const float* weight,
+                               const void* d_y, const void* d_residual_out, void* dx,
+                               float* dweight, void* workspace, size_t workspace_bytes,
+                               void* stream);
 
 #ifdef __cplusplus
 }

@@ -5,17 +5,23 @@ bit-identical results per sequence (whatever shares the batch, however the
 tokens arrive); a chunked WY-form backward supplies gradients.  The compute
 lives in libgdn.so (C ABI: include/gdn.h for the recurrence,
 include/gdn_layer.h for the gate activations, the short causal conv with its
-state cache and gradient, the q/k norm with rotation, and the gated RMSNorm
-around it, include/gdn_scan.h for the selective state space scan,
+state cache and gradient, the q/k norm with rotation, the gated RMSNorm and the
+RMSNorm with the residual's addition around it, include/gdn_scan.h for the
+selective state space scan, include/gdn_linrec.h for the gated linear recurrence,
 include/gdn_replay.h for the chunk-order-replaying variant); this package is
 its ctypes binding plus the seeded synthetic-input generators.
 """
 from .binding import (  # noqa: F401
+    AddNormShape,
     ConvShape,
     GdnError,
     GdnShape,
+    LinrecShape,
     QkShape,
     ScanShape,
+    gdn_add_rmsnorm,
+    gdn_add_rmsnorm_bwd,
+    gdn_add_rmsnorm_fp8,
     gdn_causal_conv1d_bwd,
     gdn_causal_conv1d_fwd,
     gdn_causal_conv1d_update,
@@ -23,6 +29,9 @@ from .binding import (  # noqa: F401
     gdn_gates,
     gdn_chunk_bwd,
     gdn_decode_step,
+    gdn_linear_recurrence_bwd,
+    gdn_linear_recurrence_fwd,
+    gdn_linear_recurrence_update,
     gdn_qk_norm_rope,
     gdn_qk_norm_rope_bwd,
     gdn_recurrent_fwd,

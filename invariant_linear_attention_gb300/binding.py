@@ -30,7 +30,10 @@ SYMBOLS = ("gdn_workspace_size", "gdn_recurrent_fwd", "gdn_decode_step", "gdn_ch
            "gdn_replay_prefill", "gdn_replay_decode", "gdn_causal_conv1d_bwd",
            "gdn_causal_conv1d_bwd_workspace_size", "gdn_qk_norm_rope", "gdn_qk_norm_rope_bwd",
            "gdn_qk_norm_rope_bwd_workspace_size", "gdn_selective_scan_fwd", "gdn_selective_scan_update",
-           "gdn_selective_scan_bwd", "gdn_selective_scan_bwd_workspace_size")
+           "gdn_selective_scan_bwd", "gdn_selective_scan_bwd_workspace_size", "gdn_add_rmsnorm",
+           "gdn_add_rmsnorm_fp8", "gdn_add_rmsnorm_bwd", "gdn_add_rmsnorm_bwd_workspace_size",
+           "gdn_linear_recurrence_fwd", "gdn_linear_recurrence_update", "gdn_linear_recurrence_bwd",
+           "gdn_linear_recurrence_bwd_workspace_size")
 
 
 class GdnShape(ctypes.Structure):
@@ -56,6 +59,17 @@ class ScanShape(ctypes.Structure):
                 ("S", ctypes.c_int), ("dtype", ctypes.c_int), ("dt_softplus", ctypes.c_int),
                 ("ldx", ctypes.c_int64), ("lddt", ctypes.c_int64), ("ldz", ctypes.c_int64),
                 ("ldB", ctypes.c_int64), ("ldC", ctypes.c_int64)]
+
+
+class AddNormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("group", ctypes.c_int), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64)]
+
+
+class LinrecShape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("T_total", ctypes.c_int), ("C", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("scale", ctypes.c_int), ("activation", ctypes.c_int), ("decay", ctypes.c_float),
+                ("ldx", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldg", ctypes.c_int64), ("ldz", ctypes.c_int64)]
 
 
 class GdnError(RuntimeError):
@@ -106,7 +120,7 @@ def lib():
         L.gdn_replay_decode.argtypes = [ctypes.POINTER(GdnShape)] + [_P] * 8 + [ctypes.c_int, _P, _P]
         L.gdn_replay_decode.restype = ctypes.c_int
         i, n, z = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-        conv, qk, scan = (ctypes.POINTER(c) for c in (ConvShape, QkShape, ScanShape))
+        conv, qk, scan, norm, rec = (ctypes.POINTER(c) for c in (ConvShape, QkShape, ScanShape, AddNormShape, LinrecShape))
         for name, args, res in (
                 ("gdn_causal_conv1d_bwd_workspace_size", [conv], z),
                 ("gdn_causal_conv1d_bwd", [conv] + [_P] * 12 + [z, _P], i),
@@ -116,7 +130,15 @@ def lib():
                 ("gdn_selective_scan_fwd", [scan] + [_P] * 11 + [i, _P, _P, _P], i),
                 ("gdn_selective_scan_update", [scan] + [_P] * 10 + [i, _P, _P], i),
                 ("gdn_selective_scan_bwd_workspace_size", [scan], z),
-                ("gdn_selective_scan_bwd", [scan] + [_P] * 22 + [z, _P], i)):
+                ("gdn_selective_scan_bwd", [scan] + [_P] * 22 + [z, _P], i),
+                ("gdn_add_rmsnorm", [norm] + [_P] * 6, i),
+                ("gdn_add_rmsnorm_fp8", [norm] + [_P] * 7, i),
+                ("gdn_add_rmsnorm_bwd_workspace_size", [norm], z),
+                ("gdn_add_rmsnorm_bwd", [norm] + [_P] * 7 + [z, _P], i),
+                ("gdn_linear_recurrence_fwd", [rec] + [_P] * 8 + [i, _P, _P, _P], i),
+                ("gdn_linear_recurrence_update", [rec] + [_P] * 7 + [i, _P, _P], i),
+                ("gdn_linear_recurrence_bwd_workspace_size", [rec], z),
+                ("gdn_linear_recurrence_bwd", [rec] + [_P] * 16 + [z, _P], i)):
             getattr(L, name).argtypes, getattr(L, name).restype = args, res
         L.gdn_status_string.argtypes = [ctypes.c_int]
         L.gdn_status_string.restype = ctypes.c_char_p
@@ -780,6 +802,179 @@ def gdn_selective_scan_bwd(x, dt, A_log, B, C, cu_seqlens, d_out, D=None, z=None
                d_init_state=torch.empty(state, dtype=torch.float32, device=x.device) if need_d_init_state else None)
     ws = _space(workspace, _space_of("gdn_selective_scan_bwd_workspace_size", *sizes), x.device)
     _invoke("gdn_selective_scan_bwd", index, _struct(*sizes), *ptrs, *more, *map(_at, res.values()), ws.data_ptr(),
+            ws.numel())
+    return res
+
+
+def _wide(t, name, shape, dtype, index):
+    """_rows for rows of any leading dimensions: [.., d] dense, or [rows, d] with a stride between the rows."""
+    if len(shape) == 2:
+        return _rows(t, name, shape, dtype, index)
+    return _is(t, name, shape, dtype, index), shape[-1]
+
+
+def _add_norm(x, weight, residual, eps, residual_out, group):
+    """Sizes for the struct, the device index, residual_out, and the addresses of x, residual, weight and residual_out."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    shape, ty, index, xp, ldx, rp, ldr = _first(x, "x", x.dim() or 1) + (None, 0, None, 0)
+    d = shape[-1]
+    if d == 0:
+        raise ValueError("x must not have rows of width 0")
+    xp, ldx = _wide(x, "x", shape, ty, index)
+    if residual is not None:
+        rp, ldr = _wide(residual, "residual", shape, ty, index)
+        residual_out = _dense(x) if residual_out is None else residual_out
+    elif residual_out is not None:
+        raise ValueError("residual_out is written with a residual only")
+    sizes = (AddNormShape, x.numel() // d, d, _dtype_code(x), float(eps), group, ldx, ldr)
+    return sizes, index, residual_out, (xp, rp, _is(weight, "weight", (d,), torch.float32, index),
+                                        _is(residual_out, "residual_out", shape, ty, index))
+
+
+def _dense(t):
+    """A dense tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def gdn_add_rmsnorm(x, weight, residual=None, eps=1e-6, out=None, residual_out=None, stream=None):
+    """RMSNorm of s = x + residual over the last axis: s / sqrt(mean(s^2) + eps) *
+    weight, with s rounded to the dtype first.  x, residual [.., d] (bf16 or fp32,
+    dense or, with two dimensions, rows of a wider tensor); weight [d] fp32.
+    Returns dense (out, residual_out = s); residual None: (norm of x, None).  out
+    and residual_out may be x or residual where those are dense."""
+    if stream is not None:
+        return _on(gdn_add_rmsnorm, locals())
+    sizes, index, residual_out, ptrs = _add_norm(x, weight, residual, eps, residual_out, 0)
+    out = _dense(x) if out is None else out
+    _invoke("gdn_add_rmsnorm", index, _struct(*sizes), *ptrs, _is(out, "out", x.shape, x.dtype, index))
+    return out, residual_out
+
+
+def gdn_add_rmsnorm_fp8(x, weight, residual=None, eps=1e-6, group=128, out=None, scales=None, residual_out=None,
+                        stream=None):
+    """gdn_add_rmsnorm with its output in 8 bits: (out [.., d] float8_e4m3fn, scales
+    [.., ceil(d / group)] fp32, residual_out).  scale = max |values of the group| /
+    448 and out = value / scale; group 32, 64 or 128 consecutive values, or 0 for
+    one scale per row ([.., 1])."""
+    if stream is not None:
+        return _on(gdn_add_rmsnorm_fp8, locals())
+    sizes, index, residual_out, ptrs = _add_norm(x, weight, residual, eps, residual_out, int(group))
+    shape, d = x.shape, x.shape[-1]
+    cols = shape[:-1] + ((d + group - 1) // group if group > 0 else 1,)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty(cols, dtype=torch.float32, device=x.device)
+    _invoke("gdn_add_rmsnorm_fp8", index, _struct(*sizes), *ptrs, _is(out, "out", shape, torch.float8_e4m3fn, index),
+            _is(scales, "scales", cols, torch.float32, index))
+    return out, scales, residual_out
+
+
+def gdn_add_rmsnorm_bwd(s, weight, d_out, d_residual_out=None, eps=1e-6, dx=None, workspace=None, stream=None):
+    """Gradient of gdn_add_rmsnorm from s, the residual_out it returned (its x where
+    it had no residual).  d_out, d_residual_out (None: zero) like s, dense.
+    Returns dict dx (the gradient of x and of residual alike; may be d_out,
+    d_residual_out or a dense s) and dweight (fp32)."""
+    if stream is not None:
+        return _on(gdn_add_rmsnorm_bwd, locals())
+    sizes, index, _, (sp, _, wp, _) = _add_norm(s, weight, None, eps, None, 0)
+    shape, ty = s.shape, s.dtype
+    grads = (_is(d_out, "d_out", shape, ty, index), _is(d_residual_out, "d_residual_out", shape, ty, index))
+    dx = _dense(s) if dx is None else dx
+    dw = _like(weight)
+    ws = _space(workspace, _space_of("gdn_add_rmsnorm_bwd_workspace_size", *sizes), s.device)
+    _invoke("gdn_add_rmsnorm_bwd", index, _struct(*sizes), sp, wp, *grads, _is(dx, "dx", shape, ty, index), dw.data_ptr(),
+            ws.data_ptr(), ws.numel())
+    return dict(dx=dx, dweight=dw)
+
+
+# ---------------------------------------------------------------- gated linear recurrence (include/gdn_linrec.h)
+
+_SCALES = {"sqrt": 0, "linear": 1, "one": 2}
+_ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def _linrec(shape, ty, index, x, a_gate, a_param, x_gate, z, N, input_scale, decay, activation):
+    """Sizes for the struct and the inputs' addresses, x to z."""
+    if input_scale not in _SCALES:
+        raise ValueError(f"input_scale must be one of {sorted(_SCALES)}, got {input_scale!r}")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+    (xp, ldx), (ap, lda) = _rows(x, "x", shape, ty, index), _rows(a_gate, "a_gate", shape, ty, index)
+    gp, ldg = (None, 0) if x_gate is None else _rows(x_gate, "x_gate", shape, ty, index)
+    zp, ldz = (None, 0) if z is None else _rows(z, "z", shape, ty, index)
+    return (LinrecShape, N, shape[0], shape[1], _dtype_code(x), _SCALES[input_scale], _ACTIVATIONS[activation], float(decay),
+            ldx, lda, ldg, ldz), (xp, ap, _is(a_param, "a_param", (shape[1],), torch.float32, index), gp, zp)
+
+
+def gdn_linear_recurrence_fwd(x, a_gate, cu_seqlens, a_param=None, x_gate=None, z=None, state=None, state_indices=None,
+                              has_initial_state=None, input_scale="sqrt", decay=8.0, activation="silu", out=None,
+                              stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + s_t x_t sigmoid(x_gate_t), y_t =
+    h_t act(z_t), over a packed varlen batch, with a_t = exp(-decay
+    softplus(a_param) sigmoid(a_gate_t)), or sigmoid(a_gate_t) without a_param, and
+    s_t = sqrt(1 - a_t^2), 1 - a_t or 1 (input_scale "sqrt", "linear", "one").
+
+    x, a_gate, x_gate, z [T, channels] (bf16 or fp32, one dtype, rows may be slices
+    of wider ones; x_gate None: 1; z None: y = h); a_param [channels] fp32;
+    activation "silu" or "gelu" (tanh form).  cu_seqlens int32 [N+1] on the device.
+    state [slots, channels] fp32 is read as the initial state and overwritten with
+    the final state of each sequence's slot (in place; int32 state_indices,
+    has_initial_state as in gdn_causal_conv1d_fwd).  Returns y [T, channels] (rows
+    behind cu_seqlens[N] not written)."""
+    if stream is not None:
+        return _on(gdn_linear_recurrence_fwd, locals())
+    shape, ty, index = _first(x, "x", 2)
+    N, cu = _sequences(cu_seqlens, index)
+    sizes, ptrs = _linrec(shape, ty, index, x, a_gate, a_param, x_gate, z, N, input_scale, decay, activation)
+    slots = 0 if state is None else _dims(state, "state", 2)[0]
+    state_ptrs = (_is(state, "state", (slots, shape[1]), torch.float32, index),
+                  _is(state_indices, "state_indices", (N,), torch.int32, index), slots,
+                  _is(has_initial_state, "has_initial_state", (N,), torch.int32, index))
+    out = _dense(x) if out is None else out
+    _invoke("gdn_linear_recurrence_fwd", index, _struct(*sizes), *ptrs, cu, *state_ptrs, _is(out, "out", shape, ty, index))
+    return out
+
+
+def gdn_linear_recurrence_update(x, a_gate, state, state_indices=None, a_param=None, x_gate=None, z=None,
+                                 input_scale="sqrt", decay=8.0, activation="silu", out=None, stream=None):
+    """One token per sequence: x, a_gate, x_gate, z [N, channels]; state [slots,
+    channels] fp32 updated in place.  Returns y [N, channels] (rows of skipped slots
+    untouched)."""
+    if stream is not None:
+        return _on(gdn_linear_recurrence_update, locals())
+    shape, ty, index = _first(x, "x", 2)
+    sizes, ptrs = _linrec(shape, ty, index, x, a_gate, a_param, x_gate, z, shape[0], input_scale, decay, activation)
+    slots = _dims(state, "state", 2)[0]
+    state_ptrs = (_is(state, "state", (slots, shape[1]), torch.float32, index),
+                  _is(state_indices, "state_indices", (shape[0],), torch.int32, index), slots)
+    out = _dense(x) if out is None else out
+    _invoke("gdn_linear_recurrence_update", index, _struct(*sizes), *ptrs, *state_ptrs, _is(out, "out", shape, ty, index))
+    return out
+
+
+def gdn_linear_recurrence_bwd(x, a_gate, cu_seqlens, d_out, a_param=None, x_gate=None, z=None, init_state=None,
+                              d_final_state=None, input_scale="sqrt", decay=8.0, activation="silu", workspace=None,
+                              need_d_init_state=True, stream=None):
+    """Gradient of gdn_linear_recurrence_fwd.  d_out [T, channels]; init_state,
+    d_final_state [N, channels] fp32 or None (zero), in the order of the sequences.
+    Returns dict dx, da_gate, dx_gate, dz (dtype of x), da_param, d_init_state
+    (fp32); None where the input is None.  Rows behind cu_seqlens[N] are not
+    written."""
+    if stream is not None:
+        return _on(gdn_linear_recurrence_bwd, locals())
+    shape, ty, index = _first(x, "x", 2)
+    N, cu = _sequences(cu_seqlens, index)
+    sizes, ptrs = _linrec(shape, ty, index, x, a_gate, a_param, x_gate, z, N, input_scale, decay, activation)
+    state = (N, shape[1])
+    more = (cu, _is(init_state, "init_state", state, torch.float32, index), _is(d_out, "d_out", shape, ty, index),
+            _is(d_final_state, "d_final_state", state, torch.float32, index))
+    res = dict(dx=_dense(x), da_gate=_dense(x), da_param=_like(a_param), dx_gate=None if x_gate is None else _dense(x),
+               dz=None if z is None else _dense(x),
+               d_init_state=torch.empty(state, dtype=torch.float32, device=x.device) if need_d_init_state else None)
+    ws = _space(workspace, _space_of("gdn_linear_recurrence_bwd_workspace_size", *sizes), x.device)
+    _invoke("gdn_linear_recurrence_bwd", index, _struct(*sizes), *ptrs, *more, *map(_at, res.values()), ws.data_ptr(),
             ws.numel())
     return res
 

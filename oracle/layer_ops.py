@@ -160,3 +160,30 @@ def norm_rope_bwd(x, weight, cos, sin, d_out, norm="rms", eps=1e-6, interleaved=
     g = dn * (1.0 if weight is None else weight)
     share = 1.0 / x.shape[-1] if norm == "rms" else 1.0
     return r * g - x * r ** 3 * share * (g * x).sum(-1, keepdims=True), (dn * x * r).sum((0, 1))
+
+
+def add_rmsnorm(s, weight, eps=1e-6):
+    """The norm of s = x + residual (already rounded to its type) over the last axis, in float64."""
+    s, weight = map(_f64, (s, weight))
+    return s / np.sqrt((s * s).mean(-1, keepdims=True) + eps) * weight
+
+
+def group_scales(n, group):
+    """max |n| / 448 of each `group` consecutive values of a row (0: the row), at least 2^-126."""
+    d = n.shape[-1]
+    per = group or d
+    most = np.stack([np.abs(n[..., i:i + per]).max(-1) for i in range(0, d, per)], -1)
+    return np.maximum(most / 448, 2.0 ** -126)
+
+
+def add_rmsnorm_bwd(s, weight, d_out, d_residual_out=None, eps=1e-6, magnitude=False):
+    """(dx, dweight); magnitude: sums over their terms' absolute values."""
+    s, weight, dy = map(_f64, (s, weight, d_out))
+    res = 0.0 if d_residual_out is None else _f64(d_residual_out)
+    r = 1 / np.sqrt((s * s).mean(-1, keepdims=True) + eps)
+    if magnitude:
+        s, weight, dy, res = np.abs(s), np.abs(weight), np.abs(dy), np.abs(res)
+    g = dy * weight
+    second = s * r ** 3 * (g * s).mean(-1, keepdims=True)
+    dx = r * g + (second if magnitude else -second) + res
+    return dx, (dy * s * r).reshape(-1, s.shape[-1]).sum(0)
