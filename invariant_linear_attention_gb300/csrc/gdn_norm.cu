@@ -42,18 +42,24 @@ __device__ __forceinline__ float over_lanes(float v, int lanes) {
     for (int off = 1; off < lanes; off <<= 1) v = OP::of(v, __shfl_xor_sync(0xffffffffu, v, off));
     return v;
 }
-// OP over a row's threads.  Every thread of the CTA calls it; `buf` holds a value per warp.
-template <typename OP>
-__device__ __forceinline__ float over_row(float v, int tpr, float* buf) {
-    v = over_lanes<OP>(v, tpr < 32 ? tpr : 32);
-    if (tpr <= 32) return v;
+// OP over a row's threads, of N values at once.  Every thread of the CTA calls it; `buf` holds N values per
+// warp, and the next call has another one.
+template <typename OP, int N>
+__device__ __forceinline__ void over_row(float (&v)[N], int tpr, float (&buf)[N][32]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = over_lanes<OP>(v[k], tpr < 32 ? tpr : 32);
+    if (tpr <= 32) return;
     const int warp = threadIdx.x / 32, per = tpr / 32, first = warp / per * per;
-    if (threadIdx.x % 32 == 0) buf[warp] = v;
+    if (threadIdx.x % 32 == 0) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) buf[k][warp] = v[k];
+    }
     __syncthreads();
-    v = buf[first];
-    for (int i = 1; i < per; ++i) v = OP::of(v, buf[first + i]);
-    __syncthreads();
-    return v;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        v[k] = buf[k][first];
+        for (int i = 1; i < per; ++i) v[k] = OP::of(v[k], buf[k][first + i]);
+    }
 }
 
 template <typename T>
@@ -79,142 +85,248 @@ __device__ __forceinline__ void store_fp8(uint8_t* to, const float (&v)[8]) {
 }
 __device__ __forceinline__ void store_fp8(uint8_t* to, const float (&v)[4]) { *reinterpret_cast<uint32_t*>(to) = fp8x4(v[0], v[1], v[2], v[3]); }
 
-template <typename T, int NC, bool FP8>
-__global__ void __launch_bounds__(1024) add_norm_kernel(const __grid_constant__ NormParams p) {
+constexpr float kTop = 448.f, kLeast = 1.17549435e-38f;  // e4m3's largest value; the smallest scale, 2^-126
+
+// A group's scale and the factor that takes its values t = s w to 8 bits.  The scale is the norm's r max|t| / 448, but the
+// values go by 448 / max|t|: r's error and a rounding each stay out of them.  The reciprocal is the hardware's with
+// a step of Newton's method.  (Where that is past fp32, in a group of next to nothing, the values are multiplied by r first.)
+struct Scale {
+    float scale, by;
+    bool tiny;
+    template <int VN>
+    __device__ __forceinline__ void apply(float (&v)[VN], float r) const {
+        if (tiny) {
+#pragma unroll
+            for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(v[e], r);
+        }
+#pragma unroll
+        for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(v[e], by);
+    }
+};
+__device__ __forceinline__ Scale scale_of(float most, float r) {
+    Scale s;
+    s.scale = fmaxf(__fmul_rn(__fmul_rn(most, r), 1.f / kTop), kLeast);
+    s.tiny = !(most > 1e-30f);
+    const float x = s.tiny ? s.scale : most, y = rcp_approx(x);
+    const float z = __fmaf_rn(y, __fmaf_rn(-x, y, 1.f), y);
+    s.by = s.tiny ? y : __fmul_rn(kTop, most < 1e38f ? z : y);
+    return s;
+}
+
+// A CTA takes rows blockIdx.x, + gridDim.x, ..  Up to two chunks a thread (NC), it keeps its weights in registers and
+// has the next row's loads under way while a row is summed and stored.  A row waits packed, as it is stored.
+template <typename T, int NC, int NT, bool FP8>
+__global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 ? 2 : 1) add_norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int VN = V16<T>::n;
-    __shared__ float buf[32];
-    const int lane = threadIdx.x % p.tpr;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x / p.tpr) + threadIdx.x / p.tpr;
-    const bool live = row < p.rows;
-    float v[NC][VN], ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = lane + i * p.tpr;
-        if (live && c < p.chunks) {
-            unpack(ld16_stream(static_cast<const T*>(p.x) + row * p.ldx + c * VN), v[i]);
-            if (p.res) {
-                float a[VN];
-                unpack(ld16_stream(static_cast<const T*>(p.res) + row * p.ldr + c * VN), a);
-#pragma unroll
-                for (int e = 0; e < VN; ++e) v[i][e] = to_f(rounded<T>(__fadd_rn(v[i][e], a[e])));
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < VN; ++e) v[i][e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < VN; ++e) ss = __fmaf_rn(v[i][e], v[i][e], ss);
-    }
-    const float r = rsqrtf(__fmaf_rn(over_row<Sum>(ss, p.tpr, buf), p.c, p.eps));
-    float most = 0.f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c = lane + i * p.tpr;
-        const bool has = live && c < p.chunks;
-        if (has && p.res) st16(static_cast<T*>(p.res_out) + row * p.d + c * VN, pack(v[i]));
-        if (has) {
-            float w[VN];
-            load_weight(p.w + c * VN, w);
-#pragma unroll
-            for (int e = 0; e < VN; ++e) v[i][e] = __fmul_rn(__fmul_rn(v[i][e], r), w[e]);
-        }
-        if constexpr (!FP8) {
-            if (has) st16(static_cast<T*>(p.y) + row * p.d + c * VN, pack(v[i]));
-        } else {
-            float m = 0.f;
-#pragma unroll
-            for (int e = 0; e < VN; ++e) m = fmaxf(m, fabsf(v[i][e]));
-            if (p.glanes) {
-                const float scale = fmaxf(__fmul_rn(over_lanes<Max>(m, p.glanes), 1.f / 448.f), 1.17549435e-38f), inv = __frcp_rn(scale);
-#pragma unroll
-                for (int e = 0; e < VN; ++e) v[i][e] = __fmul_rn(v[i][e], inv);
-                if (has) store_fp8(static_cast<uint8_t*>(p.y) + row * p.d + c * VN, v[i]);
-                if (has && lane % p.glanes == 0) p.scales[row * p.groups + c / p.glanes] = scale;
-            } else {
-                most = fmaxf(most, m);
-            }
-        }
-    }
-    if constexpr (FP8) {
-        if (p.glanes) return;
-        const float scale = fmaxf(__fmul_rn(over_row<Max>(most, p.tpr, buf), 1.f / 448.f), 1.17549435e-38f), inv = __frcp_rn(scale);
-        if (live && lane == 0) p.scales[row] = scale;
+    constexpr bool ahead = NC <= 2;
+    __shared__ float buf[2][1][32], buf2[2][1][32];
+    const int lane = threadIdx.x % p.tpr, per = NT / p.tpr;
+    const bool res = p.res != nullptr;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 a[NC], b[NC];
+    auto load = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
-            if (!live || c >= p.chunks) continue;
+            const bool has = row < p.rows && c < p.chunks;
+            a[i] = has ? ld16_stream(static_cast<const T*>(p.x) + row * p.ldx + c * VN) : none;
+            b[i] = has && res ? ld16_stream(static_cast<const T*>(p.res) + row * p.ldr + c * VN) : none;
+        }
+    };
+    float wk[ahead ? NC : 1][VN];
+    auto weight = [&](int i, float (&w)[VN]) {
+        if (lane + i * p.tpr < p.chunks) load_weight(p.w + (lane + i * p.tpr) * VN, w);
+    };
+    auto values = [&](int i, const uint4& s, float (&v)[VN]) {  // s w
+        unpack(s, v);
+        if constexpr (!ahead) weight(i, wk[0]);
 #pragma unroll
-            for (int e = 0; e < VN; ++e) v[i][e] = __fmul_rn(v[i][e], inv);
-            store_fp8(static_cast<uint8_t*>(p.y) + row * p.d + c * VN, v[i]);
+        for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(v[e], wk[ahead ? i : 0][e]);
+    };
+    if constexpr (ahead) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) weight(i, wk[i]);
+    }
+    const int64_t step = (int64_t)gridDim.x * per;
+    int64_t first = (int64_t)blockIdx.x * per;
+    load(first + threadIdx.x / p.tpr);
+    for (int turn = 0; first < p.rows; first += step, turn ^= 1) {
+        const int64_t row = first + threadIdx.x / p.tpr;
+        uint4 s[NC];
+        float ss[1] = {0.f};
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = lane + i * p.tpr;
+            float v[VN];
+            s[i] = a[i];
+            unpack(a[i], v);
+            if (res) {
+                float add[VN];
+                unpack(b[i], add);
+#pragma unroll
+                for (int e = 0; e < VN; ++e) v[e] = __fadd_rn(v[e], add[e]);
+                s[i] = pack(v);
+                unpack(s[i], v);
+                if (row < p.rows && c < p.chunks) st16_stream(static_cast<T*>(p.res_out) + row * p.d + c * VN, s[i]);
+            }
+#pragma unroll
+            for (int e = 0; e < VN; ++e) ss[0] = __fmaf_rn(v[e], v[e], ss[0]);
+        }
+        load(row + step);
+        over_row<Sum>(ss, p.tpr, buf[turn]);
+        const float r = rsqrtf(__fmaf_rn(ss[0], p.c, p.eps));
+        float most[1] = {0.f};
+        if constexpr (FP8) {
+            if (!p.glanes) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    if (lane + i * p.tpr >= p.chunks) continue;
+                    float v[VN];
+                    values(i, s[i], v);
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) most[0] = fmaxf(most[0], fabsf(v[e]));
+                }
+                over_row<Max>(most, p.tpr, buf2[turn]);
+            }
+        }
+        [[maybe_unused]] Scale whole;
+        if constexpr (FP8) {
+            if (!p.glanes) {
+                whole = scale_of(most[0], r);
+                if (row < p.rows && lane == 0) p.scales[row] = whole.scale;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int c = lane + i * p.tpr;
+            const bool has = row < p.rows && c < p.chunks;
+            float v[VN];
+            if constexpr (!FP8) {
+                unpack(s[i], v);
+                if constexpr (!ahead) weight(i, wk[0]);
+#pragma unroll
+                for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], r), wk[ahead ? i : 0][e]);
+                if (has) st16_stream(static_cast<T*>(p.y) + row * p.d + c * VN, pack(v));
+            } else {
+                values(i, s[i], v);
+                if (!p.glanes) {
+                    whole.apply(v, r);
+                } else {
+                    float m = 0.f;
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) m = fmaxf(m, fabsf(v[e]));
+                    const Scale sc = scale_of(over_lanes<Max>(has ? m : 0.f, p.glanes), r);
+                    sc.apply(v, r);
+                    if (has && lane % p.glanes == 0) p.scales[row * p.groups + c / p.glanes] = sc.scale;
+                }
+                if (has) store_fp8(static_cast<uint8_t*>(p.y) + row * p.d + c * VN, v);
+            }
         }
     }
 }
 
-template <typename T, int NC>
-__global__ void __launch_bounds__(1024) add_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+// The gradient takes rows the same way.  sum(g s) needs no r, so that both sums go together.  dw: a thread's
+// columns in registers, with more than two chunks in its own places of shared memory.
+template <typename T, int NC, int NT>
+__global__ void __launch_bounds__(NT, NT <= 256 ? 2 : 1) add_norm_bwd_kernel(const __grid_constant__ NormParams p) {
     constexpr int VN = V16<T>::n;
-    __shared__ float buf[32];
-    extern __shared__ float acc[];  // [rows of the CTA][d]
-    const int lane = threadIdx.x % p.tpr, per = blockDim.x / p.tpr, mine = threadIdx.x / p.tpr;
-    float dw[NC][VN];
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-#pragma unroll
-        for (int e = 0; e < VN; ++e) dw[i][e] = 0.f;
-    for (int64_t first = (int64_t)blockIdx.x * per; first < p.rows; first += (int64_t)gridDim.x * per) {
-        const int64_t row = first + mine;
-        const bool live = row < p.rows;
-        float v[NC][VN], g[NC][VN], ss = 0.f, gx = 0.f;
+    constexpr bool ahead = NC <= 2;
+    __shared__ float buf[2][2][32];
+    extern __shared__ __align__(16) float acc[];  // [rows of the CTA][d]
+    const int lane = threadIdx.x % p.tpr, per = NT / p.tpr, mine = threadIdx.x / p.tpr;
+    const bool res = p.dres != nullptr;
+    const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    uint4 xn[NC], gn[NC], rn[NC];
+    auto load = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c = lane + i * p.tpr;
-            if (live && c < p.chunks) {
-                unpack(ld16_stream(static_cast<const T*>(p.x) + row * p.ldx + c * VN), v[i]);
-                unpack(ld16_stream(static_cast<const T*>(p.dy) + row * p.d + c * VN), g[i]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VN; ++e) v[i][e] = g[i][e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < VN; ++e) ss = __fmaf_rn(v[i][e], v[i][e], ss);
+            const bool has = row < p.rows && c < p.chunks;
+            xn[i] = has ? ld16_stream(static_cast<const T*>(p.x) + row * p.ldx + c * VN) : none;
+            gn[i] = has ? ld16_stream(static_cast<const T*>(p.dy) + row * p.d + c * VN) : none;
+            rn[i] = has && res ? ld16_stream(static_cast<const T*>(p.dres) + row * p.d + c * VN) : none;
         }
-        const float r = rsqrtf(__fmaf_rn(over_row<Sum>(ss, p.tpr, buf), p.c, p.eps));
+    };
+    float wk[ahead ? NC : 1][VN], dw[ahead ? NC : 1][VN];
+    auto weight = [&](int i, float (&w)[VN]) {
+        if (lane + i * p.tpr < p.chunks) load_weight(p.w + (lane + i * p.tpr) * VN, w);
+    };
+    auto put = [&](int i, const float (&v)[VN]) {
+        float4* to = reinterpret_cast<float4*>(acc + (int64_t)mine * p.d + (lane + i * p.tpr) * VN);
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            if (!live || c >= p.chunks) continue;
-            float w[VN];
-            load_weight(p.w + c * VN, w);
-#pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                dw[i][e] = __fmaf_rn(__fmul_rn(v[i][e], r), g[i][e], dw[i][e]);
-                g[i][e] = __fmul_rn(g[i][e], w[e]);
-                gx = __fmaf_rn(g[i][e], v[i][e], gx);
-            }
-        }
-        // r (g - s (r sum(g s)) (r c)): these products stay in range where r^3 is not
-        const float f = -__fmul_rn(__fmul_rn(r, over_row<Sum>(gx, p.tpr, buf)), __fmul_rn(r, p.c));
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            if (!live || c >= p.chunks) continue;
-            float o[VN];
-            if (p.dres) unpack(ld16_stream(static_cast<const T*>(p.dres) + row * p.d + c * VN), o);
-#pragma unroll
-            for (int e = 0; e < VN; ++e) o[e] = __fmaf_rn(r, __fmaf_rn(v[i][e], f, g[i][e]), p.dres ? o[e] : 0.f);
-            st16(static_cast<T*>(p.y) + row * p.d + c * VN, pack(o));
-        }
-    }
-    if (!p.part) return;
+        for (int e = 0; e < VN; e += 4) to[e / 4] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    };
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int c = lane + i * p.tpr;
-        if (c >= p.chunks) continue;
+        float (&d)[VN] = dw[ahead ? i : 0], (&w)[VN] = wk[ahead ? i : 0];
 #pragma unroll
-        for (int e = 0; e < VN; ++e) acc[(int64_t)mine * p.d + c * VN + e] = dw[i][e];
+        for (int e = 0; e < VN; ++e) w[e] = d[e] = 0.f;
+        if constexpr (ahead) weight(i, w);
+        else if (p.part && lane + i * p.tpr < p.chunks) put(i, d);
+    }
+    const int64_t step = (int64_t)gridDim.x * per;
+    int64_t first = (int64_t)blockIdx.x * per;
+    load(first + mine);
+    for (int turn = 0; first < p.rows; first += step, turn ^= 1) {
+        const int64_t row = first + mine;
+        uint4 xs[NC], gs[NC], rs[NC];
+        float sums[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float v[VN], g[VN];
+            xs[i] = xn[i], gs[i] = gn[i], rs[i] = rn[i];
+            unpack(xs[i], v);
+            unpack(gs[i], g);
+            if constexpr (!ahead) weight(i, wk[0]);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) {
+                sums[0] = __fmaf_rn(v[e], v[e], sums[0]);
+                sums[1] = __fmaf_rn(__fmul_rn(g[e], wk[ahead ? i : 0][e]), v[e], sums[1]);
+            }
+        }
+        if constexpr (ahead) load(row + step);
+        over_row<Sum>(sums, p.tpr, buf[turn]);
+        const float r = rsqrtf(__fmaf_rn(sums[0], p.c, p.eps));
+        // r (g - s (r sum(g s)) (r c)): these products stay in range where r^3 is not
+        const float f = -__fmul_rn(__fmul_rn(r, sums[1]), __fmul_rn(r, p.c));
+        if (row < p.rows) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                const int c = lane + i * p.tpr;
+                if (c >= p.chunks) continue;
+                float v[VN], g[VN], o[VN];
+                unpack(xs[i], v);
+                unpack(gs[i], g);
+                unpack(rs[i], o);
+                float (&d)[VN] = dw[ahead ? i : 0];
+                if constexpr (!ahead) {
+                    weight(i, wk[0]);
+                    if (p.part) {
+#pragma unroll
+                        for (int e = 0; e < VN; e += 4) unpack(*reinterpret_cast<const uint4*>(acc + (int64_t)mine * p.d + c * VN + e), reinterpret_cast<float(&)[4]>(d[e]));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < VN; ++e) {
+                    d[e] = __fmaf_rn(__fmul_rn(v[e], r), g[e], d[e]);
+                    o[e] = __fmaf_rn(r, __fmaf_rn(v[e], f, __fmul_rn(g[e], wk[ahead ? i : 0][e])), o[e]);
+                }
+                st16_stream(static_cast<T*>(p.y) + row * p.d + c * VN, pack(o));
+                if constexpr (!ahead) {
+                    if (p.part) put(i, d);
+                }
+            }
+        }
+        if constexpr (!ahead) load(row + step);
+    }
+    if (!p.part) return;
+    if constexpr (ahead) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            if (lane + i * p.tpr < p.chunks) put(i, dw[i]);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.d; e += blockDim.x) {
+    for (int e = threadIdx.x; e < p.d; e += NT) {
         float s = acc[e];
         for (int i = 1; i < per; ++i) s = __fadd_rn(s, acc[(int64_t)i * p.d + e]);
         p.part[(int64_t)blockIdx.x * p.d + e] = s;
@@ -239,7 +351,8 @@ __global__ void __launch_bounds__(256) add_norm_sum_kernel(int d, int ctas, cons
     *reinterpret_cast<float4*>(out + e) = s;
 }
 
-constexpr int kMaxWidth = 16384, kMaxChunks = 4;  // chunks a thread holds
+constexpr int kRowThreads = 256;  // of a CTA, unless a row has more
+constexpr int kMaxWidth = 16384;
 
 gdn_status check_norm(const gdn_add_norm_shape* s) {
     if (!s) return GDN_ERR_INVALID_ARG;
@@ -251,51 +364,56 @@ gdn_status check_norm(const gdn_add_norm_shape* s) {
     return GDN_OK;
 }
 
-// Threads of a row: one chunk each up to a warp, then up to kMaxChunks.
+// Threads of a row: one chunk each up to a warp, then up to two, from 512 threads on up to four.
 NormParams norm_params(const gdn_add_norm_shape* s) {
     NormParams p{};
     p.rows = s->rows, p.d = s->d, p.eps = s->eps, p.c = 1.f / (float)s->d, p.ldx = s->ldx, p.ldr = s->ldr;
     p.chunks = s->d / (s->dtype == GDN_BF16 ? 8 : 4);
     p.tpr = 1;
-    while (p.tpr < p.chunks && (p.tpr < 32 || p.tpr * kMaxChunks < p.chunks)) p.tpr *= 2;
+    while (p.tpr < p.chunks && (p.tpr < 32 || p.tpr * (p.tpr < 512 ? 2 : 4) < p.chunks)) p.tpr *= 2;
     return p;
 }
-int cta_threads(const NormParams& p) { return p.tpr > 256 ? p.tpr : 256; }
-int bwd_ctas(const NormParams& p) {
+int cta_threads(const NormParams& p) { return p.tpr > kRowThreads ? p.tpr : kRowThreads; }
+// CTAs that walk the rows: `each` threads an SM, a row for every group of threads at least.
+int ctas_for(const NormParams& p, int each) {
     const int threads = cta_threads(p);
-    const int64_t want = (p.rows * p.tpr + threads - 1) / threads, most = (int64_t)kSMs * (threads > 512 ? 1 : 2);
+    const int64_t per = threads / p.tpr, want = (p.rows + per - 1) / per, most = (int64_t)kSMs * (each > threads ? each / threads : 1);
     return (int)(want < most ? (want > 1 ? want : 1) : most);
 }
+int bwd_ctas(const NormParams& p) { return ctas_for(p, 512); }
 
-// K<T, NC>::go(grid, threads, stream, p)
-template <template <typename, int> class K, typename T>
+// K<T, NC, NT>::go(grid, stream, p)
+template <template <typename, int, int> class K, typename T>
 gdn_status by_chunks(int grid, cudaStream_t s, const NormParams& p) {
-    const int nc = (p.chunks + p.tpr - 1) / p.tpr, threads = cta_threads(p);
-    if (nc <= 1) return K<T, 1>::go(grid, threads, s, p);
-    if (nc == 2) return K<T, 2>::go(grid, threads, s, p);
-    return K<T, 4>::go(grid, threads, s, p);
+    const int nc = (p.chunks + p.tpr - 1) / p.tpr;
+    if (nc <= 1) return K<T, 1, kRowThreads>::go(grid, s, p);
+    if (nc == 2) return p.tpr <= kRowThreads ? K<T, 2, kRowThreads>::go(grid, s, p) : K<T, 2, 512>::go(grid, s, p);
+    if constexpr (sizeof(T) == 4) {
+        if (p.tpr > 512) return K<T, 4, 1024>::go(grid, s, p);
+    }
+    return K<T, 4, 512>::go(grid, s, p);
 }
-template <typename T, int NC>
+template <typename T, int NC, int NT>
 struct SameK {
-    static gdn_status go(int grid, int threads, cudaStream_t s, const NormParams& p) {
-        add_norm_kernel<T, NC, false><<<grid, threads, 0, s>>>(p);
+    static gdn_status go(int grid, cudaStream_t s, const NormParams& p) {
+        add_norm_kernel<T, NC, NT, false><<<grid, NT, 0, s>>>(p);
         return launch_status();
     }
 };
-template <typename T, int NC>
+template <typename T, int NC, int NT>
 struct Fp8K {
-    static gdn_status go(int grid, int threads, cudaStream_t s, const NormParams& p) {
-        add_norm_kernel<T, NC, true><<<grid, threads, 0, s>>>(p);
+    static gdn_status go(int grid, cudaStream_t s, const NormParams& p) {
+        add_norm_kernel<T, NC, NT, true><<<grid, NT, 0, s>>>(p);
         return launch_status();
     }
 };
-template <typename T, int NC>
+template <typename T, int NC, int NT>
 struct BwdK {
-    static gdn_status go(int grid, int threads, cudaStream_t s, const NormParams& p) {
-        const size_t smem = p.part ? (size_t)(threads / p.tpr) * p.d * sizeof(float) : 0;
-        if (smem > 48 * 1024 - 256 && cudaFuncSetAttribute(add_norm_bwd_kernel<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    static gdn_status go(int grid, cudaStream_t s, const NormParams& p) {
+        const size_t smem = p.part ? (size_t)(NT / p.tpr) * p.d * sizeof(float) : 0;
+        if (smem > 47 * 1024 && cudaFuncSetAttribute(add_norm_bwd_kernel<T, NC, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
             return GDN_ERR_CUDA;
-        add_norm_bwd_kernel<T, NC><<<grid, threads, smem, s>>>(p);
+        add_norm_bwd_kernel<T, NC, NT><<<grid, NT, smem, s>>>(p);
         return launch_status();
     }
 };
@@ -319,8 +437,7 @@ gdn_status norm_fwd(const gdn_add_norm_shape* shape, const void* x, const void* 
     // A group that takes in the whole row is the row.
     const int lanes = shape->group / vn;
     p.glanes = lanes >= p.chunks ? 0 : lanes, p.groups = p.glanes ? (p.chunks + lanes - 1) / lanes : 1;
-    const int rows = cta_threads(p) / p.tpr;
-    const int grid = (int)((p.rows + rows - 1) / rows);
+    const int grid = ctas_for(p, 3072);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (shape->dtype == GDN_BF16) return fp8 ? by_chunks<Fp8K, __nv_bfloat16>(grid, s, p) : by_chunks<SameK, __nv_bfloat16>(grid, s, p);
     return fp8 ? by_chunks<Fp8K, float>(grid, s, p) : by_chunks<SameK, float>(grid, s, p);
