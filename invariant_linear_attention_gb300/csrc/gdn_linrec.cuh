@@ -70,22 +70,23 @@ __device__ __forceinline__ void far1(float w, float& a, float& m) {
     const float e = ex2(__fmul_rn(w, -kLog2e));
     if (!(w < kNear)) a = e, m = __fadd_rn(1.f, -e);
 }
-__device__ __forceinline__ void decay2(const float2& w, float2& a, float2& m) {
-    m = near2(w);
-    a = __fadd2_rn(both(1.f), neg(m));
-    if (!(fmaxf(w.x, w.y) < kNear)) far1(w.x, a.x, m.x), far1(w.y, a.y, m.y);
+template <int NP>
+__device__ __forceinline__ void decays(const float2 (&w)[NP], float2 (&a)[NP], float2 (&m)[NP]) {
+    float most = 0.f;
+#pragma unroll
+    for (int e = 0; e < NP; ++e) {
+        m[e] = near2(w[e]);
+        a[e] = __fadd2_rn(both(1.f), neg(m[e]));
+        most = fmaxf(most, fmaxf(w[e].x, w[e].y));
+    }
+    if (most >= kNear) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) far1(w[e].x, a[e].x, m[e].x), far1(w[e].y, a[e].y, m[e].y);
+    }
 }
 
 // 1 - a^2
 __device__ __forceinline__ float2 rest_of_square(const float2& a, const float2& m) { return __ffma2_rn(m, a, m); }
-
-// b = s v of one token.
-__device__ __forceinline__ float2 intake2(int scale, const float2& a, const float2& m, const float2& v) {
-    if (scale == GDN_SCALE_ONE) return v;
-    if (scale == GDN_SCALE_LINEAR) return __fmul2_rn(m, v);
-    const float2 t = rest_of_square(a, m);
-    return __fmul2_rn(make_float2(sqrt_approx(t.x), sqrt_approx(t.y)), v);
-}
 
 // The argument of the sigmoid in act(z).
 constexpr float kGelu1 = 1.5957691216057308f, kGelu3 = 0.07135481282553144f;  // 2 sqrt(2 / pi), times 0.044715
@@ -124,14 +125,69 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// a and b of one token's pair of channels.
-__device__ __forceinline__ void step2(const Params& p, const float2& K, const float2& ag, const float2& xg, const float2& x,
-                                      float2& a, float2& b) {
-    float2 e, m;
-    const float2 r = sigmoid2(ag, e);
-    if (p.ap) decay2(__fmul2_rn(K, r), a, m);
-    else a = r, m = rest2(e, r);
-    b = intake2(p.scale, a, m, p.xg ? __fmul2_rn(x, sigmoid2(xg)) : x);
+// a and b of NP pairs of channels of one token.  The call's options are branches around whole loops: one
+// compiled form for all, and the pairs' operations still overlap.
+template <int NP>
+__device__ __forceinline__ void steps(const Params& p, const float2 (&K)[NP], const float2 (&ag)[NP], const float2 (&xg)[NP],
+                                      const float2 (&x)[NP], float2 (&a)[NP], float2 (&b)[NP]) {
+    float2 m[NP];
+    if (p.ap) {
+        float2 w[NP];
+#pragma unroll
+        for (int e = 0; e < NP; ++e) w[e] = __fmul2_rn(K[e], sigmoid2(ag[e]));
+        decays(w, a, m);
+    } else {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            float2 u;
+            a[e] = sigmoid2(ag[e], u), m[e] = rest2(u, a[e]);
+        }
+    }
+    if (p.xg) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(x[e], sigmoid2(xg[e]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) b[e] = x[e];
+    }
+    if (p.scale == GDN_SCALE_SQRT) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+            const float2 t = rest_of_square(a[e], m[e]);
+            b[e] = __fmul2_rn(make_float2(sqrt_approx(t.x), sqrt_approx(t.y)), b[e]);
+        }
+    } else if (p.scale == GDN_SCALE_LINEAR) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(m[e], b[e]);
+    }
+}
+// y = h act(z) of NP pairs.
+template <int NP>
+__device__ __forceinline__ void branch(int act, const float2 (&z)[NP], float2 (&h)[NP]) {
+    float2 u[NP];
+#pragma unroll
+    for (int e = 0; e < NP; ++e) u[e] = z[e];
+    if (act == GDN_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) u[e] = inner2(GDN_ACT_GELU, z[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < NP; ++e) h[e] = __fmul2_rn(h[e], __fmul2_rn(z[e], sigmoid2(u[e])));
+}
+
+// The values of a 16-byte chunk as packed pairs, and back.
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[4]) {
+    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+    v[2] = make_float2(bf_lo(u.z), bf_hi(u.z)), v[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
+}
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
+    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint4 pack2(const float2 (&v)[4]) {
+    return make_uint4(bf_pack(v[0].x, v[0].y), bf_pack(v[1].x, v[1].y), bf_pack(v[2].x, v[2].y), bf_pack(v[3].x, v[3].y));
+}
+__device__ __forceinline__ uint4 pack2(const float2 (&v)[2]) {
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
 }
 
 // Bounds of sequence n, whatever cu_seqlens holds.

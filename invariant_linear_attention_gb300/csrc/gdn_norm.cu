@@ -109,7 +109,7 @@ __device__ __forceinline__ Scale scale_of(float most, float r) {
     s.tiny = !(most > 1e-30f);
     const float x = s.tiny ? s.scale : most, y = rcp_approx(x);
     const float z = __fmaf_rn(y, __fmaf_rn(-x, y, 1.f), y);
-    s.by = s.tiny ? y : __fmul_rn(kTop, most < 1e38f ? z : y);
+    s.by = __fmaf_rn(r, 0.f, s.tiny ? y : __fmul_rn(kTop, most < 1e38f ? z : y));  // a row whose r is not a number has no values
     return s;
 }
 
