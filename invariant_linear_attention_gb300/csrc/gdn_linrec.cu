@@ -20,36 +20,94 @@ using namespace linrec;
 #endif
 // Prompts.  A CTA walks one sequence over CB channels in tiles of TT tokens.  Nearly all the work of a token does not
 // depend on the one before it: only h <- a h + b does, 4 cycles a token.  So in step i
-//   * the workers, a 16-byte chunk of one token each, finish tile i - 2 (gate, 16-byte stores of y) and prepare tile i
-//     (a and b, to shared memory);
+//   * the workers, each four tokens of two channels (fp32: of one), finish tile i - 2 (gate, stores of y) and prepare
+//     tile i (a and b, to shared memory);
 //   * the walkers, a lane a channel, walk tile i - 1 and leave h in b's place;
-// and one barrier ends the step.  A worker reads the h of the very places that it then writes, so two buffers do.  Workers
-// copy their own inputs asynchronously, AHEAD tiles ahead, and read back only what they copied themselves.
+// and one barrier ends the step.  A worker reads the h of the very places that it then writes, so two buffers do.  The
+// inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead.
 template <typename T, int CB>
 struct FwdTile {
     static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = LR_WORK, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
     static constexpr int AHEAD = LR_AHEAD, ST = AHEAD + 1;
-    float a[2][TT][CB], b[2][TT][CB];
-    uint4 in[ST][4][WORK];  // x, a_gate, x_gate of a tile, z of the one two before
+    static constexpr int W = VN / 4, P = CB / W;  // a worker's channels; workers of a token
+    // Four tokens of a channel are 16 bytes, the walker's unit (with 4-byte loads its three a token took 14 cycles, not 4).
+    // Even channels come first, then the odd ones: a worker's two are P units apart, and its neighbours' next to them.
+    float4 a[2][TT / 4][CB], b[2][TT / 4][CB];
+    // x, a_gate, x_gate of a tile, z of the one two before.  Rows shorter than 128 bytes share them; their order there goes
+    // by the row's group of four too, so that a warp's workers, of several groups, meet no bank twice.
+    uint4 in[ST][4][WORK];
     float K[CB];
-    // Channel c of row t lies at place(t, c): 16-byte pieces of neighbouring chunks side by side, and halves swapped in every
-    // other row where a row is short, so that the workers' accesses (eight lanes at a time: one piece of eight chunks) meet no bank twice.
-    static constexpr int PIECES = VN / 4;  // of a chunk
-    static __device__ __forceinline__ int swap(int t) { return PIECES == 1 || CB > 32 ? 0 : CB == 32 ? t & 1 : (t >> 1) & 1; }
-    static __device__ __forceinline__ int piece(int t, int ch, int e) { return ((e ^ swap(t)) * CH + ch) * 4; }
-    static __device__ __forceinline__ int place(int t, int c) { return piece(t, c / VN, c % VN / 4) + c % 4; }
+    static constexpr int RS = 8 / CH;  // rows of 128 bytes
+    static __device__ __forceinline__ int line(int t) { return (t & ~(RS - 1)) | ((t ^ (t >> 2)) & (RS - 1)); }
+    static_assert(CH <= 8 && TT % 16 == 0, "rows of at most 128 bytes, tiles of whole walks");
 };
 
+// Shared memory in the order written: the compiler moves neither across the other.
+__device__ __forceinline__ float4 ld_shared4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t at, const float4& v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
 // All threads of the CTA meet, from whichever place in the code.
 template <int THREADS>
 __device__ __forceinline__ void step_end() {
     asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
+// Four tokens of a worker's channels: values [token] of two channels (bf16), [pair of tokens] of one (fp32).
+template <typename T>
+struct Four;
+template <>
+struct Four<__nv_bfloat16> {
+    static constexpr int NP = 4;
+    static __device__ __forceinline__ void load(const uint4* in, const int (&at)[4], float2 (&v)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t u = reinterpret_cast<const uint32_t*>(in)[at[j]];
+            v[j] = make_float2(bf_lo(u), bf_hi(u));
+        }
+    }
+    static __device__ __forceinline__ void put(float4* to, int P, const float2 (&v)[4]) {
+        to[0] = make_float4(v[0].x, v[1].x, v[2].x, v[3].x), to[P] = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+    }
+    static __device__ __forceinline__ void get(const float4* from, int P, float2 (&v)[4]) {
+        const float4 x = from[0], y = from[P];
+        v[0] = make_float2(x.x, y.x), v[1] = make_float2(x.y, y.y), v[2] = make_float2(x.z, y.z), v[3] = make_float2(x.w, y.w);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* y, int64_t ld, int rows, const float2 (&v)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < rows) *reinterpret_cast<uint32_t*>(y + j * ld) = bf_pack(v[j].x, v[j].y);
+    }
+};
+template <>
+struct Four<float> {
+    static constexpr int NP = 2;
+    static __device__ __forceinline__ void load(const uint4* in, const int (&at)[4], float2 (&v)[2]) {
+        const float* f = reinterpret_cast<const float*>(in);
+        v[0] = make_float2(f[at[0]], f[at[1]]), v[1] = make_float2(f[at[2]], f[at[3]]);
+    }
+    static __device__ __forceinline__ void put(float4* to, int, const float2 (&v)[2]) { to[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
+    static __device__ __forceinline__ void get(const float4* from, int, float2 (&v)[2]) {
+        const float4 x = from[0];
+        v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
+    }
+    static __device__ __forceinline__ void store(float* y, int64_t ld, int rows, const float2 (&v)[2]) {
+        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < rows) y[j * ld] = f[j];
+    }
+};
+
 template <typename T, int CB>
 __global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel(const __grid_constant__ Params p) {
     using F = FwdTile<T, CB>;
-    constexpr int VN = F::VN, NP = VN / 2, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST;
+    using Q = Four<T>;
+    constexpr int VN = F::VN, NP = Q::NP, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST, P = F::P;
     extern __shared__ __align__(16) unsigned char raw[];
     F& sm = *reinterpret_cast<F*>(raw);
     const int blocks = (p.C + CB - 1) / CB, n = blockIdx.x / blocks, c0 = blockIdx.x % blocks * CB;
@@ -58,104 +116,133 @@ __global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel
     const int tiles = (eos - bos + TT - 1) / TT;
     if (p.ap && threadIdx.x >= WORK && threadIdx.x - WORK < CB)
         sm.K[threadIdx.x - WORK] = c0 + (int)(threadIdx.x - WORK) < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x - WORK), p.decay) : 0.f;
-    __syncthreads();
 
     if (threadIdx.x < WORK) {
-        const int tid = threadIdx.x, row = tid / CH, ch = tid % CH, c = c0 + ch * VN;
-        const bool cok = c < p.C, gate = p.z != nullptr;
-        float2 K[NP];
-#pragma unroll
-        for (int e = 0; e < NP; ++e) K[e] = make_float2(sm.K[ch * VN + 2 * e], sm.K[ch * VN + 2 * e + 1]);
-        auto copy = [&](int i) {  // what step i needs
-            uint4(&to)[4][WORK] = sm.in[i % ST];
-            const int64_t t = (int64_t)bos + (int64_t)i * TT + row, tz = t - 2 * TT;
-            if (t < eos && cok) {
-                copy16_async(&to[0][tid], static_cast<const T*>(p.x) + t * p.ldx + c);
-                copy16_async(&to[1][tid], static_cast<const T*>(p.ag) + t * p.lda + c);
-                if (p.xg) copy16_async(&to[2][tid], static_cast<const T*>(p.xg) + t * p.ldg + c);
+        const int tid = threadIdx.x;
+        const bool gate = p.z != nullptr;
+        // its copies: a chunk of row tid / CH
+        const int row = tid / CH, slot = F::line(row) * CH + tid % CH, cc = c0 + tid % CH * VN;
+        int left = cc < p.C ? eos - bos - row : 0;  // rows from the next copy's on; below 1: none to copy
+        const T* px = static_cast<const T*>(p.x) + (int64_t)(bos + row) * p.ldx + cc;
+        const T* pa = static_cast<const T*>(p.ag) + (int64_t)(bos + row) * p.lda + cc;
+        const T* pg = p.xg ? static_cast<const T*>(p.xg) + (int64_t)(bos + row) * p.ldg + cc : nullptr;
+        const T* pz = gate ? static_cast<const T*>(p.z) + (int64_t)(bos + row) * p.ldz + cc : nullptr;
+        int stage = 0, zleft = left, behind = 2;
+        auto copy = [&] {  // what the next step that has no copies yet needs
+            uint4(&to)[4][WORK] = sm.in[stage];
+            stage = stage + 1 == ST ? 0 : stage + 1;
+            if (left > 0) {
+                copy16_async(&to[0][slot], px);
+                copy16_async(&to[1][slot], pa);
+                if (p.xg) copy16_async(&to[2][slot], pg);
             }
-            if (gate && tz >= bos && tz < eos && cok) copy16_async(&to[3][tid], static_cast<const T*>(p.z) + tz * p.ldz + c);
+            px += (int64_t)TT * p.ldx, pa += (int64_t)TT * p.lda, pg += (int64_t)TT * p.ldg, left -= TT;
+            if (behind > 0) {
+                --behind;
+            } else {
+                if (gate && zleft > 0) copy16_async(&to[3][slot], pz);
+                pz += (int64_t)TT * p.ldz, zleft -= TT;
+            }
             copy_commit();
         };
-        for (int i = 0; i < AHEAD; ++i) copy(i);
-        for (int i = 0; i < tiles + 2; ++i) {
-            copy(i + AHEAD);
-            copy_wait<AHEAD>();
-            const uint4(&in)[4][WORK] = sm.in[i % ST];
-            float* ha = sm.a[i & 1][row];
-            float* hb = sm.b[i & 1][row];
-            const int64_t t = (int64_t)bos + (int64_t)i * TT + row, told = t - 2 * TT;
-            if (told >= bos && told < eos && cok) {
-                float2 h[NP];
+        // its work: tokens 4 q .. of channels c ..
+        const int q = tid / P, pr = tid % P, c = c0 + pr * F::W;
+        const bool cok = c < p.C;
+        int at[4];
 #pragma unroll
-                for (int e = 0; e < F::PIECES; ++e) {
-                    const float4 v = *reinterpret_cast<const float4*>(hb + F::piece(row, ch, e));
-                    h[2 * e] = make_float2(v.x, v.y), h[2 * e + 1] = make_float2(v.z, v.w);
-                }
+        for (int j = 0; j < 4; ++j) at[j] = F::line(4 * q + j) * P + pr;  // in units of a worker's channels
+        for (int i = 0; i < AHEAD; ++i) copy();
+        copy_wait<AHEAD - 1>();
+        step_end<F::NT>();
+        float2 K[NP];
+        const float2 k2 = F::W == 2 ? make_float2(sm.K[2 * pr], sm.K[2 * pr + 1]) : both(sm.K[pr]);
+#pragma unroll
+        for (int e = 0; e < NP; ++e) K[e] = k2;
+        const bool far = any_far(K);
+        T* y = static_cast<T*>(p.y) + (int64_t)(bos + 4 * q) * p.C + c;
+        int rows = cok ? eos - bos - 4 * q : 0, old = 0;  // tokens from this step's on, and from the one's two before
+        for (int i = 0, in = 0; i < tiles + 2; ++i) {
+            copy();
+            const uint4(&from)[4][WORK] = sm.in[in];
+            in = in + 1 == ST ? 0 : in + 1;
+            if (i == 2) old = cok ? eos - bos - 4 * q : 0;
+            if (old > 0) {
+                float2 h[NP];
+                Q::get(&sm.b[i & 1][q][pr], P, h);
                 if (gate) {
                     float2 z[NP];
-                    unpack2(in[3][tid], z);
+                    Q::load(from[3], at, z);
                     branch(p.act, z, h);
                 }
-                st16_stream(static_cast<T*>(p.y) + told * p.C + c, pack2(h));
+                Q::store(y, p.C, old, h);
+                y += (int64_t)TT * p.C, old -= TT;
             }
-            if (t < eos) {
+            if (rows > 0) {
                 float2 x[NP], ag[NP], xg[NP], a[NP], b[NP];
-                unpack2(in[0][tid], x);
-                unpack2(in[1][tid], ag);
-                unpack2(in[2][tid], xg);
-                steps(p, K, ag, xg, x, a, b);
-#pragma unroll
-                for (int e = 0; e < F::PIECES; ++e) {
-                    *reinterpret_cast<float4*>(ha + F::piece(row, ch, e)) = make_float4(a[2 * e].x, a[2 * e].y, a[2 * e + 1].x, a[2 * e + 1].y);
-                    *reinterpret_cast<float4*>(hb + F::piece(row, ch, e)) = make_float4(b[2 * e].x, b[2 * e].y, b[2 * e + 1].x, b[2 * e + 1].y);
-                }
+                Q::load(from[0], at, x);
+                Q::load(from[1], at, ag);
+                Q::load(from[2], at, xg);
+                steps(p, far, K, ag, xg, x, a, b);
+                Q::put(&sm.a[i & 1][q][pr], P, a);
+                Q::put(&sm.b[i & 1][q][pr], P, b);
+                rows -= TT;
             }
+            copy_wait<AHEAD - 1>();
             step_end<F::NT>();
         }
         copy_wait<0>();
         return;
     }
 
-    const int cl = threadIdx.x - WORK, c = c0 + cl;
-    const bool ok = cl < CB && c < p.C;
-    const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
-    const bool has_slot = ok && slot >= 0 && slot < p.num_slots;
+    const int cl = (threadIdx.x - WORK) % CB, c = c0 + cl;
+    const int pos = F::W == 2 ? cl / 2 + (cl & 1) * P : cl;
+    const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);  // (with 16 channels a second half of the lanes does the same)
+    const bool has_slot = c < p.C && slot >= 0 && slot < p.num_slots;
     float* st = p.state + (int64_t)slot * p.C + c;
     float h = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0) ? *st : 0.f;
-    const int at[4] = {F::place(0, cl % CB), F::place(1, cl % CB), F::place(2, cl % CB), F::place(3, cl % CB)};
+    step_end<F::NT>();
     for (int i = 0; i < tiles + 2; ++i) {
         const int len = i >= 1 ? min(TT, eos - bos - (i - 1) * TT) : 0;
-        const float* a = sm.a[(i - 1) & 1][0];
-        float* b = sm.b[(i - 1) & 1][0];
-        constexpr int U = 16;
-        int t = 0;
-        if (len >= U) {  // the next 16 tokens' a and b are under way while 16 are walked
-            float an[U], bn[U];
+        const uint32_t a = smem_u32(&sm.a[(i - 1) & 1][0][pos]), b = smem_u32(&sm.b[(i - 1) & 1][0][pos]);
+        constexpr int U = 4;              // units walked at a time; the next ones' loads go out first
+        constexpr uint32_t step = CB * 16;
+        const int units = len > 0 ? len / 4 : 0;
+        int u = 0;
+        auto walk4 = [&](const float4& av, const float4& bv, uint32_t to) {
+            float4 o;
+            h = o.x = __fmaf_rn(av.x, h, bv.x), h = o.y = __fmaf_rn(av.y, h, bv.y), h = o.z = __fmaf_rn(av.z, h, bv.z), h = o.w = __fmaf_rn(av.w, h, bv.w);
+            st_shared4(to, o);
+        };
+        if (units >= U) {
+            float4 ak[U], bk[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) an[k] = a[k * CB + at[k & 3]], bn[k] = b[k * CB + at[k & 3]];
-            for (; t + U <= len; t += U) {
-                float ak[U], bk[U];
+            for (int k = 0; k < U; ++k) ak[k] = ld_shared4(a + k * step), bk[k] = ld_shared4(b + k * step);
+#pragma unroll 2
+            for (; u + U <= units; u += U) {
+                float4 an[U], bn[U];
+                if (u + 2 * U <= units) {
+#pragma unroll
+                    for (int k = 0; k < U; ++k) an[k] = ld_shared4(a + (u + U + k) * step), bn[k] = ld_shared4(b + (u + U + k) * step);
+                }
+#pragma unroll
+                for (int k = 0; k < U; ++k) walk4(ak[k], bk[k], b + (u + k) * step);
 #pragma unroll
                 for (int k = 0; k < U; ++k) ak[k] = an[k], bk[k] = bn[k];
-                if (t + 2 * U <= len) {
-#pragma unroll
-                    for (int k = 0; k < U; ++k) an[k] = a[(t + U + k) * CB + at[k & 3]], bn[k] = b[(t + U + k) * CB + at[k & 3]];
-                }
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    h = __fmaf_rn(ak[k], h, bk[k]);
-                    b[(t + k) * CB + at[k & 3]] = h;
-                }
             }
         }
-        for (; t < len; ++t) {
-            h = __fmaf_rn(a[t * CB + at[t & 3]], h, b[t * CB + at[t & 3]]);
-            b[t * CB + at[t & 3]] = h;
+        for (; u < units; ++u) walk4(ld_shared4(a + u * step), ld_shared4(b + u * step), b + u * step);
+        if (4 * u < len) {
+            const float4 av = ld_shared4(a + u * step), bv = ld_shared4(b + u * step);
+            const float af[3] = {av.x, av.y, av.z}, bf[3] = {bv.x, bv.y, bv.z};
+            float o[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (4 * u + k < len) h = o[k] = __fmaf_rn(af[k], h, bf[k]);
+            st_shared4(b + u * step, make_float4(o[0], o[1], o[2], 0.f));
         }
         step_end<F::NT>();
     }
-    if (has_slot) *st = h;
+    if (has_slot && threadIdx.x - WORK < CB) *st = h;
 }
 
 // Single tokens: a thread takes a chunk of channels over `rows` batch rows, so that it works out their rates once.
@@ -167,6 +254,7 @@ __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constan
     float2 K[NP];
 #pragma unroll
     for (int e = 0; e < NP; ++e) K[e] = p.ap ? make_float2(rate_of(__ldg(p.ap + c + 2 * e), p.decay), rate_of(__ldg(p.ap + c + 2 * e + 1), p.decay)) : both(0.f);
+    const bool far = any_far(K);
     const int first = blockIdx.x / blocks * rows, last = min(first + rows, p.N);
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
     for (int64_t n = first; n < last; ++n) {
@@ -184,7 +272,7 @@ __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constan
         unpack2(xr, x);
         unpack2(ar, ag);
         unpack2(gr, xg);
-        steps(p, K, ag, xg, x, a, b);
+        steps(p, far, K, ag, xg, x, a, b);
 #pragma unroll
         for (int e = 0; e < NP; ++e) h[e] = __ffma2_rn(a[e], h[e], b[e]);
 #pragma unroll
@@ -225,7 +313,7 @@ __global__ void __launch_bounds__(128) linrec_bwd_kernel(const __grid_constant__
         const float xg = p.xg ? load1(static_cast<const T*>(p.xg) + t * p.ldg + c) : 0.f;
         const float2 K1[1] = {both(K)}, g1[1] = {both(ag)}, i1[1] = {both(xg)}, x1[1] = {both(x)};
         float2 a[1], b[1];
-        steps(p, K1, g1, i1, x1, a, b);
+        steps(p, true, K1, g1, i1, x1, a, b);
         h = __fmaf_rn(a[0].x, h, b[0].x);
         q.hs[t * p.C + c] = h;
     }
@@ -242,7 +330,7 @@ __global__ void __launch_bounds__(128) linrec_bwd_kernel(const __grid_constant__
         if (p.ap) {
             const float2 w1[1] = {__fmul2_rn(both(K), r)};
             float2 a1[1], m1[1];
-            decays(w1, a1, m1);
+            decays(true, w1, a1, m1);
             w = w1[0], a = a1[0], m = m1[0];
         } else {
             a = r, m = r1;

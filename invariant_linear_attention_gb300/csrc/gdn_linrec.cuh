@@ -37,13 +37,14 @@ __device__ __forceinline__ float rate_of(float a_param, float decay) {
     return k > FLT_MAX ? FLT_MAX : k;
 }
 
-// sigmoid(g) and, where asked for, 1 - sigmoid(g) = e^-g sigmoid(g) with its own relative accuracy.
-__device__ __forceinline__ float2 sigmoid2(const float2& g, float2& e) {
-    const float2 v = __fmul2_rn(g, both(-kLog2e));
+// 1 / (1 + 2^v), and 2^v.
+__device__ __forceinline__ float2 logistic2(const float2& v, float2& e) {
     e = make_float2(ex2(v.x), ex2(v.y));
     const float2 d = __fadd2_rn(e, both(1.f));
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
+// sigmoid(g); with rest2 1 - sigmoid(g) = e^-g sigmoid(g) with its own relative accuracy.
+__device__ __forceinline__ float2 sigmoid2(const float2& g, float2& e) { return logistic2(__fmul2_rn(g, both(-kLog2e)), e); }
 __device__ __forceinline__ float2 sigmoid2(const float2& g) {
     float2 e;
     return sigmoid2(g, e);
@@ -55,15 +56,14 @@ __device__ __forceinline__ float2 rest2(const float2& e, const float2& q) {
     return make_float2(e.x > far ? 1.f : m.x, e.y > far ? 1.f : m.y);
 }
 
-// m = 1 - e^-w and a = e^-w for w >= 0.  Below 1/2: m = w + w^2 q(w), q the interpolation of
-// ((1 - e^-w) / w - 1) / w of degree 4 (Chebyshev nodes on [0, 1/2] for the series of degree 5; 3e-9 of m), and a = 1 - m,
-// rounded once.  Above: a by the hardware exponential and m = 1 - a.
-constexpr float kNear = 0.5f;
+// m = 1 - e^-w and a = e^-w for w >= 0.  Below 1/4: m = w + w^2 q(w), q the interpolation of (1 - e^-w - w) / w^2 of
+// degree 3 at Chebyshev's nodes on [0, 1/4] (1.2e-8 of m), and a = 1 - m, rounded once.  Above: a by the
+// hardware exponential and m = 1 - a.  w = K r is at most K: channels with K below 1/4 have no far tokens.
+constexpr float kNear = 0.25f;
 __device__ __forceinline__ float2 near2(const float2& w) {
-    float2 q = __ffma2_rn(both(-0.0011234042467549443f), w, both(0.008189613930881023f));
-    q = __ffma2_rn(q, w, both(-0.04163007438182831f));
-    q = __ffma2_rn(q, w, both(0.16666242480278015f));
-    q = __ffma2_rn(q, w, both(-0.4999998211860657f));
+    float2 q = __ffma2_rn(both(0.00767176877707243f), w, both(-0.041564859449863434f));
+    q = __ffma2_rn(q, w, both(0.1666616052389145f));
+    q = __ffma2_rn(q, w, both(-0.4999999701976776f));
     return __ffma2_rn(__fmul2_rn(w, w), q, w);
 }
 __device__ __forceinline__ void far1(float w, float& a, float& m) {
@@ -71,33 +71,30 @@ __device__ __forceinline__ void far1(float w, float& a, float& m) {
     if (!(w < kNear)) a = e, m = __fadd_rn(1.f, -e);
 }
 template <int NP>
-__device__ __forceinline__ void decays(const float2 (&w)[NP], float2 (&a)[NP], float2 (&m)[NP]) {
-    float most = 0.f;
+__device__ __forceinline__ void decays(bool far, const float2 (&w)[NP], float2 (&a)[NP], float2 (&m)[NP]) {
 #pragma unroll
     for (int e = 0; e < NP; ++e) {
         m[e] = near2(w[e]);
-        a[e] = __fadd2_rn(both(1.f), neg(m[e]));
-        most = fmaxf(most, fmaxf(w[e].x, w[e].y));
+        a[e] = __ffma2_rn(m[e], both(-1.f), both(1.f));
     }
-    if (most >= kNear) {
+    if (!far) return;
 #pragma unroll
-        for (int e = 0; e < NP; ++e) far1(w[e].x, a[e].x, m[e].x), far1(w[e].y, a[e].y, m[e].y);
-    }
+    for (int e = 0; e < NP; ++e) far1(w[e].x, a[e].x, m[e].x), far1(w[e].y, a[e].y, m[e].y);
 }
 
 // 1 - a^2
 __device__ __forceinline__ float2 rest_of_square(const float2& a, const float2& m) { return __ffma2_rn(m, a, m); }
 
-// The argument of the sigmoid in act(z).
-constexpr float kGelu1 = 1.5957691216057308f, kGelu3 = 0.07135481282553144f;  // 2 sqrt(2 / pi), times 0.044715
+// act(z) = z sigmoid(i(z)); inner2 gives -i(z) log2(e), the exponent that the sigmoid takes.
+constexpr float kGelu1 = 1.5957691216057308f, kGelu3 = 0.07135481282553144f;  // i = z (2 sqrt(2 / pi) + 0.044715 times that z^2)
 __device__ __forceinline__ float2 inner2(int act, const float2& z) {
-    return act == GDN_ACT_GELU ? __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), both(kGelu3), both(kGelu1))) : z;
+    if (act != GDN_ACT_GELU) return __fmul2_rn(z, both(-kLog2e));
+    return __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), both(-kLog2e * kGelu3), both(-kLog2e * kGelu1)));
 }
-__device__ __forceinline__ float2 act2(int act, const float2& z) { return __fmul2_rn(z, sigmoid2(inner2(act, z))); }
 // act(z) and its slope p + z p (1 - p) inner'(z).
 __device__ __forceinline__ float2 act2(int act, const float2& z, float2& slope) {
     float2 e;
-    const float2 p = sigmoid2(inner2(act, z), e), r = rest2(e, p), f = __fmul2_rn(z, p);
+    const float2 p = logistic2(inner2(act, z), e), r = rest2(e, p), f = __fmul2_rn(z, p);
     float2 g = __fmul2_rn(f, r);
     if (act == GDN_ACT_GELU) g = __fmul2_rn(g, __ffma2_rn(__fmul2_rn(z, z), both(3.f * kGelu3), both(kGelu1)));
     // r is 0 far enough out; where z^2 is past fp32 its product is not
@@ -125,17 +122,26 @@ __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// a and b of NP pairs of channels of one token.  The call's options are branches around whole loops: one
-// compiled form for all, and the pairs' operations still overlap.
+// Whether a channel of these rates has far tokens.
 template <int NP>
-__device__ __forceinline__ void steps(const Params& p, const float2 (&K)[NP], const float2 (&ag)[NP], const float2 (&xg)[NP],
+__device__ __forceinline__ bool any_far(const float2 (&K)[NP]) {
+    float most = 0.f;
+#pragma unroll
+    for (int e = 0; e < NP; ++e) most = fmaxf(most, fmaxf(K[e].x, K[e].y));
+    return most >= kNear;
+}
+
+// a and b of NP pairs (neighbouring channels, or one channel's tokens).  The call's options are branches around whole
+// loops: one compiled form for all, and the pairs' operations still overlap.
+template <int NP>
+__device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&K)[NP], const float2 (&ag)[NP], const float2 (&xg)[NP],
                                       const float2 (&x)[NP], float2 (&a)[NP], float2 (&b)[NP]) {
     float2 m[NP];
     if (p.ap) {
         float2 w[NP];
 #pragma unroll
         for (int e = 0; e < NP; ++e) w[e] = __fmul2_rn(K[e], sigmoid2(ag[e]));
-        decays(w, a, m);
+        decays(far, w, a, m);
     } else {
 #pragma unroll
         for (int e = 0; e < NP; ++e) {
@@ -164,15 +170,19 @@ __device__ __forceinline__ void steps(const Params& p, const float2 (&K)[NP], co
 // y = h act(z) of NP pairs.
 template <int NP>
 __device__ __forceinline__ void branch(int act, const float2 (&z)[NP], float2 (&h)[NP]) {
-    float2 u[NP];
-#pragma unroll
-    for (int e = 0; e < NP; ++e) u[e] = z[e];
+    float2 v[NP];
     if (act == GDN_ACT_GELU) {
 #pragma unroll
-        for (int e = 0; e < NP; ++e) u[e] = inner2(GDN_ACT_GELU, z[e]);
+        for (int e = 0; e < NP; ++e) v[e] = inner2(GDN_ACT_GELU, z[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) v[e] = inner2(GDN_ACT_SILU, z[e]);
     }
 #pragma unroll
-    for (int e = 0; e < NP; ++e) h[e] = __fmul2_rn(h[e], __fmul2_rn(z[e], sigmoid2(u[e])));
+    for (int e = 0; e < NP; ++e) {
+        float2 u;
+        h[e] = __fmul2_rn(h[e], __fmul2_rn(z[e], logistic2(v[e], u)));
+    }
 }
 
 // The values of a 16-byte chunk as packed pairs, and back.
