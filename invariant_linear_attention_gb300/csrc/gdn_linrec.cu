@@ -9,6 +9,9 @@ namespace {
 
 using namespace linrec;
 
+#ifndef LR_SKIP
+#define LR_SKIP 1
+#endif
 #ifndef LR_WORK
 #define LR_WORK 256
 #endif
@@ -25,10 +28,11 @@ using namespace linrec;
 //   * the walkers, a lane a channel, walk tile i - 1 and leave h in b's place;
 // and one barrier ends the step.  A worker reads the h of the very places that it then writes, so two buffers do.  The
 // inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead.
-template <typename T, int CB>
+template <typename T, int CB, int WORKERS, int TILES, bool APART>
 struct FwdTile {
-    static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = LR_WORK, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
-    static constexpr int AHEAD = LR_AHEAD, ST = AHEAD + 1;
+    static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = WORKERS, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
+    static constexpr int LAUNCH = APART ? 32 * ((WORK / 32 + 2) / 3 * 4) + (WORK / 32 % 3 ? 32 * (WORK / 32 % 3 - 3) : 0) : NT;  // threads, with those that only keep their places
+    static constexpr int AHEAD = TILES, ST = AHEAD + 1;
     static constexpr int W = VN / 4, P = CB / W;  // a worker's channels; workers of a token
     // Four tokens of a channel are 16 bytes, the walker's unit (with 4-byte loads its three a token took 14 cycles, not 4).
     // Even channels come first, then the odd ones: a worker's two are P units apart, and its neighbours' next to them.
@@ -103,9 +107,8 @@ struct Four<float> {
     }
 };
 
-template <typename T, int CB>
-__global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel(const __grid_constant__ Params p) {
-    using F = FwdTile<T, CB>;
+template <typename T, typename F, int CB, int CTAS>
+__global__ void __launch_bounds__(F::LAUNCH, CTAS) linrec_fwd_kernel(const __grid_constant__ Params p) {
     using Q = Four<T>;
     constexpr int VN = F::VN, NP = Q::NP, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST, P = F::P;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -114,11 +117,14 @@ __global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
     const int tiles = (eos - bos + TT - 1) / TT;
-    if (p.ap && threadIdx.x >= WORK && threadIdx.x - WORK < CB)
-        sm.K[threadIdx.x - WORK] = c0 + (int)(threadIdx.x - WORK) < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x - WORK), p.decay) : 0.f;
+    if (p.ap && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
 
-    if (threadIdx.x < WORK) {
-        const int tid = threadIdx.x;
+    if (threadIdx.x >= F::WALK) {
+        int tid = threadIdx.x - F::WALK;
+        if (F::LAUNCH > F::NT) {  // every fourth warp shares the walker's scheduler
+            if (threadIdx.x / 32 % 4 == 0) return;
+            tid = threadIdx.x - 32 * (threadIdx.x / 128 + 1);
+        }
         const bool gate = p.z != nullptr;
         // its copies: a chunk of row tid / CH
         const int row = tid / CH, slot = F::line(row) * CH + tid % CH, cc = c0 + tid % CH * VN;
@@ -194,8 +200,7 @@ __global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel
         return;
     }
 
-    const int cl = (threadIdx.x - WORK) % CB, c = c0 + cl;
-    const int pos = F::W == 2 ? cl / 2 + (cl & 1) * P : cl;
+    const int pos = threadIdx.x % CB, c = c0 + (F::W == 2 ? pos % P * 2 + pos / P : pos);  // neighbouring lanes, neighbouring units
     const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);  // (with 16 channels a second half of the lanes does the same)
     const bool has_slot = c < p.C && slot >= 0 && slot < p.num_slots;
     float* st = p.state + (int64_t)slot * p.C + c;
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel
     for (int i = 0; i < tiles + 2; ++i) {
         const int len = i >= 1 ? min(TT, eos - bos - (i - 1) * TT) : 0;
         const uint32_t a = smem_u32(&sm.a[(i - 1) & 1][0][pos]), b = smem_u32(&sm.b[(i - 1) & 1][0][pos]);
-        constexpr int U = 4;              // units walked at a time; the next ones' loads go out first
+        constexpr int U = 4;  // units walked while the next ones' loads are under way; at the end those read on into what follows, unused
         constexpr uint32_t step = CB * 16;
         const int units = len > 0 ? len / 4 : 0;
         int u = 0;
@@ -213,21 +218,20 @@ __global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel
             h = o.x = __fmaf_rn(av.x, h, bv.x), h = o.y = __fmaf_rn(av.y, h, bv.y), h = o.z = __fmaf_rn(av.z, h, bv.z), h = o.w = __fmaf_rn(av.w, h, bv.w);
             st_shared4(to, o);
         };
-        if (units >= U) {
-            float4 ak[U], bk[U];
+        if (units >= 2 * U) {
+            float4 ak[U], bk[U], an[U], bn[U];
+            auto load = [&](int from, float4(&av)[U], float4(&bv)[U]) {
 #pragma unroll
-            for (int k = 0; k < U; ++k) ak[k] = ld_shared4(a + k * step), bk[k] = ld_shared4(b + k * step);
-#pragma unroll 2
-            for (; u + U <= units; u += U) {
-                float4 an[U], bn[U];
-                if (u + 2 * U <= units) {
-#pragma unroll
-                    for (int k = 0; k < U; ++k) an[k] = ld_shared4(a + (u + U + k) * step), bn[k] = ld_shared4(b + (u + U + k) * step);
-                }
+                for (int k = 0; k < U; ++k) av[k] = ld_shared4(a + (from + k) * step), bv[k] = ld_shared4(b + (from + k) * step);
+            };
+            load(0, ak, bk);
+            for (; u + 2 * U <= units; u += 2 * U) {
+                load(u + U, an, bn);
 #pragma unroll
                 for (int k = 0; k < U; ++k) walk4(ak[k], bk[k], b + (u + k) * step);
+                load(u + 2 * U, ak, bk);
 #pragma unroll
-                for (int k = 0; k < U; ++k) ak[k] = an[k], bk[k] = bn[k];
+                for (int k = 0; k < U; ++k) walk4(an[k], bn[k], b + (u + U + k) * step);
             }
         }
         for (; u < units; ++u) walk4(ld_shared4(a + u * step), ld_shared4(b + u * step), b + u * step);
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(FwdTile<T, CB>::NT, LR_MINB) linrec_fwd_kernel
         }
         step_end<F::NT>();
     }
-    if (has_slot && threadIdx.x - WORK < CB) *st = h;
+    if (has_slot && threadIdx.x < CB) *st = h;
 }
 
 // Single tokens: a thread takes a chunk of channels over `rows` batch rows, so that it works out their rates once.
@@ -378,17 +382,23 @@ __global__ void __launch_bounds__(128) linrec_param_kernel(int N, int C, float d
 #ifndef LR_CB
 #define LR_CB 0
 #endif
-template <typename T, int CB>
+#ifndef LR_WORK2
+#define LR_WORK2 512
+#endif
+#ifndef LR_AHEAD2
+#define LR_AHEAD2 4
+#endif
+template <typename T, int CB, int WORKERS, int TILES, int CTAS, bool APART>
 gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
-    using F = FwdTile<T, CB>;
-    if (cudaFuncSetAttribute(linrec_fwd_kernel<T, CB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
-    linrec_fwd_kernel<T, CB><<<(unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N, F::NT, sizeof(F), s>>>(p);
+    using F = FwdTile<T, CB, WORKERS, TILES, APART>;
+    if (cudaFuncSetAttribute(linrec_fwd_kernel<T, F, CB, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
+    linrec_fwd_kernel<T, F, CB, CTAS><<<(unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N, F::LAUNCH, sizeof(F), s>>>(p);
     return launch_status();
 }
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
-    if (LR_CB == 16 || (LR_CB == 0 && (long long)((p.C + 31) / 32) * p.N <= kSMs / 2)) return launch_fwd_of<T, 16>(s, p);
-    return launch_fwd_of<T, LR_CB ? LR_CB : 32>(s, p);
+    if (LR_CB == 16 || (LR_CB == 0 && (long long)((p.C + 31) / 32) * p.N <= kSMs / 2)) return launch_fwd_of<T, 16, LR_WORK2, LR_AHEAD2, 1, LR_SKIP != 0>(s, p);
+    return launch_fwd_of<T, 32, LR_WORK, LR_AHEAD, LR_MINB, false>(s, p);
 }
 
 gdn_status check_linrec(const gdn_linrec_shape* s, bool param, bool gate, bool z) {
