@@ -1,5 +1,7 @@
 // gdn_linrec.cu -- the gated linear recurrence: prompts (and the trainer's forward), single tokens and
 // the gradient.  The arithmetic is in gdn_linrec.cuh.
+#include <type_traits>
+
 #include "gdn_async.cuh"
 #include "gdn_host.h"
 #include "gdn_linrec.cuh"
@@ -9,9 +11,6 @@ namespace {
 
 using namespace linrec;
 
-#ifndef LR_SKIP
-#define LR_SKIP 1
-#endif
 #ifndef LR_WORK
 #define LR_WORK 256
 #endif
@@ -22,28 +21,29 @@ using namespace linrec;
 #define LR_MINB 2
 #endif
 // Prompts.  A CTA walks one sequence over CB channels in tiles of TT tokens.  Nearly all the work of a token does not
-// depend on the one before it: only h <- a h + b does, 4 cycles a token.  So in step i
-//   * the workers, each four tokens of two channels (fp32: of one), finish tile i - 2 (gate, stores of y) and prepare
+// depend on the one before it: only h <- a h + b does, 5 cycles a token.  So
+//   * the workers, each four tokens of two channels (fp32: of one), in step i finish tile i - NB (gate, stores of y) and prepare
 //     tile i (a and b, to shared memory);
-//   * the walkers, a lane a channel, walk tile i - 1 and leave h in b's place;
-// and one barrier ends the step.  A worker reads the h of the very places that it then writes, so two buffers do.  The
-// inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead.
-template <typename T, int CB, int WORKERS, int TILES, bool APART>
+//   * the walkers, a lane a channel, walk tile after tile and leave h in b's place.
+// A worker reads the h of the very places that it then writes, so it meets nobody but the walkers, NB tiles behind or ahead:
+// at named barriers full (a tile prepared) and done (it is walked), one of each per buffer, which every side passes once a
+// tile.  The inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead, for a group of workers that copies what it reads.
+template <typename T, int CB, int WORKERS, int TILES>
 struct FwdTile {
     static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = WORKERS, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
-    static constexpr int LAUNCH = APART ? 32 * ((WORK / 32 + 2) / 3 * 4) + (WORK / 32 % 3 ? 32 * (WORK / 32 % 3 - 3) : 0) : NT;  // threads, with those that only keep their places
-    static constexpr int AHEAD = TILES, ST = AHEAD + 1;
-    static constexpr int W = VN / 4, P = CB / W;  // a worker's channels; workers of a token
-    // Four tokens of a channel are 16 bytes, the walker's unit (with 4-byte loads its three a token took 14 cycles, not 4).
-    // Even channels come first, then the odd ones: a worker's two are P units apart, and its neighbours' next to them.
-    float4 a[2][TT / 4][CB], b[2][TT / 4][CB];
-    // x, a_gate, x_gate of a tile, z of the one two before.  Rows shorter than 128 bytes share them; their order there goes
-    // by the row's group of four too, so that a warp's workers, of several groups, meet no bank twice.
-    uint4 in[ST][4][WORK];
+    static constexpr int AHEAD = TILES, ST = AHEAD + 1, NB = 3;
+    static constexpr int GROUP = VN == 8 && CB == 32 ? 64 : 32;     // threads that copy for one another
+    static constexpr int kFull = 1, kDone = kFull + NB, kGroup = kDone + NB;  // barriers
+    // Four tokens of a channel are 16 bytes, the walker's unit (with 4-byte loads its three a token took 14 cycles, not 5).
+    // Unit q of channel c lies at unit(q, c) of its row: eight neighbouring lanes of a worker warp, two channels of four
+    // rows, then meet no bank twice.
+    float4 a[NB][TT / 4][CB], b[NB][TT / 4][CB];
+    static __device__ __forceinline__ int unit(int q, int c) { return c ^ 2 * (q & 3); }
+    uint4 in[ST][4][WORK];                                // x, a_gate, x_gate of a tile, z of the one NB before
+    uint4 out[std::is_same<T, float>::value ? 1 : WORK];  // bf16: a warp's y on its way from columns to rows
     float K[CB];
-    static constexpr int RS = 8 / CH;  // rows of 128 bytes
-    static __device__ __forceinline__ int line(int t) { return (t & ~(RS - 1)) | ((t ^ (t >> 2)) & (RS - 1)); }
-    static_assert(CH <= 8 && TT % 16 == 0, "rows of at most 128 bytes, tiles of whole walks");
+    static_assert(CB <= 32 && TT % 16 == 0, "rows of at most 128 bytes, tiles of whole walks");
+    static_assert(kGroup + (GROUP > 32 ? WORK / GROUP : 0) <= 16, "barriers of a CTA");
 };
 
 // Shared memory in the order written: the compiler moves neither across the other.
@@ -55,85 +55,116 @@ __device__ __forceinline__ float4 ld_shared4(uint32_t at) {
 __device__ __forceinline__ void st_shared4(uint32_t at, const float4& v) {
     asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
-// All threads of the CTA meet, from whichever place in the code.
-template <int THREADS>
-__device__ __forceinline__ void step_end() {
-    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
-}
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+__device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
-// Four tokens of a worker's channels: values [token] of two channels (bf16), [pair of tokens] of one (fp32).
-template <typename T>
-struct Four;
-template <>
-struct Four<__nv_bfloat16> {
-    static constexpr int NP = 4;
-    static __device__ __forceinline__ void load(const uint4* in, const int (&at)[4], float2 (&v)[4]) {
+// A worker's share of a tile: tokens 4 q .. 4 q + 3 of its channels.  v: packed pairs of tokens, those of one channel and then,
+// in bf16, those of the other.
+template <typename T, int CB>
+struct Share;
+
+// bf16: a warp takes 16 tokens of 16 channels, lane l channels l / 4 and l / 4 + 8 and tokens 4 (l % 4) ..  Four 8 x 8 matrices, two
+// of tokens 0, 1, 4, 5, .. and two of tokens 2, 3, 6, 7, .., each transposed on the way from and to the rows in memory,
+// put two tokens of a channel into one register: 1 instruction an input where loads of a row's pairs took 4.
+template <int CB>
+struct Share<__nv_bfloat16, CB> {
+    static constexpr int NP = 4, CH = CB / 8;
+    int c, q, at, row_at, row, row_c;  // c, row_c: within the CTA's channels; at: byte offset of this lane's matrix row in an input
+    // The 16-byte place of chunk ch of row t: a matrix's eight rows (above) lie in eight different places of a 128-byte line.
+    static __device__ __forceinline__ int place(int t, int ch, int chunks) {
+        const int g = (t >> 2) & 3;
+        return chunks == 4 ? t * 4 + (ch ^ g) : ((t * 2 + ch) & ~7) | (((t * 2 + ch) & 7) ^ ((g & 1) | (g & 2) << 1));
+    }
+    __device__ __forceinline__ Share(int tid) {
+        const int l = tid % 32, w = tid / 32, cw = w % (CB / 16), tb = w / (CB / 16) * 16;
+        const int r = l % 8, t = (r >> 1) * 4 + (r & 1) + (l & 8 ? 2 : 0);
+        c = cw * 16 + l / 4, q = tb / 4 + l % 4;
+        at = 16 * place(tb + t, cw * 2 + l / 16, CH), row_at = 16 * place(t, l / 16, 2);
+        row = tb + l / 2, row_c = cw * 16 + l % 2 * 8;
+    }
+    __device__ __forceinline__ int first() const { return q & ~3; }  // its warp's first unit
+    __device__ __forceinline__ void rates(const float* K, float2 (&k)[4]) const { k[0] = k[1] = both(K[c]), k[2] = k[3] = both(K[c + 8]); }
+    __device__ __forceinline__ void load(const uint4* in, float2 (&v)[4]) const {
+        uint32_t u[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                     : "r"(smem_u32(in) + at)
+                     : "memory");
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t u = reinterpret_cast<const uint32_t*>(in)[at[j]];
-            v[j] = make_float2(bf_lo(u), bf_hi(u));
-        }
+        for (int j = 0; j < 4; ++j) v[j] = make_float2(bf_lo(u[j]), bf_hi(u[j]));
     }
-    static __device__ __forceinline__ void put(float4* to, int P, const float2 (&v)[4]) {
-        to[0] = make_float4(v[0].x, v[1].x, v[2].x, v[3].x), to[P] = make_float4(v[0].y, v[1].y, v[2].y, v[3].y);
+    template <typename F>
+    __device__ __forceinline__ void put(float4 (&to)[F::TT / 4][CB], const float2 (&v)[4]) const {
+        to[q][F::unit(q, c)] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y), to[q][F::unit(q, c + 8)] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     }
-    static __device__ __forceinline__ void get(const float4* from, int P, float2 (&v)[4]) {
-        const float4 x = from[0], y = from[P];
-        v[0] = make_float2(x.x, y.x), v[1] = make_float2(x.y, y.y), v[2] = make_float2(x.z, y.z), v[3] = make_float2(x.w, y.w);
+    template <typename F>
+    __device__ __forceinline__ void get(const float4 (&from)[F::TT / 4][CB], float2 (&v)[4]) const {
+        const float4 x = from[q][F::unit(q, c)], y = from[q][F::unit(q, c + 8)];
+        v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w), v[2] = make_float2(y.x, y.y), v[3] = make_float2(y.z, y.w);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* y, int64_t ld, int rows, const float2 (&v)[4]) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < rows) *reinterpret_cast<uint32_t*>(y + j * ld) = bf_pack(v[j].x, v[j].y);
+    // out: its warp's 512 bytes; y: row `row` of the tile; has: whether this lane's row and channels exist.
+    __device__ __forceinline__ void store(uint4* out, __nv_bfloat16* y, bool has, const float2 (&v)[4]) const {
+        const uint32_t u[4] = {bf_pack(v[0].x, v[0].y), bf_pack(v[1].x, v[1].y), bf_pack(v[2].x, v[2].y), bf_pack(v[3].x, v[3].y)};
+        __syncwarp();
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(out) + row_at), "r"(u[0]), "r"(u[1]),
+                     "r"(u[2]), "r"(u[3])
+                     : "memory");
+        __syncwarp();
+        const int l = threadIdx.x % 32;
+        const uint4 o = out[place(l / 2, l % 2, 2)];
+        if (has) st16_stream(y, o);
     }
 };
-template <>
-struct Four<float> {
-    static constexpr int NP = 2;
-    static __device__ __forceinline__ void load(const uint4* in, const int (&at)[4], float2 (&v)[2]) {
+// fp32: a lane one channel; a warp's lanes are neighbouring channels.
+template <int CB>
+struct Share<float, CB> {
+    static constexpr int NP = 2, CH = CB / 4;
+    int c, q, row, row_c;
+    // Rows of 64 bytes share a line, in an order that goes by the row's unit too: a warp reads one row of each of two units.
+    static __device__ __forceinline__ int place(int t, int ch, int chunks) { return (chunks == 8 ? t : (t & ~1) | ((t ^ (t >> 2)) & 1)) * chunks + ch; }
+    __device__ __forceinline__ Share(int tid) { c = row_c = tid % CB, q = tid / CB, row = 4 * q; }
+    __device__ __forceinline__ int first() const { return q; }
+    __device__ __forceinline__ void rates(const float* K, float2 (&k)[2]) const { k[0] = k[1] = both(K[c]); }
+    __device__ __forceinline__ void load(const uint4* in, float2 (&v)[2]) const {
         const float* f = reinterpret_cast<const float*>(in);
-        v[0] = make_float2(f[at[0]], f[at[1]]), v[1] = make_float2(f[at[2]], f[at[3]]);
+        auto at = [&](int j) { return f[4 * place(4 * q + j, c / 4, CH) + c % 4]; };
+        v[0] = make_float2(at(0), at(1)), v[1] = make_float2(at(2), at(3));
     }
-    static __device__ __forceinline__ void put(float4* to, int, const float2 (&v)[2]) { to[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y); }
-    static __device__ __forceinline__ void get(const float4* from, int, float2 (&v)[2]) {
-        const float4 x = from[0];
+    template <typename F>
+    __device__ __forceinline__ void put(float4 (&to)[F::TT / 4][CB], const float2 (&v)[2]) const {
+        to[q][F::unit(q, c)] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+    template <typename F>
+    __device__ __forceinline__ void get(const float4 (&from)[F::TT / 4][CB], float2 (&v)[2]) const {
+        const float4 x = from[q][F::unit(q, c)];
         v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
-    }
-    static __device__ __forceinline__ void store(float* y, int64_t ld, int rows, const float2 (&v)[2]) {
-        const float f[4] = {v[0].x, v[0].y, v[1].x, v[1].y};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j < rows) y[j * ld] = f[j];
     }
 };
 
 template <typename T, typename F, int CB, int CTAS>
-__global__ void __launch_bounds__(F::LAUNCH, CTAS) linrec_fwd_kernel(const __grid_constant__ Params p) {
-    using Q = Four<T>;
-    constexpr int VN = F::VN, NP = Q::NP, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST, P = F::P;
-    extern __shared__ __align__(16) unsigned char raw[];
+__global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_constant__ Params p) {
+    using Q = Share<T, CB>;
+    constexpr int VN = F::VN, NP = Q::NP, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST;
+    extern __shared__ __align__(128) unsigned char raw[];
     F& sm = *reinterpret_cast<F*>(raw);
     const int blocks = (p.C + CB - 1) / CB, n = blockIdx.x / blocks, c0 = blockIdx.x % blocks * CB;
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
-    const int tiles = (eos - bos + TT - 1) / TT;
+    const int len = eos - bos, tiles = (len + TT - 1) / TT;
     if (p.ap && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
+    __syncthreads();
 
     if (threadIdx.x >= F::WALK) {
-        int tid = threadIdx.x - F::WALK;
-        if (F::LAUNCH > F::NT) {  // every fourth warp shares the walker's scheduler
-            if (threadIdx.x / 32 % 4 == 0) return;
-            tid = threadIdx.x - 32 * (threadIdx.x / 128 + 1);
-        }
+        const int tid = threadIdx.x - F::WALK;
         const bool gate = p.z != nullptr;
         // its copies: a chunk of row tid / CH
-        const int row = tid / CH, slot = F::line(row) * CH + tid % CH, cc = c0 + tid % CH * VN;
-        int left = cc < p.C ? eos - bos - row : 0;  // rows from the next copy's on; below 1: none to copy
+        const int row = tid / CH, slot = Q::place(row, tid % CH, CH), cc = c0 + tid % CH * VN;
+        int left = cc < p.C ? len - row : 0;  // rows from the next copy's on; below 1: none to copy
         const T* px = static_cast<const T*>(p.x) + (int64_t)(bos + row) * p.ldx + cc;
         const T* pa = static_cast<const T*>(p.ag) + (int64_t)(bos + row) * p.lda + cc;
         const T* pg = p.xg ? static_cast<const T*>(p.xg) + (int64_t)(bos + row) * p.ldg + cc : nullptr;
         const T* pz = gate ? static_cast<const T*>(p.z) + (int64_t)(bos + row) * p.ldz + cc : nullptr;
-        int stage = 0, zleft = left, behind = 2;
+        int stage = 0, zleft = left, behind = F::NB;
         auto copy = [&] {  // what the next step that has no copies yet needs
             uint4(&to)[4][WORK] = sm.in[stage];
             stage = stage + 1 == ST ? 0 : stage + 1;
@@ -151,67 +182,74 @@ __global__ void __launch_bounds__(F::LAUNCH, CTAS) linrec_fwd_kernel(const __gri
             }
             copy_commit();
         };
-        // its work: tokens 4 q .. of channels c ..
-        const int q = tid / P, pr = tid % P, c = c0 + pr * F::W;
-        const bool cok = c < p.C;
-        int at[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) at[j] = F::line(4 * q + j) * P + pr;  // in units of a worker's channels
+        const Q my(tid);
         for (int i = 0; i < AHEAD; ++i) copy();
-        copy_wait<AHEAD - 1>();
-        step_end<F::NT>();
         float2 K[NP];
-        const float2 k2 = F::W == 2 ? make_float2(sm.K[2 * pr], sm.K[2 * pr + 1]) : both(sm.K[pr]);
-#pragma unroll
-        for (int e = 0; e < NP; ++e) K[e] = k2;
+        my.rates(sm.K, K);
         const bool far = any_far(K);
-        T* y = static_cast<T*>(p.y) + (int64_t)(bos + 4 * q) * p.C + c;
-        int rows = cok ? eos - bos - 4 * q : 0, old = 0;  // tokens from this step's on, and from the one's two before
-        for (int i = 0, in = 0; i < tiles + 2; ++i) {
+        const bool cok = c0 + my.row_c < p.C;
+        T* y = static_cast<T*>(p.y) + (int64_t)(bos + my.row) * p.C + c0 + my.row_c;
+        int rows = len - 4 * my.first(), old = 0;  // tokens from its warp's first on, of this step's tile and of the one to finish
+        for (int i = 0, in = 0, buf = 0; i < tiles + F::NB; ++i) {
+            copy_wait<AHEAD - 1>();
+            if (F::GROUP > 32) bar_sync(F::kGroup + tid / F::GROUP, F::GROUP);
+            else __syncwarp();
             copy();
             const uint4(&from)[4][WORK] = sm.in[in];
             in = in + 1 == ST ? 0 : in + 1;
-            if (i == 2) old = cok ? eos - bos - 4 * q : 0;
+            if (i >= F::NB) bar_sync(F::kDone + buf, F::NT);
+            if (i == F::NB) old = len - 4 * my.first();
             if (old > 0) {
                 float2 h[NP];
-                Q::get(&sm.b[i & 1][q][pr], P, h);
+                my.template get<F>(sm.b[buf], h);
                 if (gate) {
                     float2 z[NP];
-                    Q::load(from[3], at, z);
+                    my.load(from[3], z);
                     branch(p.act, z, h);
                 }
-                Q::store(y, p.C, old, h);
+                const int here = old - (my.row - 4 * my.first());  // tokens from this lane's row on
+                if constexpr (std::is_same<T, float>::value) {
+                    const float f[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (cok && j < here) y[(int64_t)j * p.C] = f[j];
+                } else {
+                    my.store(sm.out + tid / 32 * 32, y, cok && here > 0, h);
+                }
                 y += (int64_t)TT * p.C, old -= TT;
             }
             if (rows > 0) {
                 float2 x[NP], ag[NP], xg[NP], a[NP], b[NP];
-                Q::load(from[0], at, x);
-                Q::load(from[1], at, ag);
-                Q::load(from[2], at, xg);
+                my.load(from[0], x);
+                my.load(from[1], ag);
+                my.load(from[2], xg);
                 steps(p, far, K, ag, xg, x, a, b);
-                Q::put(&sm.a[i & 1][q][pr], P, a);
-                Q::put(&sm.b[i & 1][q][pr], P, b);
+                my.template put<F>(sm.a[buf], a);
+                my.template put<F>(sm.b[buf], b);
                 rows -= TT;
             }
-            copy_wait<AHEAD - 1>();
-            step_end<F::NT>();
+            if (i < tiles) bar_arrive(F::kFull + buf, F::NT);
+            buf = buf + 1 == F::NB ? 0 : buf + 1;
         }
         copy_wait<0>();
         return;
     }
 
-    const int pos = threadIdx.x % CB, c = c0 + (F::W == 2 ? pos % P * 2 + pos / P : pos);  // neighbouring lanes, neighbouring units
+    const int cl = threadIdx.x % CB, c = c0 + cl;
     const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);  // (with 16 channels a second half of the lanes does the same)
     const bool has_slot = c < p.C && slot >= 0 && slot < p.num_slots;
     float* st = p.state + (int64_t)slot * p.C + c;
     float h = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0) ? *st : 0.f;
-    step_end<F::NT>();
-    for (int i = 0; i < tiles + 2; ++i) {
-        const int len = i >= 1 ? min(TT, eos - bos - (i - 1) * TT) : 0;
-        const uint32_t a = smem_u32(&sm.a[(i - 1) & 1][0][pos]), b = smem_u32(&sm.b[(i - 1) & 1][0][pos]);
+    uint32_t at[4];  // of units 0 to 3, in a row of a buffer
+#pragma unroll
+    for (int k = 0; k < 4; ++k) at[k] = 16u * (uint32_t)(k * CB + F::unit(k, cl));
+    for (int i = 0, buf = 0; i < tiles; ++i) {
+        const int here = min(TT, len - i * TT);
+        const uint32_t a = smem_u32(sm.a[buf]), b = smem_u32(sm.b[buf]);
+        bar_sync(F::kFull + buf, F::NT);
         constexpr int U = 4;  // units walked while the next ones' loads are under way; at the end those read on into what follows, unused
         constexpr uint32_t step = CB * 16;
-        const int units = len > 0 ? len / 4 : 0;
+        const int units = here / 4;
         int u = 0;
         auto walk4 = [&](const float4& av, const float4& bv, uint32_t to) {
             float4 o;
@@ -222,29 +260,34 @@ __global__ void __launch_bounds__(F::LAUNCH, CTAS) linrec_fwd_kernel(const __gri
             float4 ak[U], bk[U], an[U], bn[U];
             auto load = [&](int from, float4(&av)[U], float4(&bv)[U]) {
 #pragma unroll
-                for (int k = 0; k < U; ++k) av[k] = ld_shared4(a + (from + k) * step), bv[k] = ld_shared4(b + (from + k) * step);
+                for (int k = 0; k < U; ++k) av[k] = ld_shared4(a + from * step + at[k]), bv[k] = ld_shared4(b + from * step + at[k]);
             };
             load(0, ak, bk);
             for (; u + 2 * U <= units; u += 2 * U) {
                 load(u + U, an, bn);
 #pragma unroll
-                for (int k = 0; k < U; ++k) walk4(ak[k], bk[k], b + (u + k) * step);
+                for (int k = 0; k < U; ++k) walk4(ak[k], bk[k], b + u * step + at[k]);
                 load(u + 2 * U, ak, bk);
 #pragma unroll
-                for (int k = 0; k < U; ++k) walk4(an[k], bn[k], b + (u + U + k) * step);
+                for (int k = 0; k < U; ++k) walk4(an[k], bn[k], b + (u + U) * step + at[k]);
             }
         }
-        for (; u < units; ++u) walk4(ld_shared4(a + u * step), ld_shared4(b + u * step), b + u * step);
-        if (4 * u < len) {
-            const float4 av = ld_shared4(a + u * step), bv = ld_shared4(b + u * step);
-            const float af[3] = {av.x, av.y, av.z}, bf[3] = {bv.x, bv.y, bv.z};
-            float o[3] = {0.f, 0.f, 0.f};
+        for (; 4 * u < here; ++u) {
+            const uint32_t to = 16u * (uint32_t)(u * CB + F::unit(u, cl));
+            const float4 av = ld_shared4(a + to), bv = ld_shared4(b + to);
+            if (u < units) {
+                walk4(av, bv, b + to);
+            } else {
+                const float af[3] = {av.x, av.y, av.z}, bf[3] = {bv.x, bv.y, bv.z};
+                float o[3] = {0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (4 * u + k < len) h = o[k] = __fmaf_rn(af[k], h, bf[k]);
-            st_shared4(b + u * step, make_float4(o[0], o[1], o[2], 0.f));
+                for (int k = 0; k < 3; ++k)
+                    if (4 * u + k < here) h = o[k] = __fmaf_rn(af[k], h, bf[k]);
+                st_shared4(b + to, make_float4(o[0], o[1], o[2], 0.f));
+            }
         }
-        step_end<F::NT>();
+        bar_arrive(F::kDone + buf, F::NT);
+        buf = buf + 1 == F::NB ? 0 : buf + 1;
     }
     if (has_slot && threadIdx.x < CB) *st = h;
 }
@@ -386,19 +429,19 @@ __global__ void __launch_bounds__(128) linrec_param_kernel(int N, int C, float d
 #define LR_WORK2 512
 #endif
 #ifndef LR_AHEAD2
-#define LR_AHEAD2 4
+#define LR_AHEAD2 2
 #endif
-template <typename T, int CB, int WORKERS, int TILES, int CTAS, bool APART>
+template <typename T, int CB, int WORKERS, int TILES, int CTAS>
 gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
-    using F = FwdTile<T, CB, WORKERS, TILES, APART>;
+    using F = FwdTile<T, CB, WORKERS, TILES>;
     if (cudaFuncSetAttribute(linrec_fwd_kernel<T, F, CB, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
-    linrec_fwd_kernel<T, F, CB, CTAS><<<(unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N, F::LAUNCH, sizeof(F), s>>>(p);
+    linrec_fwd_kernel<T, F, CB, CTAS><<<(unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N, F::NT, sizeof(F), s>>>(p);
     return launch_status();
 }
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
-    if (LR_CB == 16 || (LR_CB == 0 && (long long)((p.C + 31) / 32) * p.N <= kSMs / 2)) return launch_fwd_of<T, 16, LR_WORK2, LR_AHEAD2, 1, LR_SKIP != 0>(s, p);
-    return launch_fwd_of<T, 32, LR_WORK, LR_AHEAD, LR_MINB, false>(s, p);
+    if (LR_CB == 16 || (LR_CB == 0 && (long long)((p.C + 31) / 32) * p.N <= kSMs / 2)) return launch_fwd_of<T, 16, LR_WORK2, LR_AHEAD2, 1>(s, p);
+    return launch_fwd_of<T, 32, LR_WORK, LR_AHEAD, LR_MINB>(s, p);
 }
 
 gdn_status check_linrec(const gdn_linrec_shape* s, bool param, bool gate, bool z) {

@@ -56,6 +56,35 @@ __device__ __forceinline__ float2 rest2(const float2& e, const float2& q) {
     return make_float2(e.x > far ? 1.f : m.x, e.y > far ? 1.f : m.y);
 }
 
+// sigmoid(g) and sigmoid(i) with one reciprocal for both, 1 / ((1 + 2^v) (1 + 2^u)): the special function unit, which
+// takes two cycles a warp for a reciprocal or a root and one for an exponential, bounds the prompts' kernel next to HBM.
+// e: 2^v.  Where a power is past 2^60 and their product might leave fp32's range, each has its own.
+template <int NP>
+__device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2 (&i)[NP], float2 (&r)[NP], float2 (&p)[NP], float2 (&e)[NP]) {
+    float2 f[NP];
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const float2 v = __fmul2_rn(g[k], both(-kLog2e)), u = __fmul2_rn(i[k], both(-kLog2e));
+        most = fmaxf(fmaxf(most, fmaxf(v.x, v.y)), fmaxf(u.x, u.y));
+        e[k] = make_float2(ex2(v.x), ex2(v.y)), f[k] = make_float2(ex2(u.x), ex2(u.y));
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const float2 d = __fadd2_rn(e[k], both(1.f)), c = __fadd2_rn(f[k], both(1.f)), D = __fmul2_rn(d, c);
+        const float2 R = make_float2(rcp_approx(D.x), rcp_approx(D.y));
+        r[k] = __fmul2_rn(R, c), p[k] = __fmul2_rn(R, d);
+    }
+    if (most > 60.f) {
+        constexpr float far = 1.152921504606847e18f;  // 2^60
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            if (fmaxf(e[k].x, f[k].x) > far) r[k].x = rcp_approx(1.f + e[k].x), p[k].x = rcp_approx(1.f + f[k].x);
+            if (fmaxf(e[k].y, f[k].y) > far) r[k].y = rcp_approx(1.f + e[k].y), p[k].y = rcp_approx(1.f + f[k].y);
+        }
+    }
+}
+
 // m = 1 - e^-w and a = e^-w for w >= 0.  Below 1/4: m = w + w^2 q(w), q the interpolation of (1 - e^-w - w) / w^2 of
 // degree 3 at Chebyshev's nodes on [0, 1/4] (1.2e-8 of m), and a = 1 - m, rounded once.  Above: a by the
 // hardware exponential and m = 1 - a.  w = K r is at most K: channels with K below 1/4 have no far tokens.
@@ -136,25 +165,23 @@ __device__ __forceinline__ bool any_far(const float2 (&K)[NP]) {
 template <int NP>
 __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&K)[NP], const float2 (&ag)[NP], const float2 (&xg)[NP],
                                       const float2 (&x)[NP], float2 (&a)[NP], float2 (&b)[NP]) {
-    float2 m[NP];
+    float2 m[NP], r[NP], u[NP];
+    if (p.xg) {
+        two_sigmoids(ag, xg, r, b, u);
+#pragma unroll
+        for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(x[e], b[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < NP; ++e) r[e] = sigmoid2(ag[e], u[e]), b[e] = x[e];
+    }
     if (p.ap) {
         float2 w[NP];
 #pragma unroll
-        for (int e = 0; e < NP; ++e) w[e] = __fmul2_rn(K[e], sigmoid2(ag[e]));
+        for (int e = 0; e < NP; ++e) w[e] = __fmul2_rn(K[e], r[e]);
         decays(far, w, a, m);
     } else {
 #pragma unroll
-        for (int e = 0; e < NP; ++e) {
-            float2 u;
-            a[e] = sigmoid2(ag[e], u), m[e] = rest2(u, a[e]);
-        }
-    }
-    if (p.xg) {
-#pragma unroll
-        for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(x[e], sigmoid2(xg[e]));
-    } else {
-#pragma unroll
-        for (int e = 0; e < NP; ++e) b[e] = x[e];
+        for (int e = 0; e < NP; ++e) a[e] = r[e], m[e] = rest2(u[e], r[e]);
     }
     if (p.scale == GDN_SCALE_SQRT) {
 #pragma unroll

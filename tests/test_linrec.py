@@ -4,15 +4,15 @@
 Tolerances, in units of u = 2^-24 of the sum of the terms' magnitudes (the oracle with
 magnitude=True).  With g the largest |gate|: sigmoid(g) = 1 / (1 + 2^(-g log2 e)) carries the
 exponent's two roundings (2 g u), the hardware exponential (2^-22.5: 3 u), a sum (u) and the
-hardware reciprocal (2 u): (2 g + 6) u; 1 - sigmoid one more.  K = decay softplus(a_param) is good
-to 8 u, so w = K r to E_w = (2 g + 15) u, and m = 1 - e^-w to E_w + 5 u.  log a is off by w E_w + 5 u a
+hardware reciprocal (2 u), or two gates' common one with two products more: (2 g + 9) u; 1 - sigmoid one more.
+K = decay softplus(a_param) is good to 8 u, so w = K r to E_w = (2 g + 18) u, and m = 1 - e^-w to E_w + 5 u.  log a is off by w E_w + 5 u a
 token (its rounding, up to 1.65 u, and m's own 4 u m / a; above w = 1/2 the hardware
-exponential, 3 u + 2 w u); over a sequence's L tokens by (2 g + 17) u min(40, s) + 5 u L, s = sum of w
+exponential, 3 u + 2 w u); over a sequence's L tokens by (2 g + 20) u min(40, s) + 5 u L, s = sum of w
 (past s = 40 a term is below e^-40 of itself).  Without an a_param a = sigmoid(g): its error,
-e / (1 + e) (2 |g| + 3) u + 3 u, is at most (2 w + 7) u, since |g| <= w for g < 0 and e |g| / (1 + e) < 0.28
-for g > 0.  s_t = sqrt(m + m a) is good to (2 g + 25) u, x sigmoid(x_gate) to (2 g + 7) u; with L
+e / (1 + e) (2 |g| + 3) u + 6 u, is at most (2 w + 10) u, since |g| <= w for g < 0 and e |g| / (1 + e) < 0.28
+for g > 0.  s_t = sqrt(m + m a) is good to (2 g + 28) u, x sigmoid(x_gate) to (2 g + 10) u; with L
 roundings of the walk:
-    E = 40 + 4 g + 8 L + (2 g + 17) min(40, s).
+    E = 40 + 4 g + 11 L + (2 g + 20) min(40, s).
 act(z) adds (8 + 6 max |inner(z)|) u of the result (inner: its sigmoid's argument, 4 roundings).
 A gradient multiplies two such recurrences and the factors of a third, 3 E and three times act's share;
 da_param's sum adds T, its factor 12 u.  dz's slope p + z p (1 - p) inner'(z) is a sum that cancels: the oracle's
@@ -83,7 +83,7 @@ class Case:
             G = ref.linear_recurrence_bwd(cu=self.cu_list, d_out=self.dy, d_final_state=self.gT, magnitude=True, **dict(self.args(), x_gate=None, input_scale="one"))["dx"]
             f = 1 if self.z is None else 1 + np.abs(to_np(self.z)).max()
             floor = 2.0 ** -62 * max(self.lens) * (1 + np.nanmax(G)) * (1 + np.nanmax(np.abs(to_np(self.x)))) * f
-        return 40 + 4 * g + 8 * max(self.lens) + (2 * g + 17) * min(40.0, s), share, floor
+        return 40 + 4 * g + 11 * max(self.lens) + (2 * g + 20) * min(40.0, s), share, floor
 
 
 def check(got, want, mag, units, dtype, floor=1e-30):
