@@ -94,24 +94,31 @@ struct Share<__nv_bfloat16, CB> {
         for (int j = 0; j < 4; ++j) v[j] = make_float2(bf_lo(u[j]), bf_hi(u[j]));
     }
     template <typename F>
-    __device__ __forceinline__ void put(float4 (&to)[F::TT / 4][CB], const float2 (&v)[4]) const {
+    __device__ __forceinline__ void put(float4 (*to)[CB], const float2 (&v)[4]) const {
         to[q][F::unit(q, c)] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y), to[q][F::unit(q, c + 8)] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     }
     template <typename F>
-    __device__ __forceinline__ void get(const float4 (&from)[F::TT / 4][CB], float2 (&v)[4]) const {
+    __device__ __forceinline__ void get(const float4 (*from)[CB], float2 (&v)[4]) const {
         const float4 x = from[q][F::unit(q, c)], y = from[q][F::unit(q, c + 8)];
         v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w), v[2] = make_float2(y.x, y.y), v[3] = make_float2(y.z, y.w);
     }
-    // out: its warp's 512 bytes; y: row `row` of the tile; has: whether this lane's row and channels exist.
-    __device__ __forceinline__ void store(uint4* out, __nv_bfloat16* y, bool has, const float2 (&v)[4]) const {
+    static __device__ __forceinline__ void transposed(uint32_t to, const float2 (&v)[4]) {
         const uint32_t u[4] = {bf_pack(v[0].x, v[0].y), bf_pack(v[1].x, v[1].y), bf_pack(v[2].x, v[2].y), bf_pack(v[3].x, v[3].y)};
         __syncwarp();
-        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(out) + row_at), "r"(u[0]), "r"(u[1]),
-                     "r"(u[2]), "r"(u[3])
-                     : "memory");
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
         __syncwarp();
+    }
+    // out: its warp's 512 bytes; y: row `row` of the tile; has: whether this lane's row and channels exist.
+    __device__ __forceinline__ void store(uint4* out, __nv_bfloat16* y, bool has, const float2 (&v)[4]) const {
+        transposed(smem_u32(out) + row_at, v);
         const int l = threadIdx.x % 32;
         const uint4 o = out[place(l / 2, l % 2, 2)];
+        if (has) st16_stream(y, o);
+    }
+    // The same through the places that its warp read an input from.
+    __device__ __forceinline__ void store_in(uint4* in, __nv_bfloat16* y, bool has, const float2 (&v)[4]) const {
+        transposed(smem_u32(in) + at, v);
+        const uint4 o = in[place(row, row_c / 8, CH)];
         if (has) st16_stream(y, o);
     }
 };
@@ -131,11 +138,11 @@ struct Share<float, CB> {
         v[0] = make_float2(at(0), at(1)), v[1] = make_float2(at(2), at(3));
     }
     template <typename F>
-    __device__ __forceinline__ void put(float4 (&to)[F::TT / 4][CB], const float2 (&v)[2]) const {
+    __device__ __forceinline__ void put(float4 (*to)[CB], const float2 (&v)[2]) const {
         to[q][F::unit(q, c)] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     }
     template <typename F>
-    __device__ __forceinline__ void get(const float4 (&from)[F::TT / 4][CB], float2 (&v)[2]) const {
+    __device__ __forceinline__ void get(const float4 (*from)[CB], float2 (&v)[2]) const {
         const float4 x = from[q][F::unit(q, c)];
         v[0] = make_float2(x.x, x.y), v[1] = make_float2(x.z, x.w);
     }
@@ -333,91 +340,391 @@ __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constan
     }
 }
 
-// Gradient: a thread one channel of one sequence, forward with every state to the workspace, then back.
-//     e = dy act(z),  G_t = e_t + a_{t+1} G_{t+1},  dx = G s p,  dx_gate = G s x p (1 - p),  dz = dy h act'(z)
-//     dL/du k = G (a h_{t-1} k - v k a^2 / s) with u = -w, k = u (or a_gate's slope 1 - a of log a):
-//     da_gate that times 1 - r (or as it is), da_param its sum over the tokens times sigmoid(a_param) decay / K
+// Gradient.  A tile is TT tokens of one sequence (its last one may be shorter); what reaches it from the tokens before
+// and behind is linear in two numbers a channel, so tiles run side by side:
+//   linrec_sum_kernel: of each tile the product P of its decays, its last state from 0 and the gradient that leaves it backwards with 0 from behind
+//   linrec_join_kernel: a sequence's tiles in order, H <- P H + h, and in reverse, G <- P G + g: the state before each tile, the gradient from behind it
+//   linrec_bwd_kernel: each tile again from these, with its gradients
+// With e = dy act(z) and G_t = e_t + a_{t+1} G_{t+1}:
+//     dx = G s p,  dx_gate = G s x p (1 - p),  dz = dy h act'(z),
+//     d = G (a h_{t-1} k - v kappa),  k = -w (or 1 - a: a_gate's slope of log a),  kappa = -k ds/du = k a^2 / s | k a | 0
+//     da_gate = d (1 - r) (or d),  da_param = sum of d over the tokens, times sigmoid(a_param) decay / K
 struct GradParams {
     Params p;
     const void* dy;
     const float *h0, *dhT;
     void *dx, *da, *dg, *dz;
-    float *dap, *dh0, *hs, *part;
+    float *dap, *dh0;
+    float *P, *h, *g, *part;  // [tiles][C]
+    int tiles;                // at most: T / TT + N, sequence n's from cu[n] / TT + n on
 };
+
 template <typename T>
-__global__ void __launch_bounds__(128) linrec_bwd_kernel(const __grid_constant__ GradParams q) {
+struct GradTile {
+    static constexpr int CB = 32, VN = V16<T>::n, CH = CB / VN, NT = 256, TT = NT / CH, NQ = TT / 4;
+    float4 a[NQ][CB], b[NQ + 1][CB], e[NQ][CB];  // units as in FwdTile; b gets the states before each token, and the last one behind them, e the G
+    uint4 in[2][5][NT];                          // x, a_gate, x_gate, z, dy of this tile and the next one; then the gradients on their way to rows
+    float K[CB];
+    float red[NT / 32][CB];
+    static __device__ __forceinline__ int unit(int q, int c) { return c ^ 2 * (q & 3); }
+};
+
+// Sequence, first token and tokens of tile v (0 where it has none), by a warp's 32-ary search.
+struct Where {
+    int t0, rows;
+};
+__device__ __forceinline__ Where tile_at(const Params& p, int TT, int v) {
+    const int lane = threadIdx.x & 31;
+    auto first = [&](int n) { return max(0, min(__ldg(p.cu + n), p.T)) / TT + n; };
+    int lo = 0, hi = p.N;  // the last n in [lo, hi) that starts at v or before
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, n = lo + lane * step;
+        const unsigned at = __ballot_sync(0xffffffffu, n < hi && first(n) <= v);
+        const int k = at ? 31 - __clz((int)at) : 0;
+        lo += k * step;
+        hi = min(hi, lo + step);
+    }
+    int bos, eos;
+    bounds(p.cu, lo, p.T, bos, eos);
+    const int64_t off = (int64_t)(v - first(lo)) * TT;
+    Where w;
+    w.rows = off < 0 ? 0 : (int)max((int64_t)0, min((int64_t)TT, eos - bos - off)), w.t0 = bos + (int)(w.rows ? off : 0);
+    return w;
+}
+
+// The asynchronous copies of a tile's inputs, in a group of their own; places as the workers' Share has them.
+template <typename T>
+__device__ __forceinline__ void copy_tile(const GradParams& q, GradTile<T>& sm, int buf, const Where& w, int c0) {
+    using F = GradTile<T>;
+    using Q = Share<T, F::CB>;
     const Params& p = q.p;
-    const int blocks = (p.C + 127) / 128, n = blockIdx.x / blocks, c = blockIdx.x % blocks * 128 + threadIdx.x;
+    const int row = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, slot = Q::place(row, ch, F::CH), c = c0 + ch * F::VN;
+    if (row < w.rows && c < p.C) {
+        const int64_t t = w.t0 + row;
+        copy16_async(&sm.in[buf][0][slot], static_cast<const T*>(p.x) + t * p.ldx + c);
+        copy16_async(&sm.in[buf][1][slot], static_cast<const T*>(p.ag) + t * p.lda + c);
+        if (p.xg) copy16_async(&sm.in[buf][2][slot], static_cast<const T*>(p.xg) + t * p.ldg + c);
+        if (p.z) copy16_async(&sm.in[buf][3][slot], static_cast<const T*>(p.z) + t * p.ldz + c);
+        copy16_async(&sm.in[buf][4][slot], static_cast<const T*>(q.dy) + t * p.C + c);
+    }
+    copy_commit();
+}
+
+// Tokens behind a tile's end pass everything on as it is: a = 1, b = e = 0.  v: pairs of tokens of `per` each channel's.
+template <int NP>
+__device__ __forceinline__ void pad(int rows, float2 (&v)[NP], float with) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        if (2 * (k & 1) >= rows) v[k].x = with;
+        if (2 * (k & 1) + 1 >= rows) v[k].y = with;
+    }
+}
+
+// e = dy act(z) and the decays and intakes of a worker's tokens to shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constant__ GradParams q) {
+    using F = GradTile<T>;
+    using Q = Share<T, F::CB>;
+    constexpr int NP = Q::NP, CB = F::CB, NQ = F::NQ;
+    extern __shared__ __align__(128) unsigned char raw[];
+    F& sm = *reinterpret_cast<F*>(raw);
+    const Params& p = q.p;
+    const int blocks = (p.C + CB - 1) / CB, lane = threadIdx.x & 31;
+    const int64_t items = (int64_t)q.tiles * blocks;
+    const Q my(threadIdx.x);
+    int64_t it = blockIdx.x;
+    Where w = tile_at(p, F::TT, (int)(it / blocks));
+    copy_tile(q, sm, 0, w, (int)(it % blocks) * CB);
+    for (int buf = 0; it < items; it += gridDim.x, buf ^= 1) {
+        const int v = (int)(it / blocks), c0 = (int)(it % blocks) * CB;
+        const int rows = w.rows;
+        if (p.ap && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
+        copy_wait<0>();
+        __syncthreads();
+        if (it + gridDim.x < items) {
+            w = tile_at(p, F::TT, (int)((it + gridDim.x) / blocks));
+            copy_tile(q, sm, buf ^ 1, w, (int)((it + gridDim.x) % blocks) * CB);
+        }
+        if (!rows) continue;
+        float2 K[NP], x[NP], ag[NP], xg[NP], a[NP], b[NP], e[NP];
+        my.rates(sm.K, K);
+        my.load(sm.in[buf][0], x);
+        my.load(sm.in[buf][1], ag);
+        my.load(sm.in[buf][2], xg);
+        my.load(sm.in[buf][4], e);
+        steps(p, any_far(K), K, ag, xg, x, a, b);
+        if (p.z) {
+            float2 z[NP];
+            my.load(sm.in[buf][3], z);
+            branch(p.act, z, e);
+        }
+        if (rows < F::TT) pad(rows - 4 * my.q, a, 1.f), pad(rows - 4 * my.q, b, 0.f), pad(rows - 4 * my.q, e, 0.f);
+        my.template put<F>(sm.a, a);
+        my.template put<F>(sm.b, b);
+        my.template put<F>(sm.e, e);
+        __syncthreads();
+        const int64_t own = (int64_t)v * p.C + c0 + lane;
+        const bool ok = c0 + lane < p.C;
+        if (threadIdx.x < 32) {
+            float h = 0.f, P = 1.f;
+#pragma unroll 4
+            for (int u = 0; u < NQ; ++u) {
+                const float4 av = sm.a[u][F::unit(u, lane)], bv = sm.b[u][F::unit(u, lane)];
+                h = __fmaf_rn(av.x, h, bv.x), h = __fmaf_rn(av.y, h, bv.y), h = __fmaf_rn(av.z, h, bv.z), h = __fmaf_rn(av.w, h, bv.w);
+                P = __fmul_rn(P, __fmul_rn(__fmul_rn(av.x, av.y), __fmul_rn(av.z, av.w)));
+            }
+            if (ok) q.P[own] = P, q.h[own] = h;
+        } else if (threadIdx.x < 64) {
+            float g = 0.f, next = 1.f;
+#pragma unroll 4
+            for (int u = NQ - 1; u >= 0; --u) {
+                const float4 av = sm.a[u][F::unit(u, lane)], ev = sm.e[u][F::unit(u, lane)];
+                g = __fmaf_rn(next, g, ev.w), g = __fmaf_rn(av.w, g, ev.z), g = __fmaf_rn(av.z, g, ev.y), g = __fmaf_rn(av.y, g, ev.x);
+                next = av.x;
+            }
+            if (ok) q.g[own] = __fmul_rn(next, g);
+        }
+    }
+    copy_wait<0>();
+}
+
+// A thread one channel of one sequence, in one direction (blockIdx.y): each tile's sum is replaced by what reaches the tile.
+__global__ void __launch_bounds__(128) linrec_join_kernel(const __grid_constant__ GradParams q, int TT) {
+    const Params& p = q.p;
+    const int blocks = (p.C + 127) / 128, c = blockIdx.x % blocks * 128 + threadIdx.x, n = blockIdx.x / blocks;
     if (c >= p.C) return;
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
-    const float K = p.ap ? rate_of(__ldg(p.ap + c), p.decay) : 0.f;
-    const int64_t own = (int64_t)n * p.C + c;
-    const float h0 = q.h0 ? q.h0[own] : 0.f;
-    float h = h0;
-    for (int64_t t = bos; t < eos; ++t) {
-        const float x = load1(static_cast<const T*>(p.x) + t * p.ldx + c), ag = load1(static_cast<const T*>(p.ag) + t * p.lda + c);
-        const float xg = p.xg ? load1(static_cast<const T*>(p.xg) + t * p.ldg + c) : 0.f;
-        const float2 K1[1] = {both(K)}, g1[1] = {both(ag)}, i1[1] = {both(xg)}, x1[1] = {both(x)};
-        float2 a[1], b[1];
-        steps(p, true, K1, g1, i1, x1, a, b);
-        h = __fmaf_rn(a[0].x, h, b[0].x);
-        q.hs[t * p.C + c] = h;
+    const int tiles = (eos - bos + TT - 1) / TT;
+    const int64_t own = (int64_t)n * p.C + c, first = (int64_t)(bos / TT + n) * p.C + c, C = p.C;
+    const bool back = blockIdx.y;
+    const float* from = back ? q.dhT : q.h0;
+    float v = from ? from[own] : 0.f;
+    float* sum = (back ? q.g : q.h) + first + (back && tiles ? (int64_t)(tiles - 1) * C : 0);
+    const float* P = q.P + (sum - (back ? q.g : q.h));
+    const int64_t step = back ? -C : C;
+    int i = 0;
+    for (; i + 8 <= tiles; i += 8) {
+        float ps[8], ss[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ps[k] = P[k * step], ss[k] = sum[k * step];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            sum[k * step] = v;
+            v = __fmaf_rn(ps[k], v, ss[k]);
+        }
+        P += 8 * step, sum += 8 * step;
     }
-    float g = q.dhT ? q.dhT[own] : 0.f, sum = 0.f;
-    for (int64_t t = eos - 1; t >= bos; --t) {
-        const float x = load1(static_cast<const T*>(p.x) + t * p.ldx + c), ag = load1(static_cast<const T*>(p.ag) + t * p.lda + c);
-        const float xg = p.xg ? load1(static_cast<const T*>(p.xg) + t * p.ldg + c) : 0.f;
-        const float dy = load1(static_cast<const T*>(q.dy) + t * p.C + c);
-        h = q.hs[t * p.C + c];
-        const float old = t > bos ? q.hs[(t - 1) * p.C + c] : h0;
-        float2 e, a, m, ep;
-        const float2 r = sigmoid2(both(ag), e), r1 = rest2(e, r);
-        float2 w = both(0.f);
-        if (p.ap) {
-            const float2 w1[1] = {__fmul2_rn(both(K), r)};
-            float2 a1[1], m1[1];
-            decays(true, w1, a1, m1);
-            w = w1[0], a = a1[0], m = m1[0];
-        } else {
-            a = r, m = r1;
-        }
-        const float k = p.ap ? -w.x : m.x;
-        float s = 1.f, kappa = 0.f;
-        if (p.scale == GDN_SCALE_SQRT) {
-            const float t2 = rest_of_square(a, m).x;
-            s = sqrt_approx(t2);
-            kappa = t2 > 0.f ? k * a.x * a.x * rsqrt_approx(t2) : 0.f;
-        } else if (p.scale == GDN_SCALE_LINEAR) {
-            s = m.x, kappa = k * a.x;
-        }
-        const float2 pg = p.xg ? sigmoid2(both(xg), ep) : both(1.f);
-        const float v = x * pg.x;
-        float ge = dy;
-        if (p.z) {
-            float2 slope;
-            const float f = act2(p.act, both(load1(static_cast<const T*>(p.z) + t * p.ldz + c)), slope).x;
-            store1(static_cast<T*>(q.dz) + t * p.C + c, dy * h * slope.x);
-            ge = dy * f;
-        }
-        g = g + ge;
-        const float dv = g * s;
-        store1(static_cast<T*>(q.dx) + t * p.C + c, dv * pg.x);
-        if (p.xg) store1(static_cast<T*>(q.dg) + t * p.C + c, dv * v * rest2(ep, pg).x);
-        const float d = g * (a.x * old * k - v * kappa);
-        store1(static_cast<T*>(q.da) + t * p.C + c, p.ap ? d * r1.x : d);
-        sum += d;
-        g = a.x * g;
+    for (; i < tiles; ++i, P += step, sum += step) {
+        const float ps = *P, ss = *sum;
+        *sum = v;
+        v = __fmaf_rn(ps, v, ss);
     }
-    if (q.dh0) q.dh0[own] = g;
-    if (q.part) q.part[own] = sum;
+    if (back && q.dh0) q.dh0[own] = v;
 }
-__global__ void __launch_bounds__(128) linrec_param_kernel(int N, int C, float decay, const float* __restrict__ ap,
+
+template <typename T>
+__global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constant__ GradParams q) {
+    using F = GradTile<T>;
+    using Q = Share<T, F::CB>;
+    constexpr int NP = Q::NP, CB = F::CB, NQ = F::NQ;
+    constexpr bool bf16 = !std::is_same<T, float>::value;
+    extern __shared__ __align__(128) unsigned char raw[];
+    F& sm = *reinterpret_cast<F*>(raw);
+    const Params& p = q.p;
+    const int blocks = (p.C + CB - 1) / CB, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t items = (int64_t)q.tiles * blocks;
+    const Q my(threadIdx.x);
+    // the last tiles first: their inputs are those that the sums' kernel read last
+    auto tile_of = [&](int64_t it) { return q.tiles - 1 - (int)(it / blocks); };
+    int64_t it = blockIdx.x;
+    Where w = tile_at(p, F::TT, tile_of(it));
+    copy_tile(q, sm, 0, w, (int)(it % blocks) * CB);
+    for (int buf = 0; it < items; it += gridDim.x, buf ^= 1) {
+        const int v = tile_of(it), c0 = (int)(it % blocks) * CB;
+        const int rows = w.rows, t0 = w.t0;
+        const int64_t own = (int64_t)v * p.C + c0 + lane;
+        const bool ok = c0 + lane < p.C;
+        float carry = 0.f;  // what reaches the tile, in the walkers
+        if (rows && warp < 2 && ok) carry = warp ? q.g[own] : q.h[own];
+        if (p.ap && threadIdx.x < CB) sm.K[threadIdx.x] = ok ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
+        copy_wait<0>();
+        __syncthreads();
+        if (it + gridDim.x < items) {
+            w = tile_at(p, F::TT, tile_of(it + gridDim.x));
+            copy_tile(q, sm, buf ^ 1, w, (int)((it + gridDim.x) % blocks) * CB);
+        }
+        if (!rows) {
+            if (q.part && threadIdx.x < CB && ok) q.part[own] = 0.f;
+            continue;
+        }
+        uint4(&in)[5][F::NT] = sm.in[buf];
+        float2 dx[NP], dg[NP], da1[NP], da0[NP], rest[NP], dz[NP];  // factors of the gradients
+        {
+            float2 K[NP], x[NP], ag[NP], xg[NP], a[NP], m[NP], r[NP], u[NP], f[NP], k[NP], s[NP];
+            my.rates(sm.K, K);
+            my.load(in[1], ag);
+            my.load(in[0], x);
+            if (p.xg) {
+                my.load(in[2], xg);
+                two_sigmoids(ag, xg, r, dx, u, f);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) r[i] = sigmoid2(ag[i], u[i]), dx[i] = both(1.f), f[i] = both(0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < NP; ++i) rest[i] = rest2(u[i], r[i]), dg[i] = rest2(f[i], dx[i]), x[i] = __fmul2_rn(x[i], dx[i]);
+            if (p.ap) {
+                float2 w2[NP];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) w2[i] = __fmul2_rn(K[i], r[i]), k[i] = neg(w2[i]);
+                decays(any_far(K), w2, a, m);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) a[i] = r[i], m[i] = rest[i], k[i] = m[i], rest[i] = both(1.f);
+            }
+#pragma unroll
+            for (int i = 0; i < NP; ++i) da1[i] = __fmul2_rn(a[i], k[i]);
+            if (p.scale == GDN_SCALE_SQRT) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const float2 t = rest_of_square(a[i], m[i]);
+                    const float2 o = make_float2(t.x > 0.f ? rsqrt_approx(t.x) : 0.f, t.y > 0.f ? rsqrt_approx(t.y) : 0.f);
+                    s[i] = __fmul2_rn(t, o), da0[i] = __fmul2_rn(__fmul2_rn(da1[i], a[i]), o);
+                }
+            } else if (p.scale == GDN_SCALE_LINEAR) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) s[i] = m[i], da0[i] = da1[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) s[i] = both(1.f), da0[i] = both(0.f);
+            }
+            float2 b[NP], e[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                b[i] = __fmul2_rn(s[i], x[i]);
+                da0[i] = neg(__fmul2_rn(da0[i], x[i]));
+                dg[i] = __fmul2_rn(b[i], dg[i]), dx[i] = __fmul2_rn(s[i], dx[i]);
+            }
+            my.load(in[4], e);
+            if (p.z) {
+                float2 z[NP];
+                my.load(in[3], z);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    float2 slope;
+                    const float2 g = act2(p.act, z[i], slope);
+                    dz[i] = __fmul2_rn(e[i], slope), e[i] = __fmul2_rn(e[i], g);
+                }
+            }
+            if (rows < F::TT) pad(rows - 4 * my.q, a, 1.f), pad(rows - 4 * my.q, b, 0.f), pad(rows - 4 * my.q, e, 0.f);
+            my.template put<F>(sm.a, a);
+            my.template put<F>(sm.b, b);
+            my.template put<F>(sm.e, e);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            float h = carry;
+#pragma unroll 4
+            for (int j = 0; j < NQ; ++j) {
+                const float4 av = sm.a[j][F::unit(j, lane)], bv = sm.b[j][F::unit(j, lane)];
+                float4 o;
+                o.x = h, o.y = __fmaf_rn(av.x, o.x, bv.x), o.z = __fmaf_rn(av.y, o.y, bv.y), o.w = __fmaf_rn(av.z, o.z, bv.z), h = __fmaf_rn(av.w, o.w, bv.w);
+                sm.b[j][F::unit(j, lane)] = o;
+            }
+            sm.b[NQ][F::unit(NQ, lane)].x = h;
+        } else if (warp == 1) {
+            float g = carry, next = 1.f;
+#pragma unroll 4
+            for (int j = NQ - 1; j >= 0; --j) {
+                const float4 av = sm.a[j][F::unit(j, lane)], ev = sm.e[j][F::unit(j, lane)];
+                float4 o;
+                o.w = __fmaf_rn(next, g, ev.w), o.z = __fmaf_rn(av.w, o.w, ev.z), o.y = __fmaf_rn(av.z, o.z, ev.y), g = o.x = __fmaf_rn(av.y, o.y, ev.x);
+                next = av.x;
+                sm.e[j][F::unit(j, lane)] = o;
+            }
+        }
+        __syncthreads();
+        float2 g[NP], old[NP], d[NP];
+        my.template get<F>(sm.e, g);
+        my.template get<F>(sm.b, old);
+        if (p.z) {  // the state after a token is the one before the next
+            float2 h[NP];
+#pragma unroll
+            for (int i = 0; i < NP; i += 2) {
+                const float after = sm.b[my.q + 1][F::unit(my.q + 1, my.c + 4 * i)].x;  // bf16: the second channel is 8 on
+                h[i] = make_float2(old[i].y, old[i + 1].x), h[i + 1] = make_float2(old[i + 1].y, after);
+            }
+#pragma unroll
+            for (int i = 0; i < NP; ++i) dz[i] = __fmul2_rn(dz[i], h[i]);
+        }
+        float2 total[NP / 2];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            d[i] = __fmul2_rn(g[i], __ffma2_rn(da1[i], old[i], da0[i]));
+            dx[i] = __fmul2_rn(g[i], dx[i]), dg[i] = __fmul2_rn(g[i], dg[i]);
+        }
+        if (q.part) {
+            if (rows < F::TT) pad(rows - 4 * my.q, d, 0.f);
+#pragma unroll
+            for (int i = 0; i < NP; i += 2) total[i / 2] = __fadd2_rn(d[i], d[i + 1]);
+            if constexpr (bf16) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float t = __fadd_rn(total[i].x, total[i].y);
+                    t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                    t = __fadd_rn(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                    if (lane % 4 == 0) sm.red[my.q / 4][my.c + 8 * i] = t;
+                }
+            } else {
+                sm.red[warp][lane] = __fadd_rn(total[0].x, total[0].y);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) d[i] = __fmul2_rn(d[i], rest[i]);
+        auto out = [&](void* to, uint4* by, const float2 (&o)[NP]) {
+            T* at = static_cast<T*>(to) + (int64_t)(t0 + my.row) * p.C + c0 + my.row_c;
+            const bool cok = c0 + my.row_c < p.C;
+            if constexpr (bf16) {
+                my.store_in(by, at, cok && my.row < rows, o);
+            } else {
+                const float f[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (cok && my.row + j < rows) at[(int64_t)j * p.C] = f[j];
+            }
+        };
+        out(q.dx, in[0], dx);
+        out(q.da, in[1], d);
+        if (p.xg) out(q.dg, in[2], dg);
+        if (p.z) out(q.dz, in[3], dz);
+        if (q.part) {
+            __syncthreads();
+            if (threadIdx.x < CB && ok) {
+                float t = sm.red[0][lane];
+#pragma unroll
+                for (int i = 1; i < (bf16 ? F::TT / 16 : F::NT / 32); ++i) t = __fadd_rn(t, sm.red[i][lane]);
+                q.part[own] = t;
+            }
+        }
+    }
+    copy_wait<0>();
+}
+
+// da_param: a CTA 32 channels; its warps add the tiles' sums warp, warp + 8, .., then the warps' in order.
+__global__ void __launch_bounds__(256) linrec_param_kernel(int tiles, int C, float decay, const float* __restrict__ ap,
                                                            const float* __restrict__ part, float* __restrict__ out) {
-    const int c = blockIdx.x * 128 + threadIdx.x;
-    if (c >= C) return;
+    __shared__ float sums[8][32];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), warp = threadIdx.x / 32;
     float s = 0.f;
-    for (int n = 0; n < N; ++n) s += part[(int64_t)n * C + c];
+    if (c < C) {
+#pragma unroll 8
+        for (int i = warp; i < tiles; i += 8) s = __fadd_rn(s, __ldg(part + (int64_t)i * C + c));
+    }
+    sums[warp][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (warp || c >= C) return;
+    for (int i = 1; i < 8; ++i) s = __fadd_rn(s, sums[i][threadIdx.x]);
     const float v = __ldg(ap + c), K = rate_of(v, decay), sp = 1.f / (1.f + expf(-v));
     out[c] = K > 0.f ? s * (decay * sp / K) : 0.f;
 }
@@ -442,6 +749,29 @@ template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
     if (LR_CB == 16 || (LR_CB == 0 && (long long)((p.C + 31) / 32) * p.N <= kSMs / 2)) return launch_fwd_of<T, 16, LR_WORK2, LR_AHEAD2, 1>(s, p);
     return launch_fwd_of<T, 32, LR_WORK, LR_AHEAD, LR_MINB>(s, p);
+}
+
+int64_t grad_tiles(int T, int N, int dtype) { return (int64_t)T / (dtype == GDN_BF16 ? GradTile<__nv_bfloat16>::TT : GradTile<float>::TT) + N; }
+
+template <typename T>
+gdn_status launch_bwd(cudaStream_t s, const GradParams& q) {
+    using F = GradTile<T>;
+    const Params& p = q.p;
+    if (cudaFuncSetAttribute(linrec_sum_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess ||
+        cudaFuncSetAttribute(linrec_bwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    const int64_t items = (int64_t)q.tiles * ((p.C + F::CB - 1) / F::CB);
+    auto ctas = [&](int each) { return (unsigned)(items < kSMs * each ? items : kSMs * each); };
+    if (p.T > 0) {
+        linrec_sum_kernel<T><<<ctas(3), F::NT, sizeof(F), s>>>(q);
+        const gdn_status st = launch_status();
+        if (st != GDN_OK) return st;
+    }
+    linrec_join_kernel<<<dim3((unsigned)((p.C + 127) / 128) * (unsigned)p.N, 2), 128, 0, s>>>(q, F::TT);
+    gdn_status st = launch_status();
+    if (st != GDN_OK || p.T == 0) return st;
+    linrec_bwd_kernel<T><<<ctas(2), F::NT, sizeof(F), s>>>(q);
+    return launch_status();
 }
 
 gdn_status check_linrec(const gdn_linrec_shape* s, bool param, bool gate, bool z) {
@@ -524,7 +854,7 @@ extern "C" gdn_status gdn_linear_recurrence_update(const gdn_linrec_shape* shape
 extern "C" size_t gdn_linear_recurrence_bwd_workspace_size(const gdn_linrec_shape* shape) {
     using namespace gdn;
     if (check_linrec(shape, false, false, false) != GDN_OK) return 0;
-    return ((size_t)shape->T_total + shape->N) * shape->C * sizeof(float);
+    return 4 * (size_t)grad_tiles(shape->T_total, shape->N, shape->dtype) * shape->C * sizeof(float);
 }
 
 extern "C" gdn_status gdn_linear_recurrence_bwd(const gdn_linrec_shape* shape, const void* x, const void* a_gate,
@@ -560,16 +890,15 @@ extern "C" gdn_status gdn_linear_recurrence_bwd(const gdn_linrec_shape* shape, c
     q.p.cu = cu_seqlens;
     q.dy = d_y, q.h0 = init_state, q.dhT = d_final_state, q.dx = dx, q.da = da_gate, q.dg = dx_gate, q.dz = dz;
     q.dap = da_param, q.dh0 = d_init_state;
-    q.hs = static_cast<float*>(workspace), q.part = da_param ? q.hs + (size_t)p.T * p.C : nullptr;
+    q.tiles = (int)grad_tiles(p.T, p.N, shape->dtype);
+    const size_t each = (size_t)q.tiles * p.C;
+    q.P = static_cast<float*>(workspace), q.h = q.P + each, q.g = q.h + each, q.part = da_param ? q.g + each : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned blocks = (unsigned)((p.C + 127) / 128);
     if (p.N > 0) {
-        if (shape->dtype == GDN_BF16) linrec_bwd_kernel<__nv_bfloat16><<<blocks * p.N, 128, 0, s>>>(q);
-        else linrec_bwd_kernel<float><<<blocks * p.N, 128, 0, s>>>(q);
-        st = launch_status();
+        st = shape->dtype == GDN_BF16 ? launch_bwd<__nv_bfloat16>(s, q) : launch_bwd<float>(s, q);
         if (st != GDN_OK) return st;
     }
     if (!da_param) return GDN_OK;
-    linrec_param_kernel<<<blocks, 128, 0, s>>>(p.N, p.C, p.decay, a_param, q.part, da_param);
+    linrec_param_kernel<<<(unsigned)((p.C + 31) / 32), 256, 0, s>>>(p.T > 0 ? q.tiles : 0, p.C, p.decay, a_param, q.part, da_param);
     return launch_status();
 }

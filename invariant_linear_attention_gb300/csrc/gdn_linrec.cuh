@@ -58,10 +58,9 @@ __device__ __forceinline__ float2 rest2(const float2& e, const float2& q) {
 
 // sigmoid(g) and sigmoid(i) with one reciprocal for both, 1 / ((1 + 2^v) (1 + 2^u)): the special function unit, which
 // takes two cycles a warp for a reciprocal or a root and one for an exponential, bounds the prompts' kernel next to HBM.
-// e: 2^v.  Where a power is past 2^60 and their product might leave fp32's range, each has its own.
+// e, f: 2^v, 2^u.  Where a power is past 2^60 and their product might leave fp32's range, each has its own.
 template <int NP>
-__device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2 (&i)[NP], float2 (&r)[NP], float2 (&p)[NP], float2 (&e)[NP]) {
-    float2 f[NP];
+__device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2 (&i)[NP], float2 (&r)[NP], float2 (&p)[NP], float2 (&e)[NP], float2 (&f)[NP]) {
     float most = 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
@@ -167,7 +166,8 @@ __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&
                                       const float2 (&x)[NP], float2 (&a)[NP], float2 (&b)[NP]) {
     float2 m[NP], r[NP], u[NP];
     if (p.xg) {
-        two_sigmoids(ag, xg, r, b, u);
+        float2 f[NP];
+        two_sigmoids(ag, xg, r, b, u, f);
 #pragma unroll
         for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(x[e], b[e]);
     } else {
