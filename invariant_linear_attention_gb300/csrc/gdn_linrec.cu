@@ -148,7 +148,7 @@ struct Share<float, CB> {
     }
 };
 
-template <typename T, typename F, int CB, int CTAS>
+template <typename T, typename F, int CB, int CTAS, Kind KIND>
 __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_constant__ Params p) {
     using Q = Share<T, CB>;
     constexpr int VN = F::VN, NP = Q::NP, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
     const int len = eos - bos, tiles = (len + TT - 1) / TT;
-    if (p.ap && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
+    if (has_param<KIND>(p) && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
     __syncthreads();
 
     if (threadIdx.x >= F::WALK) {
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
             if (left > 0) {
                 copy16_async(&to[0][slot], px);
                 copy16_async(&to[1][slot], pa);
-                if (p.xg) copy16_async(&to[2][slot], pg);
+                if (has_gate<KIND>(p)) copy16_async(&to[2][slot], pg);
             }
             px += (int64_t)TT * p.ldx, pa += (int64_t)TT * p.lda, pg += (int64_t)TT * p.ldg, left -= TT;
             if (behind > 0) {
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
                 my.load(from[0], x);
                 my.load(from[1], ag);
                 my.load(from[2], xg);
-                steps(p, far, K, ag, xg, x, a, b);
+                steps<KIND>(p, far, K, ag, xg, x, a, b);
                 my.template put<F>(sm.a[buf], a);
                 my.template put<F>(sm.b[buf], b);
                 rows -= TT;
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constan
         unpack2(xr, x);
         unpack2(ar, ag);
         unpack2(gr, xg);
-        steps(p, far, K, ag, xg, x, a, b);
+        steps<kAny>(p, far, K, ag, xg, x, a, b);
 #pragma unroll
         for (int e = 0; e < NP; ++e) h[e] = __ffma2_rn(a[e], h[e], b[e]);
 #pragma unroll
@@ -369,7 +369,20 @@ struct GradTile {
     static __device__ __forceinline__ int unit(int q, int c) { return c ^ 2 * (q & 3); }
 };
 
-// Sequence, first token and tokens of tile v (0 where it has none), by a warp's 32-ary search.
+// The (tile, block of channels) pairs of a CTA: blockIdx.x, + gridDim.x, ..
+struct Items {
+    int blocks, tile, block, tiles_on, blocks_on;
+    __device__ __forceinline__ Items(int C, int CB) {
+        blocks = (C + CB - 1) / CB, tile = blockIdx.x / blocks, block = blockIdx.x % blocks;
+        tiles_on = gridDim.x / blocks, blocks_on = gridDim.x % blocks;
+    }
+    __device__ __forceinline__ void advance() {
+        tile += tiles_on, block += blocks_on;
+        if (block >= blocks) block -= blocks, ++tile;
+    }
+};
+
+// First token and tokens of tile v (0 where it has none), by a warp's 32-ary search.
 struct Where {
     int t0, rows;
 };
@@ -421,7 +434,7 @@ __device__ __forceinline__ void pad(int rows, float2 (&v)[NP], float with) {
 }
 
 // e = dy act(z) and the decays and intakes of a worker's tokens to shared memory.
-template <typename T>
+template <typename T, Kind KIND>
 __global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constant__ GradParams q) {
     using F = GradTile<T>;
     using Q = Share<T, F::CB>;
@@ -429,21 +442,21 @@ __global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constan
     extern __shared__ __align__(128) unsigned char raw[];
     F& sm = *reinterpret_cast<F*>(raw);
     const Params& p = q.p;
-    const int blocks = (p.C + CB - 1) / CB, lane = threadIdx.x & 31;
-    const int64_t items = (int64_t)q.tiles * blocks;
+    const int lane = threadIdx.x & 31;
     const Q my(threadIdx.x);
-    int64_t it = blockIdx.x;
-    Where w = tile_at(p, F::TT, (int)(it / blocks));
-    copy_tile(q, sm, 0, w, (int)(it % blocks) * CB);
-    for (int buf = 0; it < items; it += gridDim.x, buf ^= 1) {
-        const int v = (int)(it / blocks), c0 = (int)(it % blocks) * CB;
+    Items next(p.C, CB);
+    Where w = tile_at(p, F::TT, next.tile);
+    copy_tile(q, sm, 0, w, next.block * CB);
+    for (int buf = 0; next.tile < q.tiles; buf ^= 1) {
+        const int v = next.tile, c0 = next.block * CB;
         const int rows = w.rows;
-        if (p.ap && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
+        next.advance();
+        if (has_param<KIND>(p) && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
         copy_wait<0>();
         __syncthreads();
-        if (it + gridDim.x < items) {
-            w = tile_at(p, F::TT, (int)((it + gridDim.x) / blocks));
-            copy_tile(q, sm, buf ^ 1, w, (int)((it + gridDim.x) % blocks) * CB);
+        if (next.tile < q.tiles) {
+            w = tile_at(p, F::TT, next.tile);
+            copy_tile(q, sm, buf ^ 1, w, next.block * CB);
         }
         if (!rows) continue;
         float2 K[NP], x[NP], ag[NP], xg[NP], a[NP], b[NP], e[NP];
@@ -452,7 +465,7 @@ __global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constan
         my.load(sm.in[buf][1], ag);
         my.load(sm.in[buf][2], xg);
         my.load(sm.in[buf][4], e);
-        steps(p, any_far(K), K, ag, xg, x, a, b);
+        steps<KIND>(p, any_far(K), K, ag, xg, x, a, b);
         if (p.z) {
             float2 z[NP];
             my.load(sm.in[buf][3], z);
@@ -523,7 +536,7 @@ __global__ void __launch_bounds__(128) linrec_join_kernel(const __grid_constant_
     if (back && q.dh0) q.dh0[own] = v;
 }
 
-template <typename T>
+template <typename T, Kind KIND>
 __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constant__ GradParams q) {
     using F = GradTile<T>;
     using Q = Share<T, F::CB>;
@@ -532,27 +545,25 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
     extern __shared__ __align__(128) unsigned char raw[];
     F& sm = *reinterpret_cast<F*>(raw);
     const Params& p = q.p;
-    const int blocks = (p.C + CB - 1) / CB, lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const int64_t items = (int64_t)q.tiles * blocks;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     const Q my(threadIdx.x);
-    // the last tiles first: their inputs are those that the sums' kernel read last
-    auto tile_of = [&](int64_t it) { return q.tiles - 1 - (int)(it / blocks); };
-    int64_t it = blockIdx.x;
-    Where w = tile_at(p, F::TT, tile_of(it));
-    copy_tile(q, sm, 0, w, (int)(it % blocks) * CB);
-    for (int buf = 0; it < items; it += gridDim.x, buf ^= 1) {
-        const int v = tile_of(it), c0 = (int)(it % blocks) * CB;
+    Items next(p.C, CB);  // the last tiles first: their inputs are those that the sums' kernel read last
+    Where w = tile_at(p, F::TT, q.tiles - 1 - next.tile);
+    copy_tile(q, sm, 0, w, next.block * CB);
+    for (int buf = 0; next.tile < q.tiles; buf ^= 1) {
+        const int v = q.tiles - 1 - next.tile, c0 = next.block * CB;
         const int rows = w.rows, t0 = w.t0;
+        next.advance();
         const int64_t own = (int64_t)v * p.C + c0 + lane;
         const bool ok = c0 + lane < p.C;
         float carry = 0.f;  // what reaches the tile, in the walkers
         if (rows && warp < 2 && ok) carry = warp ? q.g[own] : q.h[own];
-        if (p.ap && threadIdx.x < CB) sm.K[threadIdx.x] = ok ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
+        if (has_param<KIND>(p) && threadIdx.x < CB) sm.K[threadIdx.x] = ok ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
         copy_wait<0>();
         __syncthreads();
-        if (it + gridDim.x < items) {
-            w = tile_at(p, F::TT, tile_of(it + gridDim.x));
-            copy_tile(q, sm, buf ^ 1, w, (int)((it + gridDim.x) % blocks) * CB);
+        if (next.tile < q.tiles) {
+            w = tile_at(p, F::TT, q.tiles - 1 - next.tile);
+            copy_tile(q, sm, buf ^ 1, w, next.block * CB);
         }
         if (!rows) {
             if (q.part && threadIdx.x < CB && ok) q.part[own] = 0.f;
@@ -565,7 +576,7 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
             my.rates(sm.K, K);
             my.load(in[1], ag);
             my.load(in[0], x);
-            if (p.xg) {
+            if (has_gate<KIND>(p)) {
                 my.load(in[2], xg);
                 two_sigmoids(ag, xg, r, dx, u, f);
             } else {
@@ -574,7 +585,7 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
             }
 #pragma unroll
             for (int i = 0; i < NP; ++i) rest[i] = rest2(u[i], r[i]), dg[i] = rest2(f[i], dx[i]), x[i] = __fmul2_rn(x[i], dx[i]);
-            if (p.ap) {
+            if (has_param<KIND>(p)) {
                 float2 w2[NP];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) w2[i] = __fmul2_rn(K[i], r[i]), k[i] = neg(w2[i]);
@@ -585,14 +596,14 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
             }
 #pragma unroll
             for (int i = 0; i < NP; ++i) da1[i] = __fmul2_rn(a[i], k[i]);
-            if (p.scale == GDN_SCALE_SQRT) {
+            if (scale_of<KIND>(p) == GDN_SCALE_SQRT) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const float2 t = rest_of_square(a[i], m[i]);
                     const float2 o = make_float2(t.x > 0.f ? rsqrt_approx(t.x) : 0.f, t.y > 0.f ? rsqrt_approx(t.y) : 0.f);
                     s[i] = __fmul2_rn(t, o), da0[i] = __fmul2_rn(__fmul2_rn(da1[i], a[i]), o);
                 }
-            } else if (p.scale == GDN_SCALE_LINEAR) {
+            } else if (scale_of<KIND>(p) == GDN_SCALE_LINEAR) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) s[i] = m[i], da0[i] = da1[i];
             } else {
@@ -696,7 +707,7 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
         };
         out(q.dx, in[0], dx);
         out(q.da, in[1], d);
-        if (p.xg) out(q.dg, in[2], dg);
+        if (has_gate<KIND>(p)) out(q.dg, in[2], dg);
         if (p.z) out(q.dz, in[3], dz);
         if (q.part) {
             __syncthreads();
@@ -741,8 +752,10 @@ __global__ void __launch_bounds__(256) linrec_param_kernel(int tiles, int C, flo
 template <typename T, int CB, int WORKERS, int TILES, int CTAS>
 gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     using F = FwdTile<T, CB, WORKERS, TILES>;
-    if (cudaFuncSetAttribute(linrec_fwd_kernel<T, F, CB, CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
-    linrec_fwd_kernel<T, F, CB, CTAS><<<(unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N, F::NT, sizeof(F), s>>>(p);
+    const Kind kind = kind_of(p);
+    auto* kernel = kind == kBothGates ? linrec_fwd_kernel<T, F, CB, CTAS, kBothGates> : kind == kForget ? linrec_fwd_kernel<T, F, CB, CTAS, kForget> : linrec_fwd_kernel<T, F, CB, CTAS, kAny>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
+    kernel<<<(unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N, F::NT, sizeof(F), s>>>(p);
     return launch_status();
 }
 template <typename T>
@@ -757,20 +770,23 @@ template <typename T>
 gdn_status launch_bwd(cudaStream_t s, const GradParams& q) {
     using F = GradTile<T>;
     const Params& p = q.p;
-    if (cudaFuncSetAttribute(linrec_sum_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess ||
-        cudaFuncSetAttribute(linrec_bwd_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
+    const Kind kind = kind_of(p);
+    auto* sum = kind == kBothGates ? linrec_sum_kernel<T, kBothGates> : kind == kForget ? linrec_sum_kernel<T, kForget> : linrec_sum_kernel<T, kAny>;
+    auto* bwd = kind == kBothGates ? linrec_bwd_kernel<T, kBothGates> : kind == kForget ? linrec_bwd_kernel<T, kForget> : linrec_bwd_kernel<T, kAny>;
+    if (cudaFuncSetAttribute(sum, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess ||
+        cudaFuncSetAttribute(bwd, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess)
         return GDN_ERR_CUDA;
     const int64_t items = (int64_t)q.tiles * ((p.C + F::CB - 1) / F::CB);
     auto ctas = [&](int each) { return (unsigned)(items < kSMs * each ? items : kSMs * each); };
     if (p.T > 0) {
-        linrec_sum_kernel<T><<<ctas(3), F::NT, sizeof(F), s>>>(q);
+        sum<<<ctas(3), F::NT, sizeof(F), s>>>(q);
         const gdn_status st = launch_status();
         if (st != GDN_OK) return st;
     }
     linrec_join_kernel<<<dim3((unsigned)((p.C + 127) / 128) * (unsigned)p.N, 2), 128, 0, s>>>(q, F::TT);
     gdn_status st = launch_status();
     if (st != GDN_OK || p.T == 0) return st;
-    linrec_bwd_kernel<T><<<ctas(2), F::NT, sizeof(F), s>>>(q);
+    bwd<<<ctas(2), F::NT, sizeof(F), s>>>(q);
     return launch_status();
 }
 

@@ -145,10 +145,21 @@ struct Params {
     void* y;
 };
 
-__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// Which of a call's options a kernel knows at compile time.  With all of them as branches, the values that meet
+// behind each branch cost about 100 of 420 instructions per 8 tokens and channels in register moves; all combinations would
+// be 36 kernels of each.  kBothGates: a_param, x_gate, scale sqrt; kForget: neither, scale linear; kAny: asks at run time.
+// The bits are the same.
+enum Kind { kAny, kBothGates, kForget };
+template <Kind KIND>
+__device__ __forceinline__ bool has_param(const Params& p) { return KIND == kAny ? p.ap != nullptr : KIND == kBothGates; }
+template <Kind KIND>
+__device__ __forceinline__ bool has_gate(const Params& p) { return KIND == kAny ? p.xg != nullptr : KIND == kBothGates; }
+template <Kind KIND>
+__device__ __forceinline__ int scale_of(const Params& p) { return KIND == kAny ? p.scale : KIND == kBothGates ? GDN_SCALE_SQRT : GDN_SCALE_LINEAR; }
+inline Kind kind_of(const Params& p) {
+    if (p.ap && p.xg && p.scale == GDN_SCALE_SQRT) return kBothGates;
+    return !p.ap && !p.xg && p.scale == GDN_SCALE_LINEAR ? kForget : kAny;
+}
 
 // Whether a channel of these rates has far tokens.
 template <int NP>
@@ -159,13 +170,13 @@ __device__ __forceinline__ bool any_far(const float2 (&K)[NP]) {
     return most >= kNear;
 }
 
-// a and b of NP pairs (neighbouring channels, or one channel's tokens).  The call's options are branches around whole
-// loops: one compiled form for all, and the pairs' operations still overlap.
-template <int NP>
+// a and b of NP pairs (neighbouring channels, or one channel's tokens).  Options are branches around whole loops, so that
+// the pairs' operations overlap.
+template <Kind KIND, int NP>
 __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&K)[NP], const float2 (&ag)[NP], const float2 (&xg)[NP],
                                       const float2 (&x)[NP], float2 (&a)[NP], float2 (&b)[NP]) {
     float2 m[NP], r[NP], u[NP];
-    if (p.xg) {
+    if (has_gate<KIND>(p)) {
         float2 f[NP];
         two_sigmoids(ag, xg, r, b, u, f);
 #pragma unroll
@@ -174,7 +185,7 @@ __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&
 #pragma unroll
         for (int e = 0; e < NP; ++e) r[e] = sigmoid2(ag[e], u[e]), b[e] = x[e];
     }
-    if (p.ap) {
+    if (has_param<KIND>(p)) {
         float2 w[NP];
 #pragma unroll
         for (int e = 0; e < NP; ++e) w[e] = __fmul2_rn(K[e], r[e]);
@@ -183,13 +194,13 @@ __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&
 #pragma unroll
         for (int e = 0; e < NP; ++e) a[e] = r[e], m[e] = rest2(u[e], r[e]);
     }
-    if (p.scale == GDN_SCALE_SQRT) {
+    if (scale_of<KIND>(p) == GDN_SCALE_SQRT) {
 #pragma unroll
         for (int e = 0; e < NP; ++e) {
             const float2 t = rest_of_square(a[e], m[e]);
             b[e] = __fmul2_rn(make_float2(sqrt_approx(t.x), sqrt_approx(t.y)), b[e]);
         }
-    } else if (p.scale == GDN_SCALE_LINEAR) {
+    } else if (scale_of<KIND>(p) == GDN_SCALE_LINEAR) {
 #pragma unroll
         for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(m[e], b[e]);
     }
@@ -197,18 +208,13 @@ __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&
 // y = h act(z) of NP pairs.
 template <int NP>
 __device__ __forceinline__ void branch(int act, const float2 (&z)[NP], float2 (&h)[NP]) {
-    float2 v[NP];
+    float2 e;
     if (act == GDN_ACT_GELU) {
 #pragma unroll
-        for (int e = 0; e < NP; ++e) v[e] = inner2(GDN_ACT_GELU, z[e]);
+        for (int k = 0; k < NP; ++k) h[k] = __fmul2_rn(h[k], __fmul2_rn(z[k], logistic2(inner2(GDN_ACT_GELU, z[k]), e)));
     } else {
 #pragma unroll
-        for (int e = 0; e < NP; ++e) v[e] = inner2(GDN_ACT_SILU, z[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < NP; ++e) {
-        float2 u;
-        h[e] = __fmul2_rn(h[e], __fmul2_rn(z[e], logistic2(v[e], u)));
+        for (int k = 0; k < NP; ++k) h[k] = __fmul2_rn(h[k], __fmul2_rn(z[k], logistic2(inner2(GDN_ACT_SILU, z[k]), e)));
     }
 }
 
