@@ -359,12 +359,17 @@ struct GradParams {
     int tiles;                // at most: T / TT + N, sequence n's from cu[n] / TT + n on
 };
 
+// A tile's first token and tokens (0: no such tile).
+struct Where {
+    int t0, rows;
+};
 template <typename T>
 struct GradTile {
     static constexpr int CB = 32, VN = V16<T>::n, CH = CB / VN, NT = 256, TT = NT / CH, NQ = TT / 4;
     float4 a[NQ][CB], b[NQ + 1][CB], e[NQ][CB];  // units as in FwdTile; b gets the states before each token, and the last one behind them, e the G
     uint4 in[2][5][NT];                          // x, a_gate, x_gate, z, dy of this tile and the next one; then the gradients on their way to rows
-    float K[CB];
+    float K[2][CB];     // of this item and the next one
+    Where where[2];
     float red[NT / 32][CB];
     static __device__ __forceinline__ int unit(int q, int c) { return c ^ 2 * (q & 3); }
 };
@@ -376,16 +381,18 @@ struct Items {
         blocks = (C + CB - 1) / CB, tile = blockIdx.x / blocks, block = blockIdx.x % blocks;
         tiles_on = gridDim.x / blocks, blocks_on = gridDim.x % blocks;
     }
+    __device__ __forceinline__ Items after() const {
+        Items a = *this;
+        a.advance();
+        return a;
+    }
     __device__ __forceinline__ void advance() {
         tile += tiles_on, block += blocks_on;
         if (block >= blocks) block -= blocks, ++tile;
     }
 };
 
-// First token and tokens of tile v (0 where it has none), by a warp's 32-ary search.
-struct Where {
-    int t0, rows;
-};
+// Tile v, by a warp's 32-ary search.
 __device__ __forceinline__ Where tile_at(const Params& p, int TT, int v) {
     const int lane = threadIdx.x & 31;
     auto first = [&](int n) { return max(0, min(__ldg(p.cu + n), p.T)) / TT + n; };
@@ -405,32 +412,39 @@ __device__ __forceinline__ Where tile_at(const Params& p, int TT, int v) {
     return w;
 }
 
-// The asynchronous copies of a tile's inputs, in a group of their own; places as the workers' Share has them.
+// The asynchronous copies of a tile's inputs, in a group of their own; places as the workers' Share has them.  Rows behind
+// the tile's end get inputs that pass everything on as it is: a = 1, no intake, no gradient of their own.
 template <typename T>
 __device__ __forceinline__ void copy_tile(const GradParams& q, GradTile<T>& sm, int buf, const Where& w, int c0) {
     using F = GradTile<T>;
     using Q = Share<T, F::CB>;
     const Params& p = q.p;
     const int row = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, slot = Q::place(row, ch, F::CH), c = c0 + ch * F::VN;
-    if (row < w.rows && c < p.C) {
+    uint4(&to)[5][F::NT] = sm.in[buf];
+    if (row >= w.rows) {
+        const uint32_t inf = std::is_same<T, float>::value ? 0x7f800000u : 0x7f807f80u, open = p.ap ? inf | (inf & 0x40004000u) << 1 : inf;
+        to[1][slot] = make_uint4(open, open, open, open);
+        to[0][slot] = to[2][slot] = to[3][slot] = to[4][slot] = make_uint4(0u, 0u, 0u, 0u);
+    } else if (c < p.C) {
         const int64_t t = w.t0 + row;
-        copy16_async(&sm.in[buf][0][slot], static_cast<const T*>(p.x) + t * p.ldx + c);
-        copy16_async(&sm.in[buf][1][slot], static_cast<const T*>(p.ag) + t * p.lda + c);
-        if (p.xg) copy16_async(&sm.in[buf][2][slot], static_cast<const T*>(p.xg) + t * p.ldg + c);
-        if (p.z) copy16_async(&sm.in[buf][3][slot], static_cast<const T*>(p.z) + t * p.ldz + c);
-        copy16_async(&sm.in[buf][4][slot], static_cast<const T*>(q.dy) + t * p.C + c);
+        copy16_async(&to[0][slot], static_cast<const T*>(p.x) + t * p.ldx + c);
+        copy16_async(&to[1][slot], static_cast<const T*>(p.ag) + t * p.lda + c);
+        if (p.xg) copy16_async(&to[2][slot], static_cast<const T*>(p.xg) + t * p.ldg + c);
+        if (p.z) copy16_async(&to[3][slot], static_cast<const T*>(p.z) + t * p.ldz + c);
+        copy16_async(&to[4][slot], static_cast<const T*>(q.dy) + t * p.C + c);
     }
     copy_commit();
 }
-
-// Tokens behind a tile's end pass everything on as it is: a = 1, b = e = 0.  v: pairs of tokens of `per` each channel's.
-template <int NP>
-__device__ __forceinline__ void pad(int rows, float2 (&v)[NP], float with) {
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-        if (2 * (k & 1) >= rows) v[k].x = with;
-        if (2 * (k & 1) + 1 >= rows) v[k].y = with;
+// One warp finds the tile of the item after next, and works out the next item's rates, while others walk.
+template <Kind KIND, typename F>
+__device__ __forceinline__ void look_ahead(const GradParams& q, F& sm, int turn, int tile, int c0) {
+    const Params& p = q.p;
+    const int lane = threadIdx.x & 31;
+    if (tile >= 0 && tile < q.tiles) {
+        const Where w = tile_at(p, F::TT, tile);
+        if (lane == 0) sm.where[turn] = w;
     }
+    if (has_param<KIND>(p)) sm.K[turn ^ 1][lane] = c0 + lane < p.C ? rate_of(__ldg(p.ap + c0 + lane), p.decay) : 0.f;
 }
 
 // e = dy act(z) and the decays and intakes of a worker's tokens to shared memory.
@@ -447,20 +461,22 @@ __global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constan
     Items next(p.C, CB);
     Where w = tile_at(p, F::TT, next.tile);
     copy_tile(q, sm, 0, w, next.block * CB);
+    if (threadIdx.x < 32) look_ahead<KIND>(q, sm, 1, next.after().tile, next.block * CB);
     for (int buf = 0; next.tile < q.tiles; buf ^= 1) {
-        const int v = next.tile, c0 = next.block * CB;
-        const int rows = w.rows;
+        const int v = next.tile, c0 = next.block * CB, rows = w.rows;
         next.advance();
-        if (has_param<KIND>(p) && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
         copy_wait<0>();
         __syncthreads();
         if (next.tile < q.tiles) {
-            w = tile_at(p, F::TT, next.tile);
+            w = sm.where[buf ^ 1];
             copy_tile(q, sm, buf ^ 1, w, next.block * CB);
         }
-        if (!rows) continue;
+        if (!rows) {
+            if (threadIdx.x / 32 == 2) look_ahead<KIND>(q, sm, buf, next.after().tile, next.block * CB);
+            continue;
+        }
         float2 K[NP], x[NP], ag[NP], xg[NP], a[NP], b[NP], e[NP];
-        my.rates(sm.K, K);
+        my.rates(sm.K[buf], K);
         my.load(sm.in[buf][0], x);
         my.load(sm.in[buf][1], ag);
         my.load(sm.in[buf][2], xg);
@@ -471,7 +487,6 @@ __global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constan
             my.load(sm.in[buf][3], z);
             branch(p.act, z, e);
         }
-        if (rows < F::TT) pad(rows - 4 * my.q, a, 1.f), pad(rows - 4 * my.q, b, 0.f), pad(rows - 4 * my.q, e, 0.f);
         my.template put<F>(sm.a, a);
         my.template put<F>(sm.b, b);
         my.template put<F>(sm.e, e);
@@ -488,14 +503,16 @@ __global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constan
             }
             if (ok) q.P[own] = P, q.h[own] = h;
         } else if (threadIdx.x < 64) {
-            float g = 0.f, next = 1.f;
+            float g = 0.f, after = 1.f;
 #pragma unroll 4
             for (int u = NQ - 1; u >= 0; --u) {
                 const float4 av = sm.a[u][F::unit(u, lane)], ev = sm.e[u][F::unit(u, lane)];
-                g = __fmaf_rn(next, g, ev.w), g = __fmaf_rn(av.w, g, ev.z), g = __fmaf_rn(av.z, g, ev.y), g = __fmaf_rn(av.y, g, ev.x);
-                next = av.x;
+                g = __fmaf_rn(after, g, ev.w), g = __fmaf_rn(av.w, g, ev.z), g = __fmaf_rn(av.z, g, ev.y), g = __fmaf_rn(av.y, g, ev.x);
+                after = av.x;
             }
-            if (ok) q.g[own] = __fmul_rn(next, g);
+            if (ok) q.g[own] = __fmul_rn(after, g);
+        } else if (threadIdx.x < 96) {
+            look_ahead<KIND>(q, sm, buf, next.after().tile, next.block * CB);
         }
     }
     copy_wait<0>();
@@ -550,6 +567,7 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
     Items next(p.C, CB);  // the last tiles first: their inputs are those that the sums' kernel read last
     Where w = tile_at(p, F::TT, q.tiles - 1 - next.tile);
     copy_tile(q, sm, 0, w, next.block * CB);
+    if (warp == 0) look_ahead<KIND>(q, sm, 1, q.tiles - 1 - next.after().tile, next.block * CB);
     for (int buf = 0; next.tile < q.tiles; buf ^= 1) {
         const int v = q.tiles - 1 - next.tile, c0 = next.block * CB;
         const int rows = w.rows, t0 = w.t0;
@@ -558,37 +576,38 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
         const bool ok = c0 + lane < p.C;
         float carry = 0.f;  // what reaches the tile, in the walkers
         if (rows && warp < 2 && ok) carry = warp ? q.g[own] : q.h[own];
-        if (has_param<KIND>(p) && threadIdx.x < CB) sm.K[threadIdx.x] = ok ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
         copy_wait<0>();
         __syncthreads();
         if (next.tile < q.tiles) {
-            w = tile_at(p, F::TT, q.tiles - 1 - next.tile);
+            w = sm.where[buf ^ 1];
             copy_tile(q, sm, buf ^ 1, w, next.block * CB);
         }
         if (!rows) {
             if (q.part && threadIdx.x < CB && ok) q.part[own] = 0.f;
+            if (warp == 2) look_ahead<KIND>(q, sm, buf, q.tiles - 1 - next.after().tile, next.block * CB);
             continue;
         }
         uint4(&in)[5][F::NT] = sm.in[buf];
         float2 dx[NP], dg[NP], da1[NP], da0[NP], rest[NP], dz[NP];  // factors of the gradients
         {
-            float2 K[NP], x[NP], ag[NP], xg[NP], a[NP], m[NP], r[NP], u[NP], f[NP], k[NP], s[NP];
-            my.rates(sm.K, K);
+            float2 K[NP], x[NP], ag[NP], xg[NP], a[NP], m[NP], r[NP], k[NP], s[NP];
+            my.rates(sm.K[buf], K);
             my.load(in[1], ag);
             my.load(in[0], x);
             if (has_gate<KIND>(p)) {
                 my.load(in[2], xg);
-                two_sigmoids(ag, xg, r, dx, u, f);
+                two_sigmoids(ag, xg, r, dx, rest, dg);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) x[i] = __fmul2_rn(x[i], dx[i]);
             } else {
+                one_sigmoid(ag, r, rest);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) r[i] = sigmoid2(ag[i], u[i]), dx[i] = both(1.f), f[i] = both(0.f);
+                for (int i = 0; i < NP; ++i) dx[i] = both(1.f), dg[i] = both(0.f);
             }
-#pragma unroll
-            for (int i = 0; i < NP; ++i) rest[i] = rest2(u[i], r[i]), dg[i] = rest2(f[i], dx[i]), x[i] = __fmul2_rn(x[i], dx[i]);
             if (has_param<KIND>(p)) {
                 float2 w2[NP];
 #pragma unroll
-                for (int i = 0; i < NP; ++i) w2[i] = __fmul2_rn(K[i], r[i]), k[i] = neg(w2[i]);
+                for (int i = 0; i < NP; ++i) w2[i] = __fmul2_rn(K[i], r[i]), k[i] = __fmul2_rn(w2[i], both(-1.f));
                 decays(any_far(K), w2, a, m);
             } else {
 #pragma unroll
@@ -600,7 +619,7 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const float2 t = rest_of_square(a[i], m[i]);
-                    const float2 o = make_float2(t.x > 0.f ? rsqrt_approx(t.x) : 0.f, t.y > 0.f ? rsqrt_approx(t.y) : 0.f);
+                    const float2 o = make_float2(rsqrt_approx(fmaxf(t.x, FLT_MIN)), rsqrt_approx(fmaxf(t.y, FLT_MIN)));  // t = 0: s = 0, and k is 0 as well
                     s[i] = __fmul2_rn(t, o), da0[i] = __fmul2_rn(__fmul2_rn(da1[i], a[i]), o);
                 }
             } else if (scale_of<KIND>(p) == GDN_SCALE_LINEAR) {
@@ -614,21 +633,18 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
                 b[i] = __fmul2_rn(s[i], x[i]);
-                da0[i] = neg(__fmul2_rn(da0[i], x[i]));
+                da0[i] = __fmul2_rn(da0[i], __fmul2_rn(x[i], both(-1.f)));
                 dg[i] = __fmul2_rn(b[i], dg[i]), dx[i] = __fmul2_rn(s[i], dx[i]);
             }
             my.load(in[4], e);
             if (p.z) {
                 float2 z[NP];
                 my.load(in[3], z);
+                float2 f[NP];
+                act_slope(p.act, z, f, dz);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    float2 slope;
-                    const float2 g = act2(p.act, z[i], slope);
-                    dz[i] = __fmul2_rn(e[i], slope), e[i] = __fmul2_rn(e[i], g);
-                }
+                for (int i = 0; i < NP; ++i) dz[i] = __fmul2_rn(e[i], dz[i]), e[i] = __fmul2_rn(e[i], f[i]);
             }
-            if (rows < F::TT) pad(rows - 4 * my.q, a, 1.f), pad(rows - 4 * my.q, b, 0.f), pad(rows - 4 * my.q, e, 0.f);
             my.template put<F>(sm.a, a);
             my.template put<F>(sm.b, b);
             my.template put<F>(sm.e, e);
@@ -645,15 +661,17 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
             }
             sm.b[NQ][F::unit(NQ, lane)].x = h;
         } else if (warp == 1) {
-            float g = carry, next = 1.f;
+            float g = carry, after = 1.f;
 #pragma unroll 4
             for (int j = NQ - 1; j >= 0; --j) {
                 const float4 av = sm.a[j][F::unit(j, lane)], ev = sm.e[j][F::unit(j, lane)];
                 float4 o;
-                o.w = __fmaf_rn(next, g, ev.w), o.z = __fmaf_rn(av.w, o.w, ev.z), o.y = __fmaf_rn(av.z, o.z, ev.y), g = o.x = __fmaf_rn(av.y, o.y, ev.x);
-                next = av.x;
+                o.w = __fmaf_rn(after, g, ev.w), o.z = __fmaf_rn(av.w, o.w, ev.z), o.y = __fmaf_rn(av.z, o.z, ev.y), g = o.x = __fmaf_rn(av.y, o.y, ev.x);
+                after = av.x;
                 sm.e[j][F::unit(j, lane)] = o;
             }
+        } else if (warp == 2) {
+            look_ahead<KIND>(q, sm, buf, q.tiles - 1 - next.after().tile, next.block * CB);
         }
         __syncthreads();
         float2 g[NP], old[NP], d[NP];
@@ -676,7 +694,6 @@ __global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constan
             dx[i] = __fmul2_rn(g[i], dx[i]), dg[i] = __fmul2_rn(g[i], dg[i]);
         }
         if (q.part) {
-            if (rows < F::TT) pad(rows - 4 * my.q, d, 0.f);
 #pragma unroll
             for (int i = 0; i < NP; i += 2) total[i / 2] = __fadd2_rn(d[i], d[i + 1]);
             if constexpr (bf16) {

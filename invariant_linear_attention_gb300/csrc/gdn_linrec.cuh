@@ -43,24 +43,19 @@ __device__ __forceinline__ float2 logistic2(const float2& v, float2& e) {
     const float2 d = __fadd2_rn(e, both(1.f));
     return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
-// sigmoid(g); with rest2 1 - sigmoid(g) = e^-g sigmoid(g) with its own relative accuracy.
-__device__ __forceinline__ float2 sigmoid2(const float2& g, float2& e) { return logistic2(__fmul2_rn(g, both(-kLog2e)), e); }
-__device__ __forceinline__ float2 sigmoid2(const float2& g) {
-    float2 e;
-    return sigmoid2(g, e);
-}
-// The product is 0 times infinity for far negative g, where 1 stands for it.
-__device__ __forceinline__ float2 rest2(const float2& e, const float2& q) {
-    const float2 m = __fmul2_rn(e, q);
-    constexpr float far = 1.2676506002282294e30f;  // 2^100
-    return make_float2(e.x > far ? 1.f : m.x, e.y > far ? 1.f : m.y);
+// 1 / (1 + e) and e / (1 + e) for any e, infinity too.
+constexpr float kFar = 1.152921504606847e18f;  // 2^60
+__device__ __forceinline__ void apart(float e, float& r, float& r1) {
+    r = rcp_approx(__fadd_rn(1.f, e));
+    r1 = e > 1e36f ? 1.f : __fmul_rn(e, r);
 }
 
-// sigmoid(g) and sigmoid(i) with one reciprocal for both, 1 / ((1 + 2^v) (1 + 2^u)): the special function unit, which
+// sigmoid(g) = r and sigmoid(i) = p with one reciprocal for both, 1 / ((1 + 2^v) (1 + 2^u)): the special function unit, which
 // takes two cycles a warp for a reciprocal or a root and one for an exponential, bounds the prompts' kernel next to HBM.
-// e, f: 2^v, 2^u.  Where a power is past 2^60 and their product might leave fp32's range, each has its own.
+// r1, p1: 1 - r and 1 - p.  Where a power is past 2^60 and their product might leave fp32's range, each has its own.
 template <int NP>
-__device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2 (&i)[NP], float2 (&r)[NP], float2 (&p)[NP], float2 (&e)[NP], float2 (&f)[NP]) {
+__device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2 (&i)[NP], float2 (&r)[NP], float2 (&p)[NP], float2 (&r1)[NP], float2 (&p1)[NP]) {
+    float2 e[NP], f[NP];
     float most = 0.f;
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
@@ -73,13 +68,32 @@ __device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2
         const float2 d = __fadd2_rn(e[k], both(1.f)), c = __fadd2_rn(f[k], both(1.f)), D = __fmul2_rn(d, c);
         const float2 R = make_float2(rcp_approx(D.x), rcp_approx(D.y));
         r[k] = __fmul2_rn(R, c), p[k] = __fmul2_rn(R, d);
+        r1[k] = __fmul2_rn(e[k], r[k]), p1[k] = __fmul2_rn(f[k], p[k]);
     }
     if (most > 60.f) {
-        constexpr float far = 1.152921504606847e18f;  // 2^60
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            if (fmaxf(e[k].x, f[k].x) > far) r[k].x = rcp_approx(1.f + e[k].x), p[k].x = rcp_approx(1.f + f[k].x);
-            if (fmaxf(e[k].y, f[k].y) > far) r[k].y = rcp_approx(1.f + e[k].y), p[k].y = rcp_approx(1.f + f[k].y);
+            if (fmaxf(e[k].x, f[k].x) > kFar) apart(e[k].x, r[k].x, r1[k].x), apart(f[k].x, p[k].x, p1[k].x);
+            if (fmaxf(e[k].y, f[k].y) > kFar) apart(e[k].y, r[k].y, r1[k].y), apart(f[k].y, p[k].y, p1[k].y);
+        }
+    }
+}
+// sigmoid(g) = r alone, and 1 - r.
+template <int NP>
+__device__ __forceinline__ void one_sigmoid(const float2 (&g)[NP], float2 (&r)[NP], float2 (&r1)[NP]) {
+    float2 e[NP];
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const float2 v = __fmul2_rn(g[k], both(-kLog2e));
+        most = fmaxf(most, fmaxf(v.x, v.y));
+        r[k] = logistic2(v, e[k]), r1[k] = __fmul2_rn(e[k], r[k]);
+    }
+    if (most > 60.f) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            if (e[k].x > kFar) apart(e[k].x, r[k].x, r1[k].x);
+            if (e[k].y > kFar) apart(e[k].y, r[k].y, r1[k].y);
         }
     }
 }
@@ -119,15 +133,34 @@ __device__ __forceinline__ float2 inner2(int act, const float2& z) {
     if (act != GDN_ACT_GELU) return __fmul2_rn(z, both(-kLog2e));
     return __fmul2_rn(z, __ffma2_rn(__fmul2_rn(z, z), both(-kLog2e * kGelu3), both(-kLog2e * kGelu1)));
 }
-// act(z) and its slope p + z p (1 - p) inner'(z).
-__device__ __forceinline__ float2 act2(int act, const float2& z, float2& slope) {
-    float2 e;
-    const float2 p = logistic2(inner2(act, z), e), r = rest2(e, p), f = __fmul2_rn(z, p);
-    float2 g = __fmul2_rn(f, r);
-    if (act == GDN_ACT_GELU) g = __fmul2_rn(g, __ffma2_rn(__fmul2_rn(z, z), both(3.f * kGelu3), both(kGelu1)));
-    // r is 0 far enough out; where z^2 is past fp32 its product is not
-    slope = make_float2(r.x == 0.f || p.x == 0.f ? p.x : __fadd_rn(p.x, g.x), r.y == 0.f || p.y == 0.f ? p.y : __fadd_rn(p.y, g.y));
-    return f;
+// f = act(z) and its slope p + z p (1 - p) i'(z), where p and 1 - p have their own relative accuracy; far out, where
+// these products leave fp32's range, the slope is 0 or 1.
+template <int NP>
+__device__ __forceinline__ void act_slope(int act, const float2 (&z)[NP], float2 (&f)[NP], float2 (&slope)[NP]) {
+    float2 v[NP];
+    float most = 0.f;
+    if (act == GDN_ACT_GELU) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) v[k] = inner2(GDN_ACT_GELU, z[k]), slope[k] = __ffma2_rn(__fmul2_rn(z[k], z[k]), both(3.f * kGelu3), both(kGelu1));
+    } else {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) v[k] = inner2(GDN_ACT_SILU, z[k]), slope[k] = both(1.f);
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        most = fmaxf(most, fmaxf(fabsf(v[k].x), fabsf(v[k].y)));
+        float2 e;
+        const float2 p = logistic2(v[k], e);
+        f[k] = __fmul2_rn(z[k], p);
+        slope[k] = __ffma2_rn(__fmul2_rn(f[k], __fmul2_rn(e, p)), slope[k], p);
+    }
+    if (most > 120.f) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            if (fabsf(v[k].x) > 120.f) slope[k].x = v[k].x > 0.f ? 0.f : 1.f;
+            if (fabsf(v[k].y) > 120.f) slope[k].y = v[k].y > 0.f ? 0.f : 1.f;
+        }
+    }
 }
 
 struct Params {
@@ -175,15 +208,16 @@ __device__ __forceinline__ bool any_far(const float2 (&K)[NP]) {
 template <Kind KIND, int NP>
 __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&K)[NP], const float2 (&ag)[NP], const float2 (&xg)[NP],
                                       const float2 (&x)[NP], float2 (&a)[NP], float2 (&b)[NP]) {
-    float2 m[NP], r[NP], u[NP];
+    float2 m[NP], r[NP], r1[NP];
     if (has_gate<KIND>(p)) {
-        float2 f[NP];
-        two_sigmoids(ag, xg, r, b, u, f);
+        float2 p1[NP];
+        two_sigmoids(ag, xg, r, b, r1, p1);
 #pragma unroll
         for (int e = 0; e < NP; ++e) b[e] = __fmul2_rn(x[e], b[e]);
     } else {
+        one_sigmoid(ag, r, r1);
 #pragma unroll
-        for (int e = 0; e < NP; ++e) r[e] = sigmoid2(ag[e], u[e]), b[e] = x[e];
+        for (int e = 0; e < NP; ++e) b[e] = x[e];
     }
     if (has_param<KIND>(p)) {
         float2 w[NP];
@@ -192,7 +226,7 @@ __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&
         decays(far, w, a, m);
     } else {
 #pragma unroll
-        for (int e = 0; e < NP; ++e) a[e] = r[e], m[e] = rest2(u[e], r[e]);
+        for (int e = 0; e < NP; ++e) a[e] = r[e], m[e] = r1[e];
     }
     if (scale_of<KIND>(p) == GDN_SCALE_SQRT) {
 #pragma unroll
