@@ -365,7 +365,11 @@ struct Where {
 };
 template <typename T>
 struct GradTile {
-    static constexpr int CB = 32, VN = V16<T>::n, CH = CB / VN, NT = 256, TT = NT / CH, NQ = TT / 4;
+    static constexpr int CB = 32, VN = V16<T>::n, CH = CB / VN, NT = VN == 8 ? 128 : 256, TT = NT / CH, NQ = TT / 4;
+    // CTAs an SM of the two kernels.  Smaller CTAs walk while others compute (8 documents, 16384 x 4096, bf16: 483 us, with 256
+    // threads and 3 and 2 CTAs 535); fewer registers spill (5 CTAs: 560).  fp32 holds half the values a thread: 267 us for 16384 x
+    // 2048 so, 307 with bf16's numbers.
+    static constexpr int SUM = VN == 8 ? 6 : 4, GRAD = VN == 8 ? 4 : 3;
     float4 a[NQ][CB], b[NQ + 1][CB], e[NQ][CB];  // units as in FwdTile; b gets the states before each token, and the last one behind them, e the G
     uint4 in[2][5][NT];                          // x, a_gate, x_gate, z, dy of this tile and the next one; then the gradients on their way to rows
     float K[2][CB];     // of this item and the next one
@@ -449,7 +453,7 @@ __device__ __forceinline__ void look_ahead(const GradParams& q, F& sm, int turn,
 
 // e = dy act(z) and the decays and intakes of a worker's tokens to shared memory.
 template <typename T, Kind KIND>
-__global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constant__ GradParams q) {
+__global__ void __launch_bounds__(GradTile<T>::NT, GradTile<T>::SUM) linrec_sum_kernel(const __grid_constant__ GradParams q) {
     using F = GradTile<T>;
     using Q = Share<T, F::CB>;
     constexpr int NP = Q::NP, CB = F::CB, NQ = F::NQ;
@@ -518,43 +522,53 @@ __global__ void __launch_bounds__(256, 3) linrec_sum_kernel(const __grid_constan
     copy_wait<0>();
 }
 
-// A thread one channel of one sequence, in one direction (blockIdx.y): each tile's sum is replaced by what reaches the tile.
-__global__ void __launch_bounds__(128) linrec_join_kernel(const __grid_constant__ GradParams q, int TT) {
+// A CTA 32 channels of one sequence, in one direction (blockIdx.y): each tile's sum is replaced by what reaches the tile.  Its
+// warps take an eighth of the tiles each, first from 0 and then from what the eighths before them leave.
+__global__ void __launch_bounds__(256) linrec_join_kernel(const __grid_constant__ GradParams q, int TT) {
+    __shared__ float Ps[8][32], vs[8][32];
     const Params& p = q.p;
-    const int blocks = (p.C + 127) / 128, c = blockIdx.x % blocks * 128 + threadIdx.x, n = blockIdx.x / blocks;
-    if (c >= p.C) return;
+    const int blocks = (p.C + 31) / 32, lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x % blocks * 32 + lane, n = blockIdx.x / blocks;
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
-    const int tiles = (eos - bos + TT - 1) / TT;
-    const int64_t own = (int64_t)n * p.C + c, first = (int64_t)(bos / TT + n) * p.C + c, C = p.C;
-    const bool back = blockIdx.y;
+    const int tiles = (eos - bos + TT - 1) / TT, each = (tiles + 7) / 8, lo = min(warp * each, tiles), count = min(each, tiles - lo);
+    const bool back = blockIdx.y, ok = c < p.C;
+    const int64_t own = (int64_t)n * p.C + c, step = back ? -(int64_t)p.C : p.C;
+    const int64_t at = (int64_t)(bos / TT + n + (back ? tiles - 1 - lo : lo)) * p.C + c;
+    float* sum = (back ? q.g : q.h) + at;
+    const float* P = q.P + at;
+    constexpr int U = 8;
+    float ps[U], ss[U];
+    auto load = [&](int i) {  // tiles i .. of its eighth; behind its end: pass on
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const bool has = ok && i + k < count;
+            ps[k] = has ? P[(i + k) * step] : 1.f, ss[k] = has ? sum[(i + k) * step] : 0.f;
+        }
+    };
+    float v = 0.f, all = 1.f;
+    for (int i = 0; i < count; i += U) {
+        load(i);
+#pragma unroll
+        for (int k = 0; k < U; ++k) v = __fmaf_rn(ps[k], v, ss[k]), all = __fmul_rn(all, ps[k]);
+    }
+    Ps[warp][lane] = all, vs[warp][lane] = v;
+    __syncthreads();
     const float* from = back ? q.dhT : q.h0;
-    float v = from ? from[own] : 0.f;
-    float* sum = (back ? q.g : q.h) + first + (back && tiles ? (int64_t)(tiles - 1) * C : 0);
-    const float* P = q.P + (sum - (back ? q.g : q.h));
-    const int64_t step = back ? -C : C;
-    int i = 0;
-    for (; i + 8 <= tiles; i += 8) {
-        float ps[8], ss[8];
+    v = from && ok ? from[own] : 0.f;
+    for (int i = 0; i < warp; ++i) v = __fmaf_rn(Ps[i][lane], v, vs[i][lane]);
+    for (int i = 0; i < count; i += U) {
+        if (count > U) load(i);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) ps[k] = P[k * step], ss[k] = sum[k * step];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            sum[k * step] = v;
+        for (int k = 0; k < U; ++k) {
+            if (ok && i + k < count) sum[(i + k) * step] = v;
             v = __fmaf_rn(ps[k], v, ss[k]);
         }
-        P += 8 * step, sum += 8 * step;
     }
-    for (; i < tiles; ++i, P += step, sum += step) {
-        const float ps = *P, ss = *sum;
-        *sum = v;
-        v = __fmaf_rn(ps, v, ss);
-    }
-    if (back && q.dh0) q.dh0[own] = v;
+    if (warp == 7 && back && q.dh0 && ok) q.dh0[own] = v;
 }
 
 template <typename T, Kind KIND>
-__global__ void __launch_bounds__(256, 2) linrec_bwd_kernel(const __grid_constant__ GradParams q) {
+__global__ void __launch_bounds__(GradTile<T>::NT, GradTile<T>::GRAD) linrec_bwd_kernel(const __grid_constant__ GradParams q) {
     using F = GradTile<T>;
     using Q = Share<T, F::CB>;
     constexpr int NP = Q::NP, CB = F::CB, NQ = F::NQ;
@@ -796,14 +810,14 @@ gdn_status launch_bwd(cudaStream_t s, const GradParams& q) {
     const int64_t items = (int64_t)q.tiles * ((p.C + F::CB - 1) / F::CB);
     auto ctas = [&](int each) { return (unsigned)(items < kSMs * each ? items : kSMs * each); };
     if (p.T > 0) {
-        sum<<<ctas(3), F::NT, sizeof(F), s>>>(q);
+        sum<<<ctas(F::SUM), F::NT, sizeof(F), s>>>(q);
         const gdn_status st = launch_status();
         if (st != GDN_OK) return st;
     }
-    linrec_join_kernel<<<dim3((unsigned)((p.C + 127) / 128) * (unsigned)p.N, 2), 128, 0, s>>>(q, F::TT);
+    linrec_join_kernel<<<dim3((unsigned)((p.C + 31) / 32) * (unsigned)p.N, 2), 256, 0, s>>>(q, F::TT);
     gdn_status st = launch_status();
     if (st != GDN_OK || p.T == 0) return st;
-    bwd<<<ctas(2), F::NT, sizeof(F), s>>>(q);
+    bwd<<<ctas(F::GRAD), F::NT, sizeof(F), s>>>(q);
     return launch_status();
 }
 
