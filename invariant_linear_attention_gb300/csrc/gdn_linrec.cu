@@ -11,6 +11,9 @@ namespace {
 
 using namespace linrec;
 
+#ifndef LR_RANK
+#define LR_RANK 1
+#endif
 #ifndef LR_WORK
 #define LR_WORK 256
 #endif
@@ -46,15 +49,6 @@ struct FwdTile {
     static_assert(kGroup + (GROUP > 32 ? WORK / GROUP : 0) <= 16, "barriers of a CTA");
 };
 
-// Shared memory in the order written: the compiler moves neither across the other.
-__device__ __forceinline__ float4 ld_shared4(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_shared4(uint32_t at, const float4& v) {
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 
@@ -148,13 +142,35 @@ struct Share<float, CB> {
     }
 };
 
+// The sequence of rank `rank` by length, the longest first (ties by number), so that the longest walks do not start last.
+// A CTA's N^2 comparisons have to be few against its walk of T / N tokens: up to N^3 = 256 T, as for the selective scan.
+constexpr int kRanked = 256;
+__device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
+    __shared__ int lens[kRanked], found;
+    for (int i = threadIdx.x; i < p.N; i += threads) {
+        int bos, eos;
+        bounds(p.cu, i, p.T, bos, eos);
+        lens[i] = eos - bos;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.N; i += threads) {
+        const int mine = lens[i];
+        int before = 0;
+        for (int k = 0; k < p.N; ++k) before += lens[k] > mine || (lens[k] == mine && k < i);
+        if (before == rank) found = i;
+    }
+    __syncthreads();
+    return found;
+}
+
 template <typename T, typename F, int CB, int CTAS, Kind KIND>
 __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_constant__ Params p) {
     using Q = Share<T, CB>;
     constexpr int VN = F::VN, NP = Q::NP, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST;
     extern __shared__ __align__(128) unsigned char raw[];
     F& sm = *reinterpret_cast<F*>(raw);
-    const int blocks = (p.C + CB - 1) / CB, n = blockIdx.x / blocks, c0 = blockIdx.x % blocks * CB;
+    const int blocks = (p.C + CB - 1) / CB, order = blockIdx.x / blocks, c0 = blockIdx.x % blocks * CB;
+    const int n = p.ranked ? ranked(p, order, F::NT) : order;
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
     const int len = eos - bos, tiles = (len + TT - 1) / TT;
@@ -247,50 +263,54 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
     const bool has_slot = c < p.C && slot >= 0 && slot < p.num_slots;
     float* st = p.state + (int64_t)slot * p.C + c;
     float h = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0) ? *st : 0.f;
-    uint32_t at[4];  // of units 0 to 3, in a row of a buffer
-#pragma unroll
-    for (int k = 0; k < 4; ++k) at[k] = 16u * (uint32_t)(k * CB + F::unit(k, cl));
     for (int i = 0, buf = 0; i < tiles; ++i) {
         const int here = min(TT, len - i * TT);
-        const uint32_t a = smem_u32(sm.a[buf]), b = smem_u32(sm.b[buf]);
         bar_sync(F::kFull + buf, F::NT);
-        constexpr int U = 4;  // units walked while the next ones' loads are under way; at the end those read on into what follows, unused
-        constexpr uint32_t step = CB * 16;
+        // S sets of V units in registers: while one is walked, the loads of the others are under way (at the end they read on
+        // into what follows, unused).
+        constexpr int S = 2, V = 4;
         const int units = here / 4;
+        float4 (*pa)[CB] = sm.a[buf], (*pb)[CB] = sm.b[buf];
         int u = 0;
-        auto walk4 = [&](const float4& av, const float4& bv, uint32_t to) {
+        auto walk4 = [&](const float4& av, const float4& bv) {
             float4 o;
             h = o.x = __fmaf_rn(av.x, h, bv.x), h = o.y = __fmaf_rn(av.y, h, bv.y), h = o.z = __fmaf_rn(av.z, h, bv.z), h = o.w = __fmaf_rn(av.w, h, bv.w);
-            st_shared4(to, o);
+            return o;
         };
-        if (units >= 2 * U) {
-            float4 ak[U], bk[U], an[U], bn[U];
-            auto load = [&](int from, float4(&av)[U], float4(&bv)[U]) {
+        if (units >= S * V) {
+            const float4* ra[4];  // units 0 to 3, and every fourth from there
+            float4* rb[4];
 #pragma unroll
-                for (int k = 0; k < U; ++k) av[k] = ld_shared4(a + from * step + at[k]), bv[k] = ld_shared4(b + from * step + at[k]);
+            for (int k = 0; k < 4; ++k) ra[k] = &pa[0][F::unit(k, cl)], rb[k] = &pb[0][F::unit(k, cl)];
+            float4 ak[S][V], bk[S][V];
+            auto load = [&](int unit, int set) {  // from this turn's first unit on
+#pragma unroll
+                for (int k = 0; k < V; ++k) ak[set][k] = ra[(unit + k) & 3][(unit + k) * CB], bk[set][k] = rb[(unit + k) & 3][(unit + k) * CB];
             };
-            load(0, ak, bk);
-            for (; u + 2 * U <= units; u += 2 * U) {
-                load(u + U, an, bn);
 #pragma unroll
-                for (int k = 0; k < U; ++k) walk4(ak[k], bk[k], b + u * step + at[k]);
-                load(u + 2 * U, ak, bk);
+            for (int j = 0; j < S - 1; ++j) load(j * V, j);
+            for (; u + S * V <= units; u += S * V) {
 #pragma unroll
-                for (int k = 0; k < U; ++k) walk4(an[k], bn[k], b + (u + U) * step + at[k]);
+                for (int j = 0; j < S; ++j) {
+                    load((j + S - 1) * V, (j + S - 1) % S);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) rb[(j * V + k) & 3][(j * V + k) * CB] = walk4(ak[j][k], bk[j][k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ra[k] += S * V * CB, rb[k] += S * V * CB;
             }
         }
         for (; 4 * u < here; ++u) {
-            const uint32_t to = 16u * (uint32_t)(u * CB + F::unit(u, cl));
-            const float4 av = ld_shared4(a + to), bv = ld_shared4(b + to);
+            const float4 av = pa[u][F::unit(u, cl)], bv = pb[u][F::unit(u, cl)];
             if (u < units) {
-                walk4(av, bv, b + to);
+                pb[u][F::unit(u, cl)] = walk4(av, bv);
             } else {
                 const float af[3] = {av.x, av.y, av.z}, bf[3] = {bv.x, bv.y, bv.z};
                 float o[3] = {0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < 3; ++k)
                     if (4 * u + k < here) h = o[k] = __fmaf_rn(af[k], h, bf[k]);
-                st_shared4(b + to, make_float4(o[0], o[1], o[2], 0.f));
+                pb[u][F::unit(u, cl)] = make_float4(o[0], o[1], o[2], 0.f);
             }
         }
         bar_arrive(F::kDone + buf, F::NT);
@@ -786,7 +806,10 @@ gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     const Kind kind = kind_of(p);
     auto* kernel = kind == kBothGates ? linrec_fwd_kernel<T, F, CB, CTAS, kBothGates> : kind == kForget ? linrec_fwd_kernel<T, F, CB, CTAS, kForget> : linrec_fwd_kernel<T, F, CB, CTAS, kAny>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
-    kernel<<<(unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N, F::NT, sizeof(F), s>>>(p);
+    const unsigned ctas = (unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N;
+    Params q = p;
+    q.ranked = LR_RANK && p.N > 1 && p.N <= kRanked && ctas > (unsigned)(kSMs * CTAS) && (long long)p.N * p.N * p.N <= 256LL * p.T;
+    kernel<<<ctas, F::NT, sizeof(F), s>>>(q);
     return launch_status();
 }
 template <typename T>

@@ -176,6 +176,7 @@ struct Params {
     int num_slots;
     const int32_t* has_init;
     void* y;
+    int ranked;  // prompts: take the sequences in order of length
 };
 
 // Which of a call's options a kernel knows at compile time.  With all of them as branches, the values that meet
