@@ -11,18 +11,6 @@ namespace {
 
 using namespace linrec;
 
-#ifndef LR_RANK
-#define LR_RANK 1
-#endif
-#ifndef LR_WORK
-#define LR_WORK 256
-#endif
-#ifndef LR_AHEAD
-#define LR_AHEAD 2
-#endif
-#ifndef LR_MINB
-#define LR_MINB 2
-#endif
 // Prompts.  A CTA walks one sequence over CB channels in tiles of TT tokens.  Nearly all the work of a token does not
 // depend on the one before it: only h <- a h + b does, 5 cycles a token.  So
 //   * the workers, each four tokens of two channels (fp32: of one), in step i finish tile i - NB (gate, stores of y) and prepare
@@ -31,10 +19,10 @@ using namespace linrec;
 // A worker reads the h of the very places that it then writes, so it meets nobody but the walkers, NB tiles behind or ahead:
 // at named barriers full (a tile prepared) and done (it is walked), one of each per buffer, which every side passes once a
 // tile.  The inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead, for a group of workers that copies what it reads.
-template <typename T, int CB, int WORKERS, int TILES>
+template <typename T, int CB, int WORKERS>
 struct FwdTile {
     static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = WORKERS, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
-    static constexpr int AHEAD = TILES, ST = AHEAD + 1, NB = 3;
+    static constexpr int AHEAD = 2, ST = AHEAD + 1, NB = 3;
     static constexpr int GROUP = VN == 8 && CB == 32 ? 64 : 32;     // threads that copy for one another
     static constexpr int kFull = 1, kDone = kFull + NB, kGroup = kDone + NB;  // barriers
     // Four tokens of a channel are 16 bytes, the walker's unit (with 4-byte loads its three a token took 14 cycles, not 5).
@@ -791,31 +779,29 @@ __global__ void __launch_bounds__(256) linrec_param_kernel(int tiles, int C, flo
     out[c] = K > 0.f ? s * (decay * sp / K) : 0.f;
 }
 
-#ifndef LR_CB
-#define LR_CB 0
-#endif
-#ifndef LR_WORK2
-#define LR_WORK2 512
-#endif
-#ifndef LR_AHEAD2
-#define LR_AHEAD2 2
-#endif
-template <typename T, int CB, int WORKERS, int TILES, int CTAS>
+template <typename T, int CB, int WORKERS, int CTAS>
 gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
-    using F = FwdTile<T, CB, WORKERS, TILES>;
+    using F = FwdTile<T, CB, WORKERS>;
     const Kind kind = kind_of(p);
     auto* kernel = kind == kBothGates ? linrec_fwd_kernel<T, F, CB, CTAS, kBothGates> : kind == kForget ? linrec_fwd_kernel<T, F, CB, CTAS, kForget> : linrec_fwd_kernel<T, F, CB, CTAS, kAny>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
     const unsigned ctas = (unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N;
     Params q = p;
-    q.ranked = LR_RANK && p.N > 1 && p.N <= kRanked && ctas > (unsigned)(kSMs * CTAS) && (long long)p.N * p.N * p.N <= 256LL * p.T;
+    q.ranked = p.N > 1 && p.N <= kRanked && ctas > (unsigned)(kSMs * CTAS) && (long long)p.N * p.N * p.N <= 256LL * p.T;
     kernel<<<ctas, F::NT, sizeof(F), s>>>(q);
     return launch_status();
 }
+// Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16, 6.4 ns with 16 channels and 512 workers, 10 ns with 32
+// and 512, 12 ns with 32 and 256, and 20 ns each of two of the last kind on one SM; a batch of several sequences ends with its longest alone.
+// us with the three forms: 1 x 16384 x 1024 114, 186, 218; 3 ragged, 16000 x 1600 (n = 150) 91, 109, 124; 1 x 16384 x 4096 (128)
+// 228, 187, 217; 2, 8000 x 2560 (160) 85, 77, 83; 4, 8192 x 2048 (256) 67, 56, 69; 1 x 16384 x 8192 (256) 454, 371, 331;
+// 16, 32768 x 4096 (2048) 460, 350, 283.  fp32 the same way.
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
-    if (LR_CB == 16 || (LR_CB == 0 && (long long)((p.C + 31) / 32) * p.N <= kSMs / 2)) return launch_fwd_of<T, 16, LR_WORK2, LR_AHEAD2, 1>(s, p);
-    return launch_fwd_of<T, 32, LR_WORK, LR_AHEAD, LR_MINB>(s, p);
+    const long long n = (long long)((p.C + 31) / 32) * p.N;
+    if (n <= kSMs / 2 || (p.N > 1 && n <= kSMs)) return launch_fwd_of<T, 16, 512, 1>(s, p);
+    if (n <= kSMs + kSMs / 8 || (p.N >= 4 && n <= 2 * kSMs + kSMs / 8)) return launch_fwd_of<T, 32, 512, 1>(s, p);
+    return launch_fwd_of<T, 32, 256, 2>(s, p);
 }
 
 int64_t grad_tiles(int T, int N, int dtype) { return (int64_t)T / (dtype == GDN_BF16 ? GradTile<__nv_bfloat16>::TT : GradTile<float>::TT) + N; }
