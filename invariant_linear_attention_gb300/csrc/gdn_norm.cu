@@ -62,28 +62,18 @@ __device__ __forceinline__ void over_row(float (&v)[N], int tpr, float (&buf)[N]
     }
 }
 
-template <typename T>
-__device__ __forceinline__ T rounded(float v);
-template <>
-__device__ __forceinline__ float rounded<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-
 __device__ __forceinline__ void load_weight(const float* w, float (&v)[8]) {
     unpack(ld16(w), reinterpret_cast<float(&)[4]>(v[0]));
     unpack(ld16(w + 4), reinterpret_cast<float(&)[4]>(v[4]));
 }
 __device__ __forceinline__ void load_weight(const float* w, float (&v)[4]) { unpack(ld16(w), v); }
 
-__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t fp8x4(const float2& a, const float2& b) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3), hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
 }
-__device__ __forceinline__ void store_fp8(uint8_t* to, const float (&v)[8]) {
-    *reinterpret_cast<uint2*>(to) = make_uint2(fp8x4(v[0], v[1], v[2], v[3]), fp8x4(v[4], v[5], v[6], v[7]));
-}
-__device__ __forceinline__ void store_fp8(uint8_t* to, const float (&v)[4]) { *reinterpret_cast<uint32_t*>(to) = fp8x4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void store_fp8(uint8_t* to, const float2 (&v)[4]) { *reinterpret_cast<uint2*>(to) = make_uint2(fp8x4(v[0], v[1]), fp8x4(v[2], v[3])); }
+__device__ __forceinline__ void store_fp8(uint8_t* to, const float2 (&v)[2]) { *reinterpret_cast<uint32_t*>(to) = fp8x4(v[0], v[1]); }
 
 constexpr float kTop = 448.f, kLeast = 1.17549435e-38f;  // e4m3's largest value; the smallest scale, 2^-126
 
@@ -93,14 +83,14 @@ constexpr float kTop = 448.f, kLeast = 1.17549435e-38f;  // e4m3's largest value
 struct Scale {
     float scale, by;
     bool tiny;
-    template <int VN>
-    __device__ __forceinline__ void apply(float (&v)[VN], float r) const {
+    template <int NP>
+    __device__ __forceinline__ void apply(float2 (&v)[NP], float r) const {
         if (tiny) {
 #pragma unroll
-            for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(v[e], r);
+            for (int e = 0; e < NP; ++e) v[e] = __fmul2_rn(v[e], make_float2(r, r));
         }
 #pragma unroll
-        for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(v[e], by);
+        for (int e = 0; e < NP; ++e) v[e] = __fmul2_rn(v[e], make_float2(by, by));
     }
 };
 __device__ __forceinline__ Scale scale_of(float most, float r) {
@@ -113,115 +103,152 @@ __device__ __forceinline__ Scale scale_of(float most, float r) {
     return s;
 }
 
+// A chunk's values as packed pairs, and back.
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[4]) {
+    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
+    v[2] = make_float2(bf_lo(u.z), bf_hi(u.z)), v[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
+}
+__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
+    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ uint4 pack2(const float2 (&v)[4]) {
+    return make_uint4(bf_pack(v[0].x, v[0].y), bf_pack(v[1].x, v[1].y), bf_pack(v[2].x, v[2].y), bf_pack(v[3].x, v[3].y));
+}
+__device__ __forceinline__ uint4 pack2(const float2 (&v)[2]) {
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+}
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
+
 // A CTA takes rows blockIdx.x, + gridDim.x, ..  Up to two chunks a thread (NC), it keeps its weights in registers and
-// has the next row's loads under way while a row is summed and stored.  A row waits packed, as it is stored.
+// has the next row's loads under way while a row is summed and stored.  A row waits packed, as it is stored.  Its places
+// in memory are pointers that go on by a fixed step: with addresses from the row's number the 8-bit form spent half of its
+// instructions on them.
 template <typename T, int NC, int NT, bool FP8>
 __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 ? 2 : 1) add_norm_kernel(const __grid_constant__ NormParams p) {
-    constexpr int VN = V16<T>::n;
+    constexpr int VN = V16<T>::n, NP = VN / 2;
     constexpr bool ahead = NC <= 2;
     __shared__ float buf[2][1][32], buf2[2][1][32];
     const int lane = threadIdx.x % p.tpr, per = NT / p.tpr;
     const bool res = p.res != nullptr;
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    const int64_t step = (int64_t)gridDim.x * per;
+    int64_t first = (int64_t)blockIdx.x * per, row = first + threadIdx.x / p.tpr;
+    const int far = p.tpr * VN;  // from one of a thread's chunks to the next
+    bool in[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) in[i] = lane + i * p.tpr < p.chunks;
+    const T* px = static_cast<const T*>(p.x) + row * p.ldx + lane * VN;
+    const T* pr = res ? static_cast<const T*>(p.res) + row * p.ldr + lane * VN : nullptr;
+    T* po = res ? static_cast<T*>(p.res_out) + row * p.d + lane * VN : nullptr;
+    T* py = static_cast<T*>(p.y) + (FP8 ? 0 : row * p.d + lane * VN);
+    uint8_t* pq = static_cast<uint8_t*>(p.y) + (FP8 ? row * p.d + lane * VN : 0);
+    const int64_t sx = step * p.ldx, sr = step * p.ldr, sd = step * p.d;
     uint4 a[NC], b[NC];
-    auto load = [&](int64_t row) {
+    auto load = [&](bool live) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            const bool has = row < p.rows && c < p.chunks;
-            a[i] = has ? ld16_stream(static_cast<const T*>(p.x) + row * p.ldx + c * VN) : none;
-            b[i] = has && res ? ld16_stream(static_cast<const T*>(p.res) + row * p.ldr + c * VN) : none;
+            a[i] = live && in[i] ? ld16_stream(px + i * far) : none;
+            b[i] = live && in[i] && res ? ld16_stream(pr + i * far) : none;
         }
     };
-    float wk[ahead ? NC : 1][VN];
-    auto weight = [&](int i, float (&w)[VN]) {
-        if (lane + i * p.tpr < p.chunks) load_weight(p.w + (lane + i * p.tpr) * VN, w);
+    float2 wk[ahead ? NC : 1][NP];
+    auto weight = [&](int i, float2 (&w)[NP]) {
+        if (!in[i]) return;
+#pragma unroll
+        for (int e = 0; e < NP; e += 2) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p.w + (lane + i * p.tpr) * VN + 2 * e));
+            w[e] = make_float2(v.x, v.y), w[e + 1] = make_float2(v.z, v.w);
+        }
     };
-    auto values = [&](int i, const uint4& s, float (&v)[VN]) {  // s w
-        unpack(s, v);
+    auto values = [&](int i, const uint4& s, float2 (&v)[NP]) {  // s w
+        unpack2(s, v);
         if constexpr (!ahead) weight(i, wk[0]);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(v[e], wk[ahead ? i : 0][e]);
+        for (int e = 0; e < NP; ++e) v[e] = __fmul2_rn(v[e], wk[ahead ? i : 0][e]);
+    };
+    auto largest = [&](const float2 (&v)[NP]) {
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < NP; ++e) m = fmaxf(m, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
+        return m;
     };
     if constexpr (ahead) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) weight(i, wk[i]);
     }
-    const int64_t step = (int64_t)gridDim.x * per;
-    int64_t first = (int64_t)blockIdx.x * per;
-    load(first + threadIdx.x / p.tpr);
+    load(row < p.rows);
     for (int turn = 0; first < p.rows; first += step, turn ^= 1) {
-        const int64_t row = first + threadIdx.x / p.tpr;
+        const bool live = row < p.rows;
         uint4 s[NC];
-        float ss[1] = {0.f};
+        float2 s2 = twice(0.f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            float v[VN];
+            float2 v[NP];
             s[i] = a[i];
-            unpack(a[i], v);
+            unpack2(a[i], v);
             if (res) {
-                float add[VN];
-                unpack(b[i], add);
+                float2 add[NP];
+                unpack2(b[i], add);
 #pragma unroll
-                for (int e = 0; e < VN; ++e) v[e] = __fadd_rn(v[e], add[e]);
-                s[i] = pack(v);
-                unpack(s[i], v);
-                if (row < p.rows && c < p.chunks) st16_stream(static_cast<T*>(p.res_out) + row * p.d + c * VN, s[i]);
+                for (int e = 0; e < NP; ++e) v[e] = __fadd2_rn(v[e], add[e]);
+                s[i] = pack2(v);
+                unpack2(s[i], v);
+                if (live && in[i]) st16_stream(po + i * far, s[i]);
             }
 #pragma unroll
-            for (int e = 0; e < VN; ++e) ss[0] = __fmaf_rn(v[e], v[e], ss[0]);
+            for (int e = 0; e < NP; ++e) s2 = __ffma2_rn(v[e], v[e], s2);
         }
-        load(row + step);
+        px += sx, pr += sr, po += sd;
+        load(row + step < p.rows);
+        float ss[1] = {__fadd_rn(s2.x, s2.y)};
         over_row<Sum>(ss, p.tpr, buf[turn]);
         const float r = rsqrtf(__fmaf_rn(ss[0], p.c, p.eps));
-        float most[1] = {0.f};
-        if constexpr (FP8) {
-            if (!p.glanes) {
+        if constexpr (!FP8) {
 #pragma unroll
-                for (int i = 0; i < NC; ++i) {
-                    if (lane + i * p.tpr >= p.chunks) continue;
-                    float v[VN];
-                    values(i, s[i], v);
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) most[0] = fmaxf(most[0], fabsf(v[e]));
-                }
-                over_row<Max>(most, p.tpr, buf2[turn]);
-            }
-        }
-        [[maybe_unused]] Scale whole;
-        if constexpr (FP8) {
-            if (!p.glanes) {
-                whole = scale_of(most[0], r);
-                if (row < p.rows && lane == 0) p.scales[row] = whole.scale;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-            const int c = lane + i * p.tpr;
-            const bool has = row < p.rows && c < p.chunks;
-            float v[VN];
-            if constexpr (!FP8) {
-                unpack(s[i], v);
+            for (int i = 0; i < NC; ++i) {
+                float2 v[NP];
+                unpack2(s[i], v);
                 if constexpr (!ahead) weight(i, wk[0]);
 #pragma unroll
-                for (int e = 0; e < VN; ++e) v[e] = __fmul_rn(__fmul_rn(v[e], r), wk[ahead ? i : 0][e]);
-                if (has) st16_stream(static_cast<T*>(p.y) + row * p.d + c * VN, pack(v));
-            } else {
-                values(i, s[i], v);
-                if (!p.glanes) {
-                    whole.apply(v, r);
-                } else {
-                    float m = 0.f;
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) m = fmaxf(m, fabsf(v[e]));
-                    const Scale sc = scale_of(over_lanes<Max>(has ? m : 0.f, p.glanes), r);
-                    sc.apply(v, r);
-                    if (has && lane % p.glanes == 0) p.scales[row * p.groups + c / p.glanes] = sc.scale;
-                }
-                if (has) store_fp8(static_cast<uint8_t*>(p.y) + row * p.d + c * VN, v);
+                for (int e = 0; e < NP; ++e) v[e] = __fmul2_rn(__fmul2_rn(v[e], twice(r)), wk[ahead ? i : 0][e]);
+                if (live && in[i]) st16_stream(py + i * far, pack2(v));
             }
+            py += sd;
+        } else if (p.glanes) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                float2 v[NP];
+                values(i, s[i], v);
+                const Scale sc = scale_of(over_lanes<Max>(in[i] ? largest(v) : 0.f, p.glanes), r);
+                sc.apply(v, r);
+                if (live && in[i]) {
+                    store_fp8(pq + i * far, v);
+                    if (lane % p.glanes == 0) p.scales[row * p.groups + (lane + i * p.tpr) / p.glanes] = sc.scale;
+                }
+            }
+            pq += sd;
+        } else {
+            float most[1] = {0.f};
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                float2 v[NP];
+                if (!in[i]) continue;
+                values(i, s[i], v);
+                most[0] = fmaxf(most[0], largest(v));
+            }
+            over_row<Max>(most, p.tpr, buf2[turn]);
+            const Scale sc = scale_of(most[0], r);
+            if (live && lane == 0) p.scales[row] = sc.scale;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) {
+                float2 v[NP];
+                values(i, s[i], v);
+                sc.apply(v, r);
+                if (live && in[i]) store_fp8(pq + i * far, v);
+            }
+            pq += sd;
         }
+        row += step;
     }
 }
 
