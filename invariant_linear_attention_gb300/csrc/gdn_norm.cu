@@ -5,8 +5,7 @@
 //     g = d_y w:   dx = r (g - s r^2 mean(g s)) + d_residual_out,   dw = sum over rows of d_y s r
 //
 // Every value is read once and written once: HBM bounds it.  A row stays in the registers of a group of
-// threads, lane i of it 16-byte chunks i, i + lanes, ..; a warp's sums are xor butterflies, a row's warps
-// are added in ascending order.
+// threads, lane i of it 16-byte chunks i, i + lanes, ..; sums are xor butterflies, in the warps and then over a row's warps.
 #include <cuda_fp8.h>
 
 #include "../../include/gdn_layer.h"
@@ -39,27 +38,26 @@ struct Max {
 // OP over the `lanes` (a power of two up to 32) neighbours of a lane.
 template <typename OP>
 __device__ __forceinline__ float over_lanes(float v, int lanes) {
-    for (int off = 1; off < lanes; off <<= 1) v = OP::of(v, __shfl_xor_sync(0xffffffffu, v, off));
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1)
+        if (off < lanes) v = OP::of(v, __shfl_xor_sync(0xffffffffu, v, off));
     return v;
 }
-// OP over a row's threads, of N values at once.  Every thread of the CTA calls it; `buf` holds N values per
-// warp, and the next call has another one.
+// OP over a row's threads, of N values at once: in the warps, then over the warps' results.  Every thread of the CTA
+// calls it; `buf` holds N values per warp, and the next call has another one.
 template <typename OP, int N>
 __device__ __forceinline__ void over_row(float (&v)[N], int tpr, float (&buf)[N][32]) {
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = over_lanes<OP>(v[k], tpr < 32 ? tpr : 32);
     if (tpr <= 32) return;
-    const int warp = threadIdx.x / 32, per = tpr / 32, first = warp / per * per;
-    if (threadIdx.x % 32 == 0) {
+    const int warp = threadIdx.x / 32, per = tpr / 32, lane = threadIdx.x % 32;
+    if (lane == 0) {
 #pragma unroll
         for (int k = 0; k < N; ++k) buf[k][warp] = v[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        v[k] = buf[k][first];
-        for (int i = 1; i < per; ++i) v[k] = OP::of(v[k], buf[k][first + i]);
-    }
+    for (int k = 0; k < N; ++k) v[k] = over_lanes<OP>(buf[k][(warp & -per) + (lane & (per - 1))], per);
 }
 
 __device__ __forceinline__ void load_weight(const float* w, float (&v)[8]) {
@@ -124,9 +122,9 @@ __device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 // in memory are pointers that go on by a fixed step: with addresses from the row's number the 8-bit form spent half of its
 // instructions on them.
 template <typename T, int NC, int NT, bool FP8>
-__global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 ? 2 : 1) add_norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 && NC <= 2 ? 2 : 1) add_norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int VN = V16<T>::n, NP = VN / 2;
-    constexpr bool ahead = NC <= 2;
+    constexpr bool ahead = NC <= 2, early = NT < 1024;  // the registers of 1024 threads hold one row
     __shared__ float buf[2][1][32], buf2[2][1][32];
     const int lane = threadIdx.x % p.tpr, per = NT / p.tpr;
     const bool res = p.res != nullptr;
@@ -176,9 +174,10 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 ? 2 : 1) add_nor
 #pragma unroll
         for (int i = 0; i < NC; ++i) weight(i, wk[i]);
     }
-    load(row < p.rows);
+    if (early) load(row < p.rows);
     for (int turn = 0; first < p.rows; first += step, turn ^= 1) {
         const bool live = row < p.rows;
+        if (!early) load(live);
         uint4 s[NC];
         float2 s2 = twice(0.f);
 #pragma unroll
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 ? 2 : 1) add_nor
             for (int e = 0; e < NP; ++e) s2 = __ffma2_rn(v[e], v[e], s2);
         }
         px += sx, pr += sr, po += sd;
-        load(row + step < p.rows);
+        if (early) load(row + step < p.rows);
         float ss[1] = {__fadd_rn(s2.x, s2.y)};
         over_row<Sum>(ss, p.tpr, buf[turn]);
         const float r = rsqrtf(__fmaf_rn(ss[0], p.c, p.eps));
@@ -464,7 +463,7 @@ gdn_status norm_fwd(const gdn_add_norm_shape* shape, const void* x, const void* 
     // A group that takes in the whole row is the row.
     const int lanes = shape->group / vn;
     p.glanes = lanes >= p.chunks ? 0 : lanes, p.groups = p.glanes ? (p.chunks + lanes - 1) / lanes : 1;
-    const int grid = ctas_for(p, 3072);
+    const int grid = ctas_for(p, p.tpr > 256 ? 1024 : 3072);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (shape->dtype == GDN_BF16) return fp8 ? by_chunks<Fp8K, __nv_bfloat16>(grid, s, p) : by_chunks<SameK, __nv_bfloat16>(grid, s, p);
     return fp8 ? by_chunks<Fp8K, float>(grid, s, p) : by_chunks<SameK, float>(grid, s, p);
