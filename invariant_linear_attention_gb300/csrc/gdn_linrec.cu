@@ -86,23 +86,19 @@ struct Share<__nv_bfloat16, CB> {
     }
     static __device__ __forceinline__ void transposed(uint32_t to, const float2 (&v)[4]) {
         const uint32_t u[4] = {bf_pack(v[0].x, v[0].y), bf_pack(v[1].x, v[1].y), bf_pack(v[2].x, v[2].y), bf_pack(v[3].x, v[3].y)};
-        __syncwarp();
         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
-        __syncwarp();
     }
     // out: its warp's 512 bytes; y: row `row` of the tile; has: whether this lane's row and channels exist.
     __device__ __forceinline__ void store(uint4* out, __nv_bfloat16* y, bool has, const float2 (&v)[4]) const {
+        __syncwarp();
         transposed(smem_u32(out) + row_at, v);
+        __syncwarp();
         const int l = threadIdx.x % 32;
         const uint4 o = out[place(l / 2, l % 2, 2)];
         if (has) st16_stream(y, o);
     }
-    // The same through the places that its warp read an input from.
-    __device__ __forceinline__ void store_in(uint4* in, __nv_bfloat16* y, bool has, const float2 (&v)[4]) const {
-        transposed(smem_u32(in) + at, v);
-        const uint4 o = in[place(row, row_c / 8, CH)];
-        if (has) st16_stream(y, o);
-    }
+    // To the places that its warp read an input from.
+    __device__ __forceinline__ void put_in(uint4* in, const float2 (&v)[4]) const { transposed(smem_u32(in) + at, v); }
 };
 // fp32: a lane one channel; a warp's lanes are neighbouring channels.
 template <int CB>
@@ -732,30 +728,41 @@ __global__ void __launch_bounds__(GradTile<T>::NT, GradTile<T>::GRAD) linrec_bwd
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) d[i] = __fmul2_rn(d[i], rest[i]);
-        auto out = [&](void* to, uint4* by, const float2 (&o)[NP]) {
-            T* at = static_cast<T*>(to) + (int64_t)(t0 + my.row) * p.C + c0 + my.row_c;
-            const bool cok = c0 + my.row_c < p.C;
-            if constexpr (bf16) {
-                my.store_in(by, at, cok && my.row < rows, o);
-            } else {
+        if constexpr (bf16) {  // through the inputs' places to whole rows: with a warp's 32 bytes a row, 16 rows a store, the stores took most of the path to memory
+            my.put_in(in[0], dx);
+            my.put_in(in[1], d);
+            if (has_gate<KIND>(p)) my.put_in(in[2], dg);
+            if (p.z) my.put_in(in[3], dz);
+            __syncthreads();
+            const int row = threadIdx.x / F::CH, ch = threadIdx.x % F::CH, slot = Q::place(row, ch, F::CH), c = c0 + ch * F::VN;
+            if (row < rows && c < p.C) {
+                const int64_t to = (int64_t)(t0 + row) * p.C + c;
+                st16_stream(static_cast<T*>(q.dx) + to, in[0][slot]);
+                st16_stream(static_cast<T*>(q.da) + to, in[1][slot]);
+                if (has_gate<KIND>(p)) st16_stream(static_cast<T*>(q.dg) + to, in[2][slot]);
+                if (p.z) st16_stream(static_cast<T*>(q.dz) + to, in[3][slot]);
+            }
+        } else {
+            const int64_t to = (int64_t)(t0 + my.row) * p.C + c0 + my.c;
+            auto out = [&](void* y, const float2 (&o)[NP]) {
                 const float f[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (cok && my.row + j < rows) at[(int64_t)j * p.C] = f[j];
+                    if (my.row + j < rows) __stcs(static_cast<float*>(y) + to + (int64_t)j * p.C, f[j]);
+            };
+            if (c0 + my.c < p.C) {
+                out(q.dx, dx);
+                out(q.da, d);
+                if (has_gate<KIND>(p)) out(q.dg, dg);
+                if (p.z) out(q.dz, dz);
             }
-        };
-        out(q.dx, in[0], dx);
-        out(q.da, in[1], d);
-        if (has_gate<KIND>(p)) out(q.dg, in[2], dg);
-        if (p.z) out(q.dz, in[3], dz);
-        if (q.part) {
-            __syncthreads();
-            if (threadIdx.x < CB && ok) {
-                float t = sm.red[0][lane];
+            if (q.part) __syncthreads();
+        }
+        if (q.part && threadIdx.x < CB && ok) {
+            float t = sm.red[0][lane];
 #pragma unroll
-                for (int i = 1; i < (bf16 ? F::TT / 16 : F::NT / 32); ++i) t = __fadd_rn(t, sm.red[i][lane]);
-                q.part[own] = t;
-            }
+            for (int i = 1; i < (bf16 ? F::TT / 16 : F::NT / 32); ++i) t = __fadd_rn(t, sm.red[i][lane]);
+            q.part[own] = t;
         }
     }
     copy_wait<0>();
