@@ -30,8 +30,8 @@ struct FwdTile {
     // rows, then meet no bank twice.
     float4 a[NB][TT / 4][CB], b[NB][TT / 4][CB];
     static __device__ __forceinline__ int unit(int q, int c) { return c ^ 2 * (q & 3); }
-    uint4 in[ST][4][WORK];                                // x, a_gate, x_gate of a tile, z of the one NB before
-    uint4 out[std::is_same<T, float>::value ? 1 : WORK];  // bf16: a warp's y on its way from columns to rows
+    uint4 in[ST][4][WORK];                                   // x, a_gate, x_gate of a tile, z of the one NB before
+    uint4 out[2][std::is_same<T, float>::value ? 1 : WORK];  // bf16: y on its way from columns to rows; a group of two warps stores it a step later
     float K[CB];
     static_assert(CB <= 32 && TT % 16 == 0, "rows of at most 128 bytes, tiles of whole walks");
     static_assert(kGroup + (GROUP > 32 ? WORK / GROUP : 0) <= 16, "barriers of a CTA");
@@ -51,7 +51,7 @@ struct Share;
 template <int CB>
 struct Share<__nv_bfloat16, CB> {
     static constexpr int NP = 4, CH = CB / 8;
-    int c, q, at, row_at, row, row_c;  // c, row_c: within the CTA's channels; at: byte offset of this lane's matrix row in an input
+    int c, q, at;  // c: within the CTA's channels; at: byte offset of this lane's matrix row in an input
     // The 16-byte place of chunk ch of row t: a matrix's eight rows (above) lie in eight different places of a 128-byte line.
     static __device__ __forceinline__ int place(int t, int ch, int chunks) {
         const int g = (t >> 2) & 3;
@@ -61,8 +61,7 @@ struct Share<__nv_bfloat16, CB> {
         const int l = tid % 32, w = tid / 32, cw = w % (CB / 16), tb = w / (CB / 16) * 16;
         const int r = l % 8, t = (r >> 1) * 4 + (r & 1) + (l & 8 ? 2 : 0);
         c = cw * 16 + l / 4, q = tb / 4 + l % 4;
-        at = 16 * place(tb + t, cw * 2 + l / 16, CH), row_at = 16 * place(t, l / 16, 2);
-        row = tb + l / 2, row_c = cw * 16 + l % 2 * 8;
+        at = 16 * place(tb + t, cw * 2 + l / 16, CH);
     }
     __device__ __forceinline__ int first() const { return q & ~3; }  // its warp's first unit
     __device__ __forceinline__ void rates(const float* K, float2 (&k)[4]) const { k[0] = k[1] = both(K[c]), k[2] = k[3] = both(K[c + 8]); }
@@ -88,15 +87,6 @@ struct Share<__nv_bfloat16, CB> {
         const uint32_t u[4] = {bf_pack(v[0].x, v[0].y), bf_pack(v[1].x, v[1].y), bf_pack(v[2].x, v[2].y), bf_pack(v[3].x, v[3].y)};
         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
     }
-    // out: its warp's 512 bytes; y: row `row` of the tile; has: whether this lane's row and channels exist.
-    __device__ __forceinline__ void store(uint4* out, __nv_bfloat16* y, bool has, const float2 (&v)[4]) const {
-        __syncwarp();
-        transposed(smem_u32(out) + row_at, v);
-        __syncwarp();
-        const int l = threadIdx.x % 32;
-        const uint4 o = out[place(l / 2, l % 2, 2)];
-        if (has) st16_stream(y, o);
-    }
     // To the places that its warp read an input from.
     __device__ __forceinline__ void put_in(uint4* in, const float2 (&v)[4]) const { transposed(smem_u32(in) + at, v); }
 };
@@ -104,10 +94,10 @@ struct Share<__nv_bfloat16, CB> {
 template <int CB>
 struct Share<float, CB> {
     static constexpr int NP = 2, CH = CB / 4;
-    int c, q, row, row_c;
+    int c, q;
     // Rows of 64 bytes share a line, in an order that goes by the row's unit too: a warp reads one row of each of two units.
     static __device__ __forceinline__ int place(int t, int ch, int chunks) { return (chunks == 8 ? t : (t & ~1) | ((t ^ (t >> 2)) & 1)) * chunks + ch; }
-    __device__ __forceinline__ Share(int tid) { c = row_c = tid % CB, q = tid / CB, row = 4 * q; }
+    __device__ __forceinline__ Share(int tid) { c = tid % CB, q = tid / CB; }
     __device__ __forceinline__ int first() const { return q; }
     __device__ __forceinline__ void rates(const float* K, float2 (&k)[2]) const { k[0] = k[1] = both(K[c]); }
     __device__ __forceinline__ void load(const uint4* in, float2 (&v)[2]) const {
@@ -194,17 +184,24 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
         float2 K[NP];
         my.rates(sm.K, K);
         const bool far = any_far(K);
-        const bool cok = c0 + my.row_c < p.C;
-        T* y = static_cast<T*>(p.y) + (int64_t)(bos + my.row) * p.C + c0 + my.row_c;
+        constexpr bool bf16 = !std::is_same<T, float>::value, later = bf16 && F::GROUP > 32;
+        const bool cok = c0 + my.c < p.C;
+        T* y = static_cast<T*>(p.y) + (bf16 ? (int64_t)(bos + row) * p.C + cc : (int64_t)(bos + 4 * my.q) * p.C + c0 + my.c);
         int rows = len - 4 * my.first(), old = 0;  // tokens from its warp's first on, of this step's tile and of the one to finish
-        for (int i = 0, in = 0, buf = 0; i < tiles + F::NB; ++i) {
+        int yleft = cc < p.C ? len - row : 0;      // bf16: rows from the next one on that it stores
+        for (int i = 0, in = 0, buf = 0; i < tiles + F::NB + later; ++i) {
             copy_wait<AHEAD - 1>();
             if (F::GROUP > 32) bar_sync(F::kGroup + tid / F::GROUP, F::GROUP);
             else __syncwarp();
             copy();
             const uint4(&from)[4][WORK] = sm.in[in];
             in = in + 1 == ST ? 0 : in + 1;
-            if (i >= F::NB) bar_sync(F::kDone + buf, F::NT);
+            auto flush = [&](int which) {
+                if (yleft > 0) st16_stream(y, sm.out[which][slot]);
+                y += (int64_t)TT * p.C, yleft -= TT;
+            };
+            if (later && i > F::NB) flush((i & 1) ^ 1);
+            if (i >= F::NB && i < tiles + F::NB) bar_sync(F::kDone + buf, F::NT);
             if (i == F::NB) old = len - 4 * my.first();
             if (old > 0) {
                 float2 h[NP];
@@ -214,16 +211,21 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
                     my.load(from[3], z);
                     branch(p.act, z, h);
                 }
-                const int here = old - (my.row - 4 * my.first());  // tokens from this lane's row on
-                if constexpr (std::is_same<T, float>::value) {
+                if constexpr (bf16) {
+                    if (!later) __syncwarp();
+                    my.put_in(sm.out[i & 1], h);
+                    if (!later) {
+                        __syncwarp();
+                        flush(i & 1);
+                    }
+                } else {
                     const float f[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (cok && j < here) y[(int64_t)j * p.C] = f[j];
-                } else {
-                    my.store(sm.out + tid / 32 * 32, y, cok && here > 0, h);
+                        if (cok && j < old) __stcs(reinterpret_cast<float*>(y) + (int64_t)j * p.C, f[j]);
+                    y += (int64_t)TT * p.C;
                 }
-                y += (int64_t)TT * p.C, old -= TT;
+                old -= TT;
             }
             if (rows > 0) {
                 float2 x[NP], ag[NP], xg[NP], a[NP], b[NP];
@@ -743,12 +745,12 @@ __global__ void __launch_bounds__(GradTile<T>::NT, GradTile<T>::GRAD) linrec_bwd
                 if (p.z) st16_stream(static_cast<T*>(q.dz) + to, in[3][slot]);
             }
         } else {
-            const int64_t to = (int64_t)(t0 + my.row) * p.C + c0 + my.c;
+            const int64_t to = (int64_t)(t0 + 4 * my.q) * p.C + c0 + my.c;
             auto out = [&](void* y, const float2 (&o)[NP]) {
                 const float f[4] = {o[0].x, o[0].y, o[1].x, o[1].y};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (my.row + j < rows) __stcs(static_cast<float*>(y) + to + (int64_t)j * p.C, f[j]);
+                    if (4 * my.q + j < rows) __stcs(static_cast<float*>(y) + to + (int64_t)j * p.C, f[j]);
             };
             if (c0 + my.c < p.C) {
                 out(q.dx, dx);
