@@ -101,8 +101,12 @@ gdn_status gdn_linear_recurrence_update(const gdn_linrec_shape* shape, const voi
  * not written).  Outputs must not alias inputs.  The states are recomputed;
  * nothing of the forward call is needed.  fp32 sums, each in an order fixed by
  * the shape and cu_seqlens: deterministic; the sum over tokens in da_param is
- * not batch-invariant.  (Where a_t = 1 in fp32, the slope of scale sqrt is
- * taken as 0: there a_gate's share of the exponent is 0 as well.)
+ * not batch-invariant.  (Where 1 - a_t is 0, the slope of scale sqrt is
+ * infinite and a_gate's share of the exponent 0; their product is taken as 0.)
+ *
+ * The workspace holds four fp32 values per channel and tile of 32 tokens, at
+ * most T_total / 32 + N tiles: half a byte per token and channel, and 16 C bytes
+ * per sequence, empty ones too.
  */
 size_t gdn_linear_recurrence_bwd_workspace_size(const gdn_linrec_shape* shape);
 

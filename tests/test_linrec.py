@@ -166,7 +166,7 @@ def test_bits_do_not_depend_on_the_batch_or_on_how_tokens_arrive(dtype, C, param
     assert torch.equal(bits(torch.cat(parts)), bits(y[a:a + 230])) and torch.equal(bits(st[2]), bits(pool[2]))
 
 
-@pytest.mark.parametrize("dtype,N,C,longest", [(BF, 110, 2056, 130), (F32, 110, 1036, 130), (BF, 3, 4104, 700), (F32, 2, 8200, 300), (BF, 700, 40, 9), (BF, 9, 264, 1500)])
+@pytest.mark.parametrize("dtype,N,C,longest", [(BF, 110, 2056, 130), (F32, 110, 1036, 130), (BF, 3, 4104, 700), (F32, 2, 8200, 300), (BF, 700, 40, 9), (BF, 9, 264, 1500), (F32, 5, 4100, 200)])
 def test_large_batches_agree_with_a_sequence_alone(dtype, N, C, longest):
     lens = [(37 * i) % longest + (longest // 2 if i == 0 else 0) for i in range(N)]
     c = Case(lens, C, dtype, 13, act="gelu")
@@ -230,6 +230,17 @@ def test_backward_of_sequences_of_every_length(dtype, C, lens, param, act):
         assert g[k] is None or torch.equal(bits(g[k]), bits(again[k])), k
     with pytest.raises(gdn.GdnError):
         check_backward(c, workspace=ws[:8])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_sequences_than_a_grids_second_dimension_holds(dtype):
+    lens = [(1, 0, 2, 1)[i % 4] for i in range(66000)]
+    lens[40000] = 300
+    c = Case(lens, 8, dtype, 41, act="silu")
+    pool = c.h0.clone()
+    y = gdn.gdn_linear_recurrence_fwd(cu_seqlens=c.cu, state=pool, **c.args())
+    check_forward(c, y, pool, c.h0)
+    check_backward(c)
 
 
 def test_gradient_by_differences():

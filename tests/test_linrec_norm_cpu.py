@@ -172,6 +172,12 @@ def test_recurrence_backward_pointers(lib, change, expect):
     assert lib.gdn_linear_recurrence_bwd_workspace_size(ctypes.byref(s)) > 0
 
 
+@pytest.mark.parametrize("T,N,C,dtype", [(100, 3, 64, binding.GDN_BF16), (0, 5, 8, binding.GDN_F32), (1 << 20, 1, 4096, binding.GDN_BF16), (2 ** 31 - 300, 1, 8, binding.GDN_F32)])
+def test_recurrence_workspace_follows_the_tokens_and_the_sequences(lib, T, N, C, dtype):
+    s = rec_shape(T_total=T, N=N, C=C, dtype=dtype, ldx=C, lda=C, ldg=C, ldz=C)
+    assert lib.gdn_linear_recurrence_bwd_workspace_size(ctypes.byref(s)) == 16 * (T // 32 + N) * C
+
+
 def norm_shape(**kw):
     return gdn.AddNormShape(**dict(dict(rows=10, d=64, dtype=binding.GDN_BF16, eps=1e-6, group=32, ldx=64, ldr=64), **kw))
 
