@@ -19,6 +19,13 @@ using namespace linrec;
 // A worker reads the h of the very places that it then writes, so it meets nobody but the walkers, NB tiles behind or ahead:
 // at named barriers full (a tile prepared) and done (it is walked), one of each per buffer, which every side passes once a
 // tile.  The inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead, for a group of workers that copies what it reads.
+//
+// What bounds it.  fp32: HBM (8 prompts, 16384 x 4096, gated: 205 us, 0.96 of the measured peak).  bf16 with full SMs (16
+// prompts, 32768 x 4096, gated: 283 us, 0.70): nothing alone; issue slots are half taken, the special function units (72
+// cycles for 256 values; 160 us by themselves before the gates shared a reciprocal) and the path from shared memory as well,
+// by 18 warps an SM that the registers and 104 KB of buffers leave.  With trivial work in the workers' place it takes 240 us, without
+// the walk 261.  A single sequence: the walk, 6.3 ns a token with its stores and the workers beside it, 3.7 ns alone (65536 x
+// 2048: 410 us, 300 without the walk).
 template <typename T, int CB, int WORKERS>
 struct FwdTile {
     static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = WORKERS, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
@@ -305,7 +312,8 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
     if (has_slot && threadIdx.x < CB) *st = h;
 }
 
-// Single tokens: a thread takes a chunk of channels over `rows` batch rows, so that it works out their rates once.
+// Single tokens: a thread takes a chunk of channels over `rows` batch rows, so that it works out their rates once.  A launch and a chain
+// of loads (slot, state) for small batches; 256 x 4096, bf16, gated: 7.2 us, 0.39 of HBM; 512 x 8192: 17.8, 0.62.
 template <typename T>
 __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constant__ Params p, int rows) {
     constexpr int VN = V16<T>::n, NP = VN / 2;
@@ -355,6 +363,9 @@ __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constan
 //     dx = G s p,  dx_gate = G s x p (1 - p),  dz = dy h act'(z),
 //     d = G (a h_{t-1} k - v kappa),  k = -w (or 1 - a: a_gate's slope of log a),  kappa = -k ds/du = k a^2 / s | k a | 0
 //     da_gate = d (1 - r) (or d),  da_param = sum of d over the tokens, times sigmoid(a_param) decay / K
+// The inputs are read twice: 28 bytes a value where 18 cannot be done without (bf16, gated).  8 documents, 16384 x 4096: 454 us,
+// sums 157, join 13, gradients 270, da_param 8.  Issue slots (63 and 49 % taken) and the path from shared memory (50 and 70 %, the
+// latter before the gradients left in whole rows) bound it, not HBM (56 and 46 %).
 struct GradParams {
     Params p;
     const void* dy;
@@ -372,9 +383,9 @@ struct Where {
 template <typename T>
 struct GradTile {
     static constexpr int CB = 32, VN = V16<T>::n, CH = CB / VN, NT = VN == 8 ? 128 : 256, TT = NT / CH, NQ = TT / 4;
-    // CTAs an SM of the two kernels.  Smaller CTAs walk while others compute (8 documents, 16384 x 4096, bf16: 483 us, with 256
-    // threads and 3 and 2 CTAs 535); fewer registers spill (5 CTAs: 560).  fp32 holds half the values a thread: 267 us for 16384 x
-    // 2048 so, 307 with bf16's numbers.
+    // CTAs an SM of the two kernels.  Smaller CTAs walk while others compute (8 documents, 16384 x 4096, bf16, when it was chosen: 483
+    // us; with 256 threads and 3 and 2 CTAs 535); fewer registers spill (5 CTAs: 560).  fp32 holds half the values a thread: 267 us
+    // for 16384 x 2048 so, 307 with 128 threads and 6 and 4 CTAs.
     static constexpr int SUM = VN == 8 ? 6 : 4, GRAD = VN == 8 ? 4 : 3;
     float4 a[NQ][CB], b[NQ + 1][CB], e[NQ][CB];  // units as in FwdTile; b gets the states before each token, and the last one behind them, e the G
     uint4 in[2][5][NT];                          // x, a_gate, x_gate, z, dy of this tile and the next one; then the gradients on their way to rows
@@ -800,11 +811,11 @@ gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     kernel<<<ctas, F::NT, sizeof(F), s>>>(q);
     return launch_status();
 }
-// Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16, 6.4 ns with 16 channels and 512 workers, 10 ns with 32
-// and 512, 12 ns with 32 and 256, and 20 ns each of two of the last kind on one SM; a batch of several sequences ends with its longest alone.
-// us with the three forms: 1 x 16384 x 1024 114, 186, 218; 3 ragged, 16000 x 1600 (n = 150) 91, 109, 124; 1 x 16384 x 4096 (128)
-// 228, 187, 217; 2, 8000 x 2560 (160) 85, 77, 83; 4, 8192 x 2048 (256) 67, 56, 69; 1 x 16384 x 8192 (256) 454, 371, 331;
-// 16, 32768 x 4096 (2048) 460, 350, 283.  fp32 the same way.
+// Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16 and gated, 7 ns with 16 channels and 512 workers, 11 ns
+// with 32 and 512, 14 ns with 32 and 256, and 20 ns each of two of the last kind on one SM; a batch of several sequences ends with its
+// longest alone.  us with the three forms: 1 x 16384 x 1024 115, 177, 228; 3 ragged, 16000 x 1600 (n = 150) 91, 104, 133; 1 x 16384 x 4096
+// (128) 231, 178, 229; 2, 8000 x 2560 (160) 85, 75, 83; 4, 8192 x 2048 (256) 66, 54, 70; 1 x 16384 x 8192 (256) 459, 351, 329; 16, 32768 x
+// 4096 (2048) 459, 335, 284.  fp32 the same way: 125, 213, 272; 100, 129, 163; 246, 217, 285; 93, 91, 101; 72, 66, 84; 504, 457, 423; 493, 429, 405.
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
     const long long n = (long long)((p.C + 31) / 32) * p.N;

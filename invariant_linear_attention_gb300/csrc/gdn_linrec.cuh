@@ -16,8 +16,6 @@ namespace gdn {
 namespace linrec {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 neg(const float2& v) { return make_float2(-v.x, -v.y); }
-__device__ __forceinline__ float2 sub(const float2& a, const float2& b) { return __fadd2_rn(a, neg(b)); }
 
 __device__ __forceinline__ float sqrt_approx(float x) {
     float r;
@@ -179,10 +177,9 @@ struct Params {
     int ranked;  // prompts: take the sequences in order of length
 };
 
-// Which of a call's options a kernel knows at compile time.  With all of them as branches, the values that meet
-// behind each branch cost about 100 of 420 instructions per 8 tokens and channels in register moves; all combinations would
-// be 36 kernels of each.  kBothGates: a_param, x_gate, scale sqrt; kForget: neither, scale linear; kAny: asks at run time.
-// The bits are the same.
+// Which of a call's options a kernel knows at compile time.  With all of them as branches the values that meet
+// behind each branch are moved about (16 prompts, 32768 x 4096: 307 us, so 283); all combinations would be 36 kernels of
+// each.  kBothGates: a_param, x_gate, scale sqrt; kForget: neither, scale linear; kAny: asks at run time.  The bits are the same.
 enum Kind { kAny, kBothGates, kForget };
 template <Kind KIND>
 __device__ __forceinline__ bool has_param(const Params& p) { return KIND == kAny ? p.ap != nullptr : KIND == kBothGates; }

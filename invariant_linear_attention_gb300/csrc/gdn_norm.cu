@@ -119,8 +119,12 @@ __device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
 // A CTA takes rows blockIdx.x, + gridDim.x, ..  Up to two chunks a thread (NC), it keeps its weights in registers and
 // has the next row's loads under way while a row is summed and stored.  A row waits packed, as it is stored.  Its places
-// in memory are pointers that go on by a fixed step: with addresses from the row's number the 8-bit form spent half of its
-// instructions on them.
+// in memory are pointers that go on by a fixed step (addresses from the row's number: 174 us for the 8-bit case below, so 157; its
+// reductions unrolled 149).
+//
+// HBM bounds it: 32768 x 4096, bf16, residual: 161 us, 0.98 of the measured peak; in 8 bits with a scale for each 128 values 149 us,
+// 0.93, with 69 % of the issue slots taken.  Without a residual the 8-bit form has half the bytes for the same instructions
+// and is bound by them (120 us, 0.50).
 template <typename T, int NC, int NT, bool FP8>
 __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 && NC <= 2 ? 2 : 1) add_norm_kernel(const __grid_constant__ NormParams p) {
     constexpr int VN = V16<T>::n, NP = VN / 2;
@@ -252,7 +256,8 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 && NC <= 2 ? 2 :
 }
 
 // The gradient takes rows the same way.  sum(g s) needs no r, so that both sums go together.  dw: a thread's
-// columns in registers, with more than two chunks in its own places of shared memory.
+// columns in registers, with more than two chunks in its own places of shared memory.  32768 x 4096, bf16, with the residual's
+// gradient: 171 us, 0.92 of HBM; rows past 8192 (fp32 4096) values hold more than the registers do: 8192 x 16384 305 us, 0.52.
 template <typename T, int NC, int NT>
 __global__ void __launch_bounds__(NT, NT <= 256 ? 2 : 1) add_norm_bwd_kernel(const __grid_constant__ NormParams p) {
     constexpr int VN = V16<T>::n;
