@@ -37,9 +37,10 @@ struct FwdTile {
     // rows, then meet no bank twice.
     float4 a[NB][TT / 4][CB], b[NB][TT / 4][CB];
     static __device__ __forceinline__ int unit(int q, int c) { return c ^ 2 * (q & 3); }
-    uint4 in[ST][4][WORK];                                   // x, a_gate, x_gate of a tile, z of the one NB before
-    uint4 out[2][std::is_same<T, float>::value ? 1 : WORK];  // bf16: y on its way from columns to rows; a group of two warps stores it a step later
+    uint4 in[ST][4][WORK];                                    // x, a_gate, x_gate of a tile, z of the one NB before
+    uint4 out[NB][std::is_same<T, float>::value ? 1 : WORK];  // bf16: y on its way from columns to rows; a group of two warps stores it a step later
     float K[CB];
+    static_assert(ST == 3 && NB == 3, "a step's copies and buffers come round together");
     static_assert(CB <= 32 && TT % 16 == 0, "rows of at most 128 bytes, tiles of whole walks");
     static_assert(kGroup + (GROUP > 32 ? WORK / GROUP : 0) <= 16, "barriers of a CTA");
 };
@@ -161,91 +162,90 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
     if (threadIdx.x >= F::WALK) {
         const int tid = threadIdx.x - F::WALK;
         const bool gate = p.z != nullptr;
-        // its copies: a chunk of row tid / CH
+        // its copies: a chunk of row tid / CH of each tile
         const int row = tid / CH, slot = Q::place(row, tid % CH, CH), cc = c0 + tid % CH * VN;
-        int left = cc < p.C ? len - row : 0;  // rows from the next copy's on; below 1: none to copy
-        const T* px = static_cast<const T*>(p.x) + (int64_t)(bos + row) * p.ldx + cc;
-        const T* pa = static_cast<const T*>(p.ag) + (int64_t)(bos + row) * p.lda + cc;
-        const T* pg = p.xg ? static_cast<const T*>(p.xg) + (int64_t)(bos + row) * p.ldg + cc : nullptr;
-        const T* pz = gate ? static_cast<const T*>(p.z) + (int64_t)(bos + row) * p.ldz + cc : nullptr;
-        int stage = 0, zleft = left, behind = F::NB;
-        auto copy = [&] {  // what the next step that has no copies yet needs
+        const int upto = cc < p.C ? max(len - row, 0) : 0;  // tiles that start before this token have a row to copy
+        auto at = [&](const void* from, int64_t ld, int t) { return static_cast<const char*>(from) + ((int64_t)(bos + row + t) * ld + cc) * (int64_t)sizeof(T); };
+        const char *px = at(p.x, p.ldx, 0), *pa = at(p.ag, p.lda, 0), *pg = at(p.xg, p.ldg, 0), *pz = at(p.z, p.ldz, -F::NB * TT);
+        auto copy = [&](int stage, int t) {  // what the step whose tile starts at t needs
             uint4(&to)[4][WORK] = sm.in[stage];
-            stage = stage + 1 == ST ? 0 : stage + 1;
-            if (left > 0) {
+            if (t < upto) {
                 copy16_async(&to[0][slot], px);
                 copy16_async(&to[1][slot], pa);
                 if (has_gate<KIND>(p)) copy16_async(&to[2][slot], pg);
             }
-            px += (int64_t)TT * p.ldx, pa += (int64_t)TT * p.lda, pg += (int64_t)TT * p.ldg, left -= TT;
-            if (behind > 0) {
-                --behind;
-            } else {
-                if (gate && zleft > 0) copy16_async(&to[3][slot], pz);
-                pz += (int64_t)TT * p.ldz, zleft -= TT;
-            }
+            if (gate && (unsigned)(t - F::NB * TT) < (unsigned)upto) copy16_async(&to[3][slot], pz);
+            px += p.sx, pa += p.sa, pg += p.sg, pz += p.sz;
             copy_commit();
         };
         const Q my(tid);
-        for (int i = 0; i < AHEAD; ++i) copy();
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) copy(i, i * TT);
         float2 K[NP];
         my.rates(sm.K, K);
         const bool far = any_far(K);
         constexpr bool bf16 = !std::is_same<T, float>::value, later = bf16 && F::GROUP > 32;
-        const bool cok = c0 + my.c < p.C;
-        T* y = static_cast<T*>(p.y) + (bf16 ? (int64_t)(bos + row) * p.C + cc : (int64_t)(bos + 4 * my.q) * p.C + c0 + my.c);
-        int rows = len - 4 * my.first(), old = 0;  // tokens from its warp's first on, of this step's tile and of the one to finish
-        int yleft = cc < p.C ? len - row : 0;      // bf16: rows from the next one on that it stores
-        for (int i = 0, in = 0, buf = 0; i < tiles + F::NB + later; ++i) {
+        const int mine = 4 * my.first();  // its warp's first token of a tile
+        char* y = static_cast<char*>(p.y) + (bf16 ? (int64_t)(bos + row) * p.C + cc : (int64_t)(bos + 4 * my.q) * p.C + c0 + my.c) * (int64_t)sizeof(T);
+        // Step i, J = i % 3: the tile from token t on, and the one NB before.
+        auto step = [&](auto J_, int i, int t) {
+            constexpr int J = decltype(J_)::value, before = (J + 2) % 3;
             copy_wait<AHEAD - 1>();
             if (F::GROUP > 32) bar_sync(F::kGroup + tid / F::GROUP, F::GROUP);
             else __syncwarp();
-            copy();
-            const uint4(&from)[4][WORK] = sm.in[in];
-            in = in + 1 == ST ? 0 : in + 1;
-            auto flush = [&](int which) {
-                if (yleft > 0) st16_stream(y, sm.out[which][slot]);
-                y += (int64_t)TT * p.C, yleft -= TT;
+            copy((J + AHEAD) % ST, t + AHEAD * TT);
+            const uint4(&from)[4][WORK] = sm.in[J];
+            auto flush = [&](int which, int old) {  // bf16: a row of the tile from `old` on
+                if (old < upto) st16_stream(y, sm.out[which][slot]);
+                y += p.sy;
             };
-            if (later && i > F::NB) flush((i & 1) ^ 1);
-            if (i >= F::NB && i < tiles + F::NB) bar_sync(F::kDone + buf, F::NT);
-            if (i == F::NB) old = len - 4 * my.first();
-            if (old > 0) {
-                float2 h[NP];
-                my.template get<F>(sm.b[buf], h);
-                if (gate) {
-                    float2 z[NP];
-                    my.load(from[3], z);
-                    branch(p.act, z, h);
-                }
-                if constexpr (bf16) {
-                    if (!later) __syncwarp();
-                    my.put_in(sm.out[i & 1], h);
-                    if (!later) {
-                        __syncwarp();
-                        flush(i & 1);
+            const int old = t - F::NB * TT;
+            if (later && i > F::NB) flush(before, old - TT);
+            if (i >= F::NB && i < tiles + F::NB) {
+                bar_sync(F::kDone + J, F::NT);
+                if (old + mine < len) {
+                    float2 h[NP];
+                    my.template get<F>(sm.b[J], h);
+                    if (gate) {
+                        float2 z[NP];
+                        my.load(from[3], z);
+                        branch(p.act, z, h);
                     }
-                } else {
-                    const float f[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
+                    if constexpr (bf16) {
+                        if (!later) __syncwarp();
+                        my.put_in(sm.out[J], h);
+                        if (!later) {
+                            __syncwarp();
+                            flush(J, old);
+                        }
+                    } else {
+                        const float f[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
+                        const int has = c0 + my.c < p.C ? len - old - mine : 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (cok && j < old) __stcs(reinterpret_cast<float*>(y) + (int64_t)j * p.C, f[j]);
-                    y += (int64_t)TT * p.C;
+                        for (int j = 0; j < 4; ++j)
+                            if (j < has) __stcs(reinterpret_cast<float*>(y) + (int64_t)j * p.C, f[j]);
+                        y += p.sy;
+                    }
                 }
-                old -= TT;
             }
-            if (rows > 0) {
-                float2 x[NP], ag[NP], xg[NP], a[NP], b[NP];
-                my.load(from[0], x);
-                my.load(from[1], ag);
-                my.load(from[2], xg);
-                steps<KIND>(p, far, K, ag, xg, x, a, b);
-                my.template put<F>(sm.a[buf], a);
-                my.template put<F>(sm.b[buf], b);
-                rows -= TT;
+            if (i < tiles) {
+                if (t + mine < len) {
+                    float2 x[NP], ag[NP], xg[NP], a[NP], b[NP];
+                    my.load(from[0], x);
+                    my.load(from[1], ag);
+                    my.load(from[2], xg);
+                    steps<KIND>(p, far, K, ag, xg, x, a, b);
+                    my.template put<F>(sm.a[J], a);
+                    my.template put<F>(sm.b[J], b);
+                }
+                bar_arrive(F::kFull + J, F::NT);
             }
-            if (i < tiles) bar_arrive(F::kFull + buf, F::NT);
-            buf = buf + 1 == F::NB ? 0 : buf + 1;
+        };
+        const int last = tiles + F::NB + later;
+        for (int i = 0, t = 0; i < last; i += 3, t += 3 * TT) {
+            step(std::integral_constant<int, 0>{}, i, t);
+            if (i + 1 < last) step(std::integral_constant<int, 1>{}, i + 1, t + TT);
+            if (i + 2 < last) step(std::integral_constant<int, 2>{}, i + 2, t + 2 * TT);
         }
         copy_wait<0>();
         return;
@@ -807,6 +807,8 @@ gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
     const unsigned ctas = (unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N;
     Params q = p;
+    constexpr int64_t tile = (int64_t)F::TT * sizeof(T);
+    q.sx = tile * p.ldx, q.sa = tile * p.lda, q.sg = tile * p.ldg, q.sz = tile * p.ldz, q.sy = tile * p.C;
     q.ranked = p.N > 1 && p.N <= kRanked && ctas > (unsigned)(kSMs * CTAS) && (long long)p.N * p.N * p.N <= 256LL * p.T;
     kernel<<<ctas, F::NT, sizeof(F), s>>>(q);
     return launch_status();
@@ -859,8 +861,8 @@ gdn_status check_linrec(const gdn_linrec_shape* s, bool param, bool gate, bool z
     if (param && !(s->decay > 0.f && s->decay <= FLT_MAX)) return GDN_ERR_INVALID_ARG;
     const int vn = s->dtype == GDN_BF16 ? 8 : 4;
     if (s->C % vn) return GDN_ERR_UNSUPPORTED;
-    // CTAs are numbered, and states per sequence indexed, in 31 bits
-    if (s->T_total > INT_MAX - 256 || (long long)s->N * s->C >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
+    // CTAs are numbered, states per sequence and tokens a few tiles behind the last indexed in 31 bits
+    if (s->T_total > INT_MAX - 4096 || (long long)s->N * s->C >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
     if (s->ldx < s->C || s->lda < s->C || (gate && s->ldg < s->C) || (z && s->ldz < s->C)) return GDN_ERR_INVALID_ARG;
     if (s->ldx % vn || s->lda % vn || (gate && s->ldg % vn) || (z && s->ldz % vn)) return GDN_ERR_INVALID_ARG;
     return GDN_OK;

@@ -174,7 +174,8 @@ struct Params {
     int num_slots;
     const int32_t* has_init;
     void* y;
-    int ranked;  // prompts: take the sequences in order of length
+    int ranked;                  // prompts: take the sequences in order of length
+    int64_t sx, sa, sg, sz, sy;  // prompts: bytes from a tile's row of x, a_gate, x_gate, z, y to the next tile's
 };
 
 // Which of a call's options a kernel knows at compile time.  With all of them as branches the values that meet
