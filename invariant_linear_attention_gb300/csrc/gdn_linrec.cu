@@ -20,12 +20,12 @@ using namespace linrec;
 // at named barriers full (a tile prepared) and done (it is walked), one of each per buffer, which every side passes once a
 // tile.  The inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead, for a group of workers that copies what it reads.
 //
-// What bounds it.  fp32: HBM (8 prompts, 16384 x 4096, gated: 205 us, 0.96 of the measured peak).  bf16 with full SMs (16
-// prompts, 32768 x 4096, gated: 283 us, 0.70): nothing alone; issue slots are half taken, the special function units (72
+// What bounds it.  fp32: HBM (16 prompts, 32768 x 4096, gated: 401 us, 0.98 of the measured peak).  bf16 with full SMs (16
+// prompts, 32768 x 4096, gated: 264 us, 0.75): nothing alone; issue slots are half taken, the special function units (72
 // cycles for 256 values; 160 us by themselves before the gates shared a reciprocal) and the path from shared memory as well,
-// by 18 warps an SM that the registers and 104 KB of buffers leave.  With trivial work in the workers' place it takes 240 us, without
-// the walk 261.  A single sequence: the walk, 6.3 ns a token with its stores and the workers beside it, 3.7 ns alone (65536 x
-// 2048: 410 us, 300 without the walk).
+// by 18 warps an SM that the registers and 108 KB of buffers leave.  (When it took 284 us: 240 with trivial work in the workers'
+// place, 261 without the walk.)  A single sequence: the walk, 6.3 ns a token with its stores and the workers beside it, 3.7 ns
+// alone (65536 x 2048: 414 us; 300 without the walk).
 template <typename T, int CB, int WORKERS>
 struct FwdTile {
     static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = WORKERS, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
 }
 
 // Single tokens: a thread takes a chunk of channels over `rows` batch rows, so that it works out their rates once.  A launch and a chain
-// of loads (slot, state) for small batches; 256 x 4096, bf16, gated: 7.2 us, 0.39 of HBM; 512 x 8192: 17.8, 0.62.
+// of loads (slot, state) for small batches; 256 x 4096, bf16, gated: 7.2 us, 0.39 of HBM; 512 x 8192: 17.8 us, 0.62.
 template <typename T>
 __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constant__ Params p, int rows) {
     constexpr int VN = V16<T>::n, NP = VN / 2;
@@ -813,11 +813,17 @@ gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     kernel<<<ctas, F::NT, sizeof(F), s>>>(q);
     return launch_status();
 }
-// Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16 and gated, 7 ns with 16 channels and 512 workers, 11 ns
-// with 32 and 512, 14 ns with 32 and 256, and 20 ns each of two of the last kind on one SM; a batch of several sequences ends with its
-// longest alone.  us with the three forms: 1 x 16384 x 1024 115, 177, 228; 3 ragged, 16000 x 1600 (n = 150) 91, 104, 133; 1 x 16384 x 4096
-// (128) 231, 178, 229; 2, 8000 x 2560 (160) 85, 75, 83; 4, 8192 x 2048 (256) 66, 54, 70; 1 x 16384 x 8192 (256) 459, 351, 329; 16, 32768 x
-// 4096 (2048) 459, 335, 284.  fp32 the same way: 125, 213, 272; 100, 129, 163; 246, 217, 285; 93, 91, 101; 72, 66, 84; 504, 457, 423; 493, 429, 405.
+// Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16 and gated, 7 ns with 16 channels and 512 workers, 10 ns
+// with 32 and 512, 12 ns with 32 and 256, and 19 ns each of two of the last kind on one SM; a batch of several sequences ends with its
+// longest alone.  us with the three forms, bf16 / fp32:
+//     1 x 16384 x 1024 (n = 32)             115, 161, 201 / 123, 191, 263
+//     1 x 16384 x 4096 (128)                230, 162, 203 / 240, 210, 279
+//     3 ragged, 16000 x 1600 (150)           90,  95, 118 /  97, 120, 159
+//     2, 8000 x 2560 (160)                   85,  68,  78 /  91,  87,  95
+//     4, 8192 x 2048 (256)                   66,  49,  65 /  69,  63,  79
+//     1 x 16384 x 8192 (256)                458, 319, 305 / 495, 440, 413
+//     13, 20000 x 2560 (1040)               187, 125, 108 / 194, 167, 156
+//     16, 32768 x 4096 (2048)               461, 307, 264 / 477, 420, 401
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
     const long long n = (long long)((p.C + 31) / 32) * p.N;

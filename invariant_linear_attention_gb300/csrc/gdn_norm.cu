@@ -468,7 +468,7 @@ gdn_status norm_fwd(const gdn_add_norm_shape* shape, const void* x, const void* 
     // A group that takes in the whole row is the row.
     const int lanes = shape->group / vn;
     p.glanes = lanes >= p.chunks ? 0 : lanes, p.groups = p.glanes ? (p.chunks + lanes - 1) / lanes : 1;
-    const int grid = ctas_for(p, p.tpr > 256 ? 1024 : 3072);
+    const int grid = ctas_for(p, p.tpr > kRowThreads ? 1024 : 12 * kRowThreads);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (shape->dtype == GDN_BF16) return fp8 ? by_chunks<Fp8K, __nv_bfloat16>(grid, s, p) : by_chunks<SameK, __nv_bfloat16>(grid, s, p);
     return fp8 ? by_chunks<Fp8K, float>(grid, s, p) : by_chunks<SameK, float>(grid, s, p);

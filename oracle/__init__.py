@@ -20,6 +20,9 @@ Parity status of each function (what pins it is in ``tests/test_oracle_pins.py``
                           ``gdn_fwd``'s final state; its d rows equal the
                           chunked WY form's U rows.
 * ``layer_ops``        -- gates, causal conv, gated RMSNorm: pinned in
-                          ``tests/test_oracle_layer_pins.py``.
+                          ``tests/test_oracle_layer_pins.py``; RMSNorm with the
+                          residual's addition: ``tests/test_linrec_norm_cpu.py``.
+* ``linrec_ops``       -- gated linear recurrence: pinned in
+                          ``tests/test_linrec_norm_cpu.py``.
 """
 from .oracle import gdn_fwd, gdn_bwd, gdn_fwd_chunked, gdn_replay_state, max_threads  # noqa: F401
