@@ -313,30 +313,35 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
 }
 
 // Single tokens: a thread takes a chunk of channels over `rows` batch rows, so that it works out their rates once.  A launch and a chain
-// of loads (slot, state) for small batches; 256 x 4096, bf16, gated: 7.2 us, 0.39 of HBM; 512 x 8192: 17.8 us, 0.62.
+// of loads (slot, state) for small batches; 256 x 4096, bf16, gated: 6.4 us, 0.43 of HBM; 512 x 8192: 16.5 us, 0.68; 2048 x 8192: 52.9 us, 0.84 (fp32 68, 1.0).
 template <typename T>
 __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constant__ Params p, int rows) {
     constexpr int VN = V16<T>::n, NP = VN / 2;
     const int chunks = p.C / VN, blocks = (chunks + 127) / 128, ch = blockIdx.x % blocks * 128 + threadIdx.x, c = ch * VN;
     if (ch >= chunks) return;
-    float2 K[NP];
-#pragma unroll
-    for (int e = 0; e < NP; ++e) K[e] = p.ap ? make_float2(rate_of(__ldg(p.ap + c + 2 * e), p.decay), rate_of(__ldg(p.ap + c + 2 * e + 1), p.decay)) : both(0.f);
-    const bool far = any_far(K);
     const int first = blockIdx.x / blocks * rows, last = min(first + rows, p.N);
     const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+    float2 K[NP];
+    bool far = false;
     for (int64_t n = first; n < last; ++n) {
+        // A row's inputs do not wait for its slot, nor its loads for the rates.
         const int slot = p.idx ? __ldg(p.idx + n) : (int)n;
-        if (slot < 0 || slot >= p.num_slots) continue;
-        float4* st = reinterpret_cast<float4*>(p.state + (int64_t)slot * p.C + c);
         const uint4 xr = ld16(static_cast<const T*>(p.x) + n * p.ldx + c), ar = ld16(static_cast<const T*>(p.ag) + n * p.lda + c);
         const uint4 gr = p.xg ? ld16(static_cast<const T*>(p.xg) + n * p.ldg + c) : none, zr = p.z ? ld16(static_cast<const T*>(p.z) + n * p.ldz + c) : none;
+        const bool live = slot >= 0 && slot < p.num_slots;
+        float4* st = reinterpret_cast<float4*>(p.state + (int64_t)(live ? slot : 0) * p.C + c);
+        float4 v[NP / 2];
+#pragma unroll
+        for (int e = 0; e < NP / 2; ++e) v[e] = live ? st[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (n == first) {
+#pragma unroll
+            for (int e = 0; e < NP; ++e) K[e] = p.ap ? make_float2(rate_of(__ldg(p.ap + c + 2 * e), p.decay), rate_of(__ldg(p.ap + c + 2 * e + 1), p.decay)) : both(0.f);
+            far = any_far(K);
+        }
+        if (!live) continue;
         float2 h[NP], x[NP], ag[NP], xg[NP], a[NP], b[NP];
 #pragma unroll
-        for (int e = 0; e < NP; e += 2) {
-            const float4 v = st[e / 2];
-            h[e] = make_float2(v.x, v.y), h[e + 1] = make_float2(v.z, v.w);
-        }
+        for (int e = 0; e < NP; e += 2) h[e] = make_float2(v[e / 2].x, v[e / 2].y), h[e + 1] = make_float2(v[e / 2].z, v[e / 2].w);
         unpack2(xr, x);
         unpack2(ar, ag);
         unpack2(gr, xg);
@@ -925,10 +930,13 @@ extern "C" gdn_status gdn_linear_recurrence_update(const gdn_linrec_shape* shape
     if (p.N == 0) return GDN_OK;
     if (!state) return GDN_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // as many rows a thread as leave every SM 16 CTAs
-    const int blocks = (p.C / (shape->dtype == GDN_BF16 ? 8 : 4) + 127) / 128;
-    const long long most = (long long)blocks * p.N / (kSMs * 16);
-    const int rows = most < 1 ? 1 : most > 16 ? 16 : (int)most;
+    // Rows a thread: bf16, of which registers hold 5 CTAs an SM, as many as make it one wave, up to 8; fp32 up to 3.  us with 1, 2, 3, 6, 8 rows,
+    // gated, bf16: 128 x 4096 3.8, 3.8, 4.6, 5.9, 7.4; 256 x 4096 7.3, 6.4, 7.4, 10.3, 12.0; 512 x 8192 18.6, 17.8, 17.4, 16.9, 18.1; 2048 x 8192 60.0, 54.5, 53.4,
+    // 52.9, 52.9; fp32: 256 x 2560 4.6, 5.1, 5.8, 8.2, 9.8; 512 x 4096 12.0, 11.6, 11.2, 13.1, 14.1; 2048 x 8192 70.3, 68.3, 68.3, 68.7, 69.0.
+    const bool bf16 = shape->dtype == GDN_BF16;
+    const int blocks = (p.C / (bf16 ? 8 : 4) + 127) / 128, wave = kSMs * (bf16 ? 5 : 12), most = bf16 ? 8 : 3;
+    const long long want = ((long long)blocks * p.N + wave - 1) / wave;
+    const int rows = (int)(want < most ? want : most);
     const unsigned grid = (unsigned)blocks * (unsigned)((p.N + rows - 1) / rows);
     if (shape->dtype == GDN_BF16) linrec_update_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(p, rows);
     else linrec_update_kernel<float><<<grid, 128, 0, s>>>(p, rows);
