@@ -189,6 +189,22 @@ def test_large_updates_agree_with_prompts_of_one_token(dtype, B, C, param, act):
     assert torch.equal(bits(y), bits(z)) and torch.equal(bits(a), bits(b))
 
 
+@pytest.mark.parametrize("dtype,B,C", [(BF, 1001, 4160), (BF, 250, 8200), (F32, 1001, 4164)])
+def test_large_updates_skip_rows_anywhere(dtype, B, C):
+    """Threads that take several rows, with skipped ones first, last and side by side among them."""
+    c = Case([1] * B, C, dtype, 25, act="gelu")
+    slots = torch.randperm(B, generator=torch.Generator().manual_seed(3)).to(torch.int32)
+    slots[::3] = -1
+    slots[7:40] = B
+    idx, keep = slots.to(DEV), (slots >= 0) & (slots < B)
+    a, b = c.h0.clone(), c.h0.clone()
+    out = torch.full((B, C), 7.0, dtype=dtype, device=DEV)
+    y = gdn.gdn_linear_recurrence_fwd(cu_seqlens=c.cu, state=a, state_indices=idx, **c.args())
+    gdn.gdn_linear_recurrence_update(state=b, state_indices=idx, out=out, **c.args())
+    keep = keep.to(DEV)
+    assert torch.equal(bits(out[keep]), bits(y[keep])) and torch.all(out[~keep] == 7) and torch.equal(bits(a), bits(b))
+
+
 @pytest.mark.parametrize("dtype,C,param,xgate,act,scale", GRID)
 def test_update_vs_oracle_and_skips(dtype, C, param, xgate, act, scale):
     B = 11
