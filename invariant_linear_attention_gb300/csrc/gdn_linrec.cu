@@ -145,20 +145,14 @@ __device__ __forceinline__ int ranked(const Params& p, int rank, int threads) {
     return found;
 }
 
-template <typename T, typename F, int CB, int CTAS, Kind KIND>
-__global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_constant__ Params p) {
+// Sequence n over the CTA's channels.
+template <typename T, typename F, int CB, Kind KIND>
+__device__ __forceinline__ void walk_sequence(const Params& p, F& sm, int n, int c0) {
     using Q = Share<T, CB>;
     constexpr int VN = F::VN, NP = Q::NP, CH = F::CH, TT = F::TT, WORK = F::WORK, AHEAD = F::AHEAD, ST = F::ST;
-    extern __shared__ __align__(128) unsigned char raw[];
-    F& sm = *reinterpret_cast<F*>(raw);
-    const int blocks = (p.C + CB - 1) / CB, order = blockIdx.x / blocks, c0 = blockIdx.x % blocks * CB;
-    const int n = p.ranked ? ranked(p, order, F::NT) : order;
     int bos, eos;
     bounds(p.cu, n, p.T, bos, eos);
     const int len = eos - bos, tiles = (len + TT - 1) / TT;
-    if (has_param<KIND>(p) && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
-    __syncthreads();
-
     if (threadIdx.x >= F::WALK) {
         const int tid = threadIdx.x - F::WALK;
         const bool gate = p.z != nullptr;
@@ -310,6 +304,99 @@ __global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_co
         buf = buf + 1 == F::NB ? 0 : buf + 1;
     }
     if (has_slot && threadIdx.x < CB) *st = h;
+}
+
+template <typename F, int CB, Kind KIND>
+__device__ __forceinline__ void load_rates(const Params& p, F& sm, int c0) {
+    if (has_param<KIND>(p) && threadIdx.x < CB) sm.K[threadIdx.x] = c0 + (int)threadIdx.x < p.C ? rate_of(__ldg(p.ap + c0 + threadIdx.x), p.decay) : 0.f;
+    __syncthreads();
+}
+
+template <typename T, typename F, int CB, int CTAS, Kind KIND>
+__global__ void __launch_bounds__(F::NT, CTAS) linrec_fwd_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(128) unsigned char raw[];
+    F& sm = *reinterpret_cast<F*>(raw);
+    const int blocks = (p.C + CB - 1) / CB, order = blockIdx.x / blocks, c0 = blockIdx.x % blocks * CB;
+    const int n = p.ranked ? ranked(p, order, F::NT) : order;
+    load_rates<F, CB, KIND>(p, sm, c0);
+    walk_sequence<T, F, CB, KIND>(p, sm, n, c0);
+}
+
+// Many sequences, most of them short: a CTA for each would cost 2.3 us whatever it holds.  Those of up to kShort tokens go to
+// linrec_short_kernel, a thread a chunk of channels of a sequence; here a CTA takes all the longer ones among sequences g, g + groups, ..
+constexpr int kShort = 32;
+template <typename T, typename F, int CB, int CTAS, Kind KIND>
+__global__ void __launch_bounds__(F::NT, CTAS) linrec_long_kernel(const __grid_constant__ Params p, int groups) {
+    extern __shared__ __align__(128) unsigned char raw[];
+    F& sm = *reinterpret_cast<F*>(raw);
+    const int blocks = (p.C + CB - 1) / CB, g = blockIdx.x / blocks, c0 = blockIdx.x % blocks * CB;
+    bool first = true;
+    for (int64_t base = g; base < p.N; base += 32 * groups) {  // every warp looks at the same 32 sequences
+        const int64_t at = base + (int64_t)(threadIdx.x & 31) * groups;
+        int bos = 0, eos = 0;
+        if (at < p.N) bounds(p.cu, (int)at, p.T, bos, eos);
+        for (unsigned longer = __ballot_sync(0xffffffffu, eos - bos > kShort); longer; longer &= longer - 1) {
+            if (first) load_rates<F, CB, KIND>(p, sm, c0);
+            else __syncthreads();  // the sequence before is through with the buffers
+            first = false;
+            walk_sequence<T, F, CB, KIND>(p, sm, (int)base + (__ffs(longer) - 1) * groups, c0);
+        }
+    }
+}
+// A chain of loads (place, slot, state), then a step a token, the next one's loads under way: 4096 sequences of 1 token x 4096, bf16: 0.40 of HBM.
+template <typename T>
+__global__ void __launch_bounds__(128) linrec_short_kernel(const __grid_constant__ Params p) {
+    constexpr int VN = V16<T>::n, NP = VN / 2;
+    const int chunks = p.C / VN, blocks = (chunks + 127) / 128, ch = blockIdx.x % blocks * 128 + threadIdx.x, c = ch * VN, n = blockIdx.x / blocks;
+    int bos, eos;
+    bounds(p.cu, n, p.T, bos, eos);
+    if (ch >= chunks || eos - bos > kShort) return;
+    const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
+    float4* st = slot >= 0 && slot < p.num_slots ? reinterpret_cast<float4*>(p.state + (int64_t)slot * p.C + c) : nullptr;
+    const bool init = st && (!p.has_init || __ldg(p.has_init + n) != 0);
+    struct Token {
+        uint4 x, ag, xg, z;
+    };
+    auto load = [&](int64_t t) {
+        Token k;
+        k.xg = k.z = make_uint4(0u, 0u, 0u, 0u);
+        k.x = ld16(static_cast<const T*>(p.x) + t * p.ldx + c), k.ag = ld16(static_cast<const T*>(p.ag) + t * p.lda + c);
+        if (p.xg) k.xg = ld16(static_cast<const T*>(p.xg) + t * p.ldg + c);
+        if (p.z) k.z = ld16(static_cast<const T*>(p.z) + t * p.ldz + c);
+        return k;
+    };
+    Token next{};
+    if (bos < eos) next = load(bos);
+    float2 h[NP], K[NP];
+#pragma unroll
+    for (int e = 0; e < NP; e += 2) {
+        const float4 v = init ? st[e / 2] : make_float4(0.f, 0.f, 0.f, 0.f);
+        h[e] = make_float2(v.x, v.y), h[e + 1] = make_float2(v.z, v.w);
+    }
+#pragma unroll
+    for (int e = 0; e < NP; ++e) K[e] = p.ap ? make_float2(rate_of(__ldg(p.ap + c + 2 * e), p.decay), rate_of(__ldg(p.ap + c + 2 * e + 1), p.decay)) : both(0.f);
+    const bool far = any_far(K);
+#pragma unroll 1
+    for (int t = bos; t < eos; ++t) {
+        const Token k = next;
+        if (t + 1 < eos) next = load(t + 1);
+        float2 x[NP], ag[NP], xg[NP], a[NP], b[NP];
+        unpack2(k.x, x);
+        unpack2(k.ag, ag);
+        unpack2(k.xg, xg);
+        steps<kAny>(p, far, K, ag, xg, x, a, b);
+#pragma unroll
+        for (int e = 0; e < NP; ++e) x[e] = h[e] = __ffma2_rn(a[e], h[e], b[e]);
+        if (p.z) {
+            float2 z[NP];
+            unpack2(k.z, z);
+            branch(p.act, z, x);
+        }
+        st16(static_cast<T*>(p.y) + (int64_t)t * p.C + c, pack2(x));
+    }
+    if (!st) return;
+#pragma unroll
+    for (int e = 0; e < NP; e += 2) st[e / 2] = make_float4(h[e].x, h[e].y, h[e + 1].x, h[e + 1].y);
 }
 
 // Single tokens: a thread takes a chunk of channels over `rows` batch rows, so that it works out their rates once.  A launch and a chain
@@ -804,6 +891,12 @@ __global__ void __launch_bounds__(256) linrec_param_kernel(int tiles, int C, flo
     out[c] = K > 0.f ? s * (decay * sp / K) : 0.f;
 }
 
+template <typename T, typename F>
+Params strides(Params q) {
+    constexpr int64_t tile = (int64_t)F::TT * sizeof(T);
+    q.sx = tile * q.ldx, q.sa = tile * q.lda, q.sg = tile * q.ldg, q.sz = tile * q.ldz, q.sy = tile * q.C;
+    return q;
+}
 template <typename T, int CB, int WORKERS, int CTAS>
 gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     using F = FwdTile<T, CB, WORKERS>;
@@ -811,9 +904,7 @@ gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     auto* kernel = kind == kBothGates ? linrec_fwd_kernel<T, F, CB, CTAS, kBothGates> : kind == kForget ? linrec_fwd_kernel<T, F, CB, CTAS, kForget> : linrec_fwd_kernel<T, F, CB, CTAS, kAny>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
     const unsigned ctas = (unsigned)((p.C + CB - 1) / CB) * (unsigned)p.N;
-    Params q = p;
-    constexpr int64_t tile = (int64_t)F::TT * sizeof(T);
-    q.sx = tile * p.ldx, q.sa = tile * p.lda, q.sg = tile * p.ldg, q.sz = tile * p.ldz, q.sy = tile * p.C;
+    Params q = strides<T, F>(p);
     q.ranked = p.N > 1 && p.N <= kRanked && ctas > (unsigned)(kSMs * CTAS) && (long long)p.N * p.N * p.N <= 256LL * p.T;
     kernel<<<ctas, F::NT, sizeof(F), s>>>(q);
     return launch_status();
@@ -829,9 +920,27 @@ gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
 //     1 x 16384 x 8192 (256)                458, 319, 305 / 495, 440, 413
 //     13, 20000 x 2560 (1040)               187, 125, 108 / 194, 167, 156
 //     16, 32768 x 4096 (2048)               461, 307, 264 / 477, 420, 401
+// Short sequences by themselves, in a second launch what is left: worth it where the CTAs that it saves are many.  us so and with a CTA each,
+// bf16, gated: 256 sequences of 1 token x 4096 13.5, 244; 4096 of 1 104, 3892; 1024 of 4 on average 58, 1121; 256 of 16 65, 301, of 32 173, 319,
+// of 64 335, 362, of 128 479, 461; 16 of 1 x 8192 3.6, 35, of 56 65, 54.  fp32 the same way: 256 of 1 13.8, 217, of 32 185, 307, of 64 353, 378, of 128 564, 549.
+template <typename T, int CB, int WORKERS, int CTAS>
+gdn_status launch_many(cudaStream_t s, const Params& p) {
+    const long long cut = (p.C / V16<T>::n + 127) / 128;
+    linrec_short_kernel<T><<<(unsigned)(cut * p.N), 128, 0, s>>>(p);
+    gdn_status st = launch_status();
+    if (st != GDN_OK || p.T <= kShort) return st;
+    using F = FwdTile<T, CB, WORKERS>;
+    const Kind kind = kind_of(p);
+    auto* kernel = kind == kBothGates ? linrec_long_kernel<T, F, CB, CTAS, kBothGates> : kind == kForget ? linrec_long_kernel<T, F, CB, CTAS, kForget> : linrec_long_kernel<T, F, CB, CTAS, kAny>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(F)) != cudaSuccess) return GDN_ERR_CUDA;
+    const int blocks = (p.C + CB - 1) / CB, most = 4 * CTAS * kSMs / blocks, groups = most < 1 ? 1 : most < p.N ? most : p.N;
+    kernel<<<(unsigned)blocks * (unsigned)groups, F::NT, sizeof(F), s>>>(strides<T, F>(p), groups);
+    return launch_status();
+}
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
     const long long n = (long long)((p.C + 31) / 32) * p.N;
+    if (n > 2 * kSMs && p.T < (n > 64 * kSMs ? 128LL : 48LL) * p.N) return launch_many<T, 32, 256, 2>(s, p);
     if (n <= kSMs / 2 || (p.N > 1 && n <= kSMs)) return launch_fwd_of<T, 16, 512, 1>(s, p);
     if (n <= kSMs + kSMs / 8 || (p.N >= 4 && n <= 2 * kSMs + kSMs / 8)) return launch_fwd_of<T, 32, 512, 1>(s, p);
     return launch_fwd_of<T, 32, 256, 2>(s, p);

@@ -189,6 +189,35 @@ def test_large_updates_agree_with_prompts_of_one_token(dtype, B, C, param, act):
     assert torch.equal(bits(y), bits(z)) and torch.equal(bits(a), bits(b))
 
 
+@pytest.mark.parametrize("param,xgate,scale", [(True, True, "sqrt"), (False, False, "linear"), (True, False, "one")])
+@pytest.mark.parametrize("dtype,N,C,every", [(BF, 300, 264, 135), (F32, 300, 260, 135), (BF, 5000, 64, 608), (F32, 40, 9000, 3), (BF, 1, 9800, 1)])
+def test_short_sequences_with_long_ones_among_them(dtype, N, C, every, param, xgate, scale):
+    """Lengths around 32, empty ones, and long ones `every` sequences apart."""
+    lens = [[1, 0, 32, 33, 7, 1, 31, 2][(5 * i) % 8] for i in range(N)]
+    lens[5 % N::every] = [(40 + 97 * i) % 700 if N < 5000 else 300 for i in range(len(lens[5 % N::every]))] if N > 40 else [60] * len(lens[5 % N::every])
+    c = Case(lens, C, dtype, 26, param, xgate, "gelu", scale, strided=True, behind=9)
+    idx = torch.randperm(N + 2, generator=torch.Generator().manual_seed(4))[:N].to(torch.int32)
+    idx[3::11] = -1
+    has = (torch.arange(N) % 3 != 0).to(torch.int32).to(DEV)
+    pool0 = torch.randn(N + 2, C, generator=torch.Generator().manual_seed(5)).to(DEV)
+    pool, out = pool0.clone(), torch.full((sum(lens) + 9, C), 7.0, dtype=dtype, device=DEV)
+    gdn.gdn_linear_recurrence_fwd(cu_seqlens=c.cu, state=pool, state_indices=idx.to(DEV), has_initial_state=has, out=out, **c.args())
+    assert torch.all(out[sum(lens):] == 7)
+    for n in {*range(0, N, max(1, N // 40)), *range(5 % N, N, max(every, N // 20)), 3 % N}:
+        t, slot = slice(c.cu_list[n], c.cu_list[n + 1]), int(idx[n])
+        st = pool0[slot:slot + 1].clone() if slot >= 0 and has[n] else torch.zeros(1, C, device=DEV)
+        y = []
+        for k in range(t.start, t.stop, 257):  # alone, in chained calls
+            part = slice(k, min(k + 257, t.stop))
+            y.append(gdn.gdn_linear_recurrence_fwd(cu_seqlens=torch.tensor([0, part.stop - k], dtype=torch.int32, device=DEV), state=st, **c.args(part)))
+        if y:
+            assert torch.equal(bits(torch.cat(y)), bits(out[t])), n
+        if slot >= 0:
+            assert torch.equal(bits(st[0]), bits(pool[slot])), n
+    spare = sorted(set(range(N + 2)) - set(idx.tolist()))
+    assert torch.equal(bits(pool[spare]), bits(pool0[spare]))
+
+
 @pytest.mark.parametrize("dtype,B,C", [(BF, 1001, 4160), (BF, 250, 8200), (F32, 1001, 4164)])
 def test_large_updates_skip_rows_anywhere(dtype, B, C):
     """Threads that take several rows, with skipped ones first, last and side by side among them."""
