@@ -909,17 +909,6 @@ gdn_status launch_fwd_of(cudaStream_t s, const Params& p) {
     kernel<<<ctas, F::NT, sizeof(F), s>>>(q);
     return launch_status();
 }
-// Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16 and gated, 7 ns with 16 channels and 512 workers, 10 ns
-// with 32 and 512, 12 ns with 32 and 256, and 19 ns each of two of the last kind on one SM; a batch of several sequences ends with its
-// longest alone.  us with the three forms, bf16 / fp32:
-//     1 x 16384 x 1024 (n = 32)             115, 161, 201 / 123, 191, 263
-//     1 x 16384 x 4096 (128)                230, 162, 203 / 240, 210, 279
-//     3 ragged, 16000 x 1600 (150)           90,  95, 118 /  97, 120, 159
-//     2, 8000 x 2560 (160)                   85,  68,  78 /  91,  87,  95
-//     4, 8192 x 2048 (256)                   66,  49,  65 /  69,  63,  79
-//     1 x 16384 x 8192 (256)                458, 319, 305 / 495, 440, 413
-//     13, 20000 x 2560 (1040)               187, 125, 108 / 194, 167, 156
-//     16, 32768 x 4096 (2048)               461, 307, 264 / 477, 420, 401
 // Short sequences by themselves, in a second launch what is left: worth it where the CTAs that it saves are many.  us so and with a CTA each,
 // bf16, gated: 256 sequences of 1 token x 4096 13.5, 244; 4096 of 1 104, 3892; 1024 of 4 on average 58, 1121; 256 of 16 65, 301, of 32 173, 319,
 // of 64 335, 362, of 128 479, 461; 16 of 1 x 8192 3.6, 35, of 56 65, 54.  fp32 the same way: 256 of 1 13.8, 217, of 32 185, 307, of 64 353, 378, of 128 564, 549.
@@ -937,6 +926,17 @@ gdn_status launch_many(cudaStream_t s, const Params& p) {
     kernel<<<(unsigned)blocks * (unsigned)groups, F::NT, sizeof(F), s>>>(strides<T, F>(p), groups);
     return launch_status();
 }
+// Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16 and gated, 7 ns with 16 channels and 512 workers, 10 ns
+// with 32 and 512, 12 ns with 32 and 256, and 19 ns each of two of the last kind on one SM; a batch of several sequences ends with its
+// longest alone.  us with the three forms, bf16 / fp32:
+//     1 x 16384 x 1024 (n = 32)             115, 161, 201 / 123, 191, 263
+//     1 x 16384 x 4096 (128)                230, 162, 203 / 240, 210, 279
+//     3 ragged, 16000 x 1600 (150)           90,  95, 118 /  97, 120, 159
+//     2, 8000 x 2560 (160)                   85,  68,  78 /  91,  87,  95
+//     4, 8192 x 2048 (256)                   66,  49,  65 /  69,  63,  79
+//     1 x 16384 x 8192 (256)                458, 319, 305 / 495, 440, 413
+//     13, 20000 x 2560 (1040)               187, 125, 108 / 194, 167, 156
+//     16, 32768 x 4096 (2048)               461, 307, 264 / 477, 420, 401
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
     const long long n = (long long)((p.C + 31) / 32) * p.N;
