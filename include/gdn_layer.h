@@ -231,7 +231,8 @@ gdn_status gdn_add_rmsnorm_fp8(const gdn_add_norm_shape* shape, const void* x, c
  * s (residual_out of the forward, or its x; ldx), d_y and d_residual_out (NULL:
  * zero) [rows, d] dense, dx [rows, d] dense in dtype, which is the gradient of x and of
  * residual alike, and dweight [d] fp32 (NULL: not written, and no workspace is needed).  dx may alias d_y,
- * d_residual_out or (dense) s.  fp32 sums in an order fixed by the shape.
+ * d_residual_out or (dense) s.  Without rows dweight is 0 (and weight is needed all the same).  fp32 sums in an order
+ * fixed by the shape.
  * shape->group and ldr are not read.
  */
 size_t gdn_add_rmsnorm_bwd_workspace_size(const gdn_add_norm_shape* shape);

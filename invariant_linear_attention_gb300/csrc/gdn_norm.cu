@@ -500,7 +500,8 @@ extern "C" gdn_status gdn_add_rmsnorm_bwd(const gdn_add_norm_shape* shape, const
     gdn_status st = check_norm(shape);
     if (st != GDN_OK) return st;
     const bool rows = shape->rows > 0;
-    if (rows && (!s || !weight || !d_y || !dx)) return GDN_ERR_INVALID_ARG;
+    if (rows && (!s || !d_y || !dx)) return GDN_ERR_INVALID_ARG;
+    if ((rows || dweight) && !weight) return GDN_ERR_INVALID_ARG;  // without rows dweight is written by the same kernels, which read the weight
     if (!aligned16(s) || !aligned16(weight) || !aligned16(d_y) || !aligned16(d_residual_out) || !aligned16(dx) || !aligned16(dweight)) return GDN_ERR_INVALID_ARG;
     if (rows && dx == s && shape->ldx != shape->d) return GDN_ERR_INVALID_ARG;
     if (dweight && (!workspace || !aligned16(workspace) || workspace_bytes < gdn_add_rmsnorm_bwd_workspace_size(shape))) return GDN_ERR_WORKSPACE;

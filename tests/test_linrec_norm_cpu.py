@@ -228,3 +228,12 @@ def test_binding_refuses_before_the_library():
                         (ValueError, lambda: gdn.gdn_add_rmsnorm_fp8(x, w)), (ValueError, lambda: gdn.gdn_add_rmsnorm_bwd(x, w, x))):
         with pytest.raises(error):
             call()
+
+
+def test_norm_gradient_of_no_rows_needs_the_weight_of_dweight(lib):
+    """With no rows dweight is still written, by a kernel that reads the weight; without dweight there is nothing to do."""
+    b = ptrs("s", "w", "dy", "dr", "dx", "dw", "ws")
+    for d, dtype in ((64, binding.GDN_BF16), (4, binding.GDN_F32), (16384, binding.GDN_BF16)):
+        s = norm_shape(rows=0, d=d, dtype=dtype, ldx=d)
+        assert lib.gdn_add_rmsnorm_bwd(ctypes.byref(s), *dict(b, w=None).values(), 1 << 40, None) == INVALID
+        assert lib.gdn_add_rmsnorm_bwd(ctypes.byref(s), *dict.fromkeys(b, None).values(), 0, None) == 0
