@@ -246,12 +246,13 @@ __device__ __forceinline__ void walk_sequence(const Params& p, F& sm, int n, int
     }
 
     const int cl = threadIdx.x % CB, c = c0 + cl;
-    const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);  // (with 16 channels a second half of the lanes does the same)
-    const bool has_slot = c < p.C && slot >= 0 && slot < p.num_slots;
+    const bool walks = CB == F::WALK || threadIdx.x < CB;  // with 16 channels the other half of the warp passes the barriers only
+    const int slot = !p.state ? -1 : (p.idx ? __ldg(p.idx + n) : n);
+    const bool has_slot = walks && c < p.C && slot >= 0 && slot < p.num_slots;
     float* st = p.state + (int64_t)slot * p.C + c;
     float h = has_slot && (!p.has_init || __ldg(p.has_init + n) != 0) ? *st : 0.f;
     for (int i = 0, buf = 0; i < tiles; ++i) {
-        const int here = min(TT, len - i * TT);
+        const int here = walks ? min(TT, len - i * TT) : 0;
         bar_sync(F::kFull + buf, F::NT);
         // S sets of V units in registers: while one is walked, the loads of the others are under way (at the end they read on
         // into what follows, unused).
@@ -300,10 +301,11 @@ __device__ __forceinline__ void walk_sequence(const Params& p, F& sm, int n, int
                 pb[u][F::unit(u, cl)] = make_float4(o[0], o[1], o[2], 0.f);
             }
         }
+        if (CB != F::WALK) __syncwarp();
         bar_arrive(F::kDone + buf, F::NT);
         buf = buf + 1 == F::NB ? 0 : buf + 1;
     }
-    if (has_slot && threadIdx.x < CB) *st = h;
+    if (has_slot) *st = h;
 }
 
 template <typename F, int CB, Kind KIND>

@@ -179,6 +179,19 @@ def test_large_batches_agree_with_a_sequence_alone(dtype, N, C, longest):
         assert torch.equal(bits(alone), bits(y[t])) and torch.equal(bits(st[0]), bits(pool[n])), n
 
 
+@pytest.mark.parametrize("dtype,C,lens", [(BF, 24, [521, 2, 259]), (F32, 20, [263, 0, 130, 5]), (BF, 1032, [258]), (F32, 36, [1, 2, 3])])
+def test_few_channels_walk_as_single_tokens_do(dtype, C, lens):
+    """Batches of few CTAs, a half of a warp for each: whole and part tiles, units and channel blocks."""
+    c = Case(lens, C, dtype, 27, act="silu")
+    pool, st = c.h0.clone(), c.h0.clone()
+    y = gdn.gdn_linear_recurrence_fwd(cu_seqlens=c.cu, state=pool, **c.args())
+    for n, (lo, hi) in enumerate(zip(c.cu_list, c.cu_list[1:])):
+        slot = torch.tensor([n], dtype=torch.int32, device=DEV)
+        one = [gdn.gdn_linear_recurrence_update(state=st, state_indices=slot, **c.args(slice(t, t + 1))) for t in range(lo, hi)]
+        assert not one or torch.equal(bits(torch.cat(one)), bits(y[lo:hi])), n
+    assert torch.equal(bits(st), bits(pool))
+
+
 @pytest.mark.parametrize("dtype,B,C", [(BF, 300, 4160), (F32, 150, 4164), (F32, 37, 1000), (BF, 1, 8)])
 @pytest.mark.parametrize("param,act", [(True, "gelu"), (False, "silu"), (True, "")])
 def test_large_updates_agree_with_prompts_of_one_token(dtype, B, C, param, act):
