@@ -77,7 +77,8 @@ constexpr float kTop = 448.f, kLeast = 1.17549435e-38f;  // e4m3's largest value
 
 // A group's scale and the factor that takes its values t = s w to 8 bits.  The scale is the norm's r max|t| / 448, but the
 // values go by 448 / max|t|: r's error and a rounding each stay out of them.  The reciprocal is the hardware's with
-// a step of Newton's method.  (Where that is past fp32, in a group of next to nothing, the values are multiplied by r first.)
+// a step of Newton's method.  (Where that is past fp32, in a group of next to nothing, and where the scale is the smallest one and
+// not the group's, the values are multiplied by r and go by the scale.)
 struct Scale {
     float scale, by;
     bool tiny;
@@ -93,8 +94,9 @@ struct Scale {
 };
 __device__ __forceinline__ Scale scale_of(float most, float r) {
     Scale s;
-    s.scale = fmaxf(__fmul_rn(__fmul_rn(most, r), 1.f / kTop), kLeast);
-    s.tiny = !(most > 1e-30f);
+    const float own = __fmul_rn(__fmul_rn(most, r), 1.f / kTop);
+    s.scale = fmaxf(own, kLeast);
+    s.tiny = !(most > 1e-30f && own > kLeast);
     const float x = s.tiny ? s.scale : most, y = rcp_approx(x);
     const float z = __fmaf_rn(y, __fmaf_rn(-x, y, 1.f), y);
     s.by = __fmaf_rn(r, 0.f, s.tiny ? y : __fmul_rn(kTop, most < 1e38f ? z : y));  // a row whose r is not a number has no values

@@ -16,7 +16,7 @@ import invariant_linear_attention_gb300 as gdn
 from oracle import layer_ops
 from oracle import linrec_ops
 from helpers import BF16_ROUND, normwise, to_np
-from test_linrec import BF, DEV, F32, U, bits
+from test_linrec import BF, DEV, F32, INF, U, bits
 
 pytestmark = pytest.mark.gpu
 
@@ -176,6 +176,28 @@ def test_values_far_out():
         g = gdn.gdn_add_rmsnorm_bwd(s, w, d4, eps=0.0)
         within(g["dx"], dx, mx, 3 * 256 + 32, F32)
         within(g["dweight"], dw, mw, 3 * 256 + 36, F32)
+
+
+@pytest.mark.parametrize("dtype,d", [(F32, 256), (BF, 512), (F32, 8196)])
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_fp8_values_go_by_the_stored_scale(dtype, d, group):
+    """Groups whose scale is the smallest one, 2^-126: y is still value / scale.  Rows whose sum of squares is past fp32 have a norm of 0."""
+    x = torch.randn(4, d, generator=torch.Generator().manual_seed(15))
+    x[0, 3], x[1, 5], x[2], x[3] = INF, 1e20, x[2] * 1e-20, x[3] * 1e-24
+    x[2:, 0] = 1e17  # r: sqrt(d) 1e-17; values of 1e-35 to 1e-39 behind it
+    x = x.to(dtype).to(DEV)
+    w = (1 + 0.1 * torch.randn(d, generator=torch.Generator().manual_seed(16))).to(DEV)
+    q, k, _ = gdn.gdn_add_rmsnorm_fp8(x, w, eps=0.0, group=group)
+    q, least = q.float(), 2.0 ** -126
+    assert torch.isnan(q[0, 3]) and torch.all(q[0, 4:] == 0) and torch.all(q[0, :3] == 0) and torch.all(q[1] == 0) and torch.all(k[:2] == least)
+    n = layer_ops.add_rmsnorm(x[2:], w, 0.0)
+    want = layer_ops.group_scales(n, group)
+    assert group == 0 or np.any(want == least)
+    within(k[2:], want, want, d / 2 + 12, F32)
+    each = np.repeat(want, group or d, axis=1)[:, :d]
+    # half a step of e4m3, and the value's own error (module docstring); below 2^-126 the product s w r may lose half of 2^-149
+    err = np.abs(to_np(q[2:]) * each - n)
+    assert np.all(err <= np.maximum(2.0 ** -4 * np.abs(n), 2.0 ** -10 * each) + (d + 28) * U * np.abs(n) + 2.0 ** -149)
 
 
 def test_offsets_past_2_31():
