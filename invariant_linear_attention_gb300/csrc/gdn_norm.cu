@@ -460,7 +460,8 @@ gdn_status norm_fwd(const gdn_add_norm_shape* shape, const void* x, const void* 
     if (shape->rows == 0) return GDN_OK;
     if (!x || !w || !y || (res && !res_out) || (fp8 && !scales)) return GDN_ERR_INVALID_ARG;
     if (res && (shape->ldr < shape->d || shape->ldr % vn)) return GDN_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(res) || !aligned16(w) || !aligned16(res_out) || !aligned16(y) || !aligned4(scales)) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(res) || !aligned16(w) || !aligned16(res_out) || !aligned4(scales)) return GDN_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(y) & (fp8 ? 7u : 15u)) return GDN_ERR_INVALID_ARG;  // 8 bits: a chunk's values are one store of 8 or 4 bytes
     const void* to[] = {y, res ? res_out : nullptr};
     for (int i = fp8 ? 1 : 0; i < 2; ++i)
         if (to[i] && ((to[i] == x && shape->ldx != shape->d) || (to[i] == res && shape->ldr != shape->d))) return GDN_ERR_INVALID_ARG;

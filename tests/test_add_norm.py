@@ -137,6 +137,21 @@ def test_in_place(dtype, d):
         assert got is v[which] and torch.equal(bits(got), bits(g))
 
 
+@pytest.mark.parametrize("dtype,d,group", [(BF, 72, 32), (F32, 72, 0), (BF, 4096, 128), (F32, 1160, 64)])
+def test_fp8_out_at_8_bytes(dtype, d, group):
+    """y in 8 bits needs 8-byte alignment only."""
+    x, r, w, _, _ = inputs(5, d, dtype, 17)
+    q, k, _ = gdn.gdn_add_rmsnorm_fp8(x, w, residual=r, group=group)
+    whole = torch.full((5 * d + 24,), 0x55, dtype=torch.uint8, device=DEV)
+    out = whole[8:8 + 5 * d].view(torch.float8_e4m3fn).view(5, d)
+    got, k2, _ = gdn.gdn_add_rmsnorm_fp8(x, w, residual=r, group=group, out=out)
+    assert got is out and out.data_ptr() % 16 == 8
+    assert torch.equal(out.view(torch.uint8), q.view(torch.uint8)) and torch.equal(k, k2)
+    assert torch.all(whole[:8] == 0x55) and torch.all(whole[8 + 5 * d:] == 0x55)
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_add_rmsnorm_fp8(x, w, residual=r, group=group, out=whole[4:4 + 5 * d].view(torch.float8_e4m3fn).view(5, d))
+
+
 def test_no_rows_and_leading_dimensions():
     w = torch.ones(64, device=DEV)
     for shape in ((0, 64), (2, 0, 64)):

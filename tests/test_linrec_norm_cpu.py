@@ -237,3 +237,12 @@ def test_norm_gradient_of_no_rows_needs_the_weight_of_dweight(lib):
         s = norm_shape(rows=0, d=d, dtype=dtype, ldx=d)
         assert lib.gdn_add_rmsnorm_bwd(ctypes.byref(s), *dict(b, w=None).values(), 1 << 40, None) == INVALID
         assert lib.gdn_add_rmsnorm_bwd(ctypes.byref(s), *dict.fromkeys(b, None).values(), 0, None) == 0
+
+
+def test_norm_output_alignment(lib):
+    """8 bytes for y in 8 bits, 16 in the input's type."""
+    p = ptrs("x", "res", "w", "ro", "y")
+    for off in (1, 2, 4, 12):
+        assert norm_calls(lib, norm_shape(), dict(p, y=p["y"] + off)) == (INVALID, INVALID)
+    v = [dict(p, y=p["y"] + 8)[k] for k in ("x", "res", "w", "ro", "y")]
+    assert lib.gdn_add_rmsnorm(ctypes.byref(norm_shape()), *v, None) == INVALID
