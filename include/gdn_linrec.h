@@ -20,7 +20,8 @@
  * (1 - a)(1 + a), so that decays next to 1 keep their inputs' scale (1 - a
  * below 2^-126 counts as 0).  An
  * a_gate of -inf under an a_param keeps the state and takes nothing in (scale
- * sqrt and linear); without an a_param it forgets the state.
+ * sqrt and linear); without an a_param it forgets the state, and +inf keeps it
+ * bit for bit.  A decay is never above 1.
  *
  * Invariance.  The bits of y and of the final state of a sequence depend only
  * on that sequence's own inputs: not on the batch around it, and not on

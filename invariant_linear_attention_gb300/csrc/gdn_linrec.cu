@@ -735,8 +735,9 @@ __global__ void __launch_bounds__(GradTile<T>::NT, GradTile<T>::GRAD) linrec_bwd
                 for (int i = 0; i < NP; ++i) w2[i] = __fmul2_rn(K[i], r[i]), k[i] = __fmul2_rn(w2[i], both(-1.f));
                 decays(any_far(K), w2, a, m);
             } else {
+                forget(r, rest, a);
 #pragma unroll
-                for (int i = 0; i < NP; ++i) a[i] = r[i], m[i] = rest[i], k[i] = m[i], rest[i] = both(1.f);
+                for (int i = 0; i < NP; ++i) m[i] = rest[i], k[i] = m[i], rest[i] = both(1.f);
             }
 #pragma unroll
             for (int i = 0; i < NP; ++i) da1[i] = __fmul2_rn(a[i], k[i]);

@@ -96,6 +96,17 @@ __device__ __forceinline__ void one_sigmoid(const float2 (&g)[NP], float2 (&r)[N
     }
 }
 
+// The decay without an a_param, sigmoid(g).  Next to 1 it is 1 minus its rest r1, rounded once, and so never past 1: r, from the reciprocal that two
+// gates share, is up to an ulp off 1 on either side, which a kept state would take at every token (4096 open gates: 5e-4 of it).
+template <int NP>
+__device__ __forceinline__ void forget(const float2 (&r)[NP], const float2 (&r1)[NP], float2 (&a)[NP]) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const float2 o = __ffma2_rn(r1[k], both(-1.f), both(1.f));
+        a[k] = make_float2(r1[k].x < 0.5f ? o.x : r[k].x, r1[k].y < 0.5f ? o.y : r[k].y);
+    }
+}
+
 // m = 1 - e^-w and a = e^-w for w >= 0.  Below 1/4: m = w + w^2 q(w), q the interpolation of (1 - e^-w - w) / w^2 of
 // degree 3 at Chebyshev's nodes on [0, 1/4] (1.2e-8 of m), and a = 1 - m, rounded once.  Above: a by the
 // hardware exponential and m = 1 - a.  w = K r is at most K: channels with K below 1/4 have no far tokens.
@@ -224,8 +235,9 @@ __device__ __forceinline__ void steps(const Params& p, bool far, const float2 (&
         for (int e = 0; e < NP; ++e) w[e] = __fmul2_rn(K[e], r[e]);
         decays(far, w, a, m);
     } else {
+        forget(r, r1, a);
 #pragma unroll
-        for (int e = 0; e < NP; ++e) a[e] = r[e], m[e] = r1[e];
+        for (int e = 0; e < NP; ++e) m[e] = r1[e];
     }
     if (scale_of<KIND>(p) == GDN_SCALE_SQRT) {
 #pragma unroll

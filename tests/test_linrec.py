@@ -350,6 +350,42 @@ def test_gates_far_out(dtype, scale):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("scale", ["sqrt", "linear"])
+@pytest.mark.parametrize("xgate", [True, False])
+def test_open_forget_gates_keep_the_state(dtype, scale, xgate):
+    """Without an a_param a gate of +inf, or of 30 and nothing taken in, keeps the state's bits whatever x_gate is, and the
+    gradient's; no gate makes it grow.  Gates of 12: a state of 1 stays within [0.97, 1], where a token's two roundings, of a = 1 - 6e-6
+    and of the product, are half of u = 2^-24 each."""
+    C, T = 1024, 4096
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    x = torch.zeros(T, C, dtype=dtype, device=DEV)
+    xg = torch.linspace(-12, 12, C, device=DEV).to(dtype).expand(T, C).contiguous() if xgate else None
+    one = torch.ones(1, C, device=DEV)
+
+    def run(gate, state, x=x):
+        ag = torch.full((T, C), gate, dtype=dtype, device=DEV)
+        y = gdn.gdn_linear_recurrence_fwd(x, ag, cu, x_gate=xg, state=state, input_scale=scale)
+        return y, gdn.gdn_linear_recurrence_bwd(x, ag, cu, torch.zeros_like(x), x_gate=xg, init_state=one, d_final_state=one, input_scale=scale)["d_init_state"]
+
+    for gate in (INF, 100.0, 30.0):
+        st = one.clone()
+        y, d_init = run(gate, st, torch.randn(T, C, device=DEV).to(dtype) if gate == INF else x)
+        assert torch.equal(st, one) and torch.all(y == 1) and torch.equal(d_init, one), gate
+        st, ag = one.clone(), torch.full((1, C), gate, dtype=dtype, device=DEV)
+        for _ in range(3):
+            gdn.gdn_linear_recurrence_update(x[:1], ag, st, x_gate=None if xg is None else xg[:1], input_scale=scale)
+        assert torch.equal(st, one), gate
+    for gate in (0.0, 1.0, 4.0, 8.0, 16.0):
+        st = one.clone()
+        _, d_init = run(gate, st)
+        assert torch.all(st <= 1) and torch.all(d_init <= 1), gate
+    st = one.clone()
+    _, d_init = run(12.0, st)
+    want = np.exp(-T * np.logaddexp(0, -12.0))
+    assert np.abs(to_np(st) - want).max() < 1.1 * T * U and np.abs(to_np(d_init) - want).max() < 1.1 * T * U
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_decays_next_to_one(dtype):
     """1 - a and 1 - a^2 keep their relative accuracy: with K = 8e-6 and less they are past what a's own rounding shows."""
     c = Case([64, 3], 16, dtype, 33)
