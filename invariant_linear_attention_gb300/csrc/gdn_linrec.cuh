@@ -109,7 +109,8 @@ __device__ __forceinline__ void forget(const float2 (&r)[NP], const float2 (&r1)
 
 // m = 1 - e^-w and a = e^-w for w >= 0.  Below 1/4: m = w + w^2 q(w), q the interpolation of (1 - e^-w - w) / w^2 of
 // degree 3 at Chebyshev's nodes on [0, 1/4] (1.2e-8 of m), and a = 1 - m, rounded once.  Above: a by the
-// hardware exponential and m = 1 - a.  w = K r is at most K: channels with K below 1/4 have no far tokens.
+// hardware exponential and m = 1 - a.  w = K r, and r, an approximation, is past 1 by 2^-22 at most: channels whose K is below 1/4
+// by 2^-20 of it have no far tokens.
 constexpr float kNear = 0.25f;
 __device__ __forceinline__ float2 near2(const float2& w) {
     float2 q = __ffma2_rn(both(0.00767176877707243f), w, both(-0.041564859449863434f));
@@ -210,7 +211,7 @@ __device__ __forceinline__ bool any_far(const float2 (&K)[NP]) {
     float most = 0.f;
 #pragma unroll
     for (int e = 0; e < NP; ++e) most = fmaxf(most, fmaxf(K[e].x, K[e].y));
-    return most >= kNear;
+    return most >= kNear * (1.f - 0x1p-20f);
 }
 
 // a and b of NP pairs (neighbouring channels, or one channel's tokens).  Options are branches around whole loops, so that

@@ -351,6 +351,27 @@ def test_gates_far_out(dtype, scale):
 
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("scale", ["sqrt", "linear"])
+def test_exponents_around_a_quarter_have_one_form(dtype, scale):
+    """K = decay softplus(a_param) just below and above 1/4, where 1 - e^-w goes from one form to the other, beside channels far past
+    it: which channels share a thread differs between a prompt and single tokens, the bits do not."""
+    C, T = 2048, 192
+    # softplus(0) = log 2; from -1e-6 to 1e-6 it takes every fp32 value there, K some ulp each
+    ap = torch.linspace(-1e-6, 1e-6, C, device=DEV)
+    ap[::8], ap[5::16] = 8.0, 8.0
+    gen = torch.Generator().manual_seed(28)
+    x, xg = (torch.randn(T, C, generator=gen).mul(4).to(dtype).to(DEV) for _ in range(2))
+    ag = torch.full((T, C), 30.0, dtype=dtype, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    for k in range(-2, 3):  # decays a few ulp apart
+        kw = dict(a_param=ap, input_scale=scale, decay=float(np.float32(0.25 / np.log(2)) * (1 + k * 2.0 ** -23)))
+        a, b = torch.zeros(1, C, device=DEV), torch.zeros(1, C, device=DEV)
+        y = gdn.gdn_linear_recurrence_fwd(x, ag, cu, x_gate=xg, state=a, **kw)
+        z = torch.cat([gdn.gdn_linear_recurrence_update(x[t:t + 1], ag[t:t + 1], b, x_gate=xg[t:t + 1], **kw) for t in range(T)])
+        assert torch.equal(bits(y), bits(z)) and torch.equal(bits(a), bits(b)), k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("scale", ["sqrt", "linear"])
 @pytest.mark.parametrize("xgate", [True, False])
 def test_open_forget_gates_keep_the_state(dtype, scale, xgate):
     """Without an a_param a gate of +inf, or of 30 and nothing taken in, keeps the state's bits whatever x_gate is, and the
