@@ -28,11 +28,12 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
     return r;
 }
 
-// K of a channel.  Past fp32's range the largest finite value stands for it: a gate that is not 0
-// still forgets at once, but a gate of 0 keeps the state and is not 0 times infinity.
+// K of a channel.  Near and past fp32's range kMost stands for it: a gate that is not 0 still forgets at once, but a gate of 0 keeps
+// the state and is not 0 times infinity, and K r stays finite where r rounds past 1 (the gradient's e^-w w is not 0 times infinity).
+constexpr float kMost = 3e38f;
 __device__ __forceinline__ float rate_of(float a_param, float decay) {
     const float k = __fmul_rn(decay, __fadd_rn(fmaxf(a_param, 0.f), log1pf(expf(-fabsf(a_param)))));
-    return k > FLT_MAX ? FLT_MAX : k;
+    return k > kMost ? kMost : k;
 }
 
 // 1 / (1 + 2^v), and 2^v.

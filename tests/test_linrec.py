@@ -423,6 +423,27 @@ def test_decays_next_to_one(dtype):
     assert all(torch.isfinite(v).all() for v in g.values() if v is not None)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("ap", [INF, 3e38, 4.25e37, 1e30])
+def test_rates_at_the_end_of_the_range(dtype, ap):
+    """K = 8 a_param past fp32's range, or near its end: open gates forget at once, with gradients of 0 and none that is NaN, whatever x_gate is."""
+    C, T = 4096, 5
+    xg = torch.linspace(-12, 12, C, device=DEV).to(dtype).expand(T, C).contiguous()
+    x, one = torch.ones(T, C, dtype=dtype, device=DEV), torch.ones(1, C, device=DEV)
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    for gate in (INF, 30.0, 5.0, 0.0):
+        ag = torch.full((T, C), gate, dtype=dtype, device=DEV)
+        kw = dict(a_param=torch.full((C,), ap, device=DEV), x_gate=xg)
+        st = 3 * one
+        y = gdn.gdn_linear_recurrence_fwd(x, ag, cu, state=st, **kw)
+        want = torch.sigmoid(xg.double())
+        bound = (2 * 12 + 10) * U + (BF16_ROUND if dtype == BF else U)  # x sigmoid(x_gate), s = 1 (module docstring)
+        assert torch.all((y.double() - want).abs() <= bound * want)
+        g = gdn.gdn_linear_recurrence_bwd(x, ag, cu, x, init_state=one, **kw)
+        assert torch.all(g["da_gate"] == 0) and torch.all(g["da_param"] == 0) and torch.all(g["d_init_state"] == 0)
+        assert torch.all((g["dx"].double() - want).abs() <= bound * want) and torch.isfinite(g["dx_gate"]).all()
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 def test_branch_values_far_out(act):
     """z up to the type's range: act(z) is z or 0, its slope 1 or 0."""
