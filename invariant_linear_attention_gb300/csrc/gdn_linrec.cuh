@@ -36,6 +36,13 @@ __device__ __forceinline__ float rate_of(float a_param, float decay) {
     return k > kMost ? kMost : k;
 }
 
+// The largest of three, or NaN if one is.
+__device__ __forceinline__ float most_or_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // 1 / (1 + 2^v), and 2^v.
 __device__ __forceinline__ float2 logistic2(const float2& v, float2& e) {
     e = make_float2(ex2(v.x), ex2(v.y));
@@ -51,7 +58,8 @@ __device__ __forceinline__ void apart(float e, float& r, float& r1) {
 
 // sigmoid(g) = r and sigmoid(i) = p with one reciprocal for both, 1 / ((1 + 2^v) (1 + 2^u)): the special function unit, which
 // takes two cycles a warp for a reciprocal or a root and one for an exponential, bounds the prompts' kernel next to HBM.
-// r1, p1: 1 - r and 1 - p.  Where a power is past 2^60 and their product might leave fp32's range, each has its own.
+// r1, p1: 1 - r and 1 - p.  Where a power is past 2^60 and their product might leave fp32's range, or one is not a number and would
+// make the other gate's sigmoid so too, each has its own.
 template <int NP>
 __device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2 (&i)[NP], float2 (&r)[NP], float2 (&p)[NP], float2 (&r1)[NP], float2 (&p1)[NP]) {
     float2 e[NP], f[NP];
@@ -59,7 +67,7 @@ __device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
         const float2 v = __fmul2_rn(g[k], both(-kLog2e)), u = __fmul2_rn(i[k], both(-kLog2e));
-        most = fmaxf(fmaxf(most, fmaxf(v.x, v.y)), fmaxf(u.x, u.y));
+        most = most_or_nan(most_or_nan(most, v.x, v.y), u.x, u.y);
         e[k] = make_float2(ex2(v.x), ex2(v.y)), f[k] = make_float2(ex2(u.x), ex2(u.y));
     }
 #pragma unroll
@@ -69,11 +77,11 @@ __device__ __forceinline__ void two_sigmoids(const float2 (&g)[NP], const float2
         r[k] = __fmul2_rn(R, c), p[k] = __fmul2_rn(R, d);
         r1[k] = __fmul2_rn(e[k], r[k]), p1[k] = __fmul2_rn(f[k], p[k]);
     }
-    if (most > 60.f) {
+    if (!(most <= 60.f)) {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            if (fmaxf(e[k].x, f[k].x) > kFar) apart(e[k].x, r[k].x, r1[k].x), apart(f[k].x, p[k].x, p1[k].x);
-            if (fmaxf(e[k].y, f[k].y) > kFar) apart(e[k].y, r[k].y, r1[k].y), apart(f[k].y, p[k].y, p1[k].y);
+            if (!(most_or_nan(0.f, e[k].x, f[k].x) <= kFar)) apart(e[k].x, r[k].x, r1[k].x), apart(f[k].x, p[k].x, p1[k].x);
+            if (!(most_or_nan(0.f, e[k].y, f[k].y) <= kFar)) apart(e[k].y, r[k].y, r1[k].y), apart(f[k].y, p[k].y, p1[k].y);
         }
     }
 }

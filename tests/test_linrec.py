@@ -477,6 +477,36 @@ def test_nan_stays_in_its_sequence_and_channel():
     assert torch.equal(bits(g2["da_param"][rest]), bits(g["da_param"][rest]))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("param,scale", [(True, "sqrt"), (False, "linear"), (True, "one")])
+@pytest.mark.parametrize("which", ["xg", "ag"])
+def test_nan_in_one_gate_leaves_the_other(dtype, param, scale, which):
+    """A gate that is not a number reaches what the definition says and nothing else: not the other gate's sigmoid, and so not the
+    gradients of the tokens before (x_gate) or behind (a_gate)."""
+    lens, at, C = [70, 90, 20], 110, 24
+    c = Case(lens, C, dtype, 35, param, act="silu", scale=scale)
+    call = lambda: (gdn.gdn_linear_recurrence_fwd(cu_seqlens=c.cu, **c.args()),  # noqa: E731
+                    gdn.gdn_linear_recurrence_bwd(cu_seqlens=c.cu, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args()))
+    y0, g0 = call()
+    getattr(c, which)[at, 5] = float("nan")
+    y, g = call()
+    with np.errstate(invalid="ignore"):
+        want = ref.linear_recurrence_bwd(cu=c.cu_list, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args())
+        wy, _ = ref.linear_recurrence(cu=c.cu_list, init_state=c.h0, **c.args())
+    assert np.array_equal(np.isnan(to_np(y)), np.isnan(wy))
+    ok = ~torch.isnan(y)
+    assert torch.equal(y[ok], y0[ok])
+    for k in ("dx", "da_gate", "dx_gate", "dz", "d_init_state") + (("da_param",) if param else ()):
+        nan = np.isnan(want[k])
+        assert np.array_equal(np.isnan(to_np(g[k])), nan), k
+        if k != "da_param":
+            assert nan.any() == (k != "d_init_state" or which == "ag") and not nan.all()
+        ok = torch.from_numpy(~nan).to(DEV)
+        if which == "ag" and k in ("dx", "dx_gate"):
+            ok[at, 5] = False  # dx, dx_gate: p by its own reciprocal here
+        assert torch.equal(g[k][ok], g0[k][ok]), k
+
+
 # ---------------------------------------------------------------- rows, slots, streams, refusals
 
 def test_rows_behind_the_last_sequence_are_neither_read_nor_written():
