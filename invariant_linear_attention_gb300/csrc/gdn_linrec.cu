@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(256) linrec_param_kernel(int tiles, int C, flo
     if (warp || c >= C) return;
     for (int i = 1; i < 8; ++i) s = __fadd_rn(s, sums[i][threadIdx.x]);
     const float v = __ldg(ap + c), K = rate_of(v, decay), sp = 1.f / (1.f + expf(-v));
-    out[c] = K > 0.f ? s * (decay * sp / K) : 0.f;
+    out[c] = K == 0.f ? 0.f : s * (decay * sp / K);  // (NaN where a_param is)
 }
 
 template <typename T, typename F>

@@ -507,6 +507,22 @@ def test_nan_in_one_gate_leaves_the_other(dtype, param, scale, which):
         assert torch.equal(g[k][ok], g0[k][ok]), k
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_nan_in_a_rate_is_seen_in_its_gradient(dtype):
+    """A channel whose a_param is not a number: its outputs and gradients, da_param's among them, are none either; the others' bits stay."""
+    c = Case([40, 9, 0, 33], 72, dtype, 36, act="silu")
+    call = lambda: (gdn.gdn_linear_recurrence_fwd(cu_seqlens=c.cu, **c.args()),  # noqa: E731
+                    gdn.gdn_linear_recurrence_bwd(cu_seqlens=c.cu, d_out=c.dy, init_state=c.h0, d_final_state=c.gT, **c.args()))
+    y0, g0 = call()
+    c.ap[7] = float("nan")
+    y, g = call()
+    rest = [i for i in range(72) if i != 7]
+    assert torch.isnan(y[:, 7]).all() and torch.equal(bits(y[:, rest]), bits(y0[:, rest]))
+    assert torch.isnan(g["da_param"][7]) and torch.isnan(g["da_gate"][:, 7]).all()
+    for k in g:
+        assert torch.equal(bits(g[k][..., rest]), bits(g0[k][..., rest])), k
+
+
 # ---------------------------------------------------------------- rows, slots, streams, refusals
 
 def test_rows_behind_the_last_sequence_are_neither_read_nor_written():
