@@ -984,8 +984,8 @@ gdn_status check_linrec(const gdn_linrec_shape* s, bool param, bool gate, bool z
     if (param && !(s->decay > 0.f && s->decay <= FLT_MAX)) return GDN_ERR_INVALID_ARG;
     const int vn = s->dtype == GDN_BF16 ? 8 : 4;
     if (s->C % vn) return GDN_ERR_UNSUPPORTED;
-    // CTAs are numbered, states per sequence and tokens a few tiles behind the last indexed in 31 bits
-    if (s->T_total > INT_MAX - 4096 || (long long)s->N * s->C >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
+    // CTAs are numbered, states per sequence, channels up to the end of a block and tokens a few tiles behind the last indexed in 31 bits
+    if (s->T_total > INT_MAX - 4096 || s->C > INT_MAX - 64 || (long long)s->N * s->C >= (1LL << 31)) return GDN_ERR_UNSUPPORTED;
     if (s->ldx < s->C || s->lda < s->C || (gate && s->ldg < s->C) || (z && s->ldz < s->C)) return GDN_ERR_INVALID_ARG;
     if (s->ldx % vn || s->lda % vn || (gate && s->ldg % vn) || (z && s->ldz % vn)) return GDN_ERR_INVALID_ARG;
     return GDN_OK;

@@ -132,6 +132,19 @@ def test_recurrence_shapes(lib, shape, expect):
         assert lib.gdn_linear_recurrence_bwd_workspace_size(ctypes.byref(s)) == 0
 
 
+@pytest.mark.parametrize("C", [2 ** 31 - 8, 2 ** 31 - 32])
+@pytest.mark.parametrize("N", [0, 1])
+def test_recurrence_channels_at_the_end_of_31_bits(lib, C, N):
+    """Blocks of 32 channels are counted in 31 bits: refused, not launched with a count that has passed them."""
+    a = ptrs(*FWD)
+    wide = dict(N=N, T_total=N, C=C, ldx=C, lda=C, ldg=C, ldz=C)
+    assert fwd(lib, rec_shape(**wide), a) == UNSUPPORTED and update(lib, rec_shape(**wide), a) == UNSUPPORTED
+    assert lib.gdn_linear_recurrence_bwd(ctypes.byref(rec_shape(**wide)), *ptrs(*BWD).values(), 1 << 62, None) == UNSUPPORTED
+    assert lib.gdn_linear_recurrence_bwd_workspace_size(ctypes.byref(rec_shape(**wide))) == 0
+    fits = dict(dict.fromkeys(("C", "ldx", "lda", "ldg", "ldz"), 2 ** 31 - 72), N=1, T_total=1)
+    assert lib.gdn_linear_recurrence_bwd_workspace_size(ctypes.byref(rec_shape(**fits))) == 16 * (2 ** 31 - 72)
+
+
 @pytest.mark.parametrize("change,expect", [
     (dict(x=0), INVALID), (dict(ag=0), INVALID), (dict(cu=0), INVALID), (dict(y=0), INVALID), (dict(x=FAKE + 8), INVALID), (dict(ap=FAKE + 4), INVALID),
     (dict(st=FAKE + 4), INVALID), (dict(idx=FAKE + 1), INVALID), (dict(y="x"), INVALID), (dict(y="ag"), INVALID), (dict(y="xg"), INVALID),
