@@ -231,6 +231,26 @@ def test_short_sequences_with_long_ones_among_them(dtype, N, C, every, param, xg
     assert torch.equal(bits(pool[spare]), bits(pool0[spare]))
 
 
+@pytest.mark.parametrize("dtype,C,longest", [(BF, 264, 5003), (F32, 132, 5003), (BF, 1040, 40001), (F32, 516, 20001)])
+@pytest.mark.parametrize("where", [0, 100, 299])
+def test_a_long_prompt_among_single_tokens(dtype, C, longest, where):
+    """Decoding sequences of one token and a prompt of thousands in one batch, by either form that their mean length takes: the single
+    tokens have an update's bits, the prompt those it has alone, and the gradient holds at both."""
+    lens = [1] * 300
+    lens[where] = longest
+    c = Case(lens, C, dtype, 42, act="gelu")
+    pool, st = c.h0.clone(), c.h0.clone()
+    y = gdn.gdn_linear_recurrence_fwd(cu_seqlens=c.cu, state=pool, **c.args())
+    t, single = slice(where, where + longest), [n for n in range(300) if n != where]
+    rows = torch.tensor([c.cu_list[n] for n in single], device=DEV)
+    alone = gdn.gdn_linear_recurrence_fwd(cu_seqlens=torch.tensor([0, longest], dtype=torch.int32, device=DEV), state=st[where:where + 1], **c.args(t))
+    one = gdn.gdn_linear_recurrence_update(state=st, state_indices=torch.tensor(single, dtype=torch.int32, device=DEV), **c.args(rows))
+    assert torch.equal(bits(alone), bits(y[t])) and torch.equal(bits(one), bits(y[rows])) and torch.equal(bits(st), bits(pool))
+    if longest < 10000:
+        check_forward(c, y, pool, c.h0)
+        check_backward(c)
+
+
 @pytest.mark.parametrize("dtype,B,C", [(BF, 1001, 4160), (BF, 250, 8200), (F32, 1001, 4164)])
 def test_large_updates_skip_rows_anywhere(dtype, B, C):
     """Threads that take several rows, with skipped ones first, last and side by side among them."""
