@@ -465,7 +465,7 @@ struct GradParams {
     const void* dy;
     const float *h0, *dhT;
     void *dx, *da, *dg, *dz;
-    float *dap, *dh0;
+    float* dh0;
     float *P, *h, *g, *part;  // [tiles][C]
     int tiles;                // at most: T / TT + N, sequence n's from cu[n] / TT + n on
 };
@@ -1093,7 +1093,7 @@ extern "C" gdn_status gdn_linear_recurrence_bwd(const gdn_linrec_shape* shape, c
         return GDN_ERR_WORKSPACE;
     q.p.cu = cu_seqlens;
     q.dy = d_y, q.h0 = init_state, q.dhT = d_final_state, q.dx = dx, q.da = da_gate, q.dg = dx_gate, q.dz = dz;
-    q.dap = da_param, q.dh0 = d_init_state;
+    q.dh0 = d_init_state;
     q.tiles = (int)grad_tiles(p.T, p.N, shape->dtype);
     const size_t each = (size_t)q.tiles * p.C;
     q.P = static_cast<float*>(workspace), q.h = q.P + each, q.g = q.h + each, q.part = da_param ? q.g + each : nullptr;

@@ -103,20 +103,6 @@ __device__ __forceinline__ Scale scale_of(float most, float r) {
     return s;
 }
 
-// A chunk's values as packed pairs, and back.
-__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[4]) {
-    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
-    v[2] = make_float2(bf_lo(u.z), bf_hi(u.z)), v[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
-}
-__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
-    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-}
-__device__ __forceinline__ uint4 pack2(const float2 (&v)[4]) {
-    return make_uint4(bf_pack(v[0].x, v[0].y), bf_pack(v[1].x, v[1].y), bf_pack(v[2].x, v[2].y), bf_pack(v[3].x, v[3].y));
-}
-__device__ __forceinline__ uint4 pack2(const float2 (&v)[2]) {
-    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
-}
 __device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
 // A CTA takes rows blockIdx.x, + gridDim.x, ..  Up to two chunks a thread (NC), it keeps its weights in registers and

@@ -106,15 +106,6 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float2 (&v)[2]) {
     v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
 }
 
-// The values of a 16-byte chunk as packed pairs.
-__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[4]) {
-    v[0] = make_float2(bf_lo(u.x), bf_hi(u.x)), v[1] = make_float2(bf_lo(u.y), bf_hi(u.y));
-    v[2] = make_float2(bf_lo(u.z), bf_hi(u.z)), v[3] = make_float2(bf_lo(u.w), bf_hi(u.w));
-}
-__device__ __forceinline__ void unpack2(const uint4& u, float2 (&v)[2]) {
-    v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-}
-
 // Named barriers between a CTA's warps, and registers moved between its warpgroups.
 __device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
 __device__ __forceinline__ void bar_arrive(int id, int threads) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
