@@ -23,6 +23,11 @@
  * sqrt and linear); without an a_param it forgets the state, and +inf keeps it
  * bit for bit.  A decay is never above 1.
  *
+ * The factor s_t holds for every token, a sequence's first too.  For a layer that
+ * takes the first token's input unscaled, the state after that token is its
+ * x sigmoid(x_gate) and its y that state's: give it as the initial state and
+ * start from the second token (d_init_state is then its gradient).
+ *
  * Invariance.  The bits of y and of the final state of a sequence depend only
  * on that sequence's own inputs: not on the batch around it, and not on
  * whether its tokens arrive in one gdn_linear_recurrence_fwd call, in several

@@ -20,12 +20,12 @@ using namespace linrec;
 // at named barriers full (a tile prepared) and done (it is walked), one of each per buffer, which every side passes once a
 // tile.  The inputs arrive by asynchronous 16-byte copies, AHEAD tiles ahead, for a group of workers that copies what it reads.
 //
-// What bounds it.  fp32: HBM (16 prompts, 32768 x 4096, gated: 401 us, 0.98 of the measured peak).  bf16 with full SMs (16
+// What bounds it.  fp32: HBM (16 prompts, 32768 x 4096, gated: 398 us, 0.99 of the measured peak).  bf16 with full SMs (16
 // prompts, 32768 x 4096, gated: 264 us, 0.75): nothing alone; issue slots are half taken, the special function units (72
 // cycles for 256 values; 160 us by themselves before the gates shared a reciprocal) and the path from shared memory as well,
 // by 18 warps an SM that the registers and 108 KB of buffers leave.  (When it took 284 us: 240 with trivial work in the workers'
-// place, 261 without the walk.)  A single sequence: the walk, 6.3 ns a token with its stores and the workers beside it, 3.7 ns
-// alone (65536 x 2048: 414 us; 300 without the walk).
+// place, 261 without the walk.)  A single sequence: the walk, 6.0 ns a token with its stores and the workers beside it (65536 x 2048:
+// 396 us; the workers without it 300), 3.7 ns alone; its dependent steps by themselves 2.6 ns.
 template <typename T, int CB, int WORKERS>
 struct FwdTile {
     static constexpr int VN = V16<T>::n, CH = CB / VN, WORK = WORKERS, TT = WORK / CH, WALK = CB < 32 ? 32 : CB, NT = WORK + WALK;
@@ -458,8 +458,8 @@ __global__ void __launch_bounds__(128) linrec_update_kernel(const __grid_constan
 //     d = G (a h_{t-1} k - v kappa),  k = -w (or 1 - a: a_gate's slope of log a),  kappa = -k ds/du = k a^2 / s | k a | 0
 //     da_gate = d (1 - r) (or d),  da_param = sum of d over the tokens, times sigmoid(a_param) decay / K
 // The inputs are read twice: 28 bytes a value where 18 cannot be done without (bf16, gated).  8 documents, 16384 x 4096: 454 us,
-// sums 157, join 13, gradients 270, da_param 8.  Issue slots (63 and 49 % taken) and the path from shared memory (50 and 70 %, the
-// latter before the gradients left in whole rows) bound it, not HBM (56 and 46 %).
+// sums 157, join 13, gradients 270, da_param 8.  Issue slots (63 and 52 % taken) and the path from shared memory (51 and 62 %) bound
+// it, not HBM (56 and 49 %).
 struct GradParams {
     Params p;
     const void* dy;
@@ -931,15 +931,20 @@ gdn_status launch_many(cudaStream_t s, const Params& p) {
 }
 // Which form, by the number n of CTAs of 32 channels.  A token takes a CTA, bf16 and gated, 7 ns with 16 channels and 512 workers, 10 ns
 // with 32 and 512, 12 ns with 32 and 256, and 19 ns each of two of the last kind on one SM; a batch of several sequences ends with its
-// longest alone.  us with the three forms, bf16 / fp32:
-//     1 x 16384 x 1024 (n = 32)             115, 161, 201 / 123, 191, 263
-//     1 x 16384 x 4096 (128)                230, 162, 203 / 240, 210, 279
-//     3 ragged, 16000 x 1600 (150)           90,  95, 118 /  97, 120, 159
-//     2, 8000 x 2560 (160)                   85,  68,  78 /  91,  87,  95
-//     4, 8192 x 2048 (256)                   66,  49,  65 /  69,  63,  79
-//     1 x 16384 x 8192 (256)                458, 319, 305 / 495, 440, 413
-//     13, 20000 x 2560 (1040)               187, 125, 108 / 194, 167, 156
-//     16, 32768 x 4096 (2048)               461, 307, 264 / 477, 420, 401
+// longest alone, which 16 channels shorten where the lengths differ and do not where they are near one another (the host does not
+// know them).  us with the three forms, bf16 / fp32:
+//     1 x 16384 x 1024 (n = 32)             113, 160, 200 / 121, 189, 263
+//     1 x 16384 x 4096 (128)                230, 161, 202 / 238, 210, 280
+//     2 of 13142 and 2858 x 2048 (128)      111, 132, 165 / 122, 158, 216
+//     2 of 4882 and 3118 x 2048 (128)        64,  52,  63 /  66,  64,  86
+//     3 ragged, 16000 x 1600 (150)           87,  95, 118 /  97, 119, 158
+//     2, 8000 x 2560 (160)                   83,  69,  77 /  90,  86,  95
+//     4, 8192 x 2048 (256)                   65,  50,  65 /  68,  63,  79
+//     1 x 16384 x 8192 (256)                459, 318, 305 / 489, 436, 407
+//     13, 20000 x 2560 (1040)               184, 125, 108 / 193, 167, 154
+//     16, 32768 x 4096 (2048)               451, 307, 265 / 472, 416, 398
+// launch_many goes by the mean length alone: 255 sequences of one token beside one of 65536 x 2048 are past it and take 806 us, the long
+// one alone 444 (with a branch; one of 8192 x 4096 168 and 86).
 template <typename T>
 gdn_status launch_fwd(cudaStream_t s, const Params& p) {
     const long long n = (long long)((p.C + 31) / 32) * p.N;

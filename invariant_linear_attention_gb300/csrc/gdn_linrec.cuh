@@ -106,7 +106,8 @@ __device__ __forceinline__ void one_sigmoid(const float2 (&g)[NP], float2 (&r)[N
 }
 
 // The decay without an a_param, sigmoid(g).  Next to 1 it is 1 minus its rest r1, rounded once, and so never past 1: r, from the reciprocal that two
-// gates share, is up to an ulp off 1 on either side, which a kept state would take at every token (4096 open gates: 5e-4 of it).
+// gates share, is up to an ulp off 1 on either side, which a kept state would take at every token (4096 open gates: 5e-4 of it).  Costs
+// 16 prompts, 32768 x 4096, bf16, 231 -> 239 us with an x_gate and 193 -> 195 without, the gradient 693 -> 713 and 541 -> 549.
 template <int NP>
 __device__ __forceinline__ void forget(const float2 (&r)[NP], const float2 (&r1)[NP], float2 (&a)[NP]) {
 #pragma unroll

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(NT, NT <= 256 ? 3 : NT == 512 && NC <= 2 ? 2 :
 
 // The gradient takes rows the same way.  sum(g s) needs no r, so that both sums go together.  dw: a thread's
 // columns in registers, with more than two chunks in its own places of shared memory.  32768 x 4096, bf16, with the residual's
-// gradient: 171 us, 0.92 of HBM; rows past 8192 (fp32 4096) values hold more than the registers do: 8192 x 16384 305 us, 0.52.
+// gradient: 171 us, 0.93 of HBM; rows past 8192 (fp32 4096) values hold more than the registers do: 8192 x 16384 277 us, 0.57.
 template <typename T, int NC, int NT>
 __global__ void __launch_bounds__(NT, NT <= 256 ? 2 : 1) add_norm_bwd_kernel(const __grid_constant__ NormParams p) {
     constexpr int VN = V16<T>::n;
