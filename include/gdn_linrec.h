@@ -18,7 +18,7 @@
  * sigmoid(z) or gelu(z) = z sigmoid(2 sqrt(2 / pi) (z + 0.044715 z^3)) (the
  * tanh form).  1 - a is taken as -expm1 of the exponent and 1 - a^2 as
  * (1 - a)(1 + a), so that decays next to 1 keep their inputs' scale (1 - a
- * below 2^-126 counts as 0).  An
+ * below 2^-126 counts as 0; decay softplus(a_param) past 3e38 counts as 3e38).  An
  * a_gate of -inf under an a_param keeps the state and takes nothing in (scale
  * sqrt and linear); without an a_param it forgets the state, and +inf keeps it
  * bit for bit.  A decay is never above 1.
