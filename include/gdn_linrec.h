@@ -21,7 +21,7 @@
  * below 2^-126 counts as 0; decay softplus(a_param) past 3e38 counts as 3e38).  An
  * a_gate of -inf under an a_param keeps the state and takes nothing in (scale
  * sqrt and linear); without an a_param it forgets the state, and +inf keeps it
- * bit for bit.  A decay is never above 1.
+ * bit for bit (scale one adds the input all the same).  A decay is never above 1.
  *
  * The factor s_t holds for every token, a sequence's first too.  For a layer that
  * takes the first token's input unscaled, the state after that token is its

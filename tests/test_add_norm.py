@@ -16,7 +16,7 @@ import invariant_linear_attention_gb300 as gdn
 from oracle import layer_ops
 from oracle import linrec_ops
 from helpers import BF16_ROUND, normwise, to_np
-from test_linrec import BF, DEV, F32, INF, U, bits
+from test_linrec import BF, DEV, F32, U, bits
 
 pytestmark = pytest.mark.gpu
 
@@ -198,7 +198,7 @@ def test_values_far_out():
 def test_fp8_values_go_by_the_stored_scale(dtype, d, group):
     """Groups whose scale is the smallest one, 2^-126: y is still value / scale.  Rows whose sum of squares is past fp32 have a norm of 0."""
     x = torch.randn(4, d, generator=torch.Generator().manual_seed(15))
-    x[0, 3], x[1, 5], x[2], x[3] = INF, 1e20, x[2] * 1e-20, x[3] * 1e-24
+    x[0, 3], x[1, 5], x[2], x[3] = float("inf"), 1e20, x[2] * 1e-20, x[3] * 1e-24
     x[2:, 0] = 1e17  # r: sqrt(d) 1e-17; values of 1e-35 to 1e-39 behind it
     x = x.to(dtype).to(DEV)
     w = (1 + 0.1 * torch.randn(d, generator=torch.Generator().manual_seed(16))).to(DEV)
